@@ -14,14 +14,17 @@ import os
 from . import build as _build
 
 __all__ = [
-    "QGemmError", "QTensor", "F16", "E4M3", "INT8", "INT4", "E2M1", "load_library", "library_path",
+    "QGemmError", "QTensor", "F16", "E4M3", "INT8", "INT4", "E2M1", "BF16", "load_library", "library_path",
     "qgemm_version", "qgemm_debug_build", "qgemm_create_tensor", "qgemm_tensor_slice", "qgemm_destroy_tensor",
     "qgemm_mxfp8", "qgemm_mxfp8_scratch_bytes", "qgemm_mxfp8_host", "qgemm_mxfp4", "gemm_f16", "qgemm_w4a16", "qgemm_w4a16_f16s", "qgemm_attention", "qgemm_w8_gemv", "qgemm_dequant_debug",
     "qgemm_status_string", "qgemm_poll_device_error", "qgemm_set_wait_timeout_ns",
     "qgemm_selftest_wait_timeout", "qgemm_sm_clock_probe",
+    "Rotation", "KVCache", "qgemm_create_rope", "qgemm_rope", "qgemm_create_kv_cache", "qgemm_kv_append",
+    "qgemm_paged_attention_workspace", "qgemm_paged_attention", "qgemm_kv_resize", "qgemm_kv_fork",
+    "qgemm_kv_compact", "qgemm_kv_copy_pages",
 ]
 
-F16, E4M3, INT8, INT4, E2M1 = 0, 1, 2, 3, 4
+F16, E4M3, INT8, INT4, E2M1, BF16 = 0, 1, 2, 3, 4, 5
 OK = 0
 STATUS_NAMES = {0: "QGEMM_OK", 1: "QGEMM_ERR_INVALID_ARG", 2: "QGEMM_ERR_UNSUPPORTED_SHAPE",
                 3: "QGEMM_ERR_MISALIGNED", 4: "QGEMM_ERR_UNSUPPORTED_DTYPE", 5: "QGEMM_ERR_CUDA",
@@ -64,6 +67,8 @@ def load_library():
     lib = ctypes.CDLL(path)
     P, I64, I32, U64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_uint64
     S = ctypes.c_int
+    D, F = ctypes.c_double, ctypes.c_float
+    meta = [P, P, I64, I64, I64, P, P]       # cache, table, its stride and shape, lengths, counts
     sig = {
         "qgemm_version": (I32, []),
         "qgemm_debug_build": (I32, []),
@@ -97,6 +102,21 @@ def load_library():
         "qgemm_set_wait_timeout_ns": (None, [U64]),
         "qgemm_selftest_wait_timeout": (S, [U64, P]),
         "qgemm_sm_clock_probe": (S, [U64, P, P]),
+        "qgemm_create_rope": (S, [ctypes.POINTER(P), I64, I32, D, I32, D, D, D, D, D]),
+        "qgemm_destroy_rope": (None, [P]),
+        "qgemm_rope": (S, [P, I64, I64, P, I64, I64, I32, I64, I64, I64, P, P, I32, P]),
+        "qgemm_create_kv_cache": (S, [ctypes.POINTER(P), I32, I64, I64, I64, I64, I64, P, P,
+                                      ctypes.POINTER(I64), P, P, ctypes.POINTER(I64)]),
+        "qgemm_destroy_kv_cache": (None, [P]),
+        "qgemm_kv_append": (S, [P, I64, P, I64, I64, P, I64, I64, I32, I64, P, P, P, I64, I64, I64,
+                                P, P, I64, I64, I64, P, I64, I64, P]),
+        "qgemm_paged_attention_workspace_bytes": (S, [P, I64, I64, ctypes.POINTER(I64)]),
+        "qgemm_paged_attention": (S, [P, I64, I64, I32, I64, I64, P, I64, P, I64, I64, I64, P, P, P,
+                                      I64, I64, P, F, I64, P, I64, P]),
+        "qgemm_kv_resize": (S, meta + [P, P, I64, P]),
+        "qgemm_kv_fork": (S, meta + [P, P, I64, P]),
+        "qgemm_kv_compact": (S, meta + [P]),
+        "qgemm_kv_copy_pages": (S, [P, P, P, I64, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -370,3 +390,233 @@ def qgemm_sm_clock_probe(window_ns: int, out, stream=None):
     device tensor `out` (from the GPU, on `stream`)."""
     _check(load_library().qgemm_sm_clock_probe(int(window_ns), _ptr(out), _stream(stream)),
            "qgemm_sm_clock_probe")
+
+
+# ------------------------------------------------------------------------------ decode serving
+class Rotation:
+    """Owning handle of rotary frequencies (qgemm_create_rope)."""
+
+    def __init__(self, handle: int, rot_dim: int):
+        self.handle = ctypes.c_void_p(handle)
+        self.rot_dim = rot_dim
+
+    def close(self):
+        if self.handle and self.handle.value:
+            load_library().qgemm_destroy_rope(self.handle)
+            self.handle = ctypes.c_void_p(None)
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class KVCache:
+    """Owning handle of a paged key-value cache view; keeps the borrowed torch tensors alive."""
+
+    def __init__(self, handle: int, dtype: int, shape, refs):
+        self.handle = ctypes.c_void_p(handle)
+        self.dtype = dtype
+        self.layers, self.pages, self.heads, self.page_size, self.d = shape
+        self._refs = refs
+
+    def close(self):
+        if self.handle and self.handle.value:
+            load_library().qgemm_destroy_kv_cache(self.handle)
+            self.handle = ctypes.c_void_p(None)
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+_ROPE_SCALING = {"none": 0, "linear": 1, "by_parts": 2}
+
+
+def _dtype16(t) -> int:
+    import torch
+    if t.dtype == torch.float16:
+        return F16
+    if t.dtype == torch.bfloat16:
+        return BF16
+    raise ValueError(f"expected an fp16 or bf16 tensor, got {t.dtype}")
+
+
+def _rows3(t, what: str):
+    """(pointer, token stride, head stride) of a [tokens, heads, d] tensor."""
+    if t.dim() != 3 or t.stride(2) != 1 and t.shape[2] > 1:
+        raise ValueError(f"{what}: expected a [tokens, heads, d] tensor with a contiguous last dimension")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def _ints(t, what: str, n: int | None = None):
+    import torch
+    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous 1-D int32 tensor")
+    if n is not None and t.shape[0] < n:
+        raise ValueError(f"{what}: {t.shape[0]} entries, {n} needed")
+    return t.data_ptr()
+
+
+def _table(t):
+    import torch
+    if t.dtype != torch.int32 or t.dim() != 2 or t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError("page table: expected a 2-D int32 tensor with contiguous rows")
+    return t.data_ptr(), t.stride(0), t.shape[0], t.shape[1]
+
+
+def qgemm_create_rope(rot_dim: int, base: float = 10000.0, interleaved: bool = False,
+                      scaling: str = "none", factor: float = 1.0, original_len: float = 0.0,
+                      low_turns: float = 1.0, high_turns: float = 4.0, mscale: float = 1.0) -> Rotation:
+    """Rotary frequencies for the first ``rot_dim`` elements of a head; ``scaling`` is "none",
+    "linear" (all divided by ``factor``) or "by_parts" (slow pairs divided, fast ones kept)."""
+    if scaling not in _ROPE_SCALING:
+        raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALING)}")
+    out = ctypes.c_void_p()
+    _check(load_library().qgemm_create_rope(ctypes.byref(out), rot_dim, int(bool(interleaved)), base,
+                                            _ROPE_SCALING[scaling], factor, original_len, low_turns,
+                                            high_turns, mscale), "qgemm_create_rope")
+    return Rotation(out.value, rot_dim)
+
+
+def qgemm_rope(X, positions, rope: Rotation, out=None, inverse: bool = False, stream=None):
+    """X [tokens, heads, d] (fp16 or bf16) rotated to ``positions`` (int32 [tokens]), into ``out``
+    (default: in place).  ``inverse`` rotates back, which is the gradient."""
+    Y = X if out is None else out
+    if Y.shape != X.shape or Y.dtype != X.dtype:
+        raise ValueError("out: shape and type must be X's")
+    T, H, d = X.shape
+    _check(load_library().qgemm_rope(*_rows3(X, "X"), *_rows3(Y, "out"), _dtype16(X), T, H, d,
+                                     _ints(positions, "positions", T), rope.handle, int(bool(inverse)),
+                                     _stream(stream)), "qgemm_rope")
+    return Y
+
+
+def qgemm_create_kv_cache(k, v, k_scales=None, v_scales=None) -> KVCache:
+    """View of a paged cache: ``k`` and ``v`` are [layers, pages, heads, page_size, d] device tensors
+    of any strides with contiguous rows (a permuted view for another order in memory), fp16, bf16, or
+    uint8 / float8_e4m3fn codes with uint8 UE8M0 scales [..., 4 bytes] in ``k_scales``, ``v_scales``."""
+    import torch
+    if k.dim() != 5 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+        raise ValueError("k and v: expected two [layers, pages, heads, page_size, d] tensors of one layout")
+    if k.stride(4) != 1:
+        raise ValueError("rows must be contiguous")
+    if k.dtype in (torch.uint8, torch.float8_e4m3fn):
+        dt = E4M3
+    else:
+        dt = _dtype16(k)
+    item = k.element_size()
+    strides = (ctypes.c_int64 * 4)(*(s * item for s in k.stride()[:4]))
+    sstrides = None
+    if k_scales is not None or v_scales is not None:
+        if k_scales is None or v_scales is None or k_scales.shape != v_scales.shape or \
+                k_scales.stride() != v_scales.stride():
+            raise ValueError("k_scales and v_scales: expected two tensors of one layout")
+        if k_scales.dtype != torch.uint8 or k_scales.dim() != 5 or k_scales.shape[:4] != k.shape[:4] or \
+                k_scales.shape[4] < k.shape[4] // 32 or k_scales.stride(4) != 1:
+            raise ValueError("scales: expected uint8 [layers, pages, heads, page_size, d / 32 or more]")
+        sstrides = (ctypes.c_int64 * 4)(*k_scales.stride()[:4])
+    out = ctypes.c_void_p()
+    _check(load_library().qgemm_create_kv_cache(ctypes.byref(out), dt, *k.shape, _ptr(k), _ptr(v), strides,
+                                                _ptr(k_scales), _ptr(v_scales), sstrides),
+           "qgemm_create_kv_cache")
+    return KVCache(out.value, dt, tuple(k.shape), (k, v, k_scales, v_scales))
+
+
+def qgemm_kv_append(kv: KVCache, layer: int, K, V, seqs, positions, table, rope: Rotation | None = None,
+                    Q=None, Q_out=None, stream=None):
+    """Store new keys (rotated) and values [tokens, heads, d] at ``positions`` of sequences ``seqs``,
+    and rotate the tokens' queries ``Q`` [tokens, q_heads, d] into ``Q_out`` (default: in place)."""
+    T = K.shape[0]
+    dt = _dtype16(K)
+    if K.shape != V.shape or tuple(K.shape) != (T, kv.heads, kv.d) or V.dtype != K.dtype:
+        raise ValueError(f"K and V: expected [tokens, {kv.heads}, {kv.d}] of one type")
+    q = qo = (None, 0, 0)
+    hq = 0
+    if Q is not None:
+        Q_out = Q if Q_out is None else Q_out
+        if Q.shape[0] != T or Q.shape[2] != kv.d or Q_out.shape != Q.shape or Q.dtype != K.dtype or \
+                Q_out.dtype != K.dtype:
+            raise ValueError(f"Q and Q_out: expected [{T}, q_heads, {kv.d}] of K's type")
+        hq = Q.shape[1]
+        q, qo = _rows3(Q, "Q"), _rows3(Q_out, "Q_out")
+    _check(load_library().qgemm_kv_append(
+        kv.handle, layer, *_rows3(K, "K"), *_rows3(V, "V"), dt, T, _ints(seqs, "seqs", T),
+        _ints(positions, "positions", T), *_table(table), rope.handle if rope is not None else None,
+        *q, hq, *qo, _stream(stream)), "qgemm_kv_append")
+    return Q_out
+
+
+def qgemm_paged_attention_workspace(kv: KVCache, batch: int, q_heads: int):
+    """A zeroed workspace for qgemm_paged_attention calls of up to ``batch`` sequences, one after
+    another on one stream."""
+    import torch
+    n = ctypes.c_int64(0)
+    _check(load_library().qgemm_paged_attention_workspace_bytes(kv.handle, batch, q_heads, ctypes.byref(n)),
+           "qgemm_paged_attention_workspace_bytes")
+    return torch.zeros(n.value, dtype=torch.uint8, device=kv._refs[0].device)
+
+
+def qgemm_paged_attention(Q, kv: KVCache, layer: int, table, lens, O, seqs=None, lse=None, scale=None,
+                          window: int = 0, workspace=None, stream=None):
+    """O[b] = attention of Q[b] [q_heads, d] over the first ``lens[s]`` cached tokens of sequence s =
+    ``seqs[b]`` (default b), the last ``window`` of them (0: all); ``lse`` (fp32 [batch, q_heads])
+    receives the log of the softmax sums.  ``workspace`` comes from qgemm_paged_attention_workspace
+    (one made for the call otherwise, on the current stream)."""
+    import torch
+    B, H, d = Q.shape
+    if O.shape != Q.shape or O.dtype != Q.dtype or d != kv.d:
+        raise ValueError(f"Q and O: expected [batch, q_heads, {kv.d}] of one type")
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (B, H) or not lse.is_contiguous()):
+        raise ValueError("lse: expected a contiguous fp32 [batch, q_heads] tensor")
+    if workspace is None:
+        s = stream if stream is not None and not isinstance(stream, int) else torch.cuda.current_stream()
+        if isinstance(stream, int) and stream != s.cuda_stream:
+            raise ValueError("a raw stream needs a workspace of its own")
+        with torch.cuda.stream(s):
+            workspace = qgemm_paged_attention_workspace(kv, B, H)
+    t = _table(table)
+    _check(load_library().qgemm_paged_attention(
+        *_rows3(Q, "Q"), _dtype16(Q), B, H, kv.handle, layer, *t, _ints(lens, "lens", t[2]),
+        None if seqs is None else _ints(seqs, "seqs", B), *_rows3(O, "O"), _ptr(lse),
+        kv.d ** -0.5 if scale is None else float(scale), window, workspace.data_ptr(), workspace.numel(),
+        _stream(stream)), "qgemm_paged_attention")
+    return O
+
+
+def _meta(kv: KVCache, table, lens, refs):
+    t = _table(table)
+    return (kv.handle, *t, _ints(lens, "lens", t[2]), _ints(refs, "refs", kv.pages))
+
+
+def qgemm_kv_resize(kv: KVCache, table, lens, refs, seqs, new_lens=None, stream=None):
+    """Give sequences ``seqs`` ``new_lens`` tokens (None: free them): ``table`` [max_seqs, max_pages],
+    ``lens`` [max_seqs] and ``refs`` [pages] (int32) are updated on the device."""
+    n = seqs.shape[0]
+    _check(load_library().qgemm_kv_resize(*_meta(kv, table, lens, refs), _ints(seqs, "seqs"),
+                                          None if new_lens is None else _ints(new_lens, "new_lens", n), n,
+                                          _stream(stream)), "qgemm_kv_resize")
+
+
+def qgemm_kv_fork(kv: KVCache, table, lens, refs, parents, children, stream=None):
+    """Make sequences ``children`` copies of ``parents``: whole pages shared, a partly filled last
+    page copied."""
+    n = children.shape[0]
+    _check(load_library().qgemm_kv_fork(*_meta(kv, table, lens, refs), _ints(parents, "parents", n),
+                                        _ints(children, "children"), n, _stream(stream)), "qgemm_kv_fork")
+
+
+def qgemm_kv_compact(kv: KVCache, table, lens, refs, stream=None):
+    """Move the pages in use to the front of the cache."""
+    _check(load_library().qgemm_kv_compact(*_meta(kv, table, lens, refs), _stream(stream)),
+           "qgemm_kv_compact")
+
+
+def qgemm_kv_copy_pages(kv: KVCache, src, dst, stream=None):
+    """Copy pages ``src`` to ``dst`` (int32, on the device) in every layer."""
+    n = src.shape[0]
+    _check(load_library().qgemm_kv_copy_pages(kv.handle, _ints(src, "src"), _ints(dst, "dst", n), n,
+                                              _stream(stream)), "qgemm_kv_copy_pages")

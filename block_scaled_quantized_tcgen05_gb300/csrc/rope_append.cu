@@ -1,0 +1,400 @@
+// rope_append.cu -- rotary positions, alone or on the way into the paged key-value cache.
+//
+// A pair (a, b) of a head at position p becomes (a cos t - b sin t, a sin t + b cos t) times the
+// magnitude factor, t = p w_i.  The inverse (the rotation's transpose, which is its gradient)
+// turns by -t.  Pairs are (2i, 2i + 1) (interleaved) or (i, i + rot_dim / 2) (halves); elements
+// past rot_dim pass through.
+//
+// Angles.  w_i / 2 pi is held as a 64-bit fraction of a turn, so position times frequency modulo
+// one turn is one wrapping integer product, exact to 2^-64 p of a turn at every position (an fp32
+// angle at position 10^5 is off by 2^-8 rad).  The top 32 bits as a signed fraction go to
+// sincospif: the angle's error is 2^-25 of itself, far below the output's rounding.
+//
+// Appending stores keys (rotated) and values as they are or as E4M3 codes with one power of two
+// per 32 elements: X = floor(log2 amax) - 8, code = e4m3_rn(x 2^-X) saturated at 448, straight
+// from the fp32 rotation (one rounding).  fp16 sources stop at X = -15: below that 2^-24, the
+// half's own quantum, is finer than E4M3's grid, and every code times its scale stays a half.
+//
+// Bound: memory (one read and one write of every element; at 16384 x 48 rows of 128 about 0.4 GB).
+// A block takes the rows (token, head) of a few tokens: the sines and cosines of its tokens are
+// computed once into shared memory, while the first rows' loads are already in flight, and every
+// row is read 16 bytes a lane, LPR lanes a row, four rows a lane before the first is used.  A pair's
+// other half comes from the lane that holds it (a shuffle), so each element is read once.
+#include "kv_common.cuh"
+
+namespace qg {
+namespace {
+
+constexpr int THREADS = 256;
+constexpr int ROWS = 4;          // rows a lane has in flight
+constexpr int MAX_TPC = 8;       // tokens of one block
+
+struct RopeParams {
+    const uint8_t *x[3];         // q, k, v
+    int64_t xt[3], xh[3];        // token and head strides, bytes
+    uint8_t *y;                  // rotated q
+    int64_t yt, yh;
+    uint8_t *pk[2], *ps[2];      // cache planes of this layer: data and scales of keys, values
+    int64_t page, head, token, spage, shead, stoken;
+    int64_t extent, sextent;     // bytes of a plane from this layer's base (debug checks)
+    const int32_t *seqs, *pos, *table;
+    int64_t table_stride;
+    int32_t T, d, hq, hkv, tpc, hsplit;
+    int32_t max_seqs, max_pages, page_size, pages;
+    int32_t rot;                 // 0: no rotation
+    int32_t min_exp;             // smallest X of an E4M3 block
+    float mscale, sign;
+    unsigned *err;
+};
+struct Frequencies {
+    uint64_t f[128];
+};
+
+// 8 elements of a row from element e0 on; those at d and beyond read as zero.
+template <bool VEC>
+__device__ __forceinline__ uint4 load8(const uint8_t *row, int e0, int d) {
+    if (e0 >= d) return make_uint4(0, 0, 0, 0);
+    if (VEC) return *reinterpret_cast<const uint4 *>(row + 2 * e0);
+    uint32_t w[4] = {0, 0, 0, 0};
+    const uint16_t *p = reinterpret_cast<const uint16_t *>(row);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (e0 + i < d) w[i / 2] |= uint32_t(p[e0 + i]) << (16 * (i & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8(uint8_t *row, int e0, int d, uint4 v) {
+    if (e0 >= d) return;
+    if (VEC) {
+        *reinterpret_cast<uint4 *>(row + 2 * e0) = v;
+        return;
+    }
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint16_t *p = reinterpret_cast<uint16_t *>(row);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (e0 + i < d) p[e0 + i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+}
+
+// The block's 8 values as E4M3 with the scale of their 32 (four lanes hold a block).  Returns the
+// codes; *byte is the UE8M0 scale.  fmaxf passes over NaN, whose code is E4M3's NaN.
+__device__ __forceinline__ uint2 quantise8(const float (&x)[8], int min_exp, uint32_t *byte) {
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
+    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+    // floor(log2) is the exponent field; fp32 subnormals (field 0) are below every X that is kept
+    int X = int(__float_as_uint(amax) >> 23) - 127 - 8;
+    X = amax > 0.0f ? max(X, min_exp) : 0;
+    *byte = uint32_t(X + 127);
+    const float inv = __uint_as_float(uint32_t(127 - X) << 23);    // 2^-X, X in [-127, 120]
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint16_t lo, hi;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+            : "=h"(lo)
+            : "f"(x[4 * i + 1] * inv), "f"(x[4 * i] * inv));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+            : "=h"(hi)
+            : "f"(x[4 * i + 3] * inv), "f"(x[4 * i + 2] * inv));
+        w[i] = uint32_t(lo) | (uint32_t(hi) << 16);
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+// LPR lanes a row of 8 elements each; INTER: interleaved pairs; VEC: rows are 16-byte aligned and
+// d, and for halves rot / 2, multiples of 8; E4M3: the cache's planes are quantised.
+template <class TY, int LPR, bool INTER, bool VEC, bool E4M3>
+__global__ void __launch_bounds__(THREADS) rope_append_kernel(const __grid_constant__ RopeParams p,
+                                                              const __grid_constant__ Frequencies fr) {
+    extern __shared__ __align__(16) float s_cs[];      // [tpc][2][half]: cosines, sines
+    __shared__ int64_t s_slot[MAX_TPC], s_sslot[MAX_TPC];
+    const int tid = threadIdx.x, half = p.rot / 2;
+    const int t0 = blockIdx.x * p.tpc, nt = min(p.tpc, p.T - t0);
+    constexpr int RPP = THREADS / LPR;                 // rows a pass
+    const int lane_r = tid % LPR, row_r = tid / LPR;
+    const int e0 = 8 * lane_r;
+    const int heads = p.hq + 2 * p.hkv;
+    // this block's heads (few tokens: a token's heads are dealt to several blocks)
+    const int h0 = heads * int(blockIdx.y) / p.hsplit, h1 = heads * int(blockIdx.y + 1) / p.hsplit;
+    const int nh = h1 - h0, rows = nt * nh;
+
+    auto source = [&](int r, int &t, int &h, int &side) {
+        t = r / nh;
+        h = h0 + r - t * nh;
+        side = h < p.hq ? 0 : (h < p.hq + p.hkv ? 1 : 2);
+        h -= side == 0 ? 0 : (side == 1 ? p.hq : p.hq + p.hkv);
+        return p.x[side] + (t0 + t) * p.xt[side] + h * p.xh[side];
+    };
+    auto fetch = [&](int base, uint4 (&v)[ROWS]) {
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const int r = base + i * RPP + row_r;
+            if (r < rows) {
+                int t, h, side;
+                v[i] = load8<VEC>(source(r, t, h, side), e0, p.d);
+            }
+        }
+    };
+    uint4 v[ROWS];
+    fetch(0, v);
+
+    // slots of the block's tokens in the cache, and their sines and cosines
+    if (p.hkv > 0 && tid < nt) {
+        const int t = t0 + tid, seq = p.seqs[t];
+        int32_t page = 0, off = 0;
+        bool ok = seq >= 0 && seq < p.max_seqs;
+        ok = ok && kvi::locate(p.table + seq * p.table_stride, p.max_pages, p.page_size, p.pages,
+                               p.pos[t], &page, &off);
+        if (!ok) report_index(p.err);
+        s_slot[tid] = ok ? page * p.page + off * p.token : -1;
+        s_sslot[tid] = page * p.spage + off * p.stoken;
+    }
+    for (int i = tid; i < nt * half; i += THREADS) {
+        const int t = i / half, j = i - t * half;
+        const uint64_t turn = uint64_t(int64_t(p.pos[t0 + t])) * fr.f[j];
+        float s, c;
+        sincospif(float(int32_t(turn >> 32)) * 0x1p-31f, &s, &c);
+        s_cs[(2 * t) * half + j] = c * p.mscale;
+        s_cs[(2 * t + 1) * half + j] = s * (p.mscale * p.sign);
+    }
+    __syncthreads();
+
+    for (int base = 0; base < rows; base += ROWS * RPP) {
+        if (base) {
+            // rows of an earlier pass were stored above; these are other rows, so an output that
+            // is the input itself is still read before it is written
+            fetch(base, v);
+        }
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const int r = base + i * RPP + row_r;
+            if (base + i * RPP >= rows) break;          // the same for every lane
+            const bool live = r < rows;
+            int t = 0, h = 0, side = 0;
+            const uint8_t *src = live ? source(r, t, h, side) : nullptr;
+            float x[8];
+            {
+                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = TY::unpack(w[j]);
+                    x[2 * j] = f.x;
+                    x[2 * j + 1] = f.y;
+                }
+            }
+            const bool turned = half > 0 && side < 2;
+            const float *cs = s_cs + (2 * t) * half, *sn = cs + half;
+            if (INTER) {
+                if (live && turned) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int pair = e0 / 2 + j;
+                        if (pair < half) {
+                            const float a = x[2 * j], b = x[2 * j + 1], c = cs[pair], s = sn[pair];
+                            x[2 * j] = a * c - b * s;
+                            x[2 * j + 1] = a * s + b * c;
+                        }
+                    }
+                }
+            } else if (VEC) {
+                // the other halves of this lane's pairs are in the lane half / 8 further or back
+                const int hl = half / 8;
+                const bool first = lane_r < hl;
+                const int other = (tid & 31) - lane_r + (first ? lane_r + hl : lane_r - hl);
+                const bool in = lane_r < 2 * hl;
+                uint32_t ow[4];
+                ow[0] = __shfl_sync(0xFFFFFFFFu, v[i].x, in ? other : 0);
+                ow[1] = __shfl_sync(0xFFFFFFFFu, v[i].y, in ? other : 0);
+                ow[2] = __shfl_sync(0xFFFFFFFFu, v[i].z, in ? other : 0);
+                ow[3] = __shfl_sync(0xFFFFFFFFu, v[i].w, in ? other : 0);
+                if (live && turned && in) {
+                    const int j0 = first ? e0 : e0 - half;
+#pragma unroll
+                    for (int j = 0; j < 8; j += 4) {
+                        const float4 c = *reinterpret_cast<const float4 *>(cs + j0 + j);
+                        const float4 s = *reinterpret_cast<const float4 *>(sn + j0 + j);
+                        const float2 o0 = TY::unpack(ow[j / 2]), o1 = TY::unpack(ow[j / 2 + 1]);
+                        const float o[4] = {o0.x, o0.y, o1.x, o1.y};
+                        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            x[j + k] = first ? x[j + k] * cc[k] - o[k] * ss[k]
+                                             : o[k] * ss[k] + x[j + k] * cc[k];
+                    }
+                }
+            } else {
+                // ragged halves: each element's other half straight from memory, before any lane
+                // of the warp stores (the output may be the input itself)
+                float o[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int e = e0 + j;
+                    o[j] = 0.0f;
+                    if (live && turned && e < p.rot) {
+                        const uint16_t u = reinterpret_cast<const uint16_t *>(
+                            src)[e < half ? e + half : e - half];
+                        o[j] = TY::unpack(u).x;
+                    }
+                }
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int e = e0 + j;
+                    if (live && turned && e < p.rot) {
+                        const int pair = e < half ? e : e - half;
+                        x[j] = e < half ? x[j] * cs[pair] - o[j] * sn[pair]
+                                        : o[j] * sn[pair] + x[j] * cs[pair];
+                    }
+                }
+            }
+            uint32_t byte = 0;
+            uint2 codes = make_uint2(0, 0);
+            if (E4M3) codes = quantise8(x, p.min_exp, &byte);       // every lane: it shuffles
+            if (!live) continue;
+            const uint4 out = make_uint4(TY::pack(x[0], x[1]), TY::pack(x[2], x[3]),
+                                         TY::pack(x[4], x[5]), TY::pack(x[6], x[7]));
+            if (side == 0) {
+                store8<VEC>(p.y + (t0 + t) * p.yt + h * p.yh, e0, p.d, out);
+            } else if (s_slot[t] >= 0 && e0 < p.d) {
+                const int64_t at = s_slot[t] + h * p.head;
+                uint8_t *plane = p.pk[side - 1];
+                if (E4M3) {
+                    const int64_t sat = s_sslot[t] + h * p.shead;
+                    if (QG_IN_BOUNDS(p.err, at >= 0 && at + p.d <= p.extent &&
+                                                sat >= 0 && sat + p.d / 32 <= p.sextent)) {
+                        *reinterpret_cast<uint2 *>(plane + at + e0) = codes;
+                        if (lane_r % 4 == 0)
+                            p.ps[side - 1][sat + lane_r / 4] = static_cast<uint8_t>(byte);
+                    }
+                } else if (QG_IN_BOUNDS(p.err, at >= 0 && at + 2 * p.d <= p.extent)) {
+                    *reinterpret_cast<uint4 *>(plane + at + 2 * e0) = out;   // planes are aligned
+                }
+            }
+        }
+    }
+}
+
+template <class TY, int LPR, bool INTER, bool VEC, bool E4M3>
+cudaError_t launch(const RopeParams &p, const Frequencies &fr, dim3 grid, size_t smem,
+                   cudaStream_t stream) {
+    rope_append_kernel<TY, LPR, INTER, VEC, E4M3><<<grid, THREADS, smem, stream>>>(p, fr);
+    return cudaGetLastError();
+}
+
+template <class TY, int LPR, bool E4M3>
+cudaError_t launch_layout(const RopeParams &p, const Frequencies &fr, bool inter, bool vec,
+                          dim3 grid, size_t smem, cudaStream_t stream) {
+    if (inter) return vec ? launch<TY, LPR, true, true, E4M3>(p, fr, grid, smem, stream)
+                          : launch<TY, LPR, true, false, E4M3>(p, fr, grid, smem, stream);
+    return vec ? launch<TY, LPR, false, true, E4M3>(p, fr, grid, smem, stream)
+               : launch<TY, LPR, false, false, E4M3>(p, fr, grid, smem, stream);
+}
+
+template <class TY>
+cudaError_t launch_type(const RopeParams &p, const Frequencies &fr, bool inter, bool vec, bool e4m3,
+                        dim3 grid, size_t smem, cudaStream_t stream) {
+    if (e4m3)      // d is 64 or 128
+        return p.d <= 64 ? launch_layout<TY, 8, true>(p, fr, inter, vec, grid, smem, stream)
+                         : launch_layout<TY, 16, true>(p, fr, inter, vec, grid, smem, stream);
+    if (p.d <= 64) return launch_layout<TY, 8, false>(p, fr, inter, vec, grid, smem, stream);
+    if (p.d <= 128) return launch_layout<TY, 16, false>(p, fr, inter, vec, grid, smem, stream);
+    return launch_layout<TY, 32, false>(p, fr, inter, vec, grid, smem, stream);
+}
+
+}  // namespace
+}  // namespace qg
+
+namespace qgi {
+
+cudaError_t launch_rope_append(const AppendArgs &a, const LaunchCtx &ctx) {
+    qg::RopeParams p = {};
+    qg::Frequencies fr = {};
+    const bool append = a.kv != nullptr;
+    auto aligned = [](const void *b, int64_t ts, int64_t hs) {
+        return reinterpret_cast<uintptr_t>(b) % 16 == 0 && ts % 8 == 0 && hs % 8 == 0;
+    };
+    bool vec = a.d % 8 == 0;
+    p.hq = a.q.heads;
+    if (p.hq > 0) {
+        p.x[0] = static_cast<const uint8_t *>(a.q.x);
+        p.xt[0] = 2 * a.q.xt;
+        p.xh[0] = 2 * a.q.xh;
+        p.y = static_cast<uint8_t *>(a.q.y);
+        p.yt = 2 * a.q.yt;
+        p.yh = 2 * a.q.yh;
+        vec = vec && aligned(a.q.x, a.q.xt, a.q.xh) && aligned(a.q.y, a.q.yt, a.q.yh);
+    }
+    bool e4m3 = false;
+    if (append) {
+        const qgemm_kv_cache *c = a.kv;
+        e4m3 = c->dtype == QGEMM_E4M3;
+        p.x[1] = static_cast<const uint8_t *>(a.k);
+        p.x[2] = static_cast<const uint8_t *>(a.v);
+        p.xt[1] = 2 * a.kt;
+        p.xh[1] = 2 * a.kh;
+        p.xt[2] = 2 * a.vt;
+        p.xh[2] = 2 * a.vh;
+        vec = vec && aligned(a.k, a.kt, a.kh) && aligned(a.v, a.vt, a.vh);
+        p.hkv = (int32_t)c->heads;
+        p.pk[0] = c->k + a.layer * c->st[0];
+        p.pk[1] = c->v + a.layer * c->st[0];
+        p.extent = c->extent - a.layer * c->st[0];
+        p.page = c->st[1];
+        p.head = c->st[2];
+        p.token = c->st[3];
+        if (e4m3) {
+            p.ps[0] = c->ks + a.layer * c->sst[0];
+            p.ps[1] = c->vs + a.layer * c->sst[0];
+            p.sextent = c->sextent - a.layer * c->sst[0];
+            p.spage = c->sst[1];
+            p.shead = c->sst[2];
+            p.stoken = c->sst[3];
+        }
+        p.page_size = (int32_t)c->page_size;
+        p.pages = (int32_t)c->pages;
+        p.seqs = a.seqs;
+        p.table = a.table;
+        p.table_stride = a.table_stride;
+        p.max_seqs = a.max_seqs;
+        p.max_pages = a.max_pages;
+    }
+    p.pos = a.pos;
+    p.T = a.T;
+    p.d = a.d;
+    p.min_exp = a.bf16 ? -127 : -15;
+    p.mscale = 1.0f;
+    p.sign = a.inverse ? -1.0f : 1.0f;
+    p.err = ctx.err;
+    bool inter = true;
+    if (a.rope) {
+        p.rot = a.rope->rot_dim;
+        p.mscale = a.rope->mscale;
+        inter = a.rope->interleaved != 0;
+        for (int i = 0; i < p.rot / 2; ++i) fr.f[i] = a.rope->freq[i];
+        if (!inter) vec = vec && p.rot % 16 == 0;
+    }
+    // Tokens a block: enough rows for two passes of every lane's four, so that the sines are
+    // shared and the blocks are few; with few tokens one token a block and its heads dealt to
+    // several blocks, two blocks an SM.
+    const int heads = p.hq + 2 * p.hkv;
+    const int lpr = a.d <= 64 ? 8 : (a.d <= 128 ? 16 : 32);
+    const int rpp = qg::THREADS / lpr;
+    const int64_t slots = 2 * (int64_t)ctx.num_sms;
+    int tpc = (2 * qg::ROWS * rpp + heads - 1) / heads;
+    if (tpc > qg::MAX_TPC) tpc = qg::MAX_TPC;
+    while (tpc > 1 && ((int64_t)a.T + tpc - 1) / tpc < slots) --tpc;
+    p.tpc = tpc;
+    int64_t split = a.T < slots ? slots / a.T : 1;
+    const int64_t most = (heads + rpp - 1) / rpp;
+    p.hsplit = (int32_t)(split < most ? split : most);
+    const dim3 grid((unsigned)((a.T + tpc - 1) / tpc), (unsigned)p.hsplit);
+    const size_t smem = sizeof(float) * (size_t)tpc * (p.rot > 0 ? p.rot : 1);
+    return a.bf16 ? qg::launch_type<qg::TypeBF16>(p, fr, inter, vec, e4m3, grid, smem, ctx.stream)
+                  : qg::launch_type<qg::TypeF16>(p, fr, inter, vec, e4m3, grid, smem, ctx.stream);
+}
+
+}  // namespace qgi

@@ -58,9 +58,10 @@ typedef enum {
     QGEMM_E4M3 = 1,  /* FP8 E4M3 (OCP, no infinity), one byte per element                    */
     QGEMM_INT8 = 2,  /* two's complement int8, one byte per element                          */
     QGEMM_INT4 = 3,  /* two's complement int4, two per byte, even k in the low nibble        */
-    QGEMM_E2M1 = 4   /* FP4 E2M1 (sign, 2 exponent bits with bias 1, 1 mantissa bit; values
+    QGEMM_E2M1 = 4,  /* FP4 E2M1 (sign, 2 exponent bits with bias 1, 1 mantissa bit; values
                         0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), two per byte, even k in
                         the low nibble                                                        */
+    QGEMM_BF16 = 5   /* bfloat16: activations and caches of the decode-serving calls only     */
 } qgemm_dtype;
 
 /* Opaque, host-side, NON-owning view of one quantized matrix [rows, k]. */
@@ -371,6 +372,166 @@ qgemm_status qgemm_w8_gemv_ex(const void *X_f16, int64_t ldx, int64_t M, const q
                               void *Y_f16, int64_t ldy, const qgemm_epilogue *epilogue,
                               void *stream);
 
+/* ------------------------------------------------------------------- decode serving
+ * Rotary positions, a paged key-value cache, attention of one new token per sequence over it, and
+ * the cache's page operations.  The pages have no counterpart: these are the calls a decode loop
+ * makes between this library's products.
+ *
+ * A cache is two planes of rows of d elements, [layers, pages, heads, page_size]: keys and values.
+ * Token t of a sequence lies in row t % page_size of the page its page-table row names at t /
+ * page_size.  The page table ([max_seqs, max_pages] int32, row stride in entries), the lengths
+ * (int32 [max_seqs], tokens) and the reference counts (int32 [pages], 0 = free) are device memory of
+ * the caller; a sequence of n tokens holds the first ceil(n / page_size) entries of its row.
+ *
+ * Indices the kernels read from device memory are checked there: a sequence number, position,
+ * length or page-table entry out of range sets bit 64 of the device error word, and what it names is
+ * skipped (nothing is read or written through it; attention treats the token as absent).
+ *
+ * Activations are QGEMM_F16 or QGEMM_BF16, a cache has their type or is QGEMM_E4M3 with one UE8M0
+ * scale per 32 elements of a row.  Strides of activations are in ELEMENTS, of cache planes in BYTES. */
+
+/* Frequencies of the rotary positions: pair i of rot_dim / 2 turns by w_i radians per position. */
+typedef struct qgemm_rotation qgemm_rotation;
+
+enum {
+    QGEMM_ROPE_PLAIN = 0,    /* w_i = base^(-2 i / rot_dim)                                    */
+    QGEMM_ROPE_LINEAR = 1,   /* w_i / factor (interpolated positions)                          */
+    QGEMM_ROPE_BY_PARTS = 2  /* pairs that turn at least high_turns times in original_len
+                                positions keep w_i, those that turn at most low_turns times take
+                                w_i / factor, linear in the number of turns between            */
+};
+
+/* Make the frequencies (host memory only; made once, used by every call).
+ *   rot_dim      elements of a head that are rotated, the first ones; even, 2 .. 256.
+ *   interleaved  1: pairs (2i, 2i + 1); 0: pairs (i, i + rot_dim / 2).
+ *   base         > 0.  scaling: QGEMM_ROPE_*; factor > 0 unless plain; original_len > 0 and
+ *                high_turns > low_turns by parts.
+ *   mscale       factor on the rotated elements (1: none).
+ * Frequencies are 64-bit fractions of a turn, so angles are exact at any 32-bit position.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE (rot_dim > 256). */
+qgemm_status qgemm_create_rope(qgemm_rotation **out, int64_t rot_dim, int32_t interleaved, double base,
+                               int32_t scaling, double factor, double original_len, double low_turns,
+                               double high_turns, double mscale);
+/* Free it.  NULL is a no-op. */
+void qgemm_destroy_rope(qgemm_rotation *rope);
+
+/* Y[t, h] = X[t, h] with its first rot_dim elements rotated to positions[t] (int32, any value);
+ * the others are copied.  inverse = 1 rotates back (the transpose, times mscale): the gradient of
+ * X from that of Y.  fp32 arithmetic, one rounding.
+ *   X, Y  device [T, heads, d], rot_dim <= d <= 256, a contiguous last dimension; Y is X with the same
+ *         strides (in place) or does not overlap it; Y's own rows must not overlap.
+ * 16-byte aligned bases, strides and d in multiples of 8 (and rot_dim of 16, unless interleaved) take
+ * the vector path; any 2-byte alignment works.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, UNSUPPORTED_DTYPE, MISALIGNED; CUDA. */
+qgemm_status qgemm_rope(const void *X, int64_t x_token_stride, int64_t x_head_stride, void *Y,
+                        int64_t y_token_stride, int64_t y_head_stride, int32_t dtype, int64_t T,
+                        int64_t heads, int64_t d, const int32_t *positions, const qgemm_rotation *rope,
+                        int32_t inverse, void *stream);
+
+/* Non-owning view of a paged cache. */
+typedef struct qgemm_kv_cache qgemm_kv_cache;
+
+/* Create a view of a cache of `pages` pages in each of `layers` layers.
+ *   dtype          QGEMM_F16, QGEMM_BF16 or QGEMM_E4M3.
+ *   k, v           device planes; element (l, p, h, t, c) at base + l * strides[0] + p * strides[1] +
+ *                  h * strides[2] + t * strides[3] bytes + c elements.  16-byte aligned bases, strides in
+ *                  multiples of 16; the rows of a plane must not overlap.
+ *   k_scales,      E4M3 only: UE8M0 planes, d / 32 bytes a row at the same indices under
+ *   v_scales       scale_strides, in rows of 4 bytes (d = 64 uses the first two): 4-byte aligned bases,
+ *                  strides in multiples of 4.  NULL otherwise.
+ * Requirements: d is 64 or 128; layers, heads, page_size in 1 .. 65536, pages in 1 .. 2^30.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, UNSUPPORTED_DTYPE, MISALIGNED. */
+qgemm_status qgemm_create_kv_cache(qgemm_kv_cache **out, int32_t dtype, int64_t layers, int64_t pages,
+                                   int64_t heads, int64_t page_size, int64_t d, void *k, void *v,
+                                   const int64_t *strides, uint8_t *k_scales, uint8_t *v_scales,
+                                   const int64_t *scale_strides);
+/* Free the view (host memory only).  NULL is a no-op. */
+void qgemm_destroy_kv_cache(qgemm_kv_cache *kv);
+
+/* Store the keys and values of T new tokens in a layer of the cache, keys rotated to their
+ * positions, and rotate the tokens' queries beside them (one launch).  Token t goes to position
+ * positions[t] of sequence seqs[t]; its page must be held already (qgemm_kv_resize).  Two tokens with one slot
+ * leave either's row.
+ *   K, V      device [T, heads of the cache, d] 16-bit, strides in elements.
+ *   rope      NULL: no rotation.
+ *   Q, Q_out  device [T, q_heads, d]: rotated into Q_out (may be Q itself); q_heads = 0: none.
+ * A 16-bit cache stores the rotation rounded once.  An E4M3 cache stores, per 32 elements, X =
+ * floor(log2(amax)) - 8 as byte X + 127 and e4m3_rn(x * 2^-X) saturated to +-448, from the fp32
+ * rotation; an all-zero block gets byte 127, and X stops at -15 for F16 activations (every stored value
+ * is then a half).  NaN elements become E4M3's NaN.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, UNSUPPORTED_DTYPE, MISALIGNED (nothing enqueued); CUDA. */
+qgemm_status qgemm_kv_append(const qgemm_kv_cache *kv, int64_t layer, const void *K,
+                             int64_t k_token_stride, int64_t k_head_stride, const void *V,
+                             int64_t v_token_stride, int64_t v_head_stride, int32_t dtype, int64_t T,
+                             const int32_t *seqs, const int32_t *positions, const int32_t *page_table,
+                             int64_t table_stride, int64_t max_seqs, int64_t max_pages,
+                             const qgemm_rotation *rope, const void *Q, int64_t q_token_stride,
+                             int64_t q_head_stride, int64_t q_heads, void *Q_out,
+                             int64_t qo_token_stride, int64_t qo_head_stride, void *stream);
+
+/* Bytes of workspace qgemm_paged_attention takes on the current device for up to `batch` sequences
+ * and q_heads query heads.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE; CUDA. */
+qgemm_status qgemm_paged_attention_workspace_bytes(const qgemm_kv_cache *kv, int64_t batch,
+                                                   int64_t q_heads, int64_t *bytes);
+
+/* Attention of one new token per sequence over the cache: for sequence b and query head h, with
+ * g = h / (q_heads / heads) its key-value head and j over the last `window` (0: all) of the first
+ * lens[s] tokens, s = seqs[b] (seqs NULL: b),
+ *   O[b, h, :] = sum_j softmax_j(scale * <Q[b, h, :], K_j[g]>) V_j[g],
+ *   lse[b, h]  = ln sum_j exp(scale * <Q[b, h, :], K_j[g]>)     (lse may be NULL; fp32 [batch, q_heads]).
+ * A sequence without tokens gives O = 0 and lse = -inf.  Scores, softmax and sums are fp32; E4M3
+ * values are the nearest half (bfloat16) to code * 2^(byte - 127).  Tokens outside the range are not read.
+ *   Q, O       device [batch, q_heads, d], 16-byte aligned, strides in multiples of 8 elements; O's rows must
+ *              not overlap.  q_heads is a multiple of the cache's heads.
+ *   workspace  device, 16-byte aligned, qgemm_paged_attention_workspace_bytes at least.  Its bytes
+ *              must be ZERO before its first call; every call leaves it ready for the next one on the
+ *              same stream, of any batch and q_heads that fit it, on caches of the same d.  Calls that
+ *              may overlap need workspaces of their own.
+ * Launch: one kernel of up to one CTA per SM; the lengths are read on the device, so a captured call
+ * serves any lengths.  Repeatable bit for bit for the same inputs and SM count.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, UNSUPPORTED_DTYPE, MISALIGNED (nothing enqueued); CUDA. */
+qgemm_status qgemm_paged_attention(const void *Q, int64_t q_batch_stride, int64_t q_head_stride,
+                                   int32_t dtype, int64_t batch, int64_t q_heads, const qgemm_kv_cache *kv,
+                                   int64_t layer, const int32_t *page_table, int64_t table_stride,
+                                   int64_t max_seqs, int64_t max_pages, const int32_t *lens,
+                                   const int32_t *seqs, void *O, int64_t o_batch_stride,
+                                   int64_t o_head_stride, float *lse, float scale, int64_t window,
+                                   void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Give sequence seqs[i] new_lens[i] tokens, i < n (new_lens NULL: none, which frees it).  Shrinking
+ * gives back the pages past the new length (entries become -1); growing takes free pages, and a
+ * partly filled last page that other sequences hold too becomes a copy of its own first.  All
+ * releases come before all growth; free pages go to the items in order, lowest first.  An item whose
+ * pages (with those of the items before it) exceed the free ones keeps its length and sets bit 128 of the
+ * device error word.  The sequences of one call must differ.
+ * Scratch (also qgemm_kv_fork, qgemm_kv_compact): about 4 bytes a page and 24 an item from the library's pool
+ * on `stream`.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED (nothing enqueued); CUDA. */
+qgemm_status qgemm_kv_resize(const qgemm_kv_cache *kv, int32_t *page_table, int64_t table_stride,
+                             int64_t max_seqs, int64_t max_pages, int32_t *lens, int32_t *refs,
+                             const int32_t *seqs, const int32_t *new_lens, int64_t n, void *stream);
+
+/* Make sequence children[i] a copy of parents[i], i < n, in every layer: what the child's slot held
+ * is given back, whole pages are shared (their counts rise), a partly filled last page is copied to a free
+ * one (lowest first, in the order of the items).  A child whose page cannot be had is left empty and bit 128
+ * of the device error word is set.  Children must differ from one another and from every parent; a
+ * parent may appear several times.  Errors: as qgemm_kv_resize. */
+qgemm_status qgemm_kv_fork(const qgemm_kv_cache *kv, int32_t *page_table, int64_t table_stride,
+                           int64_t max_seqs, int64_t max_pages, int32_t *lens, int32_t *refs,
+                           const int32_t *parents, const int32_t *children, int64_t n, void *stream);
+
+/* Move the pages in use to the front of the cache, in every layer: with U pages in use, those at U
+ * and above move, in order, to the free ones below U; counts and every sequence's entries follow.  Pages
+ * past U keep their old bytes.  Errors: as qgemm_kv_resize. */
+qgemm_status qgemm_kv_compact(const qgemm_kv_cache *kv, int32_t *page_table, int64_t table_stride,
+                              int64_t max_seqs, int64_t max_pages, int32_t *lens, int32_t *refs,
+                              void *stream);
+
+/* Copy page src[i] to page dst[i], i < n (device int32), in every layer: keys, values and scales.  No
+ * dst may be another item's src or dst.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED; CUDA. */
+qgemm_status qgemm_kv_copy_pages(const qgemm_kv_cache *kv, const int32_t *src, const int32_t *dst,
+                                 int64_t n, void *stream);
+
 /* Dequantise-only debug kernel: out[r, k] = decode(t.data[r, k]) * 2^(t.scales[r, k/32] - 127)
  * as fp32 (fp16 views: the value itself), written densely as [rows, k] row-major.  Exists so
  * that the decoded operand values can be compared bit for bit with the CPU reference, as the
@@ -393,7 +554,9 @@ const char *qgemm_last_error_message(void);
  * *code_out (may be NULL) receives the raw word: 0 = no kernel gave up; otherwise bits name the
  * wait that ran out (1 producer, 2 MMA issuer, 4 epilogue, 8 drain, 16 test wait) or, in the
  * debug build (libqgemm_debug.so, compiled with QGEMM_DEBUG), 32 = a kernel's own bounds check
- * failed and the access was skipped.
+ * failed and the access was skipped.  Two bits of the decode-serving calls name no wait: 64 = an
+ * index in device memory was out of range and what it named was skipped, 128 = a page operation found
+ * too few free pages.
  * Returns QGEMM_ERR_TIMEOUT if the word was non-zero, QGEMM_ERR_CUDA if synchronisation failed. */
 qgemm_status qgemm_poll_device_error(void *stream, uint32_t *code_out);
 
