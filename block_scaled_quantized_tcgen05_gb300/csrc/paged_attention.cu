@@ -8,25 +8,27 @@
 // row is read once (per 16 query heads).
 //
 // Bound: HBM.  A cached key and value of d = 128 take 512 bytes (fp16) or 264 (E4M3) and 4 x 128
-// flops per query head, so at 8 heads a key-value head the product needs about an eighth of the
+// flops per query head, so at 8 heads a key-value head the products need about an eighth of the
 // legacy tensor rate the stream leaves time for.  The matrix unit is therefore used through
-// mma.sync with the 16 query rows as its M: scores come out in the layout the second product takes
-// its left operand in, so the probabilities never leave the registers, and a tcgen05 tile of 64 or
-// 128 rows would be filled to an eighth and send scores and probabilities through TMEM and shared
-// memory.
+// mma.sync, with cached rows as the left operand: 16 tokens are the M of the scores S^T = K Q^T, 16
+// elements of d that of O^T = V^T P^T, and 8 query heads the N of both, so nothing is padded at 8 heads a
+// key-value head; P reaches the second product's layout by a register transpose (movmatrix).  A tcgen05
+// tile would take its 128 rows of K and V straight from shared memory, but E4M3 rows have to pass
+// through registers to meet their scales, and scores and probabilities would go through TMEM and
+// shared memory between the two products of every tile.
 //
 // Work.  A unit is (sequence, key-value head, up to 16 of its query heads); its tokens are cut into
-// tiles of TILE and the tiles of all units, in order, are dealt to the CTAs in equal contiguous
-// ranges, so that ragged lengths load every SM alike whatever the batch.  Each CTA finds its range
-// from the lengths on the device (the call is the same for any lengths, so it can be captured).  A
-// unit cut by range boundaries leaves fp32 partial rows (max, sum, weighted values) in the
-// workspace; the CTA that arrives last merges them in the order of the ranges, so the bits do not
-// depend on timing, and nothing waits on another CTA.
+// tiles of 128, and the tiles of all units, in order, are dealt to the CTAs in equal contiguous
+// ranges, so that ragged lengths load every SM alike whatever the batch.  A unit counts EXTRA tiles more
+// than it has, for its start and end.  Each CTA finds its range from the lengths on the device (the call
+// is the same for any lengths, so it can be captured).  A unit cut by range boundaries leaves fp32 partial
+// rows (max, sum, weighted values) in the workspace; the CTA that arrives last merges them in the order
+// of the ranges, so the bits do not depend on timing, and nothing waits on another CTA.
 //
-// Inside a CTA the warps are on their own: each takes STEP tokens of every tile, copies their rows
-// into its own ring of shared memory with cp.async (STAGES steps ahead, across unit boundaries: with
-// 8 warps about 190 KB an SM are in flight) and keeps its own running maximum, sum and output.
-// They meet once per unit, to merge.
+// Inside a CTA the warps are on their own: each takes 16 tokens of every tile, copies their rows into
+// its own ring of shared memory with cp.async (two steps ahead or more, across unit boundaries: about
+// 130 KB an SM are in flight) and keeps its own running maximum, sum and output.  They meet once per
+// unit, to merge.
 //
 // Masked places (past the length, outside the window, a bad page) are never read: their rows are
 // zero-filled and their scores -inf, so whatever the pages hold there (NaN of an earlier owner) stays
@@ -34,10 +36,11 @@
 //
 // Precision: scores, softmax and sums in fp32.  P, times 2^15 so that the halves' range is used down to
 // 2^-39 of the largest weight, is split into two 16-bit values, hi = p rounded towards zero and lo = rn(p -
-// hi) (relative error 2^-21 in fp16, 2^-15 in bf16): with up to 8 query heads the lower 8 of the tile's 16
-// rows carry lo at no cost, above 8 it takes a second product.  lo is kept above zero, at 2^-39 of the
-// largest weight at least, so that an infinite value stays one (0 x inf and inf - inf would be NaN).  E4M3
+// hi) (relative error 2^-21 in fp16, 2^-15 in bf16), and both are multiplied: the matrix unit has the time.
+// lo is kept above zero, at 2^-39 of the largest weight at least, so that an infinite value stays one (0 x
+// inf and inf - inf would be NaN).  E4M3
 // values become the nearest half (bf16) to code * 2^(byte - 127): exact for every block the append writes.
+#include <atomic>
 #include <type_traits>
 
 #include "kv_common.cuh"
@@ -47,7 +50,10 @@ namespace {
 
 constexpr int NWARPS = 8;
 constexpr int THREADS = 32 * NWARPS;
-constexpr int ROWS = 16;                    // query rows of a unit (the mma's M)
+constexpr int ROWS = 16;                    // query heads of a unit at most
+constexpr int STEP = 16;                    // tokens of a warp's step (the scores' M)
+constexpr int TILE = STEP * NWARPS;
+constexpr int EXTRA = 1;                    // what a unit costs beyond its tiles, in tiles
 constexpr float P_SHIFT = 15.0f;            // P is held times 2^P_SHIFT
 constexpr float P_LEAST = 0x1p-24f;         // the smallest half
 constexpr float LN2 = 0.69314718055994531f;
@@ -64,32 +70,33 @@ struct AttnParams {
     int64_t table_stride;
     int32_t B, hq, hkv, group, chunks;      // chunks: units per key-value head
     int32_t max_seqs, max_pages, page_size, pages, window;
+    bool one_page;                          // page_size is a multiple of STEP
     float scale_log2;
     int32_t *counters;
     float *partial;
     unsigned *err;
 };
 
-template <class TY_, int D_, bool E4M3_, bool WIDE_>
+template <class TY_, int D_, bool E4M3_, int NH_>
 struct Cfg {
     using TY = TY_;
     static constexpr int D = D_;
     static constexpr bool E4M3 = E4M3_;
-    static constexpr bool WIDE = WIDE_;                  // more than 8 query heads a unit
+    static constexpr int NH = NH_;                       // groups of 8 query heads of a unit
     static constexpr int ROWB = E4M3 ? D : 2 * D;        // bytes of a cached row
-    static constexpr int STEP = E4M3 ? 32 : 16;          // tokens of a warp's step
-    static constexpr int TILE = STEP * NWARPS;
     static constexpr int CHUNKS = ROWB / 16;             // 16-byte pieces of a row
     static constexpr int PLANE = STEP * ROWB;            // bytes of a step's keys (or values)
     static constexpr int SCALEB = E4M3 ? STEP * 4 : 0;   // scale bytes of a step's keys
     static constexpr int STAGEB = 2 * (PLANE + SCALEB);
-    // rows merged at a time: as many as leave room for three stages
-    static constexpr int MERGE_ROWS = E4M3 && D == 128 ? 4 : 8;
+    // Two CTAs an SM where their registers (8 heads) and three stages each fit; otherwise one
+    static constexpr bool TWO = NH == 1 && STAGEB <= 4224;
+    static constexpr int MERGE_ROWS = TWO ? 2 : 8;       // heads merged at a time
     static constexpr int MERGEB = NWARPS * MERGE_ROWS * D * 4;
-    static constexpr int FIT = (224 * 1024 - MERGEB) / (NWARPS * STAGEB);
+    static constexpr int ROOM = (TWO ? 111 : 224) * 1024;
+    static constexpr int FIT = (ROOM - MERGEB) / (NWARPS * STAGEB);
     static constexpr int NSTAGES = FIT > 6 ? 6 : FIT;
     static constexpr int SMEM = NWARPS * NSTAGES * STAGEB + MERGEB;
-    static constexpr int NT = D / 8;                     // 8-column tiles of the output
+    static constexpr int MT = D / 16;                    // 16-element tiles of the output
     static constexpr int PARTIAL = ROWS * (D + 2);       // floats of a partial
 };
 
@@ -121,6 +128,13 @@ __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
                      : "r"(addr));
 }
 
+// The transpose of an 8 x 8 matrix of 16-bit values, a row's pairs over four lanes.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
@@ -130,6 +144,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
     uint2 v;
     asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
     return v;
 }
 __device__ __forceinline__ uint32_t lds8(uint32_t a) {
@@ -201,43 +220,54 @@ __device__ __forceinline__ bool far_scale(uint32_t byte) { return byte - 103u > 
 
 // A position in the work: which unit, and which of its tiles.  Held alike by every lane.
 struct Cursor {
+    int64_t pos;          // of the tile, in tiles and EXTRAs over all units
+    int64_t row;          // page-table row (element offset)
     int32_t b;            // sequence of the batch
     int32_t hc;           // key-value head * chunks + chunk
     int32_t tile, ntiles; // tile inside the unit, tiles of the unit
     int32_t first, n;     // tokens [first, n)
-    int64_t row;          // page-table row (element offset), -1: none
+    int32_t next_seq, next_len;   // of sequence b + 1, read ahead (-1: none)
 };
 
-__device__ __forceinline__ void seek(Cursor &c, const AttnParams &p, int b, int tile_tokens) {
-    c.b = b;
-    c.row = -1;
-    int32_t len = 0;
-    if (b < p.B) {
-        const int32_t seq = p.seqs ? p.seqs[b] : b;
-        if (seq >= 0 && seq < p.max_seqs) {
-            c.row = seq * p.table_stride;
-            len = p.lens[seq];
-        }
-    }
-    kvi::seen_range(len, p.max_pages * p.page_size, p.window, &c.first, &c.n);
-    c.ntiles = kvi::tiles_of(c.n - c.first, tile_tokens);
+__device__ __forceinline__ int32_t sequence(const AttnParams &p, int b) {
+    if (b >= p.B) return -1;
+    const int32_t seq = p.seqs ? p.seqs[b] : b;
+    return seq >= 0 && seq < p.max_seqs ? seq : -1;
 }
-
-__device__ __forceinline__ void advance(Cursor &c, const AttnParams &p, int tile_tokens) {
+// Tokens, and tiles from the 16-token boundary before the first one on.
+__device__ __forceinline__ int32_t extent(const AttnParams &p, int32_t len, int32_t *first, int32_t *n) {
+    kvi::seen_range(len, p.max_pages * p.page_size, p.window, first, n);
+    return kvi::tiles_of(*n - *first / STEP * STEP, TILE);
+}
+__device__ __forceinline__ void read_ahead(Cursor &c, const AttnParams &p) {
+    c.next_seq = sequence(p, c.b + 1);
+    c.next_len = c.next_seq >= 0 ? p.lens[c.next_seq] : 0;
+}
+__device__ __forceinline__ void enter(Cursor &c, const AttnParams &p, int32_t seq, int32_t len) {
+    c.row = (seq >= 0 ? seq : 0) * p.table_stride;
+    c.ntiles = extent(p, len, &c.first, &c.n);
+}
+__device__ __forceinline__ void advance(Cursor &c, const AttnParams &p) {
+    ++c.pos;
     if (++c.tile < c.ntiles) return;
     c.tile = 0;
+    c.pos += EXTRA;
     if (++c.hc < p.hkv * p.chunks) return;
     c.hc = 0;
-    seek(c, p, c.b + 1, tile_tokens);
+    ++c.b;
+    enter(c, p, c.next_seq, c.next_len);
+    read_ahead(c, p);
 }
 
 template <class C>
-__global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
+    paged_attention_kernel(const __grid_constant__ AttnParams p) {
     using TY = typename C::TY;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_m[NWARPS][ROWS], s_l[NWARPS][ROWS];
     __shared__ int64_t s_scan[NWARPS];
-    __shared__ int32_t s_start[4];
+    __shared__ int64_t s_at;
+    __shared__ int32_t s_start[2];
     __shared__ uint32_t s_mask[NWARPS][C::NSTAGES];
     __shared__ int s_last;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -249,14 +279,14 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
     const int per = (p.B + THREADS - 1) / THREADS;
     const int lo_b = min(p.B, tid * per), hi_b = min(p.B, lo_b + per);
     int64_t mine = 0;
+    int32_t unit_first = 1;              // tiles of a unit of the piece's first sequence
     for (int b = lo_b; b < hi_b; ++b) {
-        Cursor c;
-        seek(c, p, b, C::TILE);
-        mine += (int64_t)c.ntiles * units_b;
-        if (blockIdx.x == 0) {
-            const int32_t seq = p.seqs ? p.seqs[b] : b;
-            if (c.row < 0 || p.lens[seq] != c.n) report_index(p.err);
-        }
+        int32_t first, n;
+        const int32_t seq = sequence(p, b), len = seq >= 0 ? p.lens[seq] : 0;
+        const int32_t tiles = extent(p, len, &first, &n);
+        if (b == lo_b) unit_first = tiles;
+        mine += (int64_t)(tiles + EXTRA) * units_b;
+        if (blockIdx.x == 0 && (seq < 0 || len != n)) report_index(p.err);
     }
     int64_t incl = mine;
 #pragma unroll
@@ -266,27 +296,30 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
     }
     if (lane == 31) s_scan[warp] = incl;
     __syncthreads();
-    int64_t before = incl - mine, total = 0;
+    int64_t at = incl - mine, W = 0;
 #pragma unroll
     for (int w = 0; w < NWARPS; ++w) {
-        if (w < warp) before += s_scan[w];
-        total += s_scan[w];
+        if (w < warp) at += s_scan[w];
+        W += s_scan[w];
     }
-    const int64_t W = total;
     const int64_t G = min((int64_t)gridDim.x, W);
     const int64_t cta = blockIdx.x;
     if (cta >= G) return;
     const int64_t begin = kvi::range_begin(W, G, cta), end = kvi::range_begin(W, G, cta + 1);
-    if (begin >= before && begin < before + mine) {
-        int64_t at = before;
+    if (begin >= at && begin < at + mine) {
+        int32_t tiles = unit_first;
         for (int b = lo_b; b < hi_b; ++b) {
-            Cursor c;
-            seek(c, p, b, C::TILE);
-            const int64_t n = (int64_t)c.ntiles * units_b;
+            if (b > lo_b) {
+                int32_t first, n;
+                const int32_t seq = sequence(p, b);
+                tiles = extent(p, seq >= 0 ? p.lens[seq] : 0, &first, &n);
+            }
+            const int64_t n = (int64_t)(tiles + EXTRA) * units_b;
             if (begin < at + n) {
+                const int32_t hc = (int32_t)((begin - at) / (tiles + EXTRA));
                 s_start[0] = b;
-                s_start[1] = (int32_t)((begin - at) / c.ntiles);
-                s_start[2] = (int32_t)((begin - at) % c.ntiles);
+                s_start[1] = hc;
+                s_at = at + (int64_t)hc * (tiles + EXTRA);
                 break;
             }
             at += n;
@@ -294,44 +327,55 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
     }
     __syncthreads();
 
-    Cursor use;          // the tile being computed
-    seek(use, p, s_start[0], C::TILE);
+    Cursor use;                          // the tile being computed
+    use.b = s_start[0];
     use.hc = s_start[1];
-    use.tile = s_start[2];
-    Cursor load = use;   // the tile whose pages are being looked up
-    int64_t left = end - begin;             // tiles to compute
-    int64_t to_load = left;
+    int64_t unit_at = s_at;              // where the unit begins in the whole order
+    {
+        const int32_t seq = sequence(p, use.b);
+        enter(use, p, seq, seq >= 0 ? p.lens[seq] : 0);
+        read_ahead(use, p);
+    }
+    use.tile = (int32_t)max((int64_t)0, begin - unit_at - EXTRA);
+    use.pos = unit_at + EXTRA + use.tile;
+    if (use.pos >= end) return;          // a range inside a unit's EXTRA
+    Cursor load = use;                   // the tile whose pages are being looked up
     const uint32_t ring = smem_u32(smem) + warp * (C::NSTAGES * C::STAGEB);
     float *merge = reinterpret_cast<float *>(smem + NWARPS * C::NSTAGES * C::STAGEB);
 
     // ---- page look-up of this warp's tokens of the tile `load` points at, one step ahead of the
-    // copies that use it: lane l holds token l's page
-    int32_t pg = -1, pt = -1;      // page-table entry and token (-1: none) of the looked-up step
-    int32_t phc = 0;               // its head
+    // copies that use it.  Steps begin at multiples of 16 tokens: with pages of a multiple of 16 tokens
+    // a step lies in one page, and every lane holds its entry; otherwise lane l holds token l's.
+    int32_t pg = -1, pt = 0;             // page-table entry, first token of the looked-up step
+    int32_t phc = 0, pfirst = 0, pn = 0; // its head and the tokens of its sequence
     auto look_up = [&] {
-        pt = -1;
-        if (to_load > 0) {
-            const int32_t t = load.first + load.tile * C::TILE + warp * C::STEP + lane;
+        pn = 0;
+        if (load.pos < end) {
+            pt = load.first / STEP * STEP + load.tile * TILE + warp * STEP;
             phc = load.hc;
-            if (lane < C::STEP && t < load.n) {
-                pt = t;
+            pfirst = load.first;
+            pn = load.n;
+            const int32_t t = p.one_page ? max(pt, pfirst) : pt + lane;
+            if ((p.one_page || lane < STEP) && t >= pfirst && t < pn)
                 pg = p.table[load.row + (uint32_t)t / (uint32_t)p.page_size];
-            }
-            --to_load;
-            if (to_load > 0) advance(load, p, C::TILE);
+            advance(load, p);
         }
     };
     // ---- the copies of the looked-up step into ring slot `slot`
+    constexpr int RPI = 32 / C::CHUNKS;          // rows an instruction of the warp copies
+    const int chunk = lane % C::CHUNKS, row0 = lane / C::CHUNKS;
     auto issue = [&](int slot) {
-        bool ok = pt >= 0;
-        int64_t off = 0, soff = 0;
+        const int32_t t = pt + lane;
+        bool ok = lane < STEP && t >= pfirst && t < pn;
+        const int32_t h = phc / p.chunks;
+        const uint32_t kd = ring + slot * C::STAGEB, vd = kd + C::PLANE;
+        int64_t off = 0, soff = 0;               // lane l: row l's place
         if (ok) {
             if (pg < 0 || pg >= p.pages) {
                 report_index(p.err);
                 ok = false;
             } else {
-                const int32_t r = pt - (int32_t)((uint32_t)pt / (uint32_t)p.page_size) * p.page_size;
-                const int32_t h = phc / p.chunks;
+                const int32_t r = t - (int32_t)((uint32_t)t / (uint32_t)p.page_size) * p.page_size;
                 off = pg * p.page + r * p.token + h * p.head;
                 if (C::E4M3) soff = pg * p.spage + r * p.stoken + h * p.shead;
                 ok = QG_IN_BOUNDS(p.err, off >= 0 && off + C::ROWB <= p.extent);
@@ -340,254 +384,264 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         }
         const uint32_t mask = __ballot_sync(0xFFFFFFFFu, ok);
         if (lane == 0) s_mask[warp][slot] = mask;
-        const uint32_t kd = ring + slot * C::STAGEB, vd = kd + C::PLANE;
-        constexpr int RPI = 32 / C::CHUNKS;      // rows an instruction of the warp copies
-        const int chunk = lane % C::CHUNKS;
+        if (p.one_page && mask == (1u << STEP) - 1) {
+            // a whole step of one page: rows a token stride apart
+            int64_t o = __shfl_sync(0xFFFFFFFFu, off, 0) + row0 * p.token + chunk * 16;
 #pragma unroll
-        for (int i = 0; i < C::STEP / RPI; ++i) {
-            const int r = i * RPI + lane / C::CHUNKS;
-            const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r) + chunk * 16;
-            const uint32_t n = (mask >> r) & 1 ? 16 : 0;
-            const uint32_t d = r * C::ROWB + swizzle<C>(r, chunk) * 16;
-            cp_async_16(kd + d, p.k + o, n);
-            cp_async_16(vd + d, p.v + o, n);
+            for (int i = 0; i < STEP / RPI; ++i) {
+                const int r = i * RPI + row0;
+                const uint32_t d = r * C::ROWB + swizzle<C>(r, chunk) * 16;
+                cp_async_16(kd + d, p.k + o, 16);
+                cp_async_16(vd + d, p.v + o, 16);
+                o += RPI * p.token;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < STEP / RPI; ++i) {
+                const int r = i * RPI + row0;
+                const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r) + chunk * 16;
+                const uint32_t n = (mask >> r) & 1 ? 16 : 0;
+                const uint32_t d = r * C::ROWB + swizzle<C>(r, chunk) * 16;
+                cp_async_16(kd + d, p.k + o, n);
+                cp_async_16(vd + d, p.v + o, n);
+            }
         }
         if (C::E4M3) {
-            cp_async_4(vd + C::PLANE + lane * 4, p.ks + soff, ok ? 4 : 0);
-            cp_async_4(vd + C::PLANE + C::SCALEB + lane * 4, p.vs + soff, ok ? 4 : 0);
+            // lanes 0-15: the keys' scale rows, lanes 16-31: the values'
+            const int r = lane % STEP;
+            const int64_t o = __shfl_sync(0xFFFFFFFFu, soff, r);
+            const uint8_t *src = lane < STEP ? p.ks : p.vs;
+            cp_async_4(vd + C::PLANE + lane * 4, src + o, (mask >> r) & 1 ? 4 : 0);
         }
     };
 
     // ---- state of the unit in progress
-    uint32_t qa[C::D / 16][4];              // query fragments
-    float acc[C::NT][4];
-    float m[2], l[2];
-    auto start_unit = [&] {
-        const int chunk = use.hc % p.chunks, h0 = (use.hc / p.chunks) * p.group + chunk * ROWS;
-        const int rows = min(ROWS, p.group - chunk * ROWS);
-        const uint8_t *q0 = p.q + use.b * p.qb + (h0 + g) * p.qh;
-        const uint8_t *q8 = q0 + 8 * p.qh;
-        const bool in0 = g < rows, in8 = C::WIDE && g + 8 < rows;
+    uint32_t qb[C::NH][C::D / 16][2];       // query fragments
+    float acc[C::NH][C::MT][4];             // rows of d, columns of heads 2 c4, 2 c4 + 1
+    float m[C::NH][2], l[C::NH][2];
+    auto load_queries = [&](const Cursor &c) {
+        const int part = c.hc % p.chunks, h0 = (c.hc / p.chunks) * p.group + part * ROWS;
+        const int rows = min(ROWS, p.group - part * ROWS);
 #pragma unroll
-        for (int kk = 0; kk < C::D / 16; ++kk) {
-            // 16-bit rows: the fragments ldmatrix gives; 8-bit rows: thread c4 holds 16 consecutive
-            // elements of every 64, four for each product, and the queries follow
-            const int e = C::E4M3 ? (kk / 4) * 64 + c4 * 16 + (kk % 4) * 4 : kk * 16 + c4 * 2;
-            const int e2 = C::E4M3 ? e + 2 : e + 8;
-            qa[kk][0] = in0 ? *reinterpret_cast<const uint32_t *>(q0 + 2 * e) : 0;
-            qa[kk][2] = in0 ? *reinterpret_cast<const uint32_t *>(q0 + 2 * e2) : 0;
-            qa[kk][1] = in8 ? *reinterpret_cast<const uint32_t *>(q8 + 2 * e) : 0;
-            qa[kk][3] = in8 ? *reinterpret_cast<const uint32_t *>(q8 + 2 * e2) : 0;
+        for (int n = 0; n < C::NH; ++n) {
+            const bool in = 8 * n + g < rows;
+            const uint8_t *q = p.q + c.b * p.qb + (h0 + 8 * n + g) * p.qh;
+#pragma unroll
+            for (int kk = 0; kk < C::D / 16; ++kk) {
+                // 16-bit rows: the fragments ldmatrix gives; 8-bit rows: thread c4 holds 16 consecutive
+                // elements of every 64, four for each product, and the queries follow
+                const int e = C::E4M3 ? (kk / 4) * 64 + c4 * 16 + (kk % 4) * 4 : kk * 16 + c4 * 2;
+                const int e2 = C::E4M3 ? e + 2 : e + 8;
+                qb[n][kk][0] = in ? *reinterpret_cast<const uint32_t *>(q + 2 * e) : 0;
+                qb[n][kk][1] = in ? *reinterpret_cast<const uint32_t *>(q + 2 * e2) : 0;
+            }
         }
+    };
+    auto clear = [&] {
 #pragma unroll
-        for (int j = 0; j < C::NT; ++j)
+        for (int n = 0; n < C::NH; ++n) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
-        m[0] = m[1] = -INFINITY;
-        l[0] = l[1] = 0.0f;
+            for (int j = 0; j < C::MT; ++j) acc[n][j][0] = acc[n][j][1] = acc[n][j][2] = acc[n][j][3] = 0.0f;
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.0f;
+        }
     };
 
-    // ---- one step: scores of STEP tokens, the running softmax, the weighted values
+    // ---- one step: scores of 16 tokens, the running softmax, the weighted values
     auto step = [&](int slot, auto fast_tag) {
         [[maybe_unused]] constexpr bool FAST = decltype(fast_tag)::value;
         const uint32_t kd = ring + slot * C::STAGEB, vd = kd + C::PLANE;
         const uint32_t mask = s_mask[warp][slot];
-        float s[C::STEP / 8][4];
+        // two accumulators a group of heads, so that the products' chains are half as long
+        float s[C::NH][4], s2[C::NH][4];
 #pragma unroll
-        for (int j = 0; j < C::STEP / 8; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.0f;
+        for (int n = 0; n < C::NH; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[n][i] = s2[n][i] = 0.0f;
+        auto score = [&](int kk, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+            for (int n = 0; n < C::NH; ++n)
+                mma16816(TY::BF16, kk % 2 ? s2[n] : s[n], a0, a1, a2, a3, qb[n][kk][0], qb[n][kk][1]);
+        };
         if constexpr (!C::E4M3) {
 #pragma unroll
             for (int kk = 0; kk < C::D / 16; ++kk) {
-                uint32_t b[4];       // lanes 0-15: tokens at piece 2 kk, lanes 16-31: 2 kk + 1
+                uint32_t a[4];       // tokens 0-7 and 8-15 of piece 2 kk, then of 2 kk + 1
                 const int r = lane % 16, ch = 2 * kk + lane / 16;
-                ldsm4<false>(kd + r * C::ROWB + swizzle<C>(r, ch) * 16, b);
-                mma16816(TY::BF16, s[0], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b[0], b[2]);
-                mma16816(TY::BF16, s[1], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b[1], b[3]);
+                ldsm4<false>(kd + r * C::ROWB + swizzle<C>(r, ch) * 16, a);
+                score(kk, a[0], a[1], a[2], a[3]);
             }
         } else {
             const uint32_t ksd = vd + C::PLANE;
 #pragma unroll
-            for (int j = 0; j < C::STEP / 8; ++j) {
-                const int r = 8 * j + g;
-#pragma unroll
-                for (int hf = 0; hf < C::D / 64; ++hf) {
-                    const uint4 w = lds128(kd + r * C::ROWB + swizzle<C>(r, 4 * hf + c4) * 16);
-                    const uint32_t byte = lds8(ksd + r * 4 + 2 * hf + c4 / 2);
-                    const Scale2 sc = make_scale<TY>(byte, byte);
-                    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t b0 = decode2<TY, FAST>(uint16_t(ww[i] & 0xFFFF), sc);
-                        const uint32_t b1 = decode2<TY, FAST>(uint16_t(ww[i] >> 16), sc);
-                        const int kk = 4 * hf + i;
-                        mma16816(TY::BF16, s[j], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b0, b1);
-                    }
-                }
-            }
-        }
-        // scores in units of log 2; masked ones -inf
-        constexpr uint32_t ALL = C::STEP == 32 ? 0xFFFFFFFFu : (1u << (C::STEP % 32)) - 1u;
-#pragma unroll
-        for (int j = 0; j < C::STEP / 8; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[j][i] *= p.scale_log2;
-        if (mask != ALL) {
-#pragma unroll
-            for (int j = 0; j < C::STEP / 8; ++j)
+            for (int hf = 0; hf < C::D / 64; ++hf) {
+                const uint4 x = lds128(kd + g * C::ROWB + swizzle<C>(g, 4 * hf + c4) * 16);
+                const uint4 y = lds128(kd + (g + 8) * C::ROWB + swizzle<C>(g + 8, 4 * hf + c4) * 16);
+                const uint32_t bx = lds8(ksd + g * 4 + 2 * hf + c4 / 2);
+                const uint32_t by = lds8(ksd + (g + 8) * 4 + 2 * hf + c4 / 2);
+                const Scale2 sx = make_scale<TY>(bx, bx), sy = make_scale<TY>(by, by);
+                const uint32_t xx[4] = {x.x, x.y, x.z, x.w}, yy[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (!((mask >> (8 * j + 2 * c4 + (i & 1))) & 1)) s[j][i] = -INFINITY;
+                    score(4 * hf + i, decode2<TY, FAST>(uint16_t(xx[i] & 0xFFFF), sx),
+                          decode2<TY, FAST>(uint16_t(yy[i] & 0xFFFF), sy),
+                          decode2<TY, FAST>(uint16_t(xx[i] >> 16), sx),
+                          decode2<TY, FAST>(uint16_t(yy[i] >> 16), sy));
+            }
         }
-        constexpr int NR = C::WIDE ? 2 : 1;
+        // scores in units of log 2, masked ones -inf: [0], [1] of token g, [2], [3] of token g + 8
+#pragma unroll
+        for (int n = 0; n < C::NH; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[n][i] = (s[n][i] + s2[n][i]) * p.scale_log2;
+        if (mask != (1u << STEP) - 1) {
+            const bool in0 = (mask >> g) & 1, in8 = (mask >> (g + 8)) & 1;
+#pragma unroll
+            for (int n = 0; n < C::NH; ++n) {
+                if (!in0) s[n][0] = s[n][1] = -INFINITY;
+                if (!in8) s[n][2] = s[n][3] = -INFINITY;
+            }
+        }
         bool grown = false;
-        float nm[2];
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            float x = m[r];
-#pragma unroll
-            for (int j = 0; j < C::STEP / 8; ++j) x = fmaxf(x, fmaxf(s[j][2 * r], s[j][2 * r + 1]));
-            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
-            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
-            nm[r] = x;
-            grown = grown || x > m[r];
-        }
+        for (int n = 0; n < C::NH; ++n)
+            grown = grown || fmaxf(s[n][0], s[n][2]) > m[n][0] || fmaxf(s[n][1], s[n][3]) > m[n][1];
         if (__any_sync(0xFFFFFFFFu, grown)) {
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                // m = -inf has nothing to scale (its sums are zero)
-                const float f = m[r] == -INFINITY ? 0.0f : ex2(m[r] - nm[r]);
-                m[r] = nm[r];
-                l[r] *= f;
+            for (int n = 0; n < C::NH; ++n)
 #pragma unroll
-                for (int j = 0; j < C::NT; ++j) {
-                    acc[j][2 * r] *= f;
-                    acc[j][2 * r + 1] *= f;
-                    if (!C::WIDE) {
-                        acc[j][2] *= f;
-                        acc[j][3] *= f;
+                for (int i = 0; i < 2; ++i) {
+                    float x = fmaxf(m[n][i], fmaxf(s[n][i], s[n][i + 2]));
+                    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+                    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+                    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+                    // m = -inf has nothing to scale (its sums are zero)
+                    const float f = m[n][i] == -INFINITY ? 0.0f : ex2(m[n][i] - x);
+                    m[n][i] = x;
+                    l[n][i] *= f;
+#pragma unroll
+                    for (int j = 0; j < C::MT; ++j) {
+                        acc[n][j][i] *= f;
+                        acc[n][j][i + 2] *= f;
                     }
                 }
+        }
+        uint32_t hi[C::NH][2], lo[C::NH][2];
+#pragma unroll
+        for (int n = 0; n < C::NH; ++n) {
+            const float m0 = m[n][0] == -INFINITY ? 0.0f : m[n][0] - P_SHIFT;
+            const float m1 = m[n][1] == -INFINITY ? 0.0f : m[n][1] - P_SHIFT;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float a = ex2(s[n][2 * i] - m0), b = ex2(s[n][2 * i + 1] - m1);
+                l[n][0] += a;
+                l[n][1] += b;
+                const uint32_t h = TY::pack_down(a, b);
+                const float2 f = TY::unpack(h);
+                hi[n][i] = transpose8(h);
+                lo[n][i] = transpose8(TY::pack(fmaxf(a - f.x, P_LEAST), fmaxf(b - f.y, P_LEAST)));
             }
         }
-        uint32_t hi[C::STEP / 8][2], lo[C::STEP / 8][2];
+        auto weigh = [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            const float mm = m[r] == -INFINITY ? 0.0f : m[r] - P_SHIFT;
-#pragma unroll
-            for (int j = 0; j < C::STEP / 8; ++j) {
-                const float a = ex2(s[j][2 * r] - mm), b = ex2(s[j][2 * r + 1] - mm);
-                l[r] += a + b;
-                hi[j][r] = TY::pack_down(a, b);
-                const float2 h = TY::unpack(hi[j][r]);
-                lo[j][r] = TY::pack(fmaxf(a - h.x, P_LEAST), fmaxf(b - h.y, P_LEAST));
-            }
-        }
-        auto weigh = [&](float (&o)[4], int t, uint32_t b0, uint32_t b1) {
-            // tokens 16 t .. 16 t + 15 of the step
-            if (C::WIDE) {
-                mma16816(TY::BF16, o, hi[2 * t][0], hi[2 * t][1], hi[2 * t + 1][0], hi[2 * t + 1][1], b0, b1);
-                mma16816(TY::BF16, o, lo[2 * t][0], lo[2 * t][1], lo[2 * t + 1][0], lo[2 * t + 1][1], b0, b1);
-            } else {
-                mma16816(TY::BF16, o, hi[2 * t][0], lo[2 * t][0], hi[2 * t + 1][0], lo[2 * t + 1][0], b0, b1);
+            for (int n = 0; n < C::NH; ++n) {
+                mma16816(TY::BF16, acc[n][j], a0, a1, a2, a3, hi[n][0], hi[n][1]);
+                mma16816(TY::BF16, acc[n][j], a0, a1, a2, a3, lo[n][0], lo[n][1]);
             }
         };
         if constexpr (!C::E4M3) {
 #pragma unroll
-            for (int jj = 0; jj < C::NT / 2; ++jj) {
-                uint32_t b[4];       // tokens 0-7 and 8-15 of columns 16 jj .. + 7, then of + 8 .. + 15
-                const int r = lane % 16, ch = 2 * jj + lane / 16;
-                ldsm4<true>(vd + r * C::ROWB + swizzle<C>(r, ch) * 16, b);
-                weigh(acc[2 * jj], 0, b[0], b[1]);
-                weigh(acc[2 * jj + 1], 0, b[2], b[3]);
+            for (int j = 0; j < C::MT; ++j) {
+                uint32_t a[4];       // tokens 0-7: elements 16 j .. + 7, + 8 .. + 15; tokens 8-15 likewise
+                const int r = lane % 8 + lane / 16 * 8, ch = 2 * j + (lane / 8) % 2;
+                ldsm4<true>(vd + r * C::ROWB + swizzle<C>(r, ch) * 16, a);
+                weigh(j, a[0], a[1], a[2], a[3]);
             }
         } else {
-            // thread (g, c4) takes columns NT g .. NT g + NT - 1 of four tokens: tile j holds column
-            // NT n + j in its place n
+            // thread (g, c4) takes elements D / 8 g .. + D / 8 - 1 of four tokens: tile j holds element
+            // D / 8 r + 2 j in its row r and the next one in row r + 8
             const uint32_t vsd = vd + C::PLANE + C::SCALEB;
+            uint32_t w[4][C::D / 32];
+            uint32_t byte[4];
 #pragma unroll
-            for (int t = 0; t < C::STEP / 16; ++t) {
-                uint32_t w[4][C::NT / 4];
-                uint32_t byte[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = 16 * t + 2 * c4 + (i & 1) + 8 * (i >> 1);
-                    byte[i] = lds8(vsd + r * 4 + (C::NT * g) / 32);
-                    if constexpr (C::D == 128) {
-                        const uint4 x = lds128(vd + r * C::ROWB + swizzle<C>(r, g) * 16);
-                        w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
-                    } else {
-                        const uint2 x = lds64(vd + r * C::ROWB + swizzle<C>(r, g / 2) * 16 + (g & 1) * 8);
-                        w[i][0] = x.x, w[i][1] = x.y;
-                    }
+            for (int i = 0; i < 4; ++i) {
+                const int r = 2 * c4 + (i & 1) + 8 * (i >> 1);
+                byte[i] = lds8(vsd + r * 4 + (C::D / 8 * g) / 32);
+                if constexpr (C::D == 128) {
+                    const uint4 x = lds128(vd + r * C::ROWB + swizzle<C>(r, g) * 16);
+                    w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
+                } else {
+                    const uint2 x = lds64(vd + r * C::ROWB + swizzle<C>(r, g / 2) * 16 + (g & 1) * 8);
+                    w[i][0] = x.x, w[i][1] = x.y;
                 }
-                const Scale2 s01 = make_scale<TY>(byte[0], byte[1]), s23 = make_scale<TY>(byte[2], byte[3]);
+            }
+            const Scale2 s01 = make_scale<TY>(byte[0], byte[1]), s23 = make_scale<TY>(byte[2], byte[3]);
 #pragma unroll
-                for (int x = 0; x < C::NT / 4; ++x) {
-                    const uint32_t a0 = __byte_perm(w[0][x], w[1][x], 0x5140);
-                    const uint32_t a1 = __byte_perm(w[0][x], w[1][x], 0x7362);
-                    const uint32_t b0 = __byte_perm(w[2][x], w[3][x], 0x5140);
-                    const uint32_t b1 = __byte_perm(w[2][x], w[3][x], 0x7362);
-                    weigh(acc[4 * x], t, decode2<TY, FAST>(uint16_t(a0 & 0xFFFF), s01),
-                          decode2<TY, FAST>(uint16_t(b0 & 0xFFFF), s23));
-                    weigh(acc[4 * x + 1], t, decode2<TY, FAST>(uint16_t(a0 >> 16), s01),
-                          decode2<TY, FAST>(uint16_t(b0 >> 16), s23));
-                    weigh(acc[4 * x + 2], t, decode2<TY, FAST>(uint16_t(a1 & 0xFFFF), s01),
-                          decode2<TY, FAST>(uint16_t(b1 & 0xFFFF), s23));
-                    weigh(acc[4 * x + 3], t, decode2<TY, FAST>(uint16_t(a1 >> 16), s01),
-                          decode2<TY, FAST>(uint16_t(b1 >> 16), s23));
+            for (int x = 0; x < C::D / 32; ++x) {
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const uint32_t a = __byte_perm(w[0][x], w[1][x], y ? 0x7362 : 0x5140);
+                    const uint32_t b = __byte_perm(w[2][x], w[3][x], y ? 0x7362 : 0x5140);
+                    weigh(2 * x + y, decode2<TY, FAST>(uint16_t(a & 0xFFFF), s01),
+                          decode2<TY, FAST>(uint16_t(a >> 16), s01), decode2<TY, FAST>(uint16_t(b & 0xFFFF), s23),
+                          decode2<TY, FAST>(uint16_t(b >> 16), s23));
                 }
             }
         }
     };
 
-    // Column of acc[j][i] (i & 1 selects the second of the pair).
-    auto column = [&](int j, int i) { return C::E4M3 ? C::NT * (2 * c4 + i) + j : 8 * j + 2 * c4 + i; };
+    // Element of d that acc[][j][0] (half 0) and acc[][j][2] (half 1) hold.
+    auto element = [&](int j, int half) {
+        return C::E4M3 ? C::D / 8 * g + 2 * j + half : 16 * j + g + 8 * half;
+    };
 
-    // Writes four consecutive columns of a finished row.
-    auto finish_row = [&](int row, int col, float4 o, float L, float M) {
-        const int chunk = use.hc % p.chunks, hkv = use.hc / p.chunks;
-        const int in_group = chunk * ROWS + row;
+    // Writes four consecutive elements of a finished row.
+    auto finish_row = [&](const Cursor &c, int row, int col, float4 o, float L, float M) {
+        const int in_group = c.hc % p.chunks * ROWS + row;
         if (in_group >= p.group) return;
-        const int h = hkv * p.group + in_group;
+        const int h = c.hc / p.chunks * p.group + in_group;
         const float inv = L > 0.0f || L != L ? 1.0f / L : 0.0f;     // an empty row is 0
-        *reinterpret_cast<uint2 *>(p.o + use.b * p.ob + h * p.oh + 2 * col) =
+        *reinterpret_cast<uint2 *>(p.o + c.b * p.ob + h * p.oh + 2 * col) =
             make_uint2(TY::pack(o.x * inv, o.y * inv), TY::pack(o.z * inv, o.w * inv));
         if (p.lse && col == 0)
-            p.lse[(int64_t)use.b * p.hq + h] = L == 0.0f ? -INFINITY : M * LN2 + logf(L);
+            p.lse[(int64_t)c.b * p.hq + h] = L == 0.0f ? -INFINITY : M * LN2 + logf(L);
     };
 
     // ---- end of the tiles this CTA has of a unit: the warps' rows are merged; a whole unit is
     // written out, a part goes to the workspace
-    int64_t unit_at = begin - use.tile;         // the unit's first tile in the whole order
-    auto end_unit = [&] {
-        const int64_t c_first = kvi::range_owner(W, G, unit_at);
-        const int64_t c_last = kvi::range_owner(W, G, unit_at + use.ntiles - 1);
-        const bool whole = c_first == c_last;
-        float *part = p.partial + (2 * cta + (cta == c_first ? 1 : 0)) * C::PARTIAL;
+    auto end_unit = [&](const Cursor &c) {
+        const int64_t t0 = unit_at + EXTRA, t1 = t0 + c.ntiles - 1;     // the unit's first and last tile
+        const bool whole = t0 >= begin && t1 < end, opens = t0 >= begin;
+        float *part = p.partial + (2 * cta + (opens ? 1 : 0)) * C::PARTIAL;
 #pragma unroll
-        for (int r = 0; r < (C::WIDE ? 2 : 1); ++r) {
-            l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 1);
-            l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 2);
-            if (c4 == 0) {
-                s_m[warp][g + 8 * r] = m[r] - P_SHIFT;     // the sums are times 2^P_SHIFT
-                s_l[warp][g + 8 * r] = l[r];
+        for (int n = 0; n < C::NH; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, l[n][i], 4);
+                l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, l[n][i], 8);
+                l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, l[n][i], 16);
+                if (g == 0) {
+                    s_m[warp][8 * n + 2 * c4 + i] = m[n][i] - P_SHIFT;     // the sums are times 2^P_SHIFT
+                    s_l[warp][8 * n + 2 * c4 + i] = l[n][i];
+                }
             }
-        }
 #pragma unroll
-        for (int blk = 0; blk < (C::WIDE ? 16 : 8) / C::MERGE_ROWS; ++blk) {
-            const int row0 = blk * C::MERGE_ROWS, half = row0 / 8;
-            if (blk) __syncthreads();             // the block before has been read
-            if (g >= row0 % 8 && g < row0 % 8 + C::MERGE_ROWS) {
-                float *mine_m = merge + (warp * C::MERGE_ROWS + g - row0 % 8) * C::D;
+        for (int blk = 0; blk < 8 * C::NH / C::MERGE_ROWS; ++blk) {
+            const int row0 = blk * C::MERGE_ROWS, n = row0 / 8;
+            const int mine_r = 2 * c4 - row0 % 8;         // this lane's first head in the block
+            if (blk) __syncthreads();                     // the block before has been read
+            if (mine_r >= 0 && mine_r < C::MERGE_ROWS) {
+                float *dst = merge + (warp * C::MERGE_ROWS + mine_r) * C::D;
 #pragma unroll
-                for (int j = 0; j < C::NT; ++j)
+                for (int j = 0; j < C::MT; ++j)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        mine_m[column(j, i)] =
-                            C::WIDE ? acc[j][2 * half + i] : acc[j][i] + acc[j][2 + i];
+                    for (int i = 0; i < 2; ++i) {
+                        dst[i * C::D + element(j, 0)] = acc[n][j][i];
+                        dst[i * C::D + element(j, 1)] = acc[n][j][i + 2];
+                    }
             }
             __syncthreads();
-            // 4 columns a thread
+            // 4 elements a thread
             for (int x = tid; x < C::MERGE_ROWS * C::D / 4; x += THREADS) {
                 const int r = x / (C::D / 4), row = row0 + r, col = x % (C::D / 4) * 4;
                 float M = -INFINITY;
@@ -605,7 +659,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
                     L += f * s_l[w][row];
                 }
                 if (whole) {
-                    finish_row(row, col, o, L, M);
+                    finish_row(c, row, col, o, L, M);
                 } else {
                     *reinterpret_cast<float4 *>(part + row * C::D + col) = o;
                     if (col == 0) {
@@ -617,25 +671,25 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         }
         if (!whole) {
             // the last CTA to arrive merges all parts, in the order of the ranges
+            const int64_t c_first = kvi::range_owner(W, G, t0), c_last = kvi::range_owner(W, G, t1);
             __threadfence();
             __syncthreads();
-            const int64_t unit = (int64_t)use.b * units_b + use.hc;
-            const int pieces = (int)(c_last - c_first + 1);
+            const int64_t unit = (int64_t)c.b * units_b + c.hc;
             if (tid == 0) {
                 const int old = atomicAdd(p.counters + unit, 1);
-                s_last = old == pieces - 1;
+                s_last = old == (int)(c_last - c_first);
                 if (s_last) p.counters[unit] = 0;          // ready for the next call
             }
             __syncthreads();
             if (s_last) {
                 __threadfence();
-                constexpr int NROWS = C::WIDE ? 16 : 8;
-                for (int x = tid; x < NROWS * C::D / 4; x += THREADS) {
+                for (int x = tid; x < 8 * C::NH * C::D / 4; x += THREADS) {
                     const int row = x / (C::D / 4), col = x % (C::D / 4) * 4;
                     float M = -INFINITY, L = 0.0f;
                     float4 o = make_float4(0, 0, 0, 0);
-                    for (int64_t c = c_first; c <= c_last; ++c) {
-                        const float *q = p.partial + (2 * c + (c == c_first ? 1 : 0)) * C::PARTIAL;
+#pragma unroll 4
+                    for (int64_t i = c_first; i <= c_last; ++i) {
+                        const float *q = p.partial + (2 * i + (i == c_first ? 1 : 0)) * C::PARTIAL;
                         const float mc = __ldcg(q + ROWS * C::D + row);
                         const float lc = __ldcg(q + ROWS * C::D + ROWS + row);
                         const float4 a = __ldcg(reinterpret_cast<const float4 *>(q + row * C::D + col));
@@ -649,7 +703,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
                         o.z = o.z * fo + a.z * fc;
                         o.w = o.w * fo + a.w * fc;
                     }
-                    finish_row(row, col, o, L, M);
+                    finish_row(c, row, col, o, L, M);
                 }
             }
         }
@@ -664,24 +718,23 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         cp_commit();
         look_up();
     }
-    start_unit();
+    load_queries(use);
+    clear();
     int slot = 0, fill = C::NSTAGES - 1;
-    while (left > 0) {
+    while (true) {
         issue(fill);                            // the slot the step before this one has left
         cp_commit();
         look_up();
         cp_wait<C::NSTAGES - 1>();
         __syncwarp();
-        if (s_mask[warp][slot] != 0) {
+        const uint32_t mask = s_mask[warp][slot];
+        if (mask != 0) {
             bool far = false;
             if (C::E4M3 && !TY::BF16) {
-                const uint32_t sd = ring + slot * C::STAGEB + 2 * C::PLANE;
-                const uint32_t mask = s_mask[warp][slot];
-                if ((mask >> lane) & 1) {
+                if ((mask >> (lane % STEP)) & 1) {
+                    const uint32_t w = lds32(ring + slot * C::STAGEB + 2 * C::PLANE + lane * 4);
 #pragma unroll
-                    for (int i = 0; i < C::D / 32; ++i)
-                        far = far || far_scale(lds8(sd + lane * 4 + i)) ||
-                              far_scale(lds8(sd + C::SCALEB + lane * 4 + i));
+                    for (int i = 0; i < C::D / 32; ++i) far = far || far_scale((w >> (8 * i)) & 255u);
                 }
                 far = __any_sync(0xFFFFFFFFu, far);
             }
@@ -691,45 +744,49 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         __syncwarp();                           // every lane has read the slot
         slot = slot + 1 == C::NSTAGES ? 0 : slot + 1;
         fill = fill + 1 == C::NSTAGES ? 0 : fill + 1;
-        --left;
-        const bool unit_done = use.tile + 1 == use.ntiles;
-        if (unit_done || left == 0) {
-            end_unit();
-            if (left == 0) break;
-            unit_at += use.ntiles;
-            advance(use, p, C::TILE);
-            start_unit();
-        } else {
-            ++use.tile;
+        const Cursor done = use;
+        advance(use, p);
+        const bool more = use.pos < end;
+        if (use.tile == 0 || !more) {
+            if (more) load_queries(use);        // in flight while the warps merge
+            end_unit(done);
+            if (!more) break;
+            unit_at += done.ntiles + EXTRA;
+            clear();
         }
     }
     cp_wait<0>();
 }
 
 template <class C>
-cudaError_t launch(const AttnParams &p, int grid, cudaStream_t stream) {
-    static_assert(C::SMEM + 3072 <= 227 * 1024, "shared memory");
+cudaError_t launch(const AttnParams &p, int64_t most, const qgi::LaunchCtx &ctx) {
+    static_assert(C::SMEM + 2048 <= (C::TWO ? 113 : 226) * 1024, "shared memory");
     static_assert(C::NSTAGES >= 3, "stages");
-    cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel<C>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (e != cudaSuccess) return e;
-    paged_attention_kernel<C><<<grid, THREADS, C::SMEM, stream>>>(p);
+    // the attribute stays with the device's context: set once on each device
+    static std::atomic<uint64_t> ready{0};
+    if (!(ready.load(std::memory_order_relaxed) >> ctx.device & 1)) {
+        const cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel<C>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(uint64_t(1) << ctx.device, std::memory_order_relaxed);
+    }
+    const int64_t room = (int64_t)ctx.num_sms * (C::TWO ? 2 : 1);
+    paged_attention_kernel<C><<<(unsigned)(most < room ? most : room), THREADS, C::SMEM, ctx.stream>>>(p);
     return cudaGetLastError();
 }
 
 template <class TY, int D>
-cudaError_t launch_cache(const AttnParams &p, bool e4m3, int grid, cudaStream_t stream) {
+cudaError_t launch_cache(const AttnParams &p, bool e4m3, int64_t most, const qgi::LaunchCtx &ctx) {
     const bool wide = p.group > 8;
-    if (e4m3) return wide ? launch<Cfg<TY, D, true, true>>(p, grid, stream)
-                          : launch<Cfg<TY, D, true, false>>(p, grid, stream);
-    return wide ? launch<Cfg<TY, D, false, true>>(p, grid, stream)
-                : launch<Cfg<TY, D, false, false>>(p, grid, stream);
+    if (e4m3) return wide ? launch<Cfg<TY, D, true, 2>>(p, most, ctx) : launch<Cfg<TY, D, true, 1>>(p, most, ctx);
+    return wide ? launch<Cfg<TY, D, false, 2>>(p, most, ctx) : launch<Cfg<TY, D, false, 1>>(p, most, ctx);
 }
 
 int64_t chunks_of(int64_t group) { return (group + ROWS - 1) / ROWS; }
 size_t counters_bytes(int64_t units) { return (size_t)((units * 4 + 255) / 256 * 256); }
 size_t partial_bytes(int64_t d, int num_sms) {
-    return ((size_t)num_sms * 2 * ROWS * (size_t)(d + 2) * sizeof(float) + 255) / 256 * 256;
+    // two a CTA, up to two CTAs an SM
+    return ((size_t)num_sms * 4 * ROWS * (size_t)(d + 2) * sizeof(float) + 255) / 256 * 256;
 }
 
 }  // namespace
@@ -788,16 +845,15 @@ cudaError_t launch_paged_attention(const PagedAttnArgs &a, const LaunchCtx &ctx)
     p.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + a.workspace_bytes / 256 * 256 -
                                           qg::partial_bytes(c->d, ctx.num_sms));
     p.err = ctx.err;
-    // no more CTAs than tiles the table rows can hold
-    const int64_t cap = (int64_t)a.max_pages * c->page_size;
-    const int tile = qg::NWARPS * (e4m3 ? 32 : 16);
-    const int64_t most = units * kvi::tiles_of((int32_t)(cap < 0x7FFFFFFF ? cap : 0x7FFFFFFF), tile);
-    const int grid = (int)(most < ctx.num_sms ? most : ctx.num_sms);
+    p.one_page = c->page_size % qg::STEP == 0;
+    // no more CTAs than tiles (and EXTRAs) the table rows can hold
+    const int64_t most =
+        units * (kvi::tiles_of(a.max_pages * (int32_t)c->page_size, qg::TILE) + qg::EXTRA);
     if (a.bf16)
-        return c->d == 64 ? qg::launch_cache<qg::TypeBF16, 64>(p, e4m3, grid, ctx.stream)
-                          : qg::launch_cache<qg::TypeBF16, 128>(p, e4m3, grid, ctx.stream);
-    return c->d == 64 ? qg::launch_cache<qg::TypeF16, 64>(p, e4m3, grid, ctx.stream)
-                      : qg::launch_cache<qg::TypeF16, 128>(p, e4m3, grid, ctx.stream);
+        return c->d == 64 ? qg::launch_cache<qg::TypeBF16, 64>(p, e4m3, most, ctx)
+                          : qg::launch_cache<qg::TypeBF16, 128>(p, e4m3, most, ctx);
+    return c->d == 64 ? qg::launch_cache<qg::TypeF16, 64>(p, e4m3, most, ctx)
+                      : qg::launch_cache<qg::TypeF16, 128>(p, e4m3, most, ctx);
 }
 
 }  // namespace qgi

@@ -322,3 +322,36 @@ def test_reference_pages_keep_their_counts():
             for x in p.table[s][:n]:
                 held[x] += 1
         assert held == p.refs
+
+
+def test_every_tile_has_one_cta(idx):
+    """The attention's walk over its range, restated: with a unit counting `extra` tiles beyond its own, every tile
+    is computed by one CTA, and the parts of a cut unit are those of consecutive CTAs."""
+    rng = random.Random(7)
+    for _ in range(200):
+        extra = rng.choice([0, 1, 2, 3])
+        units = [rng.choice([1, 1, 2, rng.randint(1, 40), rng.randint(1, 500)]) for _ in range(rng.randint(1, 40))]
+        starts, at = [], 0
+        for n in units:
+            starts.append(at)
+            at += n + extra
+        W = at
+        G = min(rng.choice([1, 2, 7, 152, 304]), W)
+        seen = [[] for _ in units]
+        for c in range(G):
+            begin, end = idx.range_begin(W, G, c), idx.range_begin(W, G, c + 1)
+            u = max(i for i, s in enumerate(starts) if s <= begin)
+            tile = max(0, begin - starts[u] - extra)
+            pos = starts[u] + extra + tile
+            while pos < end:
+                seen[u].append((tile, c))
+                pos, tile = pos + 1, tile + 1
+                if tile == units[u]:
+                    u, tile, pos = u + 1, 0, pos + extra
+        for u, n in enumerate(units):
+            assert [t for t, _ in seen[u]] == list(range(n))
+            t0 = starts[u] + extra
+            first, last = idx.range_owner(W, G, t0), idx.range_owner(W, G, t0 + n - 1)
+            assert sorted({c for _, c in seen[u]}) == list(range(first, last + 1))
+            for c in range(first, last + 1):          # who opens the unit, as each CTA sees it
+                assert (t0 >= idx.range_begin(W, G, c)) == (c == first)
