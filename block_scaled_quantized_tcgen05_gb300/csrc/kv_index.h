@@ -27,6 +27,19 @@ KV_HD bool locate(const int32_t *row, int32_t max_pages, int32_t page_size, int3
     return p >= 0 && p < pages;
 }
 
+// Division of a token number t < 2^31 by the page size as a product and a shift: magic = ceil(2^shift /
+// page_size) with shift = 31 + l, 2^(l - 1) < page_size <= 2^l, lies in [2^31, 2^32), and its excess times t
+// stays below 2^shift / page_size.
+KV_HD void page_divisor(int32_t page_size, uint32_t *magic, uint32_t *shift) {
+    uint32_t l = 0;
+    while ((int64_t(1) << l) < page_size) ++l;
+    *shift = 31 + l;
+    *magic = (uint32_t)(((uint64_t(1) << *shift) + (uint64_t)page_size - 1) / (uint64_t)page_size);
+}
+KV_HD int32_t page_of(uint32_t t, uint32_t magic, uint32_t shift) {
+    return (int32_t)(((uint64_t)t * magic) >> shift);
+}
+
 // Pages that hold n tokens.
 KV_HD int32_t pages_of(int32_t n, int32_t page_size) { return n > 0 ? (n - 1) / page_size + 1 : 0; }
 

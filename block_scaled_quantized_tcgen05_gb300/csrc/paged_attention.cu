@@ -39,7 +39,8 @@
 // hi) (relative error 2^-21 in fp16, 2^-15 in bf16), and both are multiplied: the matrix unit has the time.
 // lo is kept above zero, at 2^-39 of the largest weight at least, so that an infinite value stays one (0 x
 // inf and inf - inf would be NaN).  E4M3
-// values become the nearest half (bf16) to code * 2^(byte - 127): exact for every block the append writes.
+// codes are exact in 16 bits; a key block's scale goes onto its part of the score in fp32, and a value
+// becomes the nearest half (bf16) to code * 2^(byte - 127): exact for every block the append writes.
 #include <atomic>
 #include <type_traits>
 
@@ -71,6 +72,7 @@ struct AttnParams {
     int32_t B, hq, hkv, group, chunks;      // chunks: units per key-value head
     int32_t max_seqs, max_pages, page_size, pages, window;
     bool one_page;                          // page_size is a multiple of STEP
+    uint32_t page_magic, page_shift;        // of kvi::page_of
     float scale_log2;
     int32_t *counters;
     float *partial;
@@ -176,8 +178,9 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // The 16-byte piece `chunk` of row `row` lies at this piece of the row's place in shared memory.
-// 16-bit rows: eight rows of one piece (an ldmatrix) fall into eight bank groups.  8-bit rows: so do
-// two rows of four pieces (a key fragment) and four even or four odd rows of two (a value fragment).
+// 16-bit rows: eight rows of one piece (an ldmatrix) fall into eight bank groups.  8-bit rows of 128: so
+// do four rows of one block's two pieces (a key fragment: rows 0-3 or 4-7, 8 bytes a lane) and four even
+// or four odd rows of two pieces (a value fragment).
 template <class C>
 __device__ __forceinline__ int swizzle(int row, int chunk) {
     if (!C::E4M3) return chunk ^ (row & (C::CHUNKS < 8 ? C::CHUNKS - 1 : 7));
@@ -185,16 +188,37 @@ __device__ __forceinline__ int swizzle(int row, int chunk) {
     return chunk ^ ((row >> 1) & 3);
 }
 
-// Two E4M3 codes (low and high byte) times the scales of their blocks, rounded once to the pair of
-// 16-bit values.  FAST: both scales are halves (2^-24 .. 2^15), so one half multiply does it.
-struct Scale2 {
-    uint32_t h2;         // both as halves
-    float lo, hi;        // and as fp32 (any byte)
-};
+// Two E4M3 codes (low and high byte) as a pair of 16-bit values: exact.
+template <class TY>
+__device__ __forceinline__ uint32_t decode2(uint16_t codes) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(codes));
+    if (!TY::BF16) return h;
+    const float2 f = TypeF16::unpack(h);
+    return TY::pack(f.x, f.y);
+}
+// Byte i of a word as the scale 2^(byte - 127): byte 0 is the fp32 subnormal 2^-127, byte 255 NaN.
+// FAST: neither occurs (but for the 0 of a masked row, whose codes are 0).
+template <bool FAST>
 __device__ __forceinline__ float scale_f32(uint32_t byte) {
-    // 2^(byte - 127): byte 0 is the fp32 subnormal 2^-127, byte 255 NaN
+    if (FAST) return __uint_as_float(byte << 23);
     return __uint_as_float(byte == 0 ? 0x00400000u : (byte == 255 ? 0x7FC00000u : byte << 23));
 }
+// The scales of a pair of tokens.
+struct Scale2 {
+    uint32_t h2;         // as halves
+    float lo, hi;        // as fp32
+};
+template <class TY, bool FAST>
+__device__ __forceinline__ Scale2 make_scale(uint32_t lo, uint32_t hi) {
+    Scale2 s;
+    s.lo = scale_f32<FAST>(lo);
+    s.hi = scale_f32<FAST>(hi);
+    s.h2 = TY::BF16 || !FAST ? 0u : TypeF16::pack(s.lo, s.hi);
+    return s;
+}
+// Two codes times their scales, rounded once.  FAST: the scales are halves (2^-24 .. 2^15), so one
+// half multiply does it; through fp32, where the product is exact, otherwise.
 template <class TY, bool FAST>
 __device__ __forceinline__ uint32_t decode2(uint16_t codes, const Scale2 &s) {
     uint32_t h;
@@ -207,23 +231,12 @@ __device__ __forceinline__ uint32_t decode2(uint16_t codes, const Scale2 &s) {
     const float2 f = TypeF16::unpack(h);
     return TY::pack(f.x * s.lo, f.y * s.hi);
 }
-template <class TY>
-__device__ __forceinline__ Scale2 make_scale(uint32_t lo, uint32_t hi) {
-    Scale2 s;
-    s.lo = scale_f32(lo);
-    s.hi = scale_f32(hi);
-    s.h2 = TY::BF16 ? 0u : TypeF16::pack(s.lo, s.hi);
-    return s;
-}
-// Whether a scale byte is outside the halves.
-__device__ __forceinline__ bool far_scale(uint32_t byte) { return byte - 103u > 39u; }
-
 // A position in the work: which unit, and which of its tiles.  Held alike by every lane.
 struct Cursor {
     int64_t pos;          // of the tile, in tiles and EXTRAs over all units
     int64_t row;          // page-table row (element offset)
     int32_t b;            // sequence of the batch
-    int32_t hc;           // key-value head * chunks + chunk
+    int32_t h, part;      // key-value head, and which 16 of its query heads
     int32_t tile, ntiles; // tile inside the unit, tiles of the unit
     int32_t first, n;     // tokens [first, n)
     int32_t next_seq, next_len;   // of sequence b + 1, read ahead (-1: none)
@@ -252,8 +265,10 @@ __device__ __forceinline__ void advance(Cursor &c, const AttnParams &p) {
     if (++c.tile < c.ntiles) return;
     c.tile = 0;
     c.pos += EXTRA;
-    if (++c.hc < p.hkv * p.chunks) return;
-    c.hc = 0;
+    if (++c.part < p.chunks) return;
+    c.part = 0;
+    if (++c.h < p.hkv) return;
+    c.h = 0;
     ++c.b;
     enter(c, p, c.next_seq, c.next_len);
     read_ahead(c, p);
@@ -329,7 +344,8 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
 
     Cursor use;                          // the tile being computed
     use.b = s_start[0];
-    use.hc = s_start[1];
+    use.h = s_start[1] / p.chunks;
+    use.part = s_start[1] - use.h * p.chunks;
     int64_t unit_at = s_at;              // where the unit begins in the whole order
     {
         const int32_t seq = sequence(p, use.b);
@@ -346,18 +362,24 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
     // ---- page look-up of this warp's tokens of the tile `load` points at, one step ahead of the
     // copies that use it.  Steps begin at multiples of 16 tokens: with pages of a multiple of 16 tokens
     // a step lies in one page, and every lane holds its entry; otherwise lane l holds token l's.
-    int32_t pg = -1, pt = 0;             // page-table entry, first token of the looked-up step
-    int32_t phc = 0, pfirst = 0, pn = 0; // its head and the tokens of its sequence
+    int32_t pg = -1, pr = 0;             // page-table entry and row inside the page
+    int32_t p_lo = 0, p_hi = 0;          // rows of the step that are tokens of the range
+    int64_t p_off = 0, p_soff = 0;       // the head's place in a page
     auto look_up = [&] {
-        pn = 0;
+        p_lo = p_hi = 0;
         if (load.pos < end) {
-            pt = load.first / STEP * STEP + load.tile * TILE + warp * STEP;
-            phc = load.hc;
-            pfirst = load.first;
-            pn = load.n;
-            const int32_t t = p.one_page ? max(pt, pfirst) : pt + lane;
-            if ((p.one_page || lane < STEP) && t >= pfirst && t < pn)
-                pg = p.table[load.row + (uint32_t)t / (uint32_t)p.page_size];
+            const int32_t t0 = load.first / STEP * STEP + load.tile * TILE + warp * STEP;
+            p_lo = max(load.first - t0, 0);
+            p_hi = min(load.n - t0, STEP);
+            p_off = load.h * p.head;
+            if (C::E4M3) p_soff = load.h * p.shead;
+            const int32_t l = p.one_page ? 0 : lane;
+            if (p_lo < p_hi && l < STEP) {
+                const int32_t t = t0 + l, i = kvi::page_of((uint32_t)t, p.page_magic, p.page_shift);
+                pr = t - i * p.page_size + (p.one_page ? lane : 0);
+                // rows before the range's first token may lie in a page of no interest
+                if (p.one_page || (l >= p_lo && l < p_hi)) pg = p.table[load.row + i];
+            }
             advance(load, p);
         }
     };
@@ -365,9 +387,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
     constexpr int RPI = 32 / C::CHUNKS;          // rows an instruction of the warp copies
     const int chunk = lane % C::CHUNKS, row0 = lane / C::CHUNKS;
     auto issue = [&](int slot) {
-        const int32_t t = pt + lane;
-        bool ok = lane < STEP && t >= pfirst && t < pn;
-        const int32_t h = phc / p.chunks;
+        bool ok = lane >= p_lo && lane < p_hi;
         const uint32_t kd = ring + slot * C::STAGEB, vd = kd + C::PLANE;
         int64_t off = 0, soff = 0;               // lane l: row l's place
         if (ok) {
@@ -375,9 +395,8 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
                 report_index(p.err);
                 ok = false;
             } else {
-                const int32_t r = t - (int32_t)((uint32_t)t / (uint32_t)p.page_size) * p.page_size;
-                off = pg * p.page + r * p.token + h * p.head;
-                if (C::E4M3) soff = pg * p.spage + r * p.stoken + h * p.shead;
+                off = p_off + pg * p.page + pr * p.token;
+                if (C::E4M3) soff = p_soff + pg * p.spage + pr * p.stoken;
                 ok = QG_IN_BOUNDS(p.err, off >= 0 && off + C::ROWB <= p.extent);
                 if (!ok) off = soff = 0;
             }
@@ -420,17 +439,17 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
     float acc[C::NH][C::MT][4];             // rows of d, columns of heads 2 c4, 2 c4 + 1
     float m[C::NH][2], l[C::NH][2];
     auto load_queries = [&](const Cursor &c) {
-        const int part = c.hc % p.chunks, h0 = (c.hc / p.chunks) * p.group + part * ROWS;
-        const int rows = min(ROWS, p.group - part * ROWS);
+        const int h0 = c.h * p.group + c.part * ROWS;
+        const int rows = min(ROWS, p.group - c.part * ROWS);
 #pragma unroll
         for (int n = 0; n < C::NH; ++n) {
             const bool in = 8 * n + g < rows;
             const uint8_t *q = p.q + c.b * p.qb + (h0 + 8 * n + g) * p.qh;
 #pragma unroll
             for (int kk = 0; kk < C::D / 16; ++kk) {
-                // 16-bit rows: the fragments ldmatrix gives; 8-bit rows: thread c4 holds 16 consecutive
-                // elements of every 64, four for each product, and the queries follow
-                const int e = C::E4M3 ? (kk / 4) * 64 + c4 * 16 + (kk % 4) * 4 : kk * 16 + c4 * 2;
+                // 16-bit rows: the fragments ldmatrix gives; 8-bit rows: thread c4 holds 8 consecutive
+                // elements of every 32, four for each product, and the queries follow
+                const int e = C::E4M3 ? (kk / 2) * 32 + c4 * 8 + (kk % 2) * 4 : kk * 16 + c4 * 2;
                 const int e2 = C::E4M3 ? e + 2 : e + 8;
                 qb[n][kk][0] = in ? *reinterpret_cast<const uint32_t *>(q + 2 * e) : 0;
                 qb[n][kk][1] = in ? *reinterpret_cast<const uint32_t *>(q + 2 * e2) : 0;
@@ -452,48 +471,61 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
         [[maybe_unused]] constexpr bool FAST = decltype(fast_tag)::value;
         const uint32_t kd = ring + slot * C::STAGEB, vd = kd + C::PLANE;
         const uint32_t mask = s_mask[warp][slot];
-        // two accumulators a group of heads, so that the products' chains are half as long
-        float s[C::NH][4], s2[C::NH][4];
+        float s[C::NH][4];
 #pragma unroll
-        for (int n = 0; n < C::NH; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[n][i] = s2[n][i] = 0.0f;
-        auto score = [&](int kk, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-#pragma unroll
-            for (int n = 0; n < C::NH; ++n)
-                mma16816(TY::BF16, kk % 2 ? s2[n] : s[n], a0, a1, a2, a3, qb[n][kk][0], qb[n][kk][1]);
-        };
+        for (int n = 0; n < C::NH; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
         if constexpr (!C::E4M3) {
+            // two accumulators a group of heads, so that the products' chains are half as long
+            float s2[C::NH][4];
+#pragma unroll
+            for (int n = 0; n < C::NH; ++n) s2[n][0] = s2[n][1] = s2[n][2] = s2[n][3] = 0.0f;
 #pragma unroll
             for (int kk = 0; kk < C::D / 16; ++kk) {
                 uint32_t a[4];       // tokens 0-7 and 8-15 of piece 2 kk, then of 2 kk + 1
                 const int r = lane % 16, ch = 2 * kk + lane / 16;
                 ldsm4<false>(kd + r * C::ROWB + swizzle<C>(r, ch) * 16, a);
-                score(kk, a[0], a[1], a[2], a[3]);
+#pragma unroll
+                for (int n = 0; n < C::NH; ++n)
+                    mma16816(TY::BF16, kk % 2 ? s2[n] : s[n], a[0], a[1], a[2], a[3], qb[n][kk][0], qb[n][kk][1]);
             }
+#pragma unroll
+            for (int n = 0; n < C::NH; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[n][i] += s2[n][i];
         } else {
+            // one block of 32 at a time, thread c4 with 8 consecutive bytes of it in two products;
+            // the block's scale goes onto its sum, in fp32
             const uint32_t ksd = vd + C::PLANE;
+            const uint32_t bx = lds32(ksd + g * 4), by = lds32(ksd + (g + 8) * 4);
 #pragma unroll
-            for (int hf = 0; hf < C::D / 64; ++hf) {
-                const uint4 x = lds128(kd + g * C::ROWB + swizzle<C>(g, 4 * hf + c4) * 16);
-                const uint4 y = lds128(kd + (g + 8) * C::ROWB + swizzle<C>(g + 8, 4 * hf + c4) * 16);
-                const uint32_t bx = lds8(ksd + g * 4 + 2 * hf + c4 / 2);
-                const uint32_t by = lds8(ksd + (g + 8) * 4 + 2 * hf + c4 / 2);
-                const Scale2 sx = make_scale<TY>(bx, bx), sy = make_scale<TY>(by, by);
-                const uint32_t xx[4] = {x.x, x.y, x.z, x.w}, yy[4] = {y.x, y.y, y.z, y.w};
+            for (int blk = 0; blk < C::D / 32; ++blk) {
+                const int ch = 2 * blk + c4 / 2, in = c4 % 2 * 8;
+                const uint2 x = lds64(kd + g * C::ROWB + swizzle<C>(g, ch) * 16 + in);
+                const uint2 y = lds64(kd + (g + 8) * C::ROWB + swizzle<C>(g + 8, ch) * 16 + in);
+                const float sx = scale_f32<FAST>((bx >> (8 * blk)) & 255u);
+                const float sy = scale_f32<FAST>((by >> (8 * blk)) & 255u);
+                const uint32_t a[8] = {
+                    decode2<TY>(uint16_t(x.x & 0xFFFF)), decode2<TY>(uint16_t(y.x & 0xFFFF)),
+                    decode2<TY>(uint16_t(x.x >> 16)), decode2<TY>(uint16_t(y.x >> 16)),
+                    decode2<TY>(uint16_t(x.y & 0xFFFF)), decode2<TY>(uint16_t(y.y & 0xFFFF)),
+                    decode2<TY>(uint16_t(x.y >> 16)), decode2<TY>(uint16_t(y.y >> 16))};
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    score(4 * hf + i, decode2<TY, FAST>(uint16_t(xx[i] & 0xFFFF), sx),
-                          decode2<TY, FAST>(uint16_t(yy[i] & 0xFFFF), sy),
-                          decode2<TY, FAST>(uint16_t(xx[i] >> 16), sx),
-                          decode2<TY, FAST>(uint16_t(yy[i] >> 16), sy));
+                for (int n = 0; n < C::NH; ++n) {
+                    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    mma16816(TY::BF16, part, a[0], a[1], a[2], a[3], qb[n][2 * blk][0], qb[n][2 * blk][1]);
+                    mma16816(TY::BF16, part, a[4], a[5], a[6], a[7], qb[n][2 * blk + 1][0], qb[n][2 * blk + 1][1]);
+                    s[n][0] += sx * part[0];
+                    s[n][1] += sx * part[1];
+                    s[n][2] += sy * part[2];
+                    s[n][3] += sy * part[3];
+                }
             }
         }
         // scores in units of log 2, masked ones -inf: [0], [1] of token g, [2], [3] of token g + 8
 #pragma unroll
         for (int n = 0; n < C::NH; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[n][i] = (s[n][i] + s2[n][i]) * p.scale_log2;
+            for (int i = 0; i < 4; ++i) s[n][i] *= p.scale_log2;
         if (mask != (1u << STEP) - 1) {
             const bool in0 = (mask >> g) & 1, in8 = (mask >> (g + 8)) & 1;
 #pragma unroll
@@ -575,7 +607,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
                     w[i][0] = x.x, w[i][1] = x.y;
                 }
             }
-            const Scale2 s01 = make_scale<TY>(byte[0], byte[1]), s23 = make_scale<TY>(byte[2], byte[3]);
+            const Scale2 s01 = make_scale<TY, FAST>(byte[0], byte[1]), s23 = make_scale<TY, FAST>(byte[2], byte[3]);
 #pragma unroll
             for (int x = 0; x < C::D / 32; ++x) {
 #pragma unroll
@@ -597,9 +629,9 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
 
     // Writes four consecutive elements of a finished row.
     auto finish_row = [&](const Cursor &c, int row, int col, float4 o, float L, float M) {
-        const int in_group = c.hc % p.chunks * ROWS + row;
+        const int in_group = c.part * ROWS + row;
         if (in_group >= p.group) return;
-        const int h = c.hc / p.chunks * p.group + in_group;
+        const int h = c.h * p.group + in_group;
         const float inv = L > 0.0f || L != L ? 1.0f / L : 0.0f;     // an empty row is 0
         *reinterpret_cast<uint2 *>(p.o + c.b * p.ob + h * p.oh + 2 * col) =
             make_uint2(TY::pack(o.x * inv, o.y * inv), TY::pack(o.z * inv, o.w * inv));
@@ -674,7 +706,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
             const int64_t c_first = kvi::range_owner(W, G, t0), c_last = kvi::range_owner(W, G, t1);
             __threadfence();
             __syncthreads();
-            const int64_t unit = (int64_t)c.b * units_b + c.hc;
+            const int64_t unit = ((int64_t)c.b * p.hkv + c.h) * p.chunks + c.part;
             if (tid == 0) {
                 const int old = atomicAdd(p.counters + unit, 1);
                 s_last = old == (int)(c_last - c_first);
@@ -730,11 +762,16 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
         const uint32_t mask = s_mask[warp][slot];
         if (mask != 0) {
             bool far = false;
-            if (C::E4M3 && !TY::BF16) {
+            if (C::E4M3) {
+                // values' scales that are no halves (bfloat16: 0 and 255, as for the keys)
                 if ((mask >> (lane % STEP)) & 1) {
                     const uint32_t w = lds32(ring + slot * C::STAGEB + 2 * C::PLANE + lane * 4);
+                    const bool narrow = lane >= STEP && !TY::BF16;
 #pragma unroll
-                    for (int i = 0; i < C::D / 32; ++i) far = far || far_scale((w >> (8 * i)) & 255u);
+                    for (int i = 0; i < C::D / 32; ++i) {
+                        const uint32_t byte = (w >> (8 * i)) & 255u;
+                        far = far || byte - (narrow ? 103u : 1u) > (narrow ? 39u : 253u);
+                    }
                 }
                 far = __any_sync(0xFFFFFFFFu, far);
             }
@@ -846,6 +883,7 @@ cudaError_t launch_paged_attention(const PagedAttnArgs &a, const LaunchCtx &ctx)
                                           qg::partial_bytes(c->d, ctx.num_sms));
     p.err = ctx.err;
     p.one_page = c->page_size % qg::STEP == 0;
+    kvi::page_divisor(p.page_size, &p.page_magic, &p.page_shift);
     // no more CTAs than tiles (and EXTRAs) the table rows can hold
     const int64_t most =
         units * (kvi::tiles_of(a.max_pages * (int32_t)c->page_size, qg::TILE) + qg::EXTRA);

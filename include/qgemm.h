@@ -480,7 +480,7 @@ qgemm_status qgemm_paged_attention_workspace_bytes(const qgemm_kv_cache *kv, int
  *   O[b, h, :] = sum_j softmax_j(scale * <Q[b, h, :], K_j[g]>) V_j[g],
  *   lse[b, h]  = ln sum_j exp(scale * <Q[b, h, :], K_j[g]>)     (lse may be NULL; fp32 [batch, q_heads]).
  * A sequence without tokens gives O = 0 and lse = -inf.  Scores, softmax and sums are fp32; E4M3
- * values are the nearest half (bfloat16) to code * 2^(byte - 127).  Tokens outside the range are not read.
+ * keys are code * 2^(byte - 127), values the half (bfloat16) nearest to it.  Tokens outside the range are not read.
  *   Q, O       device [batch, q_heads, d], 16-byte aligned, strides in multiples of 8 elements; O's rows must
  *              not overlap.  q_heads is a multiple of the cache's heads.
  *   workspace  device, 16-byte aligned, qgemm_paged_attention_workspace_bytes at least.  Its bytes

@@ -199,6 +199,11 @@ void seen_range(int32_t len, int32_t cap, int32_t window, int32_t *first, int32_
     kvi::seen_range(len, cap, window, first, n);
 }
 int32_t tiles_of(int32_t tokens, int32_t tile) { return kvi::tiles_of(tokens, tile); }
+int32_t page_div(int32_t ps, uint32_t t) {
+    uint32_t m, s;
+    kvi::page_divisor(ps, &m, &s);
+    return kvi::page_of(t, m, s);
+}
 int64_t range_begin(int64_t W, int64_t G, int64_t c) { return kvi::range_begin(W, G, c); }
 int64_t range_owner(int64_t W, int64_t G, int64_t x) { return kvi::range_owner(W, G, x); }
 }
@@ -245,6 +250,14 @@ def test_counts_at_the_ends(idx):
                                       (2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, (0, 2 ** 31 - 1))):
         idx.seen_range(length, cap, window, ctypes.byref(first), ctypes.byref(n))
         assert (first.value, n.value) == want
+
+
+def test_page_division(idx):
+    rng = random.Random(1)
+    for ps in list(range(1, 300)) + [2 ** k + e for k in range(8, 17) for e in (-1, 0, 1) if 2 ** k + e <= 65536]:
+        ts = {0, 1, ps - 1, ps, ps + 1, 2 ** 31 - 1, 2 ** 31 - 2, (2 ** 31 - 1) // ps * ps, max(0, (2 ** 31 - 1) // ps * ps - 1)}
+        for t in ts | {rng.randrange(2 ** 31) for _ in range(40)}:
+            assert idx.page_div(ps, t) == t // ps
 
 
 def test_ranges_cover_every_tile_once(idx):
