@@ -7,8 +7,8 @@
 //
 // Angles.  w_i / 2 pi is held as a 64-bit fraction of a turn, so position times frequency modulo
 // one turn is one wrapping integer product, exact to 2^-64 p of a turn at every position (an fp32
-// angle at position 10^5 is off by 2^-8 rad).  The top 32 bits as a signed fraction go to
-// sincospif: the angle's error is 2^-25 of itself, far below the output's rounding.
+// angle at position 10^5 is off by 2^-8 rad).  The top 32 bits are a signed fraction: its leading 24
+// go to sincospif, the rest turns the result, so sine and cosine are off by sincospif's error alone.
 //
 // Appending stores keys (rotated) and values as they are or as E4M3 codes with one power of two
 // per 32 elements: X = floor(log2 amax) - 8, code = e4m3_rn(x 2^-X) saturated at 448, straight
@@ -106,44 +106,67 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], int min_exp, uin
 }
 
 // LPR lanes a row of 8 elements each; INTER: interleaved pairs; VEC: rows are 16-byte aligned and
-// d, and for halves rot / 2, multiples of 8; E4M3: the cache's planes are quantised.
-template <class TY, int LPR, bool INTER, bool VEC, bool E4M3>
+// d, and for halves rot / 2, multiples of 8; CACHE: 0 none (rotation alone), 1 planes of the activations'
+// type, 2 E4M3.
+template <class TY, int LPR, bool INTER, bool VEC, int CACHE>
 __global__ void __launch_bounds__(THREADS) rope_append_kernel(const __grid_constant__ RopeParams p,
                                                               const __grid_constant__ Frequencies fr) {
-    extern __shared__ __align__(16) float s_cs[];      // [tpc][2][half]: cosines, sines
+    extern __shared__ __align__(16) float s_cs[];      // [tpc][2][pitch]: cosines, sines
     __shared__ int64_t s_slot[MAX_TPC], s_sslot[MAX_TPC];
-    const int tid = threadIdx.x, half = p.rot / 2;
+    const int tid = threadIdx.x, half = p.rot / 2, pitch = (half + 3) & ~3;
     const int t0 = blockIdx.x * p.tpc, nt = min(p.tpc, p.T - t0);
     constexpr int RPP = THREADS / LPR;                 // rows a pass
-    const int lane_r = tid % LPR, row_r = tid / LPR;
+    const int lane_r = tid % LPR;
     const int e0 = 8 * lane_r;
-    const int heads = p.hq + 2 * p.hkv;
+    const int heads = p.hq + (CACHE ? 2 * p.hkv : 0);
     // this block's heads (few tokens: a token's heads are dealt to several blocks)
-    const int h0 = heads * int(blockIdx.y) / p.hsplit, h1 = heads * int(blockIdx.y + 1) / p.hsplit;
-    const int nh = h1 - h0, rows = nt * nh;
+    const int h0 = heads * int(blockIdx.y) / p.hsplit, nh = heads * int(blockIdx.y + 1) / p.hsplit - h0;
 
-    auto source = [&](int r, int &t, int &h, int &side) {
-        t = r / nh;
-        h = h0 + r - t * nh;
-        side = h < p.hq ? 0 : (h < p.hq + p.hkv ? 1 : 2);
-        h -= side == 0 ? 0 : (side == 1 ? p.hq : p.hq + p.hkv);
-        return p.x[side] + (t0 + t) * p.xt[side] + h * p.xh[side];
+    // This lane's rows, RPP apart in the order token, head: the next one without a division.
+    struct Row {
+        int t, h;
     };
-    auto fetch = [&](int base, uint4 (&v)[ROWS]) {
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-            const int r = base + i * RPP + row_r;
-            if (r < rows) {
-                int t, h, side;
-                v[i] = load8<VEC>(source(r, t, h, side), e0, p.d);
-            }
+    const int dt = RPP / nh, dh = RPP - dt * nh;
+    auto next = [&](Row &r) {
+        r.t += dt;
+        r.h += dh;
+        if (r.h >= nh) {
+            r.h -= nh;
+            ++r.t;
         }
     };
+    // Which of q, k, v the row is of, and its head there.
+    auto side_of = [&](const Row &r, int &h) {
+        h = h0 + r.h;
+        if (!CACHE || h < p.hq) return 0;
+        h -= p.hq;
+        if (h < p.hkv) return 1;
+        h -= p.hkv;
+        return 2;
+    };
+    auto source = [&](const Row &r) {
+        int h;
+        const int side = side_of(r, h);
+        const uint8_t *x = side == 0 ? p.x[0] : (side == 1 ? p.x[1] : p.x[2]);
+        const int64_t xt = side == 0 ? p.xt[0] : (side == 1 ? p.xt[1] : p.xt[2]);
+        const int64_t xh = side == 0 ? p.xh[0] : (side == 1 ? p.xh[1] : p.xh[2]);
+        return x + (t0 + r.t) * xt + h * xh;
+    };
+    auto fetch = [&](Row r, uint4 (&v)[ROWS]) {
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            if (r.t < nt) v[i] = load8<VEC>(source(r), e0, p.d);
+            next(r);
+        }
+        return r;
+    };
+    const int r0 = tid / LPR;
+    Row row = {r0 / nh, r0 % nh};
     uint4 v[ROWS];
-    fetch(0, v);
+    Row ahead = fetch(row, v);
 
     // slots of the block's tokens in the cache, and their sines and cosines
-    if (p.hkv > 0 && tid < nt) {
+    if (CACHE && tid < nt) {
         const int t = t0 + tid, seq = p.seqs[t];
         int32_t page = 0, off = 0;
         bool ok = seq >= 0 && seq < p.max_seqs;
@@ -156,62 +179,66 @@ __global__ void __launch_bounds__(THREADS) rope_append_kernel(const __grid_const
     for (int i = tid; i < nt * half; i += THREADS) {
         const int t = i / half, j = i - t * half;
         const uint64_t turn = uint64_t(int64_t(p.pos[t0 + t])) * fr.f[j];
+        // the top 32 bits as a signed fraction of half a turn: the 24 an fp32 holds, and the angle of
+        // the rest, which turns the result by the first two terms of its series
+        const int32_t top = int32_t(turn >> 32);
+        const float x = float(top);
+        const float rest = float(top - (x < 0x1p31f ? int32_t(x) : 0x7FFFFFFF)) * (3.14159265358979f * 0x1p-31f);
         float s, c;
-        sincospif(float(int32_t(turn >> 32)) * 0x1p-31f, &s, &c);
-        s_cs[(2 * t) * half + j] = c * p.mscale;
-        s_cs[(2 * t + 1) * half + j] = s * (p.mscale * p.sign);
+        sincospif(x * 0x1p-31f, &s, &c);
+        s_cs[(2 * t) * pitch + j] = (c - rest * s) * p.mscale;
+        s_cs[(2 * t + 1) * pitch + j] = (s + rest * c) * (p.mscale * p.sign);
     }
     __syncthreads();
 
-    for (int base = 0; base < rows; base += ROWS * RPP) {
-        if (base) {
-            // rows of an earlier pass were stored above; these are other rows, so an output that
-            // is the input itself is still read before it is written
-            fetch(base, v);
-        }
+    // every lane of the block makes the same number of rounds (the rows' exchanges are by warp)
+    for (int done = 0; done < nt * nh; done += ROWS * RPP) {
+        // the next rows' loads are in flight while these are turned: an output that is the input
+        // itself is read before it is written, rows never share elements
+        uint4 w[ROWS];
+        const Row after = fetch(ahead, w);
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
-            const int r = base + i * RPP + row_r;
-            if (base + i * RPP >= rows) break;          // the same for every lane
-            const bool live = r < rows;
-            int t = 0, h = 0, side = 0;
-            const uint8_t *src = live ? source(r, t, h, side) : nullptr;
+            if (done + i * RPP >= nt * nh) break;       // the same for every lane
+            const bool live = row.t < nt;
+            const int t = live ? row.t : 0;
+            int h;
+            const int side = side_of(row, h);
             float x[8];
             {
-                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float2 f = TY::unpack(w[j]);
+                    const float2 f = TY::unpack(u[j]);
                     x[2 * j] = f.x;
                     x[2 * j + 1] = f.y;
                 }
             }
-            const bool turned = half > 0 && side < 2;
-            const float *cs = s_cs + (2 * t) * half, *sn = cs + half;
+            const bool turned = live && half > 0 && (!CACHE || side < 2);
+            const float *cs = s_cs + (2 * t) * pitch, *sn = cs + pitch;
             if (INTER) {
-                if (live && turned) {
+                if (turned && e0 < p.rot) {
+                    const float4 c = *reinterpret_cast<const float4 *>(cs + e0 / 2);
+                    const float4 s = *reinterpret_cast<const float4 *>(sn + e0 / 2);
+                    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int pair = e0 / 2 + j;
-                        if (pair < half) {
-                            const float a = x[2 * j], b = x[2 * j + 1], c = cs[pair], s = sn[pair];
-                            x[2 * j] = a * c - b * s;
-                            x[2 * j + 1] = a * s + b * c;
+                    for (int j = 0; j < 4; ++j)
+                        if (e0 / 2 + j < half) {
+                            const float a = x[2 * j], b = x[2 * j + 1];
+                            x[2 * j] = a * cc[j] - b * ss[j];
+                            x[2 * j + 1] = a * ss[j] + b * cc[j];
                         }
-                    }
                 }
             } else if (VEC) {
                 // the other halves of this lane's pairs are in the lane half / 8 further or back
                 const int hl = half / 8;
-                const bool first = lane_r < hl;
-                const int other = (tid & 31) - lane_r + (first ? lane_r + hl : lane_r - hl);
-                const bool in = lane_r < 2 * hl;
-                uint32_t ow[4];
-                ow[0] = __shfl_sync(0xFFFFFFFFu, v[i].x, in ? other : 0);
-                ow[1] = __shfl_sync(0xFFFFFFFFu, v[i].y, in ? other : 0);
-                ow[2] = __shfl_sync(0xFFFFFFFFu, v[i].z, in ? other : 0);
-                ow[3] = __shfl_sync(0xFFFFFFFFu, v[i].w, in ? other : 0);
-                if (live && turned && in) {
+                const bool first = lane_r < hl, in = lane_r < 2 * hl;
+                const int other = in ? (tid & 31) + (first ? hl : -hl) : 0;
+                const uint32_t ow[4] = {__shfl_sync(0xFFFFFFFFu, v[i].x, other),
+                                        __shfl_sync(0xFFFFFFFFu, v[i].y, other),
+                                        __shfl_sync(0xFFFFFFFFu, v[i].z, other),
+                                        __shfl_sync(0xFFFFFFFFu, v[i].w, other)};
+                if (turned && in) {
                     const int j0 = first ? e0 : e0 - half;
 #pragma unroll
                     for (int j = 0; j < 8; j += 4) {
@@ -222,19 +249,19 @@ __global__ void __launch_bounds__(THREADS) rope_append_kernel(const __grid_const
                         const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            x[j + k] = first ? x[j + k] * cc[k] - o[k] * ss[k]
-                                             : o[k] * ss[k] + x[j + k] * cc[k];
+                            x[j + k] = x[j + k] * cc[k] + o[k] * (first ? -ss[k] : ss[k]);
                     }
                 }
             } else {
                 // ragged halves: each element's other half straight from memory, before any lane
                 // of the warp stores (the output may be the input itself)
                 float o[8];
+                const uint8_t *src = turned ? source(row) : nullptr;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int e = e0 + j;
                     o[j] = 0.0f;
-                    if (live && turned && e < p.rot) {
+                    if (turned && e < p.rot) {
                         const uint16_t u = reinterpret_cast<const uint16_t *>(
                             src)[e < half ? e + half : e - half];
                         o[j] = TY::unpack(u).x;
@@ -244,65 +271,73 @@ __global__ void __launch_bounds__(THREADS) rope_append_kernel(const __grid_const
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int e = e0 + j;
-                    if (live && turned && e < p.rot) {
+                    if (turned && e < p.rot) {
                         const int pair = e < half ? e : e - half;
-                        x[j] = e < half ? x[j] * cs[pair] - o[j] * sn[pair]
-                                        : o[j] * sn[pair] + x[j] * cs[pair];
+                        x[j] = x[j] * cs[pair] + o[j] * (e < half ? -sn[pair] : sn[pair]);
                     }
                 }
             }
             uint32_t byte = 0;
             uint2 codes = make_uint2(0, 0);
-            if (E4M3) codes = quantise8(x, p.min_exp, &byte);       // every lane: it shuffles
-            if (!live) continue;
+            if (CACHE == 2) codes = quantise8(x, p.min_exp, &byte);     // every lane: it shuffles
             const uint4 out = make_uint4(TY::pack(x[0], x[1]), TY::pack(x[2], x[3]),
                                          TY::pack(x[4], x[5]), TY::pack(x[6], x[7]));
-            if (side == 0) {
-                store8<VEC>(p.y + (t0 + t) * p.yt + h * p.yh, e0, p.d, out);
-            } else if (s_slot[t] >= 0 && e0 < p.d) {
-                const int64_t at = s_slot[t] + h * p.head;
-                uint8_t *plane = p.pk[side - 1];
-                if (E4M3) {
-                    const int64_t sat = s_sslot[t] + h * p.shead;
-                    if (QG_IN_BOUNDS(p.err, at >= 0 && at + p.d <= p.extent &&
-                                                sat >= 0 && sat + p.d / 32 <= p.sextent)) {
-                        *reinterpret_cast<uint2 *>(plane + at + e0) = codes;
-                        if (lane_r % 4 == 0)
-                            p.ps[side - 1][sat + lane_r / 4] = static_cast<uint8_t>(byte);
+            if (live) {
+                if (side == 0) {
+                    store8<VEC>(p.y + (t0 + t) * p.yt + h * p.yh, e0, p.d, out);
+                } else if (s_slot[t] >= 0 && e0 < p.d) {
+                    const int64_t at = s_slot[t] + h * p.head;
+                    uint8_t *plane = side == 1 ? p.pk[0] : p.pk[1];
+                    if (CACHE == 2) {
+                        const int64_t sat = s_sslot[t] + h * p.shead;
+                        if (QG_IN_BOUNDS(p.err, at >= 0 && at + p.d <= p.extent &&
+                                                    sat >= 0 && sat + p.d / 32 <= p.sextent)) {
+                            *reinterpret_cast<uint2 *>(plane + at + e0) = codes;
+                            if (lane_r % 4 == 0)
+                                (side == 1 ? p.ps[0] : p.ps[1])[sat + lane_r / 4] = static_cast<uint8_t>(byte);
+                        }
+                    } else if (QG_IN_BOUNDS(p.err, at >= 0 && at + 2 * p.d <= p.extent)) {
+                        *reinterpret_cast<uint4 *>(plane + at + 2 * e0) = out;   // planes are aligned
                     }
-                } else if (QG_IN_BOUNDS(p.err, at >= 0 && at + 2 * p.d <= p.extent)) {
-                    *reinterpret_cast<uint4 *>(plane + at + 2 * e0) = out;   // planes are aligned
                 }
             }
+            next(row);
         }
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) v[i] = w[i];
+        row = ahead;
+        ahead = after;
     }
 }
 
-template <class TY, int LPR, bool INTER, bool VEC, bool E4M3>
+template <class TY, int LPR, bool INTER, bool VEC, int CACHE>
 cudaError_t launch(const RopeParams &p, const Frequencies &fr, dim3 grid, size_t smem,
                    cudaStream_t stream) {
-    rope_append_kernel<TY, LPR, INTER, VEC, E4M3><<<grid, THREADS, smem, stream>>>(p, fr);
+    rope_append_kernel<TY, LPR, INTER, VEC, CACHE><<<grid, THREADS, smem, stream>>>(p, fr);
     return cudaGetLastError();
 }
 
-template <class TY, int LPR, bool E4M3>
+template <class TY, int LPR, int CACHE>
 cudaError_t launch_layout(const RopeParams &p, const Frequencies &fr, bool inter, bool vec,
                           dim3 grid, size_t smem, cudaStream_t stream) {
-    if (inter) return vec ? launch<TY, LPR, true, true, E4M3>(p, fr, grid, smem, stream)
-                          : launch<TY, LPR, true, false, E4M3>(p, fr, grid, smem, stream);
-    return vec ? launch<TY, LPR, false, true, E4M3>(p, fr, grid, smem, stream)
-               : launch<TY, LPR, false, false, E4M3>(p, fr, grid, smem, stream);
+    if (inter) return vec ? launch<TY, LPR, true, true, CACHE>(p, fr, grid, smem, stream)
+                          : launch<TY, LPR, true, false, CACHE>(p, fr, grid, smem, stream);
+    return vec ? launch<TY, LPR, false, true, CACHE>(p, fr, grid, smem, stream)
+               : launch<TY, LPR, false, false, CACHE>(p, fr, grid, smem, stream);
 }
 
 template <class TY>
-cudaError_t launch_type(const RopeParams &p, const Frequencies &fr, bool inter, bool vec, bool e4m3,
+cudaError_t launch_type(const RopeParams &p, const Frequencies &fr, bool inter, bool vec, int cache,
                         dim3 grid, size_t smem, cudaStream_t stream) {
-    if (e4m3)      // d is 64 or 128
-        return p.d <= 64 ? launch_layout<TY, 8, true>(p, fr, inter, vec, grid, smem, stream)
-                         : launch_layout<TY, 16, true>(p, fr, inter, vec, grid, smem, stream);
-    if (p.d <= 64) return launch_layout<TY, 8, false>(p, fr, inter, vec, grid, smem, stream);
-    if (p.d <= 128) return launch_layout<TY, 16, false>(p, fr, inter, vec, grid, smem, stream);
-    return launch_layout<TY, 32, false>(p, fr, inter, vec, grid, smem, stream);
+    if (cache == 2)      // a cache's d is 64 or 128
+        return p.d <= 64 ? launch_layout<TY, 8, 2>(p, fr, inter, vec, grid, smem, stream)
+                         : launch_layout<TY, 16, 2>(p, fr, inter, vec, grid, smem, stream);
+    if (cache == 1)
+        return p.d <= 64 ? launch_layout<TY, 8, 1>(p, fr, inter, vec, grid, smem, stream)
+                         : launch_layout<TY, 16, 1>(p, fr, inter, vec, grid, smem, stream);
+    if (p.d <= 64) return launch_layout<TY, 8, 0>(p, fr, inter, vec, grid, smem, stream);
+    if (p.d <= 128) return launch_layout<TY, 16, 0>(p, fr, inter, vec, grid, smem, stream);
+    return launch_layout<TY, 32, 0>(p, fr, inter, vec, grid, smem, stream);
 }
 
 }  // namespace
@@ -392,9 +427,10 @@ cudaError_t launch_rope_append(const AppendArgs &a, const LaunchCtx &ctx) {
     const int64_t most = (heads + rpp - 1) / rpp;
     p.hsplit = (int32_t)(split < most ? split : most);
     const dim3 grid((unsigned)((a.T + tpc - 1) / tpc), (unsigned)p.hsplit);
-    const size_t smem = sizeof(float) * (size_t)tpc * (p.rot > 0 ? p.rot : 1);
-    return a.bf16 ? qg::launch_type<qg::TypeBF16>(p, fr, inter, vec, e4m3, grid, smem, ctx.stream)
-                  : qg::launch_type<qg::TypeF16>(p, fr, inter, vec, e4m3, grid, smem, ctx.stream);
+    const size_t smem = sizeof(float) * (size_t)tpc * 2 * ((p.rot / 2 + 3) / 4 * 4 + 4);
+    const int cache = append ? (e4m3 ? 2 : 1) : 0;
+    return a.bf16 ? qg::launch_type<qg::TypeBF16>(p, fr, inter, vec, cache, grid, smem, ctx.stream)
+                  : qg::launch_type<qg::TypeF16>(p, fr, inter, vec, cache, grid, smem, ctx.stream);
 }
 
 }  // namespace qgi
