@@ -353,6 +353,8 @@ qgemm_status qgemm_paged_attention(const void *Q, int64_t q_batch_stride, int64_
     if (!aligned(seqs, 4) || !aligned(lse, 4)) return fail(QGEMM_ERR_MISALIGNED, "seqs and lse must be 4-byte aligned");
     qgi::LaunchCtx ctx;
     QG_TRY(qgi::launch_ctx(stream, &ctx));
+    if (batch * q_heads * (max_pages * kv->page_size / 128 + 3) / ctx.num_sms > MAX_COUNT)
+        return fail(QGEMM_ERR_UNSUPPORTED_SHAPE, "more than 2^31 tiles of 128 tokens an SM");
     const int64_t need = (int64_t)qgi::paged_attention_workspace(kv, batch, q_heads, ctx.num_sms);
     if (!workspace || workspace_bytes < need)
         return fail(QGEMM_ERR_INVALID_ARG, "workspace of %lld bytes, %lld needed",

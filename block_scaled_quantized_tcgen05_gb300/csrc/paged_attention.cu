@@ -233,14 +233,22 @@ __device__ __forceinline__ uint32_t decode2(uint16_t codes, const Scale2 &s) {
 }
 // A position in the work: which unit, and which of its tiles.  Held alike by every lane.
 struct Cursor {
-    int64_t pos;          // of the tile, in tiles and EXTRAs over all units
-    int64_t row;          // page-table row (element offset)
+    int32_t rel;          // the tile's place after the range's begin, in tiles and EXTRAs
     int32_t b;            // sequence of the batch
     int32_t h, part;      // key-value head, and which 16 of its query heads
     int32_t tile, ntiles; // tile inside the unit, tiles of the unit
     int32_t first, n;     // tokens [first, n)
+    int32_t seq;          // page-table row
     int32_t next_seq, next_len;   // of sequence b + 1, read ahead (-1: none)
 };
+// What the computing side has to know of a step, left in shared memory by the look-up.
+struct Step {
+    int32_t b, hp;        // sequence, key-value head * chunks + part
+    int32_t t0;           // place of the unit's first tile after the range's begin (negative: before it)
+    uint32_t tiles;       // of the unit; LAST: the unit's or the range's last tile, END: the range's
+};
+constexpr uint32_t LAST = 0x80000000u, END = 0x40000000u;
+constexpr int STEPS = 8;  // steps looked up and not yet computed, at most
 
 __device__ __forceinline__ int32_t sequence(const AttnParams &p, int b) {
     if (b >= p.B) return -1;
@@ -257,14 +265,14 @@ __device__ __forceinline__ void read_ahead(Cursor &c, const AttnParams &p) {
     c.next_len = c.next_seq >= 0 ? p.lens[c.next_seq] : 0;
 }
 __device__ __forceinline__ void enter(Cursor &c, const AttnParams &p, int32_t seq, int32_t len) {
-    c.row = (seq >= 0 ? seq : 0) * p.table_stride;
+    c.seq = max(seq, 0);
     c.ntiles = extent(p, len, &c.first, &c.n);
 }
 __device__ __forceinline__ void advance(Cursor &c, const AttnParams &p) {
-    ++c.pos;
+    ++c.rel;
     if (++c.tile < c.ntiles) return;
     c.tile = 0;
-    c.pos += EXTRA;
+    c.rel += EXTRA;
     if (++c.part < p.chunks) return;
     c.part = 0;
     if (++c.h < p.hkv) return;
@@ -282,8 +290,9 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
     __shared__ float s_m[NWARPS][ROWS], s_l[NWARPS][ROWS];
     __shared__ int64_t s_scan[NWARPS];
     __shared__ int64_t s_at;
-    __shared__ int32_t s_start[2];
+    __shared__ int32_t s_start[3];
     __shared__ uint32_t s_mask[NWARPS][C::NSTAGES];
+    __shared__ __align__(16) Step s_step[NWARPS][STEPS];
     __shared__ int s_last;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int g = lane / 4, c4 = lane % 4;
@@ -342,20 +351,20 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
     }
     __syncthreads();
 
-    Cursor use;                          // the tile being computed
-    use.b = s_start[0];
-    use.h = s_start[1] / p.chunks;
-    use.part = s_start[1] - use.h * p.chunks;
-    int64_t unit_at = s_at;              // where the unit begins in the whole order
+    const int32_t span = (int32_t)(end - begin);
+    Cursor load;                         // the tile whose pages are being looked up
+    load.b = s_start[0];
+    load.h = s_start[1] / p.chunks;
+    load.part = s_start[1] - load.h * p.chunks;
     {
-        const int32_t seq = sequence(p, use.b);
-        enter(use, p, seq, seq >= 0 ? p.lens[seq] : 0);
-        read_ahead(use, p);
+        const int32_t seq = sequence(p, load.b);
+        enter(load, p, seq, seq >= 0 ? p.lens[seq] : 0);
+        read_ahead(load, p);
+        const int64_t into = begin - s_at - EXTRA;      // below 0: inside the unit's EXTRA
+        load.tile = (int32_t)max((int64_t)0, into);
+        load.rel = (int32_t)max((int64_t)0, -into);
     }
-    use.tile = (int32_t)max((int64_t)0, begin - unit_at - EXTRA);
-    use.pos = unit_at + EXTRA + use.tile;
-    if (use.pos >= end) return;          // a range inside a unit's EXTRA
-    Cursor load = use;                   // the tile whose pages are being looked up
+    if (load.rel >= span) return;        // no tile in the range
     const uint32_t ring = smem_u32(smem) + warp * (C::NSTAGES * C::STAGEB);
     float *merge = reinterpret_cast<float *>(smem + NWARPS * C::NSTAGES * C::STAGEB);
 
@@ -364,23 +373,30 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
     // a step lies in one page, and every lane holds its entry; otherwise lane l holds token l's.
     int32_t pg = -1, pr = 0;             // page-table entry and row inside the page
     int32_t p_lo = 0, p_hi = 0;          // rows of the step that are tokens of the range
-    int64_t p_off = 0, p_soff = 0;       // the head's place in a page
-    auto look_up = [&] {
+    int32_t ph = 0;                      // its key-value head
+    auto look_up = [&](int k) {          // the range's k-th step
         p_lo = p_hi = 0;
-        if (load.pos < end) {
+        if (load.rel < span) {
             const int32_t t0 = load.first / STEP * STEP + load.tile * TILE + warp * STEP;
             p_lo = max(load.first - t0, 0);
             p_hi = min(load.n - t0, STEP);
-            p_off = load.h * p.head;
-            if (C::E4M3) p_soff = load.h * p.shead;
+            ph = load.h;
             const int32_t l = p.one_page ? 0 : lane;
             if (p_lo < p_hi && l < STEP) {
                 const int32_t t = t0 + l, i = kvi::page_of((uint32_t)t, p.page_magic, p.page_shift);
                 pr = t - i * p.page_size + (p.one_page ? lane : 0);
                 // rows before the range's first token may lie in a page of no interest
-                if (p.one_page || (l >= p_lo && l < p_hi)) pg = p.table[load.row + i];
+                if (p.one_page || (l >= p_lo && l < p_hi)) pg = p.table[load.seq * p.table_stride + i];
             }
+            Step st;
+            st.b = load.b;
+            st.hp = load.h * p.chunks + load.part;
+            st.t0 = load.rel - load.tile;
+            st.tiles = load.ntiles;
             advance(load, p);
+            if (load.tile == 0) st.tiles |= LAST;
+            if (load.rel >= span) st.tiles |= LAST | END;
+            if (lane == 0) s_step[warp][k % STEPS] = st;
         }
     };
     // ---- the copies of the looked-up step into ring slot `slot`
@@ -395,8 +411,8 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
                 report_index(p.err);
                 ok = false;
             } else {
-                off = p_off + pg * p.page + pr * p.token;
-                if (C::E4M3) soff = p_soff + pg * p.spage + pr * p.stoken;
+                off = pg * p.page + pr * p.token + ph * p.head;
+                if (C::E4M3) soff = pg * p.spage + pr * p.stoken + ph * p.shead;
                 ok = QG_IN_BOUNDS(p.err, off >= 0 && off + C::ROWB <= p.extent);
                 if (!ok) off = soff = 0;
             }
@@ -438,13 +454,13 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
     uint32_t qb[C::NH][C::D / 16][2];       // query fragments
     float acc[C::NH][C::MT][4];             // rows of d, columns of heads 2 c4, 2 c4 + 1
     float m[C::NH][2], l[C::NH][2];
-    auto load_queries = [&](const Cursor &c) {
-        const int h0 = c.h * p.group + c.part * ROWS;
-        const int rows = min(ROWS, p.group - c.part * ROWS);
+    auto load_queries = [&](const Step &u) {
+        const int h = u.hp / p.chunks, part = u.hp - h * p.chunks;
+        const int h0 = h * p.group + part * ROWS, rows = min(ROWS, p.group - part * ROWS);
 #pragma unroll
         for (int n = 0; n < C::NH; ++n) {
             const bool in = 8 * n + g < rows;
-            const uint8_t *q = p.q + c.b * p.qb + (h0 + 8 * n + g) * p.qh;
+            const uint8_t *q = p.q + u.b * p.qb + (h0 + 8 * n + g) * p.qh;
 #pragma unroll
             for (int kk = 0; kk < C::D / 16; ++kk) {
                 // 16-bit rows: the fragments ldmatrix gives; 8-bit rows: thread c4 holds 8 consecutive
@@ -628,22 +644,22 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
     };
 
     // Writes four consecutive elements of a finished row.
-    auto finish_row = [&](const Cursor &c, int row, int col, float4 o, float L, float M) {
-        const int in_group = c.part * ROWS + row;
+    auto finish_row = [&](const Step &u, int row, int col, float4 o, float L, float M) {
+        const int hk = u.hp / p.chunks, in_group = (u.hp - hk * p.chunks) * ROWS + row;
         if (in_group >= p.group) return;
-        const int h = c.h * p.group + in_group;
+        const int h = hk * p.group + in_group;
         const float inv = L > 0.0f || L != L ? 1.0f / L : 0.0f;     // an empty row is 0
-        *reinterpret_cast<uint2 *>(p.o + c.b * p.ob + h * p.oh + 2 * col) =
+        *reinterpret_cast<uint2 *>(p.o + u.b * p.ob + h * p.oh + 2 * col) =
             make_uint2(TY::pack(o.x * inv, o.y * inv), TY::pack(o.z * inv, o.w * inv));
         if (p.lse && col == 0)
-            p.lse[(int64_t)c.b * p.hq + h] = L == 0.0f ? -INFINITY : M * LN2 + logf(L);
+            p.lse[(int64_t)u.b * p.hq + h] = L == 0.0f ? -INFINITY : M * LN2 + logf(L);
     };
 
     // ---- end of the tiles this CTA has of a unit: the warps' rows are merged; a whole unit is
     // written out, a part goes to the workspace
-    auto end_unit = [&](const Cursor &c) {
-        const int64_t t0 = unit_at + EXTRA, t1 = t0 + c.ntiles - 1;     // the unit's first and last tile
-        const bool whole = t0 >= begin && t1 < end, opens = t0 >= begin;
+    auto end_unit = [&](const Step &u) {
+        const int32_t tiles = (int32_t)(u.tiles & ~(LAST | END));
+        const bool opens = u.t0 >= 0, whole = opens && u.t0 + tiles <= span;
         float *part = p.partial + (2 * cta + (opens ? 1 : 0)) * C::PARTIAL;
 #pragma unroll
         for (int n = 0; n < C::NH; ++n)
@@ -691,7 +707,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
                     L += f * s_l[w][row];
                 }
                 if (whole) {
-                    finish_row(c, row, col, o, L, M);
+                    finish_row(u, row, col, o, L, M);
                 } else {
                     *reinterpret_cast<float4 *>(part + row * C::D + col) = o;
                     if (col == 0) {
@@ -703,10 +719,11 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
         }
         if (!whole) {
             // the last CTA to arrive merges all parts, in the order of the ranges
-            const int64_t c_first = kvi::range_owner(W, G, t0), c_last = kvi::range_owner(W, G, t1);
+            const int64_t c_first = kvi::range_owner(W, G, begin + u.t0);
+            const int64_t c_last = kvi::range_owner(W, G, begin + u.t0 + tiles - 1);
             __threadfence();
             __syncthreads();
-            const int64_t unit = ((int64_t)c.b * p.hkv + c.h) * p.chunks + c.part;
+            const int64_t unit = (int64_t)u.b * units_b + u.hp;
             if (tid == 0) {
                 const int old = atomicAdd(p.counters + unit, 1);
                 s_last = old == (int)(c_last - c_first);
@@ -735,7 +752,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
                         o.z = o.z * fo + a.z * fc;
                         o.w = o.w * fo + a.w * fc;
                     }
-                    finish_row(c, row, col, o, L, M);
+                    finish_row(u, row, col, o, L, M);
                 }
             }
         }
@@ -743,20 +760,21 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
     };
 
     // ---- the loop
-    look_up();
-#pragma unroll
+    look_up(0);
     for (int i = 0; i < C::NSTAGES - 1; ++i) {
         issue(i);
         cp_commit();
-        look_up();
+        look_up(i + 1);
     }
-    load_queries(use);
+    __syncwarp();
+    load_queries(s_step[warp][0]);
     clear();
     int slot = 0, fill = C::NSTAGES - 1;
-    while (true) {
+#pragma unroll 1
+    for (int k = 0;; ++k) {
         issue(fill);                            // the slot the step before this one has left
         cp_commit();
-        look_up();
+        look_up(k + C::NSTAGES);
         cp_wait<C::NSTAGES - 1>();
         __syncwarp();
         const uint32_t mask = s_mask[warp][slot];
@@ -781,14 +799,12 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
         __syncwarp();                           // every lane has read the slot
         slot = slot + 1 == C::NSTAGES ? 0 : slot + 1;
         fill = fill + 1 == C::NSTAGES ? 0 : fill + 1;
-        const Cursor done = use;
-        advance(use, p);
-        const bool more = use.pos < end;
-        if (use.tile == 0 || !more) {
-            if (more) load_queries(use);        // in flight while the warps merge
+        if (s_step[warp][k % STEPS].tiles & LAST) {
+            const Step done = s_step[warp][k % STEPS];
+            const bool more = !(done.tiles & END);
+            if (more) load_queries(s_step[warp][(k + 1) % STEPS]);   // in flight while the warps merge
             end_unit(done);
             if (!more) break;
-            unit_at += done.ntiles + EXTRA;
             clear();
         }
     }
@@ -797,7 +813,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
 
 template <class C>
 cudaError_t launch(const AttnParams &p, int64_t most, const qgi::LaunchCtx &ctx) {
-    static_assert(C::SMEM + 2048 <= (C::TWO ? 113 : 226) * 1024, "shared memory");
+    static_assert(C::SMEM + 2560 <= (C::TWO ? 113 : 227) * 1024, "shared memory");
     static_assert(C::NSTAGES >= 3, "stages");
     // the attribute stays with the device's context: set once on each device
     static std::atomic<uint64_t> ready{0};
