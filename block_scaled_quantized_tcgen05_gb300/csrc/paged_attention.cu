@@ -54,7 +54,6 @@ constexpr int THREADS = 32 * NWARPS;
 constexpr int ROWS = 16;                    // query heads of a unit at most
 constexpr int STEP = 16;                    // tokens of a warp's step (the scores' M)
 constexpr int TILE = STEP * NWARPS;
-constexpr int EXTRA = 1;                    // what a unit costs beyond its tiles, in tiles
 constexpr float P_SHIFT = 15.0f;            // P is held times 2^P_SHIFT
 constexpr float P_LEAST = 0x1p-24f;         // the smallest half
 constexpr float LN2 = 0.69314718055994531f;
@@ -98,6 +97,9 @@ struct Cfg {
     static constexpr int FIT = (ROOM - MERGEB) / (NWARPS * STAGEB);
     static constexpr int NSTAGES = FIT > 6 ? 6 : FIT;
     static constexpr int SMEM = NWARPS * NSTAGES * STAGEB + MERGEB;
+    // What a unit costs beyond its tiles, in tiles (measured, 128 ragged E4M3 sequences: 0 / 1 / 2 / 3 /
+    // 4 extra 226 / 187 / 166 / 164 / 167 us; 64 ragged fp16 ones 134 / 124 / 124 / 124)
+    static constexpr int EXTRA = E4M3 ? 3 : 1;
     static constexpr int MT = D / 16;                    // 16-element tiles of the output
     static constexpr int PARTIAL = ROWS * (D + 2);       // floats of a partial
 };
@@ -188,17 +190,24 @@ __device__ __forceinline__ int swizzle(int row, int chunk) {
     return chunk ^ ((row >> 1) & 3);
 }
 
-// Two E4M3 codes (low and high byte) as a pair of 16-bit values: exact.
-template <class TY>
-__device__ __forceinline__ uint32_t decode2(uint16_t codes) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(codes));
-    if (!TY::BF16) return h;
-    const float2 f = TypeF16::unpack(h);
-    return TY::pack(f.x, f.y);
+// Four E4M3 codes as two pairs of 16-bit values (bytes 0, 1 and 2, 3): exact.
+__device__ __forceinline__ void decode4_f16(uint32_t codes, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(codes));
 }
-// Byte i of a word as the scale 2^(byte - 127): byte 0 is the fp32 subnormal 2^-127, byte 255 NaN.
-// FAST: neither occurs (but for the 0 of a masked row, whose codes are 0).
+template <class TY>
+__device__ __forceinline__ void decode4(uint32_t codes, uint32_t &lo, uint32_t &hi) {
+    decode4_f16(codes, lo, hi);
+    if (TY::BF16) {
+        const float2 a = TypeF16::unpack(lo), b = TypeF16::unpack(hi);
+        lo = TY::pack(a.x, a.y);
+        hi = TY::pack(b.x, b.y);
+    }
+}
+// The scale 2^(byte - 127): byte 0 is the fp32 subnormal 2^-127, byte 255 NaN.  FAST: neither occurs
+// (but for the 0 of a masked row, whose codes are 0).
 template <bool FAST>
 __device__ __forceinline__ float scale_f32(uint32_t byte) {
     if (FAST) return __uint_as_float(byte << 23);
@@ -217,20 +226,21 @@ __device__ __forceinline__ Scale2 make_scale(uint32_t lo, uint32_t hi) {
     s.h2 = TY::BF16 || !FAST ? 0u : TypeF16::pack(s.lo, s.hi);
     return s;
 }
-// Two codes times their scales, rounded once.  FAST: the scales are halves (2^-24 .. 2^15), so one
-// half multiply does it; through fp32, where the product is exact, otherwise.
+// Four codes times their scales (a pair of tokens' in each half), rounded once.  FAST: the scales
+// are halves, so one half multiply does it; through fp32, where the product is exact, otherwise.
 template <class TY, bool FAST>
-__device__ __forceinline__ uint32_t decode2(uint16_t codes, const Scale2 &s) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(codes));
+__device__ __forceinline__ void decode4(uint32_t codes, const Scale2 &s, uint32_t &lo, uint32_t &hi) {
+    decode4_f16(codes, lo, hi);
     if (FAST && !TY::BF16) {
-        uint32_t r;
-        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(s.h2));
-        return r;
+        asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(s.h2));
+        asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(s.h2));
+        return;
     }
-    const float2 f = TypeF16::unpack(h);
-    return TY::pack(f.x * s.lo, f.y * s.hi);
+    const float2 a = TypeF16::unpack(lo), b = TypeF16::unpack(hi);
+    lo = TY::pack(a.x * s.lo, a.y * s.hi);
+    hi = TY::pack(b.x * s.lo, b.y * s.hi);
 }
+
 // A position in the work: which unit, and which of its tiles.  Held alike by every lane.
 struct Cursor {
     int32_t rel;          // the tile's place after the range's begin, in tiles and EXTRAs
@@ -268,11 +278,12 @@ __device__ __forceinline__ void enter(Cursor &c, const AttnParams &p, int32_t se
     c.seq = max(seq, 0);
     c.ntiles = extent(p, len, &c.first, &c.n);
 }
+template <class C>
 __device__ __forceinline__ void advance(Cursor &c, const AttnParams &p) {
     ++c.rel;
     if (++c.tile < c.ntiles) return;
     c.tile = 0;
-    c.rel += EXTRA;
+    c.rel += C::EXTRA;
     if (++c.part < p.chunks) return;
     c.part = 0;
     if (++c.h < p.hkv) return;
@@ -309,7 +320,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
         const int32_t seq = sequence(p, b), len = seq >= 0 ? p.lens[seq] : 0;
         const int32_t tiles = extent(p, len, &first, &n);
         if (b == lo_b) unit_first = tiles;
-        mine += (int64_t)(tiles + EXTRA) * units_b;
+        mine += (int64_t)(tiles + C::EXTRA) * units_b;
         if (blockIdx.x == 0 && (seq < 0 || len != n)) report_index(p.err);
     }
     int64_t incl = mine;
@@ -338,12 +349,12 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
                 const int32_t seq = sequence(p, b);
                 tiles = extent(p, seq >= 0 ? p.lens[seq] : 0, &first, &n);
             }
-            const int64_t n = (int64_t)(tiles + EXTRA) * units_b;
+            const int64_t n = (int64_t)(tiles + C::EXTRA) * units_b;
             if (begin < at + n) {
-                const int32_t hc = (int32_t)((begin - at) / (tiles + EXTRA));
+                const int32_t hc = (int32_t)((begin - at) / (tiles + C::EXTRA));
                 s_start[0] = b;
                 s_start[1] = hc;
-                s_at = at + (int64_t)hc * (tiles + EXTRA);
+                s_at = at + (int64_t)hc * (tiles + C::EXTRA);
                 break;
             }
             at += n;
@@ -360,7 +371,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
         const int32_t seq = sequence(p, load.b);
         enter(load, p, seq, seq >= 0 ? p.lens[seq] : 0);
         read_ahead(load, p);
-        const int64_t into = begin - s_at - EXTRA;      // below 0: inside the unit's EXTRA
+        const int64_t into = begin - s_at - C::EXTRA;      // below 0: inside the unit's EXTRA
         load.tile = (int32_t)max((int64_t)0, into);
         load.rel = (int32_t)max((int64_t)0, -into);
     }
@@ -384,7 +395,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
             const int32_t l = p.one_page ? 0 : lane;
             if (p_lo < p_hi && l < STEP) {
                 const int32_t t = t0 + l, i = kvi::page_of((uint32_t)t, p.page_magic, p.page_shift);
-                pr = t - i * p.page_size + (p.one_page ? lane : 0);
+                pr = t - i * p.page_size;
                 // rows before the range's first token may lie in a page of no interest
                 if (p.one_page || (l >= p_lo && l < p_hi)) pg = p.table[load.seq * p.table_stride + i];
             }
@@ -393,7 +404,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
             st.hp = load.h * p.chunks + load.part;
             st.t0 = load.rel - load.tile;
             st.tiles = load.ntiles;
-            advance(load, p);
+            advance<C>(load, p);
             if (load.tile == 0) st.tiles |= LAST;
             if (load.rel >= span) st.tiles |= LAST | END;
             if (lane == 0) s_step[warp][k % STEPS] = st;
@@ -402,7 +413,31 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
     // ---- the copies of the looked-up step into ring slot `slot`
     constexpr int RPI = 32 / C::CHUNKS;          // rows an instruction of the warp copies
     const int chunk = lane % C::CHUNKS, row0 = lane / C::CHUNKS;
+    const int64_t lane_off = row0 * p.token + chunk * 16;
+    const int64_t lane_soff = C::E4M3 ? lane % STEP * p.stoken : 0;
     auto issue = [&](int slot) {
+        if (p.one_page && p_hi - p_lo == STEP && pg >= 0 && pg < p.pages) {
+            // a whole step of one page: rows a token stride apart
+            const uint32_t kd = ring + slot * C::STAGEB, vd = kd + C::PLANE;
+            const int64_t base = pg * p.page + pr * p.token + ph * p.head;
+            if (QG_IN_BOUNDS(p.err, base >= 0 && base + (STEP - 1) * p.token + C::ROWB <= p.extent)) {
+                const uint8_t *k = p.k + base + lane_off, *v = p.v + base + lane_off;
+#pragma unroll
+                for (int i = 0; i < STEP / RPI; ++i) {
+                    const int r = i * RPI + row0;
+                    const uint32_t d = r * C::ROWB + swizzle<C>(r, chunk) * 16;
+                    cp_async_16(kd + d, k, 16);
+                    cp_async_16(vd + d, v, 16);
+                    k += RPI * p.token;
+                    v += RPI * p.token;
+                }
+                if (C::E4M3)     // lanes 0-15: the keys' scale rows, lanes 16-31: the values'
+                    cp_async_4(vd + C::PLANE + lane * 4,
+                               (lane < STEP ? p.ks : p.vs) + pg * p.spage + pr * p.stoken + ph * p.shead + lane_soff, 4);
+                if (lane == 0) s_mask[warp][slot] = (1u << STEP) - 1;
+                return;
+            }
+        }
         bool ok = lane >= p_lo && lane < p_hi;
         const uint32_t kd = ring + slot * C::STAGEB, vd = kd + C::PLANE;
         int64_t off = 0, soff = 0;               // lane l: row l's place
@@ -411,35 +446,23 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
                 report_index(p.err);
                 ok = false;
             } else {
-                off = pg * p.page + pr * p.token + ph * p.head;
-                if (C::E4M3) soff = pg * p.spage + pr * p.stoken + ph * p.shead;
+                const int32_t r = pr + (p.one_page ? lane : 0);
+                off = pg * p.page + r * p.token + ph * p.head;
+                if (C::E4M3) soff = pg * p.spage + r * p.stoken + ph * p.shead;
                 ok = QG_IN_BOUNDS(p.err, off >= 0 && off + C::ROWB <= p.extent);
                 if (!ok) off = soff = 0;
             }
         }
         const uint32_t mask = __ballot_sync(0xFFFFFFFFu, ok);
         if (lane == 0) s_mask[warp][slot] = mask;
-        if (p.one_page && mask == (1u << STEP) - 1) {
-            // a whole step of one page: rows a token stride apart
-            int64_t o = __shfl_sync(0xFFFFFFFFu, off, 0) + row0 * p.token + chunk * 16;
 #pragma unroll
-            for (int i = 0; i < STEP / RPI; ++i) {
-                const int r = i * RPI + row0;
-                const uint32_t d = r * C::ROWB + swizzle<C>(r, chunk) * 16;
-                cp_async_16(kd + d, p.k + o, 16);
-                cp_async_16(vd + d, p.v + o, 16);
-                o += RPI * p.token;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < STEP / RPI; ++i) {
-                const int r = i * RPI + row0;
-                const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r) + chunk * 16;
-                const uint32_t n = (mask >> r) & 1 ? 16 : 0;
-                const uint32_t d = r * C::ROWB + swizzle<C>(r, chunk) * 16;
-                cp_async_16(kd + d, p.k + o, n);
-                cp_async_16(vd + d, p.v + o, n);
-            }
+        for (int i = 0; i < STEP / RPI; ++i) {
+            const int r = i * RPI + row0;
+            const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r) + chunk * 16;
+            const uint32_t n = (mask >> r) & 1 ? 16 : 0;
+            const uint32_t d = r * C::ROWB + swizzle<C>(r, chunk) * 16;
+            cp_async_16(kd + d, p.k + o, n);
+            cp_async_16(vd + d, p.v + o, n);
         }
         if (C::E4M3) {
             // lanes 0-15: the keys' scale rows, lanes 16-31: the values'
@@ -520,11 +543,11 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
                 const uint2 y = lds64(kd + (g + 8) * C::ROWB + swizzle<C>(g + 8, ch) * 16 + in);
                 const float sx = scale_f32<FAST>((bx >> (8 * blk)) & 255u);
                 const float sy = scale_f32<FAST>((by >> (8 * blk)) & 255u);
-                const uint32_t a[8] = {
-                    decode2<TY>(uint16_t(x.x & 0xFFFF)), decode2<TY>(uint16_t(y.x & 0xFFFF)),
-                    decode2<TY>(uint16_t(x.x >> 16)), decode2<TY>(uint16_t(y.x >> 16)),
-                    decode2<TY>(uint16_t(x.y & 0xFFFF)), decode2<TY>(uint16_t(y.y & 0xFFFF)),
-                    decode2<TY>(uint16_t(x.y >> 16)), decode2<TY>(uint16_t(y.y >> 16))};
+                uint32_t a[8];
+                decode4<TY>(x.x, a[0], a[2]);
+                decode4<TY>(y.x, a[1], a[3]);
+                decode4<TY>(x.y, a[4], a[6]);
+                decode4<TY>(y.y, a[5], a[7]);
 #pragma unroll
                 for (int n = 0; n < C::NH; ++n) {
                     float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -630,9 +653,10 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
                 for (int y = 0; y < 2; ++y) {
                     const uint32_t a = __byte_perm(w[0][x], w[1][x], y ? 0x7362 : 0x5140);
                     const uint32_t b = __byte_perm(w[2][x], w[3][x], y ? 0x7362 : 0x5140);
-                    weigh(2 * x + y, decode2<TY, FAST>(uint16_t(a & 0xFFFF), s01),
-                          decode2<TY, FAST>(uint16_t(a >> 16), s01), decode2<TY, FAST>(uint16_t(b & 0xFFFF), s23),
-                          decode2<TY, FAST>(uint16_t(b >> 16), s23));
+                    uint32_t t[4];
+                    decode4<TY, FAST>(a, s01, t[0], t[1]);
+                    decode4<TY, FAST>(b, s23, t[2], t[3]);
+                    weigh(2 * x + y, t[0], t[1], t[2], t[3]);
                 }
             }
         }
@@ -781,16 +805,11 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
         if (mask != 0) {
             bool far = false;
             if (C::E4M3) {
-                // values' scales that are no halves (bfloat16: 0 and 255, as for the keys)
-                if ((mask >> (lane % STEP)) & 1) {
-                    const uint32_t w = lds32(ring + slot * C::STAGEB + 2 * C::PLANE + lane * 4);
-                    const bool narrow = lane >= STEP && !TY::BF16;
-#pragma unroll
-                    for (int i = 0; i < C::D / 32; ++i) {
-                        const uint32_t byte = (w >> (8 * i)) & 255u;
-                        far = far || byte - (narrow ? 103u : 1u) > (narrow ? 39u : 253u);
-                    }
-                }
+                // FAST scales: bytes 112 .. 127 (2^-15 .. 1: blocks of the append up to 512), halves all.
+                // Others take the step through fp32.
+                constexpr uint32_t HIGH = C::D == 128 ? 0xF0F0F0F0u : 0xF0F0u;
+                const uint32_t w = lds32(ring + slot * C::STAGEB + 2 * C::PLANE + lane * 4);
+                far = ((mask >> (lane % STEP)) & 1) && (w & HIGH) != (HIGH & 0x70707070u);
                 far = __any_sync(0xFFFFFFFFu, far);
             }
             if (far) step(slot, std::false_type{});
@@ -901,8 +920,7 @@ cudaError_t launch_paged_attention(const PagedAttnArgs &a, const LaunchCtx &ctx)
     p.one_page = c->page_size % qg::STEP == 0;
     kvi::page_divisor(p.page_size, &p.page_magic, &p.page_shift);
     // no more CTAs than tiles (and EXTRAs) the table rows can hold
-    const int64_t most =
-        units * (kvi::tiles_of(a.max_pages * (int32_t)c->page_size, qg::TILE) + qg::EXTRA);
+    const int64_t most = units * (kvi::tiles_of(a.max_pages * (int32_t)c->page_size, qg::TILE) + 3);
     if (a.bf16)
         return c->d == 64 ? qg::launch_cache<qg::TypeBF16, 64>(p, e4m3, most, ctx)
                           : qg::launch_cache<qg::TypeBF16, 128>(p, e4m3, most, ctx);
