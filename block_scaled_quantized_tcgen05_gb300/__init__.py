@@ -419,6 +419,7 @@ class KVCache:
         self.handle = ctypes.c_void_p(handle)
         self.dtype = dtype
         self.layers, self.pages, self.heads, self.page_size, self.d = shape
+        self.scale = self.d ** -0.5
         self._refs = refs
 
     def close(self):
@@ -436,36 +437,57 @@ class KVCache:
 _ROPE_SCALING = {"none": 0, "linear": 1, "by_parts": 2}
 
 
+# A decode step makes several of these calls per layer, each a few microseconds of GPU time: the
+# marshalling reads a tensor's strides once and takes the raw current stream.
+torch = None
+
+
+def _load_torch():
+    global torch
+    import torch as th
+    torch = th
+    return th
+
+
+def _raw_stream(stream) -> int:
+    """cudaStream_t of a stream (default: torch's current one) as an integer."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
 def _dtype16(t) -> int:
-    import torch
-    if t.dtype == torch.float16:
+    dt = t.dtype
+    if dt is torch.float16:
         return F16
-    if t.dtype == torch.bfloat16:
+    if dt is torch.bfloat16:
         return BF16
-    raise ValueError(f"expected an fp16 or bf16 tensor, got {t.dtype}")
+    raise ValueError(f"expected an fp16 or bf16 tensor, got {dt}")
 
 
 def _rows3(t, what: str):
     """(pointer, token stride, head stride) of a [tokens, heads, d] tensor."""
-    if t.dim() != 3 or t.stride(2) != 1 and t.shape[2] > 1:
+    s = t.stride()
+    if len(s) != 3 or s[2] != 1 and t.shape[2] > 1:
         raise ValueError(f"{what}: expected a [tokens, heads, d] tensor with a contiguous last dimension")
-    return t.data_ptr(), t.stride(0), t.stride(1)
+    return t.data_ptr(), s[0], s[1]
 
 
-def _ints(t, what: str, n: int | None = None):
-    import torch
-    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+def _ints(t, what: str, n: int = 0):
+    if t.dtype is not torch.int32 or t.dim() != 1 or not t.is_contiguous():
         raise ValueError(f"{what}: expected a contiguous 1-D int32 tensor")
-    if n is not None and t.shape[0] < n:
-        raise ValueError(f"{what}: {t.shape[0]} entries, {n} needed")
+    if t.numel() < n:
+        raise ValueError(f"{what}: {t.numel()} entries, {n} needed")
     return t.data_ptr()
 
 
 def _table(t):
-    import torch
-    if t.dtype != torch.int32 or t.dim() != 2 or t.stride(1) != 1 and t.shape[1] > 1:
+    """(pointer, row stride, rows, entries a row)."""
+    s = t.stride()
+    if t.dtype is not torch.int32 or len(s) != 2 or s[1] != 1 and t.shape[1] > 1:
         raise ValueError("page table: expected a 2-D int32 tensor with contiguous rows")
-    return t.data_ptr(), t.stride(0), t.shape[0], t.shape[1]
+    shape = t.shape
+    return t.data_ptr(), s[0], shape[0], shape[1]
 
 
 def qgemm_create_rope(rot_dim: int, base: float = 10000.0, interleaved: bool = False,
@@ -473,6 +495,7 @@ def qgemm_create_rope(rot_dim: int, base: float = 10000.0, interleaved: bool = F
                       low_turns: float = 1.0, high_turns: float = 4.0, mscale: float = 1.0) -> Rotation:
     """Rotary frequencies for the first ``rot_dim`` elements of a head; ``scaling`` is "none",
     "linear" (all divided by ``factor``) or "by_parts" (slow pairs divided, fast ones kept)."""
+    _load_torch()
     if scaling not in _ROPE_SCALING:
         raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALING)}")
     out = ctypes.c_void_p()
@@ -485,21 +508,26 @@ def qgemm_create_rope(rot_dim: int, base: float = 10000.0, interleaved: bool = F
 def qgemm_rope(X, positions, rope: Rotation, out=None, inverse: bool = False, stream=None):
     """X [tokens, heads, d] (fp16 or bf16) rotated to ``positions`` (int32 [tokens]), into ``out``
     (default: in place).  ``inverse`` rotates back, which is the gradient."""
-    Y = X if out is None else out
-    if Y.shape != X.shape or Y.dtype != X.dtype:
-        raise ValueError("out: shape and type must be X's")
-    T, H, d = X.shape
-    _check(load_library().qgemm_rope(*_rows3(X, "X"), *_rows3(Y, "out"), _dtype16(X), T, H, d,
-                                     _ints(positions, "positions", T), rope.handle, int(bool(inverse)),
-                                     _stream(stream)), "qgemm_rope")
-    return Y
+    shape = X.shape
+    x = _rows3(X, "X")
+    y = x
+    if out is not None:
+        if out.shape != shape or out.dtype is not X.dtype:
+            raise ValueError("out: shape and type must be X's")
+        y = _rows3(out, "out")
+    T, H, d = shape
+    st = (_lib or load_library()).qgemm_rope(*x, *y, _dtype16(X), T, H, d, _ints(positions, "positions", T),
+                                             rope.handle, 1 if inverse else 0, _raw_stream(stream))
+    if st:
+        _check(st, "qgemm_rope")
+    return X if out is None else out
 
 
 def qgemm_create_kv_cache(k, v, k_scales=None, v_scales=None) -> KVCache:
     """View of a paged cache: ``k`` and ``v`` are [layers, pages, heads, page_size, d] device tensors
     of any strides with contiguous rows (a permuted view for another order in memory), fp16, bf16, or
     uint8 / float8_e4m3fn codes with uint8 UE8M0 scales [..., 4 bytes] in ``k_scales``, ``v_scales``."""
-    import torch
+    _load_torch()
     if k.dim() != 5 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
         raise ValueError("k and v: expected two [layers, pages, heads, page_size, d] tensors of one layout")
     if k.stride(4) != 1:
@@ -530,30 +558,37 @@ def qgemm_kv_append(kv: KVCache, layer: int, K, V, seqs, positions, table, rope:
                     Q=None, Q_out=None, stream=None):
     """Store new keys (rotated) and values [tokens, heads, d] at ``positions`` of sequences ``seqs``,
     and rotate the tokens' queries ``Q`` [tokens, q_heads, d] into ``Q_out`` (default: in place)."""
-    T = K.shape[0]
-    dt = _dtype16(K)
-    if K.shape != V.shape or tuple(K.shape) != (T, kv.heads, kv.d) or V.dtype != K.dtype:
+    shape = K.shape
+    T = shape[0]
+    dt = K.dtype
+    if shape != V.shape or tuple(shape) != (T, kv.heads, kv.d) or V.dtype is not dt:
         raise ValueError(f"K and V: expected [tokens, {kv.heads}, {kv.d}] of one type")
     q = qo = (None, 0, 0)
     hq = 0
     if Q is not None:
-        Q_out = Q if Q_out is None else Q_out
-        if Q.shape[0] != T or Q.shape[2] != kv.d or Q_out.shape != Q.shape or Q.dtype != K.dtype or \
-                Q_out.dtype != K.dtype:
-            raise ValueError(f"Q and Q_out: expected [{T}, q_heads, {kv.d}] of K's type")
-        hq = Q.shape[1]
-        q, qo = _rows3(Q, "Q"), _rows3(Q_out, "Q_out")
-    _check(load_library().qgemm_kv_append(
-        kv.handle, layer, *_rows3(K, "K"), *_rows3(V, "V"), dt, T, _ints(seqs, "seqs", T),
+        qshape = Q.shape
+        q = qo = _rows3(Q, "Q")
+        if Q_out is None:
+            Q_out = Q
+        elif Q_out is not Q:
+            if Q_out.shape != qshape or Q_out.dtype is not dt:
+                raise ValueError("Q_out: shape and type must be Q's")
+            qo = _rows3(Q_out, "Q_out")
+        hq = qshape[1]
+        if qshape[0] != T or qshape[2] != kv.d or Q.dtype is not dt:
+            raise ValueError(f"Q: expected [{T}, q_heads, {kv.d}] of K's type")
+    st = (_lib or load_library()).qgemm_kv_append(
+        kv.handle, layer, *_rows3(K, "K"), *_rows3(V, "V"), _dtype16(K), T, _ints(seqs, "seqs", T),
         _ints(positions, "positions", T), *_table(table), rope.handle if rope is not None else None,
-        *q, hq, *qo, _stream(stream)), "qgemm_kv_append")
+        *q, hq, *qo, _raw_stream(stream))
+    if st:
+        _check(st, "qgemm_kv_append")
     return Q_out
 
 
 def qgemm_paged_attention_workspace(kv: KVCache, batch: int, q_heads: int):
     """A zeroed workspace for qgemm_paged_attention calls of up to ``batch`` sequences, one after
     another on one stream."""
-    import torch
     n = ctypes.c_int64(0)
     _check(load_library().qgemm_paged_attention_workspace_bytes(kv.handle, batch, q_heads, ctypes.byref(n)),
            "qgemm_paged_attention_workspace_bytes")
@@ -566,11 +601,12 @@ def qgemm_paged_attention(Q, kv: KVCache, layer: int, table, lens, O, seqs=None,
     ``seqs[b]`` (default b), the last ``window`` of them (0: all); ``lse`` (fp32 [batch, q_heads])
     receives the log of the softmax sums.  ``workspace`` comes from qgemm_paged_attention_workspace
     (one made for the call otherwise, on the current stream)."""
-    import torch
-    B, H, d = Q.shape
-    if O.shape != Q.shape or O.dtype != Q.dtype or d != kv.d:
+    shape = Q.shape
+    q = _rows3(Q, "Q")
+    B, H, d = shape
+    if O.shape != shape or O.dtype is not Q.dtype or d != kv.d:
         raise ValueError(f"Q and O: expected [batch, q_heads, {kv.d}] of one type")
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (B, H) or not lse.is_contiguous()):
+    if lse is not None and (lse.dtype is not torch.float32 or tuple(lse.shape) != (B, H) or not lse.is_contiguous()):
         raise ValueError("lse: expected a contiguous fp32 [batch, q_heads] tensor")
     if workspace is None:
         s = stream if stream is not None and not isinstance(stream, int) else torch.cuda.current_stream()
@@ -579,11 +615,13 @@ def qgemm_paged_attention(Q, kv: KVCache, layer: int, table, lens, O, seqs=None,
         with torch.cuda.stream(s):
             workspace = qgemm_paged_attention_workspace(kv, B, H)
     t = _table(table)
-    _check(load_library().qgemm_paged_attention(
-        *_rows3(Q, "Q"), _dtype16(Q), B, H, kv.handle, layer, *t, _ints(lens, "lens", t[2]),
-        None if seqs is None else _ints(seqs, "seqs", B), *_rows3(O, "O"), _ptr(lse),
-        kv.d ** -0.5 if scale is None else float(scale), window, workspace.data_ptr(), workspace.numel(),
-        _stream(stream)), "qgemm_paged_attention")
+    st = (_lib or load_library()).qgemm_paged_attention(
+        *q, _dtype16(Q), B, H, kv.handle, layer, *t, _ints(lens, "lens", t[2]),
+        None if seqs is None else _ints(seqs, "seqs", B), *_rows3(O, "O"),
+        None if lse is None else lse.data_ptr(), kv.scale if scale is None else scale, window,
+        workspace.data_ptr(), workspace.numel(), _raw_stream(stream))
+    if st:
+        _check(st, "qgemm_paged_attention")
     return O
 
 
@@ -596,27 +634,28 @@ def qgemm_kv_resize(kv: KVCache, table, lens, refs, seqs, new_lens=None, stream=
     """Give sequences ``seqs`` ``new_lens`` tokens (None: free them): ``table`` [max_seqs, max_pages],
     ``lens`` [max_seqs] and ``refs`` [pages] (int32) are updated on the device."""
     n = seqs.shape[0]
-    _check(load_library().qgemm_kv_resize(*_meta(kv, table, lens, refs), _ints(seqs, "seqs"),
-                                          None if new_lens is None else _ints(new_lens, "new_lens", n), n,
-                                          _stream(stream)), "qgemm_kv_resize")
+    _check((_lib or load_library()).qgemm_kv_resize(
+        *_meta(kv, table, lens, refs), _ints(seqs, "seqs"),
+        None if new_lens is None else _ints(new_lens, "new_lens", n), n, _raw_stream(stream)), "qgemm_kv_resize")
 
 
 def qgemm_kv_fork(kv: KVCache, table, lens, refs, parents, children, stream=None):
     """Make sequences ``children`` copies of ``parents``: whole pages shared, a partly filled last
     page copied."""
     n = children.shape[0]
-    _check(load_library().qgemm_kv_fork(*_meta(kv, table, lens, refs), _ints(parents, "parents", n),
-                                        _ints(children, "children"), n, _stream(stream)), "qgemm_kv_fork")
+    _check((_lib or load_library()).qgemm_kv_fork(
+        *_meta(kv, table, lens, refs), _ints(parents, "parents", n), _ints(children, "children"), n,
+        _raw_stream(stream)), "qgemm_kv_fork")
 
 
 def qgemm_kv_compact(kv: KVCache, table, lens, refs, stream=None):
     """Move the pages in use to the front of the cache."""
-    _check(load_library().qgemm_kv_compact(*_meta(kv, table, lens, refs), _stream(stream)),
+    _check((_lib or load_library()).qgemm_kv_compact(*_meta(kv, table, lens, refs), _raw_stream(stream)),
            "qgemm_kv_compact")
 
 
 def qgemm_kv_copy_pages(kv: KVCache, src, dst, stream=None):
     """Copy pages ``src`` to ``dst`` (int32, on the device) in every layer."""
     n = src.shape[0]
-    _check(load_library().qgemm_kv_copy_pages(kv.handle, _ints(src, "src"), _ints(dst, "dst", n), n,
-                                              _stream(stream)), "qgemm_kv_copy_pages")
+    _check((_lib or load_library()).qgemm_kv_copy_pages(kv.handle, _ints(src, "src"), _ints(dst, "dst", n), n,
+                                                        _raw_stream(stream)), "qgemm_kv_copy_pages")

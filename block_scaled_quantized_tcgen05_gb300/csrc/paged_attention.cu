@@ -649,14 +649,20 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
             const Scale2 s01 = make_scale<TY, FAST>(byte[0], byte[1]), s23 = make_scale<TY, FAST>(byte[2], byte[3]);
 #pragma unroll
             for (int x = 0; x < C::D / 32; ++x) {
+                uint32_t t[2][4];
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     const uint32_t a = __byte_perm(w[0][x], w[1][x], y ? 0x7362 : 0x5140);
                     const uint32_t b = __byte_perm(w[2][x], w[3][x], y ? 0x7362 : 0x5140);
-                    uint32_t t[4];
-                    decode4<TY, FAST>(a, s01, t[0], t[1]);
-                    decode4<TY, FAST>(b, s23, t[2], t[3]);
-                    weigh(2 * x + y, t[0], t[1], t[2], t[3]);
+                    decode4<TY, FAST>(a, s01, t[y][0], t[y][1]);
+                    decode4<TY, FAST>(b, s23, t[y][2], t[y][3]);
+                }
+#pragma unroll
+                for (int n = 0; n < C::NH; ++n) {
+                    mma16816(TY::BF16, acc[n][2 * x], t[0][0], t[0][1], t[0][2], t[0][3], hi[n][0], hi[n][1]);
+                    mma16816(TY::BF16, acc[n][2 * x + 1], t[1][0], t[1][1], t[1][2], t[1][3], hi[n][0], hi[n][1]);
+                    mma16816(TY::BF16, acc[n][2 * x], t[0][0], t[0][1], t[0][2], t[0][3], lo[n][0], lo[n][1]);
+                    mma16816(TY::BF16, acc[n][2 * x + 1], t[1][0], t[1][1], t[1][2], t[1][3], lo[n][0], lo[n][1]);
                 }
             }
         }
