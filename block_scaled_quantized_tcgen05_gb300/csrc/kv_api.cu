@@ -313,7 +313,7 @@ qgemm_status qgemm_paged_attention_workspace_bytes(const qgemm_kv_cache *kv, int
         return fail(QGEMM_ERR_UNSUPPORTED_SHAPE, "batch and q_heads <= 65536");
     qgi::LaunchCtx ctx;
     QG_TRY(qgi::launch_ctx(nullptr, &ctx));
-    *bytes = (int64_t)qgi::paged_attention_workspace(kv, batch, q_heads, ctx.num_sms);
+    *bytes = (int64_t)qgi::paged_attention_workspace(kv, ctx.num_sms);
     return QGEMM_OK;
 }
 
@@ -355,7 +355,7 @@ qgemm_status qgemm_paged_attention(const void *Q, int64_t q_batch_stride, int64_
     QG_TRY(qgi::launch_ctx(stream, &ctx));
     if (batch * q_heads * (max_pages * kv->page_size / 128 + 3) / ctx.num_sms > MAX_COUNT)
         return fail(QGEMM_ERR_UNSUPPORTED_SHAPE, "more than 2^31 tiles of 128 tokens an SM");
-    const int64_t need = (int64_t)qgi::paged_attention_workspace(kv, batch, q_heads, ctx.num_sms);
+    const int64_t need = (int64_t)qgi::paged_attention_workspace(kv, ctx.num_sms);
     if (!workspace || workspace_bytes < need)
         return fail(QGEMM_ERR_INVALID_ARG, "workspace of %lld bytes, %lld needed",
                     (long long)(workspace ? workspace_bytes : 0), (long long)need);
@@ -382,7 +382,6 @@ qgemm_status qgemm_paged_attention(const void *Q, int64_t q_batch_stride, int64_
     a.window = (int32_t)(window > MAX_COUNT ? MAX_COUNT : window);
     a.scale = scale;
     a.workspace = workspace;
-    a.workspace_bytes = workspace_bytes;
     const cudaError_t e = qgi::launch_paged_attention(a, ctx);
     return e == cudaSuccess ? QGEMM_OK : cuda_fail(e, "qgemm_paged_attention launch");
 }

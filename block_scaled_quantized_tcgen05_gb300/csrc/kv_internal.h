@@ -77,11 +77,10 @@ struct PagedAttnArgs {
     int32_t window;          // 0: every cached token
     float scale;
     void *workspace;
-    int64_t workspace_bytes;
 };
-// Workspace: counters (one per unit, zero before the first call and after each) at its front, the
-// fp32 partial rows of units cut by range boundaries at its end.
-size_t paged_attention_workspace(const qgemm_kv_cache *kv, int64_t B, int64_t hq, int num_sms);
+// Workspace: counters (zero before the first call and after each) and the fp32 partial rows of units
+// cut by range boundaries; the same whatever the batch.
+size_t paged_attention_workspace(const qgemm_kv_cache *kv, int num_sms);
 cudaError_t launch_paged_attention(const PagedAttnArgs &a, const LaunchCtx &ctx);
 
 struct PageArgs {

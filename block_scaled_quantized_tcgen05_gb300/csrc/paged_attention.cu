@@ -22,8 +22,9 @@
 // ranges, so that ragged lengths load every SM alike whatever the batch.  A unit counts EXTRA tiles more
 // than it has, for its start and end.  Each CTA finds its range from the lengths on the device (the call
 // is the same for any lengths, so it can be captured).  A unit cut by range boundaries leaves fp32 partial
-// rows (max, sum, weighted values) in the workspace; the CTA that arrives last merges them in the order
-// of the ranges, so the bits do not depend on timing, and nothing waits on another CTA.
+// rows (max, sum, weighted values) in the workspace; of 32 parts in a row the CTA that arrives last merges
+// them in the order of the ranges, then of 32 merged ones, so the bits do not depend on timing, and nothing
+// waits on another CTA.
 //
 // Inside a CTA the warps are on their own: each takes 16 tokens of every tile, copies their rows into
 // its own ring of shared memory with cp.async (two steps ahead or more, across unit boundaries: about
@@ -74,6 +75,7 @@ struct AttnParams {
     uint32_t page_magic, page_shift;        // of kvi::page_of
     float scale_log2;
     int32_t *counters;
+    int64_t slots;                          // parts there is room for
     float *partial;
     unsigned *err;
 };
@@ -258,6 +260,8 @@ struct Step {
     uint32_t tiles;       // of the unit; LAST: the unit's or the range's last tile, END: the range's
 };
 constexpr uint32_t LAST = 0x80000000u, END = 0x40000000u;
+constexpr int FAN = 32;   // parts of a unit merged at once
+constexpr int LEVELS = 2; // FAN^LEVELS parts at most
 constexpr int STEPS = 8;  // steps looked up and not yet computed, at most
 
 __device__ __forceinline__ int32_t sequence(const AttnParams &p, int b) {
@@ -293,6 +297,84 @@ __device__ __forceinline__ void advance(Cursor &c, const AttnParams &p) {
     read_ahead(c, p);
 }
 
+// Writes four consecutive elements of a finished row of the unit.
+template <class C>
+__device__ __forceinline__ void finish_row(const AttnParams &p, const Step &u, int row, int col, float4 o,
+                                           float L, float M) {
+    using TY = typename C::TY;
+    const int hk = u.hp / p.chunks, in_group = (u.hp - hk * p.chunks) * ROWS + row;
+    if (in_group >= p.group) return;
+    const int h = hk * p.group + in_group;
+    const float inv = L > 0.0f || L != L ? 1.0f / L : 0.0f;     // an empty row is 0
+    *reinterpret_cast<uint2 *>(p.o + u.b * p.ob + h * p.oh + 2 * col) =
+        make_uint2(TY::pack(o.x * inv, o.y * inv), TY::pack(o.z * inv, o.w * inv));
+    if (p.lse && col == 0) p.lse[(int64_t)u.b * p.hq + h] = L == 0.0f ? -INFINITY : M * LN2 + logf(L);
+}
+
+// A part of a cut unit is in the workspace (by the whole CTA).  Of FAN parts in a row the CTA that
+// arrives last merges them, in the order of the ranges; then, of FAN merged ones, likewise; the last of all
+// writes the rows.  Part i of the unit is that of range first + i, in the first slot of its CTA, or in the
+// second when it opens the unit.  (32768 tokens of one key-value head, 152 parts: 17 us, and 30 when one
+// CTA merges all.  The loops stay rolled: what runs once a call is first fetched, and the same merge
+// unrolled by 16 took 1 us more at 6 parts.)
+template <class C>
+__device__ __forceinline__ void merge_parts(const AttnParams &p, const Step &u, int64_t first, int parts, int mine,
+                                         int *s_last) {
+    const int tid = threadIdx.x;
+    auto slot = [&](int i) { return 2 * (first + i) + (i == 0 ? 1 : 0); };
+    int stride = 1;
+    for (int level = 0; level < LEVELS; ++level, stride *= FAN) {
+        const int i0 = mine - mine % (FAN * stride);
+        const int members = min(FAN, (parts - i0 + stride - 1) / stride);
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) {
+            int32_t *c = p.counters + (int64_t)level * p.slots + slot(i0);
+            const int last = atomicAdd(c, 1) == members - 1;
+            if (last) *c = 0;                              // ready for the next call
+            *s_last = last;
+        }
+        __syncthreads();
+        if (!*s_last) return;
+        __threadfence();
+        const bool all = i0 == 0 && members * stride >= parts;
+        for (int x = tid; x < 8 * C::NH * C::D / 4; x += THREADS) {
+            const int row = x / (C::D / 4), col = x % (C::D / 4) * 4;
+            float M = -INFINITY, L = 0.0f;
+            float4 o = make_float4(0, 0, 0, 0);
+            const float *ml = p.partial + ROWS * C::D + row;
+#pragma unroll 4
+            for (int k = 0; k < members; ++k) {            // the loads wait for nothing
+                const int64_t at = slot(i0 + k * stride) * C::PARTIAL;
+                const float mc = __ldcg(ml + at), lc = __ldcg(ml + at + ROWS);
+                const float4 a = __ldcg(reinterpret_cast<const float4 *>(p.partial + at + row * C::D + col));
+                const float nM = fmaxf(M, mc);
+                const float fo = M == -INFINITY ? 0.0f : ex2(M - nM);
+                const float fc = mc == -INFINITY ? 0.0f : ex2(mc - nM);
+                M = nM;
+                L = L * fo + lc * fc;
+                o.x = o.x * fo + a.x * fc;
+                o.y = o.y * fo + a.y * fc;
+                o.z = o.z * fo + a.z * fc;
+                o.w = o.w * fo + a.w * fc;
+            }
+            __syncwarp();                                  // a row's lanes have read its M and L
+            if (all) {
+                finish_row<C>(p, u, row, col, o, L, M);
+            } else {                                       // in the place of the first part
+                float *q = p.partial + slot(i0) * C::PARTIAL;
+                *reinterpret_cast<float4 *>(q + row * C::D + col) = o;
+                if (col == 0) {
+                    q[ROWS * C::D + row] = M;
+                    q[ROWS * C::D + ROWS + row] = L;
+                }
+            }
+        }
+        if (all) return;
+        mine = i0;
+    }
+}
+
 template <class C>
 __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
     paged_attention_kernel(const __grid_constant__ AttnParams p) {
@@ -300,7 +382,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_m[NWARPS][ROWS], s_l[NWARPS][ROWS];
     __shared__ int64_t s_scan[NWARPS];
-    __shared__ int64_t s_at;
+    __shared__ int64_t s_at, s_range[3];     // where the first unit begins; steps in all, ranges, this one's begin
     __shared__ int32_t s_start[3];
     __shared__ uint32_t s_mask[NWARPS][C::NSTAGES];
     __shared__ __align__(16) Step s_step[NWARPS][STEPS];
@@ -360,6 +442,11 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
             at += n;
         }
     }
+    if (tid == 0) {                      // for the ends of units: not worth registers
+        s_range[0] = W;
+        s_range[1] = G;
+        s_range[2] = begin;
+    }
     __syncthreads();
 
     const int32_t span = (int32_t)(end - begin);
@@ -382,22 +469,24 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
     // ---- page look-up of this warp's tokens of the tile `load` points at, one step ahead of the
     // copies that use it.  Steps begin at multiples of 16 tokens: with pages of a multiple of 16 tokens
     // a step lies in one page, and every lane holds its entry; otherwise lane l holds token l's.
-    int32_t pg = -1, pr = 0;             // page-table entry and row inside the page
-    int32_t p_lo = 0, p_hi = 0;          // rows of the step that are tokens of the range
-    int32_t ph = 0;                      // its key-value head
+    struct {
+        int32_t pg = -1, pr = 0;         // page-table entry and row inside the page
+        int32_t lo = 0, hi = 0;          // rows of the step that are tokens of the range
+        int32_t h = 0;                   // its key-value head
+    } x;
     auto look_up = [&](int k) {          // the range's k-th step
-        p_lo = p_hi = 0;
+        x.lo = x.hi = 0;
         if (load.rel < span) {
             const int32_t t0 = load.first / STEP * STEP + load.tile * TILE + warp * STEP;
-            p_lo = max(load.first - t0, 0);
-            p_hi = min(load.n - t0, STEP);
-            ph = load.h;
+            x.lo = max(load.first - t0, 0);
+            x.hi = min(load.n - t0, STEP);
+            x.h = load.h;
             const int32_t l = p.one_page ? 0 : lane;
-            if (p_lo < p_hi && l < STEP) {
+            if (x.lo < x.hi && l < STEP) {
                 const int32_t t = t0 + l, i = kvi::page_of((uint32_t)t, p.page_magic, p.page_shift);
-                pr = t - i * p.page_size;
+                x.pr = t - i * p.page_size;
                 // rows before the range's first token may lie in a page of no interest
-                if (p.one_page || (l >= p_lo && l < p_hi)) pg = p.table[load.seq * p.table_stride + i];
+                if (p.one_page || (l >= x.lo && l < x.hi)) x.pg = p.table[load.seq * p.table_stride + i];
             }
             Step st;
             st.b = load.b;
@@ -416,7 +505,8 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
     const int64_t lane_off = row0 * p.token + chunk * 16;
     const int64_t lane_soff = C::E4M3 ? lane % STEP * p.stoken : 0;
     auto issue = [&](int slot) {
-        if (p.one_page && p_hi - p_lo == STEP && pg >= 0 && pg < p.pages) {
+        const int32_t pg = x.pg, pr = x.pr, ph = x.h;
+        if (p.one_page && x.hi - x.lo == STEP && pg >= 0 && pg < p.pages) {
             // a whole step of one page: rows a token stride apart
             const uint32_t kd = ring + slot * C::STAGEB, vd = kd + C::PLANE;
             const int64_t base = pg * p.page + pr * p.token + ph * p.head;
@@ -438,7 +528,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
                 return;
             }
         }
-        bool ok = lane >= p_lo && lane < p_hi;
+        bool ok = lane >= x.lo && lane < x.hi;
         const uint32_t kd = ring + slot * C::STAGEB, vd = kd + C::PLANE;
         int64_t off = 0, soff = 0;               // lane l: row l's place
         if (ok) {
@@ -668,21 +758,12 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
         }
     };
 
-    // Element of d that acc[][j][0] (half 0) and acc[][j][2] (half 1) hold.
-    auto element = [&](int j, int half) {
-        return C::E4M3 ? C::D / 8 * g + 2 * j + half : 16 * j + g + 8 * half;
-    };
-
-    // Writes four consecutive elements of a finished row.
-    auto finish_row = [&](const Step &u, int row, int col, float4 o, float L, float M) {
-        const int hk = u.hp / p.chunks, in_group = (u.hp - hk * p.chunks) * ROWS + row;
-        if (in_group >= p.group) return;
-        const int h = hk * p.group + in_group;
-        const float inv = L > 0.0f || L != L ? 1.0f / L : 0.0f;     // an empty row is 0
-        *reinterpret_cast<uint2 *>(p.o + u.b * p.ob + h * p.oh + 2 * col) =
-            make_uint2(TY::pack(o.x * inv, o.y * inv), TY::pack(o.z * inv, o.w * inv));
-        if (p.lse && col == 0)
-            p.lse[(int64_t)u.b * p.hq + h] = L == 0.0f ? -INFINITY : M * LN2 + logf(L);
+    // Place in the merge buffer of 16-byte piece u of a row: the four pairs of heads, whose lanes write
+    // together, go to different banks.
+    auto place = [&](int u, int row) {
+        const int pair = (row >> 1) & 3;
+        if (!C::E4M3) return u ^ (2 * pair);
+        return u ^ (C::D == 128 ? pair : (pair & 1) | ((pair & 2) << 1));
     };
 
     // ---- end of the tiles this CTA has of a unit: the warps' rows are merged; a whole unit is
@@ -690,7 +771,8 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
     auto end_unit = [&](const Step &u) {
         const int32_t tiles = (int32_t)(u.tiles & ~(LAST | END));
         const bool opens = u.t0 >= 0, whole = opens && u.t0 + tiles <= span;
-        float *part = p.partial + (2 * cta + (opens ? 1 : 0)) * C::PARTIAL;
+        // a part lies in the slot of its CTA's range: the second when it opens the unit
+        float *part = p.partial + (2 * (int64_t)blockIdx.x + (opens ? 1 : 0)) * C::PARTIAL;
 #pragma unroll
         for (int n = 0; n < C::NH; ++n)
 #pragma unroll
@@ -711,12 +793,22 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
             if (mine_r >= 0 && mine_r < C::MERGE_ROWS) {
                 float *dst = merge + (warp * C::MERGE_ROWS + mine_r) * C::D;
 #pragma unroll
-                for (int j = 0; j < C::MT; ++j)
+                for (int i = 0; i < 2; ++i) {
+                    if constexpr (C::E4M3) {         // D / 8 consecutive elements a lane
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        dst[i * C::D + element(j, 0)] = acc[n][j][i];
-                        dst[i * C::D + element(j, 1)] = acc[n][j][i + 2];
+                        for (int j = 0; j < C::MT; j += 2)
+                            *reinterpret_cast<float4 *>(dst + i * C::D + 4 * place((C::D / 8 * g + 2 * j) / 4, 2 * c4)) =
+                                make_float4(acc[n][j][i], acc[n][j][i + 2], acc[n][j + 1][i], acc[n][j + 1][i + 2]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < C::MT; ++j)
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                const int e = 16 * j + 8 * half + g;
+                                dst[i * C::D + 4 * place(e / 4, 2 * c4) + e % 4] = acc[n][j][i + 2 * half];
+                            }
                     }
+                }
             }
             __syncthreads();
             // 4 elements a thread
@@ -732,12 +824,12 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
                     const float mw = s_m[w][row];
                     const float f = mw == -INFINITY ? 0.0f : ex2(mw - M);
                     const float4 a = *reinterpret_cast<const float4 *>(
-                        merge + (w * C::MERGE_ROWS + r) * C::D + col);
+                        merge + (w * C::MERGE_ROWS + r) * C::D + 4 * place(col / 4, row));
                     o.x += f * a.x, o.y += f * a.y, o.z += f * a.z, o.w += f * a.w;
                     L += f * s_l[w][row];
                 }
                 if (whole) {
-                    finish_row(u, row, col, o, L, M);
+                    finish_row<C>(p, u, row, col, o, L, M);
                 } else {
                     *reinterpret_cast<float4 *>(part + row * C::D + col) = o;
                     if (col == 0) {
@@ -748,43 +840,9 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
             }
         }
         if (!whole) {
-            // the last CTA to arrive merges all parts, in the order of the ranges
-            const int64_t c_first = kvi::range_owner(W, G, begin + u.t0);
-            const int64_t c_last = kvi::range_owner(W, G, begin + u.t0 + tiles - 1);
-            __threadfence();
-            __syncthreads();
-            const int64_t unit = (int64_t)u.b * units_b + u.hp;
-            if (tid == 0) {
-                const int old = atomicAdd(p.counters + unit, 1);
-                s_last = old == (int)(c_last - c_first);
-                if (s_last) p.counters[unit] = 0;          // ready for the next call
-            }
-            __syncthreads();
-            if (s_last) {
-                __threadfence();
-                for (int x = tid; x < 8 * C::NH * C::D / 4; x += THREADS) {
-                    const int row = x / (C::D / 4), col = x % (C::D / 4) * 4;
-                    float M = -INFINITY, L = 0.0f;
-                    float4 o = make_float4(0, 0, 0, 0);
-#pragma unroll 4
-                    for (int64_t i = c_first; i <= c_last; ++i) {
-                        const float *q = p.partial + (2 * i + (i == c_first ? 1 : 0)) * C::PARTIAL;
-                        const float mc = __ldcg(q + ROWS * C::D + row);
-                        const float lc = __ldcg(q + ROWS * C::D + ROWS + row);
-                        const float4 a = __ldcg(reinterpret_cast<const float4 *>(q + row * C::D + col));
-                        const float nM = fmaxf(M, mc);
-                        const float fo = M == -INFINITY ? 0.0f : ex2(M - nM);
-                        const float fc = mc == -INFINITY ? 0.0f : ex2(mc - nM);
-                        M = nM;
-                        L = L * fo + lc * fc;
-                        o.x = o.x * fo + a.x * fc;
-                        o.y = o.y * fo + a.y * fc;
-                        o.z = o.z * fo + a.z * fc;
-                        o.w = o.w * fo + a.w * fc;
-                    }
-                    finish_row(u, row, col, o, L, M);
-                }
-            }
+            const int64_t first = kvi::range_owner(s_range[0], s_range[1], s_range[2] + u.t0);
+            const int64_t last = kvi::range_owner(s_range[0], s_range[1], s_range[2] + u.t0 + tiles - 1);
+            merge_parts<C>(p, u, first, (int)(last - first + 1), (int)(blockIdx.x - first), &s_last);
         }
         __syncthreads();                        // the merge buffer and s_m are free again
     };
@@ -802,9 +860,10 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
     int slot = 0, fill = C::NSTAGES - 1;
 #pragma unroll 1
     for (int k = 0;; ++k) {
-        issue(fill);                            // the slot the step before this one has left
+        issue(fill);                     // the slot the step before this one has left
         cp_commit();
         look_up(k + C::NSTAGES);
+        fill = fill + 1 == C::NSTAGES ? 0 : fill + 1;
         cp_wait<C::NSTAGES - 1>();
         __syncwarp();
         const uint32_t mask = s_mask[warp][slot];
@@ -823,7 +882,6 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
         }
         __syncwarp();                           // every lane has read the slot
         slot = slot + 1 == C::NSTAGES ? 0 : slot + 1;
-        fill = fill + 1 == C::NSTAGES ? 0 : fill + 1;
         if (s_step[warp][k % STEPS].tiles & LAST) {
             const Step done = s_step[warp][k % STEPS];
             const bool more = !(done.tiles & END);
@@ -861,10 +919,11 @@ cudaError_t launch_cache(const AttnParams &p, bool e4m3, int64_t most, const qgi
 }
 
 int64_t chunks_of(int64_t group) { return (group + ROWS - 1) / ROWS; }
-size_t counters_bytes(int64_t units) { return (size_t)((units * 4 + 255) / 256 * 256); }
-size_t partial_bytes(int64_t d, int num_sms) {
-    // two a CTA, up to two CTAs an SM
-    return ((size_t)num_sms * 4 * ROWS * (size_t)(d + 2) * sizeof(float) + 255) / 256 * 256;
+// Parts that can wait at once: two a CTA (the unit that began before its range, the one that goes on
+// after it), up to two CTAs an SM.
+int64_t slots_of(int num_sms) { return 4 * (int64_t)num_sms; }
+size_t counters_bytes(int num_sms) {
+    return (size_t)((LEVELS * slots_of(num_sms) * sizeof(int32_t) + 255) / 256 * 256);
 }
 
 }  // namespace
@@ -872,9 +931,9 @@ size_t partial_bytes(int64_t d, int num_sms) {
 
 namespace qgi {
 
-size_t paged_attention_workspace(const qgemm_kv_cache *kv, int64_t B, int64_t hq, int num_sms) {
-    const int64_t units = B * kv->heads * qg::chunks_of(hq / kv->heads);
-    return qg::counters_bytes(units) + qg::partial_bytes(kv->d, num_sms);
+size_t paged_attention_workspace(const qgemm_kv_cache *kv, int num_sms) {
+    return qg::counters_bytes(num_sms) +
+           (size_t)qg::slots_of(num_sms) * qg::ROWS * (size_t)(kv->d + 2) * sizeof(float);
 }
 
 cudaError_t launch_paged_attention(const PagedAttnArgs &a, const LaunchCtx &ctx) {
@@ -919,9 +978,8 @@ cudaError_t launch_paged_attention(const PagedAttnArgs &a, const LaunchCtx &ctx)
     p.scale_log2 = a.scale * qg::LOG2E;
     const int64_t units = (int64_t)a.B * p.hkv * p.chunks;
     p.counters = static_cast<int32_t *>(a.workspace);
-    // counters from the front, partial rows at the end: calls of different batches share a workspace
-    p.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + a.workspace_bytes / 256 * 256 -
-                                          qg::partial_bytes(c->d, ctx.num_sms));
+    p.slots = qg::slots_of(ctx.num_sms);
+    p.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + qg::counters_bytes(ctx.num_sms));
     p.err = ctx.err;
     p.one_page = c->page_size % qg::STEP == 0;
     kvi::page_divisor(p.page_size, &p.page_magic, &p.page_shift);

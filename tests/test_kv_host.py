@@ -368,3 +368,33 @@ def test_every_tile_has_one_cta(idx):
             assert sorted({c for _, c in seen[u]}) == list(range(first, last + 1))
             for c in range(first, last + 1):          # who opens the unit, as each CTA sees it
                 assert (t0 >= idx.range_begin(W, G, c)) == (c == first)
+
+
+def test_parts_are_merged_once_each():
+    """The merging of a cut unit's n parts, restated: whatever order they arrive in, one part's owner finishes with
+    all of them merged in order, every counter is back at zero, and no part is read after it was replaced."""
+    rng = random.Random(11)
+    fan, levels = 16, 3
+    for n in [2, 3, 15, 16, 17, 31, 32, 33, 152, 255, 256, 257, 304, 4096]:
+        for _ in range(3):
+            order = list(range(n))
+            rng.shuffle(order)
+            held, counters, finished = {}, {}, []
+            for first in order:
+                i, stride, value = first, 1, [first]
+                for level in range(levels):
+                    held[i] = value
+                    i0 = i - i % (fan * stride)
+                    members = min(fan, (n - i0 + stride - 1) // stride)
+                    counters[level, i0] = counters.get((level, i0), 0) + 1
+                    if counters[level, i0] != members:
+                        break
+                    counters[level, i0] = 0
+                    value = sum((held.pop(i0 + k * stride) for k in range(members)), [])
+                    if i0 == 0 and members * stride >= n:
+                        finished.append(value)
+                        break
+                    i, stride = i0, stride * fan
+                else:
+                    raise AssertionError("more levels needed")
+            assert finished == [list(range(n))] and not any(counters.values())
