@@ -50,6 +50,24 @@ struct TypeBF16 {
     }
 };
 
+// Launches a kernel as a programmatic dependent of the one before it on the stream: its blocks may be
+// resident before that one ends, and wait for it (griddep_wait, first thing in every thread).
+template <class... Params, class... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                             const Args &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // A sequence number, position, length or page-table entry was out of range: what it named is
 // skipped and the device error word says so.
 __device__ __forceinline__ void report_index(unsigned *err) { atomicOr(err, qgi::ERR_INDEX); }

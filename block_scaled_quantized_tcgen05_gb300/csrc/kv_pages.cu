@@ -10,8 +10,8 @@
 // Two kernels a call.  The first, one block of 1024 threads, does the bookkeeping: it releases,
 // scans what every item needs, scans the reference counts for that many free pages (8192 counts a
 // pass, stopping when it has enough) and writes the table.  The second moves the data: a warp
-// copies the rows of one (page, layer, plane, head), eight 16-byte loads a lane in flight.  It is
-// launched as a programmatic dependent, so its blocks are resident when the list of copies is ready.
+// copies the rows of one (page, layer, plane, head), eight 16-byte loads a lane in flight.  Both are
+// launched as programmatic dependents, so the second's blocks are resident when the list of copies is ready.
 //
 // Bound: the data (HBM, read and write) when pages move, launch latency and the chain of dependent
 // table reads when they do not.
@@ -145,6 +145,7 @@ __global__ void __launch_bounds__(META_THREADS, 1)
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     if (threadIdx.x == 0) s_copies = 0;
     griddep_launch_dependents();
+    griddep_wait();
     const int32_t capacity = m.max_pages * m.page_size;
 
     // ---- release: what is cut off, and what the children's slots held
@@ -286,6 +287,7 @@ __global__ void __launch_bounds__(META_THREADS, 1)
     __shared__ int32_t s_warp[META_WARPS];
     __shared__ int32_t s_cnt[SCAN_K * META_WARPS + META_WARPS];
     griddep_launch_dependents();
+    griddep_wait();
     int32_t mine = 0, U;
 #pragma unroll 8
     for (int i = threadIdx.x; i < m.pages; i += META_THREADS) mine += __ldcg(m.refs + i) > 0;
@@ -327,6 +329,7 @@ __global__ void __launch_bounds__(COPY_THREADS)
     copy_kernel(const __grid_constant__ Plane pl, const Copies c, const Meta m, const int32_t *map,
                 const int32_t *used, unsigned *err) {
     const int lane = threadIdx.x % 32;
+    griddep_launch_dependents();
     griddep_wait();
     if (REMAP) {
         const int32_t U = *used;
@@ -441,25 +444,16 @@ Meta meta_of(const qgi::PageArgs &a, const qgi::LaunchCtx &ctx) {
     return m;
 }
 
-// The data kernel for at most `items` copies, two blocks an SM, as a programmatic dependent of the
-// bookkeeping kernel when there is one.
+// The data kernel for at most `items` copies, two blocks an SM.
 template <bool REMAP>
 cudaError_t launch_copy(const qgemm_kv_cache *kv, const Copies &c, const Meta &m, const int32_t *map,
-                        const int32_t *used, int64_t items, bool dependent, const qgi::LaunchCtx &ctx) {
+                        const int32_t *used, int64_t items, const qgi::LaunchCtx &ctx) {
     const int64_t jobs = items * kv->layers * 2 * kv->heads;
     int64_t blocks = (jobs + COPY_THREADS / 32 - 1) / (COPY_THREADS / 32);
     if (blocks > 2 * (int64_t)ctx.num_sms) blocks = 2 * (int64_t)ctx.num_sms;
     if (blocks < 1) blocks = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(COPY_THREADS);
-    cfg.stream = ctx.stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = dependent ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, copy_kernel<REMAP>, plane_of(kv), c, m, map, used, ctx.err);
+    return launch_dependent(copy_kernel<REMAP>, dim3((unsigned)blocks), COPY_THREADS, 0, ctx.stream, plane_of(kv), c, m,
+                            map, used, ctx.err);
 }
 
 template <bool RESIZE>
@@ -475,9 +469,8 @@ cudaError_t launch_update(const qgi::PageArgs &a, const int32_t *x, const int32_
     c.dst = w + 4 * (size_t)n;
     c.tokens = w + 5 * (size_t)n;
     c.count = w + 6 * (size_t)n;
-    update_kernel<RESIZE><<<1, META_THREADS, 0, ctx.stream>>>(m, x, y, n, w, c.count + 1, c);
-    e = cudaGetLastError();
-    if (e == cudaSuccess) e = launch_copy<false>(a.kv, c, m, nullptr, nullptr, n, true, ctx);
+    e = launch_dependent(update_kernel<RESIZE>, dim3(1), META_THREADS, 0, ctx.stream, m, x, y, n, w, c.count + 1, c);
+    if (e == cudaSuccess) e = launch_copy<false>(a.kv, c, m, nullptr, nullptr, n, ctx);
     const cudaError_t f = qgi::scratch_free(scratch, ctx);
     return e != cudaSuccess ? e : f;
 }
@@ -508,10 +501,8 @@ cudaError_t launch_kv_compact(const PageArgs &a, const LaunchCtx &ctx) {
     c.src = map + m.pages;
     c.dst = c.src + m.pages;
     c.count = w + 1;
-    qg::compact_kernel<<<1, qg::META_THREADS, 0, ctx.stream>>>(m, map, used, c);
-    e = cudaGetLastError();
-    if (e == cudaSuccess)
-        e = qg::launch_copy<true>(a.kv, c, m, map, used, m.pages, true, ctx);
+    e = qg::launch_dependent(qg::compact_kernel, dim3(1), qg::META_THREADS, 0, ctx.stream, m, map, used, c);
+    if (e == cudaSuccess) e = qg::launch_copy<true>(a.kv, c, m, map, used, m.pages, ctx);
     const cudaError_t f = scratch_free(scratch, ctx);
     return e != cudaSuccess ? e : f;
 }
@@ -522,7 +513,7 @@ cudaError_t launch_kv_copy_pages(const qgemm_kv_cache *kv, const int32_t *src, c
     c.src = const_cast<int32_t *>(src);
     c.dst = const_cast<int32_t *>(dst);
     c.n = n;
-    return qg::launch_copy<false>(kv, c, qg::Meta{}, nullptr, nullptr, n, false, ctx);
+    return qg::launch_copy<false>(kv, c, qg::Meta{}, nullptr, nullptr, n, ctx);
 }
 
 }  // namespace qgi

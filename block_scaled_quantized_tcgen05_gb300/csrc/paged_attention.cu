@@ -387,6 +387,8 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
     __shared__ uint32_t s_mask[NWARPS][C::NSTAGES];
     __shared__ __align__(16) Step s_step[NWARPS][STEPS];
     __shared__ int s_last;
+    griddep_launch_dependents();
+    griddep_wait();
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int g = lane / 4, c4 = lane % 4;
     const int units_b = p.hkv * p.chunks;
@@ -907,8 +909,8 @@ cudaError_t launch(const AttnParams &p, int64_t most, const qgi::LaunchCtx &ctx)
         ready.fetch_or(uint64_t(1) << ctx.device, std::memory_order_relaxed);
     }
     const int64_t room = (int64_t)ctx.num_sms * (C::TWO ? 2 : 1);
-    paged_attention_kernel<C><<<(unsigned)(most < room ? most : room), THREADS, C::SMEM, ctx.stream>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(paged_attention_kernel<C>, dim3((unsigned)(most < room ? most : room)), THREADS, C::SMEM,
+                            ctx.stream, p);
 }
 
 template <class TY, int D>

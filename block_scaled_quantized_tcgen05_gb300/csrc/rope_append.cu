@@ -114,6 +114,8 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rope_append_kernel(const __gr
                                                               const __grid_constant__ Frequencies fr) {
     extern __shared__ __align__(16) float s_cs[];      // [tpc][2][pitch]: cosines, sines
     __shared__ int64_t s_slot[MAX_TPC], s_sslot[MAX_TPC];
+    griddep_launch_dependents();
+    griddep_wait();
     const int tid = threadIdx.x, half = p.rot / 2, pitch = (half + 3) & ~3;
     const int t0 = blockIdx.x * p.tpc, nt = min(p.tpc, p.T - t0);
     constexpr int RPP = THREADS / LPR;                 // rows a pass
@@ -317,8 +319,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rope_append_kernel(const __gr
 template <class TY, int LPR, bool INTER, bool VEC, int CACHE>
 cudaError_t launch(const RopeParams &p, const Frequencies &fr, dim3 grid, size_t smem,
                    cudaStream_t stream) {
-    rope_append_kernel<TY, LPR, INTER, VEC, CACHE><<<grid, THREADS, smem, stream>>>(p, fr);
-    return cudaGetLastError();
+    return launch_dependent(rope_append_kernel<TY, LPR, INTER, VEC, CACHE>, grid, THREADS, smem, stream, p, fr);
 }
 
 template <class TY, int LPR, int CACHE>
