@@ -17,9 +17,10 @@
 //
 // Bound: memory (one read and one write of every element; at 16384 x 48 rows of 128 about 0.4 GB).
 // A block takes the rows (token, head) of a few tokens: the sines and cosines of its tokens are
-// computed once into shared memory, while the first rows' loads are already in flight, and every
-// row is read 16 bytes a lane, LPR lanes a row, four rows a lane before the first is used.  A pair's
-// other half comes from the lane that holds it (a shuffle), so each element is read once.
+// computed once into shared memory, while the first rows' loads are already in flight, and the next
+// rows' loads are in flight while a row is turned.  Aligned rows go through rope_pair_kernel; the general
+// kernel reads 16 bytes a lane, LPR lanes a row, or single elements where rows are not aligned, and takes a
+// pair's other half from the lane that holds it (a shuffle) or from memory.
 #include "kv_common.cuh"
 
 namespace qg {
@@ -27,7 +28,9 @@ namespace {
 
 constexpr int THREADS = 128;
 constexpr int BLOCKS = 8;        // resident on an SM (64 registers a thread)
+constexpr int PAIR_BLOCKS = 7;   // of the paired kernel (72 registers)
 constexpr int ROWS = 4;          // rows a lane has in flight
+constexpr int PAIR_ROWS = 2;     // and in the paired kernel, of two pieces each
 constexpr int MAX_TPC = 16;      // tokens of one block
 
 struct RopeParams {
@@ -45,6 +48,7 @@ struct RopeParams {
     int32_t rot;                 // 0: no rotation
     int32_t min_exp;             // smallest X of an E4M3 block
     float mscale, sign;
+    int32_t xt32[3], xh32[3], yt32, yh32, head32, shead32;   // the strides, where they fit (paired kernel)
     unsigned *err;
 };
 struct Frequencies {
@@ -104,6 +108,36 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], int min_exp, uin
         w[i] = uint32_t(lo) | (uint32_t(hi) << 16);
     }
     return make_uint2(w[0], w[1]);
+}
+
+// The slots of the block's tokens in the cache, and their sines and cosines ([token][2][pitch]).
+template <bool CACHE>
+__device__ __forceinline__ void set_up(const RopeParams &p, const Frequencies &fr, int t0, int nt, int pitch,
+                                       float *s_cs, int64_t *s_slot, int64_t *s_sslot) {
+    const int tid = threadIdx.x, half = p.rot / 2;
+    if (CACHE && tid < nt) {
+        const int t = t0 + tid, seq = p.seqs[t];
+        int32_t page = 0, off = 0;
+        bool ok = seq >= 0 && seq < p.max_seqs;
+        ok = ok && kvi::locate(p.table + seq * p.table_stride, p.max_pages, p.page_size, p.pages,
+                               p.pos[t], &page, &off);
+        if (!ok) report_index(p.err);
+        s_slot[tid] = ok ? page * p.page + off * p.token : -1;
+        s_sslot[tid] = page * p.spage + off * p.stoken;
+    }
+    for (int i = tid; i < nt * half; i += THREADS) {
+        const int t = i / half, j = i - t * half;
+        const uint64_t turn = uint64_t(int64_t(p.pos[t0 + t])) * fr.f[j];
+        // the top 32 bits as a signed fraction of half a turn: the 24 an fp32 holds, and the angle of
+        // the rest, which turns the result by the first two terms of its series
+        const int32_t top = int32_t(turn >> 32);
+        const float x = float(top);
+        const float rest = float(top - (x < 0x1p31f ? int32_t(x) : 0x7FFFFFFF)) * (3.14159265358979f * 0x1p-31f);
+        float s, c;
+        sincospif(x * 0x1p-31f, &s, &c);
+        s_cs[(2 * t) * pitch + j] = (c - rest * s) * p.mscale;
+        s_cs[(2 * t + 1) * pitch + j] = (s + rest * c) * (p.mscale * p.sign);
+    }
 }
 
 // LPR lanes a row of 8 elements each; INTER: interleaved pairs; VEC: rows are 16-byte aligned and
@@ -168,30 +202,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rope_append_kernel(const __gr
     uint4 v[ROWS];
     Row ahead = fetch(row, v);
 
-    // slots of the block's tokens in the cache, and their sines and cosines
-    if (CACHE && tid < nt) {
-        const int t = t0 + tid, seq = p.seqs[t];
-        int32_t page = 0, off = 0;
-        bool ok = seq >= 0 && seq < p.max_seqs;
-        ok = ok && kvi::locate(p.table + seq * p.table_stride, p.max_pages, p.page_size, p.pages,
-                               p.pos[t], &page, &off);
-        if (!ok) report_index(p.err);
-        s_slot[tid] = ok ? page * p.page + off * p.token : -1;
-        s_sslot[tid] = page * p.spage + off * p.stoken;
-    }
-    for (int i = tid; i < nt * half; i += THREADS) {
-        const int t = i / half, j = i - t * half;
-        const uint64_t turn = uint64_t(int64_t(p.pos[t0 + t])) * fr.f[j];
-        // the top 32 bits as a signed fraction of half a turn: the 24 an fp32 holds, and the angle of
-        // the rest, which turns the result by the first two terms of its series
-        const int32_t top = int32_t(turn >> 32);
-        const float x = float(top);
-        const float rest = float(top - (x < 0x1p31f ? int32_t(x) : 0x7FFFFFFF)) * (3.14159265358979f * 0x1p-31f);
-        float s, c;
-        sincospif(x * 0x1p-31f, &s, &c);
-        s_cs[(2 * t) * pitch + j] = (c - rest * s) * p.mscale;
-        s_cs[(2 * t + 1) * pitch + j] = (s + rest * c) * (p.mscale * p.sign);
-    }
+    set_up<CACHE != 0>(p, fr, t0, nt, pitch, s_cs, s_slot, s_sslot);
     __syncthreads();
 
     // every lane of the block makes the same number of rounds (the rows' exchanges are by warp)
@@ -316,6 +327,213 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rope_append_kernel(const __gr
     }
 }
 
+// The aligned case: a lane takes 16 elements as two pieces of 8, so that for halves both elements of its
+// pairs are its own (no exchange, one sine and cosine for two outputs) and what a row costs besides its
+// elements is spent once for 16.  Halves: piece k of the first half and of the second for k < rot / 16, then
+// the two halves of what is not rotated; interleaved: piece k of the row's first half and of its second.
+// Needs rows 16-byte aligned, strides below 2^31 bytes, d a multiple of 16, rot of 16 (halves) or 8; for
+// E4M3, whose blocks of 32 are four neighbouring lanes' pieces, rot of 64 (halves).  Elsewhere the kernel
+// above, 8 elements a lane, bound by its instructions.  (30011 x 12 rows of 96, rot 48, fp16: 27.3 us, 5.1
+// TB/s, against 32.8; 15009 x 36 rows of 128 into E4M3: 43.7, 6.0 TB/s, against 62.4; 16384 x 48 rows of 128 into
+// bf16: 62.9, 6.4 TB/s, against 70.6; 8192 x 40 interleaved rows of 128, bf16: 27.1, 6.2 TB/s, against 28.3.)
+template <class TY, int LPR, bool INTER, int CACHE>
+__global__ void __launch_bounds__(THREADS, PAIR_BLOCKS) rope_pair_kernel(const __grid_constant__ RopeParams p,
+                                                            const __grid_constant__ Frequencies fr) {
+    griddep_launch_dependents();
+    griddep_wait();
+    extern __shared__ __align__(16) float s_cs[];
+    __shared__ int64_t s_slot[MAX_TPC], s_sslot[MAX_TPC];
+    const int tid = threadIdx.x, half = p.rot / 2, pitch = (half + 3) & ~3;
+    const int t0 = blockIdx.x * p.tpc, nt = min(p.tpc, p.T - t0);
+    constexpr int RPP = THREADS / LPR;
+    constexpr int PR = PAIR_ROWS;
+    const int k = tid % LPR;
+    const bool lane = 16 * k < p.d;
+    const int heads = p.hq + (CACHE ? 2 * p.hkv : 0);
+    const int h0 = heads * int(blockIdx.y) / p.hsplit, nh = heads * int(blockIdx.y + 1) / p.hsplit - h0;
+
+    // the lane's two pieces, and whether they are rotated
+    int ea, eb;
+    bool turn_a, turn_b;
+    if (INTER) {
+        ea = 8 * k;
+        eb = p.d / 2 + 8 * k;
+        turn_a = ea < p.rot;
+        turn_b = eb < p.rot;
+    } else {
+        const int hl = p.rot / 16, rest = (p.d - p.rot) / 16;
+        turn_a = turn_b = k < hl;
+        ea = turn_a ? 8 * k : p.rot + 8 * (k - hl);
+        eb = turn_a ? half + 8 * k : p.rot + 8 * (rest + k - hl);
+    }
+    turn_a = turn_a && lane;
+    turn_b = turn_b && lane;
+
+    struct Row {
+        int t, h;
+    };
+    const int dt = RPP / nh, dh = RPP - dt * nh;
+    auto next = [&](Row &r) {
+        r.t += dt;
+        r.h += dh;
+        if (r.h >= nh) {
+            r.h -= nh;
+            ++r.t;
+        }
+    };
+    auto side_of = [&](const Row &r, int &h) {
+        h = h0 + r.h;
+        if (!CACHE || h < p.hq) return 0;
+        h -= p.hq;
+        if (h < p.hkv) return 1;
+        h -= p.hkv;
+        return 2;
+    };
+    auto fetch = [&](Row r, uint4 (&a)[PR], uint4 (&b)[PR]) {
+#pragma unroll
+        for (int i = 0; i < PR; ++i) {
+            if (r.t < nt && lane) {
+                int h;
+                const int side = side_of(r, h);
+                const uint8_t *x = side == 0 ? p.x[0] : (side == 1 ? p.x[1] : p.x[2]);
+                const int32_t xt = side == 0 ? p.xt32[0] : (side == 1 ? p.xt32[1] : p.xt32[2]);
+                const int32_t xh = side == 0 ? p.xh32[0] : (side == 1 ? p.xh32[1] : p.xh32[2]);
+                const uint8_t *row = x + int64_t(t0 + r.t) * xt + int64_t(h) * xh;
+                a[i] = *reinterpret_cast<const uint4 *>(row + 2 * ea);
+                b[i] = *reinterpret_cast<const uint4 *>(row + 2 * eb);
+            }
+            next(r);
+        }
+        return r;
+    };
+    auto unpack = [](const uint4 &v, float (&x)[8]) {
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = TY::unpack(u[j]);
+            x[2 * j] = f.x;
+            x[2 * j + 1] = f.y;
+        }
+    };
+    auto pack = [](const float (&x)[8]) {
+        return make_uint4(TY::pack(x[0], x[1]), TY::pack(x[2], x[3]), TY::pack(x[4], x[5]), TY::pack(x[6], x[7]));
+    };
+    auto pairs = [](float (&x)[8], const float *cs, const float *sn) {     // interleaved pairs of a piece
+        const float4 c = *reinterpret_cast<const float4 *>(cs), s = *reinterpret_cast<const float4 *>(sn);
+        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float u = x[2 * j], v = x[2 * j + 1];
+            x[2 * j] = u * cc[j] - v * ss[j];
+            x[2 * j + 1] = u * ss[j] + v * cc[j];
+        }
+    };
+
+    Row row = {tid / LPR / nh, tid / LPR % nh};
+    uint4 va[PR], vb[PR];
+    Row ahead = fetch(row, va, vb);
+    set_up<CACHE != 0>(p, fr, t0, nt, pitch, s_cs, s_slot, s_sslot);
+    __syncthreads();
+
+    for (int done = 0; done < nt * nh; done += PR * RPP) {
+        uint4 wa[PR], wb[PR];
+        const Row after = fetch(ahead, wa, wb);        // in flight while these are turned
+#pragma unroll
+        for (int i = 0; i < PR; ++i) {
+            const bool live = row.t < nt && lane;
+            const int t = row.t < nt ? row.t : 0;
+            int h;
+            const int side = side_of(row, h);
+            next(row);
+            float a[8], b[8];
+            unpack(va[i], a);
+            unpack(vb[i], b);
+            const bool rotate = p.rot > 0 && (!CACHE || side < 2);
+            const float *cs = s_cs + (2 * t) * pitch, *sn = cs + pitch;
+            if (INTER) {
+                if (rotate && turn_a) pairs(a, cs + ea / 2, sn + ea / 2);
+                if (rotate && turn_b) pairs(b, cs + eb / 2, sn + eb / 2);
+            } else if (rotate && turn_a) {
+#pragma unroll
+                for (int j = 0; j < 8; j += 4) {
+                    const float4 c = *reinterpret_cast<const float4 *>(cs + ea + j);
+                    const float4 s = *reinterpret_cast<const float4 *>(sn + ea + j);
+                    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float u = a[j + q], v = b[j + q];
+                        a[j + q] = u * cc[q] - v * ss[q];
+                        b[j + q] = u * ss[q] + v * cc[q];
+                    }
+                }
+            }
+            if (!CACHE || side == 0) {
+                if (live) {
+                    uint8_t *y = p.y + int64_t(t0 + t) * p.yt32 + int64_t(h) * p.yh32;
+                    *reinterpret_cast<uint4 *>(y + 2 * ea) = pack(a);
+                    *reinterpret_cast<uint4 *>(y + 2 * eb) = pack(b);
+                }
+            }
+            if (CACHE == 2) {
+                // every lane of a warp that has a key or a value: it shuffles
+                if (__any_sync(0xFFFFFFFFu, live && side > 0)) {
+                    uint32_t ba, bb;
+                    const uint2 ca = quantise8(a, p.min_exp, &ba), cb = quantise8(b, p.min_exp, &bb);
+                    if (live && side > 0 && s_slot[t] >= 0) {
+                        const int64_t at = s_slot[t] + int64_t(h) * p.head32, sat = s_sslot[t] + int64_t(h) * p.shead32;
+                        if (QG_IN_BOUNDS(p.err, at >= 0 && at + p.d <= p.extent && sat >= 0 &&
+                                                    sat + p.d / 32 <= p.sextent)) {
+                            uint8_t *plane = (side == 1 ? p.pk[0] : p.pk[1]) + at;
+                            *reinterpret_cast<uint2 *>(plane + ea) = ca;
+                            *reinterpret_cast<uint2 *>(plane + eb) = cb;
+                            if (k % 4 == 0) {
+                                uint8_t *scales = (side == 1 ? p.ps[0] : p.ps[1]) + sat;
+                                scales[ea / 32] = static_cast<uint8_t>(ba);
+                                scales[eb / 32] = static_cast<uint8_t>(bb);
+                            }
+                        }
+                    }
+                }
+            } else if (CACHE == 1 && live && side > 0 && s_slot[t] >= 0) {
+                const int64_t at = s_slot[t] + int64_t(h) * p.head32;
+                if (QG_IN_BOUNDS(p.err, at >= 0 && at + 2 * p.d <= p.extent)) {
+                    uint8_t *plane = (side == 1 ? p.pk[0] : p.pk[1]) + at;
+                    *reinterpret_cast<uint4 *>(plane + 2 * ea) = pack(a);
+                    *reinterpret_cast<uint4 *>(plane + 2 * eb) = pack(b);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < PR; ++i) {
+            va[i] = wa[i];
+            vb[i] = wb[i];
+        }
+        row = ahead;
+        ahead = after;
+    }
+}
+
+template <class TY, int LPR, int CACHE>
+cudaError_t launch_pair(const RopeParams &p, const Frequencies &fr, bool inter, dim3 grid, size_t smem,
+                        cudaStream_t stream) {
+    return inter ? launch_dependent(rope_pair_kernel<TY, LPR, true, CACHE>, grid, THREADS, smem, stream, p, fr)
+                 : launch_dependent(rope_pair_kernel<TY, LPR, false, CACHE>, grid, THREADS, smem, stream, p, fr);
+}
+
+template <class TY>
+cudaError_t launch_pair_type(const RopeParams &p, const Frequencies &fr, bool inter, int cache, dim3 grid, size_t smem,
+                             cudaStream_t stream) {
+    if (cache == 2)
+        return p.d <= 64 ? launch_pair<TY, 4, 2>(p, fr, inter, grid, smem, stream)
+                         : launch_pair<TY, 8, 2>(p, fr, inter, grid, smem, stream);
+    if (cache == 1)
+        return p.d <= 64 ? launch_pair<TY, 4, 1>(p, fr, inter, grid, smem, stream)
+                         : launch_pair<TY, 8, 1>(p, fr, inter, grid, smem, stream);
+    if (p.d <= 64) return launch_pair<TY, 4, 0>(p, fr, inter, grid, smem, stream);
+    if (p.d <= 128) return launch_pair<TY, 8, 0>(p, fr, inter, grid, smem, stream);
+    return launch_pair<TY, 16, 0>(p, fr, inter, grid, smem, stream);
+}
+
 template <class TY, int LPR, bool INTER, bool VEC, int CACHE>
 cudaError_t launch(const RopeParams &p, const Frequencies &fr, dim3 grid, size_t smem,
                    cudaStream_t stream) {
@@ -419,13 +637,27 @@ cudaError_t launch_rope_append(const AppendArgs &a, const LaunchCtx &ctx) {
     }
     // Tokens a block: enough rows for four rounds of every lane's four, so that the sines are shared
     // and the last rounds short against the rest; with few tokens one token a block and its heads dealt
-    // to several blocks, two blocks an SM.  (Measured at 128 threads, 8192 x 40 rows of 128: four rounds
-    // 28.9 us, eight 31.6; 256 threads 29.9; two rows a lane in flight 31.8.)
+    // to several blocks, two blocks an SM.  (8192 x 40 rows of 128, paired kernel: four rounds 27.1 us, six
+    // 28.4, eight 31.1; one row a lane in flight 29.1.)
     const int heads = p.hq + 2 * p.hkv;
-    const int lpr = a.d <= 64 ? 8 : (a.d <= 128 ? 16 : 32);
+    bool pair = vec && a.d % 16 == 0 && (inter ? p.rot % 8 == 0 : p.rot % (e4m3 ? 64 : 16) == 0);
+    auto fits = [&](int64_t stride, int32_t *to) {
+        pair = pair && stride <= INT32_MAX;
+        *to = (int32_t)(pair ? stride : 0);
+    };
+    for (int i = 0; i < 3; ++i) {
+        fits(p.xt[i], &p.xt32[i]);
+        fits(p.xh[i], &p.xh32[i]);
+    }
+    fits(p.yt, &p.yt32);
+    fits(p.yh, &p.yh32);
+    fits(p.head, &p.head32);
+    fits(p.shead, &p.shead32);
+    int lpr = a.d <= 64 ? 8 : (a.d <= 128 ? 16 : 32);
+    if (pair) lpr /= 2;
     const int rpp = qg::THREADS / lpr;
     const int64_t slots = 2 * (int64_t)ctx.num_sms;
-    int tpc = (4 * qg::ROWS * rpp + heads - 1) / heads;
+    int tpc = (4 * (pair ? qg::PAIR_ROWS : qg::ROWS) * rpp + heads - 1) / heads;
     if (tpc > qg::MAX_TPC) tpc = qg::MAX_TPC;
     while (tpc > 1 && ((int64_t)a.T + tpc - 1) / tpc < slots) --tpc;
     p.tpc = tpc;
@@ -435,6 +667,9 @@ cudaError_t launch_rope_append(const AppendArgs &a, const LaunchCtx &ctx) {
     const dim3 grid((unsigned)((a.T + tpc - 1) / tpc), (unsigned)p.hsplit);
     const size_t smem = sizeof(float) * (size_t)tpc * 2 * ((p.rot / 2 + 3) / 4 * 4 + 4);
     const int cache = append ? (e4m3 ? 2 : 1) : 0;
+    if (pair)
+        return a.bf16 ? qg::launch_pair_type<qg::TypeBF16>(p, fr, inter, cache, grid, smem, ctx.stream)
+                      : qg::launch_pair_type<qg::TypeF16>(p, fr, inter, cache, grid, smem, ctx.stream);
     return a.bf16 ? qg::launch_type<qg::TypeBF16>(p, fr, inter, vec, cache, grid, smem, ctx.stream)
                   : qg::launch_type<qg::TypeF16>(p, fr, inter, vec, cache, grid, smem, ctx.stream);
 }
