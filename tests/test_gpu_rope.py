@@ -51,6 +51,7 @@ def _positions(T, seed):
     (333, 3, 64, 32, True, "linear", True), (17, 7, 96, 48, False, "linear", True),
     (17, 7, 96, 38, False, "none", False), (9, 5, 80, 40, False, "none", True), (9, 5, 80, 34, True, "none", False),
     (1000, 12, 256, 256, False, "by_parts", False), (4, 2, 256, 102, True, "none", True),
+    (33, 5, 72, 32, False, "none", False), (33, 5, 104, 96, False, "linear", True), (65, 9, 112, 64, True, "none", False),
     (3, 2, 2, 2, False, "none", False), (3, 3, 50, 50, False, "linear", False), (700, 48, 128, 64, True, "none", False),
 ])
 def test_rope_matches(dev, dtype, T, H, d, rot, inter, scaling, inverse):
@@ -89,6 +90,18 @@ def test_rope_strides_alignment_and_guards(dev, rot, inter):
         y.fill_(7.0)
         assert bool((out == 7.0).all())
     _clean()
+
+
+def test_rope_strides_past_31_bits(dev):
+    """Heads more than 2^31 bytes apart, of the input and of the output."""
+    T, H, d, far = 5, 2, 128, 2 ** 30 + 64
+    x = torch.empty(far + T * d, dtype=torch.float16, device=dev).as_strided((T, H, d), (d, far, 1))
+    y = torch.empty(far + T * d, dtype=torch.float16, device=dev).as_strided((T, H, d), (d, far, 1))
+    x.copy_(torch.randn(T, H, d))
+    pos = torch.arange(T, dtype=torch.int32) * 777
+    q.qgemm_rope(x, pos.to(dev), q.qgemm_create_rope(d), out=y)
+    _clean()
+    _close(y, *ref.rotate(x.cpu(), pos, d), "far heads")
 
 
 def test_rope_gradient_against_differences(dev):
@@ -165,6 +178,8 @@ def _check_e4m3(codes, scales, x, mag, dtype, what):
 @pytest.mark.parametrize("d,hq,hkv,page,rot,inter,order", [
     (128, 8, 2, 16, 128, False, "lphtd"), (128, 7, 1, 24, 64, True, "plhtd"), (64, 12, 4, 5, 64, False, "lpthd"),
     (64, 0, 3, 1, 0, False, "lphtd"), (128, 32, 8, 64, 40, False, "lpthd"),
+    (128, 4, 2, 16, 96, False, "lphtd"), (128, 3, 1, 32, 32, False, "plhtd"), (64, 5, 5, 16, 32, True, "lphtd"),
+    (64, 2, 1, 8, 16, False, "lphtd"), (128, 6, 3, 16, 100, True, "lphtd"),
 ])
 def test_append_matches(dev, dtype, e4m3, d, hq, hkv, page, rot, inter, order):
     layers, lens, new = 3, [0, 5, 2 * page + 1, 3], [4, 1, 2 * page + 3, 0]
