@@ -161,6 +161,8 @@ qgemm_status qgemm_create_kv_cache(qgemm_kv_cache **out, int32_t dtype, int64_t 
         return fail(QGEMM_ERR_UNSUPPORTED_SHAPE, "head dimension must be 64 or 128 (got %lld)", (long long)d);
     if (layers > 65536 || pages > MAX_PAGES || heads > 65536 || page_size > 65536)
         return fail(QGEMM_ERR_UNSUPPORTED_SHAPE, "layers, heads, page_size <= 65536, pages <= 2^30");
+    if (layers * heads * page_size >= (int64_t(1) << 31))
+        return fail(QGEMM_ERR_UNSUPPORTED_SHAPE, "a page has 2^31 rows or more in all layers");
     if (!k || !v || !strides) return fail(QGEMM_ERR_INVALID_ARG, "k, v or strides is NULL");
     if (k == v) return fail(QGEMM_ERR_INVALID_ARG, "k and v are the same plane");
     const bool e4m3 = dtype == QGEMM_E4M3;

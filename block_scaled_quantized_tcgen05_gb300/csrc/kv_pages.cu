@@ -7,10 +7,12 @@
 // pages are taken lowest first, in the order of the call's items, so the outcome is a function of
 // the inputs alone (atomics only add whole numbers).
 //
-// Two kernels a call.  The first, one block of 1024 threads, does the bookkeeping: it releases,
-// scans what every item needs, scans the reference counts for that many free pages (8192 counts a
-// pass, stopping when it has enough) and writes the table.  The second moves the data: a warp
-// copies the rows of one (page, layer, plane, head), eight 16-byte loads a lane in flight.  Both are
+// Two kernels a call.  The first, one block of 512 threads, does the bookkeeping: it releases,
+// scans what every item needs, scans the reference counts for that many free pages (4096 counts a
+// pass, stopping when it has enough) and writes the table.  It is a chain of dependent reads: what an item
+// is, its lengths, its table entries, the counts.  So each is read once, the items and the free pages
+// stay in shared memory (up to 1024 of each), and lines needed later are fetched into L2 early.  The second moves the data: a warp
+// copies 2 KB of the rows of one (page, layer, plane, head), four 16-byte loads a lane in flight.  Both are
 // launched as programmatic dependents, so the second's blocks are resident when the list of copies is ready.
 //
 // Bound: the data (HBM, read and write) when pages move, launch latency and the chain of dependent
@@ -20,9 +22,12 @@
 namespace qg {
 namespace {
 
-constexpr int META_THREADS = 1024;
+constexpr int META_THREADS = 512;
 constexpr int META_WARPS = META_THREADS / 32;
 constexpr int SCAN_K = 8;                       // counts a thread tests in one pass
+constexpr int SCAN = SCAN_K * META_THREADS;     // counts of a pass
+static_assert(SCAN_K * META_WARPS == 128, "four counts of hits a lane");
+constexpr int CACHED = 1024;                    // items, and listed pages, kept in shared memory
 
 struct Meta {
     int32_t *table;
@@ -42,6 +47,10 @@ struct Copies {
 
 __device__ __forceinline__ bool good_page(const Meta &m, int32_t p) { return p >= 0 && p < m.pages; }
 __device__ __forceinline__ bool good_seq(const Meta &m, int32_t s) { return s >= 0 && s < m.max_seqs; }
+
+__device__ __forceinline__ void fetch_line(const void *p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
 
 // A sequence's length as far as its table row goes.
 __device__ __forceinline__ int32_t held_tokens(const Meta &m, int32_t seq) {
@@ -76,117 +85,151 @@ __device__ __forceinline__ I block_prefix(I x, I *s_warp, I *total) {
     }
     if (lane == 31) s_warp[warp] = incl;
     __syncthreads();
-    I w = s_warp[lane];                          // META_WARPS == 32
+    const I w = lane < META_WARPS ? s_warp[lane] : I(0);
     I wi = w;
 #pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
+    for (int o = 1; o < META_WARPS; o *= 2) {
         const I y = __shfl_up_sync(0xFFFFFFFFu, wi, o);
         if (lane >= o) wi += y;
     }
-    *total = __shfl_sync(0xFFFFFFFFu, wi, 31);
+    *total = __shfl_sync(0xFFFFFFFFu, wi, META_WARPS - 1);
     const I base = __shfl_sync(0xFFFFFFFFu, wi - w, warp);
     __syncthreads();                             // s_warp is free again
     return base + incl - x;
 }
 
-// Writes the pages of [from, to) whose count is 0 (want_free) or above, in order, to `list` until
-// at least `enough` are found; returns how many were found (those past `enough` may be listed too,
-// the list has room for `room`).
-__device__ int32_t list_pages(const Meta &m, int32_t from, int32_t to, bool want_free, int32_t enough,
-                              int32_t *list, int32_t room, int32_t *s_cnt) {
+// Writes the pages of [0, pages) that are free (below `border`) or in use (from it on), in order, to
+// `list`, until at least `enough` are found; returns how many (the last pass may list more, up to
+// `room`).  s_cnt: two rows of SCAN_K x META_WARPS counts.
+__device__ int32_t list_pages(const Meta &m, int32_t border, int32_t enough, int32_t *list, int32_t room,
+                              int32_t (*s_cnt)[SCAN_K * META_WARPS]) {
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     int32_t found = 0;
-    for (int32_t base = from; base < to && found < enough; base += SCAN_K * META_THREADS) {
-        bool hit[SCAN_K];
+    int pass = 0;
+    for (int32_t base = 0; base < m.pages && found < enough; base += SCAN, pass ^= 1) {
         uint32_t votes[SCAN_K];
+        int32_t mine[SCAN_K];
 #pragma unroll
         for (int k = 0; k < SCAN_K; ++k) {
             const int32_t i = base + k * META_THREADS + (int)threadIdx.x;
-            hit[k] = i < to && i >= base && (__ldcg(m.refs + i) > 0) != want_free;
+            mine[k] = i < m.pages ? __ldcg(m.refs + i) : 0;
         }
 #pragma unroll
         for (int k = 0; k < SCAN_K; ++k) {
-            votes[k] = __ballot_sync(0xFFFFFFFFu, hit[k]);
-            if (lane == 0) s_cnt[k * META_WARPS + warp] = __popc(votes[k]);
+            const int32_t i = base + k * META_THREADS + (int)threadIdx.x;
+            votes[k] = __ballot_sync(0xFFFFFFFFu, i < m.pages && (mine[k] > 0) != (i < border));
+            if (lane == 0) s_cnt[pass][k * META_WARPS + warp] = __popc(votes[k]);
         }
         __syncthreads();
-        // exclusive prefix over the SCAN_K x META_WARPS counts
-        int32_t x = threadIdx.x < SCAN_K * META_WARPS ? s_cnt[threadIdx.x] : 0, total;
-        __syncthreads();
-        const int32_t pre = block_prefix(x, s_cnt + SCAN_K * META_WARPS, &total);
-        if (threadIdx.x < SCAN_K * META_WARPS) s_cnt[threadIdx.x] = pre;
-        __syncthreads();
+        // every warp scans the 128 counts, four a lane; the other row is free for the next pass
+        const int4 c = reinterpret_cast<const int4 *>(s_cnt[pass])[lane];
+        const int32_t sum = c.x + c.y + c.z + c.w;
+        int32_t incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int32_t y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        const int32_t e0 = incl - sum, e1 = e0 + c.x, e2 = e1 + c.y, e3 = e2 + c.z;
+        const int32_t pick = warp % 4 == 0 ? e0 : (warp % 4 == 1 ? e1 : (warp % 4 == 2 ? e2 : e3));
 #pragma unroll
         for (int k = 0; k < SCAN_K; ++k) {
-            const int32_t at = found + s_cnt[k * META_WARPS + warp] + __popc(votes[k] & ((1u << lane) - 1));
-            if (hit[k] && at < room) list[at] = base + k * META_THREADS + (int)threadIdx.x;
+            const int32_t before = __shfl_sync(0xFFFFFFFFu, pick, (k * META_WARPS + warp) / 4);
+            const int32_t at = found + before + __popc(votes[k] & ((1u << lane) - 1));
+            if (((votes[k] >> lane) & 1) && at < room) list[at] = base + k * META_THREADS + (int)threadIdx.x;
         }
-        __syncthreads();
-        found += total;
+        found += __shfl_sync(0xFFFFFFFFu, incl, 31);
     }
+    __syncthreads();
     return found;
 }
 
-// What item i takes, and what becomes of it.
+// An item of a call as the bookkeeping keeps it.
+struct Item {
+    int32_t seq;         // the sequence that changes (-1: skip the item)
+    int32_t from;        // fork: the parent
+    int32_t now;         // tokens it holds
+    int32_t want;        // tokens it gets
+};
 struct Need {
+    int32_t at;          // its first page in the list of free ones
     int32_t pages;       // free pages it needs
     int32_t copy;        // tokens of a page it has to copy (0: none)
 };
 
-// RESIZE: sequence seqs[i] gets new_lens[i] tokens (null: none).  Otherwise a fork: children[i]
-// (b) becomes a copy of parents[i] (a).
+// RESIZE: sequence a[i] gets b[i] tokens (b null: none).  Otherwise a fork: b[i] becomes a copy of a[i].
 template <bool RESIZE>
 __global__ void __launch_bounds__(META_THREADS, 1)
-    update_kernel(const Meta m, const int32_t *a, const int32_t *b, int32_t n, int32_t *offset,
-                  int32_t *free_list, const Copies copies) {
+    update_kernel(const Meta m, const int32_t *a, const int32_t *b, int32_t n, Need *far_needs,
+                  int32_t *far_list, const Copies copies) {
     __shared__ int64_t s_warp[META_WARPS];
-    __shared__ int32_t s_cnt[SCAN_K * META_WARPS + META_WARPS];
+    __shared__ __align__(16) int32_t s_cnt[2][SCAN_K * META_WARPS];
+    __shared__ Item s_items[CACHED];
+    __shared__ Need s_needs[CACHED];
+    __shared__ int32_t s_list[CACHED];
     __shared__ int32_t s_copies;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     if (threadIdx.x == 0) s_copies = 0;
     griddep_launch_dependents();
     griddep_wait();
     const int32_t capacity = m.max_pages * m.page_size;
+    if (threadIdx.x * 32 < min(m.pages, SCAN)) fetch_line(m.refs + threadIdx.x * 32);
+
+    auto read_item = [&](int i) {
+        Item x = {-1, 0, 0, 0};
+        const int32_t p = a[i], q = RESIZE ? (b ? b[i] : 0) : b[i];
+        const bool ok = RESIZE ? good_seq(m, p) && q >= 0 && q <= capacity : good_seq(m, p) && good_seq(m, q);
+        if (!ok) {
+            report_index(m.err);
+            return x;
+        }
+        x.seq = RESIZE ? p : q;
+        x.from = RESIZE ? 0 : p;
+        x.now = held_tokens(m, x.seq);
+        x.want = RESIZE ? q : held_tokens(m, p);
+        return x;
+    };
+    for (int i = threadIdx.x; i < min(n, CACHED); i += META_THREADS) s_items[i] = read_item(i);
+    __syncthreads();
+    auto item = [&](int i) { return i < CACHED ? s_items[i] : read_item(i); };
 
     // ---- release: what is cut off, and what the children's slots held
     for (int i = warp; i < n; i += META_WARPS) {
-        const int32_t seq = RESIZE ? a[i] : b[i];
-        const int32_t len = RESIZE ? (b ? b[i] : 0) : 0;
-        const bool ok = good_seq(m, seq) && len >= 0 && len <= capacity && (RESIZE || good_seq(m, a[i]));
-        if (!ok) {
-            if (lane == 0) report_index(m.err);
-            continue;
-        }
-        const int32_t old = held_tokens(m, seq);
-        if (len < old) {
-            release(m, seq, kvi::pages_of(len, m.page_size), kvi::pages_of(old, m.page_size), lane);
+        const Item x = item(i);
+        if (x.seq < 0) continue;
+        const int32_t keep = RESIZE ? x.want : 0;
+        if (!RESIZE)         // the parent's entries are read below
+            for (int j = lane * 32; j < kvi::pages_of(x.want, m.page_size); j += 32 * 32)
+                fetch_line(m.table + x.from * m.table_stride + j);
+        if (keep < x.now) {
+            release(m, x.seq, kvi::pages_of(keep, m.page_size), kvi::pages_of(x.now, m.page_size), lane);
             __syncwarp();
-            if (lane == 0) m.lens[seq] = len;
+            if (lane == 0) m.lens[x.seq] = keep;
         }
     }
     __threadfence_block();
     __syncthreads();
 
-    // ---- what each item needs, and where its pages begin in the list of free ones
+    // ---- what each item needs, and where its pages begin in the list of free ones; fixed here, since
+    // serving one changes the counts
     auto need_of = [&](int i) {
-        Need need = {0, 0};
+        Need need = {0, 0, 0};
+        const Item x = item(i);
+        if (x.seq < 0) return need;
         if (RESIZE) {
-            const int32_t seq = a[i], len = b ? b[i] : 0;
-            if (!good_seq(m, seq) || len < 0 || len > capacity) return need;
-            const int32_t old = held_tokens(m, seq);
-            if (len <= old) return need;
-            need.pages = kvi::pages_of(len, m.page_size) - kvi::pages_of(old, m.page_size);
+            if (x.want <= x.now) return need;
+            need.pages = kvi::pages_of(x.want, m.page_size) - kvi::pages_of(x.now, m.page_size);
             // a last page that others hold too is not written into: it becomes a copy
-            const int32_t tail = old % m.page_size;
+            const int32_t tail = x.now % m.page_size;
             if (tail) {
-                const int32_t last = m.table[seq * m.table_stride + old / m.page_size];
+                const int32_t last = m.table[x.seq * m.table_stride + x.now / m.page_size];
                 if (good_page(m, last) && __ldcg(m.refs + last) > 1) {
                     need.copy = tail;
                     need.pages += 1;
                 }
             }
-        } else if (good_seq(m, a[i]) && good_seq(m, b[i])) {
-            need.copy = held_tokens(m, a[i]) % m.page_size;
+        } else {
+            need.copy = x.want % m.page_size;
             need.pages = need.copy > 0;
         }
         return need;
@@ -194,86 +237,78 @@ __global__ void __launch_bounds__(META_THREADS, 1)
     int64_t wanted = 0;
     for (int base = 0; base < n; base += META_THREADS) {
         const int i = base + (int)threadIdx.x;
-        Need need = {0, 0};
+        Need need = {0, 0, 0};
         if (i < n) need = need_of(i);
         int64_t total;
         const int64_t at = wanted + block_prefix<int64_t>(need.pages, s_warp, &total);
-        if (i < n) {
-            // the item's needs are fixed here: serving another changes the counts
-            offset[3 * i] = (int32_t)(at <= m.pages ? at : m.pages);
-            offset[3 * i + 1] = need.pages;
-            offset[3 * i + 2] = need.copy;
-        }
+        need.at = (int32_t)(at <= m.pages ? at : m.pages);
+        if (i < n) (i < CACHED ? s_needs[i] : far_needs[i]) = need;
         wanted += total;
     }
     const int32_t enough = (int32_t)(wanted < m.pages ? wanted : m.pages);
+    int32_t *list = enough <= CACHED ? s_list : far_list;
     const int32_t found =
-        enough > 0 ? list_pages(m, 0, m.pages, true, enough, free_list, m.pages, s_cnt) : 0;
+        enough > 0 ? list_pages(m, m.pages, enough, list, enough <= CACHED ? CACHED : m.pages, s_cnt) : 0;
     __threadfence_block();
     __syncthreads();
 
     // ---- serve the items
     for (int i = warp; i < n; i += META_WARPS) {
-        const int32_t at = offset[3 * i], pages = offset[3 * i + 1], copy = offset[3 * i + 2];
+        const Need need = i < CACHED ? s_needs[i] : far_needs[i];
+        Item x = item(i);
+        if (x.seq < 0) continue;
+        if (need.pages > 0 && (need.at > found || need.pages > found - need.at)) {
+            if (lane == 0) atomicOr(m.err, qgi::ERR_PAGES);
+            continue;
+        }
+        int32_t *row = m.table + x.seq * m.table_stride;
         int32_t src = -1, dst = -1;
-        const bool ok = RESIZE ? good_seq(m, a[i]) : good_seq(m, a[i]) && good_seq(m, b[i]);
-        const bool served = ok && (pages == 0 || (at <= found && pages <= found - at));
-        if (ok && !served && lane == 0) atomicOr(m.err, qgi::ERR_PAGES);
-        if (served) {
-            if (RESIZE) {
-                const int32_t seq = a[i], len = b ? b[i] : 0;
-                if (len >= 0 && len <= capacity) {
-                    const int32_t old = held_tokens(m, seq);
-                    int32_t *row = m.table + seq * m.table_stride;
-                    if (len > old) {
-                        const int32_t have = kvi::pages_of(old, m.page_size);
-                        const int first = copy > 0 ? 1 : 0;
-                        for (int j = lane; j < pages - first; j += 32) {
-                            const int32_t page = free_list[at + first + j];
-                            row[have + j] = page;
-                            m.refs[page] = 1;
-                        }
-                        if (first) {
-                            src = row[have - 1];
-                            dst = free_list[at];
-                            __syncwarp();
-                            if (lane == 0) {
-                                row[have - 1] = dst;
-                                m.refs[dst] = 1;
-                                atomicSub(m.refs + src, 1);
-                            }
-                        }
-                        __syncwarp();
-                        if (lane == 0) m.lens[seq] = len;
-                    }
+        if (RESIZE) {
+            if (x.want <= x.now) continue;
+            const int32_t have = kvi::pages_of(x.now, m.page_size);
+            const int first = need.copy > 0 ? 1 : 0;
+            for (int j = lane; j < need.pages - first; j += 32) {
+                const int32_t page = list[need.at + first + j];
+                row[have + j] = page;
+                m.refs[page] = 1;
+            }
+            if (first) {
+                src = row[have - 1];
+                dst = list[need.at];
+                __syncwarp();
+                if (lane == 0) {
+                    row[have - 1] = dst;
+                    m.refs[dst] = 1;
+                    atomicSub(m.refs + src, 1);
                 }
-            } else {
-                const int32_t parent = a[i], child = b[i], len = held_tokens(m, parent);
-                const int32_t *from = m.table + parent * m.table_stride;
-                int32_t *row = m.table + child * m.table_stride;
-                const int32_t full = len / m.page_size;
-                for (int j = lane; j < full; j += 32) {
-                    const int32_t page = from[j];
-                    row[j] = page;
-                    if (good_page(m, page)) atomicAdd(m.refs + page, 1);
-                    else report_index(m.err);
+            }
+            __syncwarp();
+        } else {
+            const int32_t *from = m.table + x.from * m.table_stride;
+            const int32_t full = x.want / m.page_size;
+            if (need.copy > 0) src = from[full];
+            for (int j = lane; j < full; j += 32) {
+                const int32_t page = from[j];
+                row[j] = page;
+                if (good_page(m, page)) atomicAdd(m.refs + page, 1);
+                else report_index(m.err);
+            }
+            if (need.copy > 0) {
+                dst = list[need.at];
+                if (lane == 0) {
+                    row[full] = dst;
+                    m.refs[dst] = 1;
                 }
-                if (copy > 0 && pages > 0) {
-                    src = from[full];
-                    dst = free_list[at];
-                    if (lane == 0) {
-                        row[full] = dst;
-                        m.refs[dst] = 1;
-                    }
-                }
-                if (lane == 0) m.lens[child] = len;
             }
         }
-        if (dst >= 0 && lane == 0) {            // the copies' order does not matter
-            const int32_t x = atomicAdd(&s_copies, 1);
-            copies.src[x] = src;
-            copies.dst[x] = dst;
-            copies.tokens[x] = copy;
+        if (lane == 0) {
+            m.lens[x.seq] = x.want;
+            if (dst >= 0) {                      // the copies' order does not matter
+                const int32_t c = atomicAdd(&s_copies, 1);
+                copies.src[c] = src;
+                copies.dst[c] = dst;
+                copies.tokens[c] = need.copy;
+            }
         }
     }
     __syncthreads();
@@ -281,11 +316,13 @@ __global__ void __launch_bounds__(META_THREADS, 1)
 }
 
 // Compaction: with U pages in use, those at U and above go to the free ones below U, both in order.
-// map[page] is the new place of a page at U or above; *used receives U.
+// map[page] is the new place of a page at U or above; *used receives U.  `list` holds the free ones
+// below U, then the pages in use from U on: as many of the one as of the other.
 __global__ void __launch_bounds__(META_THREADS, 1)
-    compact_kernel(const Meta m, int32_t *map, int32_t *used, const Copies copies) {
+    compact_kernel(const Meta m, int32_t *map, int32_t *used, int32_t *far_list, const Copies copies) {
     __shared__ int32_t s_warp[META_WARPS];
-    __shared__ int32_t s_cnt[SCAN_K * META_WARPS + META_WARPS];
+    __shared__ __align__(16) int32_t s_cnt[2][SCAN_K * META_WARPS];
+    __shared__ int32_t s_list[2 * CACHED];
     griddep_launch_dependents();
     griddep_wait();
     int32_t mine = 0, U;
@@ -294,13 +331,15 @@ __global__ void __launch_bounds__(META_THREADS, 1)
     block_prefix(mine, s_warp, &U);
     // an entry that names a page nobody counts stays as it is
     for (int i = U + (int)threadIdx.x; i < m.pages; i += META_THREADS) map[i] = i;
-    const int32_t holes = list_pages(m, 0, U, true, m.pages, copies.dst, m.pages, s_cnt);
-    const int32_t movers = list_pages(m, U, m.pages, false, m.pages, copies.src, m.pages, s_cnt);
-    const int32_t n = min(holes, movers);        // equal: U counts the pages in use
+    const bool small = m.pages <= 2 * CACHED;
+    int32_t *list = small ? s_list : far_list;
+    const int32_t n = list_pages(m, U, m.pages + 1, list, m.pages, s_cnt) / 2;
     __threadfence_block();
     __syncthreads();
     for (int j = threadIdx.x; j < n; j += META_THREADS) {
-        const int32_t from = copies.src[j], to = copies.dst[j];
+        const int32_t to = list[j], from = list[n + j];
+        copies.src[j] = from;
+        copies.dst[j] = to;
         map[from] = to;
         m.refs[to] = __ldcg(m.refs + from);
         m.refs[from] = 0;
@@ -320,24 +359,26 @@ struct Plane {
     bool scaled;
 };
 
-// Copies one (page, layer, plane, head) a warp; REMAP: also replaces the moved pages in the table.
+// Copies 2 KB of a (page, layer, plane, head) a warp; REMAP: also replaces the moved pages in the table, 32
+// entries a warp, the last warps first (they have the fewest copies).
 constexpr int COPY_THREADS = 512;
-constexpr int REMAP_TILE = COPY_THREADS;
+constexpr int PIECES = 128;                     // 16-byte pieces of a job, four a lane
 
 template <bool REMAP>
-__global__ void __launch_bounds__(COPY_THREADS)
+__global__ void __launch_bounds__(COPY_THREADS, 2)
     copy_kernel(const __grid_constant__ Plane pl, const Copies c, const Meta m, const int32_t *map,
                 const int32_t *used, unsigned *err) {
     const int lane = threadIdx.x % 32;
     griddep_launch_dependents();
     griddep_wait();
+    const int64_t warps = (int64_t)gridDim.x * (COPY_THREADS / 32);
+    const int64_t warp = (int64_t)blockIdx.x * (COPY_THREADS / 32) + threadIdx.x / 32;
     if (REMAP) {
-        const int32_t U = *used;
-        const int per_row = (m.max_pages + REMAP_TILE - 1) / REMAP_TILE;
-        for (int64_t x = blockIdx.x; x < (int64_t)m.max_seqs * per_row; x += gridDim.x) {
+        const int per_row = (m.max_pages + 31) / 32;
+        for (int64_t x = warps - 1 - warp; x < (int64_t)m.max_seqs * per_row; x += warps) {
             const int32_t seq = (int32_t)(x / per_row);
-            const int32_t j = (int32_t)(x % per_row) * REMAP_TILE + (int)threadIdx.x;
-            const int32_t len = m.lens[seq];
+            const int32_t j = (int32_t)(x % per_row) * 32 + lane;
+            const int32_t len = m.lens[seq], U = *used;
             if (len <= 0 || j >= m.max_pages || j >= kvi::pages_of(len, m.page_size)) continue;
             int32_t *e = m.table + seq * m.table_stride + j;
             const int32_t page = *e;
@@ -346,66 +387,61 @@ __global__ void __launch_bounds__(COPY_THREADS)
         }
     }
     const int32_t n = c.count ? *c.count : c.n;
-    const int64_t jobs = (int64_t)n * pl.layers * 2 * pl.heads;
-    const int64_t warps = (int64_t)gridDim.x * (COPY_THREADS / 32);
+    // 2 KB of a (page, layer, plane, head) a job: its 8, 16 or 32 rows from `t0` on.  (256 pages of 8 layers,
+    // 554 MB read and written: 92 us at 2 KB, 6.0 TB/s, 98 at 4 KB, whose loads take the registers of a second block.)
     const int cpr = pl.rowb / 16;                // 16-byte pieces of a row
-    for (int64_t job = (int64_t)blockIdx.x * (COPY_THREADS / 32) + threadIdx.x / 32; job < jobs;
-         job += warps) {
-        const int32_t head = (int32_t)(job % pl.heads);
-        int64_t rest = job / pl.heads;
-        const int plane = (int)(rest & 1);
-        rest >>= 1;
-        const int32_t layer = (int32_t)(rest % pl.layers), item = (int32_t)(rest / pl.layers);
+    const int rows = PIECES / cpr, slices = (pl.page_size + rows - 1) / rows;
+    const uint32_t strip = 2u * pl.heads * slices, page_jobs = strip * pl.layers;     // below 2^32
+    const int64_t jobs = (int64_t)n * page_jobs;
+    for (int64_t job = warp; job < jobs; job += warps) {
+        const int32_t item = jobs <= 0xFFFFFFFFll ? (int32_t)((uint32_t)job / page_jobs) : (int32_t)(job / page_jobs);
+        uint32_t rest = (uint32_t)(job - (int64_t)item * page_jobs);
+        const uint32_t layer = rest / strip;
+        rest -= layer * strip;
+        const uint32_t hp = rest / slices, head = hp >> 1;
+        const int plane = (int)(hp & 1);
+        const int32_t t0 = (int32_t)(rest - hp * slices) * rows;
         const int32_t src = c.src[item], dst = c.dst[item];
-        const int32_t tokens = c.tokens ? c.tokens[item] : pl.page_size;
+        const int32_t tokens = min((c.tokens ? c.tokens[item] : pl.page_size) - t0, rows);
         if (tokens <= 0) continue;
         if (src < 0 || src >= pl.pages || dst < 0 || dst >= pl.pages) {
             if (lane == 0) report_index(err);
             continue;
         }
         if (src == dst) continue;
-        const int64_t at = layer * pl.layer + head * pl.head;
+        const int64_t at = layer * pl.layer + head * pl.head + t0 * pl.token;
         const uint8_t *from = pl.base[plane] + at + src * pl.page;
         uint8_t *to = pl.base[plane] + at + dst * pl.page;
         [[maybe_unused]] const int64_t last = at + (tokens - 1) * pl.token + pl.rowb;
         if (!QG_IN_BOUNDS(err, at >= 0 && last + src * pl.page <= pl.extent &&
                                    last + dst * pl.page <= pl.extent))
             continue;
-        const bool dense = pl.token == pl.rowb;
+        // the row and the place in it of this lane's first piece; the next ones are 32 pieces on
+        const int row0 = lane / cpr, step = 32 / cpr;
+        const int64_t first = row0 * pl.token + lane % cpr * 16;
         const int pieces = tokens * cpr;
-        constexpr int K = 8;
-        for (int base = lane; base < pieces; base += 32 * K) {
-            uint4 v[K];
+        uint4 v[PIECES / 32];
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const int x = base + 32 * k;
-                if (x < pieces) {
-                    const int64_t o = dense ? (int64_t)x * 16 : x / cpr * pl.token + x % cpr * 16;
-                    v[k] = __ldcs(reinterpret_cast<const uint4 *>(from + o));
-                }
-            }
+        for (int k = 0; k < PIECES / 32; ++k)
+            if (lane + 32 * k < pieces)
+                v[k] = __ldcs(reinterpret_cast<const uint4 *>(from + first + k * step * pl.token));
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const int x = base + 32 * k;
-                if (x < pieces) {
-                    const int64_t o = dense ? (int64_t)x * 16 : x / cpr * pl.token + x % cpr * 16;
-                    *reinterpret_cast<uint4 *>(to + o) = v[k];
-                }
-            }
-        }
+        for (int k = 0; k < PIECES / 32; ++k)
+            if (lane + 32 * k < pieces) *reinterpret_cast<uint4 *>(to + first + k * step * pl.token) = v[k];
         if (pl.scaled) {
-            const int64_t sat = layer * pl.slayer + head * pl.shead;
+            const int64_t sat = layer * pl.slayer + head * pl.shead + t0 * pl.stoken;
             const uint8_t *sf = pl.base[2 + plane] + sat + src * pl.spage;
             uint8_t *st = pl.base[2 + plane] + sat + dst * pl.spage;
-            for (int t = lane; t < tokens; t += 32)
-                for (int w = 0; w < pl.rowb; w += 128)       // 4 scale bytes every 128 elements
-                    *reinterpret_cast<uint32_t *>(st + t * pl.stoken + w / 32) =
-                        *reinterpret_cast<const uint32_t *>(sf + t * pl.stoken + w / 32);
+            for (int t = lane; t < tokens; t += 32)      // a row's 4 bytes of scales (d <= 128)
+                *reinterpret_cast<uint32_t *>(st + t * pl.stoken) =
+                    *reinterpret_cast<const uint32_t *>(sf + t * pl.stoken);
         }
     }
 }
 
-Plane plane_of(const qgemm_kv_cache *c) {
+// whole: the copies are of whole pages, so heads that follow one another are taken as one of all
+// their rows.
+Plane plane_of(const qgemm_kv_cache *c, bool whole) {
     Plane p = {};
     p.base[0] = c->k;
     p.base[1] = c->v;
@@ -427,6 +463,11 @@ Plane plane_of(const qgemm_kv_cache *c) {
     p.rowb = (int32_t)(c->d * (p.scaled ? 1 : 2));
     p.page_size = (int32_t)c->page_size;
     p.pages = (int32_t)c->pages;
+    if (whole && c->heads > 1 && p.head == c->page_size * p.token &&
+        (!p.scaled || p.shead == c->page_size * p.stoken)) {
+        p.page_size *= p.heads;
+        p.heads = 1;
+    }
     return p;
 }
 
@@ -448,12 +489,14 @@ Meta meta_of(const qgi::PageArgs &a, const qgi::LaunchCtx &ctx) {
 template <bool REMAP>
 cudaError_t launch_copy(const qgemm_kv_cache *kv, const Copies &c, const Meta &m, const int32_t *map,
                         const int32_t *used, int64_t items, const qgi::LaunchCtx &ctx) {
-    const int64_t jobs = items * kv->layers * 2 * kv->heads;
+    const Plane p = plane_of(kv, c.tokens == nullptr);
+    const int64_t rows = PIECES / (p.rowb / 16);
+    const int64_t jobs = items * p.layers * 2 * p.heads * ((p.page_size + rows - 1) / rows);
     int64_t blocks = (jobs + COPY_THREADS / 32 - 1) / (COPY_THREADS / 32);
     if (blocks > 2 * (int64_t)ctx.num_sms) blocks = 2 * (int64_t)ctx.num_sms;
     if (blocks < 1) blocks = 1;
-    return launch_dependent(copy_kernel<REMAP>, dim3((unsigned)blocks), COPY_THREADS, 0, ctx.stream, plane_of(kv), c, m,
-                            map, used, ctx.err);
+    return launch_dependent(copy_kernel<REMAP>, dim3((unsigned)blocks), COPY_THREADS, 0, ctx.stream, p, c, m, map, used,
+                            ctx.err);
 }
 
 template <bool RESIZE>
@@ -464,12 +507,13 @@ cudaError_t launch_update(const qgi::PageArgs &a, const int32_t *x, const int32_
     cudaError_t e = qgi::scratch_alloc(sizeof(int32_t) * (6 * (size_t)n + 1 + (size_t)m.pages), ctx, &scratch);
     if (e != cudaSuccess) return e;
     int32_t *w = static_cast<int32_t *>(scratch);
-    Copies c = {};
+    Copies c = {};               // after the needs (three words each) of the items
     c.src = w + 3 * (size_t)n;
     c.dst = w + 4 * (size_t)n;
     c.tokens = w + 5 * (size_t)n;
     c.count = w + 6 * (size_t)n;
-    e = launch_dependent(update_kernel<RESIZE>, dim3(1), META_THREADS, 0, ctx.stream, m, x, y, n, w, c.count + 1, c);
+    e = launch_dependent(update_kernel<RESIZE>, dim3(1), META_THREADS, 0, ctx.stream, m, x, y, n,
+                         reinterpret_cast<Need *>(w), c.count + 1, c);
     if (e == cudaSuccess) e = launch_copy<false>(a.kv, c, m, nullptr, nullptr, n, ctx);
     const cudaError_t f = qgi::scratch_free(scratch, ctx);
     return e != cudaSuccess ? e : f;
@@ -493,7 +537,7 @@ cudaError_t launch_kv_fork(const PageArgs &a, const int32_t *parents, const int3
 cudaError_t launch_kv_compact(const PageArgs &a, const LaunchCtx &ctx) {
     const qg::Meta m = qg::meta_of(a, ctx);
     void *scratch = nullptr;
-    cudaError_t e = scratch_alloc(sizeof(int32_t) * (3 * (size_t)m.pages + 2), ctx, &scratch);
+    cudaError_t e = scratch_alloc(sizeof(int32_t) * (4 * (size_t)m.pages + 2), ctx, &scratch);
     if (e != cudaSuccess) return e;
     int32_t *w = static_cast<int32_t *>(scratch);
     int32_t *map = w + 2, *used = w;
@@ -501,7 +545,8 @@ cudaError_t launch_kv_compact(const PageArgs &a, const LaunchCtx &ctx) {
     c.src = map + m.pages;
     c.dst = c.src + m.pages;
     c.count = w + 1;
-    e = qg::launch_dependent(qg::compact_kernel, dim3(1), qg::META_THREADS, 0, ctx.stream, m, map, used, c);
+    e = qg::launch_dependent(qg::compact_kernel, dim3(1), qg::META_THREADS, 0, ctx.stream, m, map, used,
+                             c.dst + m.pages, c);
     if (e == cudaSuccess) e = qg::launch_copy<true>(a.kv, c, m, map, used, m.pages, ctx);
     const cudaError_t f = scratch_free(scratch, ctx);
     return e != cudaSuccess ? e : f;

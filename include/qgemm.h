@@ -439,7 +439,8 @@ typedef struct qgemm_kv_cache qgemm_kv_cache;
  *   k_scales,      E4M3 only: UE8M0 planes, d / 32 bytes a row at the same indices under
  *   v_scales       scale_strides, in rows of 4 bytes (d = 64 uses the first two): 4-byte aligned bases,
  *                  strides in multiples of 4.  NULL otherwise.
- * Requirements: d is 64 or 128; layers, heads, page_size in 1 .. 65536, pages in 1 .. 2^30.
+ * Requirements: d is 64 or 128; layers, heads, page_size in 1 .. 65536, layers * heads * page_size below
+ * 2^31, pages in 1 .. 2^30.
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, UNSUPPORTED_DTYPE, MISALIGNED. */
 qgemm_status qgemm_create_kv_cache(qgemm_kv_cache **out, int32_t dtype, int64_t layers, int64_t pages,
                                    int64_t heads, int64_t page_size, int64_t d, void *k, void *v,

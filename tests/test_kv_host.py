@@ -50,6 +50,7 @@ def _cache(lib, dtype=q.F16, layers=2, pages=8, heads=4, page=16, d=128, k=A, v=
     (dict(st=(131072, 16384, 256, 1024)), 0),                    # tokens outside heads
     (dict(st=(32768, 32768, 4096, 256)), INVALID),               # pages and layers coincide
     (dict(st=(16384, 32768, 4096, 256)), 0),                     # layers inside pages
+    (dict(layers=4096, heads=1024, page=512, pages=1, st=(1 << 27, 1 << 40, 1 << 17, 256)), SHAPE),   # 2^31 rows a page
     (dict(ks=A, vs=B_), DTYPE), (dict(dtype=q.E4M3, sst=(512, 64, 16, 2), ks=A, vs=B_), MISALIGNED),
     (dict(dtype=q.E4M3, sst=(2048, 256, 64, 4), ks=A + 2, vs=B_), MISALIGNED),
     (dict(dtype=q.E4M3, sst=(2048, 256, 32, 4), ks=A, vs=B_), INVALID),
