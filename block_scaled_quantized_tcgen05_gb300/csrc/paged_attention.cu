@@ -93,15 +93,16 @@ struct Cfg {
     static constexpr int STAGEB = 2 * (PLANE + SCALEB);
     // Two CTAs an SM where their registers (8 heads) and three stages each fit; otherwise one
     static constexpr bool TWO = NH == 1 && STAGEB <= 4224;
-    static constexpr int MERGE_ROWS = TWO ? 2 : 8;       // heads merged at a time
-    static constexpr int MERGEB = NWARPS * MERGE_ROWS * D * 4;
-    static constexpr int ROOM = (TWO ? 111 : 224) * 1024;
-    static constexpr int FIT = (ROOM - MERGEB) / (NWARPS * STAGEB);
+    // heads merged at a time, through the slot of the ring each warp has just read
+    static constexpr int MERGE_ROWS = NH == 2 && STAGEB >= 16 * D * 4 ? 16 : 8;
+    static_assert(STAGEB >= MERGE_ROWS * D * 4, "a warp's rows fit a slot");
+    static constexpr int ROOM = (TWO ? 110 : 224) * 1024;
+    static constexpr int FIT = ROOM / (NWARPS * STAGEB);
     static constexpr int NSTAGES = FIT > 6 ? 6 : FIT;
-    static constexpr int SMEM = NWARPS * NSTAGES * STAGEB + MERGEB;
-    // What a unit costs beyond its tiles, in tiles (measured, 128 ragged E4M3 sequences: 0 / 1 / 2 / 3 /
-    // 4 extra 226 / 187 / 166 / 164 / 167 us; 64 ragged fp16 ones 134 / 124 / 124 / 124)
-    static constexpr int EXTRA = E4M3 ? 3 : 1;
+    static constexpr int SMEM = 256 + NWARPS * NSTAGES * STAGEB;
+    // What a unit costs beyond its tiles, in tiles (measured, 128 ragged E4M3 sequences: 1 / 2 / 3 extra
+    // 138 / 135 / 138 us; 64 ragged fp16 ones 0 / 1 / 2: 134 / 118 / 118)
+    static constexpr int EXTRA = ROWB <= 128 ? 2 : 1;
     static constexpr int MT = D / 16;                    // 16-element tiles of the output
     static constexpr int PARTIAL = ROWS * (D + 2);       // floats of a partial
 };
@@ -465,8 +466,10 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
         load.rel = (int32_t)max((int64_t)0, -into);
     }
     if (load.rel >= span) return;        // no tile in the range
-    const uint32_t ring = smem_u32(smem) + warp * (C::NSTAGES * C::STAGEB);
-    float *merge = reinterpret_cast<float *>(smem + NWARPS * C::NSTAGES * C::STAGEB);
+    // A row's pieces are found by exclusive or from a lane's first address, which takes bases that are
+    // multiples of a row (128 bytes for 8-bit rows, whose stages are a multiple of that)
+    uint8_t *const base256 = smem + (256 - smem_u32(smem) % 256) % 256;
+    const uint32_t ring = smem_u32(base256) + warp * (C::NSTAGES * C::STAGEB);
 
     // ---- page look-up of this warp's tokens of the tile `load` points at, one step ahead of the
     // copies that use it.  Steps begin at multiples of 16 tokens: with pages of a multiple of 16 tokens
@@ -505,26 +508,27 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
     constexpr int RPI = 32 / C::CHUNKS;          // rows an instruction of the warp copies
     const int chunk = lane % C::CHUNKS, row0 = lane / C::CHUNKS;
     const int64_t lane_off = row0 * p.token + chunk * 16;
+    const uint32_t lane_to = row0 * C::ROWB + swizzle<C>(row0, chunk) * 16;
     const int64_t lane_soff = C::E4M3 ? lane % STEP * p.stoken : 0;
     auto issue = [&](int slot) {
         const int32_t pg = x.pg, pr = x.pr, ph = x.h;
         if (p.one_page && x.hi - x.lo == STEP && pg >= 0 && pg < p.pages) {
             // a whole step of one page: rows a token stride apart
-            const uint32_t kd = ring + slot * C::STAGEB, vd = kd + C::PLANE;
+            const uint32_t kd = ring + slot * C::STAGEB;
             const int64_t base = pg * p.page + pr * p.token + ph * p.head;
             if (QG_IN_BOUNDS(p.err, base >= 0 && base + (STEP - 1) * p.token + C::ROWB <= p.extent)) {
                 const uint8_t *k = p.k + base + lane_off, *v = p.v + base + lane_off;
 #pragma unroll
                 for (int i = 0; i < STEP / RPI; ++i) {
-                    const int r = i * RPI + row0;
-                    const uint32_t d = r * C::ROWB + swizzle<C>(r, chunk) * 16;
-                    cp_async_16(kd + d, k, 16);
-                    cp_async_16(vd + d, v, 16);
+                    // swizzle(a + b, c) = swizzle(a, 0) ^ swizzle(b, c) for rows a and b without common bits
+                    const uint32_t d = (kd + lane_to) ^ (swizzle<C>(i * RPI, 0) * 16);
+                    cp_async_16(d + i * RPI * C::ROWB, k, 16);
+                    cp_async_16(d + i * RPI * C::ROWB + C::PLANE, v, 16);
                     k += RPI * p.token;
                     v += RPI * p.token;
                 }
                 if (C::E4M3)     // lanes 0-15: the keys' scale rows, lanes 16-31: the values'
-                    cp_async_4(vd + C::PLANE + lane * 4,
+                    cp_async_4(kd + 2 * C::PLANE + lane * 4,
                                (lane < STEP ? p.ks : p.vs) + pg * p.spage + pr * p.stoken + ph * p.shead + lane_soff, 4);
                 if (lane == 0) s_mask[warp][slot] = (1u << STEP) - 1;
                 return;
@@ -597,6 +601,14 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
         }
     };
 
+    // Places of this lane's fragments in a step's keys and values: the first piece; the others follow by
+    // exclusive or (16-bit rows: the addresses of ldmatrix).
+    const int k_row = C::E4M3 ? g : lane % 16, v_row = C::E4M3 ? 2 * c4 : lane % 8 + lane / 16 * 8;
+    const uint32_t k_at = k_row * C::ROWB + swizzle<C>(k_row, C::E4M3 ? c4 / 2 : lane / 16) * 16 + (C::E4M3 ? c4 % 2 * 8 : 0);
+    const uint32_t v_at =
+        v_row * C::ROWB + (!C::E4M3 ? swizzle<C>(v_row, lane / 8 % 2) * 16
+                                    : C::D == 128 ? swizzle<C>(v_row, g) * 16 : swizzle<C>(v_row, g / 2) * 16 + g % 2 * 8);
+
     // ---- one step: scores of 16 tokens, the running softmax, the weighted values
     auto step = [&](int slot, auto fast_tag) {
         [[maybe_unused]] constexpr bool FAST = decltype(fast_tag)::value;
@@ -613,8 +625,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
 #pragma unroll
             for (int kk = 0; kk < C::D / 16; ++kk) {
                 uint32_t a[4];       // tokens 0-7 and 8-15 of piece 2 kk, then of 2 kk + 1
-                const int r = lane % 16, ch = 2 * kk + lane / 16;
-                ldsm4<false>(kd + r * C::ROWB + swizzle<C>(r, ch) * 16, a);
+                ldsm4<false>((kd + k_at) ^ (32 * kk), a);
 #pragma unroll
                 for (int n = 0; n < C::NH; ++n)
                     mma16816(TY::BF16, kk % 2 ? s2[n] : s[n], a[0], a[1], a[2], a[3], qb[n][kk][0], qb[n][kk][1]);
@@ -630,9 +641,8 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
             const uint32_t bx = lds32(ksd + g * 4), by = lds32(ksd + (g + 8) * 4);
 #pragma unroll
             for (int blk = 0; blk < C::D / 32; ++blk) {
-                const int ch = 2 * blk + c4 / 2, in = c4 % 2 * 8;
-                const uint2 x = lds64(kd + g * C::ROWB + swizzle<C>(g, ch) * 16 + in);
-                const uint2 y = lds64(kd + (g + 8) * C::ROWB + swizzle<C>(g + 8, ch) * 16 + in);
+                const uint32_t at = (kd + k_at) ^ (32 * blk);
+                const uint2 x = lds64(at), y = lds64(at + 8 * C::ROWB);       // rows g and g + 8
                 const float sx = scale_f32<FAST>((bx >> (8 * blk)) & 255u);
                 const float sy = scale_f32<FAST>((by >> (8 * blk)) & 255u);
                 uint32_t a[8];
@@ -716,8 +726,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
 #pragma unroll
             for (int j = 0; j < C::MT; ++j) {
                 uint32_t a[4];       // tokens 0-7: elements 16 j .. + 7, + 8 .. + 15; tokens 8-15 likewise
-                const int r = lane % 8 + lane / 16 * 8, ch = 2 * j + (lane / 8) % 2;
-                ldsm4<true>(vd + r * C::ROWB + swizzle<C>(r, ch) * 16, a);
+                ldsm4<true>((vd + v_at) ^ (32 * j), a);
                 weigh(j, a[0], a[1], a[2], a[3]);
             }
         } else {
@@ -731,10 +740,12 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
                 const int r = 2 * c4 + (i & 1) + 8 * (i >> 1);
                 byte[i] = lds8(vsd + r * 4 + (C::D / 8 * g) / 32);
                 if constexpr (C::D == 128) {
-                    const uint4 x = lds128(vd + r * C::ROWB + swizzle<C>(r, g) * 16);
+                    const uint4 x = lds128(((vd + v_at) ^ (i & 1 ? swizzle<C>(1, 0) * 16 : 0)) +
+                                           ((i & 1) + 8 * (i >> 1)) * C::ROWB);
                     w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
                 } else {
-                    const uint2 x = lds64(vd + r * C::ROWB + swizzle<C>(r, g / 2) * 16 + (g & 1) * 8);
+                    const uint2 x = lds64(((vd + v_at) ^ (i & 1 ? swizzle<C>(1, 0) * 16 : 0)) +
+                                          ((i & 1) + 8 * (i >> 1)) * C::ROWB);
                     w[i][0] = x.x, w[i][1] = x.y;
                 }
             }
@@ -760,19 +771,24 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
         }
     };
 
-    // Place in the merge buffer of 16-byte piece u of a row: the four pairs of heads, whose lanes write
-    // together, go to different banks.
+    // Place of 16-byte piece u in a merged row: the four pairs of heads, whose lanes write together, go
+    // to different banks.
     auto place = [&](int u, int row) {
         const int pair = (row >> 1) & 3;
         if (!C::E4M3) return u ^ (2 * pair);
         return u ^ (C::D == 128 ? pair : (pair & 1) | ((pair & 2) << 1));
     };
 
-    // ---- end of the tiles this CTA has of a unit: the warps' rows are merged; a whole unit is
-    // written out, a part goes to the workspace
-    auto end_unit = [&](const Step &u) {
+    // ---- end of the tiles this CTA has of a unit: the warps' rows are merged, through the ring's slots
+    // that were just read (with a buffer of its own, 2 heads at a time beside two CTAs' rings: 152 us for
+    // the 128 ragged E4M3 sequences, 135 so); a whole unit is written out, a part goes to the workspace
+    auto end_unit = [&](const Step &u, int slot) {
         const int32_t tiles = (int32_t)(u.tiles & ~(LAST | END));
         const bool opens = u.t0 >= 0, whole = opens && u.t0 + tiles <= span;
+        // the slot `slot` of each warp's ring, read by the step before and not filled again yet
+        auto rows_of = [&](int w) {
+            return reinterpret_cast<float *>(base256 + (w * C::NSTAGES + slot) * C::STAGEB);
+        };
         // a part lies in the slot of its CTA's range: the second when it opens the unit
         float *part = p.partial + (2 * (int64_t)blockIdx.x + (opens ? 1 : 0)) * C::PARTIAL;
 #pragma unroll
@@ -789,11 +805,11 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
             }
 #pragma unroll
         for (int blk = 0; blk < 8 * C::NH / C::MERGE_ROWS; ++blk) {
-            const int row0 = blk * C::MERGE_ROWS, n = row0 / 8;
-            const int mine_r = 2 * c4 - row0 % 8;         // this lane's first head in the block
             if (blk) __syncthreads();                     // the block before has been read
-            if (mine_r >= 0 && mine_r < C::MERGE_ROWS) {
-                float *dst = merge + (warp * C::MERGE_ROWS + mine_r) * C::D;
+#pragma unroll
+            for (int n8 = 0; n8 < C::MERGE_ROWS / 8; ++n8) {
+                const int n = blk * (C::MERGE_ROWS / 8) + n8;
+                float *dst = rows_of(warp) + (8 * n8 + 2 * c4) * C::D;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     if constexpr (C::E4M3) {         // D / 8 consecutive elements a lane
@@ -815,7 +831,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
             __syncthreads();
             // 4 elements a thread
             for (int x = tid; x < C::MERGE_ROWS * C::D / 4; x += THREADS) {
-                const int r = x / (C::D / 4), row = row0 + r, col = x % (C::D / 4) * 4;
+                const int r = x / (C::D / 4), row = blk * C::MERGE_ROWS + r, col = x % (C::D / 4) * 4;
                 float M = -INFINITY;
 #pragma unroll
                 for (int w = 0; w < NWARPS; ++w) M = fmaxf(M, s_m[w][row]);
@@ -826,7 +842,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
                     const float mw = s_m[w][row];
                     const float f = mw == -INFINITY ? 0.0f : ex2(mw - M);
                     const float4 a = *reinterpret_cast<const float4 *>(
-                        merge + (w * C::MERGE_ROWS + r) * C::D + 4 * place(col / 4, row));
+                        rows_of(w) + r * C::D + 4 * place(col / 4, row));
                     o.x += f * a.x, o.y += f * a.y, o.z += f * a.z, o.w += f * a.w;
                     L += f * s_l[w][row];
                 }
@@ -846,7 +862,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
             const int64_t last = kvi::range_owner(s_range[0], s_range[1], s_range[2] + u.t0 + tiles - 1);
             merge_parts<C>(p, u, first, (int)(last - first + 1), (int)(blockIdx.x - first), &s_last);
         }
-        __syncthreads();                        // the merge buffer and s_m are free again
+        __syncthreads();                        // the slots and s_m are free again
     };
 
     // ---- the loop
@@ -883,15 +899,15 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
             else step(slot, std::true_type{});
         }
         __syncwarp();                           // every lane has read the slot
-        slot = slot + 1 == C::NSTAGES ? 0 : slot + 1;
         if (s_step[warp][k % STEPS].tiles & LAST) {
             const Step done = s_step[warp][k % STEPS];
             const bool more = !(done.tiles & END);
             if (more) load_queries(s_step[warp][(k + 1) % STEPS]);   // in flight while the warps merge
-            end_unit(done);
+            end_unit(done, slot);
             if (!more) break;
             clear();
         }
+        slot = slot + 1 == C::NSTAGES ? 0 : slot + 1;
     }
     cp_wait<0>();
 }
