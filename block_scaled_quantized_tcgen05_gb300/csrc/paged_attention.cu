@@ -92,6 +92,7 @@ struct Cfg {
     static constexpr int SCALEB = E4M3 ? STEP * 4 : 0;   // scale bytes of a step's keys
     static constexpr int STAGEB = 2 * (PLANE + SCALEB);
     // Two CTAs an SM where their registers (8 heads) and three stages each fit; otherwise one
+    // (128 ragged E4M3 sequences: 135 us, with one 165)
     static constexpr bool TWO = NH == 1 && STAGEB <= 4224;
     // heads merged at a time, through the slot of the ring each warp has just read
     static constexpr int MERGE_ROWS = NH == 2 && STAGEB >= 16 * D * 4 ? 16 : 8;
@@ -473,7 +474,8 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
 
     // ---- page look-up of this warp's tokens of the tile `load` points at, one step ahead of the
     // copies that use it.  Steps begin at multiples of 16 tokens: with pages of a multiple of 16 tokens
-    // a step lies in one page, and every lane holds its entry; otherwise lane l holds token l's.
+    // a step lies in one page, and every lane holds its entry; otherwise lane l holds token l's (147 us
+    // instead of 135 for the ragged E4M3 sequences, 119 instead of 118 for the fp16 ones).
     struct {
         int32_t pg = -1, pr = 0;         // page-table entry and row inside the page
         int32_t lo = 0, hi = 0;          // rows of the step that are tokens of the range
@@ -889,7 +891,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
             bool far = false;
             if (C::E4M3) {
                 // FAST scales: bytes 112 .. 127 (2^-15 .. 1: blocks of the append up to 512), halves all.
-                // Others take the step through fp32.
+                // Others take the step through fp32 (all steps so: 175 us instead of 135).
                 constexpr uint32_t HIGH = C::D == 128 ? 0xF0F0F0F0u : 0xF0F0u;
                 const uint32_t w = lds32(ring + slot * C::STAGEB + 2 * C::PLANE + lane * 4);
                 far = ((mask >> (lane % STEP)) & 1) && (w & HIGH) != (HIGH & 0x70707070u);
