@@ -388,7 +388,11 @@ qgemm_status qgemm_w8_gemv_ex(const void *X_f16, int64_t ldx, int64_t M, const q
  * skipped (nothing is read or written through it; attention treats the token as absent).
  *
  * Activations are QGEMM_F16 or QGEMM_BF16, a cache has their type or is QGEMM_E4M3 with one UE8M0
- * scale per 32 elements of a row.  Strides of activations are in ELEMENTS, of cache planes in BYTES. */
+ * scale per 32 elements of a row.  Strides of activations are in ELEMENTS, of cache planes in BYTES.
+ *
+ * The kernels are launched as programmatic dependents: their blocks may be resident before the work
+ * ahead of them on the stream has ended, and touch memory only after it has.  Every call can be captured
+ * into a graph; lengths, tables and counts are read when it runs. */
 
 /* Frequencies of the rotary positions: pair i of rot_dim / 2 turns by w_i radians per position. */
 typedef struct qgemm_rotation qgemm_rotation;
@@ -471,7 +475,8 @@ qgemm_status qgemm_kv_append(const qgemm_kv_cache *kv, int64_t layer, const void
                              int64_t qo_token_stride, int64_t qo_head_stride, void *stream);
 
 /* Bytes of workspace qgemm_paged_attention takes on the current device for up to `batch` sequences
- * and q_heads query heads.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE; CUDA. */
+ * and q_heads query heads (about 5 MB at d = 128 on 152 SMs, the same for every batch).
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE; CUDA. */
 qgemm_status qgemm_paged_attention_workspace_bytes(const qgemm_kv_cache *kv, int64_t batch,
                                                    int64_t q_heads, int64_t *bytes);
 
@@ -486,9 +491,9 @@ qgemm_status qgemm_paged_attention_workspace_bytes(const qgemm_kv_cache *kv, int
  *              not overlap.  q_heads is a multiple of the cache's heads.
  *   workspace  device, 16-byte aligned, qgemm_paged_attention_workspace_bytes at least.  Its bytes
  *              must be ZERO before its first call; every call leaves it ready for the next one on the
- *              same stream, of any batch and q_heads that fit it, on caches of the same d.  Calls that
- *              may overlap need workspaces of their own.
- * Launch: one kernel of up to one CTA per SM; the lengths are read on the device, so a captured call
+ *              same stream, of any batch, heads and cache whose workspace is no larger.  Calls that may
+ *              overlap need workspaces of their own.
+ * Launch: one kernel of up to two CTAs per SM; the lengths are read on the device, so a captured call
  * serves any lengths.  Repeatable bit for bit for the same inputs and SM count.
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, UNSUPPORTED_DTYPE, MISALIGNED (nothing enqueued); CUDA. */
 qgemm_status qgemm_paged_attention(const void *Q, int64_t q_batch_stride, int64_t q_head_stride,
@@ -505,8 +510,8 @@ qgemm_status qgemm_paged_attention(const void *Q, int64_t q_batch_stride, int64_
  * releases come before all growth; free pages go to the items in order, lowest first.  An item whose
  * pages (with those of the items before it) exceed the free ones keeps its length and sets bit 128 of the
  * device error word.  The sequences of one call must differ.
- * Scratch (also qgemm_kv_fork, qgemm_kv_compact): about 4 bytes a page and 24 an item from the library's pool
- * on `stream`.
+ * Scratch: 4 bytes a page and 24 an item from the library's pool on `stream` (qgemm_kv_fork the same,
+ * qgemm_kv_compact 16 bytes a page).
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED (nothing enqueued); CUDA. */
 qgemm_status qgemm_kv_resize(const qgemm_kv_cache *kv, int32_t *page_table, int64_t table_stride,
                              int64_t max_seqs, int64_t max_pages, int32_t *lens, int32_t *refs,
