@@ -375,8 +375,8 @@ def test_parts_are_merged_once_each():
     """The merging of a cut unit's n parts, restated: whatever order they arrive in, one part's owner finishes with
     all of them merged in order, every counter is back at zero, and no part is read after it was replaced."""
     rng = random.Random(11)
-    fan, levels = 16, 3
-    for n in [2, 3, 15, 16, 17, 31, 32, 33, 152, 255, 256, 257, 304, 4096]:
+    fan, levels = 32, 2
+    for n in [2, 3, 15, 16, 17, 31, 32, 33, 63, 64, 65, 152, 304, 1023, 1024]:
         for _ in range(3):
             order = list(range(n))
             rng.shuffle(order)
