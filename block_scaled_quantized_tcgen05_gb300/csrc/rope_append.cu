@@ -332,8 +332,9 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rope_append_kernel(const __gr
 // elements is spent once for 16.  Halves: piece k of the first half and of the second for k < rot / 16, then
 // the two halves of what is not rotated; interleaved: piece k of the row's first half and of its second.
 // Needs rows 16-byte aligned, strides below 2^31 bytes, d a multiple of 16, rot of 16 (halves) or 8; for
-// E4M3, whose blocks of 32 are four neighbouring lanes' pieces, rot of 64 (halves).  Elsewhere the kernel
-// above, 8 elements a lane, bound by its instructions.  (30011 x 12 rows of 96, rot 48, fp16: 27.3 us, 5.1
+// E4M3, whose blocks of 32 are four neighbouring lanes' pieces, rot of 64 (halves).  LPR = d / 16 lanes a row (a
+// cache's d is 64 or 128), or 0 for lanes counted from d: rotation alone, where no lane needs another, at d = 128
+// one percent slower.  Elsewhere the kernel above, 8 elements a lane, bound by its instructions.  (30011 x 12 rows of 96, rot 48, fp16: 27.3 us, 5.1
 // TB/s, against 32.8; 15009 x 36 rows of 128 into E4M3: 43.7, 6.0 TB/s, against 62.4; 16384 x 48 rows of 128 into
 // bf16: 62.9, 6.4 TB/s, against 70.6; 8192 x 40 interleaved rows of 128, bf16: 27.1, 6.2 TB/s, against 28.3.)
 template <class TY, int LPR, bool INTER, int CACHE>
@@ -345,10 +346,10 @@ __global__ void __launch_bounds__(THREADS, PAIR_BLOCKS) rope_pair_kernel(const _
     __shared__ int64_t s_slot[MAX_TPC], s_sslot[MAX_TPC];
     const int tid = threadIdx.x, half = p.rot / 2, pitch = (half + 3) & ~3;
     const int t0 = blockIdx.x * p.tpc, nt = min(p.tpc, p.T - t0);
-    constexpr int RPP = THREADS / LPR;
+    const int lpr = LPR ? LPR : p.d / 16, RPP = THREADS / lpr;
     constexpr int PR = PAIR_ROWS;
-    const int k = tid % LPR;
-    const bool lane = 16 * k < p.d;
+    const int r0 = tid / lpr, k = tid - r0 * lpr;
+    const bool lane = r0 < RPP;                        // the last lanes may make no whole row
     const int heads = p.hq + (CACHE ? 2 * p.hkv : 0);
     const int h0 = heads * int(blockIdx.y) / p.hsplit, nh = heads * int(blockIdx.y + 1) / p.hsplit - h0;
 
@@ -429,7 +430,7 @@ __global__ void __launch_bounds__(THREADS, PAIR_BLOCKS) rope_pair_kernel(const _
         }
     };
 
-    Row row = {tid / LPR / nh, tid / LPR % nh};
+    Row row = {r0 / nh, r0 % nh};
     uint4 va[PR], vb[PR];
     Row ahead = fetch(row, va, vb);
     set_up<CACHE != 0>(p, fr, t0, nt, pitch, s_cs, s_slot, s_sslot);
@@ -529,9 +530,8 @@ cudaError_t launch_pair_type(const RopeParams &p, const Frequencies &fr, bool in
     if (cache == 1)
         return p.d <= 64 ? launch_pair<TY, 4, 1>(p, fr, inter, grid, smem, stream)
                          : launch_pair<TY, 8, 1>(p, fr, inter, grid, smem, stream);
-    if (p.d <= 64) return launch_pair<TY, 4, 0>(p, fr, inter, grid, smem, stream);
-    if (p.d <= 128) return launch_pair<TY, 8, 0>(p, fr, inter, grid, smem, stream);
-    return launch_pair<TY, 16, 0>(p, fr, inter, grid, smem, stream);
+    if (p.d == 128) return launch_pair<TY, 8, 0>(p, fr, inter, grid, smem, stream);
+    return launch_pair<TY, 0, 0>(p, fr, inter, grid, smem, stream);
 }
 
 template <class TY, int LPR, bool INTER, bool VEC, int CACHE>
@@ -635,10 +635,13 @@ cudaError_t launch_rope_append(const AppendArgs &a, const LaunchCtx &ctx) {
         for (int i = 0; i < p.rot / 2; ++i) fr.f[i] = a.rope->freq[i];
         if (!inter) vec = vec && p.rot % 16 == 0;
     }
-    // Tokens a block: enough rows for four rounds of every lane's four, so that the sines are shared
-    // and the last rounds short against the rest; with few tokens one token a block and its heads dealt
-    // to several blocks, two blocks an SM.  (8192 x 40 rows of 128, paired kernel: four rounds 27.1 us, six
-    // 28.4, eight 31.1; one row a lane in flight 29.1.)
+    // Tokens a block: at most the rows of three rounds of what its lanes hold, five with an E4M3 cache (whose slots
+    // are another chain of reads at a block's start) and four in the general kernel; more leaves the last
+    // blocks alone on the GPU, fewer computes the sines for too few rows.  With few tokens one token a
+    // block and its heads dealt to several blocks, two blocks an SM.  A row more starts a round for
+    // itself: 30011 x 12 rows of 96, 42 a round, 10 tokens 24.6 us and 11 26.1.  (Paired kernel, tokens a block: 8192 x 40
+    // rows of 128 1 / 2 / 4 / 8: 31.4 / 26.5 / 27.3 / 29.6 us; 6038 x 26 1 / 3 / 5 / 8: 17.3 / 14.9 / 17.1 / 16.6; 15009 x
+    // 36 into E4M3 2 / 4 / 8: 48.3 / 43.5 / 45.8.)
     const int heads = p.hq + 2 * p.hkv;
     bool pair = vec && a.d % 16 == 0 && (inter ? p.rot % 8 == 0 : p.rot % (e4m3 ? 64 : 16) == 0);
     auto fits = [&](int64_t stride, int32_t *to) {
@@ -654,10 +657,12 @@ cudaError_t launch_rope_append(const AppendArgs &a, const LaunchCtx &ctx) {
     fits(p.head, &p.head32);
     fits(p.shead, &p.shead32);
     int lpr = a.d <= 64 ? 8 : (a.d <= 128 ? 16 : 32);
-    if (pair) lpr /= 2;
+    if (pair) lpr = a.d / 16;
     const int rpp = qg::THREADS / lpr;
     const int64_t slots = 2 * (int64_t)ctx.num_sms;
-    int tpc = (4 * (pair ? qg::PAIR_ROWS : qg::ROWS) * rpp + heads - 1) / heads;
+    const int rows = pair ? (e4m3 ? 5 : 3) * qg::PAIR_ROWS * rpp : 4 * qg::ROWS * rpp;
+    int tpc = rows / heads;
+    if (tpc < 1) tpc = 1;
     if (tpc > qg::MAX_TPC) tpc = qg::MAX_TPC;
     while (tpc > 1 && ((int64_t)a.T + tpc - 1) / tpc < slots) --tpc;
     p.tpc = tpc;
