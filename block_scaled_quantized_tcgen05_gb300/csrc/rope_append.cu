@@ -20,16 +20,17 @@
 // computed once into shared memory, while the first rows' loads are already in flight, and the next
 // rows' loads are in flight while a row is turned.  Aligned rows go through rope_pair_kernel; the general
 // kernel reads 16 bytes a lane, LPR lanes a row, or single elements where rows are not aligned, and takes a
-// pair's other half from the lane that holds it (a shuffle) or from memory.
+// pair's other half from the lane that holds it (a shuffle) or turns the row in shared memory.
 #include "kv_common.cuh"
 
 namespace qg {
 namespace {
 
 constexpr int THREADS = 128;
-constexpr int BLOCKS = 8;        // resident on an SM (64 registers a thread)
+constexpr int BLOCKS = 6;        // resident on an SM (80 registers a thread)
 constexpr int PAIR_BLOCKS = 7;   // of the paired kernel (72 registers)
 constexpr int ROWS = 4;          // rows a lane has in flight
+constexpr int HALF_ROWS = 2;     // of half-rotated rows
 constexpr int PAIR_ROWS = 2;     // and in the paired kernel, of two pieces each
 constexpr int MAX_TPC = 16;      // tokens of one block
 
@@ -54,6 +55,11 @@ struct RopeParams {
 struct Frequencies {
     uint64_t f[128];
 };
+
+// Floats of a token's cosines, and of its sines.
+__host__ __device__ constexpr int table_pitch(int rot) {
+    return (rot / 2 + 3) & ~3;
+}
 
 // 8 elements of a row from element e0 on; those at d and beyond read as zero.
 template <bool VEC>
@@ -140,17 +146,26 @@ __device__ __forceinline__ void set_up(const RopeParams &p, const Frequencies &f
     }
 }
 
-// LPR lanes a row of 8 elements each; INTER: interleaved pairs; VEC: rows are 16-byte aligned and
-// d, and for halves rot / 2, multiples of 8; CACHE: 0 none (rotation alone), 1 planes of the activations'
-// type, 2 E4M3.
+// LPR lanes a row of 8 elements each; INTER: interleaved pairs; VEC: rows are 16-byte aligned and d a
+// multiple of 8; CACHE: 0 none (rotation alone), 1 planes of the activations' type, 2 E4M3.  Halves whose
+// length is a multiple of 8 take a pair's other piece from the lane that holds it; of any other length it lies
+// across two lanes' pieces, so a row's lanes lay the row into shared memory, turn a pair each and take their
+// turned elements from there in 32 bits.  (30011 x 12 rows of 96, rot 38: 39.9 us; the two pieces read and
+// shifted 47.4; every element's other half from memory 93.6.  8192 x 40 rows of 120, rot 96: 33.4 us, by shared memory
+// 39.8.)
 template <class TY, int LPR, bool INTER, bool VEC, int CACHE>
 __global__ void __launch_bounds__(THREADS, BLOCKS) rope_append_kernel(const __grid_constant__ RopeParams p,
                                                               const __grid_constant__ Frequencies fr) {
     extern __shared__ __align__(16) float s_cs[];      // [tpc][2][pitch]: cosines, sines
     __shared__ int64_t s_slot[MAX_TPC], s_sslot[MAX_TPC];
+    constexpr int NR = INTER ? ROWS : HALF_ROWS;
+    // halves: rows as read and as turned; an eighth more a row, so that a warp's rows lie in different banks
+    constexpr int XP = 9 * LPR / 8, YP = 9 * LPR;      // of 16 bytes; of floats
+    __shared__ uint4 s_x[INTER ? 1 : NR * (THREADS / LPR) * XP];
+    __shared__ __align__(16) float s_y[INTER ? 1 : NR * (THREADS / LPR) * YP];
     griddep_launch_dependents();
     griddep_wait();
-    const int tid = threadIdx.x, half = p.rot / 2, pitch = (half + 3) & ~3;
+    const int tid = threadIdx.x, half = p.rot / 2, pitch = table_pitch(p.rot);
     const int t0 = blockIdx.x * p.tpc, nt = min(p.tpc, p.T - t0);
     constexpr int RPP = THREADS / LPR;                 // rows a pass
     const int lane_r = tid % LPR;
@@ -189,9 +204,9 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rope_append_kernel(const __gr
         const int64_t xh = side == 0 ? p.xh[0] : (side == 1 ? p.xh[1] : p.xh[2]);
         return x + (t0 + r.t) * xt + h * xh;
     };
-    auto fetch = [&](Row r, uint4 (&v)[ROWS]) {
+    auto fetch = [&](Row r, uint4 (&v)[NR]) {
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
+        for (int i = 0; i < NR; ++i) {
             if (r.t < nt) v[i] = load8<VEC>(source(r), e0, p.d);
             next(r);
         }
@@ -199,20 +214,45 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rope_append_kernel(const __gr
     };
     const int r0 = tid / LPR;
     Row row = {r0 / nh, r0 % nh};
-    uint4 v[ROWS];
+    uint4 v[NR];
     Row ahead = fetch(row, v);
 
     set_up<CACHE != 0>(p, fr, t0, nt, pitch, s_cs, s_slot, s_sslot);
     __syncthreads();
 
+    const bool whole = half % 8 == 0;                  // pieces' partners are pieces
+
     // every lane of the block makes the same number of rounds (the rows' exchanges are by warp)
-    for (int done = 0; done < nt * nh; done += ROWS * RPP) {
+    for (int done = 0; done < nt * nh; done += NR * RPP) {
         // the next rows' loads are in flight while these are turned: an output that is the input
         // itself is read before it is written, rows never share elements
-        uint4 w[ROWS];
+        uint4 w[NR];
         const Row after = fetch(ahead, w);
+        if (!INTER && half > 0 && !whole) {
+            __syncwarp();                               // the last round's rows have been read
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
+            for (int i = 0; i < NR; ++i) s_x[(i * RPP + r0) * XP + lane_r] = v[i];
+            __syncwarp();
+            Row r = row;
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                int h;
+                if (r.t < nt && side_of(r, h) < 2) {
+                    const uint16_t *x = reinterpret_cast<const uint16_t *>(s_x + (i * RPP + r0) * XP);
+                    float *y = s_y + (i * RPP + r0) * YP;
+                    const float *cs = s_cs + (2 * r.t) * pitch, *sn = cs + pitch;
+                    for (int j = lane_r; j < half; j += LPR) {
+                        const float a = TY::unpack(x[j]).x, b = TY::unpack(x[j + half]).x, c = cs[j], s = sn[j];
+                        y[j] = a * c - b * s;
+                        y[j + half] = a * s + b * c;
+                    }
+                }
+                next(r);
+            }
+            __syncwarp();
+        }
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
             if (done + i * RPP >= nt * nh) break;       // the same for every lane
             const bool live = row.t < nt;
             const int t = live ? row.t : 0;
@@ -243,7 +283,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rope_append_kernel(const __gr
                             x[2 * j + 1] = a * ss[j] + b * cc[j];
                         }
                 }
-            } else if (VEC) {
+            } else if (whole) {
                 // the other halves of this lane's pairs are in the lane half / 8 further or back
                 const int hl = half / 8;
                 const bool first = lane_r < hl, in = lane_r < 2 * hl;
@@ -267,30 +307,13 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rope_append_kernel(const __gr
                             x[j + k] = x[j + k] * cc[k] + o[k] * ss[k];
                     }
                 }
-            } else {
-                // ragged halves: each element's other half straight from memory, before any lane
-                // of the warp stores (the output may be the input itself)
-                float o[8];
-                const uint8_t *src = turned ? source(row) : nullptr;
+            } else if (turned && e0 < p.rot) {
+                const float *y = s_y + (i * RPP + r0) * YP + e0;
+                const float4 lo = *reinterpret_cast<const float4 *>(y), hi = *reinterpret_cast<const float4 *>(y + 4);
+                const float yy[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int e = e0 + j;
-                    o[j] = 0.0f;
-                    if (turned && e < p.rot) {
-                        const uint16_t u = reinterpret_cast<const uint16_t *>(
-                            src)[e < half ? e + half : e - half];
-                        o[j] = TY::unpack(u).x;
-                    }
-                }
-                __syncwarp();
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int e = e0 + j;
-                    if (turned && e < p.rot) {
-                        const int pair = e < half ? e : e - half;
-                        x[j] = x[j] * cs[pair] + o[j] * (e < half ? -sn[pair] : sn[pair]);
-                    }
-                }
+                for (int j = 0; j < 8; ++j)
+                    if (e0 + j < p.rot) x[j] = yy[j];
             }
             uint32_t byte = 0;
             uint2 codes = make_uint2(0, 0);
@@ -321,7 +344,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rope_append_kernel(const __gr
             next(row);
         }
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) v[i] = w[i];
+        for (int i = 0; i < NR; ++i) v[i] = w[i];
         row = ahead;
         ahead = after;
     }
@@ -331,12 +354,13 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rope_append_kernel(const __gr
 // pairs are its own (no exchange, one sine and cosine for two outputs) and what a row costs besides its
 // elements is spent once for 16.  Halves: piece k of the first half and of the second for k < rot / 16, then
 // the two halves of what is not rotated; interleaved: piece k of the row's first half and of its second.
-// Needs rows 16-byte aligned, strides below 2^31 bytes, d a multiple of 16, rot of 16 (halves) or 8; for
-// E4M3, whose blocks of 32 are four neighbouring lanes' pieces, rot of 64 (halves).  LPR = d / 16 lanes a row (a
+// Needs rows 16-byte aligned, strides below 2^31 bytes, d a multiple of 16, for halves
+// rot of 16, and for E4M3, whose blocks of 32 are four neighbouring lanes' pieces, of 64.  LPR = d / 16 lanes a row (a
 // cache's d is 64 or 128), or 0 for lanes counted from d: rotation alone, where no lane needs another, at d = 128
-// one percent slower.  Elsewhere the kernel above, 8 elements a lane, bound by its instructions.  (30011 x 12 rows of 96, rot 48, fp16: 27.3 us, 5.1
-// TB/s, against 32.8; 15009 x 36 rows of 128 into E4M3: 43.7, 6.0 TB/s, against 62.4; 16384 x 48 rows of 128 into
-// bf16: 62.9, 6.4 TB/s, against 70.6; 8192 x 40 interleaved rows of 128, bf16: 27.1, 6.2 TB/s, against 28.3.)
+// one percent slower.  Elsewhere the kernel above, 8 elements a lane, bound by its instructions.  (30011 x 12 rows
+// of 96, rot 48, fp16: 24.6 us, 5.6 TB/s, against 32.8; interleaved, rot 38: 23.0 against 29.8; 15009 x 36 rows of 128 into
+// E4M3: 43.6, 6.0 TB/s, against 62.4; 16384 x 48 rows of 128 into bf16: 61.1, 6.6 TB/s, against 70.6; 8192 x 40
+// interleaved rows of 128, bf16: 26.7, 6.3 TB/s, against 28.3.)
 template <class TY, int LPR, bool INTER, int CACHE>
 __global__ void __launch_bounds__(THREADS, PAIR_BLOCKS) rope_pair_kernel(const __grid_constant__ RopeParams p,
                                                             const __grid_constant__ Frequencies fr) {
@@ -344,7 +368,7 @@ __global__ void __launch_bounds__(THREADS, PAIR_BLOCKS) rope_pair_kernel(const _
     griddep_wait();
     extern __shared__ __align__(16) float s_cs[];
     __shared__ int64_t s_slot[MAX_TPC], s_sslot[MAX_TPC];
-    const int tid = threadIdx.x, half = p.rot / 2, pitch = (half + 3) & ~3;
+    const int tid = threadIdx.x, half = p.rot / 2, pitch = table_pitch(p.rot);
     const int t0 = blockIdx.x * p.tpc, nt = min(p.tpc, p.T - t0);
     const int lpr = LPR ? LPR : p.d / 16, RPP = THREADS / lpr;
     constexpr int PR = PAIR_ROWS;
@@ -419,11 +443,12 @@ __global__ void __launch_bounds__(THREADS, PAIR_BLOCKS) rope_pair_kernel(const _
     auto pack = [](const float (&x)[8]) {
         return make_uint4(TY::pack(x[0], x[1]), TY::pack(x[2], x[3]), TY::pack(x[4], x[5]), TY::pack(x[6], x[7]));
     };
-    auto pairs = [](float (&x)[8], const float *cs, const float *sn) {     // interleaved pairs of a piece
-        const float4 c = *reinterpret_cast<const float4 *>(cs), s = *reinterpret_cast<const float4 *>(sn);
+    auto pairs = [&](float (&x)[8], int e, const float *cs, const float *sn) {     // interleaved pairs of a piece
+        const float4 c = *reinterpret_cast<const float4 *>(cs + e / 2), s = *reinterpret_cast<const float4 *>(sn + e / 2);
         const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+            if (e / 2 + j >= half) continue;
             const float u = x[2 * j], v = x[2 * j + 1];
             x[2 * j] = u * cc[j] - v * ss[j];
             x[2 * j + 1] = u * ss[j] + v * cc[j];
@@ -452,8 +477,8 @@ __global__ void __launch_bounds__(THREADS, PAIR_BLOCKS) rope_pair_kernel(const _
             const bool rotate = p.rot > 0 && (!CACHE || side < 2);
             const float *cs = s_cs + (2 * t) * pitch, *sn = cs + pitch;
             if (INTER) {
-                if (rotate && turn_a) pairs(a, cs + ea / 2, sn + ea / 2);
-                if (rotate && turn_b) pairs(b, cs + eb / 2, sn + eb / 2);
+                if (rotate && turn_a) pairs(a, ea, cs, sn);
+                if (rotate && turn_b) pairs(b, eb, cs, sn);
             } else if (rotate && turn_a) {
 #pragma unroll
                 for (int j = 0; j < 8; j += 4) {
@@ -633,7 +658,6 @@ cudaError_t launch_rope_append(const AppendArgs &a, const LaunchCtx &ctx) {
         p.mscale = a.rope->mscale;
         inter = a.rope->interleaved != 0;
         for (int i = 0; i < p.rot / 2; ++i) fr.f[i] = a.rope->freq[i];
-        if (!inter) vec = vec && p.rot % 16 == 0;
     }
     // Tokens a block: at most the rows of three rounds of what its lanes hold, five with an E4M3 cache (whose slots
     // are another chain of reads at a block's start) and four in the general kernel; more leaves the last
@@ -643,7 +667,7 @@ cudaError_t launch_rope_append(const AppendArgs &a, const LaunchCtx &ctx) {
     // rows of 128 1 / 2 / 4 / 8: 31.4 / 26.5 / 27.3 / 29.6 us; 6038 x 26 1 / 3 / 5 / 8: 17.3 / 14.9 / 17.1 / 16.6; 15009 x
     // 36 into E4M3 2 / 4 / 8: 48.3 / 43.5 / 45.8.)
     const int heads = p.hq + 2 * p.hkv;
-    bool pair = vec && a.d % 16 == 0 && (inter ? p.rot % 8 == 0 : p.rot % (e4m3 ? 64 : 16) == 0);
+    bool pair = vec && a.d % 16 == 0 && (inter || p.rot % (e4m3 ? 64 : 16) == 0);
     auto fits = [&](int64_t stride, int32_t *to) {
         pair = pair && stride <= INT32_MAX;
         *to = (int32_t)(pair ? stride : 0);
@@ -670,7 +694,7 @@ cudaError_t launch_rope_append(const AppendArgs &a, const LaunchCtx &ctx) {
     const int64_t most = (heads + rpp - 1) / rpp;
     p.hsplit = (int32_t)(split < most ? split : most);
     const dim3 grid((unsigned)((a.T + tpc - 1) / tpc), (unsigned)p.hsplit);
-    const size_t smem = sizeof(float) * (size_t)tpc * 2 * ((p.rot / 2 + 3) / 4 * 4 + 4);
+    const size_t smem = sizeof(float) * (size_t)tpc * 2 * qg::table_pitch(p.rot);
     const int cache = append ? (e4m3 ? 2 : 1) : 0;
     if (pair)
         return a.bf16 ? qg::launch_pair_type<qg::TypeBF16>(p, fr, inter, cache, grid, smem, ctx.stream)

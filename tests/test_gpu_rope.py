@@ -124,6 +124,27 @@ def test_rope_gradient_against_differences(dev):
     _clean()
 
 
+@pytest.mark.parametrize("T,H,d,rot,inter", [
+    (5003, 1, 256, 254, False), (2500, 13, 64, 24, False), (1201, 40, 128, 50, False), (2011, 7, 80, 38, False),
+    (907, 6, 120, 96, False), (1203, 40, 96, 38, True), (3001, 5, 128, 126, True), (2003, 3, 90, 90, False),
+])
+def test_rope_parts_over_many_rounds(dev, T, H, d, rot, inter):
+    """Blocks of several tokens and rounds, in place; infinities past the rotated part stay there."""
+    g = torch.Generator().manual_seed(d + rot)
+    x = torch.randn(T, H, d, generator=g).half()
+    if rot < d:
+        x[::3, :, rot] = float("inf")
+        x[1::3, :, d - 1] = -float("inf")
+    pos = _positions(T, d)
+    rope = q.qgemm_create_rope(rot, interleaved=inter)
+    y = x.to(dev)
+    q.qgemm_rope(y, pos.to(dev), rope, out=y)
+    want, mag = ref.rotate(x, pos, rot, inter)
+    assert torch.equal(y.cpu()[..., rot:], x[..., rot:])
+    _close(y[..., :rot], want[..., :rot], mag[..., :rot], "rotated part")
+    _clean()
+
+
 def test_rope_nothing_to_do(dev):
     rope = q.qgemm_create_rope(64)
     x = torch.empty(0, 4, 64, dtype=torch.float16, device=dev)
@@ -230,6 +251,36 @@ def test_append_matches(dev, dtype, e4m3, d, hq, hkv, page, rot, inter, order):
         live = d // 32 if n in ("ks", "vs") else d
         now[1, pg, :, off, :live] = t[1, pg, :, off, :live]
         assert torch.equal(now.view(torch.uint8) if now.is_contiguous() else now, t.view(torch.uint8) if t.is_contiguous() else t), n
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("d,hq,hkv,rot,inter,T", [
+    (128, 5, 2, 100, False, 1500), (64, 3, 1, 24, False, 2000), (128, 8, 2, 102, True, 1100), (128, 3, 3, 96, False, 1300),
+])
+def test_append_parts_over_many_rounds(dev, e4m3, d, hq, hkv, rot, inter, T):
+    """One long sequence, more tokens than one round of a block, rotated in part."""
+    page = 24
+    pages = -(-T // page)
+    c = make_cache(dev, torch.float16, e4m3, 1, pages, hkv, page, d)
+    g = torch.Generator().manual_seed(rot)
+    x, k, v = (torch.randn(T, h, d, generator=g).half() for h in (hq, hkv, hkv))
+    table = torch.randperm(pages, generator=g).to(torch.int32)[None]
+    pos = torch.arange(T, dtype=torch.int32)
+    rope = q.qgemm_create_rope(rot, interleaved=inter)
+    out = torch.empty(T, hq, d, dtype=torch.float16, device=dev)
+    q.qgemm_kv_append(c["kv"], 0, k.to(dev), v.to(dev), torch.zeros(T, dtype=torch.int32, device=dev), pos.to(dev),
+                      table.to(dev), rope=rope, Q=x.to(dev), Q_out=out)
+    _clean()
+    _close(out, *ref.rotate(x, pos, rot, inter), "queries")
+    want, mag = ref.rotate(k, pos, rot, inter)
+    pg, off = table[0, (pos // page).long()].long().to(dev), (pos % page).long().to(dev)
+    if e4m3:
+        _check_e4m3(c["k"][0, pg, :, off], c["ks"][0, pg, :, off], want, mag, torch.float16, "keys")
+        _check_e4m3(c["v"][0, pg, :, off], c["vs"][0, pg, :, off], v.double(), torch.zeros_like(want), torch.float16,
+                    "values")
+    else:
+        _close(c["k"][0, pg, :, off], want, mag, "keys")
+        assert torch.equal(c["v"][0, pg, :, off].cpu(), v)
 
 
 def test_append_special_values(dev):
