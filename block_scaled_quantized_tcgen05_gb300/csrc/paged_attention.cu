@@ -71,7 +71,9 @@ struct AttnParams {
     int64_t table_stride;
     int32_t B, hq, hkv, group, chunks;      // chunks: units per key-value head
     int32_t max_seqs, max_pages, page_size, pages, window;
-    bool one_page;                          // page_size is a multiple of STEP
+    bool one_page;                          // page_size is a multiple of STEP, and offsets fit the units of the next
+    uint32_t page32, head32, token32;       // the strides in 16 bytes
+    uint32_t spage32, shead32, stoken32;    // and in 4 bytes
     uint32_t page_magic, page_shift;        // of kvi::page_of
     float scale_log2;
     int32_t *counters;
@@ -509,29 +511,28 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
     // ---- the copies of the looked-up step into ring slot `slot`
     constexpr int RPI = 32 / C::CHUNKS;          // rows an instruction of the warp copies
     const int chunk = lane % C::CHUNKS, row0 = lane / C::CHUNKS;
-    const int64_t lane_off = row0 * p.token + chunk * 16;
+    const uint8_t *const lane_k = p.k + (row0 * p.token + chunk * 16), *const lane_v = p.v + (row0 * p.token + chunk * 16);
     const uint32_t lane_to = row0 * C::ROWB + swizzle<C>(row0, chunk) * 16;
-    const int64_t lane_soff = C::E4M3 ? lane % STEP * p.stoken : 0;
+    // lanes 0-15: the keys' scale rows, lanes 16-31: the values'
+    const uint8_t *const lane_s = C::E4M3 ? (lane < STEP ? p.ks : p.vs) + lane % STEP * p.stoken : nullptr;
     auto issue = [&](int slot) {
         const int32_t pg = x.pg, pr = x.pr, ph = x.h;
         if (p.one_page && x.hi - x.lo == STEP && pg >= 0 && pg < p.pages) {
             // a whole step of one page: rows a token stride apart
             const uint32_t kd = ring + slot * C::STAGEB;
-            const int64_t base = pg * p.page + pr * p.token + ph * p.head;
-            if (QG_IN_BOUNDS(p.err, base >= 0 && base + (STEP - 1) * p.token + C::ROWB <= p.extent)) {
-                const uint8_t *k = p.k + base + lane_off, *v = p.v + base + lane_off;
+            uint32_t at = pg * p.page32 + pr * p.token32 + ph * p.head32;
+            if (QG_IN_BOUNDS(p.err, int64_t(at) * 16 + (STEP - 1) * p.token + C::ROWB <= p.extent)) {
 #pragma unroll
                 for (int i = 0; i < STEP / RPI; ++i) {
                     // swizzle(a + b, c) = swizzle(a, 0) ^ swizzle(b, c) for rows a and b without common bits
                     const uint32_t d = (kd + lane_to) ^ (swizzle<C>(i * RPI, 0) * 16);
-                    cp_async_16(d + i * RPI * C::ROWB, k, 16);
-                    cp_async_16(d + i * RPI * C::ROWB + C::PLANE, v, 16);
-                    k += RPI * p.token;
-                    v += RPI * p.token;
+                    cp_async_16(d + i * RPI * C::ROWB, lane_k + uint64_t(at) * 16, 16);
+                    cp_async_16(d + i * RPI * C::ROWB + C::PLANE, lane_v + uint64_t(at) * 16, 16);
+                    at += RPI * p.token32;
                 }
-                if (C::E4M3)     // lanes 0-15: the keys' scale rows, lanes 16-31: the values'
+                if (C::E4M3)
                     cp_async_4(kd + 2 * C::PLANE + lane * 4,
-                               (lane < STEP ? p.ks : p.vs) + pg * p.spage + pr * p.stoken + ph * p.shead + lane_soff, 4);
+                               lane_s + uint64_t(pg * p.spage32 + pr * p.stoken32 + ph * p.shead32) * 4, 4);
                 if (lane == 0) s_mask[warp][slot] = (1u << STEP) - 1;
                 return;
             }
@@ -1001,7 +1002,15 @@ cudaError_t launch_paged_attention(const PagedAttnArgs &a, const LaunchCtx &ctx)
     p.slots = qg::slots_of(ctx.num_sms);
     p.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + qg::counters_bytes(ctx.num_sms));
     p.err = ctx.err;
-    p.one_page = c->page_size % qg::STEP == 0;
+    p.one_page = c->page_size % qg::STEP == 0 && p.extent >> 36 == 0 && p.sextent >> 34 == 0;
+    if (p.one_page) {
+        p.page32 = (uint32_t)(p.page / 16);
+        p.head32 = (uint32_t)(p.head / 16);
+        p.token32 = (uint32_t)(p.token / 16);
+        p.spage32 = (uint32_t)(p.spage / 4);
+        p.shead32 = (uint32_t)(p.shead / 4);
+        p.stoken32 = (uint32_t)(p.stoken / 4);
+    }
     kvi::page_divisor(p.page_size, &p.page_magic, &p.page_shift);
     // no more CTAs than tiles (and EXTRAs) the table rows can hold
     const int64_t most = units * (kvi::tiles_of(a.max_pages * (int32_t)c->page_size, qg::TILE) + 3);
