@@ -40,8 +40,10 @@
 // hi) (relative error 2^-21 in fp16, 2^-15 in bf16), and both are multiplied: the matrix unit has the time.
 // lo is kept above zero, at 2^-39 of the largest weight at least, so that an infinite value stays one (0 x
 // inf and inf - inf would be NaN).  E4M3
-// codes are exact in 16 bits; a key block's scale goes onto its part of the score in fp32, and a value
-// becomes the nearest half (bf16) to code * 2^(byte - 127): exact for every block the append writes.
+// codes are exact in halves, and are multiplied as such; a key block's scale goes onto its part of the score
+// in fp32, and a value becomes the half code * 2^(byte - 127), exact, with P in halves too.  Where a step's scales
+// are not halves, values become the nearest 16-bit value of the activations' type, with P in that type.  (bf16
+// queries, 128 ragged E4M3 sequences: 134 us; codes brought to bf16 by way of fp32 170.)
 #include <atomic>
 #include <type_traits>
 
@@ -88,6 +90,7 @@ struct Cfg {
     static constexpr int D = D_;
     static constexpr bool E4M3 = E4M3_;
     static constexpr int NH = NH_;                       // groups of 8 query heads of a unit
+    static constexpr bool SCALED = E4M3 && TY::BF16;     // bf16 queries go into products of halves
     static constexpr int ROWB = E4M3 ? D : 2 * D;        // bytes of a cached row
     static constexpr int CHUNKS = ROWB / 16;             // 16-byte pieces of a row
     static constexpr int PLANE = STEP * ROWB;            // bytes of a step's keys (or values)
@@ -197,20 +200,11 @@ __device__ __forceinline__ int swizzle(int row, int chunk) {
 }
 
 // Four E4M3 codes as two pairs of 16-bit values (bytes 0, 1 and 2, 3): exact.
-__device__ __forceinline__ void decode4_f16(uint32_t codes, uint32_t &lo, uint32_t &hi) {
+__device__ __forceinline__ void decode4(uint32_t codes, uint32_t &lo, uint32_t &hi) {
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
         "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
         : "=r"(lo), "=r"(hi)
         : "r"(codes));
-}
-template <class TY>
-__device__ __forceinline__ void decode4(uint32_t codes, uint32_t &lo, uint32_t &hi) {
-    decode4_f16(codes, lo, hi);
-    if (TY::BF16) {
-        const float2 a = TypeF16::unpack(lo), b = TypeF16::unpack(hi);
-        lo = TY::pack(a.x, a.y);
-        hi = TY::pack(b.x, b.y);
-    }
 }
 // The scale 2^(byte - 127): byte 0 is the fp32 subnormal 2^-127, byte 255 NaN.  FAST: neither occurs
 // (but for the 0 of a masked row, whose codes are 0).
@@ -224,20 +218,20 @@ struct Scale2 {
     uint32_t h2;         // as halves
     float lo, hi;        // as fp32
 };
-template <class TY, bool FAST>
+template <bool FAST>
 __device__ __forceinline__ Scale2 make_scale(uint32_t lo, uint32_t hi) {
     Scale2 s;
     s.lo = scale_f32<FAST>(lo);
     s.hi = scale_f32<FAST>(hi);
-    s.h2 = TY::BF16 || !FAST ? 0u : TypeF16::pack(s.lo, s.hi);
+    s.h2 = FAST ? TypeF16::pack(s.lo, s.hi) : 0u;
     return s;
 }
-// Four codes times their scales (a pair of tokens' in each half), rounded once.  FAST: the scales
-// are halves, so one half multiply does it; through fp32, where the product is exact, otherwise.
+// Four codes times their scales (a pair of tokens' in each half), rounded once to TY.  FAST: TY and the
+// scales are halves, so one half multiply does it; through fp32, where the product is exact, otherwise.
 template <class TY, bool FAST>
 __device__ __forceinline__ void decode4(uint32_t codes, const Scale2 &s, uint32_t &lo, uint32_t &hi) {
-    decode4_f16(codes, lo, hi);
-    if (FAST && !TY::BF16) {
+    decode4(codes, lo, hi);
+    if (FAST) {
         asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(s.h2));
         asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(s.h2));
         return;
@@ -576,6 +570,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
     uint32_t qb[C::NH][C::D / 16][2];       // query fragments
     float acc[C::NH][C::MT][4];             // rows of d, columns of heads 2 c4, 2 c4 + 1
     float m[C::NH][2], l[C::NH][2];
+    float qs[C::NH][2];                     // SCALED: what the scores of heads 2 c4, 2 c4 + 1 are still to be times
     auto load_queries = [&](const Step &u) {
         const int h = u.hp / p.chunks, part = u.hp - h * p.chunks;
         const int h0 = h * p.group + part * ROWS, rows = min(ROWS, p.group - part * ROWS);
@@ -591,6 +586,35 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
                 const int e2 = C::E4M3 ? e + 2 : e + 8;
                 qb[n][kk][0] = in ? *reinterpret_cast<const uint32_t *>(q + 2 * e) : 0;
                 qb[n][kk][1] = in ? *reinterpret_cast<const uint32_t *>(q + 2 * e2) : 0;
+            }
+        }
+    };
+    // bf16 queries of an E4M3 cache become halves times a power of two that takes the row's largest below
+    // 2^15: exact where an element is above 2^-32 of that, off by 2^-40 of it elsewhere
+    auto scale_queries = [&] {
+        if constexpr (C::SCALED) {
+#pragma unroll
+            for (int n = 0; n < C::NH; ++n) {
+                uint32_t top = 0;            // the largest absolute value's bits, of even and of odd elements
+#pragma unroll
+                for (int kk = 0; kk < C::D / 16; ++kk)
+                    top = __vmaxu2(top, __vmaxu2(qb[n][kk][0] & 0x7FFF7FFFu, qb[n][kk][1] & 0x7FFF7FFFu));
+                top = max(top & 0xFFFFu, top >> 16);
+                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                // 2^k, k = 14 - the largest's exponent, at most 126; infinity and NaN stay what they are
+                const uint32_t up = min(268u - (top >> 7), 253u);
+                const float f = __uint_as_float(up << 23);
+#pragma unroll
+                for (int kk = 0; kk < C::D / 16; ++kk)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 x = TY::unpack(qb[n][kk][i]);
+                        qb[n][kk][i] = TypeF16::pack(x.x * f, x.y * f);
+                    }
+                const float down = __uint_as_float((254u - up) << 23);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) qs[n][i] = __shfl_sync(0xFFFFFFFFu, down, (2 * c4 + i) * 4);
             }
         }
     };
@@ -615,6 +639,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
     // ---- one step: scores of 16 tokens, the running softmax, the weighted values
     auto step = [&](int slot, auto fast_tag) {
         [[maybe_unused]] constexpr bool FAST = decltype(fast_tag)::value;
+        using PT = std::conditional_t<C::E4M3 && FAST, TypeF16, TY>;      // of P and the values
         const uint32_t kd = ring + slot * C::STAGEB, vd = kd + C::PLANE;
         const uint32_t mask = s_mask[warp][slot];
         float s[C::NH][4];
@@ -649,15 +674,18 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
                 const float sx = scale_f32<FAST>((bx >> (8 * blk)) & 255u);
                 const float sy = scale_f32<FAST>((by >> (8 * blk)) & 255u);
                 uint32_t a[8];
-                decode4<TY>(x.x, a[0], a[2]);
-                decode4<TY>(y.x, a[1], a[3]);
-                decode4<TY>(x.y, a[4], a[6]);
-                decode4<TY>(y.y, a[5], a[7]);
+                decode4(x.x, a[0], a[2]);
+                decode4(y.x, a[1], a[3]);
+                decode4(x.y, a[4], a[6]);
+                decode4(y.y, a[5], a[7]);
 #pragma unroll
                 for (int n = 0; n < C::NH; ++n) {
                     float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    mma16816(TY::BF16, part, a[0], a[1], a[2], a[3], qb[n][2 * blk][0], qb[n][2 * blk][1]);
-                    mma16816(TY::BF16, part, a[4], a[5], a[6], a[7], qb[n][2 * blk + 1][0], qb[n][2 * blk + 1][1]);
+                    mma16816(false, part, a[0], a[1], a[2], a[3], qb[n][2 * blk][0], qb[n][2 * blk][1]);
+                    mma16816(false, part, a[4], a[5], a[6], a[7], qb[n][2 * blk + 1][0], qb[n][2 * blk + 1][1]);
+                    if constexpr (C::SCALED && !FAST)       // first, so that a large scale meets no larger sum
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) part[i] *= qs[n][i & 1];
                     s[n][0] += sx * part[0];
                     s[n][1] += sx * part[1];
                     s[n][2] += sy * part[2];
@@ -669,7 +697,10 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
 #pragma unroll
         for (int n = 0; n < C::NH; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[n][i] *= p.scale_log2;
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (C::SCALED && FAST) s[n][i] *= qs[n][i & 1];
+                s[n][i] *= p.scale_log2;
+            }
         if (mask != (1u << STEP) - 1) {
             const bool in0 = (mask >> g) & 1, in8 = (mask >> (g + 8)) & 1;
 #pragma unroll
@@ -712,17 +743,17 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
                 const float a = ex2(s[n][2 * i] - m0), b = ex2(s[n][2 * i + 1] - m1);
                 l[n][0] += a;
                 l[n][1] += b;
-                const uint32_t h = TY::pack_down(a, b);
-                const float2 f = TY::unpack(h);
+                const uint32_t h = PT::pack_down(a, b);
+                const float2 f = PT::unpack(h);
                 hi[n][i] = transpose8(h);
-                lo[n][i] = transpose8(TY::pack(fmaxf(a - f.x, P_LEAST), fmaxf(b - f.y, P_LEAST)));
+                lo[n][i] = transpose8(PT::pack(fmaxf(a - f.x, P_LEAST), fmaxf(b - f.y, P_LEAST)));
             }
         }
         auto weigh = [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
             for (int n = 0; n < C::NH; ++n) {
-                mma16816(TY::BF16, acc[n][j], a0, a1, a2, a3, hi[n][0], hi[n][1]);
-                mma16816(TY::BF16, acc[n][j], a0, a1, a2, a3, lo[n][0], lo[n][1]);
+                mma16816(PT::BF16, acc[n][j], a0, a1, a2, a3, hi[n][0], hi[n][1]);
+                mma16816(PT::BF16, acc[n][j], a0, a1, a2, a3, lo[n][0], lo[n][1]);
             }
         };
         if constexpr (!C::E4M3) {
@@ -752,7 +783,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
                     w[i][0] = x.x, w[i][1] = x.y;
                 }
             }
-            const Scale2 s01 = make_scale<TY, FAST>(byte[0], byte[1]), s23 = make_scale<TY, FAST>(byte[2], byte[3]);
+            const Scale2 s01 = make_scale<FAST>(byte[0], byte[1]), s23 = make_scale<FAST>(byte[2], byte[3]);
 #pragma unroll
             for (int x = 0; x < C::D / 32; ++x) {
                 uint32_t t[2][4];
@@ -760,15 +791,15 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
                 for (int y = 0; y < 2; ++y) {
                     const uint32_t a = __byte_perm(w[0][x], w[1][x], y ? 0x7362 : 0x5140);
                     const uint32_t b = __byte_perm(w[2][x], w[3][x], y ? 0x7362 : 0x5140);
-                    decode4<TY, FAST>(a, s01, t[y][0], t[y][1]);
-                    decode4<TY, FAST>(b, s23, t[y][2], t[y][3]);
+                    decode4<PT, FAST>(a, s01, t[y][0], t[y][1]);
+                    decode4<PT, FAST>(b, s23, t[y][2], t[y][3]);
                 }
 #pragma unroll
                 for (int n = 0; n < C::NH; ++n) {
-                    mma16816(TY::BF16, acc[n][2 * x], t[0][0], t[0][1], t[0][2], t[0][3], hi[n][0], hi[n][1]);
-                    mma16816(TY::BF16, acc[n][2 * x + 1], t[1][0], t[1][1], t[1][2], t[1][3], hi[n][0], hi[n][1]);
-                    mma16816(TY::BF16, acc[n][2 * x], t[0][0], t[0][1], t[0][2], t[0][3], lo[n][0], lo[n][1]);
-                    mma16816(TY::BF16, acc[n][2 * x + 1], t[1][0], t[1][1], t[1][2], t[1][3], lo[n][0], lo[n][1]);
+                    mma16816(PT::BF16, acc[n][2 * x], t[0][0], t[0][1], t[0][2], t[0][3], hi[n][0], hi[n][1]);
+                    mma16816(PT::BF16, acc[n][2 * x + 1], t[1][0], t[1][1], t[1][2], t[1][3], hi[n][0], hi[n][1]);
+                    mma16816(PT::BF16, acc[n][2 * x], t[0][0], t[0][1], t[0][2], t[0][3], lo[n][0], lo[n][1]);
+                    mma16816(PT::BF16, acc[n][2 * x + 1], t[1][0], t[1][1], t[1][2], t[1][3], lo[n][0], lo[n][1]);
                 }
             }
         }
@@ -877,6 +908,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
     }
     __syncwarp();
     load_queries(s_step[warp][0]);
+    scale_queries();
     clear();
     int slot = 0, fill = C::NSTAGES - 1;
 #pragma unroll 1
@@ -908,6 +940,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
             if (more) load_queries(s_step[warp][(k + 1) % STEPS]);   // in flight while the warps merge
             end_unit(done, slot);
             if (!more) break;
+            scale_queries();
             clear();
         }
         slot = slot + 1 == C::NSTAGES ? 0 : slot + 1;

@@ -263,6 +263,29 @@ def test_every_scale_byte(dev):
             p.check(o, l, what=f"bytes {lo}..{hi}")
 
 
+@pytest.mark.parametrize("d,hq,hkv", [(128, 5, 1), (64, 24, 2)])
+@pytest.mark.parametrize("power,byte", [(0, 119), (60, 59), (-60, 179), (-110, 229), (100, 19), (30, 119)])
+def test_bf16_queries_of_any_size_meet_e4m3_keys(dev, d, hq, hkv, power, byte):
+    """Query rows of very different sizes, wide ranges inside a row, keys whose scales make up for them."""
+    p = Problem(dev, [200, 3], hq, hkv, d, 16, torch.bfloat16, True, seed=power % 97)
+    g = torch.Generator().manual_seed(d + power % 97)
+    p.q = (p.q.float() * 2.0 ** (power + torch.randint(-12, 1, p.q.shape, generator=g).float())).to(torch.bfloat16)
+    p.q[:, 0] = 0.0
+    if power == 30:                                       # sizes only a power of two apart from a row's own keys
+        p.q = (p.q.float() * 2.0 ** -30).to(torch.bfloat16)
+        p.q[0, 1] *= 2.0 ** -40
+        p.q[1, 2, 5] = 2.0 ** -126
+    for b, n in enumerate(p.lens):
+        t = torch.arange(n)
+        pg, off = p.table[p.rows[b], t // 16].long(), t % 16
+        sc = torch.randint(byte - 2, byte + 3, (n, hkv, 4), generator=g, dtype=torch.uint8)
+        p.ks[1, pg, :, off] = sc
+        p.seen[b][0] = ref.dequant(p.k[1, pg, :, off], sc, torch.bfloat16)
+    o, l = p.run(scale=1.0)
+    _clean()
+    p.check(o, l, scale=1.0)
+
+
 def test_bad_pages_and_lengths_are_skipped(dev):
     """Table entries that name no page: their tokens are absent; a length past the table row ends with the
     row; a sequence number out of range is an empty sequence.  The error word says so each time."""
