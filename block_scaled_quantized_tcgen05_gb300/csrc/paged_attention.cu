@@ -84,12 +84,17 @@ struct AttnParams {
     unsigned *err;
 };
 
-template <class TY_, int D_, bool E4M3_, int NH_>
+template <class TY_, int D_, bool E4M3_, int HEADS_>
 struct Cfg {
     using TY = TY_;
     static constexpr int D = D_;
     static constexpr bool E4M3 = E4M3_;
-    static constexpr int NH = NH_;                       // groups of 8 query heads of a unit
+    static constexpr int HEADS = HEADS_;                 // query heads of a unit at most: 4, 8 or 16
+    static constexpr int NH = HEADS == 16 ? 2 : 1;       // in groups of 8
+    // At most 4 heads: columns 4-7 repeat them, and weigh the values with lo where 0-3 do with hi, so that one
+    // product does both (128 ragged E4M3 sequences of 4 heads a key-value head: 122 us, with two products 127;
+    // 16-bit caches are bound by HBM either way)
+    static constexpr bool PACKED = HEADS == 4;
     static constexpr bool SCALED = E4M3 && TY::BF16;     // bf16 queries go into products of halves
     static constexpr int ROWB = E4M3 ? D : 2 * D;        // bytes of a cached row
     static constexpr int CHUNKS = ROWB / 16;             // 16-byte pieces of a row
@@ -336,7 +341,7 @@ __device__ __forceinline__ void merge_parts(const AttnParams &p, const Step &u, 
         if (!*s_last) return;
         __threadfence();
         const bool all = i0 == 0 && members * stride >= parts;
-        for (int x = tid; x < 8 * C::NH * C::D / 4; x += THREADS) {
+        for (int x = tid; x < C::HEADS * C::D / 4; x += THREADS) {
             const int row = x / (C::D / 4), col = x % (C::D / 4) * 4;
             float M = -INFINITY, L = 0.0f;
             float4 o = make_float4(0, 0, 0, 0);
@@ -576,8 +581,9 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
         const int h0 = h * p.group + part * ROWS, rows = min(ROWS, p.group - part * ROWS);
 #pragma unroll
         for (int n = 0; n < C::NH; ++n) {
-            const bool in = 8 * n + g < rows;
-            const uint8_t *q = p.q + u.b * p.qb + (h0 + 8 * n + g) * p.qh;
+            const int r = C::PACKED ? g % 4 : 8 * n + g;
+            const bool in = r < rows;
+            const uint8_t *q = p.q + u.b * p.qb + (h0 + r) * p.qh;
 #pragma unroll
             for (int kk = 0; kk < C::D / 16; ++kk) {
                 // 16-bit rows: the fragments ldmatrix gives; 8-bit rows: thread c4 holds 8 consecutive
@@ -745,8 +751,9 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
                 l[n][1] += b;
                 const uint32_t h = PT::pack_down(a, b);
                 const float2 f = PT::unpack(h);
-                hi[n][i] = transpose8(h);
-                lo[n][i] = transpose8(PT::pack(fmaxf(a - f.x, P_LEAST), fmaxf(b - f.y, P_LEAST)));
+                const uint32_t r = PT::pack(fmaxf(a - f.x, P_LEAST), fmaxf(b - f.y, P_LEAST));
+                hi[n][i] = transpose8(C::PACKED && c4 >= 2 ? r : h);
+                if (!C::PACKED) lo[n][i] = transpose8(r);
             }
         }
         auto weigh = [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
@@ -798,6 +805,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
                 for (int n = 0; n < C::NH; ++n) {
                     mma16816(PT::BF16, acc[n][2 * x], t[0][0], t[0][1], t[0][2], t[0][3], hi[n][0], hi[n][1]);
                     mma16816(PT::BF16, acc[n][2 * x + 1], t[1][0], t[1][1], t[1][2], t[1][3], hi[n][0], hi[n][1]);
+                    if (C::PACKED) continue;
                     mma16816(PT::BF16, acc[n][2 * x], t[0][0], t[0][1], t[0][2], t[0][3], lo[n][0], lo[n][1]);
                     mma16816(PT::BF16, acc[n][2 * x + 1], t[1][0], t[1][1], t[1][2], t[1][3], lo[n][0], lo[n][1]);
                 }
@@ -864,7 +872,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
             }
             __syncthreads();
             // 4 elements a thread
-            for (int x = tid; x < C::MERGE_ROWS * C::D / 4; x += THREADS) {
+            for (int x = tid; x < (C::PACKED ? 4 : C::MERGE_ROWS) * C::D / 4; x += THREADS) {
                 const int r = x / (C::D / 4), row = blk * C::MERGE_ROWS + r, col = x % (C::D / 4) * 4;
                 float M = -INFINITY;
 #pragma unroll
@@ -878,6 +886,11 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
                     const float4 a = *reinterpret_cast<const float4 *>(
                         rows_of(w) + r * C::D + 4 * place(col / 4, row));
                     o.x += f * a.x, o.y += f * a.y, o.z += f * a.z, o.w += f * a.w;
+                    if constexpr (C::PACKED) {
+                        const float4 b = *reinterpret_cast<const float4 *>(
+                            rows_of(w) + (r + 4) * C::D + 4 * place(col / 4, row + 4));
+                        o.x += f * b.x, o.y += f * b.y, o.z += f * b.z, o.w += f * b.w;
+                    }
                     L += f * s_l[w][row];
                 }
                 if (whole) {
@@ -968,8 +981,9 @@ cudaError_t launch(const AttnParams &p, int64_t most, const qgi::LaunchCtx &ctx)
 template <class TY, int D>
 cudaError_t launch_cache(const AttnParams &p, bool e4m3, int64_t most, const qgi::LaunchCtx &ctx) {
     const bool wide = p.group > 8;
-    if (e4m3) return wide ? launch<Cfg<TY, D, true, 2>>(p, most, ctx) : launch<Cfg<TY, D, true, 1>>(p, most, ctx);
-    return wide ? launch<Cfg<TY, D, false, 2>>(p, most, ctx) : launch<Cfg<TY, D, false, 1>>(p, most, ctx);
+    if (!e4m3) return wide ? launch<Cfg<TY, D, false, 16>>(p, most, ctx) : launch<Cfg<TY, D, false, 8>>(p, most, ctx);
+    if (p.group <= 4) return launch<Cfg<TY, D, true, 4>>(p, most, ctx);
+    return wide ? launch<Cfg<TY, D, true, 16>>(p, most, ctx) : launch<Cfg<TY, D, true, 8>>(p, most, ctx);
 }
 
 int64_t chunks_of(int64_t group) { return (group + ROWS - 1) / ROWS; }
