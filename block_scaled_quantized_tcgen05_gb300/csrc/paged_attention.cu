@@ -256,16 +256,15 @@ struct Cursor {
     int32_t seq;          // page-table row
     int32_t next_seq, next_len;   // of sequence b + 1, read ahead (-1: none)
 };
-// What the computing side has to know of a step, left in shared memory by the look-up.
+// What the computing side has to know of a unit, left in shared memory by the look-up.
 struct Step {
     int32_t b, hp;        // sequence, key-value head * chunks + part
     int32_t t0;           // place of the unit's first tile after the range's begin (negative: before it)
-    uint32_t tiles;       // of the unit; LAST: the unit's or the range's last tile, END: the range's
+    int32_t tiles;        // of the unit
 };
-constexpr uint32_t LAST = 0x80000000u, END = 0x40000000u;
 constexpr int FAN = 32;   // parts of a unit merged at once
 constexpr int LEVELS = 2; // FAN^LEVELS parts at most
-constexpr int STEPS = 8;  // steps looked up and not yet computed, at most
+constexpr int STEPS = 8;  // units looked up and not yet computed, at most
 
 __device__ __forceinline__ int32_t sequence(const AttnParams &p, int b) {
     if (b >= p.B) return -1;
@@ -482,7 +481,8 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
         int32_t lo = 0, hi = 0;          // rows of the step that are tokens of the range
         int32_t h = 0;                   // its key-value head
     } x;
-    auto look_up = [&](int k) {          // the range's k-th step
+    int unit = 0;                        // units looked up
+    auto look_up = [&](bool opens) {     // the next step of the range; opens: its first
         x.lo = x.hi = 0;
         if (load.rel < span) {
             const int32_t t0 = load.first / STEP * STEP + load.tile * TILE + warp * STEP;
@@ -496,15 +496,18 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
                 // rows before the range's first token may lie in a page of no interest
                 if (p.one_page || (l >= x.lo && l < x.hi)) x.pg = p.table[load.seq * p.table_stride + i];
             }
-            Step st;
-            st.b = load.b;
-            st.hp = load.h * p.chunks + load.part;
-            st.t0 = load.rel - load.tile;
-            st.tiles = load.ntiles;
+            if (load.tile == 0 || opens) {       // the unit's first tile in the range
+                if (lane == 0) {
+                    Step st;
+                    st.b = load.b;
+                    st.hp = load.h * p.chunks + load.part;
+                    st.t0 = load.rel - load.tile;
+                    st.tiles = load.ntiles;
+                    s_step[warp][unit % STEPS] = st;
+                }
+                ++unit;
+            }
             advance<C>(load, p);
-            if (load.tile == 0) st.tiles |= LAST;
-            if (load.rel >= span) st.tiles |= LAST | END;
-            if (lane == 0) s_step[warp][k % STEPS] = st;
         }
     };
     // ---- the copies of the looked-up step into ring slot `slot`
@@ -643,11 +646,10 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
                                     : C::D == 128 ? swizzle<C>(v_row, g) * 16 : swizzle<C>(v_row, g / 2) * 16 + g % 2 * 8);
 
     // ---- one step: scores of 16 tokens, the running softmax, the weighted values
-    auto step = [&](int slot, auto fast_tag) {
+    auto step = [&](int slot, uint32_t mask, auto fast_tag) {
         [[maybe_unused]] constexpr bool FAST = decltype(fast_tag)::value;
         using PT = std::conditional_t<C::E4M3 && FAST, TypeF16, TY>;      // of P and the values
         const uint32_t kd = ring + slot * C::STAGEB, vd = kd + C::PLANE;
-        const uint32_t mask = s_mask[warp][slot];
         float s[C::NH][4];
 #pragma unroll
         for (int n = 0; n < C::NH; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
@@ -825,7 +827,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
     // that were just read (with a buffer of its own, 2 heads at a time beside two CTAs' rings: 152 us for
     // the 128 ragged E4M3 sequences, 135 so); a whole unit is written out, a part goes to the workspace
     auto end_unit = [&](const Step &u, int slot) {
-        const int32_t tiles = (int32_t)(u.tiles & ~(LAST | END));
+        const int32_t tiles = u.tiles;
         const bool opens = u.t0 >= 0, whole = opens && u.t0 + tiles <= span;
         // the slot `slot` of each warp's ring, read by the step before and not filled again yet
         auto rows_of = [&](int w) {
@@ -913,22 +915,27 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
     };
 
     // ---- the loop
-    look_up(0);
+    look_up(true);
     for (int i = 0; i < C::NSTAGES - 1; ++i) {
         issue(i);
         cp_commit();
-        look_up(i + 1);
+        look_up(false);
     }
     __syncwarp();
     load_queries(s_step[warp][0]);
     scale_queries();
     clear();
     int slot = 0, fill = C::NSTAGES - 1;
+    int at_unit = 0;                     // unit being computed, and how many of its steps are left
+    auto left_of = [&](const Step &u) {                  // tiles of the unit that are the range's
+        return min(u.tiles + u.t0, span) - max(u.t0, 0);
+    };
+    int left = left_of(s_step[warp][0]);
 #pragma unroll 1
-    for (int k = 0;; ++k) {
+    for (;;) {
         issue(fill);                     // the slot the step before this one has left
         cp_commit();
-        look_up(k + C::NSTAGES);
+        look_up(false);
         fill = fill + 1 == C::NSTAGES ? 0 : fill + 1;
         cp_wait<C::NSTAGES - 1>();
         __syncwarp();
@@ -943,18 +950,20 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
                 far = ((mask >> (lane % STEP)) & 1) && (w & HIGH) != (HIGH & 0x70707070u);
                 far = __any_sync(0xFFFFFFFFu, far);
             }
-            if (far) step(slot, std::false_type{});
-            else step(slot, std::true_type{});
+            if (far) step(slot, mask, std::false_type{});
+            else step(slot, mask, std::true_type{});
         }
         __syncwarp();                           // every lane has read the slot
-        if (s_step[warp][k % STEPS].tiles & LAST) {
-            const Step done = s_step[warp][k % STEPS];
-            const bool more = !(done.tiles & END);
-            if (more) load_queries(s_step[warp][(k + 1) % STEPS]);   // in flight while the warps merge
+        if (--left == 0) {
+            const Step done = s_step[warp][at_unit % STEPS];
+            const bool more = done.t0 + done.tiles + C::EXTRA < span;
+            ++at_unit;
+            if (more) load_queries(s_step[warp][at_unit % STEPS]);   // in flight while the warps merge
             end_unit(done, slot);
             if (!more) break;
             scale_queries();
             clear();
+            left = left_of(s_step[warp][at_unit % STEPS]);
         }
         slot = slot + 1 == C::NSTAGES ? 0 : slot + 1;
     }
