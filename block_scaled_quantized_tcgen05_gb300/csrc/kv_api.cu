@@ -212,6 +212,17 @@ qgemm_status qgemm_create_kv_cache(qgemm_kv_cache **out, int32_t dtype, int64_t 
     if (page_size == 1) c->st[3] = e4m3 ? d : 2 * d;
     c->extent = extent;
     c->sextent = sextent;
+    auto unit_of = [&](const int64_t *s, int64_t least, int64_t *unit) {
+        int64_t bits = least << 16, last = 0;            // at most 2^16 of the least
+        for (int i = 1; i < 4; ++i) {
+            bits |= s[i];
+            last += (n[i] - 1) * s[i];
+        }
+        *unit = bits & -bits;
+        return last / *unit < (int64_t(1) << 32);
+    };
+    c->near = unit_of(st, 16, &c->unit);
+    c->near = unit_of(sst, 4, &c->sunit) && c->near;
     *out = c;
     return QGEMM_OK;
 }
@@ -351,6 +362,9 @@ qgemm_status qgemm_paged_attention(const void *Q, int64_t q_batch_stride, int64_
     if (!seqs && batch > max_seqs)
         return fail(QGEMM_ERR_INVALID_ARG, "batch %lld > %lld page-table rows", (long long)batch,
                     (long long)max_seqs);
+    if (!kv->near)
+        return fail(QGEMM_ERR_UNSUPPORTED_SHAPE, "a layer's rows lie 2^32 units (%lld bytes of rows, %lld of scales) apart",
+                    (long long)kv->unit, (long long)kv->sunit);
     QG_TRY(check_ints(lens, "lens"));
     if (!aligned(seqs, 4) || !aligned(lse, 4)) return fail(QGEMM_ERR_MISALIGNED, "seqs and lse must be 4-byte aligned");
     qgi::LaunchCtx ctx;

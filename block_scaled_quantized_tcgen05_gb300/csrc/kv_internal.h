@@ -18,6 +18,8 @@ struct qgemm_kv_cache {
     uint8_t *ks, *vs;      // null unless the data is E4M3
     int64_t sst[4];
     int64_t extent, sextent;   // bytes from a plane's base to the end of its last row
+    int64_t unit, sunit;       // the largest power of two in every page, head and token stride, bytes
+    bool near;                 // offsets of a layer's rows are fewer than 2^32 units
 };
 
 // Rotary frequencies: pair i of a head turns by freq[i] / 2^64 of a full turn per position.

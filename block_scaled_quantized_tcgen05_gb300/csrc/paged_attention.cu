@@ -67,15 +67,15 @@ struct AttnParams {
     int64_t qb, qh, ob, oh;                 // bytes
     uint8_t *o;
     float *lse;
-    int64_t page, head, token, spage, shead, stoken;
     int64_t extent, sextent;
     const int32_t *table, *lens, *seqs;
     int64_t table_stride;
     int32_t B, hq, hkv, group, chunks;      // chunks: units per key-value head
     int32_t max_seqs, max_pages, page_size, pages, window;
-    bool one_page;                          // page_size is a multiple of STEP, and offsets fit the units of the next
-    uint32_t page32, head32, token32;       // the strides in 16 bytes
-    uint32_t spage32, shead32, stoken32;    // and in 4 bytes
+    bool one_page;                          // page_size is a multiple of STEP
+    // The cache's strides in units that divide them all, in which a layer's offsets fit 32 bits
+    uint32_t unit, page, head, token;
+    uint32_t sunit, spage, shead, stoken;
     uint32_t page_magic, page_shift;        // of kvi::page_of
     float scale_log2;
     int32_t *counters;
@@ -513,64 +513,62 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
     // ---- the copies of the looked-up step into ring slot `slot`
     constexpr int RPI = 32 / C::CHUNKS;          // rows an instruction of the warp copies
     const int chunk = lane % C::CHUNKS, row0 = lane / C::CHUNKS;
-    const uint8_t *const lane_k = p.k + (row0 * p.token + chunk * 16), *const lane_v = p.v + (row0 * p.token + chunk * 16);
+    const uint8_t *const lane_k = p.k + chunk * 16, *const lane_v = p.v + chunk * 16;
+    const uint32_t lane_row = row0 * p.token;
     const uint32_t lane_to = row0 * C::ROWB + swizzle<C>(row0, chunk) * 16;
     // lanes 0-15: the keys' scale rows, lanes 16-31: the values'
-    const uint8_t *const lane_s = C::E4M3 ? (lane < STEP ? p.ks : p.vs) + lane % STEP * p.stoken : nullptr;
+    const uint8_t *const lane_s = lane < STEP ? p.ks : p.vs;
+    const uint32_t lane_srow = lane % STEP * p.stoken;
     auto issue = [&](int slot) {
         const int32_t pg = x.pg, pr = x.pr, ph = x.h;
-        if (p.one_page && x.hi - x.lo == STEP && pg >= 0 && pg < p.pages) {
+        const uint32_t kd = ring + slot * C::STAGEB;
+        const bool known = uint32_t(pg) < uint32_t(p.pages);
+        uint32_t at = pg * p.page + pr * p.token + ph * p.head;
+        const uint32_t sat = pg * p.spage + pr * p.stoken + ph * p.shead;
+        if (p.one_page && x.hi - x.lo == STEP && known) {
             // a whole step of one page: rows a token stride apart
-            const uint32_t kd = ring + slot * C::STAGEB;
-            uint32_t at = pg * p.page32 + pr * p.token32 + ph * p.head32;
-            if (QG_IN_BOUNDS(p.err, int64_t(at) * 16 + (STEP - 1) * p.token + C::ROWB <= p.extent)) {
+            if (QG_IN_BOUNDS(p.err, uint64_t(at + (STEP - 1) * p.token) * p.unit + C::ROWB <= uint64_t(p.extent))) {
+                at += lane_row;
 #pragma unroll
                 for (int i = 0; i < STEP / RPI; ++i) {
                     // swizzle(a + b, c) = swizzle(a, 0) ^ swizzle(b, c) for rows a and b without common bits
                     const uint32_t d = (kd + lane_to) ^ (swizzle<C>(i * RPI, 0) * 16);
-                    cp_async_16(d + i * RPI * C::ROWB, lane_k + uint64_t(at) * 16, 16);
-                    cp_async_16(d + i * RPI * C::ROWB + C::PLANE, lane_v + uint64_t(at) * 16, 16);
-                    at += RPI * p.token32;
+                    cp_async_16(d + i * RPI * C::ROWB, lane_k + uint64_t(at) * p.unit, 16);
+                    cp_async_16(d + i * RPI * C::ROWB + C::PLANE, lane_v + uint64_t(at) * p.unit, 16);
+                    at += RPI * p.token;
                 }
                 if (C::E4M3)
-                    cp_async_4(kd + 2 * C::PLANE + lane * 4,
-                               lane_s + uint64_t(pg * p.spage32 + pr * p.stoken32 + ph * p.shead32) * 4, 4);
+                    cp_async_4(kd + 2 * C::PLANE + lane * 4, lane_s + uint64_t(sat + lane_srow) * p.sunit, 4);
                 if (lane == 0) s_mask[warp][slot] = (1u << STEP) - 1;
                 return;
             }
         }
+        // lane l: row l's place
         bool ok = lane >= x.lo && lane < x.hi;
-        const uint32_t kd = ring + slot * C::STAGEB, vd = kd + C::PLANE;
-        int64_t off = 0, soff = 0;               // lane l: row l's place
-        if (ok) {
-            if (pg < 0 || pg >= p.pages) {
-                report_index(p.err);
-                ok = false;
-            } else {
-                const int32_t r = pr + (p.one_page ? lane : 0);
-                off = pg * p.page + r * p.token + ph * p.head;
-                if (C::E4M3) soff = pg * p.spage + r * p.stoken + ph * p.shead;
-                ok = QG_IN_BOUNDS(p.err, off >= 0 && off + C::ROWB <= p.extent);
-                if (!ok) off = soff = 0;
-            }
+        if (ok && !known) report_index(p.err);
+        ok = ok && known;
+        uint32_t srow = sat;
+        if (p.one_page) {
+            at += lane * p.token;
+            srow += lane_srow;
         }
+        ok = ok && QG_IN_BOUNDS(p.err, uint64_t(at) * p.unit + C::ROWB <= uint64_t(p.extent));
+        if (!ok) at = srow = 0;
         const uint32_t mask = __ballot_sync(0xFFFFFFFFu, ok);
         if (lane == 0) s_mask[warp][slot] = mask;
 #pragma unroll
         for (int i = 0; i < STEP / RPI; ++i) {
             const int r = i * RPI + row0;
-            const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r) + chunk * 16;
+            const uint64_t o = uint64_t(__shfl_sync(0xFFFFFFFFu, at, r)) * p.unit;
             const uint32_t n = (mask >> r) & 1 ? 16 : 0;
-            const uint32_t d = r * C::ROWB + swizzle<C>(r, chunk) * 16;
-            cp_async_16(kd + d, p.k + o, n);
-            cp_async_16(vd + d, p.v + o, n);
+            const uint32_t d = (kd + lane_to) ^ (swizzle<C>(i * RPI, 0) * 16);
+            cp_async_16(d + i * RPI * C::ROWB, lane_k + o, n);
+            cp_async_16(d + i * RPI * C::ROWB + C::PLANE, lane_v + o, n);
         }
         if (C::E4M3) {
-            // lanes 0-15: the keys' scale rows, lanes 16-31: the values'
             const int r = lane % STEP;
-            const int64_t o = __shfl_sync(0xFFFFFFFFu, soff, r);
-            const uint8_t *src = lane < STEP ? p.ks : p.vs;
-            cp_async_4(vd + C::PLANE + lane * 4, src + o, (mask >> r) & 1 ? 4 : 0);
+            const uint32_t so = __shfl_sync(0xFFFFFFFFu, srow, r);
+            cp_async_4(kd + 2 * C::PLANE + lane * 4, lane_s + uint64_t(so) * p.sunit, (mask >> r) & 1 ? 4 : 0);
         }
     };
 
@@ -1026,17 +1024,19 @@ cudaError_t launch_paged_attention(const PagedAttnArgs &a, const LaunchCtx &ctx)
     p.k = c->k + a.layer * c->st[0];
     p.v = c->v + a.layer * c->st[0];
     p.extent = c->extent - a.layer * c->st[0];
-    p.page = c->st[1];
-    p.head = c->st[2];
-    p.token = c->st[3];
+    p.unit = (uint32_t)c->unit;
+    p.page = (uint32_t)(c->st[1] / c->unit);
+    p.head = (uint32_t)(c->st[2] / c->unit);
+    p.token = (uint32_t)(c->st[3] / c->unit);
     const bool e4m3 = c->dtype == QGEMM_E4M3;
     if (e4m3) {
         p.ks = c->ks + a.layer * c->sst[0];
         p.vs = c->vs + a.layer * c->sst[0];
         p.sextent = c->sextent - a.layer * c->sst[0];
-        p.spage = c->sst[1];
-        p.shead = c->sst[2];
-        p.stoken = c->sst[3];
+        p.sunit = (uint32_t)c->sunit;
+        p.spage = (uint32_t)(c->sst[1] / c->sunit);
+        p.shead = (uint32_t)(c->sst[2] / c->sunit);
+        p.stoken = (uint32_t)(c->sst[3] / c->sunit);
     }
     p.table = a.table;
     p.lens = a.lens;
@@ -1058,15 +1058,7 @@ cudaError_t launch_paged_attention(const PagedAttnArgs &a, const LaunchCtx &ctx)
     p.slots = qg::slots_of(ctx.num_sms);
     p.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + qg::counters_bytes(ctx.num_sms));
     p.err = ctx.err;
-    p.one_page = c->page_size % qg::STEP == 0 && p.extent >> 36 == 0 && p.sextent >> 34 == 0;
-    if (p.one_page) {
-        p.page32 = (uint32_t)(p.page / 16);
-        p.head32 = (uint32_t)(p.head / 16);
-        p.token32 = (uint32_t)(p.token / 16);
-        p.spage32 = (uint32_t)(p.spage / 4);
-        p.shead32 = (uint32_t)(p.shead / 4);
-        p.stoken32 = (uint32_t)(p.stoken / 4);
-    }
+    p.one_page = c->page_size % qg::STEP == 0;
     kvi::page_divisor(p.page_size, &p.page_magic, &p.page_shift);
     // no more CTAs than tiles (and EXTRAs) the table rows can hold
     const int64_t most = units * (kvi::tiles_of(a.max_pages * (int32_t)c->page_size, qg::TILE) + 3);

@@ -493,6 +493,8 @@ qgemm_status qgemm_paged_attention_workspace_bytes(const qgemm_kv_cache *kv, int
  *              must be ZERO before its first call; every call leaves it ready for the next one on the
  *              same stream, of any batch, heads and cache whose workspace is no larger.  Calls that may
  *              overlap need workspaces of their own.
+ * The cache's rows of one layer lie fewer than 2^32 units apart, the unit the largest power of two that
+ * divides its page, head and token strides (rows at least, so any cache whose strides are multiples of rows).
  * Launch: one kernel of up to two CTAs per SM; the lengths are read on the device, so a captured call
  * serves any lengths.  Repeatable bit for bit for the same inputs and SM count.
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, UNSUPPORTED_DTYPE, MISALIGNED (nothing enqueued); CUDA. */

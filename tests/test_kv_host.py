@@ -149,6 +149,26 @@ def test_attention_refusals(lib, change, status):
     lib.qgemm_destroy_kv_cache(kv)
 
 
+@pytest.mark.parametrize("dtype,pages,page_bytes,scale_bytes,status", [
+    (q.F16, 1 << 21, 1 << 16, 0, CUDA),                    # 2^37 bytes in units of a row
+    (q.F16, 1 << 21, (1 << 15) + 16, 0, SHAPE),            # 2^36 in units of 16
+    (q.F16, (1 << 20) + 1, (1 << 15) + 16, 0, CUDA),       # and half of that
+    (q.E4M3, 1 << 21, 1 << 14, (1 << 13) + 4, SHAPE), (q.E4M3, 1 << 21, 1 << 14, 1 << 13, CUDA),
+])
+def test_attention_counts_offsets_in_units(lib, dtype, pages, page_bytes, scale_bytes, status):
+    if status == CUDA and torch.cuda.is_available():
+        pytest.skip("would launch")
+    row = 128 if dtype == q.E4M3 else 256
+    got, kv = _cache(lib, dtype=dtype, layers=1, pages=pages, st=(0, page_bytes, 16 * row, row), ks=A, vs=B_,
+                     sst=(0, scale_bytes, 64, 4)) if scale_bytes else \
+        _cache(lib, dtype=dtype, layers=1, pages=pages, st=(0, page_bytes, 16 * row, row))
+    assert got == 0, lib.qgemm_last_error_message()
+    got = lib.qgemm_paged_attention(P(A), 1024, 128, q.F16, 4, 8, kv, 0, P(A), 8, 4, 8, P(A), None, P(B_), 1024, 128,
+                                    None, 0.1, 0, P(A), 1 << 30, None)
+    assert got == status, lib.qgemm_last_error_message()
+    lib.qgemm_destroy_kv_cache(kv)
+
+
 @pytest.mark.parametrize("change,status", [
     (dict(), CUDA), (dict(n=0, x=0), 0), (dict(kv=0), INVALID), (dict(table=0), INVALID), (dict(ts=4), INVALID),
     (dict(ms=0), INVALID), (dict(mp=0), INVALID), (dict(lens=0), INVALID), (dict(refs=0), INVALID), (dict(x=0), INVALID),
