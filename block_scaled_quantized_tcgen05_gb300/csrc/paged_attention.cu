@@ -38,7 +38,7 @@
 // Precision: scores, softmax and sums in fp32.  P, times 2^15 so that the halves' range is used down to
 // 2^-39 of the largest weight, is split into two 16-bit values, hi = p rounded towards zero and lo = rn(p -
 // hi) (relative error 2^-21 in fp16, 2^-15 in bf16), and both are multiplied: the matrix unit has the time.
-// lo is kept above zero, at 2^-39 of the largest weight at least, so that an infinite value stays one (0 x
+// Both are kept above zero, at 2^-39 of the largest weight at least, so that an infinite value stays one (0 x
 // inf and inf - inf would be NaN).  E4M3
 // codes are exact in halves, and are multiplied as such; a key block's scale goes onto its part of the score
 // in fp32, and a value becomes the half code * 2^(byte - 127), exact, with P in halves too.  Where a step's scales
@@ -749,7 +749,9 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
                 const float a = ex2(s[n][2 * i] - m0), b = ex2(s[n][2 * i + 1] - m1);
                 l[n][0] += a;
                 l[n][1] += b;
-                const uint32_t h = PT::pack_down(a, b);
+                // halves of an E4M3 cache hold no infinity that a zero could meet
+                constexpr bool FINITE = C::E4M3 && FAST;
+                const uint32_t h = PT::pack_down(FINITE ? a : fmaxf(a, P_LEAST), FINITE ? b : fmaxf(b, P_LEAST));
                 const float2 f = PT::unpack(h);
                 const uint32_t r = PT::pack(fmaxf(a - f.x, P_LEAST), fmaxf(b - f.y, P_LEAST));
                 hi[n][i] = transpose8(C::PACKED && c4 >= 2 ? r : h);

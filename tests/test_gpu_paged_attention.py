@@ -239,6 +239,20 @@ def test_special_values_reach_the_output(dev):
             assert bool((o[0, 2:, 7] == float("inf")).all())
 
 
+def test_infinite_value_of_a_small_weight(dev):
+    """A weight far below what 16 bits hold is still not zero: times infinity it is infinity."""
+    for dtype in (torch.float16, torch.bfloat16):
+        p = Problem(dev, [100], 1, 1, 128, 16, dtype, False, seed=21)
+        p.k[1, p.table[0, 0], 0, 0] = (4 * p.q[0, 0].float()).to(dtype)      # e^45 times the others' weights
+        pg, off = int(p.table[0, 3]), 2                                # token 50
+        p.v[1, pg, 0, off, 7], p.v[1, pg, 0, off, 9] = float("inf"), float("-inf")
+        o, l = p.run()
+        _clean()
+        o = o.cpu().float()[0, 0]
+        assert o[7] == float("inf") and o[9] == float("-inf")
+        assert bool(l.isfinite().all()) and int((~o.isfinite()).sum()) == 2
+
+
 def test_every_scale_byte(dev):
     """UE8M0 bytes far outside the halves: values are the nearest half (bfloat16) to the product, infinity
     where it overflows."""
