@@ -39,11 +39,10 @@
 // 2^-39 of the largest weight, is split into two 16-bit values, hi = p rounded towards zero and lo = rn(p -
 // hi) (relative error 2^-21 in fp16, 2^-15 in bf16), and both are multiplied: the matrix unit has the time.
 // Both are kept above zero, at 2^-39 of the largest weight at least, so that an infinite value stays one (0 x
-// inf and inf - inf would be NaN).  E4M3
-// codes are exact in halves, and are multiplied as such; a key block's scale goes onto its part of the score
-// in fp32, and a value becomes the half code * 2^(byte - 127), exact, with P in halves too.  Where a step's scales
+// inf and inf - inf would be NaN).  E4M3 codes are exact in halves, and are multiplied as such; a key block's
+// scale goes onto its part of the score in fp32, and a value becomes the half code * 2^(byte - 127), exact, with P in halves too.  Where a step's scales
 // are not halves, values become the nearest 16-bit value of the activations' type, with P in that type.  (bf16
-// queries, 128 ragged E4M3 sequences: 134 us; codes brought to bf16 by way of fp32 170.)
+// queries, 128 ragged E4M3 sequences: 131 us; codes brought to bf16 by way of fp32 170.)
 #include <atomic>
 #include <type_traits>
 
@@ -102,7 +101,8 @@ struct Cfg {
     static constexpr int SCALEB = E4M3 ? STEP * 4 : 0;   // scale bytes of a step's keys
     static constexpr int STAGEB = 2 * (PLANE + SCALEB);
     // Two CTAs an SM where their registers (8 heads) and three stages each fit; otherwise one
-    // (128 ragged E4M3 sequences: 135 us, with one 165)
+    // (128 ragged E4M3 sequences: 128 us, with one 154; with 16 heads of 64
+    // two gain 9 % at many sequences, 35 -> 31 us, and lose as much where few are cut into twice the parts)
     static constexpr bool TWO = NH == 1 && STAGEB <= 4224;
     // heads merged at a time, through the slot of the ring each warp has just read
     static constexpr int MERGE_ROWS = NH == 2 && STAGEB >= 16 * D * 4 ? 16 : 8;
@@ -112,7 +112,7 @@ struct Cfg {
     static constexpr int NSTAGES = FIT > 6 ? 6 : FIT;
     static constexpr int SMEM = 256 + NWARPS * NSTAGES * STAGEB;
     // What a unit costs beyond its tiles, in tiles (measured, 128 ragged E4M3 sequences: 1 / 2 / 3 extra
-    // 138 / 135 / 138 us; 64 ragged fp16 ones 0 / 1 / 2: 134 / 118 / 118)
+    // 132 / 128 / 131 us; 64 ragged fp16 ones 0 / 1 / 2: 123 / 118 / 119)
     static constexpr int EXTRA = ROWB <= 128 ? 2 : 1;
     static constexpr int MT = D / 16;                    // 16-element tiles of the output
     static constexpr int PARTIAL = ROWS * (D + 2);       // floats of a partial
@@ -474,8 +474,8 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
 
     // ---- page look-up of this warp's tokens of the tile `load` points at, one step ahead of the
     // copies that use it.  Steps begin at multiples of 16 tokens: with pages of a multiple of 16 tokens
-    // a step lies in one page, and every lane holds its entry; otherwise lane l holds token l's (147 us
-    // instead of 135 for the ragged E4M3 sequences, 119 instead of 118 for the fp16 ones).
+    // a step lies in one page, and every lane holds its entry; otherwise lane l holds token l's (136 us
+    // instead of 128 for the ragged E4M3 sequences, 118.4 instead of 117.6 for the fp16 ones).
     struct {
         int32_t pg = -1, pr = 0;         // page-table entry and row inside the page
         int32_t lo = 0, hi = 0;          // rows of the step that are tokens of the range
@@ -824,8 +824,8 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
     };
 
     // ---- end of the tiles this CTA has of a unit: the warps' rows are merged, through the ring's slots
-    // that were just read (with a buffer of its own, 2 heads at a time beside two CTAs' rings: 152 us for
-    // the 128 ragged E4M3 sequences, 135 so); a whole unit is written out, a part goes to the workspace
+    // that were just read (a buffer of its own leaves room for 2 heads at a time beside two CTAs' rings: the
+    // 128 ragged E4M3 sequences took 12 % longer); a whole unit is written out, a part goes to the workspace
     auto end_unit = [&](const Step &u, int slot) {
         const int32_t tiles = u.tiles;
         const bool opens = u.t0 >= 0, whole = opens && u.t0 + tiles <= span;
@@ -944,7 +944,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
             bool far = false;
             if (C::E4M3) {
                 // FAST scales: bytes 112 .. 127 (2^-15 .. 1: blocks of the append up to 512), halves all.
-                // Others take the step through fp32 (all steps so: 175 us instead of 135).
+                // Others take the step through fp32 (all steps so: 169 us instead of 128).
                 constexpr uint32_t HIGH = C::D == 128 ? 0xF0F0F0F0u : 0xF0F0u;
                 const uint32_t w = lds32(ring + slot * C::STAGEB + 2 * C::PLANE + lane * 4);
                 far = ((mask >> (lane % STEP)) & 1) && (w & HIGH) != (HIGH & 0x70707070u);
