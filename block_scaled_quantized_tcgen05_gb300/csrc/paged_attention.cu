@@ -40,9 +40,10 @@
 // hi) (relative error 2^-21 in fp16, 2^-15 in bf16), and both are multiplied: the matrix unit has the time.
 // Both are kept above zero, at 2^-39 of the largest weight at least, so that an infinite value stays one (0 x
 // inf and inf - inf would be NaN).  E4M3 codes are exact in halves, and are multiplied as such; a key block's
-// scale goes onto its part of the score in fp32, and a value becomes the half code * 2^(byte - 127), exact, with P in halves too.  Where a step's scales
-// are not halves, values become the nearest 16-bit value of the activations' type, with P in that type.  (bf16
-// queries, 128 ragged E4M3 sequences: 131 us; codes brought to bf16 by way of fp32 170.)
+// scale goes onto its part of the score in fp32, and a value becomes the half code * 2^(byte - 127), exact, with
+// P in halves too.  Where a step's scales are not halves, values become the nearest 16-bit value of the
+// activations' type, with P in that type.  (bf16 queries, 128 ragged E4M3 sequences: 131 us; codes brought to bf16 by
+// way of fp32 170.)
 #include <atomic>
 #include <type_traits>
 
