@@ -38,8 +38,9 @@
 // Precision: scores, softmax and sums in fp32.  P, times 2^15 so that the halves' range is used down to
 // 2^-39 of the largest weight, is split into two 16-bit values, hi = p rounded towards zero and lo = rn(p -
 // hi) (relative error 2^-21 in fp16, 2^-15 in bf16), and both are multiplied: the matrix unit has the time.
-// Both are kept above zero, at 2^-39 of the largest weight at least, so that an infinite value stays one (0 x
-// inf and inf - inf would be NaN).  E4M3 codes are exact in halves, and are multiplied as such; a key block's
+// Both are kept above zero, at the type's smallest value that no unit flushes, so that an infinite value stays one
+// (0 x inf and inf - inf would be NaN): 2^-39 of the largest weight in fp16, whose values reach 65504 (an error of
+// 2.4e-7 a token), 2^-141 in bf16, whose values have fp32's range (2^-39 of 1e12 would be 1.8).  E4M3 codes are exact in halves, and are multiplied as such; a key block's
 // scale goes onto its part of the score in fp32, and a value becomes the half code * 2^(byte - 127), exact, with
 // P in halves too.  Where a step's scales are not halves, values become the nearest 16-bit value of the
 // activations' type, with P in that type.  (bf16 queries, 128 ragged E4M3 sequences: 131 us; codes brought to bf16 by
@@ -58,7 +59,6 @@ constexpr int ROWS = 16;                    // query heads of a unit at most
 constexpr int STEP = 16;                    // tokens of a warp's step (the scores' M)
 constexpr int TILE = STEP * NWARPS;
 constexpr float P_SHIFT = 15.0f;            // P is held times 2^P_SHIFT
-constexpr float P_LEAST = 0x1p-24f;         // the smallest half
 constexpr float LN2 = 0.69314718055994531f;
 constexpr float LOG2E = 1.4426950408889634f;
 
@@ -752,9 +752,12 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
                 l[n][1] += b;
                 // halves of an E4M3 cache hold no infinity that a zero could meet
                 constexpr bool FINITE = C::E4M3 && FAST;
-                const uint32_t h = PT::pack_down(FINITE ? a : fmaxf(a, P_LEAST), FINITE ? b : fmaxf(b, P_LEAST));
+                auto positive = [](float x) {
+                    return FINITE ? x : fmaxf(x, PT::BF16 ? 0x1p-126f : 0x1p-24f);
+                };
+                const uint32_t h = PT::pack_down(positive(a), positive(b));
                 const float2 f = PT::unpack(h);
-                const uint32_t r = PT::pack(fmaxf(a - f.x, P_LEAST), fmaxf(b - f.y, P_LEAST));
+                const uint32_t r = PT::pack(positive(a - f.x), positive(b - f.y));
                 hi[n][i] = transpose8(C::PACKED && c4 >= 2 ? r : h);
                 if (!C::PACKED) lo[n][i] = transpose8(r);
             }
