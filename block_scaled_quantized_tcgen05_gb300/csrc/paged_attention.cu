@@ -35,12 +35,14 @@
 // zero-filled and their scores -inf, so whatever the pages hold there (NaN of an earlier owner) stays
 // out.
 //
-// Precision: scores, softmax and sums in fp32.  P, times 2^15 so that the halves' range is used down to
-// 2^-39 of the largest weight, is split into two 16-bit values, hi = p rounded towards zero and lo = rn(p -
+// Precision: scores, softmax and sums in fp32.  P is split into two 16-bit values, hi = p rounded towards zero and lo = rn(p -
 // hi) (relative error 2^-21 in fp16, 2^-15 in bf16), and both are multiplied: the matrix unit has the time.
 // Both are kept above zero, at the type's smallest value that no unit flushes, so that an infinite value stays one
-// (0 x inf and inf - inf would be NaN): 2^-39 of the largest weight in fp16, whose values reach 65504 (an error of
-// 2.4e-7 a token), 2^-141 in bf16, whose values have fp32's range (2^-39 of 1e12 would be 1.8).  E4M3 codes are exact in halves, and are multiplied as such; a key block's
+// (0 x inf and inf - inf would be NaN).  Halves of P are times 2^15, so that their range is used down to 2^-39 of
+// the largest weight (values reach 65504: an error of 2.4e-7 a token).  bf16 has fp32's range, and so have its
+// values: a floor of 2^-39 would make 1.8 of a vanishing weight's 1e12, and a factor of 2^15 would take the sum past
+// fp32's end from values of 1e34 on, so P is as it is there and its floor 2^-126.  An E4M3 cache with bf16 queries
+// has both kinds of step on one accumulator: times 2^15 until a value's scale is above 2^60, then as it is.  E4M3 codes are exact in halves, and are multiplied as such; a key block's
 // scale goes onto its part of the score in fp32, and a value becomes the half code * 2^(byte - 127), exact, with
 // P in halves too.  Where a step's scales are not halves, values become the nearest 16-bit value of the
 // activations' type, with P in that type.  (bf16 queries, 128 ragged E4M3 sequences: 131 us; codes brought to bf16 by
@@ -58,7 +60,8 @@ constexpr int THREADS = 32 * NWARPS;
 constexpr int ROWS = 16;                    // query heads of a unit at most
 constexpr int STEP = 16;                    // tokens of a warp's step (the scores' M)
 constexpr int TILE = STEP * NWARPS;
-constexpr float P_SHIFT = 15.0f;            // P is held times 2^P_SHIFT
+constexpr float HALF_SHIFT = 15.0f;         // halves of P are times 2^HALF_SHIFT
+constexpr uint32_t WIDE = 127 + 60;         // the largest value scale that this factor's sums take
 constexpr float LN2 = 0.69314718055994531f;
 constexpr float LOG2E = 1.4426950408889634f;
 
@@ -96,6 +99,7 @@ struct Cfg {
     // 16-bit caches are bound by HBM either way)
     static constexpr bool PACKED = HEADS == 4;
     static constexpr bool SCALED = E4M3 && TY::BF16;     // bf16 queries go into products of halves
+    static constexpr float SHIFT = TY::BF16 && !E4M3 ? 0.0f : HALF_SHIFT;    // P is times 2^SHIFT
     static constexpr int ROWB = E4M3 ? D : 2 * D;        // bytes of a cached row
     static constexpr int CHUNKS = ROWB / 16;             // 16-byte pieces of a row
     static constexpr int PLANE = STEP * ROWB;            // bytes of a step's keys (or values)
@@ -578,6 +582,13 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
     float acc[C::NH][C::MT][4];             // rows of d, columns of heads 2 c4, 2 c4 + 1
     float m[C::NH][2], l[C::NH][2];
     float qs[C::NH][2];                     // SCALED: what the scores of heads 2 c4, 2 c4 + 1 are still to be times
+    // E4M3.  FAST scales: bytes 112 .. 127 (2^-15 .. 1: blocks of the append up to 512), halves all.  Others take the
+    // step through fp32 (all steps so: 169 us instead of 128).
+    [[maybe_unused]] constexpr uint32_t HIGH = C::D == 128 ? 0xF0F0F0F0u : 0xF0F0u, FAST_SCALES = HIGH & 0x70707070u;
+    // SCALED: what the scales' high bits have to be; nothing is, once the unit has met a value scale above WIDE and its
+    // sums hold P as it is (kept as a flag beside the test of the scales it took every step 2 - 5 % longer)
+    [[maybe_unused]] uint32_t fast_scales = FAST_SCALES;
+    auto wide = [&] { return C::SCALED && fast_scales != FAST_SCALES; };
     auto load_queries = [&](const Step &u) {
         const int h = u.hp / p.chunks, part = u.hp - h * p.chunks;
         const int h0 = h * p.group + part * ROWS, rows = min(ROWS, p.group - part * ROWS);
@@ -634,6 +645,22 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
             m[n][0] = m[n][1] = -INFINITY;
             l[n][0] = l[n][1] = 0.0f;
         }
+        fast_scales = FAST_SCALES;
+    };
+    // the sums so far without their 2^HALF_SHIFT, exactly
+    auto widen = [&] {
+        fast_scales = ~0u;
+#pragma unroll
+        for (int n = 0; n < C::NH; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                l[n][i] *= 0x1p-15f;
+#pragma unroll
+                for (int j = 0; j < C::MT; ++j) {
+                    acc[n][j][i] *= 0x1p-15f;
+                    acc[n][j][i + 2] *= 0x1p-15f;
+                }
+            }
     };
 
     // Places of this lane's fragments in a step's keys and values: the first piece; the others follow by
@@ -743,8 +770,9 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
         uint32_t hi[C::NH][2], lo[C::NH][2];
 #pragma unroll
         for (int n = 0; n < C::NH; ++n) {
-            const float m0 = m[n][0] == -INFINITY ? 0.0f : m[n][0] - P_SHIFT;
-            const float m1 = m[n][1] == -INFINITY ? 0.0f : m[n][1] - P_SHIFT;
+            const float shift = !FAST && wide() ? 0.0f : C::SHIFT;
+            const float m0 = m[n][0] == -INFINITY ? 0.0f : m[n][0] - shift;
+            const float m1 = m[n][1] == -INFINITY ? 0.0f : m[n][1] - shift;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float a = ex2(s[n][2 * i] - m0), b = ex2(s[n][2 * i + 1] - m1);
@@ -847,7 +875,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
                 l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, l[n][i], 8);
                 l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, l[n][i], 16);
                 if (g == 0) {
-                    s_m[warp][8 * n + 2 * c4 + i] = m[n][i] - P_SHIFT;     // the sums are times 2^P_SHIFT
+                    s_m[warp][8 * n + 2 * c4 + i] = m[n][i] - (wide() ? 0.0f : C::SHIFT);    // what the sums are times
                     s_l[warp][8 * n + 2 * c4 + i] = l[n][i];
                 }
             }
@@ -947,15 +975,22 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
         if (mask != 0) {
             bool far = false;
             if (C::E4M3) {
-                // FAST scales: bytes 112 .. 127 (2^-15 .. 1: blocks of the append up to 512), halves all.
-                // Others take the step through fp32 (all steps so: 169 us instead of 128).
-                constexpr uint32_t HIGH = C::D == 128 ? 0xF0F0F0F0u : 0xF0F0u;
                 const uint32_t w = lds32(ring + slot * C::STAGEB + 2 * C::PLANE + lane * 4);
-                far = ((mask >> (lane % STEP)) & 1) && (w & HIGH) != (HIGH & 0x70707070u);
+                far = ((mask >> (lane % STEP)) & 1) && (w & HIGH) != (C::SCALED ? fast_scales : FAST_SCALES);
                 far = __any_sync(0xFFFFFFFFu, far);
             }
-            if (far) step(slot, mask, std::false_type{});
-            else step(slot, mask, std::true_type{});
+            if (far) {
+                if constexpr (C::SCALED) {
+                    if (!wide()) {                      // lanes 16-31: the values' scales, 0 for masked rows
+                        const uint32_t w = lds32(ring + slot * C::STAGEB + 2 * C::PLANE + lane * 4);
+                        const uint32_t over = __vcmpgtu4(C::D == 128 ? w : w & 0xFFFFu, WIDE * 0x01010101u);
+                        if (__any_sync(0xFFFFFFFFu, lane >= STEP && over != 0)) widen();
+                    }
+                }
+                step(slot, mask, std::false_type{});
+            } else {
+                step(slot, mask, std::true_type{});
+            }
         }
         __syncwarp();                           // every lane has read the slot
         if (--left == 0) {

@@ -1,4 +1,5 @@
-"""Single-token attention with bf16 values over the type's whole range: large values of vanishing weight.
+"""Single-token attention with bf16 values over the type's whole range: large values of vanishing weight, and values
+near its end.
 
 Tolerances, beside the output's own rounding (HALF) and that of the scores (kv_reference.attend_tolerance's): a weight
 is held to 2^-15 of itself and 2^-125 of the largest one, which in bf16 is far below what any value makes visible;
@@ -84,6 +85,37 @@ def test_a_large_value_of_vanishing_weight(dev, e4m3, d, hq, hkv, at, batch):  #
         v = p.seen[0][1][it].to(BF16)
         v[..., 7], v[..., 9], v[..., 40] = 1e12, -1e9, 1e30
         set_rows(p, 0, it, "v", v)
+    o, l = p.run()
+    _clean()
+    check(p, o, l)
+
+
+@pytest.mark.parametrize("d,hq,hkv", HEADS)
+def test_values_near_the_end_of_the_range(dev, d, hq, hkv):  # noqa: F811
+    """One token of 1e35 gives 1e35, and the mean of hundreds of them is one."""
+    p = Problem(dev, [1, 300, 40, 700], hq, hkv, d, 16, BF16, False, seed=31)
+    g = torch.Generator().manual_seed(d)
+    for b, n in enumerate(p.lens):
+        v = (1e35 * (0.5 + torch.rand(n, hkv, d, generator=g)) * (torch.randint(0, 2, (n, hkv, 1), generator=g) * 2 - 1)).to(BF16)
+        set_rows(p, b, torch.arange(n), "v", v)
+    o, l = p.run()
+    _clean()
+    check(p, o, l)
+
+
+@pytest.mark.parametrize("d,hq,hkv", HEADS)
+def test_value_scales_near_the_end_of_the_range(dev, d, hq, hkv):  # noqa: F811
+    """E4M3 values of up to 5e36 in one block of a few tokens, among others of ordinary size: every element is right, those
+    of the other blocks too, with the large tokens before, between and after the others and in part of a cut sequence."""
+    p = Problem(dev, [1, 300, 20, 6000, 129], hq, hkv, d, 16, BF16, True, seed=32)
+    g = torch.Generator().manual_seed(d + 1)
+    for b, big in enumerate([[0], [3, 20, 131, 132, 260], [19], [0, 1500, 1501, 5999], [128]]):
+        t = torch.tensor(big)
+        codes = p.v[1, place(p, b, t)[0], :, place(p, b, t)[1]].clone()
+        codes[(codes & 0x78) == 0x78] = 0x30                         # below 256
+        s = torch.full((len(big), hkv, 4), 120, dtype=torch.uint8)
+        s[..., 1] = torch.randint(225, 242, (len(big), hkv), generator=g, dtype=torch.uint8)
+        set_codes(p, b, t, "v", codes, s)
     o, l = p.run()
     _clean()
     check(p, o, l)
