@@ -223,14 +223,21 @@ __global__ void __launch_bounds__(META_THREADS, 1)
             const int32_t tail = x.now % m.page_size;
             if (tail) {
                 const int32_t last = m.table[x.seq * m.table_stride + x.now / m.page_size];
-                if (good_page(m, last) && __ldcg(m.refs + last) > 1) {
+                if (!good_page(m, last)) {
+                    report_index(m.err);
+                } else if (__ldcg(m.refs + last) > 1) {
                     need.copy = tail;
                     need.pages += 1;
                 }
             }
         } else {
-            need.copy = x.want % m.page_size;
-            need.pages = need.copy > 0;
+            // a bad last entry is taken over below as the whole pages' are: a page of the child's own in its place
+            // would show what that page held before
+            const int32_t tail = x.want % m.page_size;
+            if (tail && good_page(m, m.table[x.from * m.table_stride + x.want / m.page_size])) {
+                need.copy = tail;
+                need.pages = 1;
+            }
         }
         return need;
     };
@@ -286,8 +293,9 @@ __global__ void __launch_bounds__(META_THREADS, 1)
         } else {
             const int32_t *from = m.table + x.from * m.table_stride;
             const int32_t full = x.want / m.page_size;
+            const int32_t shared = need.copy > 0 ? full : kvi::pages_of(x.want, m.page_size);
             if (need.copy > 0) src = from[full];
-            for (int j = lane; j < full; j += 32) {
+            for (int j = lane; j < shared; j += 32) {
                 const int32_t page = from[j];
                 row[j] = page;
                 if (good_page(m, page)) atomicAdd(m.refs + page, 1);

@@ -521,8 +521,8 @@ qgemm_status qgemm_kv_resize(const qgemm_kv_cache *kv, int32_t *page_table, int6
 
 /* Make sequence children[i] a copy of parents[i], i < n, in every layer: what the child's slot held
  * is given back, whole pages are shared (their counts rise), a partly filled last page is copied to a free
- * one (lowest first, in the order of the items).  A child whose page cannot be had is left empty and bit 128
- * of the device error word is set.  Children must differ from one another and from every parent; a
+ * one (lowest first, in the order of the items).  An entry that names no page is taken over as it is, the last
+ * one too.  A child whose page cannot be had is left empty and bit 128 of the device error word is set.  Children must differ from one another and from every parent; a
  * parent may appear several times.  Errors: as qgemm_kv_resize. */
 qgemm_status qgemm_kv_fork(const qgemm_kv_cache *kv, int32_t *page_table, int64_t table_stride,
                            int64_t max_seqs, int64_t max_pages, int32_t *lens, int32_t *refs,
