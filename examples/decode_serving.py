@@ -77,6 +77,12 @@ def plain_attention(queries, keys, values):
     return torch.einsum("hgt,thd->hgd", torch.softmax(s, -1), values).reshape(HQ, D)
 
 
+def in_front(refs):
+    """Whether the pages in use are the first ones."""
+    used = int((refs > 0).sum())
+    return bool((refs[:used] > 0).all())
+
+
 def main(steps=24, say=print):
     dev = torch.device("cuda:0")
     torch.manual_seed(0)
@@ -110,13 +116,17 @@ def main(steps=24, say=print):
             live += [3, 4]
         if t == steps // 2:                                     # one ends; its pages are taken together
             q.qgemm_kv_resize(m.kv, m.table, m.lens, m.refs, ints([2]))
+            if in_front(m.refs):
+                raise RuntimeError("the sequence that ended left no holes")
             q.qgemm_kv_compact(m.kv, m.table, m.lens, m.refs)
+            if not in_front(m.refs):
+                raise RuntimeError("the cache is not compact")
             live.remove(2)
         _, outs = run(live)
     if (word := q.qgemm_poll_device_error()) != 0:
         raise RuntimeError(f"device error word {word:#x}")
     used = int((m.refs > 0).sum())
-    if int((m.refs[:used] > 0).sum()) < used - len(live):
+    if not in_front(m.refs):                                    # free pages are taken lowest first
         raise RuntimeError("the cache is not compact")
 
     # an E4M3 value is off by 2^-4 of itself at most (and 2^-10 of its block's unit): scores by that of |q| |k|,
