@@ -40,6 +40,16 @@ KV_HD int32_t page_of(uint32_t t, uint32_t magic, uint32_t shift) {
     return (int32_t)(((uint64_t)t * magic) >> shift);
 }
 
+// Whether row `row` of page `page`, head `head`, its strides and offset counted in units of `unit` bytes, ends inside
+// `extent` bytes and its offset fits the 32 bits a kernel forms it in.  64-bit arithmetic: a sum that wraps fails.
+KV_HD bool row_inside(uint32_t page, uint32_t page_stride, uint32_t row, uint32_t row_stride, uint32_t head,
+                      uint32_t head_stride, uint32_t unit, uint32_t bytes, int64_t extent) {
+    const uint64_t last = 0xFFFFFFFFu;
+    const uint64_t p = (uint64_t)page * page_stride, r = (uint64_t)row * row_stride, h = (uint64_t)head * head_stride;
+    if (p > last || r > last || h > last || p + r + h > last) return false;
+    return (p + r + h) * unit + bytes <= (uint64_t)extent;
+}
+
 // Pages that hold n tokens.
 KV_HD int32_t pages_of(int32_t n, int32_t page_size) { return n > 0 ? (n - 1) / page_size + 1 : 0; }
 

@@ -436,8 +436,10 @@ __global__ void __launch_bounds__(COPY_THREADS, 2)
 #pragma unroll
         for (int k = 0; k < PIECES / 32; ++k)
             if (lane + 32 * k < pieces) *reinterpret_cast<uint4 *>(to + first + k * step * pl.token) = v[k];
-        if (pl.scaled) {
-            const int64_t sat = layer * pl.slayer + head * pl.shead + t0 * pl.stoken;
+        const int64_t sat = layer * pl.slayer + head * pl.shead + t0 * pl.stoken;
+        [[maybe_unused]] const int64_t slast = sat + (tokens - 1) * pl.stoken + 4;
+        if (pl.scaled && QG_IN_BOUNDS(err, sat >= 0 && slast + src * pl.spage <= pl.sextent &&
+                                               slast + dst * pl.spage <= pl.sextent)) {
             const uint8_t *sf = pl.base[2 + plane] + sat + src * pl.spage;
             uint8_t *st = pl.base[2 + plane] + sat + dst * pl.spage;
             for (int t = lane; t < tokens; t += 32)      // a row's 4 bytes of scales (d <= 128)

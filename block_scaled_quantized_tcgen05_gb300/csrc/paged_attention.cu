@@ -524,6 +524,10 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
     // lanes 0-15: the keys' scale rows, lanes 16-31: the values'
     const uint8_t *const lane_s = lane < STEP ? p.ks : p.vs;
     const uint32_t lane_srow = lane % STEP * p.stoken;
+    [[maybe_unused]] auto inside = [&](int32_t pg, int32_t row, int32_t h) {      // the planes, for the debug checks
+        return kvi::row_inside(pg, p.page, row, p.token, h, p.head, p.unit, C::ROWB, p.extent) &&
+               (!C::E4M3 || kvi::row_inside(pg, p.spage, row, p.stoken, h, p.shead, p.sunit, 4, p.sextent));
+    };
     auto issue = [&](int slot) {
         const int32_t pg = x.pg, pr = x.pr, ph = x.h;
         const uint32_t kd = ring + slot * C::STAGEB;
@@ -532,7 +536,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
         const uint32_t sat = pg * p.spage + pr * p.stoken + ph * p.shead;
         if (p.one_page && x.hi - x.lo == STEP && known) {
             // a whole step of one page: rows a token stride apart
-            if (QG_IN_BOUNDS(p.err, uint64_t(at + (STEP - 1) * p.token) * p.unit + C::ROWB <= uint64_t(p.extent))) {
+            if (QG_IN_BOUNDS(p.err, inside(pg, pr + STEP - 1, ph))) {
                 at += lane_row;
 #pragma unroll
                 for (int i = 0; i < STEP / RPI; ++i) {
@@ -557,7 +561,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
             at += lane * p.token;
             srow += lane_srow;
         }
-        ok = ok && QG_IN_BOUNDS(p.err, uint64_t(at) * p.unit + C::ROWB <= uint64_t(p.extent));
+        ok = ok && QG_IN_BOUNDS(p.err, inside(pg, pr + (p.one_page ? lane : 0), ph));
         if (!ok) at = srow = 0;
         const uint32_t mask = __ballot_sync(0xFFFFFFFFu, ok);
         if (lane == 0) s_mask[warp][slot] = mask;
