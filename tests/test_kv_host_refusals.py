@@ -1,0 +1,23 @@
+"""Further refusals of the decode-serving calls on the host (no GPU)."""
+import pytest
+
+from tests.test_kv_host import A, B_, CUDA, INVALID, P, SHAPE, _cache, _rope, lib  # noqa: F401
+
+
+@pytest.mark.parametrize("max_pages", [1 << 60, (1 << 60) + 8, (1 << 62) + 1, (1 << 63) - 1, 1 << 31, (1 << 32) + 8])
+def test_page_tables_of_any_size_are_counted(lib, max_pages):  # noqa: F811
+    """Pages of 16 tokens: entries whose tokens pass 2^63 are refused like those that pass 2^31."""
+    _, kv = _cache(lib)
+    rope = _rope(lib)
+    for max_seqs in (1, 4):
+        table = (P(A), max_pages, max_seqs, max_pages)
+        assert lib.qgemm_kv_append(kv, 0, P(A), 512, 128, P(B_), 512, 128, 0, 4, P(A), P(A), *table, rope, None, 0, 0, 0,
+                                   None, 0, 0, None) == SHAPE
+        assert lib.qgemm_paged_attention(P(A), 1024, 128, 0, 1, 8, kv, 0, *table, P(A), None, P(B_), 1024, 128, None, 0.1, 0,
+                                         P(A), 1 << 30, None) == SHAPE
+        meta = (kv, *table, P(A), P(A))
+        assert lib.qgemm_kv_resize(*meta, P(A), P(A), 2, None) == SHAPE
+        assert lib.qgemm_kv_fork(*meta, P(A), P(A), 2, None) == SHAPE
+        assert lib.qgemm_kv_compact(*meta, None) == SHAPE
+    lib.qgemm_destroy_kv_cache(kv)
+    lib.qgemm_destroy_rope(rope)
