@@ -113,7 +113,7 @@ qgemm_status qgemm_create_rope(qgemm_rotation **out, int64_t rot_dim, int32_t in
     if (interleaved != 0 && interleaved != 1)
         return fail(QGEMM_ERR_INVALID_ARG, "interleaved must be 0 or 1");
     if (!(base > 0) || !std::isfinite(base)) return fail(QGEMM_ERR_INVALID_ARG, "base must be finite and > 0");
-    if (!std::isfinite(mscale)) return fail(QGEMM_ERR_INVALID_ARG, "mscale must be finite");
+    if (!std::isfinite((float)mscale)) return fail(QGEMM_ERR_INVALID_ARG, "mscale must be finite in fp32");
     if (scaling < QGEMM_ROPE_PLAIN || scaling > QGEMM_ROPE_BY_PARTS)
         return fail(QGEMM_ERR_INVALID_ARG, "unknown scaling %d", scaling);
     if (scaling != QGEMM_ROPE_PLAIN && (!(factor > 0) || !std::isfinite(factor)))
@@ -135,6 +135,10 @@ qgemm_status qgemm_create_rope(qgemm_rotation **out, int64_t rot_dim, int32_t in
             double keep = (original_len * w / two_pi - low_turns) / (high_turns - low_turns);
             keep = keep < 0 ? 0 : (keep > 1 ? 1 : keep);
             w *= keep + (1 - keep) / factor;
+        }
+        if (!std::isfinite(w)) {
+            delete r;
+            return fail(QGEMM_ERR_INVALID_ARG, "the frequency of pair %lld is not finite", (long long)i);
         }
         // the fraction of a turn as 64 bits; whole turns of a position do not show
         const double turn = w / two_pi, frac = turn - std::floor(turn);

@@ -410,7 +410,7 @@ enum {
  *   interleaved  1: pairs (2i, 2i + 1); 0: pairs (i, i + rot_dim / 2).
  *   base         > 0.  scaling: QGEMM_ROPE_*; factor > 0 unless plain; original_len > 0 and
  *                high_turns > low_turns by parts.
- *   mscale       factor on the rotated elements (1: none).
+ *   mscale       factor on the rotated elements (1: none), finite in fp32; so are the frequencies in 64 bits.
  * Frequencies are 64-bit fractions of a turn, so angles are exact at any 32-bit position.
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE (rot_dim > 256). */
 qgemm_status qgemm_create_rope(qgemm_rotation **out, int64_t rot_dim, int32_t interleaved, double base,

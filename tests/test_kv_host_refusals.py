@@ -1,4 +1,6 @@
 """Further refusals of the decode-serving calls on the host (no GPU)."""
+import ctypes
+
 import pytest
 
 from tests.test_kv_host import A, B_, CUDA, INVALID, P, SHAPE, _cache, _rope, lib  # noqa: F401
@@ -21,3 +23,16 @@ def test_page_tables_of_any_size_are_counted(lib, max_pages):  # noqa: F811
         assert lib.qgemm_kv_compact(*meta, None) == SHAPE
     lib.qgemm_destroy_kv_cache(kv)
     lib.qgemm_destroy_rope(rope)
+
+
+@pytest.mark.parametrize("args", [
+    (128, 0, 1e-300, 1, 1e-20, 0.0, 1.0, 4.0, 1.0),              # 1e295 / 1e-20, past the doubles' end
+    (64, 1, 1e4, 1, 1e-320, 0.0, 1.0, 4.0, 1.0),
+    (64, 0, 1e4, 2, 1e-320, 64.0, 1.0, 1e6, 1.0),
+    (64, 0, 1e4, 0, 1.0, 0.0, 1.0, 4.0, 1e39),                   # a factor that fp32 does not hold
+    (64, 0, 1e4, 0, 1.0, 0.0, 1.0, 4.0, -4e38),
+])
+def test_rope_frequencies_are_finite(lib, args):  # noqa: F811
+    out = P()
+    assert lib.qgemm_create_rope(ctypes.byref(out), *args) == INVALID, lib.qgemm_last_error_message()
+    assert not out.value
