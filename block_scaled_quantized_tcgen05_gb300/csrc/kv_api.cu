@@ -60,6 +60,12 @@ qgemm_status check_rows(const void *x, int64_t ts, int64_t hs, const char *what)
     return QGEMM_OK;
 }
 
+// The stride of a dimension of one is never stepped and may be anything.
+void drop_unstepped(int64_t T, int64_t H, int64_t *ts, int64_t *hs) {
+    if (T == 1) *ts = 0;
+    if (H == 1) *hs = 0;
+}
+
 // An output's rows must not overlap, tokens outside heads or heads outside tokens.
 qgemm_status check_output_rows(int64_t T, int64_t H, int64_t d, int64_t ts, int64_t hs, const char *what) {
     const int64_t n[4] = {T, H, 1, 1}, st[4] = {ts, hs, 0, 0};
@@ -247,6 +253,8 @@ qgemm_status qgemm_rope(const void *X, int64_t x_token_stride, int64_t x_head_st
     if (T > MAX_COUNT || heads > 65536)
         return fail(QGEMM_ERR_UNSUPPORTED_SHAPE, "tokens < 2^31, heads <= 65536");
     if (T == 0 || heads == 0) return QGEMM_OK;
+    drop_unstepped(T, heads, &x_token_stride, &x_head_stride);
+    drop_unstepped(T, heads, &y_token_stride, &y_head_stride);
     QG_TRY(check_rows(X, x_token_stride, x_head_stride, "X"));
     QG_TRY(check_rows(Y, y_token_stride, y_head_stride, "Y"));
     QG_TRY(check_output_rows(T, heads, d, y_token_stride, y_head_stride, "Y"));
@@ -285,6 +293,10 @@ qgemm_status qgemm_kv_append(const qgemm_kv_cache *kv, int64_t layer, const void
         return fail(QGEMM_ERR_UNSUPPORTED_SHAPE, "rot_dim %d > head dimension %lld", rope->rot_dim, (long long)kv->d);
     QG_TRY(check_table(kv, page_table, table_stride, max_seqs, max_pages));
     if (T == 0) return QGEMM_OK;
+    drop_unstepped(T, kv->heads, &k_token_stride, &k_head_stride);
+    drop_unstepped(T, kv->heads, &v_token_stride, &v_head_stride);
+    drop_unstepped(T, q_heads, &q_token_stride, &q_head_stride);
+    drop_unstepped(T, q_heads, &qo_token_stride, &qo_head_stride);
     QG_TRY(check_rows(K, k_token_stride, k_head_stride, "K"));
     QG_TRY(check_rows(V, v_token_stride, v_head_stride, "V"));
     QG_TRY(check_ints(seqs, "seqs"));
@@ -356,6 +368,8 @@ qgemm_status qgemm_paged_attention(const void *Q, int64_t q_batch_stride, int64_
     if (window < 0) return fail(QGEMM_ERR_INVALID_ARG, "negative window");
     QG_TRY(check_table(kv, page_table, table_stride, max_seqs, max_pages));
     if (batch == 0) return QGEMM_OK;
+    drop_unstepped(batch, q_heads, &q_batch_stride, &q_head_stride);
+    drop_unstepped(batch, q_heads, &o_batch_stride, &o_head_stride);
     QG_TRY(check_rows(Q, q_batch_stride, q_head_stride, "Q"));
     QG_TRY(check_rows(O, o_batch_stride, o_head_stride, "O"));
     if (!aligned(Q, 16) || !aligned(O, 16) || q_batch_stride % 8 || q_head_stride % 8 || o_batch_stride % 8 ||

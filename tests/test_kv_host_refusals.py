@@ -2,6 +2,7 @@
 import ctypes
 
 import pytest
+import torch
 
 from tests.test_kv_host import A, B_, CUDA, INVALID, P, SHAPE, _cache, _rope, lib  # noqa: F401
 
@@ -36,3 +37,22 @@ def test_rope_frequencies_are_finite(lib, args):  # noqa: F811
     out = P()
     assert lib.qgemm_create_rope(ctypes.byref(out), *args) == INVALID, lib.qgemm_last_error_message()
     assert not out.value
+
+
+@pytest.mark.parametrize("batch,hq,heads,strides", [
+    (1, 8, 4, (1020, 128, 1020, 128)), (1, 8, 4, (-3, 128, 7, 128)), (4, 1, 1, (1024, 5, 1024, -1)), (1, 1, 1, (3, 3, 3, 3)),
+])
+def test_strides_that_are_never_stepped_do_not_count(lib, batch, hq, heads, strides):  # noqa: F811
+    """The stride of a dimension of one: a slice of a larger buffer may leave anything there."""
+    if torch.cuda.is_available():
+        pytest.skip("would launch")
+    _, kv = _cache(lib, heads=heads)
+    rope = _rope(lib)
+    qb, qh, ob, oh = strides
+    assert lib.qgemm_paged_attention(P(A), qb, qh, 0, batch, hq, kv, 0, P(A), 8, 4, 8, P(A), None, P(B_), ob, oh, None, 0.1, 0,
+                                     P(A), 1 << 30, None) == CUDA, lib.qgemm_last_error_message()
+    assert lib.qgemm_rope(P(A), qb, qh, P(B_), ob, oh, 0, batch, hq, 128, P(A), rope, 0, None) == CUDA
+    assert lib.qgemm_kv_append(kv, 0, P(A), qb, qh if heads == 1 else 128, P(A), qb, qh if heads == 1 else 128, 0, batch, P(A), P(A),
+                               P(A), 8, 4, 8, rope, P(A), qb, qh, hq, P(B_), ob, oh, None) == CUDA
+    lib.qgemm_destroy_kv_cache(kv)
+    lib.qgemm_destroy_rope(rope)
