@@ -473,6 +473,13 @@ def _rows3(t, what: str):
     return t.data_ptr(), s[0], s[1]
 
 
+def _rope(r):
+    """The handle of a rotation; a closed one is not taken for none."""
+    if r.handle:
+        return r.handle
+    raise ValueError("the rotation is closed")
+
+
 def _ints(t, what: str, n: int = 0):
     if t.dtype is not torch.int32 or t.dim() != 1 or not t.is_contiguous():
         raise ValueError(f"{what}: expected a contiguous 1-D int32 tensor")
@@ -517,7 +524,7 @@ def qgemm_rope(X, positions, rope: Rotation, out=None, inverse: bool = False, st
         y = _rows3(out, "out")
     T, H, d = shape
     st = (_lib or load_library()).qgemm_rope(*x, *y, _dtype16(X), T, H, d, _ints(positions, "positions", T),
-                                             rope.handle, 1 if inverse else 0, _raw_stream(stream))
+                                             _rope(rope), 1 if inverse else 0, _raw_stream(stream))
     if st:
         _check(st, "qgemm_rope")
     return X if out is None else out
@@ -579,7 +586,7 @@ def qgemm_kv_append(kv: KVCache, layer: int, K, V, seqs, positions, table, rope:
             raise ValueError(f"Q: expected [{T}, q_heads, {kv.d}] of K's type")
     st = (_lib or load_library()).qgemm_kv_append(
         kv.handle, layer, *_rows3(K, "K"), *_rows3(V, "V"), _dtype16(K), T, _ints(seqs, "seqs", T),
-        _ints(positions, "positions", T), *_table(table), rope.handle if rope is not None else None,
+        _ints(positions, "positions", T), *_table(table), _rope(rope) if rope is not None else None,
         *q, hq, *qo, _raw_stream(stream))
     if st:
         _check(st, "qgemm_kv_append")

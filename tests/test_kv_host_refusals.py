@@ -4,6 +4,7 @@ import ctypes
 import pytest
 import torch
 
+import block_scaled_quantized_tcgen05_gb300 as q
 from tests.test_kv_host import A, B_, CUDA, INVALID, P, SHAPE, _cache, _rope, lib  # noqa: F401
 
 
@@ -56,3 +57,22 @@ def test_strides_that_are_never_stepped_do_not_count(lib, batch, hq, heads, stri
                                P(A), 8, 4, 8, rope, P(A), qb, qh, hq, P(B_), ob, oh, None) == CUDA
     lib.qgemm_destroy_kv_cache(kv)
     lib.qgemm_destroy_rope(rope)
+
+
+def _operands(lib, rows=4):  # noqa: F811
+    """Host tensors and a view, as the binding takes them."""
+    _, handle = _cache(lib)
+    kv = q.KVCache(handle.value, q.F16, (2, 8, 4, 16, 128), ())
+    x = torch.zeros(rows, 4, 128, dtype=torch.float16)
+    return kv, x, torch.zeros(rows, dtype=torch.int32), torch.zeros(rows, 4, dtype=torch.int32)
+
+
+def test_a_closed_rotation_is_refused(lib):  # noqa: F811
+    """Not taken for no rotation."""
+    kv, x, i, table = _operands(lib)
+    rope = q.qgemm_create_rope(128)
+    rope.close()
+    with pytest.raises(ValueError, match="closed"):
+        q.qgemm_kv_append(kv, 0, x, x, i, i, table, rope=rope, stream=0)
+    with pytest.raises(ValueError, match="closed"):
+        q.qgemm_rope(x, i, rope, stream=0)
