@@ -465,8 +465,16 @@ def _dtype16(t) -> int:
     raise ValueError(f"expected an fp16 or bf16 tensor, got {dt}")
 
 
+def _on_device(t, what: str):
+    """Memory the GPU can read: device memory, or pinned host memory."""
+    if not t.is_pinned():
+        raise ValueError(f"{what}: expected a tensor in device memory, got one on {t.device}")
+
+
 def _rows3(t, what: str):
     """(pointer, token stride, head stride) of a [tokens, heads, d] tensor."""
+    if not t.is_cuda:
+        _on_device(t, what)
     s = t.stride()
     if len(s) != 3 or s[2] != 1 and t.shape[2] > 1:
         raise ValueError(f"{what}: expected a [tokens, heads, d] tensor with a contiguous last dimension")
@@ -485,6 +493,8 @@ def _ints(t, what: str, n: int = 0):
         raise ValueError(f"{what}: expected a contiguous 1-D int32 tensor")
     if t.numel() < n:
         raise ValueError(f"{what}: {t.numel()} entries, {n} needed")
+    if not t.is_cuda:
+        _on_device(t, what)
     return t.data_ptr()
 
 
@@ -493,6 +503,8 @@ def _table(t):
     s = t.stride()
     if t.dtype is not torch.int32 or len(s) != 2 or s[1] != 1 and t.shape[1] > 1:
         raise ValueError("page table: expected a 2-D int32 tensor with contiguous rows")
+    if not t.is_cuda:
+        _on_device(t, "page table")
     shape = t.shape
     return t.data_ptr(), s[0], shape[0], shape[1]
 
@@ -515,6 +527,7 @@ def qgemm_create_rope(rot_dim: int, base: float = 10000.0, interleaved: bool = F
 def qgemm_rope(X, positions, rope: Rotation, out=None, inverse: bool = False, stream=None):
     """X [tokens, heads, d] (fp16 or bf16) rotated to ``positions`` (int32 [tokens]), into ``out``
     (default: in place).  ``inverse`` rotates back, which is the gradient."""
+    turn = _rope(rope)
     shape = X.shape
     x = _rows3(X, "X")
     y = x
@@ -524,7 +537,7 @@ def qgemm_rope(X, positions, rope: Rotation, out=None, inverse: bool = False, st
         y = _rows3(out, "out")
     T, H, d = shape
     st = (_lib or load_library()).qgemm_rope(*x, *y, _dtype16(X), T, H, d, _ints(positions, "positions", T),
-                                             _rope(rope), 1 if inverse else 0, _raw_stream(stream))
+                                             turn, 1 if inverse else 0, _raw_stream(stream))
     if st:
         _check(st, "qgemm_rope")
     return X if out is None else out
@@ -554,6 +567,9 @@ def qgemm_create_kv_cache(k, v, k_scales=None, v_scales=None) -> KVCache:
                 k_scales.shape[4] < k.shape[4] // 32 or k_scales.stride(4) != 1:
             raise ValueError("scales: expected uint8 [layers, pages, heads, page_size, d / 32 or more]")
         sstrides = (ctypes.c_int64 * 4)(*k_scales.stride()[:4])
+    for name, t in (("k", k), ("v", v), ("k_scales", k_scales), ("v_scales", v_scales)):
+        if t is not None and not t.is_cuda:
+            _on_device(t, name)
     out = ctypes.c_void_p()
     _check(load_library().qgemm_create_kv_cache(ctypes.byref(out), dt, *k.shape, _ptr(k), _ptr(v), strides,
                                                 _ptr(k_scales), _ptr(v_scales), sstrides),
@@ -565,6 +581,7 @@ def qgemm_kv_append(kv: KVCache, layer: int, K, V, seqs, positions, table, rope:
                     Q=None, Q_out=None, stream=None):
     """Store new keys (rotated) and values [tokens, heads, d] at ``positions`` of sequences ``seqs``,
     and rotate the tokens' queries ``Q`` [tokens, q_heads, d] into ``Q_out`` (default: in place)."""
+    turn = None if rope is None else _rope(rope)
     shape = K.shape
     T = shape[0]
     dt = K.dtype
@@ -586,7 +603,7 @@ def qgemm_kv_append(kv: KVCache, layer: int, K, V, seqs, positions, table, rope:
             raise ValueError(f"Q: expected [{T}, q_heads, {kv.d}] of K's type")
     st = (_lib or load_library()).qgemm_kv_append(
         kv.handle, layer, *_rows3(K, "K"), *_rows3(V, "V"), _dtype16(K), T, _ints(seqs, "seqs", T),
-        _ints(positions, "positions", T), *_table(table), _rope(rope) if rope is not None else None,
+        _ints(positions, "positions", T), *_table(table), turn,
         *q, hq, *qo, _raw_stream(stream))
     if st:
         _check(st, "qgemm_kv_append")
@@ -615,12 +632,16 @@ def qgemm_paged_attention(Q, kv: KVCache, layer: int, table, lens, O, seqs=None,
         raise ValueError(f"Q and O: expected [batch, q_heads, {kv.d}] of one type")
     if lse is not None and (lse.dtype is not torch.float32 or tuple(lse.shape) != (B, H) or not lse.is_contiguous()):
         raise ValueError("lse: expected a contiguous fp32 [batch, q_heads] tensor")
+    if lse is not None and not lse.is_cuda:
+        _on_device(lse, "lse")
     if workspace is None:
         s = stream if stream is not None and not isinstance(stream, int) else torch.cuda.current_stream()
         if isinstance(stream, int) and stream != s.cuda_stream:
             raise ValueError("a raw stream needs a workspace of its own")
         with torch.cuda.stream(s):
             workspace = qgemm_paged_attention_workspace(kv, B, H)
+    elif not workspace.is_cuda:
+        _on_device(workspace, "workspace")
     t = _table(table)
     st = (_lib or load_library()).qgemm_paged_attention(
         *q, _dtype16(Q), B, H, kv.handle, layer, *t, _ints(lens, "lens", t[2]),

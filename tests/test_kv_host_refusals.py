@@ -76,3 +76,21 @@ def test_a_closed_rotation_is_refused(lib):  # noqa: F811
         q.qgemm_kv_append(kv, 0, x, x, i, i, table, rope=rope, stream=0)
     with pytest.raises(ValueError, match="closed"):
         q.qgemm_rope(x, i, rope, stream=0)
+
+
+def test_host_tensors_are_refused(lib):  # noqa: F811
+    """A tensor in host memory would be an address the GPU cannot read."""
+    kv, x, i, table = _operands(lib)
+    rope = q.qgemm_create_rope(128)
+    lens, refs, w = torch.zeros(4, dtype=torch.int32), torch.zeros(8, dtype=torch.int32), torch.zeros(1 << 24, dtype=torch.uint8)
+    k = torch.zeros(1, 4, 2, 16, 128, dtype=torch.float16)
+    for call in (lambda: q.qgemm_rope(x, i, rope, stream=0),
+                 lambda: q.qgemm_create_kv_cache(k, k.clone()),
+                 lambda: q.qgemm_kv_append(kv, 0, x, x, i, i, table, rope=rope, Q=x, stream=0),
+                 lambda: q.qgemm_paged_attention(x, kv, 0, table, lens, x.clone(), workspace=w, stream=0),
+                 lambda: q.qgemm_kv_resize(kv, table, lens, refs, i, i, stream=0),
+                 lambda: q.qgemm_kv_fork(kv, table, lens, refs, i, i, stream=0),
+                 lambda: q.qgemm_kv_compact(kv, table, lens, refs, stream=0),
+                 lambda: q.qgemm_kv_copy_pages(kv, i, i, stream=0)):
+        with pytest.raises(ValueError, match="device"):
+            call()
