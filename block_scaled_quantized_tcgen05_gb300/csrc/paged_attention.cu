@@ -198,6 +198,12 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// The factor that takes sums held relative to a maximum of `from` to one of `to`.  Sums of nothing (-inf) count for
+// nothing, others for 2^-126 at least, so that an infinite one stays infinite.
+__device__ __forceinline__ float rescale(float from, float to) {
+    return from == -INFINITY ? 0.0f : fmaxf(ex2(from - to), 0x1p-126f);
+}
+
 // The 16-byte piece `chunk` of row `row` lies at this piece of the row's place in shared memory.
 // 16-bit rows: eight rows of one piece (an ldmatrix) fall into eight bank groups.  8-bit rows of 128: so
 // do four rows of one block's two pieces (a key fragment: rows 0-3 or 4-7, 8 bytes a lane) and four even
@@ -356,8 +362,7 @@ __device__ __forceinline__ void merge_parts(const AttnParams &p, const Step &u, 
                 const float mc = __ldcg(ml + at), lc = __ldcg(ml + at + ROWS);
                 const float4 a = __ldcg(reinterpret_cast<const float4 *>(p.partial + at + row * C::D + col));
                 const float nM = fmaxf(M, mc);
-                const float fo = M == -INFINITY ? 0.0f : ex2(M - nM);
-                const float fc = mc == -INFINITY ? 0.0f : ex2(mc - nM);
+                const float fo = rescale(M, nM), fc = rescale(mc, nM);
                 M = nM;
                 L = L * fo + lc * fc;
                 o.x = o.x * fo + a.x * fc;
@@ -760,8 +765,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
                     x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
                     x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
                     x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
-                    // m = -inf has nothing to scale (its sums are zero)
-                    const float f = m[n][i] == -INFINITY ? 0.0f : ex2(m[n][i] - x);
+                    const float f = rescale(m[n][i], x);
                     m[n][i] = x;
                     l[n][i] *= f;
 #pragma unroll
@@ -920,7 +924,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
 #pragma unroll
                 for (int w = 0; w < NWARPS; ++w) {
                     const float mw = s_m[w][row];
-                    const float f = mw == -INFINITY ? 0.0f : ex2(mw - M);
+                    const float f = rescale(mw, M);
                     const float4 a = *reinterpret_cast<const float4 *>(
                         rows_of(w) + r * C::D + 4 * place(col / 4, row));
                     o.x += f * a.x, o.y += f * a.y, o.z += f * a.z, o.w += f * a.w;
