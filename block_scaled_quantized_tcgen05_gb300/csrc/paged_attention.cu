@@ -35,17 +35,18 @@
 // zero-filled and their scores -inf, so whatever the pages hold there (NaN of an earlier owner) stays
 // out.
 //
-// Precision: scores, softmax and sums in fp32.  P is split into two 16-bit values, hi = p rounded towards zero and lo = rn(p -
-// hi) (relative error 2^-21 in fp16, 2^-15 in bf16), and both are multiplied: the matrix unit has the time.
-// Both are kept above zero, at the type's smallest value that no unit flushes, so that an infinite value stays one
-// (0 x inf and inf - inf would be NaN).  Halves of P are times 2^15, so that their range is used down to 2^-39 of
-// the largest weight (values reach 65504: an error of 2.4e-7 a token).  bf16 has fp32's range, and so have its
-// values: a floor of 2^-39 would make 1.8 of a vanishing weight's 1e12, and a factor of 2^15 would take the sum past
-// fp32's end from values of 1e34 on, so P is as it is there and its floor 2^-126.  An E4M3 cache with bf16 queries
-// has both kinds of step on one accumulator: times 2^15 until a value's scale is above 2^60, then as it is.  E4M3 codes are exact in halves, and are multiplied as such; a key block's
-// scale goes onto its part of the score in fp32, and a value becomes the half code * 2^(byte - 127), exact, with
-// P in halves too.  Where a step's scales are not halves, values become the nearest 16-bit value of the
-// activations' type, with P in that type.  (bf16 queries, 128 ragged E4M3 sequences: 131 us; codes brought to bf16 by
+// Precision: scores, softmax and sums in fp32.  P is split into two 16-bit values, hi = p rounded towards zero
+// and lo = rn(p - hi) (relative error 2^-21 in fp16, 2^-15 in bf16), and both are multiplied: the matrix unit has
+// the time.  Both are kept above zero, so that an infinite value stays one (0 x inf and inf - inf would be NaN).
+// Halves of P are times 2^15, so that their range is used down to 2^-39 of the largest weight, the floor (values
+// reach 65504: an error of 2.4e-7 a token).  bf16 has fp32's range, and so have its values: a floor of 2^-39 would
+// make 1.8 of a vanishing weight's 1e12, and a factor of 2^15 would take the sum past fp32's end from values of
+// 1e34 on, so P is as it is there and its floor 2^-126.  E4M3 codes are exact in halves, and are multiplied as
+// such; a key block's scale goes onto its part of the score in fp32, and a value becomes the half
+// code * 2^(byte - 127), exact, with P in halves too (and no floor: such values are finite).  Where a step's scales
+// are not halves, values become the nearest 16-bit value of the activations' type, with P in that type.  bf16
+// queries then have both kinds of step on one accumulator: times 2^15 until a value's scale is above 2^60, as it
+// is from there on.  (bf16 queries, 128 ragged E4M3 sequences: 133 us; codes brought to bf16 by
 // way of fp32 170.)
 #include <atomic>
 #include <type_traits>
@@ -592,7 +593,7 @@ __global__ void __launch_bounds__(THREADS, C::TWO ? 2 : 1)
     float m[C::NH][2], l[C::NH][2];
     float qs[C::NH][2];                     // SCALED: what the scores of heads 2 c4, 2 c4 + 1 are still to be times
     // E4M3.  FAST scales: bytes 112 .. 127 (2^-15 .. 1: blocks of the append up to 512), halves all.  Others take the
-    // step through fp32 (all steps so: 169 us instead of 128).
+    // step through fp32 (all steps so: 172 us instead of 128, bf16 queries 183 instead of 133).
     [[maybe_unused]] constexpr uint32_t HIGH = C::D == 128 ? 0xF0F0F0F0u : 0xF0F0u, FAST_SCALES = HIGH & 0x70707070u;
     // SCALED: what the scales' high bits have to be; nothing is, once the unit has met a value scale above WIDE and its
     // sums hold P as it is (kept as a flag beside the test of the scales it took every step 2 - 5 % longer)

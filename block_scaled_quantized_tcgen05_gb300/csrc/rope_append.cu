@@ -6,8 +6,9 @@
 // past rot_dim pass through.
 //
 // Angles.  w_i / 2 pi is held as a 64-bit fraction of a turn, so position times frequency modulo
-// one turn is one wrapping integer product, exact to 2^-64 p of a turn at every position (an fp32
-// angle at position 10^5 is off by 2^-8 rad).  The top 32 bits are a signed fraction: its leading 24
+// one turn is one wrapping integer product and adds no error.  The fraction comes from doubles: for w_i of
+// at most a radian it is off by less than 2^-53 of a turn (pair 0 of base 10^4: 2^-56.5), so the angle at position p
+// by 2^-53 p, 2^-22 of a turn at 2^31 (an fp32 angle at position 10^5 is off by 2^-8 rad).  The top 32 bits are a signed fraction: its leading 24
 // go to sincospif, the rest turns the result, so sine and cosine are off by sincospif's error alone.
 //
 // Appending stores keys (rotated) and values as they are or as E4M3 codes with one power of two
@@ -28,7 +29,10 @@ namespace {
 
 constexpr int THREADS = 128;
 constexpr int BLOCKS = 6;        // resident on an SM (80 registers a thread)
-constexpr int PAIR_BLOCKS = 7;   // of the paired kernel (72 registers)
+// Of the paired kernel: 72 registers, of which rotation alone at d other than 128 and 16-bit appends as halves spill 8 to
+// 20 bytes; 6 blocks spill none.  7 / 6 blocks: 30011 x 12 x 96, rot 48 24.7 / 24.9 us, interleaved rot 38 23.0 / 24.2; 8192 x
+// 40 x 96, rot 96 23.8 / 22.4; appends of 16384 x 48 x 128 61.8 / 63.6, of 15009 x 36 x 64 25.1 / 26.5.
+constexpr int PAIR_BLOCKS = 7;
 constexpr int ROWS = 4;          // rows a lane has in flight
 constexpr int HALF_ROWS = 2;     // of half-rotated rows
 constexpr int PAIR_ROWS = 2;     // and in the paired kernel, of two pieces each
@@ -660,7 +664,8 @@ cudaError_t launch_rope_append(const AppendArgs &a, const LaunchCtx &ctx) {
         for (int i = 0; i < p.rot / 2; ++i) fr.f[i] = a.rope->freq[i];
     }
     // Tokens a block: at most the rows of three rounds of what its lanes hold, five with an E4M3 cache (whose slots
-    // are another chain of reads at a block's start) and four in the general kernel; more leaves the last
+    // are another chain of reads at a block's start), and in the general kernel four, eight for halves (30011 x 12 rows of
+    // 96, rot 38, four / six / eight: 41.2 / 39.8 / 39.9 us; 8192 x 40 of 128, rot 40: 39.5 / 35.8 / 35.3); more leaves the last
     // blocks alone on the GPU, fewer computes the sines for too few rows.  With few tokens one token a
     // block and its heads dealt to several blocks, two blocks an SM.  A row more starts a round for
     // itself: 30011 x 12 rows of 96, 42 a round, 10 tokens 24.6 us and 11 26.1.  (Paired kernel, tokens a block: 8192 x 40
