@@ -80,9 +80,10 @@ qgemm_status check_output_rows(int64_t T, int64_t H, int64_t d, int64_t ts, int6
 qgemm_status check_table(const qgemm_kv_cache *kv, const int32_t *table, int64_t stride, int64_t max_seqs,
                          int64_t max_pages) {
     if (max_seqs < 0 || max_pages < 0) return fail(QGEMM_ERR_INVALID_ARG, "negative page-table shape");
-    if (max_seqs > MAX_COUNT || max_pages > MAX_COUNT / kv->page_size)
+    // kernels step through a row's entries in 32 bits, 1024 at a time
+    if (max_seqs > MAX_COUNT || max_pages > MAX_PAGES || max_pages > MAX_COUNT / kv->page_size)
         return fail(QGEMM_ERR_UNSUPPORTED_SHAPE,
-                    "page table of %lld x %lld pages of %lld tokens: a row holds fewer than 2^31 tokens",
+                    "page table of %lld x %lld pages of %lld tokens: a row holds fewer than 2^31 tokens in at most 2^30 pages",
                     (long long)max_seqs, (long long)max_pages, (long long)kv->page_size);
     if (max_seqs > 0 && max_pages > 0 && !table) return fail(QGEMM_ERR_INVALID_ARG, "page table is NULL");
     if (max_seqs > 1 && stride < max_pages)

@@ -381,7 +381,8 @@ qgemm_status qgemm_w8_gemv_ex(const void *X_f16, int64_t ldx, int64_t M, const q
  * Token t of a sequence lies in row t % page_size of the page its page-table row names at t /
  * page_size.  The page table ([max_seqs, max_pages] int32, row stride in entries), the lengths
  * (int32 [max_seqs], tokens) and the reference counts (int32 [pages], 0 = free) are device memory of
- * the caller; a sequence of n tokens holds the first ceil(n / page_size) entries of its row.
+ * the caller; a sequence of n tokens holds the first ceil(n / page_size) entries of its row.  A row holds fewer than 2^31
+ * tokens in at most 2^30 pages.
  *
  * Indices the kernels read from device memory are checked there: a sequence number, position,
  * length or page-table entry out of range sets bit 64 of the device error word, and what it names is

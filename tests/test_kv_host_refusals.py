@@ -94,3 +94,17 @@ def test_host_tensors_are_refused(lib):  # noqa: F811
                  lambda: q.qgemm_kv_copy_pages(kv, i, i, stream=0)):
         with pytest.raises(ValueError, match="device"):
             call()
+
+
+@pytest.mark.parametrize("max_pages,status", [(1 << 30, CUDA), ((1 << 30) + 1, SHAPE), ((1 << 31) - 1, SHAPE)])
+def test_rows_of_more_entries_than_a_cache_has_pages(lib, max_pages, status):  # noqa: F811
+    """Pages of one token: the kernels step through a row's entries in 32 bits, up to a thousand past its end."""
+    if status == CUDA and torch.cuda.is_available():
+        pytest.skip("would launch")
+    got, kv = _cache(lib, layers=1, heads=1, page=1, st=(0, 256, 256, 256))
+    assert got == 0
+    meta = (kv, P(A), max_pages, 1, max_pages, P(A), P(A))
+    assert lib.qgemm_kv_resize(*meta, P(A), P(A), 2, None) == status
+    assert lib.qgemm_kv_fork(*meta, P(A), P(A), 2, None) == status
+    assert lib.qgemm_kv_compact(*meta, None) == status
+    lib.qgemm_destroy_kv_cache(kv)
