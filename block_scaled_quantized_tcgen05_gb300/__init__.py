@@ -22,9 +22,10 @@ __all__ = [
     "Rotation", "KVCache", "qgemm_create_rope", "qgemm_rope", "qgemm_create_kv_cache", "qgemm_kv_append",
     "qgemm_paged_attention_workspace", "qgemm_paged_attention", "qgemm_kv_resize", "qgemm_kv_fork",
     "qgemm_kv_compact", "qgemm_kv_copy_pages",
+    "F32", "qgemm_norm_quant", "qgemm_act_quant", "qgemm_w8a8", "qgemm_w8a8_ex",
 ]
 
-F16, E4M3, INT8, INT4, E2M1, BF16 = 0, 1, 2, 3, 4, 5
+F16, E4M3, INT8, INT4, E2M1, BF16, F32 = 0, 1, 2, 3, 4, 5, 6
 OK = 0
 STATUS_NAMES = {0: "QGEMM_OK", 1: "QGEMM_ERR_INVALID_ARG", 2: "QGEMM_ERR_UNSUPPORTED_SHAPE",
                 3: "QGEMM_ERR_MISALIGNED", 4: "QGEMM_ERR_UNSUPPORTED_DTYPE", 5: "QGEMM_ERR_CUDA",
@@ -117,6 +118,10 @@ def load_library():
         "qgemm_kv_fork": (S, meta + [P, P, I64, P]),
         "qgemm_kv_compact": (S, meta + [P]),
         "qgemm_kv_copy_pages": (S, [P, P, P, I64, P]),
+        "qgemm_norm_quant": (S, [P, I64, P, I64, P, I64, I32, P, I32, D, I64, I64, P, I64, I32, P, I64, P]),
+        "qgemm_act_quant": (S, [P, I64, P, I64, I32, I32, I64, I64, P, I64, I32, P, I64, P]),
+        "qgemm_w8a8": (S, [P, I64, P, P, I64, P, P, P, I64, I32, I64, I64, I64, P]),
+        "qgemm_w8a8_ex": (S, [P, I64, P, P, I64, P, P, P, I64, I32, I64, I64, I64, ctypes.POINTER(Epilogue), P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -687,3 +692,140 @@ def qgemm_kv_copy_pages(kv: KVCache, src, dst, stream=None):
     n = src.shape[0]
     _check((_lib or load_library()).qgemm_kv_copy_pages(kv.handle, _ints(src, "src"), _ints(dst, "dst", n), n,
                                                         _raw_stream(stream)), "qgemm_kv_copy_pages")
+
+
+# ------------------------------------------------------------------------------ 8-bit linear layers
+_ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2}
+
+
+def _matrix(t, what: str):
+    """(pointer, row stride) of a 2-D tensor with contiguous rows on the current device."""
+    s = t.stride()
+    if len(s) != 2 or s[1] != 1 and t.shape[1] > 1:
+        raise ValueError(f"{what}: expected a 2-D tensor with contiguous rows")
+    _on_current(t, what)
+    return t.data_ptr(), s[0]
+
+
+def _vector(t, n: int, dtype, what: str):
+    """Pointer of a contiguous 1-D tensor of n entries on the current device."""
+    if t.dtype is not dtype or t.dim() != 1 or t.numel() != n or n > 1 and t.stride(0) != 1:
+        raise ValueError(f"{what}: expected {n} contiguous entries of {dtype}")
+    _on_current(t, what)
+    return t.data_ptr()
+
+
+def _on_current(t, what: str):
+    if not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{what}: expected a tensor on the current device, got one on {t.device}")
+
+
+def _eight_bits(X, Y, scales):
+    """(Y's type, scales' pointer, scales' row stride) of a row quantiser's output."""
+    dt = Y.dtype
+    if dt is X.dtype:
+        if scales is not None:
+            raise ValueError("scales: a 16-bit output has none")
+        return _dtype16(Y), None, 0
+    if scales is None:
+        raise ValueError("scales: an 8-bit output needs them")
+    if dt is torch.int8:
+        return INT8, _vector(scales, X.shape[0], torch.float32, "scales"), 0
+    if dt is not torch.uint8 and dt is not torch.float8_e4m3fn:
+        raise ValueError(f"Y: expected int8, uint8 or float8_e4m3fn (E4M3 codes), or X's type, got {dt}")
+    if scales.dtype is not torch.uint8 or scales.dim() != 2 or tuple(scales.shape) != (X.shape[0], X.shape[1] // 32):
+        raise ValueError("scales: expected uint8 [tokens, size / 32]")
+    return E4M3, *_matrix(scales, "scales")
+
+
+def qgemm_norm_quant(X, weight, Y, scales=None, residual=None, residual_out=None, eps: float = 1e-6, stream=None):
+    """Y = (X + residual) / rms(X + residual) * weight for rows [tokens, size] of fp16 or bf16.  Y is int8
+    with fp32 ``scales`` [tokens], uint8 / float8_e4m3fn codes with uint8 UE8M0 ``scales`` [tokens, size / 32],
+    or of X's type.  ``residual_out`` (may be ``residual`` or X) receives X + residual; ``weight`` (fp16, bf16
+    or fp32 [size]) may be None."""
+    if torch is None:
+        _load_torch()
+    shape = X.shape
+    xdt = X.dtype
+    x = _matrix(X, "X")
+    dt = _dtype16(X)
+    if Y.shape != shape:
+        raise ValueError("Y: shape must be X's")
+    r = ro = (None, 0)
+    if residual is not None:
+        if residual.shape != shape or residual.dtype is not xdt:
+            raise ValueError("residual: shape and type must be X's")
+        r = _matrix(residual, "residual")
+    if residual_out is not None:
+        if residual_out.shape != shape or residual_out.dtype is not xdt:
+            raise ValueError("residual_out: shape and type must be X's")
+        ro = _matrix(residual_out, "residual_out")
+    w, wdt = None, F32
+    if weight is not None:
+        wdt = F32 if weight.dtype is torch.float32 else _dtype16(weight)
+        w = _vector(weight, shape[1], weight.dtype, "weight")
+    ydt, sp, lds = _eight_bits(X, Y, scales)
+    st = (_lib or load_library()).qgemm_norm_quant(*x, *r, *ro, dt, w, wdt, eps, shape[0], shape[1], *_matrix(Y, "Y"),
+                                                   ydt, sp, lds, _raw_stream(stream))
+    if st:
+        _check(st, "qgemm_norm_quant")
+    return Y
+
+
+def qgemm_act_quant(X, Y, scales=None, up=None, activation: str = "none", stream=None):
+    """Y = f(X) [* up] for rows [tokens, size] of fp16 or bf16, f one of "none", "silu", "gelu" (tanh form);
+    Y and ``scales`` as for qgemm_norm_quant.  With "none" and no ``up`` it quantises X as it is."""
+    if torch is None:
+        _load_torch()
+    kind = _ACTIVATIONS.get(activation)
+    if kind is None:
+        raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}")
+    shape = X.shape
+    x = _matrix(X, "X")
+    dt = _dtype16(X)
+    if Y.shape != shape:
+        raise ValueError("Y: shape must be X's")
+    u = (None, 0)
+    if up is not None:
+        if up.shape != shape or up.dtype is not X.dtype:
+            raise ValueError("up: shape and type must be X's")
+        u = _matrix(up, "up")
+    ydt, sp, lds = _eight_bits(X, Y, scales)
+    st = (_lib or load_library()).qgemm_act_quant(*x, *u, dt, kind, shape[0], shape[1], *_matrix(Y, "Y"), ydt, sp, lds,
+                                                  _raw_stream(stream))
+    if st:
+        _check(st, "qgemm_act_quant")
+    return Y
+
+
+def _w8a8(A, a_scales, W, w_scales, C, bias):
+    if torch is None:
+        _load_torch()
+    if A.dtype is not torch.int8 or W.dtype is not torch.int8:
+        raise ValueError("A and W: expected int8 tensors")
+    a, w, c = _matrix(A, "A"), _matrix(W, "W"), _matrix(C, "C")
+    M, K = A.shape
+    N = W.shape[0]
+    if W.shape[1] != K or tuple(C.shape) != (M, N):
+        raise ValueError(f"expected W [N, {K}] and C [{M}, N], got {tuple(W.shape)} and {tuple(C.shape)}")
+    f32 = torch.float32
+    return (*a, _vector(a_scales, M, f32, "a_scales"), *w, _vector(w_scales, N, f32, "w_scales"),
+            None if bias is None else _vector(bias, N, C.dtype, "bias"), *c, _dtype16(C), M, N, K)
+
+
+def qgemm_w8a8(A, a_scales, W, w_scales, C, bias=None, stream=None):
+    """C = (A W^T) * a_scales[:, None] * w_scales [+ bias]: int8 A [M, K] and W [N, K] (rows 16-byte aligned), fp32
+    scales a token and a channel, fp16 or bf16 C [M, N] and bias [N]."""
+    st = (_lib or load_library()).qgemm_w8a8(*_w8a8(A, a_scales, W, w_scales, C, bias), _raw_stream(stream))
+    if st:
+        _check(st, "qgemm_w8a8")
+    return C
+
+
+def qgemm_w8a8_ex(A, a_scales, W, w_scales, C, bias=None, accumulate=False, relu=False, stream=None):
+    """qgemm_w8a8 with the output epilogue: C = relu?(product [+ bias] [+ C])."""
+    st = (_lib or load_library()).qgemm_w8a8_ex(*_w8a8(A, a_scales, W, w_scales, C, bias), _epi(accumulate, relu),
+                                                _raw_stream(stream))
+    if st:
+        _check(st, "qgemm_w8a8_ex")
+    return C

@@ -61,7 +61,8 @@ typedef enum {
     QGEMM_E2M1 = 4,  /* FP4 E2M1 (sign, 2 exponent bits with bias 1, 1 mantissa bit; values
                         0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), two per byte, even k in
                         the low nibble                                                        */
-    QGEMM_BF16 = 5   /* bfloat16: activations and caches of the decode-serving calls only     */
+    QGEMM_BF16 = 5,  /* bfloat16: the decode-serving and 8-bit linear calls only              */
+    QGEMM_F32 = 6    /* IEEE binary32: weights of qgemm_norm_quant only                       */
 } qgemm_dtype;
 
 /* Opaque, host-side, NON-owning view of one quantized matrix [rows, k]. */
@@ -546,6 +547,88 @@ qgemm_status qgemm_kv_compact(const qgemm_kv_cache *kv, int32_t *page_table, int
  * dst may be another item's src or dst.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED; CUDA. */
 qgemm_status qgemm_kv_copy_pages(const qgemm_kv_cache *kv, const int32_t *src, const int32_t *dst,
                                  int64_t n, void *stream);
+
+/* ------------------------------------------------------------------- 8-bit linear layers
+ * What stands between this library's products in a model: the norm before a projection and the
+ * activation before the product back, leaving 8 bits with scales in the same pass, and the product of
+ * 8-bit integers that carries one scale for each token and one for each channel.  The pages have no
+ * counterpart.
+ *
+ * Eight bits are one of two formats, chosen by the output's type:
+ *   QGEMM_INT8  q[t, c] = rne(y[t, c] * 127 / a), s[t] = a / 127 (fp32), a = max(max_c |y[t, c]|, 2^-100):
+ *               the operands of qgemm_w8a8.  Codes lie in -127 .. 127.  A row that holds a NaN gets the
+ *               scale NaN, one that holds an infinity and no NaN the scale infinity with codes 0: the product's
+ *               row is NaN in both cases.
+ *   QGEMM_E4M3  per 32 elements X = floor(log2(amax)) - 8 (at least -127) as byte X + 127 and e4m3_rn(y * 2^-X)
+ *               saturated to +-448, as qgemm_kv_append stores a bfloat16 cache: the operands of
+ *               qgemm_mxfp8.  An all-zero block gets byte 127; NaN elements become E4M3's NaN, infinite
+ *               ones +-448 with byte 247.
+ * An output of the activations' own type (QGEMM_F16, QGEMM_BF16) is y rounded once, with no scales.
+ *
+ * The kernels are launched as programmatic dependents: their blocks may be resident before the work
+ * ahead of them on the stream has ended, and touch memory only after it has.  Every call can be captured
+ * into a graph and takes no workspace of the caller's. */
+
+/* Root-mean-square norm of T rows, with the residual's addition before it:
+ *   h = x + r,   y[t, c] = h[t, c] / sqrt(mean_c h[t, c]^2 + eps) * w[c],
+ * all in fp32 from the 16-bit inputs; h is not rounded on its way to y.
+ *   X             device [T, H] of dtype (QGEMM_F16 or QGEMM_BF16), row stride ldx elements.
+ *   residual      device [T, H] of dtype, or NULL (h = x).
+ *   residual_out  device [T, H] of dtype, receives h rounded once; may be NULL, X or residual (with its
+ *                 row stride).  Without a residual it must be NULL.
+ *   weight        device [H] of weight_dtype (QGEMM_F16, QGEMM_BF16 or QGEMM_F32); NULL: ones.
+ *   eps           finite, at least 2^-64.
+ *   Y             device [T, H] of y_dtype: QGEMM_INT8, QGEMM_E4M3 or dtype; row stride ldy elements.  A Y of dtype
+ *                 may be X (with its row stride), where residual_out is not; otherwise Y overlaps no input.
+ *   scales        QGEMM_INT8: fp32 [T].  QGEMM_E4M3: UE8M0 [T, H / 32], row stride lds bytes.  Else NULL.
+ * Requirements: H % 32 == 0 for QGEMM_E4M3, otherwise any H; T and H below 2^31; rows of the outputs must not overlap.
+ * Sums of squares that pass fp32's range (bfloat16 inputs above about 1e18) are taken again of h * 2^-80.
+ * Speed: 16-byte aligned X, residual, residual_out and weight with row strides in multiples of 8 elements, and a Y
+ * aligned to 8 of its elements, with H a multiple of 8 up to 32768, take the vector kernel; any other alignment works.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, UNSUPPORTED_DTYPE, MISALIGNED (nothing enqueued); CUDA. */
+qgemm_status qgemm_norm_quant(const void *X, int64_t ldx, const void *residual, int64_t ldr,
+                              void *residual_out, int64_t ldro, int32_t dtype, const void *weight,
+                              int32_t weight_dtype, double eps, int64_t T, int64_t H, void *Y,
+                              int64_t ldy, int32_t y_dtype, void *scales, int64_t lds, void *stream);
+
+enum {
+    QGEMM_ACT_NONE = 0,   /* f(x) = x                                                              */
+    QGEMM_ACT_SILU = 1,   /* f(x) = x / (1 + exp(-x))                                              */
+    QGEMM_ACT_GELU = 2    /* f(x) = x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2              */
+};
+
+/* Activation of T rows, times a second operand where there is one: y[t, c] = f(x[t, c]) [* up[t, c]], in fp32
+ * from the 16-bit inputs.  QGEMM_ACT_NONE without `up` quantises the rows as they are (an attention's
+ * output; with T channels of H weights, a weight matrix for qgemm_w8a8).
+ *   X, up   device [T, H] of dtype (QGEMM_F16 or QGEMM_BF16), row strides in elements (the halves of a fused
+ *           product's output, say); up may be NULL.
+ *   Y, scales, requirements, speed, errors: as qgemm_norm_quant; a Y of dtype may be X or up (with its row stride).
+ * f(-inf) of QGEMM_ACT_SILU and QGEMM_ACT_GELU is NaN, as the formulas give it. */
+qgemm_status qgemm_act_quant(const void *X, int64_t ldx, const void *up, int64_t ldu, int32_t dtype,
+                             int32_t activation, int64_t T, int64_t H, void *Y, int64_t ldy,
+                             int32_t y_dtype, void *scales, int64_t lds, void *stream);
+
+/* Product of 8-bit integers with a scale for each token and each channel:
+ *   C[m, n] = round( (sum_k A[m, k] W[n, k]) * a_scales[m] * w_scales[n] [+ bias[n]] ).
+ * Codes are two's complement int8, -128 included.  With M <= 16 the sums are fp32 sums of exact products on the
+ * warp-level tensor cores, otherwise on tcgen05 (the integers as halves); integer sums below 2^24 are exact, larger
+ * ones carry fp32's rounding.  Scales are applied to the sum in fp32; one rounding at the end.
+ *   A         device int8 [M, K], row stride lda bytes;  a_scales fp32 [M].
+ *   W         device int8 [N, K], row stride ldw bytes;  w_scales fp32 [N].
+ *   bias      device [N] of c_dtype, or NULL.
+ *   C         device [M, N] of c_dtype (QGEMM_F16 or QGEMM_BF16), row stride ldc elements; overlaps no input.
+ * Requirements: A and W 16-byte aligned with row strides in multiples of 16 (rows of any K are padded; the
+ * padding is not read as data and may hold anything); scales 4-byte, bias and C 2-byte aligned; M, N, K below 2^31.  M or
+ * N == 0 writes nothing; K == 0 gives the bias.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, UNSUPPORTED_DTYPE, MISALIGNED (nothing enqueued); CUDA (including a
+ * failed scratch allocation). */
+qgemm_status qgemm_w8a8(const int8_t *A, int64_t lda, const float *a_scales, const int8_t *W, int64_t ldw,
+                        const float *w_scales, const void *bias, void *C, int64_t ldc, int32_t c_dtype,
+                        int64_t M, int64_t N, int64_t K, void *stream);
+/* The same with the output epilogue of the _ex calls (NULL: none): the old C is added after the bias, then ReLU. */
+qgemm_status qgemm_w8a8_ex(const int8_t *A, int64_t lda, const float *a_scales, const int8_t *W, int64_t ldw,
+                           const float *w_scales, const void *bias, void *C, int64_t ldc, int32_t c_dtype,
+                           int64_t M, int64_t N, int64_t K, const qgemm_epilogue *epilogue, void *stream);
 
 /* Dequantise-only debug kernel: out[r, k] = decode(t.data[r, k]) * 2^(t.scales[r, k/32] - 127)
  * as fp32 (fp16 views: the value itself), written densely as [rows, k] row-major.  Exists so
