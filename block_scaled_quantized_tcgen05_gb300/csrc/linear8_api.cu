@@ -1,5 +1,5 @@
 // linear8_api.cu -- C ABI of the 8-bit linear layers: norm and activation with 8-bit output, and the
-// product of 8-bit integers.  Argument validation only; the kernels live in row_quant.cu and
+// product of 8-bit integers.  Argument validation only; the kernels live in row_quant.cuh and
 // w8a8_*.cu.
 #include <cmath>
 
