@@ -1,0 +1,548 @@
+// w8a8_pair.cu -- product of 8-bit integers on CTA pairs, both operands as halves on the fp16 tensor cores.
+//
+//   C[m, n] = round( (sum_k A[m, k] W[n, k]) * sa[m] * sw[n] [+ bias[n]] [+ C_old] ), then ReLU.
+//
+// sm_103a has no integer tensor core worth the name (mma.sync on s8 runs at the rate of dp4a, 251 products a
+// clock and SM against about 4096 on tcgen05 kind::f16; measured), and every int8 is a half, whose products are
+// exact in the fp32 accumulator as long as the sum stays below 2^24.  So the product D[n, m] = sum_k W[n, k]
+// A[m, k] runs on kind::f16:
+//
+//   * weights are the left operand: raw bytes land in shared memory by TMA (64 a row, 64-byte swizzle), converter
+//     warps turn them into halves in registers and write them to TMEM, from where the MMA reads them.  They never
+//     take shared memory's bandwidth as halves;
+//   * tokens are the right operand, in shared memory.  They are turned into halves once, by a kernel ahead of this
+//     one into pooled scratch, because every block of weight rows reads them again;
+//   * a cluster of two CTAs computes 256 weight rows x BT tokens, each CTA holding 128 weight rows in TMEM and BT / 2 tokens
+//     in shared memory;
+//   * the epilogue reads D (lane = weight row, column = token), applies the scales, and writes through shared
+//     memory and TMA stores where C allows a tensor map;
+//   * few tiles: K is split over several pairs, whose fp32 partial planes a reduction kernel adds in order.
+#include <algorithm>
+
+#include "qgemm_common.cuh"
+#include "w8a8_common.cuh"
+
+namespace {
+
+using namespace qg;
+
+constexpr int BW = 128;                 // weight rows per CTA (256 per pair: the MMA's M)
+constexpr int BK = 64;                  // k per stage
+constexpr int EPI_WARPS = 8;            // two per lane quarter, one per half of the tokens
+constexpr int CONV_WARP0 = 2 + EPI_WARPS;
+constexpr int CONV_WARPS = 8;           // two per lane quarter, alternate k-tiles
+constexpr int THREADS = 32 * (CONV_WARP0 + CONV_WARPS);
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t A_COLS = BK / 2;     // TMEM columns of a stage's weights
+
+template <int BT>
+struct Cfg {
+    static constexpr int STAGES = BT == 256 ? 6 : BT == 128 ? 10 : 14;        // even: a converter warp keeps its parity
+    static constexpr uint32_t X_BYTES = (BT / 2) * BK * 2;
+    static constexpr uint32_t RAW_BYTES = BW * BK;
+    static constexpr uint32_t STAGE_TX = 2 * X_BYTES;                         // both CTAs' tokens, on the leader
+    static constexpr int CHUNKS = BT / 64;                                    // 32-token chunks of an epilogue warp
+    static constexpr uint32_t EPI_BYTES = CHUNKS * 2048;
+    static constexpr uint32_t OFF_RAW = STAGES * X_BYTES;
+    static constexpr uint32_t OFF_EPI = OFF_RAW + STAGES * RAW_BYTES;
+    static constexpr uint32_t OFF_SA = OFF_EPI + EPI_WARPS * EPI_BYTES;       // each epilogue warp's token scales
+    static constexpr uint32_t OFF_BAR = OFF_SA + EPI_WARPS * (BT / 2) * 4;
+    static constexpr uint32_t OFF_SLOT = OFF_BAR + (3 * STAGES + 3) * 8;
+    static constexpr uint32_t SMEM = OFF_SLOT + 16 + 1024;
+    static constexpr uint32_t A_COL0 = BT;                                    // after the accumulator
+    static_assert(SMEM <= 232448, "shared memory budget");
+    static_assert(A_COL0 + STAGES * A_COLS <= TMEM_COLS, "TMEM budget");
+    // kind::f16: D fp32, A and B fp16, K-major, N = BT tokens, M = 256 weight rows (pair)
+    static constexpr uint32_t IDESC = (1u << 4) | (uint32_t(BT >> 3) << 17) | (uint32_t(256 >> 4) << 24);
+};
+
+__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint16_t v) {
+    asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
+}
+
+enum Out { OUT_F16, OUT_BF16, OUT_PARTIAL };
+
+template <int BT, int OUT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                 const __grid_constant__ CUtensorMap tmC, int c_tma, const __grid_constant__ qgi::W8A8Args a,
+                 int splits, float *__restrict__ P, int64_t ldp, int epi, unsigned *err, uint64_t timeout_ns) {
+    using G = Cfg<BT>;
+    constexpr int STAGES = G::STAGES;
+    constexpr bool PARTIAL = OUT == OUT_PARTIAL;
+    constexpr int BF16 = OUT == OUT_BF16;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align_1024(smem_raw);
+    griddep_launch_dependents();
+    const uint32_t sb = smem_u32(smem);
+    const uint32_t warp = threadIdx.x >> 5;
+    const uint32_t lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();      // 0 = leader
+    const int pair = blockIdx.x >> 1;
+    const int npairs = gridDim.x >> 1;
+    const int M = a.M, N = a.N;
+
+    auto full_bar = [&](int s) { return sb + G::OFF_BAR + 8u * s; };
+    auto empty_bar = [&](int s) { return sb + G::OFF_BAR + 8u * (STAGES + s); };
+    auto raw_full = [&](int s) { return sb + G::OFF_BAR + 8u * (2 * STAGES + s); };
+    const uint32_t tmem_full = sb + G::OFF_BAR + 8u * (3 * STAGES);
+    const uint32_t tmem_empty = tmem_full + 8;
+    const uint32_t drain_bar = tmem_full + 16;
+    volatile uint32_t *slot = reinterpret_cast<volatile uint32_t *>(smem + G::OFF_SLOT);
+
+    // tiles: weight-row blocks of 256 (the "m" of tile_coords) x token blocks of BT; work items (tile, range of K)
+    const int tiles_w = (N + 2 * BW - 1) / (2 * BW);
+    const int tiles_t = (M + BT - 1) / BT;
+    const int num_tiles = tiles_w * tiles_t;
+    const int KT = (a.K + BK - 1) / BK;
+    const int num_items = num_tiles * splits;
+    auto item_of = [&](int it, int &tile, int &split, int &kt0, int &kt1) {
+        if constexpr (PARTIAL) {
+            split_item(it, num_tiles, splits, KT, 1, tile, split, kt0, kt1);
+        } else {
+            tile = it;
+            split = 0;
+            kt0 = 0;
+            kt1 = KT;
+        }
+    };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full_bar(s), 1 + 2 * (CONV_WARPS / 2));   // expect_tx + converters of a stage
+            mbar_init(empty_bar(s), 1);                          // leader's multicast commit
+            mbar_init(raw_full(s), 1);                           // this CTA's raw weights
+        }
+        mbar_init(tmem_full, 1);
+        mbar_init(tmem_empty, 2 * EPI_WARPS);   // one lane of each epilogue warp of both CTAs
+        mbar_init(drain_bar, 1);
+        fence_barrier_init();
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmW);
+        if (c_tma) tma_prefetch_desc(&tmC);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(const_cast<uint32_t *>(slot)), TMEM_COLS);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();                   // barriers of both CTAs initialised before remote use
+    tc_fence_after();
+    const uint32_t tmem_base = *slot;
+    griddep_wait();                   // the tokens' halves, and whatever made the other operands
+
+    if (warp == 0) {
+        // ---------------------------------------------------------------- producer
+        // The whole warp runs the loop and waits; one elected lane issues the copies.
+        uint32_t stage = 0, phase = 0;
+        int issued = 0;
+        bool ok = true;
+        for (int it = pair; it < num_items && ok; it += npairs) {
+            int tile, split, kt0, kt1, wb, tb;
+            item_of(it, tile, split, kt0, kt1);
+            tile_coords(tile, tiles_w, tiles_t, wb, tb);
+            const int w0 = wb * 2 * BW + static_cast<int>(rank) * BW;     // this CTA's weights
+            const int t0 = tb * BT + static_cast<int>(rank) * (BT / 2);   // this CTA's tokens
+            for (int kt = kt0; kt < kt1; ++kt) {
+                if (!mbar_wait_warp(empty_bar(stage), phase ^ 1, timeout_ns)) {
+                    ok = false;
+                    break;
+                }
+                // debug build: the copies' innermost coordinates are multiples of 16 bytes and inside K
+                if (!QG_IN_BOUNDS(err, (kt * BK) % 16 == 0 && kt * BK < a.K)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t lead_full = map_to_cta(full_bar(stage), 0);
+                if (elect_one()) {
+                    if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), G::STAGE_TX);
+                    tma_load_2d_pair(sb + stage * G::X_BYTES, &tmX, lead_full, kt * BK, t0);
+                    mbar_arrive_expect_tx(raw_full(stage), G::RAW_BYTES);
+                    tma_load_2d(sb + G::OFF_RAW + stage * G::RAW_BYTES, &tmW, raw_full(stage), kt * BK, w0);
+                }
+                __syncwarp();
+                ++issued;
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        if (!ok && lane == 0) atomicOr(err, ERR_PRODUCER);
+        for (int i = max(0, issued - STAGES); i < issued; ++i) {
+            const bool drained = mbar_wait(raw_full(i % STAGES), (i / STAGES) & 1, timeout_ns) &&
+                                 (rank != 0 || mbar_wait_cluster(full_bar(i % STAGES), (i / STAGES) & 1, timeout_ns));
+            if (!__all_sync(0xFFFFFFFFu, drained)) {
+                if (lane == 0) atomicOr(err, ERR_DRAIN);
+                break;
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (rank == 0) {
+            // --------------------------------------------------------- MMA issuer
+            const uint64_t bdesc0 = smem_desc(sb, 16, 1024, SWZ_128B);
+            uint32_t acc_phase = 0, stage = 0, phase = 0;
+            bool ok = true;
+            for (int it = pair; it < num_items && ok; it += npairs) {
+                int tile, split, kt0, kt1;
+                item_of(it, tile, split, kt0, kt1);
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(tmem_empty, acc_phase ^ 1, timeout_ns))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                for (int kt = kt0; kt < kt1; ++kt) {
+                    if (!mbar_wait_warp(full_bar(stage), phase, timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a_col = tmem_base + G::A_COL0 + stage * A_COLS;
+                    const uint64_t bdesc = bdesc0 + stage * (G::X_BYTES >> 4);
+                    if (elect_one()) {
+                        mma_f16_pair_ta(tmem_base, a_col, bdesc, G::IDESC, kt > kt0 ? 1u : 0u);
+#pragma unroll
+                        for (uint32_t j = 1; j < BK / 16; ++j)
+                            mma_f16_pair_ta(tmem_base, a_col + 8 * j, bdesc + 2 * j, G::IDESC, 1u);
+                        tc_commit_pair(empty_bar(stage), 3);
+                    }
+                    __syncwarp();
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (!ok) break;
+                if (elect_one()) tc_commit_pair(tmem_full, 3);
+                __syncwarp();
+                acc_phase ^= 1;
+            }
+            if (elect_one()) {
+                if (!ok) atomicOr(err, ERR_MMA);
+                tc_commit_pair(drain_bar, 3);
+            }
+        }
+        __syncwarp();
+        // both CTAs: every pair MMA writing this CTA's TMEM has completed before it is freed
+        if (!mbar_wait(drain_bar, 0, timeout_ns) && lane == 0) atomicOr(err, ERR_DRAIN);
+    } else if (warp >= CONV_WARP0) {
+        // ----------------------------------------------------------------- converters
+        // Lane i of a warp of lane quarter q converts weight row 32 q + i of this CTA's 128; the two warps
+        // of a quarter take the even and the odd stages of the sequence of this pair's k-tiles.
+        const uint32_t q = warp & 3;
+        const int parity = static_cast<int>(warp - CONV_WARP0) >> 2;
+        const uint32_t lead_full = map_to_cta(full_bar(0), 0);
+        const uint32_t r = q * 32 + lane;
+        int total = 0;                           // this pair's k-tiles over all its items
+        for (int it = pair; it < num_items; it += npairs) {
+            int tile, split, kt0, kt1;
+            item_of(it, tile, split, kt0, kt1);
+            total += kt1 - kt0;
+        }
+        uint32_t stage = static_cast<uint32_t>(parity), phase = 0;
+        const uint8_t *row = smem + G::OFF_RAW + r * BK;
+        const uint32_t swz = (r >> 1) & 3;       // the 64-byte swizzle: chunk c of row r lies at c ^ (r / 2 % 4)
+        for (int i = parity; i < total; i += 2) {
+            if (!mbar_wait(raw_full(stage), phase, timeout_ns)) {
+                if (lane == 0) atomicOr(err, ERR_PRODUCER);
+                break;
+            }
+            tc_fence_after();   // the MMAs that last read this TMEM slot have completed
+            const uint8_t *raw = row + stage * G::RAW_BYTES;
+            uint32_t out[32];
+#pragma unroll
+            for (uint32_t c = 0; c < 4; ++c) {
+                const uint4 d = *reinterpret_cast<const uint4 *>(raw + ((c ^ swz) << 4));
+                i8x4_to_f16(d.x, out[8 * c], out[8 * c + 1]);
+                i8x4_to_f16(d.y, out[8 * c + 2], out[8 * c + 3]);
+                i8x4_to_f16(d.z, out[8 * c + 4], out[8 * c + 5]);
+                i8x4_to_f16(d.w, out[8 * c + 6], out[8 * c + 7]);
+            }
+            tmem_st_32x32b_x32(tmem_base + ((q * 32) << 16) + G::A_COL0 + stage * A_COLS, out);
+            tmem_wait_st();
+            tc_fence_before();
+            // the raw weights were read through the generic proxy; the slot's next fill is a TMA write
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_relaxed_cluster(lead_full + 8u * stage);
+            stage += 2;
+            if (stage >= STAGES) {
+                stage -= STAGES;
+                phase ^= 1;
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------- epilogue
+        // Lane i of a warp of lane quarter q holds output column n = weight row 32 q + i; the warp covers
+        // BT / 2 of the tile's tokens, 32 per TMEM read.
+        const uint32_t q = warp & 3;
+        const uint32_t half = (warp - 2) >> 2;
+        const uint32_t lead_empty = map_to_cta(tmem_empty, 0);
+        float *sa_room = reinterpret_cast<float *>(smem + G::OFF_SA) + (warp - 2) * (BT / 2);
+        uint32_t acc_phase = 0;
+        for (int it = pair; it < num_items; it += npairs) {
+            int tile, split, kt0, kt1, wb, tb;
+            item_of(it, tile, split, kt0, kt1);
+            tile_coords(tile, tiles_w, tiles_t, wb, tb);
+            const int n0 = wb * 2 * BW + static_cast<int>(rank) * BW + static_cast<int>(q * 32);
+            const int n = n0 + static_cast<int>(lane);
+            const int m0 = tb * BT + static_cast<int>(half) * (BT / 2);
+            float sw = 0.0f, bias = 0.0f;
+            if constexpr (!PARTIAL) {            // while the tile's MMAs run
+                if (n < N) {
+                    sw = __ldg(a.sw + n);
+                    if (a.bias) bias = load_16(a.bias, n, BF16);
+                }
+                __syncwarp();
+                for (int c = static_cast<int>(lane); c < BT / 2; c += 32)
+                    sa_room[c] = m0 + c < M ? __ldg(a.sa + m0 + c) : 0.0f;
+                __syncwarp();
+            }
+            if (!mbar_wait_sleep(tmem_full, acc_phase, timeout_ns, 128)) {
+                if (lane == 0) atomicOr(err, ERR_EPILOGUE);
+                break;
+            }
+            tc_fence_after();
+            const uint32_t stg = sb + G::OFF_EPI + (warp - 2) * G::EPI_BYTES;
+            if (!PARTIAL && c_tma) {             // the previous tile's stores have finished reading the staging
+                if (lane == 0) bulk_wait_read<0>();
+                __syncwarp();
+            }
+#pragma unroll 1
+            for (int ch = 0; ch < G::CHUNKS; ++ch) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(tmem_base + ((q * 32) << 16) + half * (BT / 2) + ch * 32, v);
+                tmem_wait_ld();
+                if (ch == G::CHUNKS - 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_relaxed_cluster(lead_empty);
+                }
+                const int mc = m0 + ch * 32;
+                if constexpr (PARTIAL) {
+                    // this range's sums into its partial plane, [token][weight row]: a store writes 32
+                    // consecutive floats of a token's row
+                    float *pl = P + (static_cast<int64_t>(split) * M + mc) * ldp + n;
+                    if (n < N) {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (mc + c < M) pl[c * ldp] = __uint_as_float(v[c]);
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 32; c += 4) {
+                        const float4 sa = *reinterpret_cast<const float4 *>(sa_room + ch * 32 + c);
+                        const float s4[4] = {sa.x, sa.y, sa.z, sa.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int m = mc + c + j;
+                            const float sum = __uint_as_float(v[c + j]);
+                            if (c_tma) {
+                                // row c + j of the chunk: token m, columns n0 .. n0 + 31
+                                st_shared_u16(stg + ch * 2048 + (c + j) * 64 + lane * 2,
+                                              round_16(finish(sum, s4[j], sw, bias, 0.0f, epi), BF16));
+                            } else if (n < N && m < M) {
+                                uint16_t *dst = static_cast<uint16_t *>(a.C) + m * a.ldc + n;
+                                const float old = epi & qgi::EPI_ACCUMULATE ? load_16(dst, 0, BF16) : 0.0f;
+                                *dst = round_16(finish(sum, s4[j], sw, bias, old, epi), BF16);
+                            }
+                        }
+                    }
+                }
+            }
+            if (!PARTIAL && c_tma) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+#pragma unroll
+                    for (int ch = 0; ch < G::CHUNKS; ++ch)   // blocks wholly past M or N are not stored
+                        if (n0 < N && m0 + ch * 32 < M) tma_store_2d(&tmC, stg + ch * 2048, n0, m0 + ch * 32);
+                    bulk_commit();
+                }
+            }
+            acc_phase ^= 1;
+        }
+        if (!PARTIAL && c_tma && lane == 0) bulk_wait_all();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();                   // no remote arrival or multicast targets an exited CTA
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem_base, TMEM_COLS);
+}
+
+// The tokens' codes as halves, rows of `ldh` (K rounded up to 16, at least): 16 codes a thread.
+__global__ void __launch_bounds__(256) codes_to_f16_kernel(const int8_t *__restrict__ A, int64_t lda, int M, int K,
+                                                           uint16_t *__restrict__ H, int64_t ldh) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int per_row = (K + 15) / 16;
+    const int64_t total = static_cast<int64_t>(M) * per_row;
+    for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < total; i += gridDim.x * int64_t(256)) {
+        const int64_t m = i / per_row;
+        const int k = static_cast<int>(i - m * per_row) * 16;
+        const int8_t *src = A + m * lda + k;
+        uint4 d;
+        if (k + 16 <= K) {
+            d = __ldg(reinterpret_cast<const uint4 *>(src));
+        } else {                                                   // a row's end: only its own bytes
+            uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (k + j < K) w[j / 4] |= uint32_t(uint8_t(__ldg(src + j))) << (8 * (j & 3));
+            d = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        uint32_t o[8];
+        i8x4_to_f16(d.x, o[0], o[1]);
+        i8x4_to_f16(d.y, o[2], o[3]);
+        i8x4_to_f16(d.z, o[4], o[5]);
+        i8x4_to_f16(d.w, o[6], o[7]);
+        uint4 *dst = reinterpret_cast<uint4 *>(H + m * ldh + k);
+        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+}
+
+// C from the partial planes, added in order: four columns a thread.
+__global__ void __launch_bounds__(256) w8a8_reduce_kernel(const float *__restrict__ P, int splits, int64_t ldp,
+                                                          const __grid_constant__ qgi::W8A8Args a, int vec, int epi) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int groups = (a.N + 3) / 4;
+    const int64_t total = static_cast<int64_t>(a.M) * groups, plane = a.M * ldp;
+    for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < total; i += gridDim.x * int64_t(256)) {
+        const int64_t m = i / groups;
+        const int n = static_cast<int>(i - m * groups) * 4;
+        const float *p = P + m * ldp + n;
+        float4 sum = __ldcg(reinterpret_cast<const float4 *>(p));
+        for (int s = 1; s < splits; ++s) {
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p + s * plane));
+            sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+        }
+        const float sa = __ldg(a.sa + m), sums[4] = {sum.x, sum.y, sum.z, sum.w};
+        uint16_t *dst = static_cast<uint16_t *>(a.C) + m * a.ldc + n;
+        uint16_t out[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (n + j >= a.N) break;
+            const float bias = a.bias ? load_16(a.bias, n + j, a.bf16) : 0.0f;
+            const float old = epi & qgi::EPI_ACCUMULATE ? load_16(dst, j, a.bf16) : 0.0f;
+            out[j] = round_16(finish(sums[j], sa, __ldg(a.sw + n + j), bias, old, epi), a.bf16);
+            if (!vec || n + 4 > a.N) dst[j] = out[j];
+        }
+        if (vec && n + 4 <= a.N)
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(out[0] | uint32_t(out[1]) << 16, out[2] | uint32_t(out[3]) << 16);
+    }
+}
+
+struct Plan {
+    int bt, splits;
+};
+
+// The tile's tokens and the split of K: the cheapest by a count of rounds over the pairs.
+Plan choose(int M, int N, int K, int num_sms) {
+    const int pairs = std::max(1, num_sms / 2), KT = (K + BK - 1) / BK;
+    const int64_t tiles_w = (N + 2 * BW - 1) / (2 * BW);
+    Plan best{256, 1};
+    double least = 1e300;
+    for (int bt : {64, 128, 256}) {
+        const int64_t tiles = tiles_w * ((M + bt - 1) / bt);
+        // us of a k-tile on every pair at once, of a tile's start and end, of a partial plane
+        const double per_kt = bt == 256 ? 0.27 : 0.19, ends = bt == 256 ? 2.5 : 1.5;
+        const double plane = double(M) * double(tiles_w) * 256 * 8 / 4e6;
+        for (int s = 1; s <= 16 && (s == 1 || KT / s >= 4); ++s) {
+            const double rounds = double((tiles * s + pairs - 1) / pairs);
+            const double cost = rounds * ((KT + s - 1) / s * per_kt + ends) + (s > 1 ? 2.0 + s * plane : 0.0);
+            if (cost < least) {
+                least = cost;
+                best = {bt, s};
+            }
+        }
+    }
+    return best;
+}
+
+template <int BT>
+cudaError_t launch_bt(const qgi::W8A8Args &a, const CUtensorMap &tmX, const CUtensorMap &tmW, const CUtensorMap &tmC,
+                      int c_tma, int splits, float *P, int64_t ldp, const qgi::LaunchCtx &ctx) {
+    const int64_t items = int64_t((a.N + 2 * BW - 1) / (2 * BW)) * ((a.M + BT - 1) / BT) * splits;
+    const int pairs = static_cast<int>(std::min<int64_t>(items, std::max(1, ctx.num_sms / 2)));
+    auto kern = splits > 1 ? w8a8_pair_kernel<BT, OUT_PARTIAL>
+                : a.bf16   ? w8a8_pair_kernel<BT, OUT_BF16>
+                           : w8a8_pair_kernel<BT, OUT_F16>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<BT>::SMEM);
+    if (e == cudaSuccess)
+        e = launch_dependent(kern, dim3(2 * pairs), THREADS, Cfg<BT>::SMEM, ctx.stream, tmX, tmW, tmC, c_tma, a, splits, P,
+                             ldp, ctx.epi, ctx.err, ctx.timeout_ns);
+    return e;
+}
+
+unsigned grid_for(int64_t threads, const qgi::LaunchCtx &ctx) {
+    return static_cast<unsigned>(std::min<int64_t>((threads + 255) / 256, 8 * ctx.num_sms));
+}
+
+}  // namespace
+
+namespace qgi {
+
+// A product of many tokens is taken in slices of rows, so that the tokens' halves never hold more scratch than this.
+constexpr int64_t SLICE_BYTES = int64_t(1) << 29;
+
+static cudaError_t launch_slice(const W8A8Args &a, uint16_t *H, int64_t ldh, float *P, int64_t ldp, const Plan &plan,
+                                const CUtensorMap &tmW, const LaunchCtx &ctx, bool *encode_ok) {
+    // Output through TMA stores where C allows a tensor map.  They write whole 16-byte units, past a row's end too
+    // where N is no multiple of 8 (measured); accumulating reads the old C: direct stores in both cases.
+    const int c_tma = plan.splits == 1 && reinterpret_cast<uintptr_t>(a.C) % 16 == 0 && a.ldc % 8 == 0 && a.N % 8 == 0 &&
+                      a.ldc < (int64_t(1) << 39) && !(ctx.epi & EPI_ACCUMULATE);
+    CUtensorMap tmX, tmC;
+    *encode_ok = encode_tma_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, H, a.K, a.M, ldh * 2, BK, plan.bt / 2,
+                               CU_TENSOR_MAP_SWIZZLE_128B);
+    if (*encode_ok && c_tma)
+        *encode_ok = encode_tma_2d(&tmC, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.C, a.N, a.M, a.ldc * 2, 32, 32,
+                                   CU_TENSOR_MAP_SWIZZLE_NONE);
+    else
+        tmC = tmX;   // unused
+    if (!*encode_ok) return cudaErrorInvalidValue;
+    cudaError_t e = launch_dependent(codes_to_f16_kernel, dim3(grid_for(a.M * int64_t((a.K + 15) / 16), ctx)), 256, 0,
+                                     ctx.stream, a.A, a.lda, a.M, a.K, H, ldh);
+    if (e == cudaSuccess)
+        e = plan.bt == 64    ? launch_bt<64>(a, tmX, tmW, tmC, c_tma, plan.splits, P, ldp, ctx)
+            : plan.bt == 128 ? launch_bt<128>(a, tmX, tmW, tmC, c_tma, plan.splits, P, ldp, ctx)
+                             : launch_bt<256>(a, tmX, tmW, tmC, c_tma, plan.splits, P, ldp, ctx);
+    if (e == cudaSuccess && plan.splits > 1) {
+        const int vec = reinterpret_cast<uintptr_t>(a.C) % 8 == 0 && a.ldc % 4 == 0;
+        e = launch_dependent(w8a8_reduce_kernel, dim3(grid_for(a.M * int64_t((a.N + 3) / 4), ctx)), 256, 0, ctx.stream, P,
+                             plan.splits, ldp, a, vec, ctx.epi);
+    }
+    return e;
+}
+
+cudaError_t launch_w8a8_pair(const W8A8Args &a, const LaunchCtx &ctx, bool *encode_ok) {
+    const int64_t ldh = (a.K + 63) / 64 * int64_t(64), ldp = (a.N + 255) / 256 * int64_t(256);
+    const int slice = static_cast<int>(std::min<int64_t>(a.M, std::max<int64_t>(SLICE_BYTES / (2 * ldh) / 256 * 256, 256)));
+    const Plan plan = choose(slice, a.N, a.K, ctx.num_sms);
+    const size_t x_bytes = (static_cast<size_t>(slice) * ldh * 2 + 255) / 256 * 256;
+    const size_t p_bytes = plan.splits > 1 ? static_cast<size_t>(plan.splits) * slice * ldp * 4 : 0;
+    CUtensorMap tmW;
+    *encode_ok = encode_tma_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.W, a.K, a.N, a.ldw, BK, BW, CU_TENSOR_MAP_SWIZZLE_64B);
+    if (!*encode_ok) return cudaErrorInvalidValue;
+    void *ws = nullptr;
+    cudaError_t e = scratch_alloc(x_bytes + p_bytes, ctx, &ws);
+    if (e != cudaSuccess) return e;
+    for (int64_t m0 = 0; m0 < a.M && e == cudaSuccess; m0 += slice) {
+        W8A8Args part = a;
+        part.A += m0 * a.lda;
+        part.sa += m0;
+        part.C = static_cast<uint16_t *>(a.C) + m0 * a.ldc;
+        part.M = static_cast<int>(std::min<int64_t>(slice, a.M - m0));
+        e = launch_slice(part, static_cast<uint16_t *>(ws), ldh, reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + x_bytes),
+                         ldp, plan, tmW, ctx, encode_ok);
+    }
+    const cudaError_t f = scratch_free(ws, ctx);
+    return e != cudaSuccess ? e : f;
+}
+
+}  // namespace qgi
