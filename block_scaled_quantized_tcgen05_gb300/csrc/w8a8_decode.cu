@@ -1,0 +1,270 @@
+// w8a8_decode.cu -- product of 8-bit integers for a few tokens, bound by the weights' bytes.
+//
+// A weight stream: a producer warp keeps STAGES boxes of 16 NF weight rows x 128 bytes of K in flight by TMA, with the
+// same 128 bytes of the tokens' rows beside each.  Four consumer warps take 32 k of a stage each, for all its rows:
+// per 16-row fragment a lane quad turns 8 consecutive int8 of rows g and g + 8 into halves (exact) and feeds two
+// mma.sync m16n8k16, weights as the 16-row operand and tokens as the 8-column operand; the 32 k are permuted alike for both, so the sums
+// are unchanged.  Sums are fp32 over the whole of K, scaled once at the end.
+//
+// A block of rows is a cluster's: where there are few blocks of rows, its K is cut over the cluster's CTAs, whose
+// sums meet through distributed shared memory (no scratch, no second launch).  Partial sums are added in the order of
+// ranks and warps, so results repeat bit for bit.
+#include <algorithm>
+
+#include "qgemm_common.cuh"
+#include "w8a8_common.cuh"
+
+namespace {
+
+using namespace qg;
+
+constexpr int CONSUMERS = 4;
+constexpr int THREADS = (CONSUMERS + 1) * 32;
+constexpr int KC = 128;                     // bytes of K per stage
+
+// NH: 8-token columns (M <= 8 NH); NF: 16-row weight fragments of a block of rows.
+template <int NH, int NF, int STAGES_>
+struct Cfg {
+    static constexpr int STAGES = STAGES_;
+    static constexpr int ROWS = 16 * NF;
+    static constexpr uint32_t W_BYTES = ROWS * KC;
+    static constexpr uint32_t X_BYTES = 8 * NH * KC;
+    static constexpr uint32_t STAGE = W_BYTES + X_BYTES;
+    static constexpr uint32_t OFF_RED = STAGES * STAGE;                 // sums of the warps: [warp][NF][NH][4][lane]
+    static constexpr uint32_t OFF_BAR = OFF_RED + CONSUMERS * NF * NH * 4 * 32 * 4;
+    static constexpr uint32_t SMEM = OFF_BAR + 2 * STAGES * 8 + 1024;
+    static_assert(STAGE % 1024 == 0, "stages stay 1 KB aligned for the 128-byte swizzle");
+};
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+    return v;
+}
+
+// One stage's products: this warp's 32 k of every row.
+template <int NH, int NF>
+__device__ __forceinline__ void stage_math(float (&acc)[NF][NH][4], const uint8_t *st, uint32_t off) {
+    uint32_t x[NH][4];
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(st + 16 * NF * KC + h * 1024 + off);
+        i8x4_to_f16(v.x, x[h][0], x[h][1]);
+        i8x4_to_f16(v.y, x[h][2], x[h][3]);
+    }
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+        const uint2 wa = *reinterpret_cast<const uint2 *>(st + off + f * 2048);
+        const uint2 wb = *reinterpret_cast<const uint2 *>(st + off + f * 2048 + 1024);
+        uint32_t a0[4], a1[4];
+        i8x4_to_f16(wa.x, a0[0], a0[2]);
+        i8x4_to_f16(wb.x, a0[1], a0[3]);
+        i8x4_to_f16(wa.y, a1[0], a1[2]);
+        i8x4_to_f16(wb.y, a1[1], a1[3]);
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+            mma_16816(acc[f][h], a0, x[h][0], x[h][1]);
+            mma_16816(acc[f][h], a1, x[h][2], x[h][3]);
+        }
+    }
+}
+
+template <int NH, int NF, int STAGES_>
+__global__ void __launch_bounds__(THREADS)
+w8a8_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                   const __grid_constant__ qgi::W8A8Args a, int splits, int epi, unsigned *err, uint64_t timeout_ns) {
+    using G = Cfg<NH, NF, STAGES_>;
+    constexpr int STAGES = G::STAGES, ROWS = G::ROWS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align_1024(smem_raw);
+    griddep_launch_dependents();
+    const uint32_t sb = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto full_bar = [&](int s) { return sb + G::OFF_BAR + 8u * s; };
+    auto empty_bar = [&](int s) { return sb + G::OFF_BAR + 8u * (STAGES + s); };
+    float *red = reinterpret_cast<float *>(smem + G::OFF_RED);
+
+    const int nrb = (a.N + ROWS - 1) / ROWS;     // blocks of rows
+    const int nkc = (a.K + KC - 1) / KC;         // stages of all of K
+    const int rank = splits > 1 ? static_cast<int>(blockIdx.x) % splits : 0;
+    const int kc0 = static_cast<int>(int64_t(nkc) * rank / splits), kc1 = static_cast<int>(int64_t(nkc) * (rank + 1) / splits);
+    const int first = static_cast<int>(blockIdx.x) / splits, step = static_cast<int>(gridDim.x) / splits;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), CONSUMERS);
+        }
+        fence_barrier_init();
+        tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmX);
+    }
+    __syncthreads();
+    griddep_wait();
+
+    if (warp == CONSUMERS) {
+        // ------------------------------------------------------------------- producer
+        if (lane == 0) {
+            uint32_t stage = 0, phase = 0;
+            int issued = 0;
+            bool ok = true;
+            const uint64_t stream_once = l2_policy_evict_first();   // the weights are read once
+            for (int rb = first; rb < nrb && ok; rb += step) {
+                for (int kc = kc0; kc < kc1; ++kc) {
+                    // debug build: innermost coordinates multiples of 16 bytes, the box begins inside the planes
+                    if (!mbar_wait(empty_bar(stage), phase ^ 1, timeout_ns) ||
+                        !QG_IN_BOUNDS(err, (kc * KC) % 16 == 0 && kc * KC < a.K && rb * ROWS < a.N)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t st = sb + stage * G::STAGE;
+                    mbar_arrive_expect_tx(full_bar(stage), G::STAGE);
+                    tma_load_2d_hint(st, &tmW, full_bar(stage), kc * KC, rb * ROWS, stream_once);
+                    tma_load_2d(st + G::W_BYTES, &tmX, full_bar(stage), kc * KC, 0);
+                    ++issued;
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            if (!ok) atomicOr(err, ERR_PRODUCER);
+            for (int i = max(0, issued - STAGES); i < issued; ++i)
+                if (!mbar_wait(full_bar(i % STAGES), (i / STAGES) & 1, timeout_ns)) {
+                    atomicOr(err, ERR_DRAIN);
+                    break;
+                }
+        }
+        __syncwarp();
+        if (splits > 1) {
+            cluster_sync();
+            cluster_sync();
+        }
+        return;
+    }
+
+    // ---------------------------------------------------------------------- consumers
+    const int g = lane >> 2, t = lane & 3;
+    // bytes 32 w + 8 t .. + 8 of row g (the 128-byte swizzle: chunk c of row r at c ^ (r % 8)); row g + 8 is 1 KB on
+    const uint32_t off = static_cast<uint32_t>(g) * 128 +
+                         ((static_cast<uint32_t>(2 * warp + (t >> 1)) ^ static_cast<uint32_t>(g)) << 4) +
+                         static_cast<uint32_t>((t & 1) * 8);
+    uint32_t stage = 0, phase = 0;
+    bool ok = true;
+    for (int rb = first; rb < nrb; rb += step) {
+        float acc[NF][NH][4];
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+#pragma unroll
+            for (int h = 0; h < NH; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[f][h][i] = 0.0f;
+        for (int kc = kc0; kc < kc1 && ok; kc += 2) {
+            // two stages at a time: twice the independent work between waits
+            const bool two = kc + 1 < kc1;
+            uint32_t stage2 = stage + 1, phase2 = phase;
+            if (stage2 == STAGES) {
+                stage2 = 0;
+                phase2 ^= 1;
+            }
+            if (!mbar_wait_warp(full_bar(stage), phase, timeout_ns) ||
+                (two && !mbar_wait_warp(full_bar(stage2), phase2, timeout_ns))) {
+                if (lane == 0) atomicOr(err, ERR_EPILOGUE);
+                ok = false;
+                break;
+            }
+            stage_math<NH, NF>(acc, smem + stage * G::STAGE, off);
+            if (two) stage_math<NH, NF>(acc, smem + stage2 * G::STAGE, off);
+            // read through the generic proxy, written next by TMA through the async proxy
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(empty_bar(stage));
+                if (two) mbar_arrive(empty_bar(stage2));
+            }
+            stage = two ? (stage2 + 1 == STAGES ? 0 : stage2 + 1) : stage2;
+            phase = two ? (stage2 + 1 == STAGES ? phase2 ^ 1 : phase2) : phase2;
+        }
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+#pragma unroll
+            for (int h = 0; h < NH; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) red[(((warp * NF + f) * NH + h) * 4 + i) * 32 + lane] = acc[f][h][i];
+        if (splits > 1) cluster_sync();
+        else asm volatile("bar.sync 1, %0;" ::"n"(CONSUMERS * 32) : "memory");
+        // an output a thread: column r of the block, token m, over all threads of the cluster
+        for (int i = rank * CONSUMERS * 32 + static_cast<int>(threadIdx.x); i < ROWS * a.M; i += splits * CONSUMERS * 32) {
+            const int m = i / ROWS, r = i - m * ROWS, n = rb * ROWS + r;
+            if (n >= a.N) continue;
+            const uint32_t at = static_cast<uint32_t>((((r >> 4) * NH + (m >> 3)) * 4 + ((r >> 3) & 1) * 2 + (m & 1)) * 32 +
+                                                      (r & 7) * 4 + ((m & 7) >> 1));
+            float sum = 0.0f;
+            for (int c = 0; c < splits; ++c) {
+                const uint32_t base = (splits > 1 ? map_to_cta(sb + G::OFF_RED, c) : sb + G::OFF_RED) + at * 4;
+#pragma unroll
+                for (int w = 0; w < CONSUMERS; ++w) sum += ld_cluster(base + w * (NF * NH * 4 * 32 * 4));
+            }
+            uint16_t *dst = static_cast<uint16_t *>(a.C) + m * a.ldc + n;
+            const float bias = a.bias ? load_16(a.bias, n, a.bf16) : 0.0f;
+            const float old = epi & qgi::EPI_ACCUMULATE ? load_16(dst, 0, a.bf16) : 0.0f;
+            *dst = round_16(finish(sum, __ldg(a.sa + m), __ldg(a.sw + n), bias, old, epi), a.bf16);
+        }
+        if (splits > 1) {                        // one block of rows a cluster
+            cluster_sync();                      // no CTA leaves while another reads its sums
+            return;
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(CONSUMERS * 32) : "memory");
+    }
+}
+
+template <int NH, int NF, int STAGES>
+cudaError_t launch_nh(const qgi::W8A8Args &a, const qgi::LaunchCtx &ctx, bool *encode_ok) {
+    using G = Cfg<NH, NF, STAGES>;
+    CUtensorMap tmW, tmX;
+    *encode_ok =
+        qgi::encode_tma_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.W, a.K, a.N, a.ldw, KC, G::ROWS, CU_TENSOR_MAP_SWIZZLE_128B) &&
+        qgi::encode_tma_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, a.K, a.M, a.lda, KC, 8 * NH, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (!*encode_ok) return cudaErrorInvalidValue;
+    auto kern = w8a8_decode_kernel<NH, NF, STAGES>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
+    if (e != cudaSuccess) return e;
+    const int64_t nrb = (int64_t(a.N) + G::ROWS - 1) / G::ROWS;
+    const int nkc = (a.K + KC - 1) / KC;
+    const int64_t room = int64_t(ctx.num_sms) * std::max(1, int(233472 / (G::SMEM + 1024)));
+    // K over a cluster of 2, 4 or 8 CTAs while all fit at once and each keeps two stages
+    int splits = 1;
+    while (splits < 8 && nrb * splits * 2 <= room && nkc >= splits * 4) splits *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(splits > 1 ? nrb * splits : std::min(nrb, room)));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = G::SMEM;
+    cfg.stream = ctx.stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(splits);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, tmW, tmX, a, splits, ctx.epi, ctx.err, ctx.timeout_ns);
+}
+
+}  // namespace
+
+namespace qgi {
+
+cudaError_t launch_w8a8_decode(const W8A8Args &a, const LaunchCtx &ctx, bool *encode_ok) {
+    if (a.M <= 8) return launch_nh<1, 3, 6>(a, ctx, encode_ok);
+    if (a.M <= 16) return launch_nh<2, 4, 5>(a, ctx, encode_ok);
+    return launch_nh<4, 4, 5>(a, ctx, encode_ok);
+}
+
+}  // namespace qgi
