@@ -21,7 +21,7 @@ __global__ void __launch_bounds__(256) w8a8_empty_kernel(const __grid_constant__
 
 namespace qgi {
 
-constexpr int DECODE_TOKENS = 32;
+constexpr int DECODE_TOKENS = 16;
 
 cudaError_t launch_w8a8(const W8A8Args &a, const LaunchCtx &ctx, bool *encode_ok) {
     return a.M <= DECODE_TOKENS ? launch_w8a8_decode(a, ctx, encode_ok) : launch_w8a8_pair(a, ctx, encode_ok);

@@ -197,26 +197,39 @@ w8a8_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
             for (int h = 0; h < NH; ++h)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) red[(((warp * NF + f) * NH + h) * 4 + i) * 32 + lane] = acc[f][h][i];
-        if (splits > 1) cluster_sync();
-        else asm volatile("bar.sync 1, %0;" ::"n"(CONSUMERS * 32) : "memory");
-        // an output a thread: column r of the block, token m, over all threads of the cluster
-        for (int i = rank * CONSUMERS * 32 + static_cast<int>(threadIdx.x); i < ROWS * a.M; i += splits * CONSUMERS * 32) {
-            const int m = i / ROWS, r = i - m * ROWS, n = rb * ROWS + r;
-            if (n >= a.N) continue;
-            const uint32_t at = static_cast<uint32_t>((((r >> 4) * NH + (m >> 3)) * 4 + ((r >> 3) & 1) * 2 + (m & 1)) * 32 +
-                                                      (r & 7) * 4 + ((m & 7) >> 1));
-            float sum = 0.0f;
-            for (int c = 0; c < splits; ++c) {
-                const uint32_t base = (splits > 1 ? map_to_cta(sb + G::OFF_RED, c) : sb + G::OFF_RED) + at * 4;
-#pragma unroll
-                for (int w = 0; w < CONSUMERS; ++w) sum += ld_cluster(base + w * (NF * NH * 4 * 32 * 4));
-            }
+        asm volatile("bar.sync 1, %0;" ::"n"(CONSUMERS * 32) : "memory");
+        // the four warps' sums, an output a thread: column r of the block of token m
+        auto place = [&](int m, int r) {
+            return (((r >> 4) * NH + (m >> 3)) * 4 + ((r >> 3) & 1) * 2 + (m & 1)) * 32 + (r & 7) * 4 + ((m & 7) >> 1);
+        };
+        auto store = [&](int m, int n, float sum) {
             uint16_t *dst = static_cast<uint16_t *>(a.C) + m * a.ldc + n;
             const float bias = a.bias ? load_16(a.bias, n, a.bf16) : 0.0f;
             const float old = epi & qgi::EPI_ACCUMULATE ? load_16(dst, 0, a.bf16) : 0.0f;
             *dst = round_16(finish(sum, __ldg(a.sa + m), __ldg(a.sw + n), bias, old, epi), a.bf16);
+        };
+        constexpr int WARP_SUMS = NF * NH * 4 * 32;
+        for (int i = static_cast<int>(threadIdx.x); i < ROWS * a.M; i += CONSUMERS * 32) {
+            const int m = i / ROWS, r = i - m * ROWS, at = place(m, r);
+            float sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < CONSUMERS; ++w) sum += red[w * WARP_SUMS + at];
+            if (splits > 1) red[at] = sum;       // its own place: no other output reads it
+            else if (rb * ROWS + r < a.N) store(m, rb * ROWS + r, sum);
         }
-        if (splits > 1) {                        // one block of rows a cluster
+        if (splits > 1) {                        // one block of rows a cluster: its CTAs' sums, an output a thread of the cluster
+            cluster_sync();
+            for (int i = rank * CONSUMERS * 32 + static_cast<int>(threadIdx.x); i < ROWS * a.M; i += splits * CONSUMERS * 32) {
+                const int m = i / ROWS, r = i - m * ROWS, n = rb * ROWS + r;
+                const uint32_t addr = sb + G::OFF_RED + 4u * place(m, r);
+                float part[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) part[c] = c < splits ? ld_cluster(map_to_cta(addr, c)) : 0.0f;
+                float sum = 0.0f;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) sum += part[c];
+                if (n < a.N) store(m, n, sum);
+            }
             cluster_sync();                      // no CTA leaves while another reads its sums
             return;
         }
@@ -263,8 +276,7 @@ namespace qgi {
 
 cudaError_t launch_w8a8_decode(const W8A8Args &a, const LaunchCtx &ctx, bool *encode_ok) {
     if (a.M <= 8) return launch_nh<1, 3, 6>(a, ctx, encode_ok);
-    if (a.M <= 16) return launch_nh<2, 4, 5>(a, ctx, encode_ok);
-    return launch_nh<4, 4, 5>(a, ctx, encode_ok);
+    return launch_nh<2, 4, 5>(a, ctx, encode_ok);
 }
 
 }  // namespace qgi

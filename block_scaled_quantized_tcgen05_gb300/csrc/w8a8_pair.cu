@@ -16,7 +16,9 @@
 //     in shared memory;
 //   * the epilogue reads D (lane = weight row, column = token), applies the scales, and writes through shared
 //     memory and TMA stores where C allows a tensor map;
-//   * few tiles: K is split over several pairs, whose fp32 partial planes a reduction kernel adds in order.
+//   * tiles go to the pairs in whole waves; what is left after them (all, where there are fewer tiles than pairs) is
+//     cut into equal ranges of K, one a pair, whatever tiles they cover: a tile that several pairs share leaves fp32 partial
+//     sums in scratch, which a reduction kernel adds in the order of K.
 #include <algorithm>
 
 #include "qgemm_common.cuh"
@@ -60,17 +62,58 @@ __device__ __forceinline__ void st_shared_u16(uint32_t addr, uint16_t v) {
     asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
 }
 
-enum Out { OUT_F16, OUT_BF16, OUT_PARTIAL };
+// The pairs' work: `full` tiles in whole waves over `pairs` pairs, then the other `rest` tiles' k-tiles (units) in
+// equal ranges over `sharers` pairs (rest <= sharers <= pairs, and no range is empty).  sharers == rest: whole tiles.
+struct Shares {
+    int pairs, full, rest, sharers, KT;
+    __host__ __device__ int64_t begin(int p) const { return int64_t(p) * rest * KT / sharers; }
+    // the pair whose range holds unit u: the last p with p U / sharers < u + 1
+    __device__ int owner(int64_t u) const { return static_cast<int>(((u + 1) * sharers - 1) / (int64_t(rest) * KT)); }
+};
 
-template <int BT, int OUT>
+// The items of one pair in order: (tile, k-tiles kt0 .. kt1, slot of its partial sums or -1 for a whole tile).
+struct Items {
+    const Shares &s;
+    int p, i;
+    int64_t u0, u, u1;
+    __device__ Items(const Shares &sh, int pair) : s(sh), p(pair), i(pair), u0(0), u(0), u1(0) {
+        if (pair < sh.sharers) {
+            u0 = u = sh.begin(pair);
+            u1 = sh.begin(pair + 1);
+        }
+    }
+    __device__ __forceinline__ bool next(int &tile, int &kt0, int &kt1, int &slot) {
+        slot = -1;
+        if (i < s.full) {
+            tile = i;
+            kt0 = 0;
+            kt1 = s.KT;
+            i += s.pairs;
+            return true;
+        }
+        if (u >= u1) return false;
+        const int t = static_cast<int>(u / s.KT);
+        tile = s.full + t;
+        kt0 = static_cast<int>(u - int64_t(t) * s.KT);
+        kt1 = static_cast<int>(min(int64_t(s.KT), kt0 + (u1 - u)));
+        if (kt1 - kt0 < s.KT) slot = 2 * p + (u == u0 ? 0 : 1);
+        u += kt1 - kt0;
+        return true;
+    }
+    __device__ int total() const {               // k-tiles of all of them
+        const int waves = s.full / s.pairs;
+        return waves * s.KT + static_cast<int>(u1 - u0);
+    }
+};
+
+template <int BT, int BF16>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                  const __grid_constant__ CUtensorMap tmC, int c_tma, const __grid_constant__ qgi::W8A8Args a,
-                 int splits, float *__restrict__ P, int64_t ldp, int epi, unsigned *err, uint64_t timeout_ns) {
+                 const __grid_constant__ Shares shares, float *__restrict__ P, int epi, unsigned *err,
+                 uint64_t timeout_ns) {
     using G = Cfg<BT>;
     constexpr int STAGES = G::STAGES;
-    constexpr bool PARTIAL = OUT == OUT_PARTIAL;
-    constexpr int BF16 = OUT == OUT_BF16;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align_1024(smem_raw);
     griddep_launch_dependents();
@@ -79,7 +122,6 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
     const uint32_t lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();      // 0 = leader
     const int pair = blockIdx.x >> 1;
-    const int npairs = gridDim.x >> 1;
     const int M = a.M, N = a.N;
 
     auto full_bar = [&](int s) { return sb + G::OFF_BAR + 8u * s; };
@@ -90,22 +132,9 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
     const uint32_t drain_bar = tmem_full + 16;
     volatile uint32_t *slot = reinterpret_cast<volatile uint32_t *>(smem + G::OFF_SLOT);
 
-    // tiles: weight-row blocks of 256 (the "m" of tile_coords) x token blocks of BT; work items (tile, range of K)
+    // tiles: weight-row blocks of 256 (the "m" of tile_coords) x token blocks of BT
     const int tiles_w = (N + 2 * BW - 1) / (2 * BW);
     const int tiles_t = (M + BT - 1) / BT;
-    const int num_tiles = tiles_w * tiles_t;
-    const int KT = (a.K + BK - 1) / BK;
-    const int num_items = num_tiles * splits;
-    auto item_of = [&](int it, int &tile, int &split, int &kt0, int &kt1) {
-        if constexpr (PARTIAL) {
-            split_item(it, num_tiles, splits, KT, 1, tile, split, kt0, kt1);
-        } else {
-            tile = it;
-            split = 0;
-            kt0 = 0;
-            kt1 = KT;
-        }
-    };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -138,9 +167,8 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
         uint32_t stage = 0, phase = 0;
         int issued = 0;
         bool ok = true;
-        for (int it = pair; it < num_items && ok; it += npairs) {
-            int tile, split, kt0, kt1, wb, tb;
-            item_of(it, tile, split, kt0, kt1);
+        int tile, kt0, kt1, where, wb, tb;
+        for (Items items(shares, pair); ok && items.next(tile, kt0, kt1, where);) {
             tile_coords(tile, tiles_w, tiles_t, wb, tb);
             const int w0 = wb * 2 * BW + static_cast<int>(rank) * BW;     // this CTA's weights
             const int t0 = tb * BT + static_cast<int>(rank) * (BT / 2);   // this CTA's tokens
@@ -185,9 +213,8 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
             const uint64_t bdesc0 = smem_desc(sb, 16, 1024, SWZ_128B);
             uint32_t acc_phase = 0, stage = 0, phase = 0;
             bool ok = true;
-            for (int it = pair; it < num_items && ok; it += npairs) {
-                int tile, split, kt0, kt1;
-                item_of(it, tile, split, kt0, kt1);
+            int tile, kt0, kt1, where;
+            for (Items items(shares, pair); ok && items.next(tile, kt0, kt1, where);) {
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(tmem_empty, acc_phase ^ 1, timeout_ns))) {
                     ok = false;
                     break;
@@ -235,12 +262,7 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
         const int parity = static_cast<int>(warp - CONV_WARP0) >> 2;
         const uint32_t lead_full = map_to_cta(full_bar(0), 0);
         const uint32_t r = q * 32 + lane;
-        int total = 0;                           // this pair's k-tiles over all its items
-        for (int it = pair; it < num_items; it += npairs) {
-            int tile, split, kt0, kt1;
-            item_of(it, tile, split, kt0, kt1);
-            total += kt1 - kt0;
-        }
+        const int total = Items(shares, pair).total();
         uint32_t stage = static_cast<uint32_t>(parity), phase = 0;
         const uint8_t *row = smem + G::OFF_RAW + r * BK;
         const uint32_t swz = (r >> 1) & 3;       // the 64-byte swizzle: chunk c of row r lies at c ^ (r / 2 % 4)
@@ -282,15 +304,15 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
         const uint32_t lead_empty = map_to_cta(tmem_empty, 0);
         float *sa_room = reinterpret_cast<float *>(smem + G::OFF_SA) + (warp - 2) * (BT / 2);
         uint32_t acc_phase = 0;
-        for (int it = pair; it < num_items; it += npairs) {
-            int tile, split, kt0, kt1, wb, tb;
-            item_of(it, tile, split, kt0, kt1);
+        int tile, kt0, kt1, where, wb, tb;
+        for (Items items(shares, pair); items.next(tile, kt0, kt1, where);) {
+            const bool partial = where >= 0;
             tile_coords(tile, tiles_w, tiles_t, wb, tb);
             const int n0 = wb * 2 * BW + static_cast<int>(rank) * BW + static_cast<int>(q * 32);
             const int n = n0 + static_cast<int>(lane);
             const int m0 = tb * BT + static_cast<int>(half) * (BT / 2);
             float sw = 0.0f, bias = 0.0f;
-            if constexpr (!PARTIAL) {            // while the tile's MMAs run
+            if (!partial) {                      // while the tile's MMAs run
                 if (n < N) {
                     sw = __ldg(a.sw + n);
                     if (a.bias) bias = load_16(a.bias, n, BF16);
@@ -306,7 +328,7 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
             }
             tc_fence_after();
             const uint32_t stg = sb + G::OFF_EPI + (warp - 2) * G::EPI_BYTES;
-            if (!PARTIAL && c_tma) {             // the previous tile's stores have finished reading the staging
+            if (!partial && c_tma) {             // the previous tile's stores have finished reading the staging
                 if (lane == 0) bulk_wait_read<0>();
                 __syncwarp();
             }
@@ -321,15 +343,12 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                     if (lane == 0) mbar_arrive_relaxed_cluster(lead_empty);
                 }
                 const int mc = m0 + ch * 32;
-                if constexpr (PARTIAL) {
-                    // this range's sums into its partial plane, [token][weight row]: a store writes 32
-                    // consecutive floats of a token's row
-                    float *pl = P + (static_cast<int64_t>(split) * M + mc) * ldp + n;
-                    if (n < N) {
+                if (partial) {
+                    // this range's sums, [token of the tile][weight row]: a store writes 32 consecutive floats
+                    float *pl = P + (int64_t(where) * BT + half * (BT / 2) + ch * 32) * (2 * BW) + rank * BW + q * 32 + lane;
 #pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (mc + c < M) pl[c * ldp] = __uint_as_float(v[c]);
-                    }
+                    for (int c = 0; c < 32; ++c)
+                        if (mc + c < M) pl[c * (2 * BW)] = __uint_as_float(v[c]);
                 } else {
 #pragma unroll
                     for (int c = 0; c < 32; c += 4) {
@@ -352,7 +371,7 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                     }
                 }
             }
-            if (!PARTIAL && c_tma) {
+            if (!partial && c_tma) {
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -364,7 +383,7 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
             }
             acc_phase ^= 1;
         }
-        if (!PARTIAL && c_tma && lane == 0) bulk_wait_all();
+        if (c_tma && lane == 0) bulk_wait_all();
     }
 
     tc_fence_before();
@@ -406,60 +425,81 @@ __global__ void __launch_bounds__(256) codes_to_f16_kernel(const int8_t *__restr
     }
 }
 
-// C from the partial planes, added in order: four columns a thread.
-__global__ void __launch_bounds__(256) w8a8_reduce_kernel(const float *__restrict__ P, int splits, int64_t ldp,
+// The tiles that several pairs shared, from their partial sums in the order of K: four columns a thread, four
+// tokens' rows of 256 columns a block.
+template <int BT>
+__global__ void __launch_bounds__(256) w8a8_reduce_kernel(const float *__restrict__ P, const __grid_constant__ Shares shares,
                                                           const __grid_constant__ qgi::W8A8Args a, int vec, int epi) {
     griddep_launch_dependents();
     griddep_wait();
-    const int groups = (a.N + 3) / 4;
-    const int64_t total = static_cast<int64_t>(a.M) * groups, plane = a.M * ldp;
-    for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < total; i += gridDim.x * int64_t(256)) {
-        const int64_t m = i / groups;
-        const int n = static_cast<int>(i - m * groups) * 4;
-        const float *p = P + m * ldp + n;
-        float4 sum = __ldcg(reinterpret_cast<const float4 *>(p));
-        for (int s = 1; s < splits; ++s) {
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p + s * plane));
-            sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
-        }
-        const float sa = __ldg(a.sa + m), sums[4] = {sum.x, sum.y, sum.z, sum.w};
-        uint16_t *dst = static_cast<uint16_t *>(a.C) + m * a.ldc + n;
-        uint16_t out[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (n + j >= a.N) break;
-            const float bias = a.bias ? load_16(a.bias, n + j, a.bf16) : 0.0f;
-            const float old = epi & qgi::EPI_ACCUMULATE ? load_16(dst, j, a.bf16) : 0.0f;
-            out[j] = round_16(finish(sums[j], sa, __ldg(a.sw + n + j), bias, old, epi), a.bf16);
-            if (!vec || n + 4 > a.N) dst[j] = out[j];
-        }
-        if (vec && n + 4 <= a.N)
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(out[0] | uint32_t(out[1]) << 16, out[2] | uint32_t(out[3]) << 16);
+    const int t = blockIdx.x / (BT / 4), part = blockIdx.x % (BT / 4);
+    const int p0 = shares.owner(int64_t(t) * shares.KT), p1 = shares.owner(int64_t(t + 1) * shares.KT - 1);
+    if (p0 == p1) return;                        // a whole tile, written by its pair
+    int wb, tb;
+    tile_coords(shares.full + t, (a.N + 2 * BW - 1) / (2 * BW), (a.M + BT - 1) / BT, wb, tb);
+    const int token = 4 * part + static_cast<int>(threadIdx.x >> 6), col = 4 * static_cast<int>(threadIdx.x & 63);
+    const int64_t m = int64_t(tb) * BT + token;
+    const int n = wb * 2 * BW + col;
+    if (m >= a.M || n >= a.N) return;
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int p = p0; p <= p1; ++p) {
+        // the tile's piece is the first of the pair's range where the range begins inside the tile or at its start
+        const int64_t slot = 2 * int64_t(p) + (shares.begin(p) >= int64_t(t) * shares.KT ? 0 : 1);
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(P + (slot * BT + token) * (2 * BW) + col));
+        sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
     }
+    const float sa = __ldg(a.sa + m), sums[4] = {sum.x, sum.y, sum.z, sum.w};
+    uint16_t *dst = static_cast<uint16_t *>(a.C) + m * a.ldc + n;
+    uint16_t out[4] = {0, 0, 0, 0};
+    const bool whole = vec && n + 4 <= a.N;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (n + j >= a.N) break;
+        const float bias = a.bias ? load_16(a.bias, n + j, a.bf16) : 0.0f;
+        const float old = epi & qgi::EPI_ACCUMULATE ? load_16(dst, j, a.bf16) : 0.0f;
+        out[j] = round_16(finish(sums[j], sa, __ldg(a.sw + n + j), bias, old, epi), a.bf16);
+        if (!whole) dst[j] = out[j];
+    }
+    if (whole) *reinterpret_cast<uint2 *>(dst) = make_uint2(out[0] | uint32_t(out[1]) << 16, out[2] | uint32_t(out[3]) << 16);
 }
 
-struct Plan {
-    int bt, splits;
-};
+// Work of M tokens in tiles of bt.
+Shares share(int bt, int M, int N, int K, int num_sms) {
+    Shares s;
+    s.KT = (K + BK - 1) / BK;
+    const int most = std::max(1, num_sms / 2);
+    const int64_t tiles = int64_t((N + 2 * BW - 1) / (2 * BW)) * ((M + bt - 1) / bt);
+    s.pairs = most;
+    s.full = static_cast<int>(tiles / most * most);
+    s.rest = static_cast<int>(tiles - s.full);
+    // The rest in equal ranges of at least 4 k-tiles, unless it nearly fills a wave as it is (then sharing would gain an
+    // eighth of a wave at most and cost the reduction).
+    s.sharers = s.rest;
+    if (8 * s.rest < 7 * most)
+        s.sharers = static_cast<int>(std::max<int64_t>(s.rest, std::min<int64_t>(most, int64_t(s.rest) * s.KT / 4)));
+    if (s.full == 0) s.pairs = s.sharers;
+    return s;
+}
 
-// The tile's tokens and the split of K: the cheapest by a count of rounds over the pairs.
-Plan choose(int M, int N, int K, int num_sms) {
-    const int pairs = std::max(1, num_sms / 2), KT = (K + BK - 1) / BK;
-    const int64_t tiles_w = (N + 2 * BW - 1) / (2 * BW);
-    Plan best{256, 1};
+// Estimated us: k-tiles one pair walks, the ends of its tiles, and the reduction.
+double cost(int bt, const Shares &s) {
+    const double per_kt = bt == 256 ? 0.27 : 0.19, ends = bt == 256 ? 2.5 : 1.5;
+    const double mine = s.rest ? double(s.rest) * s.KT / s.sharers : 0.0;
+    const int waves = s.pairs ? s.full / s.pairs : 0;
+    double us = waves * (s.KT * per_kt + ends) + (s.rest ? mine * per_kt + ends : 0.0);
+    if (s.sharers > s.rest) us += 2.0 + (s.sharers + s.rest) * bt * 256 * 8 / 4e6;
+    return us;
+}
+
+// The tile's tokens: the cheapest.
+int choose(int M, int N, int K, int num_sms) {
+    int best = 256;
     double least = 1e300;
     for (int bt : {64, 128, 256}) {
-        const int64_t tiles = tiles_w * ((M + bt - 1) / bt);
-        // us of a k-tile on every pair at once, of a tile's start and end, of a partial plane
-        const double per_kt = bt == 256 ? 0.27 : 0.19, ends = bt == 256 ? 2.5 : 1.5;
-        const double plane = double(M) * double(tiles_w) * 256 * 8 / 4e6;
-        for (int s = 1; s <= 16 && (s == 1 || KT / s >= 4); ++s) {
-            const double rounds = double((tiles * s + pairs - 1) / pairs);
-            const double cost = rounds * ((KT + s - 1) / s * per_kt + ends) + (s > 1 ? 2.0 + s * plane : 0.0);
-            if (cost < least) {
-                least = cost;
-                best = {bt, s};
-            }
+        const double us = cost(bt, share(bt, M, N, K, num_sms));
+        if (us < least) {
+            least = us;
+            best = bt;
         }
     }
     return best;
@@ -467,16 +507,16 @@ Plan choose(int M, int N, int K, int num_sms) {
 
 template <int BT>
 cudaError_t launch_bt(const qgi::W8A8Args &a, const CUtensorMap &tmX, const CUtensorMap &tmW, const CUtensorMap &tmC,
-                      int c_tma, int splits, float *P, int64_t ldp, const qgi::LaunchCtx &ctx) {
-    const int64_t items = int64_t((a.N + 2 * BW - 1) / (2 * BW)) * ((a.M + BT - 1) / BT) * splits;
-    const int pairs = static_cast<int>(std::min<int64_t>(items, std::max(1, ctx.num_sms / 2)));
-    auto kern = splits > 1 ? w8a8_pair_kernel<BT, OUT_PARTIAL>
-                : a.bf16   ? w8a8_pair_kernel<BT, OUT_BF16>
-                           : w8a8_pair_kernel<BT, OUT_F16>;
+                      int c_tma, const Shares &shares, float *P, const qgi::LaunchCtx &ctx) {
+    auto kern = a.bf16 ? w8a8_pair_kernel<BT, 1> : w8a8_pair_kernel<BT, 0>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<BT>::SMEM);
     if (e == cudaSuccess)
-        e = launch_dependent(kern, dim3(2 * pairs), THREADS, Cfg<BT>::SMEM, ctx.stream, tmX, tmW, tmC, c_tma, a, splits, P,
-                             ldp, ctx.epi, ctx.err, ctx.timeout_ns);
+        e = launch_dependent(kern, dim3(2 * shares.pairs), THREADS, Cfg<BT>::SMEM, ctx.stream, tmX, tmW, tmC, c_tma, a, shares, P,
+                             ctx.epi, ctx.err, ctx.timeout_ns);
+    if (e == cudaSuccess && shares.sharers > shares.rest) {
+        const int vec = reinterpret_cast<uintptr_t>(a.C) % 8 == 0 && a.ldc % 4 == 0;
+        e = launch_dependent(w8a8_reduce_kernel<BT>, dim3(shares.rest * (BT / 4)), 256, 0, ctx.stream, P, shares, a, vec, ctx.epi);
+    }
     return e;
 }
 
@@ -491,14 +531,14 @@ namespace qgi {
 // A product of many tokens is taken in slices of rows, so that the tokens' halves never hold more scratch than this.
 constexpr int64_t SLICE_BYTES = int64_t(1) << 29;
 
-static cudaError_t launch_slice(const W8A8Args &a, uint16_t *H, int64_t ldh, float *P, int64_t ldp, const Plan &plan,
+static cudaError_t launch_slice(const W8A8Args &a, uint16_t *H, int64_t ldh, float *P, int bt, const Shares &shares,
                                 const CUtensorMap &tmW, const LaunchCtx &ctx, bool *encode_ok) {
     // Output through TMA stores where C allows a tensor map.  They write whole 16-byte units, past a row's end too
     // where N is no multiple of 8 (measured); accumulating reads the old C: direct stores in both cases.
-    const int c_tma = plan.splits == 1 && reinterpret_cast<uintptr_t>(a.C) % 16 == 0 && a.ldc % 8 == 0 && a.N % 8 == 0 &&
+    const int c_tma = reinterpret_cast<uintptr_t>(a.C) % 16 == 0 && a.ldc % 8 == 0 && a.N % 8 == 0 &&
                       a.ldc < (int64_t(1) << 39) && !(ctx.epi & EPI_ACCUMULATE);
     CUtensorMap tmX, tmC;
-    *encode_ok = encode_tma_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, H, a.K, a.M, ldh * 2, BK, plan.bt / 2,
+    *encode_ok = encode_tma_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, H, a.K, a.M, ldh * 2, BK, bt / 2,
                                CU_TENSOR_MAP_SWIZZLE_128B);
     if (*encode_ok && c_tma)
         *encode_ok = encode_tma_2d(&tmC, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.C, a.N, a.M, a.ldc * 2, 32, 32,
@@ -509,23 +549,21 @@ static cudaError_t launch_slice(const W8A8Args &a, uint16_t *H, int64_t ldh, flo
     cudaError_t e = launch_dependent(codes_to_f16_kernel, dim3(grid_for(a.M * int64_t((a.K + 15) / 16), ctx)), 256, 0,
                                      ctx.stream, a.A, a.lda, a.M, a.K, H, ldh);
     if (e == cudaSuccess)
-        e = plan.bt == 64    ? launch_bt<64>(a, tmX, tmW, tmC, c_tma, plan.splits, P, ldp, ctx)
-            : plan.bt == 128 ? launch_bt<128>(a, tmX, tmW, tmC, c_tma, plan.splits, P, ldp, ctx)
-                             : launch_bt<256>(a, tmX, tmW, tmC, c_tma, plan.splits, P, ldp, ctx);
-    if (e == cudaSuccess && plan.splits > 1) {
-        const int vec = reinterpret_cast<uintptr_t>(a.C) % 8 == 0 && a.ldc % 4 == 0;
-        e = launch_dependent(w8a8_reduce_kernel, dim3(grid_for(a.M * int64_t((a.N + 3) / 4), ctx)), 256, 0, ctx.stream, P,
-                             plan.splits, ldp, a, vec, ctx.epi);
-    }
+        e = bt == 64    ? launch_bt<64>(a, tmX, tmW, tmC, c_tma, shares, P, ctx)
+            : bt == 128 ? launch_bt<128>(a, tmX, tmW, tmC, c_tma, shares, P, ctx)
+                        : launch_bt<256>(a, tmX, tmW, tmC, c_tma, shares, P, ctx);
     return e;
 }
 
 cudaError_t launch_w8a8_pair(const W8A8Args &a, const LaunchCtx &ctx, bool *encode_ok) {
-    const int64_t ldh = (a.K + 63) / 64 * int64_t(64), ldp = (a.N + 255) / 256 * int64_t(256);
+    const int64_t ldh = (a.K + 63) / 64 * int64_t(64);
     const int slice = static_cast<int>(std::min<int64_t>(a.M, std::max<int64_t>(SLICE_BYTES / (2 * ldh) / 256 * 256, 256)));
-    const Plan plan = choose(slice, a.N, a.K, ctx.num_sms);
+    const int bt = choose(slice, a.N, a.K, ctx.num_sms);
+    const int last = a.M % slice ? a.M % slice : slice;
+    const Shares shares = share(bt, slice, a.N, a.K, ctx.num_sms), last_shares = share(bt, last, a.N, a.K, ctx.num_sms);
     const size_t x_bytes = (static_cast<size_t>(slice) * ldh * 2 + 255) / 256 * 256;
-    const size_t p_bytes = plan.splits > 1 ? static_cast<size_t>(plan.splits) * slice * ldp * 4 : 0;
+    const bool shared = shares.sharers > shares.rest || last_shares.sharers > last_shares.rest;
+    const size_t p_bytes = shared ? static_cast<size_t>(std::max(shares.sharers, last_shares.sharers)) * 2 * bt * (2 * BW) * 4 : 0;
     CUtensorMap tmW;
     *encode_ok = encode_tma_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.W, a.K, a.N, a.ldw, BK, BW, CU_TENSOR_MAP_SWIZZLE_64B);
     if (!*encode_ok) return cudaErrorInvalidValue;
@@ -539,7 +577,7 @@ cudaError_t launch_w8a8_pair(const W8A8Args &a, const LaunchCtx &ctx, bool *enco
         part.C = static_cast<uint16_t *>(a.C) + m0 * a.ldc;
         part.M = static_cast<int>(std::min<int64_t>(slice, a.M - m0));
         e = launch_slice(part, static_cast<uint16_t *>(ws), ldh, reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + x_bytes),
-                         ldp, plan, tmW, ctx, encode_ok);
+                         bt, part.M == slice ? shares : last_shares, tmW, ctx, encode_ok);
     }
     const cudaError_t f = scratch_free(ws, ctx);
     return e != cudaSuccess ? e : f;
