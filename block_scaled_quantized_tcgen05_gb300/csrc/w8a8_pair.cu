@@ -18,7 +18,8 @@
 //     memory and TMA stores where C allows a tensor map;
 //   * tiles go to the pairs in whole waves; what is left after them (all, where there are fewer tiles than pairs) is
 //     cut into equal ranges of K, one a pair, whatever tiles they cover: a tile that several pairs share leaves fp32 partial
-//     sums in scratch, which a reduction kernel adds in the order of K.
+//     sums in scratch, which a reduction kernel adds in the order of K.  (The warp that finishes a piece last adding them at the
+//     kernel's end instead: 4096 x 14336 x 4096 in 310 us against 294, 256 x 4096 x 4096 29 against 21: too few loads in flight.)
 #include <algorithm>
 
 #include "qgemm_common.cuh"
@@ -29,18 +30,23 @@ namespace {
 using namespace qg;
 
 constexpr int BW = 128;                 // weight rows per CTA (256 per pair: the MMA's M)
-constexpr int BK = 64;                  // k per stage
 constexpr int EPI_WARPS = 8;            // two per lane quarter, one per half of the tokens
 constexpr int CONV_WARP0 = 2 + EPI_WARPS;
-constexpr int CONV_WARPS = 8;           // two per lane quarter, alternate k-tiles
+constexpr int CONV_WARPS = 8;           // two per lane quarter: alternate stages of 64 k, or a half each of every 128 k
 constexpr int THREADS = 32 * (CONV_WARP0 + CONV_WARPS);
 constexpr uint32_t TMEM_COLS = 512;
-constexpr uint32_t A_COLS = BK / 2;     // TMEM columns of a stage's weights
 
 template <int BT>
 struct Cfg {
-    static constexpr int STAGES = BT == 256 ? 6 : BT == 128 ? 10 : 14;        // even: a converter warp keeps its parity
-    static constexpr uint32_t X_BYTES = (BT / 2) * BK * 2;
+    static constexpr int BK = BT == 256 ? 64 : 128;                           // k per stage
+    static constexpr int STAGES = BT == 256 ? 6 : BT == 128 ? 5 : 7;
+    static constexpr int TURNS = BK == 64 ? 2 : 1;                            // a converter warp takes every TURNS-th stage
+    // A warp that passes over stages must come back to the same ones: it would otherwise miss phases of their barriers, whose
+    // parity then no longer tells them apart.
+    static_assert(STAGES % TURNS == 0, "stages in turn");
+    static constexpr uint32_t A_COLS = BK / 2;                                // TMEM columns of a stage's weights
+    static constexpr uint32_t X_HALF = (BT / 2) * 128;                        // 64 k of the tokens: rows of 128 bytes
+    static constexpr uint32_t X_BYTES = X_HALF * (BK / 64);
     static constexpr uint32_t RAW_BYTES = BW * BK;
     static constexpr uint32_t STAGE_TX = 2 * X_BYTES;                         // both CTAs' tokens, on the leader
     static constexpr int CHUNKS = BT / 64;                                    // 32-token chunks of an epilogue warp
@@ -113,7 +119,8 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                  const __grid_constant__ Shares shares, float *__restrict__ P, int epi, unsigned *err,
                  uint64_t timeout_ns) {
     using G = Cfg<BT>;
-    constexpr int STAGES = G::STAGES;
+    constexpr int STAGES = G::STAGES, BK = G::BK;
+    constexpr uint32_t A_COLS = G::A_COLS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align_1024(smem_raw);
     griddep_launch_dependents();
@@ -138,7 +145,7 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(full_bar(s), 1 + 2 * (CONV_WARPS / 2));   // expect_tx + converters of a stage
+            mbar_init(full_bar(s), 1 + 2 * (CONV_WARPS / G::TURNS));   // expect_tx + converters of a stage
             mbar_init(empty_bar(s), 1);                          // leader's multicast commit
             mbar_init(raw_full(s), 1);                           // this CTA's raw weights
         }
@@ -159,7 +166,6 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
     cluster_sync();                   // barriers of both CTAs initialised before remote use
     tc_fence_after();
     const uint32_t tmem_base = *slot;
-    griddep_wait();                   // the tokens' halves, and whatever made the other operands
 
     if (warp == 0) {
         // ---------------------------------------------------------------- producer
@@ -168,6 +174,19 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
         int issued = 0;
         bool ok = true;
         int tile, kt0, kt1, where, wb, tb;
+        auto issue_raw = [&](int s, int kt, int w0) {            // by the elected lane
+            mbar_arrive_expect_tx(raw_full(s), G::RAW_BYTES);
+            tma_load_2d(sb + G::OFF_RAW + s * G::RAW_BYTES, &tmW, raw_full(s), kt * BK, w0);
+        };
+        // The first stages' weights before the wait: the kernel ahead of this one makes the tokens' halves, touches no weights
+        // and has let this one start only after all work ahead of it was done.
+        int early = 0;
+        for (Items items(shares, pair); early < STAGES && items.next(tile, kt0, kt1, where);) {
+            tile_coords(tile, tiles_w, tiles_t, wb, tb);
+            for (int kt = kt0; kt < kt1 && early < STAGES; ++kt, ++early)
+                if (elect_one()) issue_raw(early, kt, wb * 2 * BW + static_cast<int>(rank) * BW);
+        }
+        griddep_wait();
         for (Items items(shares, pair); ok && items.next(tile, kt0, kt1, where);) {
             tile_coords(tile, tiles_w, tiles_t, wb, tb);
             const int w0 = wb * 2 * BW + static_cast<int>(rank) * BW;     // this CTA's weights
@@ -185,9 +204,10 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                 const uint32_t lead_full = map_to_cta(full_bar(stage), 0);
                 if (elect_one()) {
                     if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), G::STAGE_TX);
-                    tma_load_2d_pair(sb + stage * G::X_BYTES, &tmX, lead_full, kt * BK, t0);
-                    mbar_arrive_expect_tx(raw_full(stage), G::RAW_BYTES);
-                    tma_load_2d(sb + G::OFF_RAW + stage * G::RAW_BYTES, &tmW, raw_full(stage), kt * BK, w0);
+#pragma unroll
+                    for (int h = 0; h < BK / 64; ++h)   // past K's end: zeros
+                        tma_load_2d_pair(sb + stage * G::X_BYTES + h * G::X_HALF, &tmX, lead_full, kt * BK + h * 64, t0);
+                    if (issued >= early) issue_raw(stage, kt, w0);
                 }
                 __syncwarp();
                 ++issued;
@@ -198,14 +218,13 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
             }
         }
         if (!ok && lane == 0) atomicOr(err, ERR_PRODUCER);
-        for (int i = max(0, issued - STAGES); i < issued; ++i) {
-            const bool drained = mbar_wait(raw_full(i % STAGES), (i / STAGES) & 1, timeout_ns) &&
-                                 (rank != 0 || mbar_wait_cluster(full_bar(i % STAGES), (i / STAGES) & 1, timeout_ns));
-            if (!__all_sync(0xFFFFFFFFu, drained)) {
-                if (lane == 0) atomicOr(err, ERR_DRAIN);
-                break;
-            }
-        }
+        bool drained = true;                     // no copy may land after the CTA has left
+        const int raws = max(issued, early);
+        for (int i = max(0, raws - STAGES); i < raws && drained; ++i)
+            drained = mbar_wait_warp(raw_full(i % STAGES), (i / STAGES) & 1, timeout_ns);
+        for (int i = max(0, issued - STAGES); rank == 0 && i < issued && drained; ++i)
+            drained = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(full_bar(i % STAGES), (i / STAGES) & 1, timeout_ns));
+        if (!drained && lane == 0) atomicOr(err, ERR_DRAIN);
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0) {
@@ -229,10 +248,10 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                     const uint32_t a_col = tmem_base + G::A_COL0 + stage * A_COLS;
                     const uint64_t bdesc = bdesc0 + stage * (G::X_BYTES >> 4);
                     if (elect_one()) {
-                        mma_f16_pair_ta(tmem_base, a_col, bdesc, G::IDESC, kt > kt0 ? 1u : 0u);
 #pragma unroll
-                        for (uint32_t j = 1; j < BK / 16; ++j)
-                            mma_f16_pair_ta(tmem_base, a_col + 8 * j, bdesc + 2 * j, G::IDESC, 1u);
+                        for (uint32_t j = 0; j < BK / 16; ++j)
+                            mma_f16_pair_ta(tmem_base, a_col + 8 * j, bdesc + (j / 4) * (G::X_HALF >> 4) + 2 * (j % 4),
+                                            G::IDESC, kt > kt0 || j > 0 ? 1u : 0u);
                         tc_commit_pair(empty_bar(stage), 3);
                     }
                     __syncwarp();
@@ -256,17 +275,19 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
         if (!mbar_wait(drain_bar, 0, timeout_ns) && lane == 0) atomicOr(err, ERR_DRAIN);
     } else if (warp >= CONV_WARP0) {
         // ----------------------------------------------------------------- converters
-        // Lane i of a warp of lane quarter q converts weight row 32 q + i of this CTA's 128; the two warps
-        // of a quarter take the even and the odd stages of the sequence of this pair's k-tiles.
+        // Lane i of a warp of lane quarter q converts weight row 32 q + i of this CTA's 128, 64 k at a time.
         const uint32_t q = warp & 3;
-        const int parity = static_cast<int>(warp - CONV_WARP0) >> 2;
+        const int which = static_cast<int>(warp - CONV_WARP0) >> 2;      // of the quarter's two warps
+        const int first = G::TURNS == 2 ? which : 0;
+        const uint32_t h = G::TURNS == 2 ? 0 : which;
         const uint32_t lead_full = map_to_cta(full_bar(0), 0);
         const uint32_t r = q * 32 + lane;
         const int total = Items(shares, pair).total();
-        uint32_t stage = static_cast<uint32_t>(parity), phase = 0;
+        uint32_t stage = static_cast<uint32_t>(first), phase = 0;
         const uint8_t *row = smem + G::OFF_RAW + r * BK;
-        const uint32_t swz = (r >> 1) & 3;       // the 64-byte swizzle: chunk c of row r lies at c ^ (r / 2 % 4)
-        for (int i = parity; i < total; i += 2) {
+        // TMA's swizzle: chunk c of row r lies at c ^ (r % 8) of 128 bytes, or c ^ (r / 2 % 4) of 64
+        const uint32_t swz = BK == 128 ? r & 7 : (r >> 1) & 3;
+        for (int i = first; i < total; i += G::TURNS) {
             if (!mbar_wait(raw_full(stage), phase, timeout_ns)) {
                 if (lane == 0) atomicOr(err, ERR_PRODUCER);
                 break;
@@ -276,20 +297,20 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
             uint32_t out[32];
 #pragma unroll
             for (uint32_t c = 0; c < 4; ++c) {
-                const uint4 d = *reinterpret_cast<const uint4 *>(raw + ((c ^ swz) << 4));
+                const uint4 d = *reinterpret_cast<const uint4 *>(raw + (((4 * h + c) ^ swz) << 4));
                 i8x4_to_f16(d.x, out[8 * c], out[8 * c + 1]);
                 i8x4_to_f16(d.y, out[8 * c + 2], out[8 * c + 3]);
                 i8x4_to_f16(d.z, out[8 * c + 4], out[8 * c + 5]);
                 i8x4_to_f16(d.w, out[8 * c + 6], out[8 * c + 7]);
             }
-            tmem_st_32x32b_x32(tmem_base + ((q * 32) << 16) + G::A_COL0 + stage * A_COLS, out);
+            tmem_st_32x32b_x32(tmem_base + ((q * 32) << 16) + G::A_COL0 + stage * A_COLS + 32 * h, out);
             tmem_wait_st();
             tc_fence_before();
             // the raw weights were read through the generic proxy; the slot's next fill is a TMA write
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive_relaxed_cluster(lead_full + 8u * stage);
-            stage += 2;
+            stage += G::TURNS;
             if (stage >= STAGES) {
                 stage -= STAGES;
                 phase ^= 1;
@@ -302,76 +323,74 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
         const uint32_t q = warp & 3;
         const uint32_t half = (warp - 2) >> 2;
         const uint32_t lead_empty = map_to_cta(tmem_empty, 0);
+        const uint32_t stg = sb + G::OFF_EPI + (warp - 2) * G::EPI_BYTES;
         float *sa_room = reinterpret_cast<float *>(smem + G::OFF_SA) + (warp - 2) * (BT / 2);
         uint32_t acc_phase = 0;
+        griddep_wait();
         int tile, kt0, kt1, where, wb, tb;
         for (Items items(shares, pair); items.next(tile, kt0, kt1, where);) {
-            const bool partial = where >= 0;
             tile_coords(tile, tiles_w, tiles_t, wb, tb);
             const int n0 = wb * 2 * BW + static_cast<int>(rank) * BW + static_cast<int>(q * 32);
             const int n = n0 + static_cast<int>(lane);
             const int m0 = tb * BT + static_cast<int>(half) * (BT / 2);
-            float sw = 0.0f, bias = 0.0f;
-            if (!partial) {                      // while the tile's MMAs run
-                if (n < N) {
-                    sw = __ldg(a.sw + n);
-                    if (a.bias) bias = load_16(a.bias, n, BF16);
-                }
-                __syncwarp();
-                for (int c = static_cast<int>(lane); c < BT / 2; c += 32)
-                    sa_room[c] = m0 + c < M ? __ldg(a.sa + m0 + c) : 0.0f;
-                __syncwarp();
+            float sw = 0.0f, bias = 0.0f;        // while the tile's MMAs run
+            if (n < N) {
+                sw = __ldg(a.sw + n);
+                if (a.bias) bias = load_16(a.bias, n, BF16);
             }
+            __syncwarp();
+            for (int c = static_cast<int>(lane); c < BT / 2; c += 32) sa_room[c] = m0 + c < M ? __ldg(a.sa + m0 + c) : 0.0f;
+            __syncwarp();
             if (!mbar_wait_sleep(tmem_full, acc_phase, timeout_ns, 128)) {
                 if (lane == 0) atomicOr(err, ERR_EPILOGUE);
                 break;
             }
             tc_fence_after();
-            const uint32_t stg = sb + G::OFF_EPI + (warp - 2) * G::EPI_BYTES;
-            if (!partial && c_tma) {             // the previous tile's stores have finished reading the staging
+            if (c_tma) {                         // the previous tile's stores have finished reading the staging
                 if (lane == 0) bulk_wait_read<0>();
                 __syncwarp();
             }
+            const uint32_t d_col = tmem_base + ((q * 32) << 16) + half * (BT / 2);
+            acc_phase ^= 1;
 #pragma unroll 1
             for (int ch = 0; ch < G::CHUNKS; ++ch) {
                 uint32_t v[32];
-                tmem_ld_32x32b_x32(tmem_base + ((q * 32) << 16) + half * (BT / 2) + ch * 32, v);
+                tmem_ld_32x32b_x32(d_col + ch * 32, v);
                 tmem_wait_ld();
                 if (ch == G::CHUNKS - 1) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_relaxed_cluster(lead_empty);
                 }
-                const int mc = m0 + ch * 32;
-                if (partial) {
-                    // this range's sums, [token of the tile][weight row]: a store writes 32 consecutive floats
+                if (where >= 0) {
+                    // this range's sums, [token of the tile][weight row of the tile]: a store writes 32 consecutive floats
                     float *pl = P + (int64_t(where) * BT + half * (BT / 2) + ch * 32) * (2 * BW) + rank * BW + q * 32 + lane;
 #pragma unroll
                     for (int c = 0; c < 32; ++c)
-                        if (mc + c < M) pl[c * (2 * BW)] = __uint_as_float(v[c]);
-                } else {
+                        if (m0 + ch * 32 + c < M) pl[c * (2 * BW)] = __uint_as_float(v[c]);
+                    continue;
+                }
 #pragma unroll
-                    for (int c = 0; c < 32; c += 4) {
-                        const float4 sa = *reinterpret_cast<const float4 *>(sa_room + ch * 32 + c);
-                        const float s4[4] = {sa.x, sa.y, sa.z, sa.w};
+                for (int c = 0; c < 32; c += 4) {
+                    const float4 sa = *reinterpret_cast<const float4 *>(sa_room + ch * 32 + c);
+                    const float s4[4] = {sa.x, sa.y, sa.z, sa.w};
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int m = mc + c + j;
-                            const float sum = __uint_as_float(v[c + j]);
-                            if (c_tma) {
-                                // row c + j of the chunk: token m, columns n0 .. n0 + 31
-                                st_shared_u16(stg + ch * 2048 + (c + j) * 64 + lane * 2,
-                                              round_16(finish(sum, s4[j], sw, bias, 0.0f, epi), BF16));
-                            } else if (n < N && m < M) {
-                                uint16_t *dst = static_cast<uint16_t *>(a.C) + m * a.ldc + n;
-                                const float old = epi & qgi::EPI_ACCUMULATE ? load_16(dst, 0, BF16) : 0.0f;
-                                *dst = round_16(finish(sum, s4[j], sw, bias, old, epi), BF16);
-                            }
+                    for (int j = 0; j < 4; ++j) {
+                        const int m = m0 + ch * 32 + c + j;
+                        const float sum = __uint_as_float(v[c + j]);
+                        if (c_tma) {
+                            // row c + j of the chunk: token m, columns n0 .. n0 + 31
+                            st_shared_u16(stg + ch * 2048 + (c + j) * 64 + lane * 2,
+                                          round_16(finish(sum, s4[j], sw, bias, 0.0f, epi), BF16));
+                        } else if (n < N && m < M) {
+                            uint16_t *dst = static_cast<uint16_t *>(a.C) + m * a.ldc + n;
+                            const float old = epi & qgi::EPI_ACCUMULATE ? load_16(dst, 0, BF16) : 0.0f;
+                            *dst = round_16(finish(sum, s4[j], sw, bias, old, epi), BF16);
                         }
                     }
                 }
             }
-            if (!partial && c_tma) {
+            if (c_tma && where < 0) {
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -381,7 +400,6 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                     bulk_commit();
                 }
             }
-            acc_phase ^= 1;
         }
         if (c_tma && lane == 0) bulk_wait_all();
     }
@@ -396,8 +414,8 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
 // The tokens' codes as halves, rows of `ldh` (K rounded up to 16, at least): 16 codes a thread.
 __global__ void __launch_bounds__(256) codes_to_f16_kernel(const int8_t *__restrict__ A, int64_t lda, int M, int K,
                                                            uint16_t *__restrict__ H, int64_t ldh) {
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();                                   // after the wait: see the pair kernel's early copies
     const int per_row = (K + 15) / 16;
     const int64_t total = static_cast<int64_t>(M) * per_row;
     for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < total; i += gridDim.x * int64_t(256)) {
@@ -441,11 +459,13 @@ __global__ void __launch_bounds__(256) w8a8_reduce_kernel(const float *__restric
     const int64_t m = int64_t(tb) * BT + token;
     const int n = wb * 2 * BW + col;
     if (m >= a.M || n >= a.N) return;
-    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int p = p0; p <= p1; ++p) {
-        // the tile's piece is the first of the pair's range where the range begins inside the tile or at its start
-        const int64_t slot = 2 * int64_t(p) + (shares.begin(p) >= int64_t(t) * shares.KT ? 0 : 1);
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(P + (slot * BT + token) * (2 * BW) + col));
+    // piece p of the tile is the first of its pair's range where that begins inside the tile or at its start: all but p0's may
+    const float *at = P + int64_t(token) * (2 * BW) + col;
+    constexpr int64_t SLOT = int64_t(BT) * (2 * BW);
+    float4 sum = __ldcg(reinterpret_cast<const float4 *>(at + (2 * p0 + (shares.begin(p0) >= int64_t(t) * shares.KT ? 0 : 1)) * SLOT));
+#pragma unroll 8
+    for (int p = p0 + 1; p <= p1; ++p) {
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(at + 2 * p * SLOT));
         sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
     }
     const float sa = __ldg(a.sa + m), sums[4] = {sum.x, sum.y, sum.z, sum.w};
@@ -466,24 +486,25 @@ __global__ void __launch_bounds__(256) w8a8_reduce_kernel(const float *__restric
 // Work of M tokens in tiles of bt.
 Shares share(int bt, int M, int N, int K, int num_sms) {
     Shares s;
-    s.KT = (K + BK - 1) / BK;
+    const int bk = bt == 256 ? Cfg<256>::BK : Cfg<64>::BK;
+    s.KT = (K + bk - 1) / bk;
     const int most = std::max(1, num_sms / 2);
     const int64_t tiles = int64_t((N + 2 * BW - 1) / (2 * BW)) * ((M + bt - 1) / bt);
     s.pairs = most;
     s.full = static_cast<int>(tiles / most * most);
     s.rest = static_cast<int>(tiles - s.full);
-    // The rest in equal ranges of at least 4 k-tiles, unless it nearly fills a wave as it is (then sharing would gain an
+    // The rest in equal ranges of at least 256 of K, unless it nearly fills a wave as it is (then sharing would gain an
     // eighth of a wave at most and cost the reduction).
     s.sharers = s.rest;
     if (8 * s.rest < 7 * most)
-        s.sharers = static_cast<int>(std::max<int64_t>(s.rest, std::min<int64_t>(most, int64_t(s.rest) * s.KT / 4)));
+        s.sharers = static_cast<int>(std::max<int64_t>(s.rest, std::min<int64_t>(most, int64_t(s.rest) * s.KT * bk / 256)));
     if (s.full == 0) s.pairs = s.sharers;
     return s;
 }
 
 // Estimated us: k-tiles one pair walks, the ends of its tiles, and the reduction.
 double cost(int bt, const Shares &s) {
-    const double per_kt = bt == 256 ? 0.27 : 0.19, ends = bt == 256 ? 2.5 : 1.5;
+    const double per_kt = bt == 256 ? 0.33 : bt == 128 ? 0.5 : 0.45, ends = bt == 256 ? 2.5 : 1.5;
     const double mine = s.rest ? double(s.rest) * s.KT / s.sharers : 0.0;
     const int waves = s.pairs ? s.full / s.pairs : 0;
     double us = waves * (s.KT * per_kt + ends) + (s.rest ? mine * per_kt + ends : 0.0);
@@ -538,7 +559,7 @@ static cudaError_t launch_slice(const W8A8Args &a, uint16_t *H, int64_t ldh, flo
     const int c_tma = reinterpret_cast<uintptr_t>(a.C) % 16 == 0 && a.ldc % 8 == 0 && a.N % 8 == 0 &&
                       a.ldc < (int64_t(1) << 39) && !(ctx.epi & EPI_ACCUMULATE);
     CUtensorMap tmX, tmC;
-    *encode_ok = encode_tma_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, H, a.K, a.M, ldh * 2, BK, bt / 2,
+    *encode_ok = encode_tma_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, H, a.K, a.M, ldh * 2, 64, bt / 2,
                                CU_TENSOR_MAP_SWIZZLE_128B);
     if (*encode_ok && c_tma)
         *encode_ok = encode_tma_2d(&tmC, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.C, a.N, a.M, a.ldc * 2, 32, 32,
@@ -560,24 +581,26 @@ cudaError_t launch_w8a8_pair(const W8A8Args &a, const LaunchCtx &ctx, bool *enco
     const int slice = static_cast<int>(std::min<int64_t>(a.M, std::max<int64_t>(SLICE_BYTES / (2 * ldh) / 256 * 256, 256)));
     const int bt = choose(slice, a.N, a.K, ctx.num_sms);
     const int last = a.M % slice ? a.M % slice : slice;
+    const int bk = bt == 256 ? Cfg<256>::BK : Cfg<64>::BK;
     const Shares shares = share(bt, slice, a.N, a.K, ctx.num_sms), last_shares = share(bt, last, a.N, a.K, ctx.num_sms);
     const size_t x_bytes = (static_cast<size_t>(slice) * ldh * 2 + 255) / 256 * 256;
     const bool shared = shares.sharers > shares.rest || last_shares.sharers > last_shares.rest;
     const size_t p_bytes = shared ? static_cast<size_t>(std::max(shares.sharers, last_shares.sharers)) * 2 * bt * (2 * BW) * 4 : 0;
     CUtensorMap tmW;
-    *encode_ok = encode_tma_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.W, a.K, a.N, a.ldw, BK, BW, CU_TENSOR_MAP_SWIZZLE_64B);
+    *encode_ok = encode_tma_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.W, a.K, a.N, a.ldw, bk, BW,
+                               bk == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
     if (!*encode_ok) return cudaErrorInvalidValue;
     void *ws = nullptr;
     cudaError_t e = scratch_alloc(x_bytes + p_bytes, ctx, &ws);
     if (e != cudaSuccess) return e;
+    uint8_t *base = static_cast<uint8_t *>(ws);
     for (int64_t m0 = 0; m0 < a.M && e == cudaSuccess; m0 += slice) {
         W8A8Args part = a;
         part.A += m0 * a.lda;
         part.sa += m0;
         part.C = static_cast<uint16_t *>(a.C) + m0 * a.ldc;
         part.M = static_cast<int>(std::min<int64_t>(slice, a.M - m0));
-        e = launch_slice(part, static_cast<uint16_t *>(ws), ldh, reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + x_bytes),
-                         bt, part.M == slice ? shares : last_shares, tmW, ctx, encode_ok);
+        e = launch_slice(part, reinterpret_cast<uint16_t *>(base), ldh, reinterpret_cast<float *>(base + x_bytes), bt, part.M == slice ? shares : last_shares, tmW, ctx, encode_ok);
     }
     const cudaError_t f = scratch_free(ws, ctx);
     return e != cudaSuccess ? e : f;
