@@ -483,46 +483,54 @@ __global__ void __launch_bounds__(256) w8a8_reduce_kernel(const float *__restric
     if (whole) *reinterpret_cast<uint2 *>(dst) = make_uint2(out[0] | uint32_t(out[1]) << 16, out[2] | uint32_t(out[3]) << 16);
 }
 
-// Work of M tokens in tiles of bt.
-Shares share(int bt, int M, int N, int K, int num_sms) {
+struct Plan {
+    int bt;
+    Shares shares;
+};
+
+int k_of(int bt) { return bt == 256 ? Cfg<256>::BK : Cfg<64>::BK; }
+
+// Work of M tokens in tiles of bt, the tiles left after whole waves shared or not.
+Shares share(int bt, bool shared, int M, int N, int K, int num_sms) {
     Shares s;
-    const int bk = bt == 256 ? Cfg<256>::BK : Cfg<64>::BK;
+    const int bk = k_of(bt);
     s.KT = (K + bk - 1) / bk;
     const int most = std::max(1, num_sms / 2);
     const int64_t tiles = int64_t((N + 2 * BW - 1) / (2 * BW)) * ((M + bt - 1) / bt);
     s.pairs = most;
     s.full = static_cast<int>(tiles / most * most);
     s.rest = static_cast<int>(tiles - s.full);
-    // The rest in equal ranges of at least 256 of K, unless it nearly fills a wave as it is (then sharing would gain an
-    // eighth of a wave at most and cost the reduction).
     s.sharers = s.rest;
-    if (8 * s.rest < 7 * most)
+    if (shared)      // in equal ranges of at least 256 of K
         s.sharers = static_cast<int>(std::max<int64_t>(s.rest, std::min<int64_t>(most, int64_t(s.rest) * s.KT * bk / 256)));
     if (s.full == 0) s.pairs = s.sharers;
     return s;
 }
 
-// Estimated us: k-tiles one pair walks, the ends of its tiles, and the reduction.
+// Estimated us of a plan: the k-tiles a pair walks, the start and end of its tiles, the reduction's launch and traffic.
+// Measured: 0.336, 0.476 and 0.43 us a k-tile of 64, 128 and 128 k with every pair at work on 19456 rows x 16384 (256 tokens: the
+// MMAs; 64: the weights' bytes); partial sums written and read at 5 TB/s.
 double cost(int bt, const Shares &s) {
-    const double per_kt = bt == 256 ? 0.33 : bt == 128 ? 0.5 : 0.45, ends = bt == 256 ? 2.5 : 1.5;
-    const double mine = s.rest ? double(s.rest) * s.KT / s.sharers : 0.0;
+    const double per_kt = bt == 256 ? 0.336 : bt == 128 ? 0.476 : 0.43, ends = bt == 256 ? 2.5 : 1.5;
     const int waves = s.pairs ? s.full / s.pairs : 0;
-    double us = waves * (s.KT * per_kt + ends) + (s.rest ? mine * per_kt + ends : 0.0);
-    if (s.sharers > s.rest) us += 2.0 + (s.sharers + s.rest) * bt * 256 * 8 / 4e6;
+    double us = waves * (s.KT * per_kt + ends);
+    if (s.rest) us += double(s.rest) * s.KT / s.sharers * per_kt + ends;
+    if (s.sharers > s.rest) us += 2.0 + 2.0 * (s.sharers + s.rest) * bt * (2 * BW) * 4 / 5e6;
     return us;
 }
 
-// The tile's tokens: the cheapest.
-int choose(int M, int N, int K, int num_sms) {
-    int best = 256;
+Plan choose(int M, int N, int K, int num_sms) {
+    Plan best{};
     double least = 1e300;
-    for (int bt : {64, 128, 256}) {
-        const double us = cost(bt, share(bt, M, N, K, num_sms));
-        if (us < least) {
-            least = us;
-            best = bt;
+    for (int bt : {256, 128, 64})
+        for (bool shared : {false, true}) {
+            const Shares s = share(bt, shared, M, N, K, num_sms);
+            const double us = cost(bt, s);
+            if (us < least) {
+                least = us;
+                best = {bt, s};
+            }
         }
-    }
     return best;
 }
 
@@ -579,13 +587,13 @@ static cudaError_t launch_slice(const W8A8Args &a, uint16_t *H, int64_t ldh, flo
 cudaError_t launch_w8a8_pair(const W8A8Args &a, const LaunchCtx &ctx, bool *encode_ok) {
     const int64_t ldh = (a.K + 63) / 64 * int64_t(64);
     const int slice = static_cast<int>(std::min<int64_t>(a.M, std::max<int64_t>(SLICE_BYTES / (2 * ldh) / 256 * 256, 256)));
-    const int bt = choose(slice, a.N, a.K, ctx.num_sms);
-    const int last = a.M % slice ? a.M % slice : slice;
-    const int bk = bt == 256 ? Cfg<256>::BK : Cfg<64>::BK;
-    const Shares shares = share(bt, slice, a.N, a.K, ctx.num_sms), last_shares = share(bt, last, a.N, a.K, ctx.num_sms);
+    const Plan plan = choose(slice, a.N, a.K, ctx.num_sms);
+    const int bt = plan.bt, bk = k_of(bt);
+    const Shares &shares = plan.shares;
+    const Shares last = a.M % slice ? share(bt, shares.sharers > shares.rest, a.M % slice, a.N, a.K, ctx.num_sms) : shares;
     const size_t x_bytes = (static_cast<size_t>(slice) * ldh * 2 + 255) / 256 * 256;
-    const bool shared = shares.sharers > shares.rest || last_shares.sharers > last_shares.rest;
-    const size_t p_bytes = shared ? static_cast<size_t>(std::max(shares.sharers, last_shares.sharers)) * 2 * bt * (2 * BW) * 4 : 0;
+    const bool shared = shares.sharers > shares.rest || last.sharers > last.rest;
+    const size_t p_bytes = shared ? static_cast<size_t>(std::max(shares.sharers, last.sharers)) * 2 * bt * (2 * BW) * 4 : 0;
     CUtensorMap tmW;
     *encode_ok = encode_tma_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.W, a.K, a.N, a.ldw, bk, BW,
                                bk == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
@@ -600,7 +608,7 @@ cudaError_t launch_w8a8_pair(const W8A8Args &a, const LaunchCtx &ctx, bool *enco
         part.sa += m0;
         part.C = static_cast<uint16_t *>(a.C) + m0 * a.ldc;
         part.M = static_cast<int>(std::min<int64_t>(slice, a.M - m0));
-        e = launch_slice(part, reinterpret_cast<uint16_t *>(base), ldh, reinterpret_cast<float *>(base + x_bytes), bt, part.M == slice ? shares : last_shares, tmW, ctx, encode_ok);
+        e = launch_slice(part, reinterpret_cast<uint16_t *>(base), ldh, reinterpret_cast<float *>(base + x_bytes), bt, part.M == slice ? shares : last, tmW, ctx, encode_ok);
     }
     const cudaError_t f = scratch_free(ws, ctx);
     return e != cudaSuccess ? e : f;
