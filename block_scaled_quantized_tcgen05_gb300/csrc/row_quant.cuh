@@ -13,7 +13,9 @@
 // factor of the row, so max |h w| is taken beside the sum and both travel through one exchange.
 #pragma once
 
+#include <algorithm>
 #include <cfloat>
+#include <type_traits>
 
 #include "kv_common.cuh"
 #include "linear8_internal.h"
@@ -25,6 +27,8 @@ using namespace qg;
 constexpr float LEAST = 0x1p-100f;      // the least magnitude an INT8 row's scale is taken from
 constexpr float SHRINK = 0x1p-80f;      // factor on h where the sum of squares passed fp32's range
 
+constexpr int MAX_STAGES = 8;           // rows of a block's ring
+
 enum Out { OUT_INT8, OUT_E4M3, OUT_16 };
 
 // The larger of two magnitudes; NaN where either is (an INT8 row that holds one says so in its scale).
@@ -34,14 +38,54 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
+// The largest of a magnitude and of two values' magnitudes; NaN where one is (max_nan) or passing over NaN (max_num).
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float max_num(float a, float b, float c) {
+    float r;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Two products at once, each rounded as its scalar counterpart.
+__device__ __forceinline__ void mul2(float &d0, float &d1, float a0, float a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
 // f(x) = x / (1 + exp(-v)), v = x (SiLU) or 2 sqrt(2/pi) (x + 0.044715 x^3) (GELU: (1 + tanh u) / 2 is
-// 1 / (1 + exp(-2 u))).  The exponential is taken of -|v|, so that it never overflows and results go down to the
-// type's end.
+// 1 / (1 + exp(-2 u))).  The exponential is taken of -|v|, so that it never overflows, and times 2^24, so that it stays
+// normal where f is: below 0 the numerator is x exp(-|v|).  Two values at once.
+__device__ __forceinline__ void activate2(float &x0, float &x1, int kind) {
+    constexpr float DOWN = 0x1p-24f;
+    float v0 = x0, v1 = x1;
+    if (kind == QGEMM_ACT_GELU) {
+        float s0, s1;
+        mul2(s0, s1, x0, x1, x0, x1);
+        fma2(s0, s1, s0, s1, 0.0713548162726f, 0.0713548162726f, 1.5957691216057308f, 1.5957691216057308f);
+        mul2(v0, v1, x0, x1, s0, s1);
+    }
+    float t0, t1, r0, r1, n0, n1, d0, d1;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t0) : "f"(fmaf(fabsf(v0), -1.4426950408889634f, 24.0f)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t1) : "f"(fmaf(fabsf(v1), -1.4426950408889634f, 24.0f)));
+    fma2(d0, d1, t0, t1, DOWN, DOWN, 1.0f, 1.0f);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(d0));          // of 1 .. 2
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(d1));
+    mul2(n0, n1, x0, x1, DOWN, DOWN);
+    mul2(n0, n1, n0, n1, t0, t1);
+    mul2(x0, x1, v0 < 0.0f ? n0 : x0, v1 < 0.0f ? n1 : x1, r0, r1);
+}
+
 __device__ __forceinline__ float activate(float x, int kind) {
     if (kind == QGEMM_ACT_NONE) return x;
-    const float v = kind == QGEMM_ACT_SILU ? x : 1.5957691216057308f * (x + 0.044715f * x * x * x);
-    const float t = __expf(-fabsf(v));
-    return __fdividef(v < 0.0f ? x * t : x, 1.0f + t);
+    float unused = 0.0f;
+    activate2(x, unused, kind);
+    return x;
 }
 
 __device__ __forceinline__ float to_f32(const void *p, int64_t i, int32_t dtype) {
@@ -50,9 +94,16 @@ __device__ __forceinline__ float to_f32(const void *p, int64_t i, int32_t dtype)
     return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
 }
 
-// One INT8 code.  inv is 0 for a row with an infinity and NaN for one with a NaN: every code is then 0.
-__device__ __forceinline__ int code_i8(float y, float inv) {
-    return min(127, max(-127, __float2int_rn(y * inv)));
+// Four INT8 codes of y * inv, |y * inv| < 127.5: 1.5 * 2^23 added leaves the nearest integer (ties to even) in the low
+// bits.  A row with an infinity or a NaN has no finite factor: every code is 0 there.
+__device__ __forceinline__ uint32_t codes_i8(const float *y, float inv, bool finite) {
+    constexpr float HALF_WAY = 12582912.0f;
+    float c[4];
+    fma2(c[0], c[1], y[0], y[1], inv, inv, HALF_WAY, HALF_WAY);
+    fma2(c[2], c[3], y[2], y[3], inv, inv, HALF_WAY, HALF_WAY);
+    const uint32_t q = __byte_perm(__byte_perm(__float_as_uint(c[0]), __float_as_uint(c[1]), 0x0040),
+                                   __byte_perm(__float_as_uint(c[2]), __float_as_uint(c[3]), 0x0040), 0x5410);
+    return finite ? q : 0u;
 }
 
 // UE8M0 byte of a block whose largest magnitude is amax, and 2^-X.
@@ -92,9 +143,9 @@ __device__ __forceinline__ void block_reduce(float &ss, float &amax, float2 *roo
     }
 }
 
-// Any alignment, any H: one block a row, element by element, read a second time (from the caches) once
-// the row's sum and maximum are known.  Every element is read and written by one thread, so an output
-// may be an input.
+// Rows longer than a block holds in registers: one block a row, element by element, read a second time (from the
+// caches) once the row's sum and maximum are known.  Every element is read and written by one thread, so an output may
+// be an input.
 template <class TY, int OUT>
 __global__ void __launch_bounds__(256) row_quant_any_kernel(const __grid_constant__ qgi::RowQuantArgs a) {
     using T = typename TY::T;
@@ -146,6 +197,7 @@ __global__ void __launch_bounds__(256) row_quant_any_kernel(const __grid_constan
         }
         const float most = max_nan(amax, LEAST);
         const float inv8 = 127.0f / most;
+        const bool finite = most <= FLT_MAX;
         for (int c0 = threadIdx.x - lane; c0 < a.H; c0 += 256) {
             const int c = c0 + lane;
             const bool in = c < a.H;
@@ -157,7 +209,8 @@ __global__ void __launch_bounds__(256) row_quant_any_kernel(const __grid_constan
             }
             const float y = in ? (a.norm ? v * f * r * weight(c) : v) : 0.0f;
             if constexpr (OUT == OUT_INT8) {
-                if (in) (static_cast<int8_t *>(a.y) + row * a.ldy)[c] = static_cast<int8_t>(code_i8(y, inv8));
+                const float y4[4] = {y, 0.0f, 0.0f, 0.0f};
+                if (in) (static_cast<uint8_t *>(a.y) + row * a.ldy)[c] = static_cast<uint8_t>(codes_i8(y4, inv8, finite));
             } else if constexpr (OUT == OUT_E4M3) {
                 float m = fabsf(y);        // a block of 32 is a warp's; fmaxf passes over NaN
 #pragma unroll
@@ -177,8 +230,6 @@ __global__ void __launch_bounds__(256) row_quant_any_kernel(const __grid_constan
     }
 }
 
-// The vector kernel's shape: a row held by a warp (WARP, eight rows a block) or by a block, 8 elements a
-// thread and chunk, chunk i of thread t at element 8 (i nt + t).
 template <class TY>
 __device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -203,10 +254,57 @@ __device__ __forceinline__ uint4 load_once(const void *p) {
     return v;
 }
 
+// Elements 0 .. n - 1 of 16 bits from byte `off` of two 16-byte pieces on, the rest 0.
+__device__ __forceinline__ uint4 shifted(const uint4 &lo, const uint4 &hi, uint32_t off, int n) {
+    uint32_t w[5];
+    switch (off >> 2) {
+    case 0: w[0] = lo.x, w[1] = lo.y, w[2] = lo.z, w[3] = lo.w, w[4] = hi.x; break;
+    case 1: w[0] = lo.y, w[1] = lo.z, w[2] = lo.w, w[3] = hi.x, w[4] = hi.y; break;
+    case 2: w[0] = lo.z, w[1] = lo.w, w[2] = hi.x, w[3] = hi.y, w[4] = hi.z; break;
+    default: w[0] = lo.w, w[1] = hi.x, w[2] = hi.y, w[3] = hi.z, w[4] = hi.w; break;
+    }
+    const uint32_t bits = 8 * (off & 2);
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = __funnelshift_r(w[i], w[i + 1], bits);
+    if (n < 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (2 * i + 1 >= n) o[i] = 2 * i >= n ? 0u : o[i] & 0xFFFFu;
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Elements 0 .. n - 1 of 16 bits at an address of any alignment, the rest 0: the aligned 16-byte pieces that hold
+// them, shifted together.  No piece without one of the elements is read.  Pieces are read `off` bytes before the elements,
+// the same for a whole row.
+__device__ __forceinline__ uint4 load_any(const uint16_t *p, uint32_t off, int n) {
+    const uint4 *piece = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(p) - off);
+    if (off == 0 && n >= 8) return load_once(piece);
+    const uint4 lo = load_once(piece);
+    uint4 hi = make_uint4(0, 0, 0, 0);
+    if (off + 2 * n > 16) hi = load_once(piece + 1);
+    return shifted(lo, hi, off, n);
+}
+
+// The same from a stage of the ring, `p` the element's place without the offset.
+__device__ __forceinline__ uint4 shared_any(const uint8_t *p, uint32_t off, int n) {
+    const uint4 *piece = reinterpret_cast<const uint4 *>(p);
+    if (off == 0 && n >= 8) return piece[0];
+    return shifted(piece[0], off + 2 * n > 16 ? piece[1] : make_uint4(0, 0, 0, 0), off, n);
+}
+
+__device__ __forceinline__ uint32_t before_16(const void *p) { return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15); }
+
+// Weights of elements e .. e + 7 (0 past the row's end).
+template <bool ANY>
 __device__ __forceinline__ void load_weight8(const qgi::RowQuantArgs &a, int e, float (&w)[8]) {
     if (!a.weight) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i] = 1.0f;
+    } else if (ANY && (e + 8 > a.H || before_16(a.weight) != 0)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = e + i < a.H ? to_f32(a.weight, e + i, a.weight_dtype) : 0.0f;
     } else if (a.weight_dtype == QGEMM_F32) {
         const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.weight) + e);
         const float4 u = __ldg(p), v = __ldg(p + 1);
@@ -218,198 +316,373 @@ __device__ __forceinline__ void load_weight8(const qgi::RowQuantArgs &a, int e, 
     }
 }
 
-template <class TY, int OUT, bool NORM, bool SECOND, int C, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : 1024) row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a) {
-    __shared__ float2 room[32];
-    griddep_launch_dependents();
-    griddep_wait();
-    const int nt = WARP ? 32 : blockDim.x, t = WARP ? threadIdx.x & 31 : threadIdx.x;
-    const int64_t row = WARP ? blockIdx.x * int64_t(8) + (threadIdx.x >> 5) : blockIdx.x;
-    if (WARP && row >= a.T) return;                                // whole warps
-    auto join = [&](float &ss, float &amax) {
-        if constexpr (WARP) {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-                amax = max_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-            }
-        } else {
-            block_reduce(ss, amax, room);
-        }
-    };
-    const uint16_t *px = static_cast<const uint16_t *>(a.x) + row * a.ldx;
-    const uint16_t *p2 = static_cast<const uint16_t *>(a.second) + (SECOND ? row * a.ld2 : 0);
-    uint4 xv[C], sv[C];
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-        const int e = 8 * (i * nt + t);
-        const bool in = e < a.H;
-        xv[i] = in ? load_once(px + e) : make_uint4(0, 0, 0, 0);
-        if (SECOND) sv[i] = in ? load_once(p2 + e) : make_uint4(0, 0, 0, 0);
+// Eight 16-bit elements, or the first n of them, at an address of any alignment.
+__device__ __forceinline__ void store_any(uint16_t *p, const uint4 &v, int n) {
+    if (n >= 8 && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+        *reinterpret_cast<uint4 *>(p) = v;
+        return;
     }
-    auto input = [&](int i, float (&v)[8]) {                       // h, or the activation's product
-        unpack8<TY>(xv[i], v);
-        float s[8];
-        if (SECOND) unpack8<TY>(sv[i], s);
-        if constexpr (NORM) {
-            if (SECOND)
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] += s[j];
-        } else {
-            if (a.activation != QGEMM_ACT_NONE)
+    for (int i = 0; i < 8; ++i)
+        if (i < n) p[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+}
+__device__ __forceinline__ void store_any(uint8_t *p, const uint2 &v, int n) {
+    if (n >= 8 && reinterpret_cast<uintptr_t>(p) % 8 == 0) {
+        *reinterpret_cast<uint2 *>(p) = v;
+        return;
+    }
+    const uint32_t w[2] = {v.x, v.y};
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = activate(v[j], a.activation);
-            if (SECOND)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] *= s[j];
+    for (int i = 0; i < 8; ++i)
+        if (i < n) p[i] = static_cast<uint8_t>(w[i / 4] >> (8 * (i & 3)));
+}
+
+// The ring of a block's rows in shared memory.
+struct Ring {
+    int stages;
+    uint32_t second_at, stage_bytes;         // where a stage's second operand begins; a stage
+};
+
+// A row held by a warp (WARP, eight rows a block, loaded directly) or by a block, 8 elements a thread and chunk, chunk i of
+// thread t at element 8 (i nt + t).  A block walks its rows with the next ones on their way: bulk copies fill a ring of rows in
+// shared memory, so that loads go on through the row's sum, its exchange and its stores.  ANY: rows of any alignment and
+// length.
+template <class TY, int OUT, bool NORM, bool SECOND, int C, bool WARP, bool ANY>
+__global__ void __launch_bounds__(WARP ? 256 : C == 2 && ANY ? 512 : 1024)
+row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring ring, unsigned *err, uint64_t timeout_ns) {
+    __shared__ float2 room[2][32];
+    extern __shared__ uint8_t rows_smem[];
+    griddep_launch_dependents();
+    const int nt = WARP ? 32 : blockDim.x, t = WARP ? threadIdx.x & 31 : threadIdx.x;
+    int turn = 0;
+    // Sum of ss and maximum of amax (not negative: its bits' order is its own, a NaN's the largest) over the row's threads; one
+    // barrier, as the rooms alternate.  Only what the output needs.
+    constexpr bool SUM = NORM, MOST = OUT == OUT_INT8;
+    auto join = [&](float &ss, float &amax) {
+        auto over = [&](int width) {
+            if constexpr (SUM)
+                for (int o = width / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+            if constexpr (MOST) amax = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(amax)));
+        };
+        over(32);
+        if constexpr (!WARP) {
+            const int warps = nt >> 5;
+            if ((t & 31) == 0) room[turn][t >> 5] = make_float2(ss, amax);
+            __syncthreads();
+            const float2 v = (t & 31) < warps ? room[turn][t & 31] : make_float2(0.0f, 0.0f);
+            turn ^= 1;
+            ss = v.x;
+            amax = v.y;
+            over(warps > 16 ? 32 : warps > 8 ? 16 : warps > 4 ? 8 : 4);
+            // lane 0 has the sum of the warps' lanes, whatever the others added
+            if constexpr (SUM) ss = __shfl_sync(0xFFFFFFFFu, ss, 0);
         }
     };
-    float f = 1.0f, r = 1.0f, ss = 0.0f, amax = 0.0f;
-    float keep[NORM ? 1 : C][8];                                   // the activation is computed once
-    if constexpr (NORM) {
+    auto put = [](auto *p, const auto &v, int n) {
+        if constexpr (ANY) store_any(p, v, n);
+        else *reinterpret_cast<std::decay_t<decltype(v)> *>(p) = v;
+    };
+    auto row_x = [&](int64_t row) { return static_cast<const uint16_t *>(a.x) + row * a.ldx; };
+    auto row_2 = [&](int64_t row) { return static_cast<const uint16_t *>(a.second) + row * a.ld2; };
+
+    // A row's weights, kept by the thread where its registers allow (a block's for all its rows).
+    constexpr bool KEEP = NORM && C == 2;
+    float wkept[KEEP ? C : 1][8];
+    auto keep_weights = [&] {
+        if constexpr (KEEP)
 #pragma unroll
-        for (int i = 0; i < C; ++i) {
-            const int e = 8 * (i * nt + t);
-            if (e >= a.H) continue;
-            float v[8], w[8];
-            input(i, v);
-            load_weight8(a, e, w);
+            for (int i = 0; i < C; ++i)
+                if (8 * (i * nt + t) < a.H) load_weight8<ANY>(a, 8 * (i * nt + t), wkept[i]);
+    };
+    auto weights = [&](int i, int e, float (&w)[8]) {
+        if constexpr (KEEP)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                ss = fmaf(v[j], v[j], ss);
-                amax = max_nan(amax, fabsf(v[j] * w[j]));
-            }
-        }
-        join(ss, amax);
-        const bool wide = !(ss <= FLT_MAX);
-        if (wide) {                                                // rare: the sum again of h * 2^-80
-            f = SHRINK;
-            ss = 0.0f;
-#pragma unroll
-            for (int i = 0; i < C; ++i) {
-                float v[8];
-                input(i, v);                                       // zeros past the row's end
-#pragma unroll
-                for (int j = 0; j < 8; ++j) ss = fmaf(v[j] * f, v[j] * f, ss);
-            }
-            float unused = 0.0f;
-            join(ss, unused);
-        }
-        r = rsqrtf(ss / static_cast<float>(a.H) + (wide ? 0.0f : a.eps));
-        if (OUT == OUT_INT8 && (wide || !(amax <= FLT_MAX))) {
-            amax = 0.0f;
+            for (int j = 0; j < 8; ++j) w[j] = wkept[i][j];
+        else
+            load_weight8<ANY>(a, e, w);
+    };
+
+    // One row: load(e, xv, sv) gives a chunk's operands, read_done() says that all threads have theirs.
+    auto process = [&](int64_t row, auto &&load, auto &&read_done) {
+        // h, or the activation's product; zeros past the row's end
+        float v[C][8], amax = 0.0f;
+        [[maybe_unused]] float r = 1.0f, ss = 0.0f;
+        {
+            uint4 xv[C], sv[C];
 #pragma unroll
             for (int i = 0; i < C; ++i) {
                 const int e = 8 * (i * nt + t);
-                if (e >= a.H) continue;
-                float v[8], w[8];
-                input(i, v);
-                load_weight8(a, e, w);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) amax = max_nan(amax, fabsf(v[j] * f * r * w[j]));
+                xv[i] = sv[i] = make_uint4(0, 0, 0, 0);
+                if (e < a.H) load(e, xv[i], sv[i]);
             }
-            float unused = 0.0f;
-            join(unused, amax);
-        } else {
-            amax *= r;
+            if (!WARP) fence_proxy_async_smem();                   // read here, written next by the bulk copies
+            float s2[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                [[maybe_unused]] const int e = 8 * (i * nt + t);
+                unpack8<TY>(xv[i], v[i]);
+                float s[8];
+                if (SECOND) unpack8<TY>(sv[i], s);
+                if constexpr (NORM) {
+                    if (SECOND)
+#pragma unroll
+                        for (int j = 0; j < 8; j += 2) add2(v[i][j], v[i][j + 1], s[j], s[j + 1]);
+                    if (e >= a.H) continue;
+                    if (SECOND && a.sum_out)
+                        put(static_cast<uint16_t *>(a.sum_out) + row * a.ldso + e, pack8<TY>(v[i]), a.H - e);
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2)
+                        fma2(s2[0], s2[1], v[i][j], v[i][j + 1], v[i][j], v[i][j + 1], s2[0], s2[1]);
+                    if constexpr (OUT == OUT_INT8) {
+                        float w[8];
+                        weights(i, e, w);
+#pragma unroll
+                        for (int j = 0; j < 8; j += 2) {
+                            float p[2];
+                            mul2(p[0], p[1], v[i][j], v[i][j + 1], w[j], w[j + 1]);
+                            amax = max_nan(amax, p[0], p[1]);
+                        }
+                    }
+                } else {
+                    if (a.activation != QGEMM_ACT_NONE)
+#pragma unroll
+                        for (int j = 0; j < 8; j += 2) activate2(v[i][j], v[i][j + 1], a.activation);
+                    if (SECOND)
+#pragma unroll
+                        for (int j = 0; j < 8; j += 2) mul2(v[i][j], v[i][j + 1], v[i][j], v[i][j + 1], s[j], s[j + 1]);
+                    if (OUT == OUT_INT8)
+#pragma unroll
+                        for (int j = 0; j < 8; j += 2) amax = max_nan(amax, v[i][j], v[i][j + 1]);
+                }
+            }
+            ss = s2[0] + s2[1];
         }
-    } else {
+        if constexpr (NORM) {
+            join(ss, amax);
+            read_done();
+            const bool wide = !(ss <= FLT_MAX);
+            if (wide) {                                            // rare: the sum again of h * 2^-80
+                ss = 0.0f;
+#pragma unroll
+                for (int i = 0; i < C; ++i)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        v[i][j] *= SHRINK;
+                        ss = fmaf(v[i][j], v[i][j], ss);
+                    }
+                float unused = 0.0f;
+                join(ss, unused);
+            }
+            r = rsqrtf(ss / static_cast<float>(a.H) + (wide ? 0.0f : a.eps));
+            if (OUT == OUT_INT8 && (wide || !(amax <= FLT_MAX))) {
+                amax = 0.0f;
+#pragma unroll
+                for (int i = 0; i < C; ++i) {
+                    const int e = 8 * (i * nt + t);
+                    if (e >= a.H) continue;
+                    float w[8];
+                    weights(i, e, w);
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2) amax = max_nan(amax, v[i][j] * r * w[j], v[i][j + 1] * r * w[j + 1]);
+                }
+                float unused = 0.0f;
+                join(unused, amax);
+            } else {
+                amax *= r;
+            }
+        } else if constexpr (OUT == OUT_INT8) {
+            join(ss, amax);
+            read_done();
+        } else {
+            if (!WARP) __syncthreads();
+            read_done();
+        }
+        [[maybe_unused]] const float most = max_nan(amax, LEAST), inv8 = 127.0f / most;
+        [[maybe_unused]] const bool finite = most <= FLT_MAX;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-            input(i, keep[i]);
-            if (OUT == OUT_INT8)
+            const int e = 8 * (i * nt + t);
+            if (8 * (i * nt + (t & ~31)) >= a.H) continue;         // whole warps
+            const bool in = e < a.H;
+            if constexpr (NORM) {
+                float w[8];
+                weights(i, in ? e : 0, w);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) amax = max_nan(amax, fabsf(keep[i][j]));
-        }
-        if (OUT == OUT_INT8) join(ss, amax);
-    }
-    const float most = max_nan(amax, LEAST);
-    const float inv8 = 127.0f / most;
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-        const int e = 8 * (i * nt + t);
-        if (8 * (i * nt + (t & ~31)) >= a.H) continue;             // whole warps
-        const bool in = e < a.H;
-        float y[8];
-        if constexpr (NORM) {
-            float w[8];
-            input(i, y);
-            if (SECOND && a.sum_out && in)
-                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.sum_out) + row * a.ldso + e) = pack8<TY>(y);
-            load_weight8(a, in ? e : 0, w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = y[j] * f * r * w[j];
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = keep[i][j];
-        }
-        if constexpr (OUT == OUT_INT8) {
-            uint32_t q[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                int c[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) c[j] = code_i8(y[4 * h + j], inv8);
-                q[h] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+                for (int j = 0; j < 8; j += 2) {
+                    mul2(v[i][j], v[i][j + 1], v[i][j], v[i][j + 1], r, r);
+                    mul2(v[i][j], v[i][j + 1], v[i][j], v[i][j + 1], w[j], w[j + 1]);
+                }
             }
-            if (in) *reinterpret_cast<uint2 *>(static_cast<int8_t *>(a.y) + row * a.ldy + e) = make_uint2(q[0], q[1]);
-        } else if constexpr (OUT == OUT_E4M3) {
-            float m = 0.0f;                                        // fmaxf passes over NaN
+            if constexpr (OUT == OUT_INT8) {
+                const uint2 q = make_uint2(codes_i8(v[i], inv8, finite), codes_i8(v[i] + 4, inv8, finite));
+                if (in) put(static_cast<uint8_t *>(a.y) + row * a.ldy + e, q, a.H - e);
+            } else if constexpr (OUT == OUT_E4M3) {
+                float m = in ? 0.0f : 1.0f;                        // (lanes past the row's end share no block with others)
+                if (in) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(y[j]));
-            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-            float inv;
-            const uint32_t byte = block_scale(m, &inv);
-            uint32_t q[2];
+                    for (int j = 0; j < 8; j += 2) m = max_num(m, v[i][j], v[i][j + 1]);
+                }
+                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+                float inv;
+                const uint32_t byte = block_scale(m, &inv);
+                uint32_t q[2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                q[h] = uint32_t(e4m3x2(y[4 * h] * inv, y[4 * h + 1] * inv)) |
-                       uint32_t(e4m3x2(y[4 * h + 2] * inv, y[4 * h + 3] * inv)) << 16;
-            if (in) {
-                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.y) + row * a.ldy + e) = make_uint2(q[0], q[1]);
-                if ((t & 3) == 0) (static_cast<uint8_t *>(a.scales) + row * a.lds)[e / 32] = static_cast<uint8_t>(byte);
+                for (int h = 0; h < 2; ++h) {
+                    float u[4];
+                    mul2(u[0], u[1], v[i][4 * h], v[i][4 * h + 1], inv, inv);
+                    mul2(u[2], u[3], v[i][4 * h + 2], v[i][4 * h + 3], inv, inv);
+                    q[h] = uint32_t(e4m3x2(u[0], u[1])) | uint32_t(e4m3x2(u[2], u[3])) << 16;
+                }
+                if (in) {
+                    put(static_cast<uint8_t *>(a.y) + row * a.ldy + e, make_uint2(q[0], q[1]), a.H - e);
+                    if ((t & 3) == 0) (static_cast<uint8_t *>(a.scales) + row * a.lds)[e / 32] = static_cast<uint8_t>(byte);
+                }
+            } else {
+                if (in) put(static_cast<uint16_t *>(a.y) + row * a.ldy + e, pack8<TY>(v[i]), a.H - e);
             }
-        } else {
-            if (in) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.y) + row * a.ldy + e) = pack8<TY>(y);
+        }
+        if (OUT == OUT_INT8 && t == 0) static_cast<float *>(a.scales)[row] = most / 127.0f;
+    };
+
+    if constexpr (WARP) {
+        griddep_wait();
+        const int64_t row = blockIdx.x * int64_t(8) + (threadIdx.x >> 5);
+        if (row >= a.T) return;                                    // whole warps
+        keep_weights();
+        const uint16_t *px = row_x(row), *p2 = SECOND ? row_2(row) : nullptr;
+        const uint32_t offx = ANY ? before_16(px) : 0, off2 = ANY && SECOND ? before_16(p2) : 0;
+        process(
+            row,
+            [&](int e, uint4 &xv, uint4 &sv) {
+                xv = ANY ? load_any(px + e, offx, a.H - e) : load_once(px + e);
+                if (SECOND) sv = ANY ? load_any(p2 + e, off2, a.H - e) : load_once(p2 + e);
+            },
+            [] {});
+    } else {
+        __shared__ uint64_t full[MAX_STAGES];
+        const uint32_t sb = smem_u32(rows_smem), bar0 = smem_u32(full);
+        if (t == 0) {
+            for (int i = 0; i < ring.stages; ++i) mbar_init(bar0 + 8 * i, 1);
+            fence_barrier_init();
+        }
+        __syncthreads();
+        griddep_wait();
+        auto fetch = [&](int64_t row, int stage) {                 // by one thread; whole 16-byte pieces that hold the row
+            const uint16_t *px = row_x(row);
+            const uint32_t offx = ANY ? before_16(px) : 0, bytes = (2 * a.H + offx + 15) & ~15u;
+            uint32_t all = bytes, off2 = 0, bytes2 = 0;
+            const uint16_t *p2 = nullptr;
+            if (SECOND) {
+                p2 = row_2(row);
+                off2 = ANY ? before_16(p2) : 0;
+                bytes2 = (2 * a.H + off2 + 15) & ~15u;
+                all += bytes2;
+            }
+            const uint32_t bar = bar0 + 8 * stage, dst = sb + stage * ring.stage_bytes;
+            mbar_arrive_expect_tx(bar, all);
+            bulk_load(dst, reinterpret_cast<const uint8_t *>(px) - offx, bytes, bar);
+            if (SECOND) bulk_load(dst + ring.second_at, reinterpret_cast<const uint8_t *>(p2) - off2, bytes2, bar);
+        };
+        const int64_t step = gridDim.x, ahead = step * ring.stages;
+        if (t == 0)
+            for (int i = 0; i < ring.stages && blockIdx.x + i * step < a.T; ++i) fetch(blockIdx.x + i * step, i);
+        keep_weights();
+        int stage = 0;
+        uint32_t phase = 0;
+        for (int64_t row = blockIdx.x; row < a.T; row += step) {
+            if (!mbar_wait(bar0 + 8 * stage, phase, timeout_ns)) {
+                atomicOr(err, ERR_PRODUCER);
+                return;
+            }
+            const uint8_t *st = rows_smem + stage * ring.stage_bytes, *st2 = st + ring.second_at;
+            const uint32_t offx = ANY ? before_16(row_x(row)) : 0, off2 = ANY && SECOND ? before_16(row_2(row)) : 0;
+            const int at = stage;
+            process(
+                row,
+                [&](int e, uint4 &xv, uint4 &sv) {
+                    xv = ANY ? shared_any(st + 2 * e, offx, a.H - e) : *reinterpret_cast<const uint4 *>(st + 2 * e);
+                    if (SECOND) sv = ANY ? shared_any(st2 + 2 * e, off2, a.H - e) : *reinterpret_cast<const uint4 *>(st2 + 2 * e);
+                },
+                [&] {
+                    if (t == 0 && row + ahead < a.T) fetch(row + ahead, at);
+                });
+            if (++stage == ring.stages) {
+                stage = 0;
+                phase ^= 1;
+            }
         }
     }
-    if (OUT == OUT_INT8 && t == 0) static_cast<float *>(a.scales)[row] = most / 127.0f;
 }
 
-// 16-byte aligned rows of a multiple of 8 elements, 32768 at most (32 a thread).
+// Rows of a multiple of 8 elements, 16-byte aligned (8-byte in 8 bits): read and written as they are.
 inline bool vec_rows(const void *p, int64_t ld, int item) {
     return reinterpret_cast<uintptr_t>(p) % (8 * item) == 0 && ld % 8 == 0;
 }
 
 inline bool vec_eligible(const qgi::RowQuantArgs &a) {
-    return a.H % 8 == 0 && a.H <= 32768 && vec_rows(a.x, a.ldx, 2) && vec_rows(a.second, a.ld2, 2) &&
-           vec_rows(a.sum_out, a.ldso, 2) && vec_rows(a.y, a.ldy, a.y_dtype == a.dtype ? 2 : 1) &&
-           reinterpret_cast<uintptr_t>(a.weight) % 16 == 0;
+    return a.H % 8 == 0 && vec_rows(a.x, a.ldx, 2) && vec_rows(a.second, a.ld2, 2) && vec_rows(a.sum_out, a.ldso, 2) &&
+           vec_rows(a.y, a.ldy, a.y_dtype == a.dtype ? 2 : 1) && reinterpret_cast<uintptr_t>(a.weight) % 16 == 0;
 }
 
-template <class TY, int OUT, bool NORM, bool SECOND>
-cudaError_t launch_vec(const qgi::RowQuantArgs &a, const qgi::LaunchCtx &ctx) {
-    if (a.H <= 1024) {
-        const dim3 grid(static_cast<unsigned>((int64_t(a.T) + 7) / 8));
-        return a.H <= 512 ? launch_dependent(row_quant_vec_kernel<TY, OUT, NORM, SECOND, 2, true>, grid, 256, 0, ctx.stream, a)
-                          : launch_dependent(row_quant_vec_kernel<TY, OUT, NORM, SECOND, 4, true>, grid, 256, 0, ctx.stream, a);
+// A block's rows through its ring: as many blocks as the registers allow (1024 threads an SM at most), each with as many
+// rows on their way as shared memory holds (8 at most).
+template <class TY, int OUT, bool NORM, bool SECOND, int C, bool ANY>
+cudaError_t launch_ring(const qgi::RowQuantArgs &a, int threads, const qgi::LaunchCtx &ctx) {
+    constexpr int ROOM = 220 * 1024;
+    auto kern = row_quant_vec_kernel<TY, OUT, NORM, SECOND, C, false, ANY>;
+    static const int registers = [&] {
+        cudaFuncAttributes at;
+        return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? (at.numRegs + 7) / 8 * 8 : 128;
+    }();
+    Ring ring;
+    ring.second_at = (2 * a.H + (ANY ? 30 : 0)) / 16 * 16;
+    ring.stage_bytes = SECOND ? 2 * ring.second_at : ring.second_at;
+    int blocks = std::max(1, std::min({16, 1024 / threads, 65536 / (registers * threads)}));
+    while (blocks > 1 && 2 * ring.stage_bytes > unsigned(ROOM / blocks - 1536)) --blocks;
+    ring.stages = std::min(MAX_STAGES, (ROOM / blocks - 1536) / static_cast<int>(ring.stage_bytes));
+    int64_t grid = int64_t(blocks) * ctx.num_sms;
+    if (grid >= a.T) {           // one row a block
+        grid = a.T;
+        ring.stages = 1;
     }
-    const dim3 grid(static_cast<unsigned>(a.T));
-    auto threads = [&](int c) { return (a.H / 8 + 32 * c - 1) / (32 * c) * 32; };
-    if (threads(2) <= 1024)
-        return launch_dependent(row_quant_vec_kernel<TY, OUT, NORM, SECOND, 2, false>, grid, threads(2), 0, ctx.stream, a);
-    return launch_dependent(row_quant_vec_kernel<TY, OUT, NORM, SECOND, 4, false>, grid, threads(4), 0, ctx.stream, a);
+    const int smem = ring.stages * static_cast<int>(ring.stage_bytes);
+    if (smem > 40 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_dependent(kern, dim3(static_cast<unsigned>(grid)), threads, smem, ctx.stream, a, ring, ctx.err, ctx.timeout_ns);
+}
+
+template <class TY, int OUT, bool NORM, bool SECOND, bool ANY>
+cudaError_t launch_vec(const qgi::RowQuantArgs &a, const qgi::LaunchCtx &ctx) {
+    if (a.H <= 512)
+        return launch_dependent(row_quant_vec_kernel<TY, OUT, NORM, SECOND, 2, true, ANY>,
+                                dim3(static_cast<unsigned>((int64_t(a.T) + 7) / 8)), 256, 0, ctx.stream, a, Ring{}, ctx.err,
+                                ctx.timeout_ns);
+    auto threads = [&](int c) { return ((a.H + 7) / 8 + 32 * c - 1) / (32 * c) * 32; };
+    return threads(2) <= (ANY ? 512 : 1024) ? launch_ring<TY, OUT, NORM, SECOND, 2, ANY>(a, threads(2), ctx)
+                             : launch_ring<TY, OUT, NORM, SECOND, 4, ANY>(a, threads(4), ctx);
 }
 
 template <class TY, int OUT>
 cudaError_t launch_out(const qgi::RowQuantArgs &a, const qgi::LaunchCtx &ctx) {
-    if (!vec_eligible(a)) {
+    if (a.H > 32768) {           // past what a block's registers hold
         const dim3 grid(static_cast<unsigned>(a.T < 16 * ctx.num_sms ? a.T : 16 * ctx.num_sms));
         return launch_dependent(row_quant_any_kernel<TY, OUT>, grid, 256, 0, ctx.stream, a);
     }
-    if (a.norm) return a.second ? launch_vec<TY, OUT, true, true>(a, ctx) : launch_vec<TY, OUT, true, false>(a, ctx);
-    return a.second ? launch_vec<TY, OUT, false, true>(a, ctx) : launch_vec<TY, OUT, false, false>(a, ctx);
+    const int kind = 4 * a.norm + 2 * (a.second != nullptr) + vec_eligible(a);
+    switch (kind) {
+    case 0: return launch_vec<TY, OUT, false, false, true>(a, ctx);
+    case 1: return launch_vec<TY, OUT, false, false, false>(a, ctx);
+    case 2: return launch_vec<TY, OUT, false, true, true>(a, ctx);
+    case 3: return launch_vec<TY, OUT, false, true, false>(a, ctx);
+    case 4: return launch_vec<TY, OUT, true, false, true>(a, ctx);
+    case 5: return launch_vec<TY, OUT, true, false, false>(a, ctx);
+    case 6: return launch_vec<TY, OUT, true, true, true>(a, ctx);
+    default: return launch_vec<TY, OUT, true, true, false>(a, ctx);
+    }
 }
 
 template <class TY>
