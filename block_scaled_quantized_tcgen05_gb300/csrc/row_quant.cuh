@@ -106,6 +106,12 @@ __device__ __forceinline__ uint32_t codes_i8(const float *y, float inv, bool fin
     return finite ? q : 0u;
 }
 
+__device__ __forceinline__ float reciprocal(float x) {
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // UE8M0 byte of a block whose largest magnitude is amax, and 2^-X.
 __device__ __forceinline__ uint32_t block_scale(float amax, float *inv) {
     // floor(log2) is the exponent field; fp32 subnormals (field 0) are below every X that is kept
@@ -254,6 +260,15 @@ __device__ __forceinline__ uint4 load_once(const void *p) {
     return v;
 }
 
+// The first n of 8 elements, the rest 0: a row's end, out of the common path.
+__device__ __noinline__ uint4 first_of(uint4 v, int n) {
+    uint32_t o[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (2 * i + 1 >= n) o[i] = 2 * i >= n ? 0u : o[i] & 0xFFFFu;
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 // Elements 0 .. n - 1 of 16 bits from byte `off` of two 16-byte pieces on, the rest 0.
 __device__ __forceinline__ uint4 shifted(const uint4 &lo, const uint4 &hi, uint32_t off, int n) {
     uint32_t w[5];
@@ -267,12 +282,8 @@ __device__ __forceinline__ uint4 shifted(const uint4 &lo, const uint4 &hi, uint3
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = __funnelshift_r(w[i], w[i + 1], bits);
-    if (n < 8) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (2 * i + 1 >= n) o[i] = 2 * i >= n ? 0u : o[i] & 0xFFFFu;
-    }
-    return make_uint4(o[0], o[1], o[2], o[3]);
+    const uint4 all = make_uint4(o[0], o[1], o[2], o[3]);
+    return n < 8 ? first_of(all, n) : all;
 }
 
 // Elements 0 .. n - 1 of 16 bits at an address of any alignment, the rest 0: the aligned 16-byte pieces that hold
@@ -316,45 +327,47 @@ __device__ __forceinline__ void load_weight8(const qgi::RowQuantArgs &a, int e, 
     }
 }
 
-// Eight 16-bit elements, or the first n of them, at an address of any alignment.
-__device__ __forceinline__ void store_any(uint16_t *p, const uint4 &v, int n) {
-    if (n >= 8 && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
-        *reinterpret_cast<uint4 *>(p) = v;
-        return;
-    }
+// Eight 16-bit or 8-bit elements, or the first n of them, at an address of any alignment.
+__device__ __noinline__ void store_parts(uint16_t *p, uint4 v, int n) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (i < n) p[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
 }
-__device__ __forceinline__ void store_any(uint8_t *p, const uint2 &v, int n) {
-    if (n >= 8 && reinterpret_cast<uintptr_t>(p) % 8 == 0) {
-        *reinterpret_cast<uint2 *>(p) = v;
-        return;
-    }
+__device__ __noinline__ void store_parts(uint8_t *p, uint2 v, int n) {
     const uint32_t w[2] = {v.x, v.y};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (i < n) p[i] = static_cast<uint8_t>(w[i / 4] >> (8 * (i & 3)));
+}
+__device__ __forceinline__ void store_any(uint16_t *p, const uint4 &v, int n) {
+    if (n >= 8 && reinterpret_cast<uintptr_t>(p) % 16 == 0) *reinterpret_cast<uint4 *>(p) = v;
+    else store_parts(p, v, n);
+}
+__device__ __forceinline__ void store_any(uint8_t *p, const uint2 &v, int n) {
+    if (n >= 8 && reinterpret_cast<uintptr_t>(p) % 8 == 0) *reinterpret_cast<uint2 *>(p) = v;
+    else store_parts(p, v, n);
 }
 
 // The ring of a block's rows in shared memory.
 struct Ring {
     int stages;
     uint32_t second_at, stage_bytes;         // where a stage's second operand begins; a stage
+    int parts;                               // WARP: parts of a row, where an output needs nothing of the whole row
 };
 
 // A row held by a warp (WARP, eight rows a block, loaded directly) or by a block, 8 elements a thread and chunk, chunk i of
 // thread t at element 8 (i nt + t).  A block walks its rows with the next ones on their way: bulk copies fill a ring of rows in
 // shared memory, so that loads go on through the row's sum, its exchange and its stores.  ANY: rows of any alignment and
 // length.
-template <class TY, int OUT, bool NORM, bool SECOND, int C, bool WARP, bool ANY>
-__global__ void __launch_bounds__(WARP ? 256 : C == 2 && ANY ? 512 : 1024)
+template <class TY, int OUT, bool NORM, bool SECOND, int C, bool WARP, bool ANY, bool BIG>
+__global__ void __launch_bounds__(WARP ? 256 : (C == 2 && !ANY) || BIG ? 1024 : 512, WARP ? 4 : 1)
 row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring ring, unsigned *err, uint64_t timeout_ns) {
     __shared__ float2 room[2][32];
     extern __shared__ uint8_t rows_smem[];
     griddep_launch_dependents();
     const int nt = WARP ? 32 : blockDim.x, t = WARP ? threadIdx.x & 31 : threadIdx.x;
+    [[maybe_unused]] const float per_h = 1.0f / static_cast<float>(a.H);
     int turn = 0;
     // Sum of ss and maximum of amax (not negative: its bits' order is its own, a NaN's the largest) over the row's threads; one
     // barrier, as the rooms alternate.  Only what the output needs.
@@ -387,7 +400,7 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
     auto row_2 = [&](int64_t row) { return static_cast<const uint16_t *>(a.second) + row * a.ld2; };
 
     // A row's weights, kept by the thread where its registers allow (a block's for all its rows).
-    constexpr bool KEEP = NORM && C == 2;
+    constexpr bool KEEP = NORM && !BIG;
     float wkept[KEEP ? C : 1][8];
     auto keep_weights = [&] {
         if constexpr (KEEP)
@@ -404,7 +417,7 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
     };
 
     // One row: load(e, xv, sv) gives a chunk's operands, read_done() says that all threads have theirs.
-    auto process = [&](int64_t row, auto &&load, auto &&read_done) {
+    auto process = [&](int64_t row, int e0, auto &&load, auto &&read_done) {
         // h, or the activation's product; zeros past the row's end
         float v[C][8], amax = 0.0f;
         [[maybe_unused]] float r = 1.0f, ss = 0.0f;
@@ -412,7 +425,7 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
             uint4 xv[C], sv[C];
 #pragma unroll
             for (int i = 0; i < C; ++i) {
-                const int e = 8 * (i * nt + t);
+                const int e = e0 + 8 * (i * nt + t);
                 xv[i] = sv[i] = make_uint4(0, 0, 0, 0);
                 if (e < a.H) load(e, xv[i], sv[i]);
             }
@@ -420,7 +433,7 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
             float s2[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < C; ++i) {
-                [[maybe_unused]] const int e = 8 * (i * nt + t);
+                [[maybe_unused]] const int e = e0 + 8 * (i * nt + t);
                 unpack8<TY>(xv[i], v[i]);
                 float s[8];
                 if (SECOND) unpack8<TY>(sv[i], s);
@@ -474,12 +487,12 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
                 float unused = 0.0f;
                 join(ss, unused);
             }
-            r = rsqrtf(ss / static_cast<float>(a.H) + (wide ? 0.0f : a.eps));
+            r = rsqrtf(fmaf(ss, per_h, wide ? 0.0f : a.eps));
             if (OUT == OUT_INT8 && (wide || !(amax <= FLT_MAX))) {
                 amax = 0.0f;
 #pragma unroll
                 for (int i = 0; i < C; ++i) {
-                    const int e = 8 * (i * nt + t);
+                    const int e = e0 + 8 * (i * nt + t);
                     if (e >= a.H) continue;
                     float w[8];
                     weights(i, e, w);
@@ -498,12 +511,12 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
             if (!WARP) __syncthreads();
             read_done();
         }
-        [[maybe_unused]] const float most = max_nan(amax, LEAST), inv8 = 127.0f / most;
+        [[maybe_unused]] const float most = max_nan(amax, LEAST), inv8 = 127.0f * reciprocal(most);
         [[maybe_unused]] const bool finite = most <= FLT_MAX;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-            const int e = 8 * (i * nt + t);
-            if (8 * (i * nt + (t & ~31)) >= a.H) continue;         // whole warps
+            const int e = e0 + 8 * (i * nt + t);
+            if (e0 + 8 * (i * nt + (t & ~31)) >= a.H) continue;         // whole warps
             const bool in = e < a.H;
             if constexpr (NORM) {
                 float w[8];
@@ -548,13 +561,15 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
 
     if constexpr (WARP) {
         griddep_wait();
-        const int64_t row = blockIdx.x * int64_t(8) + (threadIdx.x >> 5);
+        const int64_t at = blockIdx.x * int64_t(8) + (threadIdx.x >> 5);
+        const int64_t row = ring.parts == 1 ? at : at / ring.parts;
+        const int e0 = ring.parts == 1 ? 0 : static_cast<int>(at - row * ring.parts) * 256 * C;
         if (row >= a.T) return;                                    // whole warps
         keep_weights();
         const uint16_t *px = row_x(row), *p2 = SECOND ? row_2(row) : nullptr;
         const uint32_t offx = ANY ? before_16(px) : 0, off2 = ANY && SECOND ? before_16(p2) : 0;
         process(
-            row,
+            row, e0,
             [&](int e, uint4 &xv, uint4 &sv) {
                 xv = ANY ? load_any(px + e, offx, a.H - e) : load_once(px + e);
                 if (SECOND) sv = ANY ? load_any(p2 + e, off2, a.H - e) : load_once(p2 + e);
@@ -600,7 +615,7 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
             const uint32_t offx = ANY ? before_16(row_x(row)) : 0, off2 = ANY && SECOND ? before_16(row_2(row)) : 0;
             const int at = stage;
             process(
-                row,
+                row, 0,
                 [&](int e, uint4 &xv, uint4 &sv) {
                     xv = ANY ? shared_any(st + 2 * e, offx, a.H - e) : *reinterpret_cast<const uint4 *>(st + 2 * e);
                     if (SECOND) sv = ANY ? shared_any(st2 + 2 * e, off2, a.H - e) : *reinterpret_cast<const uint4 *>(st2 + 2 * e);
@@ -626,44 +641,77 @@ inline bool vec_eligible(const qgi::RowQuantArgs &a) {
            vec_rows(a.y, a.ldy, a.y_dtype == a.dtype ? 2 : 1) && reinterpret_cast<uintptr_t>(a.weight) % 16 == 0;
 }
 
-// A block's rows through its ring: as many blocks as the registers allow (1024 threads an SM at most), each with as many
-// rows on their way as shared memory holds (8 at most).
-template <class TY, int OUT, bool NORM, bool SECOND, int C, bool ANY>
-cudaError_t launch_ring(const qgi::RowQuantArgs &a, int threads, const qgi::LaunchCtx &ctx) {
-    constexpr int ROOM = 220 * 1024;
-    auto kern = row_quant_vec_kernel<TY, OUT, NORM, SECOND, C, false, ANY>;
-    static const int registers = [&] {
-        cudaFuncAttributes at;
-        return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? (at.numRegs + 7) / 8 * 8 : 128;
-    }();
+// How rows go through blocks' rings: `c` chunks a thread, as many blocks as registers allow (1024 threads an SM at most), each
+// with as many rows on their way as shared memory holds (8 at most).
+struct RingPlan {
     Ring ring;
-    ring.second_at = (2 * a.H + (ANY ? 30 : 0)) / 16 * 16;
-    ring.stage_bytes = SECOND ? 2 * ring.second_at : ring.second_at;
-    int blocks = std::max(1, std::min({16, 1024 / threads, 65536 / (registers * threads)}));
-    while (blocks > 1 && 2 * ring.stage_bytes > unsigned(ROOM / blocks - 1536)) --blocks;
-    ring.stages = std::min(MAX_STAGES, (ROOM / blocks - 1536) / static_cast<int>(ring.stage_bytes));
-    int64_t grid = int64_t(blocks) * ctx.num_sms;
+    int threads, blocks;
+};
+
+template <class K>
+int registers_of(K kern) {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? (at.numRegs + 7) / 8 * 8 : 128;
+}
+
+inline RingPlan plan_ring(int registers, int c, int H, bool second, bool any) {
+    constexpr int ROOM = 220 * 1024;
+    RingPlan p;
+    p.threads = ((H + 7) / 8 + 32 * c - 1) / (32 * c) * 32;
+    p.ring.parts = 1;
+    p.ring.second_at = (2 * H + (any ? 30 : 0)) / 16 * 16;
+    p.ring.stage_bytes = second ? 2 * p.ring.second_at : p.ring.second_at;
+    p.blocks = std::max(1, std::min({16, 1024 / p.threads, 65536 / (registers * p.threads)}));
+    while (p.blocks > 1 && 2 * p.ring.stage_bytes > unsigned(ROOM / p.blocks - 1536)) --p.blocks;
+    p.ring.stages = std::min(MAX_STAGES, (ROOM / p.blocks - 1536) / static_cast<int>(p.ring.stage_bytes));
+    return p;
+}
+
+template <class K>
+cudaError_t launch_ring(K kern, RingPlan p, const qgi::RowQuantArgs &a, const qgi::LaunchCtx &ctx) {
+    int64_t grid = int64_t(p.blocks) * ctx.num_sms;
     if (grid >= a.T) {           // one row a block
         grid = a.T;
-        ring.stages = 1;
+        p.ring.stages = 1;
     }
-    const int smem = ring.stages * static_cast<int>(ring.stage_bytes);
+    const int smem = p.ring.stages * static_cast<int>(p.ring.stage_bytes);
     if (smem > 40 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
-    return launch_dependent(kern, dim3(static_cast<unsigned>(grid)), threads, smem, ctx.stream, a, ring, ctx.err, ctx.timeout_ns);
+    return launch_dependent(kern, dim3(static_cast<unsigned>(grid)), p.threads, smem, ctx.stream, a, p.ring, ctx.err,
+                            ctx.timeout_ns);
 }
 
 template <class TY, int OUT, bool NORM, bool SECOND, bool ANY>
 cudaError_t launch_vec(const qgi::RowQuantArgs &a, const qgi::LaunchCtx &ctx) {
-    if (a.H <= 512)
-        return launch_dependent(row_quant_vec_kernel<TY, OUT, NORM, SECOND, 2, true, ANY>,
-                                dim3(static_cast<unsigned>((int64_t(a.T) + 7) / 8)), 256, 0, ctx.stream, a, Ring{}, ctx.err,
-                                ctx.timeout_ns);
-    auto threads = [&](int c) { return ((a.H + 7) / 8 + 32 * c - 1) / (32 * c) * 32; };
-    return threads(2) <= (ANY ? 512 : 1024) ? launch_ring<TY, OUT, NORM, SECOND, 2, ANY>(a, threads(2), ctx)
-                             : launch_ring<TY, OUT, NORM, SECOND, 4, ANY>(a, threads(4), ctx);
+    // Short rows a warp each; and rows in parts of 512 elements where nothing of the whole row is needed.
+    constexpr bool APART = !NORM && OUT != OUT_INT8;
+    if (a.H <= 512 || APART) {
+        Ring ring{};
+        ring.parts = (a.H + 511) / 512;
+        const int64_t blocks = (int64_t(a.T) * ring.parts + 7) / 8;
+        if (blocks < (int64_t(1) << 31))
+            return launch_dependent(row_quant_vec_kernel<TY, OUT, NORM, SECOND, 2, true, ANY, false>,
+                                    dim3(static_cast<unsigned>(blocks)), 256, 0, ctx.stream, a, ring, ctx.err, ctx.timeout_ns);
+    }
+    if constexpr (APART) {
+        return cudaErrorInvalidConfiguration;    // 2^43 elements
+    } else {
+        // 16 elements a thread while that leaves two blocks an SM, to alternate between loads and exchanges; else 32 (measured
+        // at 4096 x 12288: norm to E4M3 56 us against 61) unless one block is all that fits either way; past 16384 elements 32 in up to
+        // 1024 threads.
+        auto k2 = row_quant_vec_kernel<TY, OUT, NORM, SECOND, 2, false, ANY, false>;
+        auto k4 = row_quant_vec_kernel<TY, OUT, NORM, SECOND, 4, false, ANY, false>;
+        auto big = row_quant_vec_kernel<TY, OUT, NORM, SECOND, 4, false, ANY, true>;
+        static const int r2 = registers_of(k2), r4 = registers_of(k4), r_big = registers_of(big);
+        if (a.H > 16384) return launch_ring(big, plan_ring(r_big, 4, a.H, SECOND, ANY), a, ctx);
+        const bool two = a.H <= (ANY ? 8192 : 16384);              // what its blocks may hold
+        const RingPlan p2 = plan_ring(r2, 2, a.H, SECOND, ANY);
+        if (two && p2.blocks >= 2) return launch_ring(k2, p2, a, ctx);
+        const RingPlan p4 = plan_ring(r4, 4, a.H, SECOND, ANY);
+        return p4.blocks >= 2 || !two ? launch_ring(k4, p4, a, ctx) : launch_ring(k2, p2, a, ctx);
+    }
 }
 
 template <class TY, int OUT>
