@@ -698,44 +698,62 @@ def qgemm_kv_copy_pages(kv: KVCache, src, dst, stream=None):
 _ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2}
 
 
-def _matrix(t, what: str):
-    """(pointer, row stride) of a 2-D tensor with contiguous rows on the current device."""
+def _current_device() -> int:
+    try:
+        return (torch or _load_torch())._C._cuda_getDevice()
+    except RuntimeError:                     # no device: no tensor is on it
+        return -2
+
+
+def _not_current(t, what: str):
+    raise ValueError(f"{what}: expected a tensor on the current device, got one on {t.device}")
+
+
+def _matrix(t, what: str, device: int):
+    """(pointer, row stride) of a 2-D tensor with contiguous rows on the device."""
     s = t.stride()
     if len(s) != 2 or s[1] != 1 and t.shape[1] > 1:
         raise ValueError(f"{what}: expected a 2-D tensor with contiguous rows")
-    _on_current(t, what)
+    if t.get_device() != device:
+        _not_current(t, what)
     return t.data_ptr(), s[0]
 
 
-def _vector(t, n: int, dtype, what: str):
-    """Pointer of a contiguous 1-D tensor of n entries on the current device."""
-    if t.dtype is not dtype or t.dim() != 1 or t.numel() != n or n > 1 and t.stride(0) != 1:
+def _same_matrix(t, like, shape, what: str, device: int):
+    if t.dtype is not like or t.shape != shape:
+        raise ValueError(f"{what}: shape and type must be X's")
+    return _matrix(t, what, device)
+
+
+def _vector(t, n: int, dtype, what: str, device: int):
+    """Pointer of a contiguous 1-D tensor of n entries on the device."""
+    s = t.shape
+    if t.dtype is not dtype or len(s) != 1 or s[0] != n or n > 1 and t.stride(0) != 1:
         raise ValueError(f"{what}: expected {n} contiguous entries of {dtype}")
-    _on_current(t, what)
+    if t.get_device() != device:
+        _not_current(t, what)
     return t.data_ptr()
 
 
-def _on_current(t, what: str):
-    if not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
-        raise ValueError(f"{what}: expected a tensor on the current device, got one on {t.device}")
-
-
-def _eight_bits(X, Y, scales):
-    """(Y's type, scales' pointer, scales' row stride) of a row quantiser's output."""
+def _eight_bits(Y, like, shape, scales, device: int):
+    """(pointer, row stride, type, scales' pointer, their row stride) of a row quantiser's output."""
+    if Y.shape != shape:
+        raise ValueError("Y: shape must be X's")
+    y, ld = _matrix(Y, "Y", device)
     dt = Y.dtype
-    if dt is X.dtype:
+    if dt is like:
         if scales is not None:
             raise ValueError("scales: a 16-bit output has none")
-        return _dtype16(Y), None, 0
+        return y, ld, _dtype16(Y), None, 0
     if scales is None:
         raise ValueError("scales: an 8-bit output needs them")
     if dt is torch.int8:
-        return INT8, _vector(scales, X.shape[0], torch.float32, "scales"), 0
+        return y, ld, INT8, _vector(scales, shape[0], torch.float32, "scales", device), 0
     if dt is not torch.uint8 and dt is not torch.float8_e4m3fn:
         raise ValueError(f"Y: expected int8, uint8 or float8_e4m3fn (E4M3 codes), or X's type, got {dt}")
-    if scales.dtype is not torch.uint8 or scales.dim() != 2 or tuple(scales.shape) != (X.shape[0], X.shape[1] // 32):
+    if scales.dtype is not torch.uint8 or tuple(scales.shape) != (shape[0], shape[1] // 32):
         raise ValueError("scales: expected uint8 [tokens, size / 32]")
-    return E4M3, *_matrix(scales, "scales")
+    return y, ld, E4M3, *_matrix(scales, "scales", device)
 
 
 def qgemm_norm_quant(X, weight, Y, scales=None, residual=None, residual_out=None, eps: float = 1e-6, stream=None):
@@ -743,30 +761,25 @@ def qgemm_norm_quant(X, weight, Y, scales=None, residual=None, residual_out=None
     with fp32 ``scales`` [tokens], uint8 / float8_e4m3fn codes with uint8 UE8M0 ``scales`` [tokens, size / 32],
     or of X's type.  ``residual_out`` (may be ``residual`` or X) receives X + residual; ``weight`` (fp16, bf16
     or fp32 [size]) may be None."""
-    if torch is None:
-        _load_torch()
-    shape = X.shape
-    xdt = X.dtype
-    x = _matrix(X, "X")
+    dev = _current_device()
+    shape, like = X.shape, X.dtype
+    x, ldx = _matrix(X, "X", dev)
     dt = _dtype16(X)
-    if Y.shape != shape:
-        raise ValueError("Y: shape must be X's")
-    r = ro = (None, 0)
+    r = ro = w = None
+    ldr = ldro = 0
+    wdt = F32
     if residual is not None:
-        if residual.shape != shape or residual.dtype is not xdt:
-            raise ValueError("residual: shape and type must be X's")
-        r = _matrix(residual, "residual")
+        r, ldr = _same_matrix(residual, like, shape, "residual", dev)
     if residual_out is not None:
-        if residual_out.shape != shape or residual_out.dtype is not xdt:
-            raise ValueError("residual_out: shape and type must be X's")
-        ro = _matrix(residual_out, "residual_out")
-    w, wdt = None, F32
+        ro, ldro = _same_matrix(residual_out, like, shape, "residual_out", dev)
     if weight is not None:
-        wdt = F32 if weight.dtype is torch.float32 else _dtype16(weight)
-        w = _vector(weight, shape[1], weight.dtype, "weight")
-    ydt, sp, lds = _eight_bits(X, Y, scales)
-    st = (_lib or load_library()).qgemm_norm_quant(*x, *r, *ro, dt, w, wdt, eps, shape[0], shape[1], *_matrix(Y, "Y"),
-                                                   ydt, sp, lds, _raw_stream(stream))
+        wlike = weight.dtype
+        if wlike is not torch.float32:
+            wdt = dt if wlike is like else _dtype16(weight)
+        w = _vector(weight, shape[1], wlike, "weight", dev)
+    y, ldy, ydt, s, lds = _eight_bits(Y, like, shape, scales, dev)
+    st = (_lib or load_library()).qgemm_norm_quant(x, ldx, r, ldr, ro, ldro, dt, w, wdt, eps, shape[0], shape[1], y, ldy, ydt, s,
+                                                   lds, _raw_stream(stream))
     if st:
         _check(st, "qgemm_norm_quant")
     return Y
@@ -775,23 +788,16 @@ def qgemm_norm_quant(X, weight, Y, scales=None, residual=None, residual_out=None
 def qgemm_act_quant(X, Y, scales=None, up=None, activation: str = "none", stream=None):
     """Y = f(X) [* up] for rows [tokens, size] of fp16 or bf16, f one of "none", "silu", "gelu" (tanh form);
     Y and ``scales`` as for qgemm_norm_quant.  With "none" and no ``up`` it quantises X as it is."""
-    if torch is None:
-        _load_torch()
+    dev = _current_device()
     kind = _ACTIVATIONS.get(activation)
     if kind is None:
         raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}")
-    shape = X.shape
-    x = _matrix(X, "X")
+    shape, like = X.shape, X.dtype
+    x, ldx = _matrix(X, "X", dev)
     dt = _dtype16(X)
-    if Y.shape != shape:
-        raise ValueError("Y: shape must be X's")
-    u = (None, 0)
-    if up is not None:
-        if up.shape != shape or up.dtype is not X.dtype:
-            raise ValueError("up: shape and type must be X's")
-        u = _matrix(up, "up")
-    ydt, sp, lds = _eight_bits(X, Y, scales)
-    st = (_lib or load_library()).qgemm_act_quant(*x, *u, dt, kind, shape[0], shape[1], *_matrix(Y, "Y"), ydt, sp, lds,
+    u, ldu = (None, 0) if up is None else _same_matrix(up, like, shape, "up", dev)
+    y, ldy, ydt, s, lds = _eight_bits(Y, like, shape, scales, dev)
+    st = (_lib or load_library()).qgemm_act_quant(x, ldx, u, ldu, dt, kind, shape[0], shape[1], y, ldy, ydt, s, lds,
                                                   _raw_stream(stream))
     if st:
         _check(st, "qgemm_act_quant")
@@ -799,18 +805,19 @@ def qgemm_act_quant(X, Y, scales=None, up=None, activation: str = "none", stream
 
 
 def _w8a8(A, a_scales, W, w_scales, C, bias):
-    if torch is None:
-        _load_torch()
-    if A.dtype is not torch.int8 or W.dtype is not torch.int8:
+    dev = _current_device()
+    i8, f32 = torch.int8, torch.float32
+    if A.dtype is not i8 or W.dtype is not i8:
         raise ValueError("A and W: expected int8 tensors")
-    a, w, c = _matrix(A, "A"), _matrix(W, "W"), _matrix(C, "C")
+    a, lda = _matrix(A, "A", dev)
+    w, ldw = _matrix(W, "W", dev)
+    c, ldc = _matrix(C, "C", dev)
     M, K = A.shape
-    N = W.shape[0]
-    if W.shape[1] != K or tuple(C.shape) != (M, N):
+    N, k = W.shape
+    if k != K or C.shape != (M, N):
         raise ValueError(f"expected W [N, {K}] and C [{M}, N], got {tuple(W.shape)} and {tuple(C.shape)}")
-    f32 = torch.float32
-    return (*a, _vector(a_scales, M, f32, "a_scales"), *w, _vector(w_scales, N, f32, "w_scales"),
-            None if bias is None else _vector(bias, N, C.dtype, "bias"), *c, _dtype16(C), M, N, K)
+    return (a, lda, _vector(a_scales, M, f32, "a_scales", dev), w, ldw, _vector(w_scales, N, f32, "w_scales", dev),
+            None if bias is None else _vector(bias, N, C.dtype, "bias", dev), c, ldc, _dtype16(C), M, N, K)
 
 
 def qgemm_w8a8(A, a_scales, W, w_scales, C, bias=None, stream=None):

@@ -33,17 +33,19 @@ constexpr int BW = 128;                 // weight rows per CTA (256 per pair: th
 constexpr int EPI_WARPS = 8;            // two per lane quarter, one per half of the tokens
 constexpr int CONV_WARP0 = 2 + EPI_WARPS;
 constexpr int CONV_WARPS = 8;           // two per lane quarter: alternate stages of 64 k, or a half each of every 128 k
-constexpr int THREADS = 32 * (CONV_WARP0 + CONV_WARPS);
+constexpr int THREADS = 32 * (CONV_WARP0 + CONV_WARPS + 1);
 constexpr uint32_t TMEM_COLS = 512;
 
 template <int BT>
 struct Cfg {
     static constexpr int BK = BT == 256 ? 64 : 128;                           // k per stage
-    static constexpr int STAGES = BT == 256 ? 6 : BT == 128 ? 5 : 7;
+    static constexpr int STAGES = BT == 256 ? 6 : BT == 128 ? 4 : 6;          // tokens' tiles and the weights' slots in TMEM
+    static constexpr int RAWS = BT == 256 ? 6 : BT == 128 ? 7 : 8;            // raw weights' tiles: their slots are free once converted
+    static constexpr int WPROD_WARP = CONV_WARP0 + CONV_WARPS;
     static constexpr int TURNS = BK == 64 ? 2 : 1;                            // a converter warp takes every TURNS-th stage
     // A warp that passes over stages must come back to the same ones: it would otherwise miss phases of their barriers, whose
     // parity then no longer tells them apart.
-    static_assert(STAGES % TURNS == 0, "stages in turn");
+    static_assert(STAGES % TURNS == 0 && RAWS % TURNS == 0, "stages in turn");
     static constexpr uint32_t A_COLS = BK / 2;                                // TMEM columns of a stage's weights
     static constexpr uint32_t X_HALF = (BT / 2) * 128;                        // 64 k of the tokens: rows of 128 bytes
     static constexpr uint32_t X_BYTES = X_HALF * (BK / 64);
@@ -52,10 +54,10 @@ struct Cfg {
     static constexpr int CHUNKS = BT / 64;                                    // 32-token chunks of an epilogue warp
     static constexpr uint32_t EPI_BYTES = CHUNKS * 2048;
     static constexpr uint32_t OFF_RAW = STAGES * X_BYTES;
-    static constexpr uint32_t OFF_EPI = OFF_RAW + STAGES * RAW_BYTES;
+    static constexpr uint32_t OFF_EPI = OFF_RAW + RAWS * RAW_BYTES;
     static constexpr uint32_t OFF_SA = OFF_EPI + EPI_WARPS * EPI_BYTES;       // each epilogue warp's token scales
     static constexpr uint32_t OFF_BAR = OFF_SA + EPI_WARPS * (BT / 2) * 4;
-    static constexpr uint32_t OFF_SLOT = OFF_BAR + (3 * STAGES + 3) * 8;
+    static constexpr uint32_t OFF_SLOT = OFF_BAR + (2 * STAGES + 2 * RAWS + 3) * 8;
     static constexpr uint32_t SMEM = OFF_SLOT + 16 + 1024;
     static constexpr uint32_t A_COL0 = BT;                                    // after the accumulator
     static_assert(SMEM <= 232448, "shared memory budget");
@@ -119,7 +121,7 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                  const __grid_constant__ Shares shares, float *__restrict__ P, int epi, unsigned *err,
                  uint64_t timeout_ns) {
     using G = Cfg<BT>;
-    constexpr int STAGES = G::STAGES, BK = G::BK;
+    constexpr int STAGES = G::STAGES, RAWS = G::RAWS, BK = G::BK;
     constexpr uint32_t A_COLS = G::A_COLS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align_1024(smem_raw);
@@ -134,7 +136,8 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
     auto full_bar = [&](int s) { return sb + G::OFF_BAR + 8u * s; };
     auto empty_bar = [&](int s) { return sb + G::OFF_BAR + 8u * (STAGES + s); };
     auto raw_full = [&](int s) { return sb + G::OFF_BAR + 8u * (2 * STAGES + s); };
-    const uint32_t tmem_full = sb + G::OFF_BAR + 8u * (3 * STAGES);
+    auto raw_empty = [&](int s) { return sb + G::OFF_BAR + 8u * (2 * STAGES + RAWS + s); };
+    const uint32_t tmem_full = sb + G::OFF_BAR + 8u * (2 * STAGES + 2 * RAWS);
     const uint32_t tmem_empty = tmem_full + 8;
     const uint32_t drain_bar = tmem_full + 16;
     volatile uint32_t *slot = reinterpret_cast<volatile uint32_t *>(smem + G::OFF_SLOT);
@@ -147,7 +150,10 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(full_bar(s), 1 + 2 * (CONV_WARPS / G::TURNS));   // expect_tx + converters of a stage
             mbar_init(empty_bar(s), 1);                          // leader's multicast commit
+        }
+        for (int s = 0; s < RAWS; ++s) {
             mbar_init(raw_full(s), 1);                           // this CTA's raw weights
+            mbar_init(raw_empty(s), CONV_WARPS / G::TURNS);      // its converters of a stage
         }
         mbar_init(tmem_full, 1);
         mbar_init(tmem_empty, 2 * EPI_WARPS);   // one lane of each epilogue warp of both CTAs
@@ -168,36 +174,20 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
     const uint32_t tmem_base = *slot;
 
     if (warp == 0) {
-        // ---------------------------------------------------------------- producer
+        // ---------------------------------------------------------------- tokens' producer
         // The whole warp runs the loop and waits; one elected lane issues the copies.
+        griddep_wait();                          // the tokens' halves
         uint32_t stage = 0, phase = 0;
         int issued = 0;
         bool ok = true;
         int tile, kt0, kt1, where, wb, tb;
-        auto issue_raw = [&](int s, int kt, int w0) {            // by the elected lane
-            mbar_arrive_expect_tx(raw_full(s), G::RAW_BYTES);
-            tma_load_2d(sb + G::OFF_RAW + s * G::RAW_BYTES, &tmW, raw_full(s), kt * BK, w0);
-        };
-        // The first stages' weights before the wait: the kernel ahead of this one makes the tokens' halves, touches no weights
-        // and has let this one start only after all work ahead of it was done.
-        int early = 0;
-        for (Items items(shares, pair); early < STAGES && items.next(tile, kt0, kt1, where);) {
-            tile_coords(tile, tiles_w, tiles_t, wb, tb);
-            for (int kt = kt0; kt < kt1 && early < STAGES; ++kt, ++early)
-                if (elect_one()) issue_raw(early, kt, wb * 2 * BW + static_cast<int>(rank) * BW);
-        }
-        griddep_wait();
         for (Items items(shares, pair); ok && items.next(tile, kt0, kt1, where);) {
             tile_coords(tile, tiles_w, tiles_t, wb, tb);
-            const int w0 = wb * 2 * BW + static_cast<int>(rank) * BW;     // this CTA's weights
             const int t0 = tb * BT + static_cast<int>(rank) * (BT / 2);   // this CTA's tokens
             for (int kt = kt0; kt < kt1; ++kt) {
-                if (!mbar_wait_warp(empty_bar(stage), phase ^ 1, timeout_ns)) {
-                    ok = false;
-                    break;
-                }
-                // debug build: the copies' innermost coordinates are multiples of 16 bytes and inside K
-                if (!QG_IN_BOUNDS(err, (kt * BK) % 16 == 0 && kt * BK < a.K)) {
+                // debug build: the copies' innermost coordinates are multiples of 16 bytes and begin inside K
+                if (!mbar_wait_warp(empty_bar(stage), phase ^ 1, timeout_ns) ||
+                    !QG_IN_BOUNDS(err, (kt * BK) % 8 == 0 && kt * BK < a.K)) {
                     ok = false;
                     break;
                 }
@@ -207,7 +197,6 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
 #pragma unroll
                     for (int h = 0; h < BK / 64; ++h)   // past K's end: zeros
                         tma_load_2d_pair(sb + stage * G::X_BYTES + h * G::X_HALF, &tmX, lead_full, kt * BK + h * 64, t0);
-                    if (issued >= early) issue_raw(stage, kt, w0);
                 }
                 __syncwarp();
                 ++issued;
@@ -218,13 +207,50 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
             }
         }
         if (!ok && lane == 0) atomicOr(err, ERR_PRODUCER);
-        bool drained = true;                     // no copy may land after the CTA has left
-        const int raws = max(issued, early);
-        for (int i = max(0, raws - STAGES); i < raws && drained; ++i)
-            drained = mbar_wait_warp(raw_full(i % STAGES), (i / STAGES) & 1, timeout_ns);
-        for (int i = max(0, issued - STAGES); rank == 0 && i < issued && drained; ++i)
-            drained = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(full_bar(i % STAGES), (i / STAGES) & 1, timeout_ns));
-        if (!drained && lane == 0) atomicOr(err, ERR_DRAIN);
+        // no copy may land after the CTAs have left
+        for (int i = max(0, issued - STAGES); rank == 0 && i < issued; ++i) {
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(full_bar(i % STAGES), (i / STAGES) & 1, timeout_ns))) {
+                if (lane == 0) atomicOr(err, ERR_DRAIN);
+                break;
+            }
+        }
+        __syncwarp();
+    } else if (warp == G::WPROD_WARP) {
+        // ---------------------------------------------------------------- weights' producer
+        // It need not wait for the kernel ahead, which makes the tokens' halves, touches no weights and has let this one start
+        // only after all work ahead of it was done: the first weights are on their way meanwhile.
+        uint32_t slot_raw = 0, phase = 0;
+        int issued = 0;
+        bool ok = true;
+        int tile, kt0, kt1, where, wb, tb;
+        for (Items items(shares, pair); ok && items.next(tile, kt0, kt1, where);) {
+            tile_coords(tile, tiles_w, tiles_t, wb, tb);
+            const int w0 = wb * 2 * BW + static_cast<int>(rank) * BW;     // this CTA's weights
+            for (int kt = kt0; kt < kt1; ++kt) {
+                if (!mbar_wait_warp(raw_empty(slot_raw), phase ^ 1, timeout_ns) ||
+                    !QG_IN_BOUNDS(err, (kt * BK) % 16 == 0 && kt * BK < a.K)) {
+                    ok = false;
+                    break;
+                }
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(raw_full(slot_raw), G::RAW_BYTES);
+                    tma_load_2d(sb + G::OFF_RAW + slot_raw * G::RAW_BYTES, &tmW, raw_full(slot_raw), kt * BK, w0);
+                }
+                __syncwarp();
+                ++issued;
+                if (++slot_raw == RAWS) {
+                    slot_raw = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        if (!ok && lane == 0) atomicOr(err, ERR_PRODUCER);
+        for (int i = max(0, issued - RAWS); i < issued; ++i) {
+            if (!mbar_wait_warp(raw_full(i % RAWS), (i / RAWS) & 1, timeout_ns)) {
+                if (lane == 0) atomicOr(err, ERR_DRAIN);
+                break;
+            }
+        }
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0) {
@@ -283,17 +309,16 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
         const uint32_t lead_full = map_to_cta(full_bar(0), 0);
         const uint32_t r = q * 32 + lane;
         const int total = Items(shares, pair).total();
-        uint32_t stage = static_cast<uint32_t>(first), phase = 0;
+        uint32_t stage = static_cast<uint32_t>(first), phase = 0, slot_raw = stage, phase_raw = 0;
         const uint8_t *row = smem + G::OFF_RAW + r * BK;
         // TMA's swizzle: chunk c of row r lies at c ^ (r % 8) of 128 bytes, or c ^ (r / 2 % 4) of 64
         const uint32_t swz = BK == 128 ? r & 7 : (r >> 1) & 3;
         for (int i = first; i < total; i += G::TURNS) {
-            if (!mbar_wait(raw_full(stage), phase, timeout_ns)) {
+            if (!mbar_wait(raw_full(slot_raw), phase_raw, timeout_ns)) {
                 if (lane == 0) atomicOr(err, ERR_PRODUCER);
                 break;
             }
-            tc_fence_after();   // the MMAs that last read this TMEM slot have completed
-            const uint8_t *raw = row + stage * G::RAW_BYTES;
+            const uint8_t *raw = row + slot_raw * G::RAW_BYTES;
             uint32_t out[32];
 #pragma unroll
             for (uint32_t c = 0; c < 4; ++c) {
@@ -303,17 +328,27 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                 i8x4_to_f16(d.z, out[8 * c + 4], out[8 * c + 5]);
                 i8x4_to_f16(d.w, out[8 * c + 6], out[8 * c + 7]);
             }
+            // read through the generic proxy, written next by TMA through the async proxy
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(raw_empty(slot_raw));
+            if (!mbar_wait(empty_bar(stage), phase ^ 1, timeout_ns)) {   // the MMAs that last read this TMEM slot have completed
+                if (lane == 0) atomicOr(err, ERR_PRODUCER);
+                break;
+            }
+            tc_fence_after();
             tmem_st_32x32b_x32(tmem_base + ((q * 32) << 16) + G::A_COL0 + stage * A_COLS + 32 * h, out);
             tmem_wait_st();
             tc_fence_before();
-            // the raw weights were read through the generic proxy; the slot's next fill is a TMA write
-            fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive_relaxed_cluster(lead_full + 8u * stage);
-            stage += G::TURNS;
-            if (stage >= STAGES) {
+            if ((stage += G::TURNS) >= STAGES) {
                 stage -= STAGES;
                 phase ^= 1;
+            }
+            if ((slot_raw += G::TURNS) >= RAWS) {
+                slot_raw -= RAWS;
+                phase_raw ^= 1;
             }
         }
     } else {
