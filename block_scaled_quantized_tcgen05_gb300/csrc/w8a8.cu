@@ -21,10 +21,15 @@ __global__ void __launch_bounds__(256) w8a8_empty_kernel(const __grid_constant__
 
 namespace qgi {
 
-constexpr int DECODE_TOKENS = 16;
+// Up to 16 tokens the weights' bytes bound the product and the weight stream is the fastest everywhere.  Up to 32 its
+// products on mma.sync begin to: it is still ahead of the pairs' three launches on small matrices (32 tokens, 4096 x 4096: 11.0 us
+// against 14.1; 8192 x 8192: 25.4 against 23.7).
+static bool few_tokens(const W8A8Args &a) {
+    return a.M <= 16 || (a.M <= 32 && int64_t(a.N) * a.K <= int64_t(1) << 25);
+}
 
 cudaError_t launch_w8a8(const W8A8Args &a, const LaunchCtx &ctx, bool *encode_ok) {
-    return a.M <= DECODE_TOKENS ? launch_w8a8_decode(a, ctx, encode_ok) : launch_w8a8_pair(a, ctx, encode_ok);
+    return few_tokens(a) ? launch_w8a8_decode(a, ctx, encode_ok) : launch_w8a8_pair(a, ctx, encode_ok);
 }
 
 cudaError_t launch_w8a8_empty(const W8A8Args &a, const LaunchCtx &ctx) {

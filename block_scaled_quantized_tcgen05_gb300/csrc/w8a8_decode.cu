@@ -237,8 +237,38 @@ w8a8_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     }
 }
 
+// How the work is laid out: NF fragments of 16 rows a block, K over `splits` CTAs, and its estimated us.
+struct Layout {
+    int splits;
+    int64_t grid;
+    double us;
+};
+
+// The best split for one block height.  Measured on 8192 x 8192 (1 token; 2 to 4 CTAs an SM, 80 to 160 KB of weights on
+// their way): an SM takes 13 + 0.216 KB^-1 x (its KB on their way) bytes a ns, so both an even share and many copies count;
+// all together at most 6.6 TB/s.  One block of rows a cluster, all of them at once (clusters of other than 2, 4 or 8 leave
+// room unused: 602 CTAs in clusters of 7 ran in two rounds where 608 fit), or with K whole as many as there are.
+template <class G>
+Layout layout(const qgi::W8A8Args &a, int num_sms) {
+    const int64_t nrb = (int64_t(a.N) + G::ROWS - 1) / G::ROWS;
+    const int nkc = (a.K + KC - 1) / KC, per_sm = std::max(1, int(233472 / (G::SMEM + 1024)));
+    const int64_t room = int64_t(num_sms) * per_sm;
+    Layout best{1, std::min(nrb, room), 1e300};
+    for (int s = 1; s <= 8; ++s) {
+        if (nkc < 2 * s && s > 1) break;
+        if (s > 1 && nrb * s > (s & (s - 1) ? room * 17 / 20 : room)) continue;
+        const int64_t ctas = std::min(nrb * s, room), rounds = (nrb * s + ctas - 1) / ctas;
+        const int64_t each = (ctas + num_sms - 1) / num_sms * rounds;                  // on the fullest SM
+        const double rate = 13.0 + 0.216 * double(std::min<int64_t>(each, per_sm) * G::STAGES * G::W_BYTES) / 1024;
+        const double own = double(each) * G::ROWS * ((nkc + s - 1) / s) * KC / 1e3 / rate;
+        const double us = std::max(own, double(a.N) * a.K / 6.6e6) + (s > 1 ? 0.8 + 0.1 * s * (1.0 + a.M / 8.0) : 0.0);
+        if (us < best.us) best = {s, ctas, us};
+    }
+    return best;
+}
+
 template <int NH, int NF, int STAGES>
-cudaError_t launch_nh(const qgi::W8A8Args &a, const qgi::LaunchCtx &ctx, bool *encode_ok) {
+cudaError_t launch_nh(const qgi::W8A8Args &a, const Layout &l, const qgi::LaunchCtx &ctx, bool *encode_ok) {
     using G = Cfg<NH, NF, STAGES>;
     CUtensorMap tmW, tmX;
     *encode_ok =
@@ -246,16 +276,12 @@ cudaError_t launch_nh(const qgi::W8A8Args &a, const qgi::LaunchCtx &ctx, bool *e
         qgi::encode_tma_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, a.K, a.M, a.lda, KC, 8 * NH, CU_TENSOR_MAP_SWIZZLE_128B);
     if (!*encode_ok) return cudaErrorInvalidValue;
     auto kern = w8a8_decode_kernel<NH, NF, STAGES>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
-    if (e != cudaSuccess) return e;
-    const int64_t nrb = (int64_t(a.N) + G::ROWS - 1) / G::ROWS;
-    const int nkc = (a.K + KC - 1) / KC;
-    const int64_t room = int64_t(ctx.num_sms) * std::max(1, int(233472 / (G::SMEM + 1024)));
-    // K over a cluster of 2, 4 or 8 CTAs while all fit at once and each keeps two stages
-    int splits = 1;
-    while (splits < 8 && nrb * splits * 2 <= room && nkc >= splits * 4) splits *= 2;
+    if (G::SMEM > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(splits > 1 ? nrb * splits : std::min(nrb, room)));
+    cfg.gridDim = dim3(static_cast<unsigned>(l.grid));
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = G::SMEM;
     cfg.stream = ctx.stream;
@@ -263,11 +289,20 @@ cudaError_t launch_nh(const qgi::W8A8Args &a, const qgi::LaunchCtx &ctx, bool *e
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(splits);
+    attr[1].val.clusterDim.x = static_cast<unsigned>(l.splits);
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, tmW, tmX, a, splits, ctx.epi, ctx.err, ctx.timeout_ns);
+    return cudaLaunchKernelEx(&cfg, kern, tmW, tmX, a, l.splits, ctx.epi, ctx.err, ctx.timeout_ns);
+}
+
+// The block height that is estimated fastest (48 rows on 28672 x 8192, 64 on 8192 x 28672, 32 on 4096 x 4096).
+template <int NH>
+cudaError_t launch_tokens(const qgi::W8A8Args &a, const qgi::LaunchCtx &ctx, bool *encode_ok) {
+    const Layout l2 = layout<Cfg<NH, 2, 8>>(a, ctx.num_sms), l3 = layout<Cfg<NH, 3, 6>>(a, ctx.num_sms),
+                 l4 = layout<Cfg<NH, 4, 5>>(a, ctx.num_sms);
+    if (l4.us <= l3.us && l4.us <= l2.us) return launch_nh<NH, 4, 5>(a, l4, ctx, encode_ok);
+    return l3.us <= l2.us ? launch_nh<NH, 3, 6>(a, l3, ctx, encode_ok) : launch_nh<NH, 2, 8>(a, l2, ctx, encode_ok);
 }
 
 }  // namespace
@@ -275,8 +310,9 @@ cudaError_t launch_nh(const qgi::W8A8Args &a, const qgi::LaunchCtx &ctx, bool *e
 namespace qgi {
 
 cudaError_t launch_w8a8_decode(const W8A8Args &a, const LaunchCtx &ctx, bool *encode_ok) {
-    if (a.M <= 8) return launch_nh<1, 3, 6>(a, ctx, encode_ok);
-    return launch_nh<2, 4, 5>(a, ctx, encode_ok);
+    if (a.M <= 8) return launch_tokens<1>(a, ctx, encode_ok);
+    if (a.M <= 16) return launch_tokens<2>(a, ctx, encode_ok);
+    return launch_nh<4, 2, 6>(a, layout<Cfg<4, 2, 6>>(a, ctx.num_sms), ctx, encode_ok);
 }
 
 }  // namespace qgi

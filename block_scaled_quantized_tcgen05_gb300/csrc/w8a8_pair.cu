@@ -478,19 +478,19 @@ __global__ void __launch_bounds__(256) codes_to_f16_kernel(const int8_t *__restr
     }
 }
 
-// The tiles that several pairs shared, from their partial sums in the order of K: four columns a thread, four
-// tokens' rows of 256 columns a block.
+// The tiles that several pairs shared, from their partial sums in the order of K: four columns a thread, a token's row
+// of 256 columns a block (many small blocks: the loads of a thread are few).
 template <int BT>
-__global__ void __launch_bounds__(256) w8a8_reduce_kernel(const float *__restrict__ P, const __grid_constant__ Shares shares,
+__global__ void __launch_bounds__(64) w8a8_reduce_kernel(const float *__restrict__ P, const __grid_constant__ Shares shares,
                                                           const __grid_constant__ qgi::W8A8Args a, int vec, int epi) {
     griddep_launch_dependents();
     griddep_wait();
-    const int t = blockIdx.x / (BT / 4), part = blockIdx.x % (BT / 4);
+    const int t = blockIdx.x / BT, token = blockIdx.x % BT;
     const int p0 = shares.owner(int64_t(t) * shares.KT), p1 = shares.owner(int64_t(t + 1) * shares.KT - 1);
     if (p0 == p1) return;                        // a whole tile, written by its pair
     int wb, tb;
     tile_coords(shares.full + t, (a.N + 2 * BW - 1) / (2 * BW), (a.M + BT - 1) / BT, wb, tb);
-    const int token = 4 * part + static_cast<int>(threadIdx.x >> 6), col = 4 * static_cast<int>(threadIdx.x & 63);
+    const int col = 4 * static_cast<int>(threadIdx.x);
     const int64_t m = int64_t(tb) * BT + token;
     const int n = wb * 2 * BW + col;
     if (m >= a.M || n >= a.N) return;
@@ -579,7 +579,7 @@ cudaError_t launch_bt(const qgi::W8A8Args &a, const CUtensorMap &tmX, const CUte
                              ctx.epi, ctx.err, ctx.timeout_ns);
     if (e == cudaSuccess && shares.sharers > shares.rest) {
         const int vec = reinterpret_cast<uintptr_t>(a.C) % 8 == 0 && a.ldc % 4 == 0;
-        e = launch_dependent(w8a8_reduce_kernel<BT>, dim3(shares.rest * (BT / 4)), 256, 0, ctx.stream, P, shares, a, vec, ctx.epi);
+        e = launch_dependent(w8a8_reduce_kernel<BT>, dim3(shares.rest * BT), 64, 0, ctx.stream, P, shares, a, vec, ctx.epi);
     }
     return e;
 }
