@@ -21,6 +21,7 @@
 //     sums in scratch, which a reduction kernel adds in the order of K.  (The warp that finishes a piece last adding them at the
 //     kernel's end instead: 4096 x 14336 x 4096 in 310 us against 294, 256 x 4096 x 4096 29 against 21: too few loads in flight.)
 #include <algorithm>
+#include <type_traits>
 
 #include "qgemm_common.cuh"
 #include "w8a8_common.cuh"
@@ -41,6 +42,7 @@ struct Cfg {
     static constexpr int BK = BT == 256 ? 64 : 128;                           // k per stage
     static constexpr int STAGES = BT == 256 ? 6 : BT == 128 ? 4 : 6;          // tokens' tiles and the weights' slots in TMEM
     static constexpr int RAWS = BT == 256 ? 6 : BT == 128 ? 7 : 8;            // raw weights' tiles: their slots are free once converted
+    static constexpr int BUFS = BT == 256 ? 1 : 2;                            // accumulators: the next tile's MMAs beside the epilogue
     static constexpr int WPROD_WARP = CONV_WARP0 + CONV_WARPS;
     static constexpr int TURNS = BK == 64 ? 2 : 1;                            // a converter warp takes every TURNS-th stage
     // A warp that passes over stages must come back to the same ones: it would otherwise miss phases of their barriers, whose
@@ -57,14 +59,21 @@ struct Cfg {
     static constexpr uint32_t OFF_EPI = OFF_RAW + RAWS * RAW_BYTES;
     static constexpr uint32_t OFF_SA = OFF_EPI + EPI_WARPS * EPI_BYTES;       // each epilogue warp's token scales
     static constexpr uint32_t OFF_BAR = OFF_SA + EPI_WARPS * (BT / 2) * 4;
-    static constexpr uint32_t OFF_SLOT = OFF_BAR + (2 * STAGES + 2 * RAWS + 3) * 8;
+    static constexpr uint32_t OFF_SLOT = OFF_BAR + (2 * STAGES + 2 * RAWS + 2 * BUFS + 1) * 8;
     static constexpr uint32_t SMEM = OFF_SLOT + 16 + 1024;
-    static constexpr uint32_t A_COL0 = BT;                                    // after the accumulator
+    static constexpr uint32_t A_COL0 = BUFS * BT;                             // after the accumulators
     static_assert(SMEM <= 232448, "shared memory budget");
     static_assert(A_COL0 + STAGES * A_COLS <= TMEM_COLS, "TMEM budget");
     // kind::f16: D fp32, A and B fp16, K-major, N = BT tokens, M = 256 weight rows (pair)
     static constexpr uint32_t IDESC = (1u << 4) | (uint32_t(BT >> 3) << 17) | (uint32_t(256 >> 4) << 24);
 };
+
+// Two sums of a column: (sum * sa) * sw + bias.
+__device__ __forceinline__ void scaled2(float &x0, float &x1, float s0, float s1, float sa0, float sa1, float sw, float bias) {
+    float t0, t1;
+    fma2(t0, t1, s0, s1, sa0, sa1, -0.0f, -0.0f);                  // the product itself: x + -0 is x
+    fma2(x0, x1, t0, t1, sw, sw, bias, bias);
+}
 
 __device__ __forceinline__ void st_shared_u16(uint32_t addr, uint16_t v) {
     asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
@@ -121,7 +130,8 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                  const __grid_constant__ Shares shares, float *__restrict__ P, int epi, unsigned *err,
                  uint64_t timeout_ns) {
     using G = Cfg<BT>;
-    constexpr int STAGES = G::STAGES, RAWS = G::RAWS, BK = G::BK;
+    using TY = std::conditional_t<BF16 != 0, TypeBF16, TypeF16>;
+    constexpr int STAGES = G::STAGES, RAWS = G::RAWS, BK = G::BK, BUFS = G::BUFS;
     constexpr uint32_t A_COLS = G::A_COLS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align_1024(smem_raw);
@@ -137,9 +147,9 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
     auto empty_bar = [&](int s) { return sb + G::OFF_BAR + 8u * (STAGES + s); };
     auto raw_full = [&](int s) { return sb + G::OFF_BAR + 8u * (2 * STAGES + s); };
     auto raw_empty = [&](int s) { return sb + G::OFF_BAR + 8u * (2 * STAGES + RAWS + s); };
-    const uint32_t tmem_full = sb + G::OFF_BAR + 8u * (2 * STAGES + 2 * RAWS);
-    const uint32_t tmem_empty = tmem_full + 8;
-    const uint32_t drain_bar = tmem_full + 16;
+    auto tmem_full = [&](int b) { return sb + G::OFF_BAR + 8u * (2 * STAGES + 2 * RAWS + b); };
+    auto tmem_empty = [&](int b) { return sb + G::OFF_BAR + 8u * (2 * STAGES + 2 * RAWS + BUFS + b); };
+    const uint32_t drain_bar = sb + G::OFF_BAR + 8u * (2 * STAGES + 2 * RAWS + 2 * BUFS);
     volatile uint32_t *slot = reinterpret_cast<volatile uint32_t *>(smem + G::OFF_SLOT);
 
     // tiles: weight-row blocks of 256 (the "m" of tile_coords) x token blocks of BT
@@ -155,8 +165,10 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
             mbar_init(raw_full(s), 1);                           // this CTA's raw weights
             mbar_init(raw_empty(s), CONV_WARPS / G::TURNS);      // its converters of a stage
         }
-        mbar_init(tmem_full, 1);
-        mbar_init(tmem_empty, 2 * EPI_WARPS);   // one lane of each epilogue warp of both CTAs
+        for (int b = 0; b < BUFS; ++b) {
+            mbar_init(tmem_full(b), 1);
+            mbar_init(tmem_empty(b), 2 * EPI_WARPS);   // one lane of each epilogue warp of both CTAs
+        }
         mbar_init(drain_bar, 1);
         fence_barrier_init();
         tma_prefetch_desc(&tmX);
@@ -256,11 +268,11 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
         if (rank == 0) {
             // --------------------------------------------------------- MMA issuer
             const uint64_t bdesc0 = smem_desc(sb, 16, 1024, SWZ_128B);
-            uint32_t acc_phase = 0, stage = 0, phase = 0;
+            uint32_t buf = 0, acc_phase = 0, stage = 0, phase = 0;
             bool ok = true;
             int tile, kt0, kt1, where;
             for (Items items(shares, pair); ok && items.next(tile, kt0, kt1, where);) {
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(tmem_empty, acc_phase ^ 1, timeout_ns))) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(tmem_empty(buf), acc_phase ^ 1, timeout_ns))) {
                     ok = false;
                     break;
                 }
@@ -276,7 +288,7 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                     if (elect_one()) {
 #pragma unroll
                         for (uint32_t j = 0; j < BK / 16; ++j)
-                            mma_f16_pair_ta(tmem_base, a_col + 8 * j, bdesc + (j / 4) * (G::X_HALF >> 4) + 2 * (j % 4),
+                            mma_f16_pair_ta(tmem_base + buf * BT, a_col + 8 * j, bdesc + (j / 4) * (G::X_HALF >> 4) + 2 * (j % 4),
                                             G::IDESC, kt > kt0 || j > 0 ? 1u : 0u);
                         tc_commit_pair(empty_bar(stage), 3);
                     }
@@ -287,9 +299,12 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                     }
                 }
                 if (!ok) break;
-                if (elect_one()) tc_commit_pair(tmem_full, 3);
+                if (elect_one()) tc_commit_pair(tmem_full(buf), 3);
                 __syncwarp();
-                acc_phase ^= 1;
+                if (++buf == BUFS) {
+                    buf = 0;
+                    acc_phase ^= 1;
+                }
             }
             if (elect_one()) {
                 if (!ok) atomicOr(err, ERR_MMA);
@@ -357,10 +372,10 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
         // BT / 2 of the tile's tokens, 32 per TMEM read.
         const uint32_t q = warp & 3;
         const uint32_t half = (warp - 2) >> 2;
-        const uint32_t lead_empty = map_to_cta(tmem_empty, 0);
+        const uint32_t lead_empty = map_to_cta(tmem_empty(0), 0);
         const uint32_t stg = sb + G::OFF_EPI + (warp - 2) * G::EPI_BYTES;
         float *sa_room = reinterpret_cast<float *>(smem + G::OFF_SA) + (warp - 2) * (BT / 2);
-        uint32_t acc_phase = 0;
+        uint32_t buf = 0, acc_phase = 0;
         griddep_wait();
         int tile, kt0, kt1, where, wb, tb;
         for (Items items(shares, pair); items.next(tile, kt0, kt1, where);) {
@@ -376,7 +391,7 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
             __syncwarp();
             for (int c = static_cast<int>(lane); c < BT / 2; c += 32) sa_room[c] = m0 + c < M ? __ldg(a.sa + m0 + c) : 0.0f;
             __syncwarp();
-            if (!mbar_wait_sleep(tmem_full, acc_phase, timeout_ns, 128)) {
+            if (!mbar_wait_sleep(tmem_full(buf), acc_phase, timeout_ns, 128)) {
                 if (lane == 0) atomicOr(err, ERR_EPILOGUE);
                 break;
             }
@@ -385,8 +400,11 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                 if (lane == 0) bulk_wait_read<0>();
                 __syncwarp();
             }
-            const uint32_t d_col = tmem_base + ((q * 32) << 16) + half * (BT / 2);
-            acc_phase ^= 1;
+            const uint32_t d_col = tmem_base + ((q * 32) << 16) + buf * BT + half * (BT / 2), release = lead_empty + 8 * buf;
+            if (++buf == BUFS) {
+                buf = 0;
+                acc_phase ^= 1;
+            }
 #pragma unroll 1
             for (int ch = 0; ch < G::CHUNKS; ++ch) {
                 uint32_t v[32];
@@ -395,33 +413,41 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                 if (ch == G::CHUNKS - 1) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_relaxed_cluster(lead_empty);
+                    if (lane == 0) mbar_arrive_relaxed_cluster(release);
                 }
+                const int mc = m0 + ch * 32;
                 if (where >= 0) {
                     // this range's sums, [token of the tile][weight row of the tile]: a store writes 32 consecutive floats
                     float *pl = P + (int64_t(where) * BT + half * (BT / 2) + ch * 32) * (2 * BW) + rank * BW + q * 32 + lane;
 #pragma unroll
                     for (int c = 0; c < 32; ++c)
-                        if (m0 + ch * 32 + c < M) pl[c * (2 * BW)] = __uint_as_float(v[c]);
-                    continue;
-                }
+                        if (mc + c < M) pl[c * (2 * BW)] = __uint_as_float(v[c]);
+                } else if (c_tma) {
+                    // row c of the chunk: token mc + c, columns n0 .. n0 + 31
+                    const uint32_t to = stg + ch * 2048 + lane * 2;
 #pragma unroll
-                for (int c = 0; c < 32; c += 4) {
-                    const float4 sa = *reinterpret_cast<const float4 *>(sa_room + ch * 32 + c);
-                    const float s4[4] = {sa.x, sa.y, sa.z, sa.w};
+                    for (int c = 0; c < 32; c += 4) {
+                        const float4 sa = *reinterpret_cast<const float4 *>(sa_room + ch * 32 + c);
+                        float x[4];
+                        scaled2(x[0], x[1], __uint_as_float(v[c]), __uint_as_float(v[c + 1]), sa.x, sa.y, sw, bias);
+                        scaled2(x[2], x[3], __uint_as_float(v[c + 2]), __uint_as_float(v[c + 3]), sa.z, sa.w, sw, bias);
+                        if (epi & qgi::EPI_RELU) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int m = m0 + ch * 32 + c + j;
-                        const float sum = __uint_as_float(v[c + j]);
-                        if (c_tma) {
-                            // row c + j of the chunk: token m, columns n0 .. n0 + 31
-                            st_shared_u16(stg + ch * 2048 + (c + j) * 64 + lane * 2,
-                                          round_16(finish(sum, s4[j], sw, bias, 0.0f, epi), BF16));
-                        } else if (n < N && m < M) {
-                            uint16_t *dst = static_cast<uint16_t *>(a.C) + m * a.ldc + n;
-                            const float old = epi & qgi::EPI_ACCUMULATE ? load_16(dst, 0, BF16) : 0.0f;
-                            *dst = round_16(finish(sum, s4[j], sw, bias, old, epi), BF16);
+                            for (int j = 0; j < 4; ++j) x[j] = fmaxf(x[j], 0.0f);
                         }
+                        const uint32_t lo = TY::pack(x[0], x[1]), hi = TY::pack(x[2], x[3]);
+                        st_shared_u16(to + c * 64, static_cast<uint16_t>(lo));
+                        st_shared_u16(to + (c + 1) * 64, static_cast<uint16_t>(lo >> 16));
+                        st_shared_u16(to + (c + 2) * 64, static_cast<uint16_t>(hi));
+                        st_shared_u16(to + (c + 3) * 64, static_cast<uint16_t>(hi >> 16));
+                    }
+                } else if (n < N) {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        if (mc + c >= M) continue;
+                        uint16_t *dst = static_cast<uint16_t *>(a.C) + (mc + c) * a.ldc + n;
+                        const float old = epi & qgi::EPI_ACCUMULATE ? load_16(dst, 0, BF16) : 0.0f;
+                        *dst = round_16(finish(__uint_as_float(v[c]), sa_room[ch * 32 + c], sw, bias, old, epi), BF16);
                     }
                 }
             }
