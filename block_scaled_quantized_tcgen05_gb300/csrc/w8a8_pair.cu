@@ -79,47 +79,56 @@ __device__ __forceinline__ void st_shared_u16(uint32_t addr, uint16_t v) {
     asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
 }
 
-// The pairs' work: `full` tiles in whole waves over `pairs` pairs, then the other `rest` tiles' k-tiles (units) in
-// equal ranges over `sharers` pairs (rest <= sharers <= pairs, and no range is empty).  sharers == rest: whole tiles.
+// The pairs' work: `full` tiles in whole waves over `pairs` pairs, then the other `rest` tiles: one a pair (sharers ==
+// rest), or their k-tiles (units) in equal ranges over more sharers, none of them empty (rest < sharers <= pairs).  Units times
+// sharers stay below 2^31, so ranges are found in 32 bits.
 struct Shares {
     int pairs, full, rest, sharers, KT;
-    __host__ __device__ int64_t begin(int p) const { return int64_t(p) * rest * KT / sharers; }
-    // the pair whose range holds unit u: the last p with p U / sharers < u + 1
-    __device__ int owner(int64_t u) const { return static_cast<int>(((u + 1) * sharers - 1) / (int64_t(rest) * KT)); }
+    __host__ __device__ bool shared() const { return sharers > rest; }
+    __device__ uint32_t begin(uint32_t p) const { return p * rest * KT / sharers; }
+    // the pair whose range holds unit u: the last p with p units / sharers < u + 1
+    __device__ uint32_t owner(uint32_t u) const { return ((u + 1) * sharers - 1) / (uint32_t(rest) * KT); }
 };
 
 // The items of one pair in order: (tile, k-tiles kt0 .. kt1, slot of its partial sums or -1 for a whole tile).
 struct Items {
     const Shares &s;
     int p, i;
-    int64_t u0, u, u1;
+    uint32_t u0, u, u1;
     __device__ Items(const Shares &sh, int pair) : s(sh), p(pair), i(pair), u0(0), u(0), u1(0) {
-        if (pair < sh.sharers) {
+        if (pair >= sh.sharers) return;
+        if (sh.shared()) {
             u0 = u = sh.begin(pair);
             u1 = sh.begin(pair + 1);
+        } else {
+            u1 = 1;                              // its one tile
         }
     }
     __device__ __forceinline__ bool next(int &tile, int &kt0, int &kt1, int &slot) {
         slot = -1;
+        kt0 = 0;
+        kt1 = s.KT;
         if (i < s.full) {
             tile = i;
-            kt0 = 0;
-            kt1 = s.KT;
             i += s.pairs;
             return true;
         }
         if (u >= u1) return false;
-        const int t = static_cast<int>(u / s.KT);
-        tile = s.full + t;
-        kt0 = static_cast<int>(u - int64_t(t) * s.KT);
-        kt1 = static_cast<int>(min(int64_t(s.KT), kt0 + (u1 - u)));
+        if (!s.shared()) {
+            tile = s.full + p;
+            u = u1;
+            return true;
+        }
+        const uint32_t t = u / s.KT;
+        tile = s.full + static_cast<int>(t);
+        kt0 = static_cast<int>(u - t * s.KT);
+        kt1 = min(s.KT, kt0 + static_cast<int>(u1 - u));
         if (kt1 - kt0 < s.KT) slot = 2 * p + (u == u0 ? 0 : 1);
         u += kt1 - kt0;
         return true;
     }
     __device__ int total() const {               // k-tiles of all of them
-        const int waves = s.full / s.pairs;
-        return waves * s.KT + static_cast<int>(u1 - u0);
+        return s.full / s.pairs * s.KT + (s.shared() ? static_cast<int>(u1 - u0) : static_cast<int>(u1) * s.KT);
     }
 };
 
@@ -504,44 +513,55 @@ __global__ void __launch_bounds__(256) codes_to_f16_kernel(const int8_t *__restr
     }
 }
 
-// The tiles that several pairs shared, from their partial sums in the order of K: four columns a thread, a token's row
-// of 256 columns a block (many small blocks: the loads of a thread are few).
+// The tiles that several pairs shared, from their partial sums in the order of K: `parts` blocks a tile, four columns a
+// thread, four tokens' rows of 256 columns at a time.  What goes by tile or column is found once a block.
 template <int BT>
-__global__ void __launch_bounds__(64) w8a8_reduce_kernel(const float *__restrict__ P, const __grid_constant__ Shares shares,
-                                                          const __grid_constant__ qgi::W8A8Args a, int vec, int epi) {
+__global__ void __launch_bounds__(256) w8a8_reduce_kernel(const float *__restrict__ P, const __grid_constant__ Shares shares,
+                                                          const __grid_constant__ qgi::W8A8Args a, int parts, int vec, int epi) {
     griddep_launch_dependents();
-    griddep_wait();
-    const int t = blockIdx.x / BT, token = blockIdx.x % BT;
-    const int p0 = shares.owner(int64_t(t) * shares.KT), p1 = shares.owner(int64_t(t + 1) * shares.KT - 1);
-    if (p0 == p1) return;                        // a whole tile, written by its pair
+    constexpr int64_t SLOT = int64_t(BT) * (2 * BW);
+    const int t = blockIdx.x / parts, part = blockIdx.x - t * parts;
+    const int p0 = shares.owner(t * shares.KT), p1 = shares.owner((t + 1) * shares.KT - 1);
     int wb, tb;
     tile_coords(shares.full + t, (a.N + 2 * BW - 1) / (2 * BW), (a.M + BT - 1) / BT, wb, tb);
-    const int col = 4 * static_cast<int>(threadIdx.x);
-    const int64_t m = int64_t(tb) * BT + token;
-    const int n = wb * 2 * BW + col;
-    if (m >= a.M || n >= a.N) return;
+    const int col = 4 * static_cast<int>(threadIdx.x & 63), n = wb * 2 * BW + col;
     // piece p of the tile is the first of its pair's range where that begins inside the tile or at its start: all but p0's may
-    const float *at = P + int64_t(token) * (2 * BW) + col;
-    constexpr int64_t SLOT = int64_t(BT) * (2 * BW);
-    float4 sum = __ldcg(reinterpret_cast<const float4 *>(at + (2 * p0 + (shares.begin(p0) >= int64_t(t) * shares.KT ? 0 : 1)) * SLOT));
-#pragma unroll 8
-    for (int p = p0 + 1; p <= p1; ++p) {
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(at + 2 * p * SLOT));
-        sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
-    }
-    const float sa = __ldg(a.sa + m), sums[4] = {sum.x, sum.y, sum.z, sum.w};
-    uint16_t *dst = static_cast<uint16_t *>(a.C) + m * a.ldc + n;
-    uint16_t out[4] = {0, 0, 0, 0};
-    const bool whole = vec && n + 4 <= a.N;
+    const float *first = P + (2 * p0 + (shares.begin(p0) >= uint32_t(t) * shares.KT ? 0 : 1)) * SLOT + col, *others = P + col;
+    if (p0 == p1 || n >= a.N) return;            // a whole tile, written by its pair
+    griddep_wait();
+    float sw[4], bias[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        if (n + j >= a.N) break;
-        const float bias = a.bias ? load_16(a.bias, n + j, a.bf16) : 0.0f;
-        const float old = epi & qgi::EPI_ACCUMULATE ? load_16(dst, j, a.bf16) : 0.0f;
-        out[j] = round_16(finish(sums[j], sa, __ldg(a.sw + n + j), bias, old, epi), a.bf16);
-        if (!whole) dst[j] = out[j];
+        sw[j] = n + j < a.N ? __ldg(a.sw + n + j) : 0.0f;
+        bias[j] = a.bias && n + j < a.N ? load_16(a.bias, n + j, a.bf16) : 0.0f;
     }
-    if (whole) *reinterpret_cast<uint2 *>(dst) = make_uint2(out[0] | uint32_t(out[1]) << 16, out[2] | uint32_t(out[3]) << 16);
+    const bool whole = vec && n + 4 <= a.N;
+    for (int token = 4 * part + static_cast<int>(threadIdx.x >> 6); token < BT; token += 4 * parts) {
+        const int64_t m = int64_t(tb) * BT + token;
+        if (m >= a.M) break;
+        const int row = token * (2 * BW);
+        float4 sum = __ldcg(reinterpret_cast<const float4 *>(first + row));
+        for (int p = p0 + 1; p <= p1; p += 8) {  // eight pieces' loads at once, whatever is left of them
+            float4 v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = p + j <= p1 ? __ldcg(reinterpret_cast<const float4 *>(others + 2 * (p + j) * SLOT + row))
+                                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum.x += v[j].x, sum.y += v[j].y, sum.z += v[j].z, sum.w += v[j].w;
+        }
+        const float sa = __ldg(a.sa + m), sums[4] = {sum.x, sum.y, sum.z, sum.w};
+        uint16_t *dst = static_cast<uint16_t *>(a.C) + m * a.ldc + n;
+        uint16_t out[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (n + j >= a.N) break;
+            const float old = epi & qgi::EPI_ACCUMULATE ? load_16(dst, j, a.bf16) : 0.0f;
+            out[j] = round_16(finish(sums[j], sa, sw[j], bias[j], old, epi), a.bf16);
+            if (!whole) dst[j] = out[j];
+        }
+        if (whole) *reinterpret_cast<uint2 *>(dst) = make_uint2(out[0] | uint32_t(out[1]) << 16, out[2] | uint32_t(out[3]) << 16);
+    }
 }
 
 struct Plan {
@@ -562,21 +582,25 @@ Shares share(int bt, bool shared, int M, int N, int K, int num_sms) {
     s.full = static_cast<int>(tiles / most * most);
     s.rest = static_cast<int>(tiles - s.full);
     s.sharers = s.rest;
-    if (shared)      // in equal ranges of at least 256 of K
-        s.sharers = static_cast<int>(std::max<int64_t>(s.rest, std::min<int64_t>(most, int64_t(s.rest) * s.KT * bk / 256)));
+    if (shared) {    // in equal ranges of at least 256 of K, about 8 a tile at most (more cost the reduction a second round of loads)
+        const int64_t most_shares = std::min<int64_t>({most, int64_t(s.rest) * s.KT * bk / 256, int64_t(s.rest) * 8});
+        if (most_shares > s.rest && int64_t(s.rest) * s.KT * most_shares < (int64_t(1) << 31)) s.sharers = static_cast<int>(most_shares);
+    }
     if (s.full == 0) s.pairs = s.sharers;
     return s;
 }
 
-// Estimated us of a plan: the k-tiles a pair walks, the start and end of its tiles, the reduction's launch and traffic.
-// Measured: 0.336, 0.476 and 0.43 us a k-tile of 64, 128 and 128 k with every pair at work on 19456 rows x 16384 (256 tokens: the
-// MMAs; 64: the weights' bytes); partial sums written and read at 5 TB/s.
-double cost(int bt, const Shares &s) {
-    const double per_kt = bt == 256 ? 0.336 : bt == 128 ? 0.476 : 0.43, ends = bt == 256 ? 2.5 : 1.5;
+// Estimated us of a plan: the waves' walks over K, the start and end of a tile, the reduction's launch and traffic.
+// Measured: a k-tile takes a pair 0.29, 0.34 and 0.30 us (64, 128 and 128 k for 256, 128 and 64 tokens; matrices that stay in L2);
+// all pairs together get 5.8 TB/s of weights from memory, which each weight leaves once however many token tiles meet it;
+// partial sums are written and read at 5 TB/s.
+double cost(int bt, const Shares &s, int M, int K) {
+    const double per_kt = bt == 256 ? 0.29 : bt == 128 ? 0.34 : 0.30, ends = bt == 256 ? 2.5 : 1.5;
+    const double tile_bytes = double(2 * BW) * K / ((M + bt - 1) / bt);
     const int waves = s.pairs ? s.full / s.pairs : 0;
-    double us = waves * (s.KT * per_kt + ends);
-    if (s.rest) us += double(s.rest) * s.KT / s.sharers * per_kt + ends;
-    if (s.sharers > s.rest) us += 2.0 + 2.0 * (s.sharers + s.rest) * bt * (2 * BW) * 4 / 5e6;
+    double us = waves * (std::max(s.KT * per_kt, s.pairs * tile_bytes / 5.8e6) + ends);
+    if (s.rest) us += std::max(double(s.rest) * s.KT / s.sharers * per_kt, s.rest * tile_bytes / 5.8e6) + ends;
+    if (s.shared()) us += 2.0 + 2.0 * (s.sharers + s.rest) * bt * (2 * BW) * 4 / 5e6;
     return us;
 }
 
@@ -586,7 +610,7 @@ Plan choose(int M, int N, int K, int num_sms) {
     for (int bt : {256, 128, 64})
         for (bool shared : {false, true}) {
             const Shares s = share(bt, shared, M, N, K, num_sms);
-            const double us = cost(bt, s);
+            const double us = cost(bt, s, M, K);
             if (us < least) {
                 least = us;
                 best = {bt, s};
@@ -603,9 +627,10 @@ cudaError_t launch_bt(const qgi::W8A8Args &a, const CUtensorMap &tmX, const CUte
     if (e == cudaSuccess)
         e = launch_dependent(kern, dim3(2 * shares.pairs), THREADS, Cfg<BT>::SMEM, ctx.stream, tmX, tmW, tmC, c_tma, a, shares, P,
                              ctx.epi, ctx.err, ctx.timeout_ns);
-    if (e == cudaSuccess && shares.sharers > shares.rest) {
+    if (e == cudaSuccess && shares.shared()) {
         const int vec = reinterpret_cast<uintptr_t>(a.C) % 8 == 0 && a.ldc % 4 == 0;
-        e = launch_dependent(w8a8_reduce_kernel<BT>, dim3(shares.rest * BT), 64, 0, ctx.stream, P, shares, a, vec, ctx.epi);
+        const int parts = std::max(1, std::min(BT / 4, (4 * ctx.num_sms + shares.rest - 1) / shares.rest));
+        e = launch_dependent(w8a8_reduce_kernel<BT>, dim3(shares.rest * parts), 256, 0, ctx.stream, P, shares, a, parts, vec, ctx.epi);
     }
     return e;
 }
@@ -651,9 +676,9 @@ cudaError_t launch_w8a8_pair(const W8A8Args &a, const LaunchCtx &ctx, bool *enco
     const Plan plan = choose(slice, a.N, a.K, ctx.num_sms);
     const int bt = plan.bt, bk = k_of(bt);
     const Shares &shares = plan.shares;
-    const Shares last = a.M % slice ? share(bt, shares.sharers > shares.rest, a.M % slice, a.N, a.K, ctx.num_sms) : shares;
+    const Shares last = a.M % slice ? share(bt, shares.shared(), a.M % slice, a.N, a.K, ctx.num_sms) : shares;
     const size_t x_bytes = (static_cast<size_t>(slice) * ldh * 2 + 255) / 256 * 256;
-    const bool shared = shares.sharers > shares.rest || last.sharers > last.rest;
+    const bool shared = shares.shared() || last.shared();
     const size_t p_bytes = shared ? static_cast<size_t>(std::max(shares.sharers, last.sharers)) * 2 * bt * (2 * BW) * 4 : 0;
     CUtensorMap tmW;
     *encode_ok = encode_tma_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.W, a.K, a.N, a.ldw, bk, BW,
