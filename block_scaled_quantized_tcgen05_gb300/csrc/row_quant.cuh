@@ -59,10 +59,9 @@ __device__ __forceinline__ void mul2(float &d0, float &d1, float a0, float a1, f
 }
 
 // f(x) = x / (1 + exp(-v)), v = x (SiLU) or 2 sqrt(2/pi) (x + 0.044715 x^3) (GELU: (1 + tanh u) / 2 is
-// 1 / (1 + exp(-2 u))).  The exponential is taken of -|v|, so that it never overflows, and times 2^24, so that it stays
-// normal where f is: below 0 the numerator is x exp(-|v|).  Two values at once.
+// 1 / (1 + exp(-2 u))).  The exponential is taken of -|v|, so that it never overflows, as the square of t = exp(-|v| / 2), so that
+// it stays normal where f is: below 0 the numerator is x t t.  Two values at once.
 __device__ __forceinline__ void activate2(float &x0, float &x1, int kind) {
-    constexpr float DOWN = 0x1p-24f;
     float v0 = x0, v1 = x1;
     if (kind == QGEMM_ACT_GELU) {
         float s0, s1;
@@ -71,12 +70,12 @@ __device__ __forceinline__ void activate2(float &x0, float &x1, int kind) {
         mul2(v0, v1, x0, x1, s0, s1);
     }
     float t0, t1, r0, r1, n0, n1, d0, d1;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t0) : "f"(fmaf(fabsf(v0), -1.4426950408889634f, 24.0f)));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t1) : "f"(fmaf(fabsf(v1), -1.4426950408889634f, 24.0f)));
-    fma2(d0, d1, t0, t1, DOWN, DOWN, 1.0f, 1.0f);
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t0) : "f"(fabsf(v0) * -0.7213475204444817f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t1) : "f"(fabsf(v1) * -0.7213475204444817f));
+    fma2(d0, d1, t0, t1, t0, t1, 1.0f, 1.0f);
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(d0));          // of 1 .. 2
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(d1));
-    mul2(n0, n1, x0, x1, DOWN, DOWN);
+    mul2(n0, n1, x0, x1, t0, t1);
     mul2(n0, n1, n0, n1, t0, t1);
     mul2(x0, x1, v0 < 0.0f ? n0 : x0, v1 < 0.0f ? n1 : x1, r0, r1);
 }
@@ -99,17 +98,13 @@ __device__ __forceinline__ float to_f32(const void *p, int64_t i, int32_t dtype)
 __device__ __forceinline__ uint32_t codes_i8(const float *y, float inv, bool finite) {
     constexpr float HALF_WAY = 12582912.0f;
     float c[4];
-    fma2(c[0], c[1], y[0], y[1], inv, inv, HALF_WAY, HALF_WAY);
-    fma2(c[2], c[3], y[2], y[3], inv, inv, HALF_WAY, HALF_WAY);
+    mul2(c[0], c[1], y[0], y[1], inv, inv);      // rounded first: values half-way between codes, common in 16 bits, come out so
+    mul2(c[2], c[3], y[2], y[3], inv, inv);
+    add2(c[0], c[1], HALF_WAY, HALF_WAY);
+    add2(c[2], c[3], HALF_WAY, HALF_WAY);
     const uint32_t q = __byte_perm(__byte_perm(__float_as_uint(c[0]), __float_as_uint(c[1]), 0x0040),
                                    __byte_perm(__float_as_uint(c[2]), __float_as_uint(c[3]), 0x0040), 0x5410);
     return finite ? q : 0u;
-}
-
-__device__ __forceinline__ float reciprocal(float x) {
-    float r;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
 }
 
 // UE8M0 byte of a block whose largest magnitude is amax, and 2^-X.
@@ -349,6 +344,32 @@ __device__ __forceinline__ void store_any(uint8_t *p, const uint2 &v, int n) {
     else store_parts(p, v, n);
 }
 
+// A warp's consecutive eights of 16-bit elements at an address of any alignment, n of them before the row's end (any number,
+// 0 and less too; whole warps): each lane writes the aligned 16 bytes that its elements end with its neighbour's, the first
+// and the last lane what is over at the ends.
+__device__ __forceinline__ void store_warp(uint16_t *p, const uint4 &v, int n) {
+    const uint32_t off = before_16(p);           // the same in all lanes
+    const int lane = threadIdx.x & 31;
+    if (off == 0) {
+        if (n > 0) store_any(p, v, n);
+        return;
+    }
+    uint4 before;
+    before.x = __shfl_up_sync(0xFFFFFFFFu, v.x, 1);
+    before.y = __shfl_up_sync(0xFFFFFFFFu, v.y, 1);
+    before.z = __shfl_up_sync(0xFFFFFFFFu, v.z, 1);
+    before.w = __shfl_up_sync(0xFFFFFFFFu, v.w, 1);
+    const int over = static_cast<int>(off) / 2;  // elements of the neighbour's in this lane's 16 bytes
+    if (lane == 0) {
+        if (n > 0) store_parts(p, v, min(n, 8 - over));
+    } else {
+        const uint4 w = shifted(before, v, 16 - off, 8);
+        if (n + over >= 8) *reinterpret_cast<uint4 *>(p - over) = w;
+        else if (n + over > 0) store_parts(p - over, w, n + over);
+    }
+    if (lane == 31 && n > 8 - over) store_parts(p + 8 - over, shifted(v, v, 16 - off, 8), min(n, 8) - (8 - over));
+}
+
 // The ring of a block's rows in shared memory.
 struct Ring {
     int stages;
@@ -361,7 +382,7 @@ struct Ring {
 // shared memory, so that loads go on through the row's sum, its exchange and its stores.  ANY: rows of any alignment and
 // length.
 template <class TY, int OUT, bool NORM, bool SECOND, int C, bool WARP, bool ANY, bool BIG>
-__global__ void __launch_bounds__(WARP ? 256 : (C == 2 && !ANY) || BIG ? 1024 : 512, WARP ? 4 : 1)
+__global__ void __launch_bounds__(WARP ? 256 : (C == 2 && !ANY) || BIG ? 1024 : 512, !WARP ? 1 : NORM ? 4 : 5)
 row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring ring, unsigned *err, uint64_t timeout_ns) {
     __shared__ float2 room[2][32];
     extern __shared__ uint8_t rows_smem[];
@@ -395,6 +416,10 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
     auto put = [](auto *p, const auto &v, int n) {
         if constexpr (ANY) store_any(p, v, n);
         else *reinterpret_cast<std::decay_t<decltype(v)> *>(p) = v;
+    };
+    auto put16 = [](uint16_t *p, const uint4 &v, int n) {          // ANY: by whole warps
+        if constexpr (ANY) store_warp(p, v, n);
+        else *reinterpret_cast<uint4 *>(p) = v;
     };
     auto row_x = [&](int64_t row) { return static_cast<const uint16_t *>(a.x) + row * a.ldx; };
     auto row_2 = [&](int64_t row) { return static_cast<const uint16_t *>(a.second) + row * a.ld2; };
@@ -441,9 +466,10 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
                     if (SECOND)
 #pragma unroll
                         for (int j = 0; j < 8; j += 2) add2(v[i][j], v[i][j + 1], s[j], s[j + 1]);
+                    if (ANY && e - 8 * (t & 31) >= a.H) continue;  // whole warps
+                    if (SECOND && a.sum_out && (ANY || e < a.H))
+                        put16(static_cast<uint16_t *>(a.sum_out) + row * a.ldso + e, pack8<TY>(v[i]), a.H - e);
                     if (e >= a.H) continue;
-                    if (SECOND && a.sum_out)
-                        put(static_cast<uint16_t *>(a.sum_out) + row * a.ldso + e, pack8<TY>(v[i]), a.H - e);
 #pragma unroll
                     for (int j = 0; j < 8; j += 2)
                         fma2(s2[0], s2[1], v[i][j], v[i][j + 1], v[i][j], v[i][j + 1], s2[0], s2[1]);
@@ -511,7 +537,7 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
             if (!WARP) __syncthreads();
             read_done();
         }
-        [[maybe_unused]] const float most = max_nan(amax, LEAST), inv8 = 127.0f * reciprocal(most);
+        [[maybe_unused]] const float most = max_nan(amax, LEAST), inv8 = 127.0f / most;
         [[maybe_unused]] const bool finite = most <= FLT_MAX;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
@@ -553,7 +579,7 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
                     if ((t & 3) == 0) (static_cast<uint8_t *>(a.scales) + row * a.lds)[e / 32] = static_cast<uint8_t>(byte);
                 }
             } else {
-                if (in) put(static_cast<uint16_t *>(a.y) + row * a.ldy + e, pack8<TY>(v[i]), a.H - e);
+                if (ANY || in) put16(static_cast<uint16_t *>(a.y) + row * a.ldy + e, pack8<TY>(v[i]), a.H - e);
             }
         }
         if (OUT == OUT_INT8 && t == 0) static_cast<float *>(a.scales)[row] = most / 127.0f;

@@ -36,11 +36,11 @@ def norm_error(size):
 def act_error(x, kind="gelu"):
     """Relative error of f(x) * up in fp32: exp(-v) through the base-2 exponential carries v's relative error |v| times.
     v is x itself for silu and 2 roundings old with the factor log2(e); for gelu v = 2 u, |v| <= 1.6 |x| (1 + x^2 / 22), with 7
-    more roundings.  Past 104 exp(-|v|) is 0 in fp32 for every such error.  The exponential, the quotient (2 units each),
-    the sum and the product with `up` add at most 12."""
+    more roundings.  Past 104 exp(-|v|) is 0 in fp32 for every such error.  The exponential (2 units, twice as a
+    square: 8), the reciprocal (1 unit: 2), the sum and five products add at most 16."""
     top = float(x.abs().max())
     v = top if kind != "gelu" else 1.6 * top * (1 + top * top / 22)
-    return ((9 if kind == "gelu" else 2) * min(104.0, v) + 12) * U32
+    return ((9 if kind == "gelu" else 2) * min(104.0, v) + 16) * U32
 
 
 def check_int8(q, s, y, e):
