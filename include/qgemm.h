@@ -610,13 +610,15 @@ qgemm_status qgemm_act_quant(const void *X, int64_t ldx, const void *up, int64_t
 
 /* Product of 8-bit integers with a scale for each token and each channel:
  *   C[m, n] = round( (sum_k A[m, k] W[n, k]) * a_scales[m] * w_scales[n] [+ bias[n]] ).
- * Codes are two's complement int8, -128 included.  With M <= 16 the sums are fp32 sums of exact products on the
- * warp-level tensor cores, otherwise on tcgen05 (the integers as halves); integer sums below 2^24 are exact, larger
- * ones carry fp32's rounding.  Scales are applied to the sum in fp32; one rounding at the end.
+ * Codes are two's complement int8, -128 included, multiplied as halves on the tensor cores (exact products, fp32 sums):
+ * integer sums below 2^24 are exact, larger ones carry fp32's rounding.  Scales are applied to the sum in fp32; one rounding at the end.
  *   A         device int8 [M, K], row stride lda bytes;  a_scales fp32 [M].
  *   W         device int8 [N, K], row stride ldw bytes;  w_scales fp32 [N].
  *   bias      device [N] of c_dtype, or NULL.
  *   C         device [M, N] of c_dtype (QGEMM_F16 or QGEMM_BF16), row stride ldc elements; overlaps no input.
+ * Scratch: up to 16 tokens none (32 on matrices of at most 2^25 elements): one launch, K over a cluster's CTAs where there
+ * are few rows.  Otherwise the tokens' codes as halves (2 M ceil(K / 64) 64 bytes, in slices of rows that hold 512 MB at most) and, where
+ * pairs of CTAs share tiles along K, fp32 partial sums (at most 40 MB on 152 SMs), from the library's pool on `stream`.
  * Requirements: A and W 16-byte aligned with row strides in multiples of 16 (rows of any K are padded; the
  * padding is not read as data and may hold anything); scales 4-byte, bias and C 2-byte aligned; M, N, K below 2^31.  M or
  * N == 0 writes nothing; K == 0 gives the bias.
