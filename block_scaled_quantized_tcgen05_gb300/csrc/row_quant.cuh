@@ -633,8 +633,8 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
         int stage = 0;
         uint32_t phase = 0;
         for (int64_t row = blockIdx.x; row < a.T; row += step) {
-            if (!mbar_wait(bar0 + 8 * stage, phase, timeout_ns)) {
-                atomicOr(err, ERR_PRODUCER);
+            if (!mbar_wait_warp(bar0 + 8 * stage, phase, timeout_ns)) {
+                if ((t & 31) == 0) atomicOr(err, ERR_PRODUCER);
                 return;
             }
             const uint8_t *st = rows_smem + stage * ring.stage_bytes, *st2 = st + ring.second_at;

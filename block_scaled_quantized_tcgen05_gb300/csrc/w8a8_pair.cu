@@ -337,11 +337,11 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
         const uint8_t *row = smem + G::OFF_RAW + r * BK;
         // TMA's swizzle: chunk c of row r lies at c ^ (r % 8) of 128 bytes, or c ^ (r / 2 % 4) of 64
         const uint32_t swz = BK == 128 ? r & 7 : (r >> 1) & 3;
+        // A wait that gave up leaves the others no time: the lanes stay together (a vote after each wait costs 64 and 128 tokens 10
+        // to 20 %), and the warp goes through its k-tiles at once, whatever they hold.
+        uint64_t limit = timeout_ns;
         for (int i = first; i < total; i += G::TURNS) {
-            if (!mbar_wait(raw_full(slot_raw), phase_raw, timeout_ns)) {
-                if (lane == 0) atomicOr(err, ERR_PRODUCER);
-                break;
-            }
+            if (!mbar_wait(raw_full(slot_raw), phase_raw, limit)) limit = 0;
             const uint8_t *raw = row + slot_raw * G::RAW_BYTES;
             uint32_t out[32];
 #pragma unroll
@@ -356,10 +356,8 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(raw_empty(slot_raw));
-            if (!mbar_wait(empty_bar(stage), phase ^ 1, timeout_ns)) {   // the MMAs that last read this TMEM slot have completed
-                if (lane == 0) atomicOr(err, ERR_PRODUCER);
-                break;
-            }
+            // the MMAs that last read this TMEM slot have completed
+            if (!mbar_wait(empty_bar(stage), phase ^ 1, limit)) limit = 0;
             tc_fence_after();
             tmem_st_32x32b_x32(tmem_base + ((q * 32) << 16) + G::A_COL0 + stage * A_COLS + 32 * h, out);
             tmem_wait_st();
@@ -375,6 +373,7 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                 phase_raw ^= 1;
             }
         }
+        if (__any_sync(0xFFFFFFFFu, limit == 0) && lane == 0) atomicOr(err, ERR_PRODUCER);
     } else {
         // ---------------------------------------------------------------- epilogue
         // Lane i of a warp of lane quarter q holds output column n = weight row 32 q + i; the warp covers
@@ -400,7 +399,7 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
             __syncwarp();
             for (int c = static_cast<int>(lane); c < BT / 2; c += 32) sa_room[c] = m0 + c < M ? __ldg(a.sa + m0 + c) : 0.0f;
             __syncwarp();
-            if (!mbar_wait_sleep(tmem_full(buf), acc_phase, timeout_ns, 128)) {
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait_sleep(tmem_full(buf), acc_phase, timeout_ns, 128))) {
                 if (lane == 0) atomicOr(err, ERR_EPILOGUE);
                 break;
             }
