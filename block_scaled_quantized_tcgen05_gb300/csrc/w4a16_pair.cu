@@ -586,8 +586,9 @@ cudaError_t launch_pair_impl(const __half *A, int64_t lda, int M, const qgemm_te
                                BK / 2, BW, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (!*encode_ok) return cudaErrorInvalidValue;
     // output through TMA stores when C and its row stride allow a tensor map
-    // (the accumulate epilogue reads the old C element by element: direct stores)
-    const int c_tma = (reinterpret_cast<uintptr_t>(C) % 16 == 0 && ldc % 8 == 0 &&
+    // (they write whole 16-byte units, past a row's end too where N is no multiple of 8; the accumulate epilogue reads the
+    // old C element by element: direct stores in both cases)
+    const int c_tma = (reinterpret_cast<uintptr_t>(C) % 16 == 0 && ldc % 8 == 0 && N % 8 == 0 &&
                        !(ctx.epi & qgi::EPI_ACCUMULATE)) ? 1 : 0;
     if (c_tma) {
         *encode_ok = qgi::encode_tma_2d(&tmC, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, C, N, M, ldc * 2, 32, 32,
