@@ -370,11 +370,25 @@ __device__ __forceinline__ void store_warp(uint16_t *p, const uint4 &v, int n) {
     if (lane == 31 && n > 8 - over) store_parts(p + 8 - over, shifted(v, v, 16 - off, 8), min(n, 8) - (8 - over));
 }
 
+__device__ __forceinline__ uint64_t l2_policy_evict_normal() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
+__device__ __forceinline__ void bulk_load_hint(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar), "l"(policy)
+        : "memory");
+}
+
 // The ring of a block's rows in shared memory.
 struct Ring {
     int stages;
     uint32_t second_at, stage_bytes;         // where a stage's second operand begins; a stage
     int parts;                               // WARP: parts of a row, where an output needs nothing of the whole row
+    int once;                                // the inputs pass through L2 (they do not fit beside what others left there)
 };
 
 // A row held by a warp (WARP, eight rows a block, loaded directly) or by a block, 8 elements a thread and chunk, chunk i of
@@ -623,8 +637,9 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
             }
             const uint32_t bar = bar0 + 8 * stage, dst = sb + stage * ring.stage_bytes;
             mbar_arrive_expect_tx(bar, all);
-            bulk_load(dst, reinterpret_cast<const uint8_t *>(px) - offx, bytes, bar);
-            if (SECOND) bulk_load(dst + ring.second_at, reinterpret_cast<const uint8_t *>(p2) - off2, bytes2, bar);
+            const uint64_t policy = ring.once ? l2_policy_evict_first() : l2_policy_evict_normal();
+            bulk_load_hint(dst, reinterpret_cast<const uint8_t *>(px) - offx, bytes, bar, policy);
+            if (SECOND) bulk_load_hint(dst + ring.second_at, reinterpret_cast<const uint8_t *>(p2) - off2, bytes2, bar, policy);
         };
         const int64_t step = gridDim.x, ahead = step * ring.stages;
         if (t == 0)
@@ -700,6 +715,9 @@ cudaError_t launch_ring(K kern, RingPlan p, const qgi::RowQuantArgs &a, const qg
         grid = a.T;
         p.ring.stages = 1;
     }
+    // Inputs of more than 64 MB (half of L2) leave it first: 8192 x 8192 with residual 79.0 us against 81.3, where 4096 x 4096, whose
+    // inputs may still be there for the next call, would take 21.8 us against 21.2.
+    p.ring.once = int64_t(a.T) * p.ring.stage_bytes > (int64_t(1) << 26);
     const int smem = p.ring.stages * static_cast<int>(p.ring.stage_bytes);
     if (smem > 40 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
