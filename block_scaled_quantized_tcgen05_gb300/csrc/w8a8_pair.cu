@@ -563,15 +563,20 @@ __global__ void __launch_bounds__(256) w8a8_reduce_kernel(const float *__restric
     }
 }
 
+// How the tiles left after whole waves are cut: not at all; each into the same number of pieces; or all together into equal
+// ranges, which keeps every pair busy but leaves pieces of two tiles to most, and so more partial sums.
+enum Cut { NONE, EVEN, EQUAL };
+
 struct Plan {
     int bt;
+    Cut cut;
     Shares shares;
 };
 
 int k_of(int bt) { return bt == 256 ? Cfg<256>::BK : Cfg<64>::BK; }
 
-// Work of M tokens in tiles of bt, the tiles left after whole waves shared or not.
-Shares share(int bt, bool shared, int M, int N, int K, int num_sms) {
+// Work of M tokens in tiles of bt.
+Shares share(int bt, Cut cut, int M, int N, int K, int num_sms) {
     Shares s;
     const int bk = k_of(bt);
     s.KT = (K + bk - 1) / bk;
@@ -581,8 +586,10 @@ Shares share(int bt, bool shared, int M, int N, int K, int num_sms) {
     s.full = static_cast<int>(tiles / most * most);
     s.rest = static_cast<int>(tiles - s.full);
     s.sharers = s.rest;
-    if (shared) {    // in equal ranges of at least 256 of K, about 8 a tile at most (more cost the reduction a second round of loads)
-        const int64_t most_shares = std::min<int64_t>({most, int64_t(s.rest) * s.KT * bk / 256, int64_t(s.rest) * 8});
+    if (cut != NONE && s.rest > 0) {
+        // ranges of at least 256 of K, about 8 a tile at most (more cost the reduction a second round of loads)
+        int64_t most_shares = std::min<int64_t>({most, int64_t(s.rest) * s.KT * bk / 256, int64_t(s.rest) * 8});
+        if (cut == EVEN) most_shares -= most_shares % s.rest;
         if (most_shares > s.rest && int64_t(s.rest) * s.KT * most_shares < (int64_t(1) << 31)) s.sharers = static_cast<int>(most_shares);
     }
     if (s.full == 0) s.pairs = s.sharers;
@@ -599,7 +606,7 @@ double cost(int bt, const Shares &s, int M, int K) {
     const int waves = s.pairs ? s.full / s.pairs : 0;
     double us = waves * (std::max(s.KT * per_kt, s.pairs * tile_bytes / 5.8e6) + ends);
     if (s.rest) us += std::max(double(s.rest) * s.KT / s.sharers * per_kt, s.rest * tile_bytes / 5.8e6) + ends;
-    if (s.shared()) us += 2.0 + 2.0 * (s.sharers + s.rest) * bt * (2 * BW) * 4 / 5e6;
+    if (s.shared()) us += 2.0 + 2.0 * (s.sharers + (s.sharers % s.rest ? s.rest : 0)) * bt * (2 * BW) * 4 / 5e6;
     return us;
 }
 
@@ -607,12 +614,12 @@ Plan choose(int M, int N, int K, int num_sms) {
     Plan best{};
     double least = 1e300;
     for (int bt : {256, 128, 64})
-        for (bool shared : {false, true}) {
-            const Shares s = share(bt, shared, M, N, K, num_sms);
+        for (Cut cut : {NONE, EVEN, EQUAL}) {
+            const Shares s = share(bt, cut, M, N, K, num_sms);
             const double us = cost(bt, s, M, K);
             if (us < least) {
                 least = us;
-                best = {bt, s};
+                best = {bt, cut, s};
             }
         }
     return best;
@@ -675,7 +682,7 @@ cudaError_t launch_w8a8_pair(const W8A8Args &a, const LaunchCtx &ctx, bool *enco
     const Plan plan = choose(slice, a.N, a.K, ctx.num_sms);
     const int bt = plan.bt, bk = k_of(bt);
     const Shares &shares = plan.shares;
-    const Shares last = a.M % slice ? share(bt, shares.shared(), a.M % slice, a.N, a.K, ctx.num_sms) : shares;
+    const Shares last = a.M % slice ? share(bt, plan.cut, a.M % slice, a.N, a.K, ctx.num_sms) : shares;
     const size_t x_bytes = (static_cast<size_t>(slice) * ldh * 2 + 255) / 256 * 256;
     const bool shared = shares.shared() || last.shared();
     const size_t p_bytes = shared ? static_cast<size_t>(std::max(shares.sharers, last.sharers)) * 2 * bt * (2 * BW) * 4 : 0;
