@@ -596,16 +596,18 @@ Shares share(int bt, Cut cut, int M, int N, int K, int num_sms) {
     return s;
 }
 
-// Estimated us of a plan: the waves' walks over K, the start and end of a tile, the reduction's launch and traffic.
+// Estimated us of a plan: the waves' walks over K, what stays open at a tile's end, the reduction's launch and traffic.
 // Measured: a k-tile takes a pair 0.29, 0.34 and 0.30 us (64, 128 and 128 k for 256, 128 and 64 tokens; matrices that stay in L2);
-// all pairs together get 5.8 TB/s of weights from memory, which each weight leaves once however many token tiles meet it;
-// partial sums are written and read at 5 TB/s.
+// a wave of 256-token tiles, with one accumulator, ends 2.8 us after its walk, of smaller ones 0.2 (1.5 the last); all pairs together
+// get 5.8 TB/s of weights from memory, which each weight leaves once however many token tiles meet it; partial sums are written and
+// read at 5 TB/s.
 double cost(int bt, const Shares &s, int M, int K) {
-    const double per_kt = bt == 256 ? 0.29 : bt == 128 ? 0.34 : 0.30, ends = bt == 256 ? 2.5 : 1.5;
-    const double tile_bytes = double(2 * BW) * K / ((M + bt - 1) / bt);
+    const double per_kt = bt == 256 ? 0.29 : bt == 128 ? 0.34 : 0.30, ends = bt == 256 ? 2.8 : 0.2;
+    const double tile_us = double(2 * BW) * K / ((M + bt - 1) / bt) / 5.8e6;           // a tile's weights from memory
     const int waves = s.pairs ? s.full / s.pairs : 0;
-    double us = waves * (std::max(s.KT * per_kt, s.pairs * tile_bytes / 5.8e6) + ends);
-    if (s.rest) us += std::max(double(s.rest) * s.KT / s.sharers * per_kt, s.rest * tile_bytes / 5.8e6) + ends;
+    double us = waves * (std::max(s.KT * per_kt, s.pairs * tile_us) + ends);
+    if (s.rest) us += std::max(double(s.rest) * s.KT / s.sharers * per_kt, s.rest * tile_us) + ends;
+    if (bt < 256) us += 1.3;
     if (s.shared()) us += 2.0 + 2.0 * (s.sharers + (s.sharers % s.rest ? s.rest : 0)) * bt * (2 * BW) * 4 / 5e6;
     return us;
 }
