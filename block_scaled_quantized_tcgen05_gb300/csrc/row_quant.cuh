@@ -93,18 +93,35 @@ __device__ __forceinline__ float to_f32(const void *p, int64_t i, int32_t dtype)
     return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
 }
 
-// Four INT8 codes of y * inv, |y * inv| < 127.5: 1.5 * 2^23 added leaves the nearest integer (ties to even) in the low
-// bits.  A row with an infinity or a NaN has no finite factor: every code is 0 there.
-__device__ __forceinline__ uint32_t codes_i8(const float *y, float inv, bool finite) {
+// 127 / a as a pair: values half-way between codes are common where rows are quantised as they are (half of the row's
+// largest is one), and a factor rounded to 32 bits moves them to either side.
+struct Factor {
+    float hi, lo;
+    bool finite;                           // a row with an infinity or a NaN has no factor: every code is 0 there
+    __device__ __forceinline__ explicit Factor(float a) : hi(127.0f / a), finite(a <= FLT_MAX) {
+        lo = fmaf(-hi, a, 127.0f) * (hi * (1.0f / 127.0f));
+    }
+};
+
+// Four INT8 codes of y times the factor (PAIR: both parts of it), at most 127 in magnitude: 1.5 * 2^23 added leaves the nearest integer (ties to even)
+// in the low bits.
+template <bool PAIR>
+__device__ __forceinline__ uint32_t codes_i8(const float *y, const Factor &f) {
     constexpr float HALF_WAY = 12582912.0f;
     float c[4];
-    mul2(c[0], c[1], y[0], y[1], inv, inv);      // rounded first: values half-way between codes, common in 16 bits, come out so
-    mul2(c[2], c[3], y[2], y[3], inv, inv);
-    add2(c[0], c[1], HALF_WAY, HALF_WAY);
-    add2(c[2], c[3], HALF_WAY, HALF_WAY);
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+        if constexpr (PAIR) {
+            mul2(c[j], c[j + 1], y[j], y[j + 1], f.lo, f.lo);
+            fma2(c[j], c[j + 1], y[j], y[j + 1], f.hi, f.hi, c[j], c[j + 1]);
+        } else {
+            mul2(c[j], c[j + 1], y[j], y[j + 1], f.hi, f.hi);
+        }
+        add2(c[j], c[j + 1], HALF_WAY, HALF_WAY);
+    }
     const uint32_t q = __byte_perm(__byte_perm(__float_as_uint(c[0]), __float_as_uint(c[1]), 0x0040),
                                    __byte_perm(__float_as_uint(c[2]), __float_as_uint(c[3]), 0x0040), 0x5410);
-    return finite ? q : 0u;
+    return f.finite ? q : 0u;
 }
 
 // UE8M0 byte of a block whose largest magnitude is amax, and 2^-X.
@@ -197,8 +214,7 @@ __global__ void __launch_bounds__(256) row_quant_any_kernel(const __grid_constan
             }
         }
         const float most = max_nan(amax, LEAST);
-        const float inv8 = 127.0f / most;
-        const bool finite = most <= FLT_MAX;
+        const Factor factor(most);
         for (int c0 = threadIdx.x - lane; c0 < a.H; c0 += 256) {
             const int c = c0 + lane;
             const bool in = c < a.H;
@@ -211,7 +227,7 @@ __global__ void __launch_bounds__(256) row_quant_any_kernel(const __grid_constan
             const float y = in ? (a.norm ? v * f * r * weight(c) : v) : 0.0f;
             if constexpr (OUT == OUT_INT8) {
                 const float y4[4] = {y, 0.0f, 0.0f, 0.0f};
-                if (in) (static_cast<uint8_t *>(a.y) + row * a.ldy)[c] = static_cast<uint8_t>(codes_i8(y4, inv8, finite));
+                if (in) (static_cast<uint8_t *>(a.y) + row * a.ldy)[c] = static_cast<uint8_t>(codes_i8<true>(y4, factor));
             } else if constexpr (OUT == OUT_E4M3) {
                 float m = fabsf(y);        // a block of 32 is a warp's; fmaxf passes over NaN
 #pragma unroll
@@ -551,8 +567,8 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
             if (!WARP) __syncthreads();
             read_done();
         }
-        [[maybe_unused]] const float most = max_nan(amax, LEAST), inv8 = 127.0f / most;
-        [[maybe_unused]] const bool finite = most <= FLT_MAX;
+        [[maybe_unused]] const float most = max_nan(amax, LEAST);
+        [[maybe_unused]] const Factor factor(most);
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const int e = e0 + 8 * (i * nt + t);
@@ -568,7 +584,7 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
                 }
             }
             if constexpr (OUT == OUT_INT8) {
-                const uint2 q = make_uint2(codes_i8(v[i], inv8, finite), codes_i8(v[i] + 4, inv8, finite));
+                const uint2 q = make_uint2(codes_i8<!NORM && !SECOND>(v[i], factor), codes_i8<!NORM && !SECOND>(v[i] + 4, factor));
                 if (in) put(static_cast<uint8_t *>(a.y) + row * a.ldy + e, q, a.H - e);
             } else if constexpr (OUT == OUT_E4M3) {
                 float m = in ? 0.0f : 1.0f;                        // (lanes past the row's end share no block with others)

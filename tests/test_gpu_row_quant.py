@@ -239,3 +239,22 @@ def test_no_rows():
     y, s = outputs(0, 64, "int8", F)
     q.qgemm_act_quant(x, y, s)
     q.qgemm_norm_quant(x, None, y, s)
+
+
+@pytest.mark.parametrize("size", [512, 4096, 4101, 33000])
+def test_ties(size):
+    """Values exactly half-way between two codes go to the even one: halves of a row's largest, whatever that is."""
+    tokens = 200
+    top = (1 + torch.arange(tokens, device="cuda") / 128).clamp(max=1.9921875).to(B)       # every bf16 significand
+    x = torch.zeros(tokens, size, dtype=B, device="cuda")
+    x[:, 0] = top
+    odd = torch.arange(1, 127, 2, device="cuda", dtype=torch.float64) / 2                    # 0.5, 1.5, ... codes
+    for k, code in enumerate(odd.tolist()):
+        v = top.double() * code / 127
+        x[:, 1 + k] = torch.where(v.to(B).double() == v, v, 0).to(B)
+    x[:, -1] = -(top.double() / 2).to(B)                                                     # -63.5
+    y, s = outputs(tokens, size, "int8", B)
+    q.qgemm_act_quant(x, y, s)
+    want = torch.round(x.double() * 127 / top.double()[:, None])
+    assert torch.equal(y.double(), want)
+    assert torch.all(y[:, -1] == -64)
