@@ -27,7 +27,7 @@ using namespace qg;
 constexpr float LEAST = 0x1p-100f;      // the least magnitude an INT8 row's scale is taken from
 constexpr float SHRINK = 0x1p-80f;      // factor on h where the sum of squares passed fp32's range
 
-constexpr int MAX_STAGES = 8;           // rows of a block's ring
+constexpr int MAX_STAGES = 8;           // of a block's ring
 
 enum Out { OUT_INT8, OUT_E4M3, OUT_16 };
 
@@ -399,7 +399,7 @@ __device__ __forceinline__ void bulk_load_hint(uint32_t dst, const void *src, ui
         : "memory");
 }
 
-// The ring of a block's rows in shared memory.
+// The ring of a block in shared memory: rows, or parts of rows where few rows fit (`unit` chunks a stage).
 struct Ring {
     int stages;
     uint32_t second_at, stage_bytes;         // where a stage's second operand begins; a stage
@@ -407,14 +407,21 @@ struct Ring {
     int once;                                // the inputs pass through L2 (they do not fit beside what others left there)
 };
 
+// Chunks of a stage: a row's, whose place is free once its exchange has shown that all threads have read it; or one, free
+// once its warps have said so, where a row of two operands takes half of shared memory and more (2048 x 28672 gated SiLU to INT8: 54 us
+// against 70; shorter rows lose 5 to 15 % by the chunks' waits, and so does the long norm, which is short of registers).
+template <bool NORM, bool SECOND, int C, bool BIG>
+constexpr int unit_of = BIG && !NORM && SECOND ? 1 : C;
+
 // A row held by a warp (WARP, eight rows a block, loaded directly) or by a block, 8 elements a thread and chunk, chunk i of
-// thread t at element 8 (i nt + t).  A block walks its rows with the next ones on their way: bulk copies fill a ring of rows in
-// shared memory, so that loads go on through the row's sum, its exchange and its stores.  ANY: rows of any alignment and
-// length.
+// thread t at element 8 (i nt + t).  A block walks its rows with the next ones on their way: bulk copies fill a ring in
+// shared memory, so that loads go on through a row's sum, its exchange and its stores.  ANY: rows of any alignment and
+// length.  BIG: 1024 threads, which leaves no registers for weights.
 template <class TY, int OUT, bool NORM, bool SECOND, int C, bool WARP, bool ANY, bool BIG>
 __global__ void __launch_bounds__(WARP ? 256 : (C == 2 && !ANY) || BIG ? 1024 : 512, !WARP ? 1 : NORM ? 4 : 5)
 row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring ring, unsigned *err, uint64_t timeout_ns) {
     __shared__ float2 room[2][32];
+    constexpr int UNIT = unit_of<NORM, SECOND, C, BIG>;
     extern __shared__ uint8_t rows_smem[];
     griddep_launch_dependents();
     const int nt = WARP ? 32 : blockDim.x, t = WARP ? threadIdx.x & 31 : threadIdx.x;
@@ -471,7 +478,7 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
             load_weight8<ANY>(a, e, w);
     };
 
-    // One row: load(e, xv, sv) gives a chunk's operands, read_done() says that all threads have theirs.
+    // One row: load(i, e, xv, sv) gives chunk i's operands, read_done() says that all threads have theirs.
     auto process = [&](int64_t row, int e0, auto &&load, auto &&read_done) {
         // h, or the activation's product; zeros past the row's end
         float v[C][8], amax = 0.0f;
@@ -482,9 +489,9 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
             for (int i = 0; i < C; ++i) {
                 const int e = e0 + 8 * (i * nt + t);
                 xv[i] = sv[i] = make_uint4(0, 0, 0, 0);
-                if (e < a.H) load(e, xv[i], sv[i]);
+                load(i, e, xv[i], sv[i]);
             }
-            if (!WARP) fence_proxy_async_smem();                   // read here, written next by the bulk copies
+            if (!WARP && UNIT == C) fence_proxy_async_smem();      // read here, written next by the bulk copies
             float s2[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < C; ++i) {
@@ -626,63 +633,120 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
         const uint32_t offx = ANY ? before_16(px) : 0, off2 = ANY && SECOND ? before_16(p2) : 0;
         process(
             row, e0,
-            [&](int e, uint4 &xv, uint4 &sv) {
+            [&](int, int e, uint4 &xv, uint4 &sv) {
+                if (e >= a.H) return;
                 xv = ANY ? load_any(px + e, offx, a.H - e) : load_once(px + e);
                 if (SECOND) sv = ANY ? load_any(p2 + e, off2, a.H - e) : load_once(p2 + e);
             },
             [] {});
     } else {
-        __shared__ uint64_t full[MAX_STAGES];
-        const uint32_t sb = smem_u32(rows_smem), bar0 = smem_u32(full);
+        __shared__ uint64_t bars[UNIT == 1 ? 2 * MAX_STAGES : MAX_STAGES];
+        const uint32_t sb = smem_u32(rows_smem), full0 = smem_u32(bars), empty0 = full0 + 8 * MAX_STAGES;
         if (t == 0) {
-            for (int i = 0; i < ring.stages; ++i) mbar_init(bar0 + 8 * i, 1);
+            for (int i = 0; i < ring.stages; ++i) {
+                mbar_init(full0 + 8 * i, 1);
+                if (UNIT == 1) mbar_init(empty0 + 8 * i, nt >> 5);
+            }
             fence_barrier_init();
         }
         __syncthreads();
         griddep_wait();
-        auto fetch = [&](int64_t row, int stage) {                 // by one thread; whole 16-byte pieces that hold the row
-            const uint16_t *px = row_x(row);
-            const uint32_t offx = ANY ? before_16(px) : 0, bytes = (2 * a.H + offx + 15) & ~15u;
-            uint32_t all = bytes, off2 = 0, bytes2 = 0;
+        // By one thread: whole 16-byte pieces that hold a stage's part of a row.
+        auto fetch = [&](int64_t row, int part, int stage) {
+            const int first = 8 * UNIT * nt * part, n = UNIT == C ? a.H : min(8 * UNIT * nt, a.H - first);
+            const uint16_t *px = row_x(row) + first;
+            const uint32_t offx = ANY ? before_16(px) : 0, bytes = (2 * n + offx + 15) & ~15u;
+            uint32_t off2 = 0, bytes2 = 0;
             const uint16_t *p2 = nullptr;
             if (SECOND) {
-                p2 = row_2(row);
+                p2 = row_2(row) + first;
                 off2 = ANY ? before_16(p2) : 0;
-                bytes2 = (2 * a.H + off2 + 15) & ~15u;
-                all += bytes2;
+                bytes2 = (2 * n + off2 + 15) & ~15u;
             }
-            const uint32_t bar = bar0 + 8 * stage, dst = sb + stage * ring.stage_bytes;
-            mbar_arrive_expect_tx(bar, all);
+            const uint32_t bar = full0 + 8 * stage, dst = sb + stage * ring.stage_bytes;
+            mbar_arrive_expect_tx(bar, bytes + bytes2);
             const uint64_t policy = ring.once ? l2_policy_evict_first() : l2_policy_evict_normal();
             bulk_load_hint(dst, reinterpret_cast<const uint8_t *>(px) - offx, bytes, bar, policy);
             if (SECOND) bulk_load_hint(dst + ring.second_at, reinterpret_cast<const uint8_t *>(p2) - off2, bytes2, bar, policy);
         };
         const int64_t step = gridDim.x, ahead = step * ring.stages;
+        int64_t f_row = blockIdx.x;              // UNIT == 1: the next part to fetch, and how many have been
+        int f_part = 0, f_stage = 0, fetched = 0;
+        auto fetch_next = [&] {
+            if (f_row >= a.T) return;
+            fetch(f_row, f_part, f_stage);
+            ++fetched;
+            if (++f_stage == ring.stages) f_stage = 0;
+            if (++f_part == C) {
+                f_part = 0;
+                f_row += step;
+            }
+        };
         if (t == 0)
-            for (int i = 0; i < ring.stages && blockIdx.x + i * step < a.T; ++i) fetch(blockIdx.x + i * step, i);
+            for (int i = 0; i < ring.stages; ++i) {
+                if (UNIT == 1) fetch_next();
+                else if (blockIdx.x + i * step < a.T) fetch(blockIdx.x + i * step, 0, i);
+            }
         keep_weights();
-        int stage = 0;
-        uint32_t phase = 0;
-        for (int64_t row = blockIdx.x; row < a.T; row += step) {
-            if (!mbar_wait_warp(bar0 + 8 * stage, phase, timeout_ns)) {
-                if ((t & 31) == 0) atomicOr(err, ERR_PRODUCER);
-                return;
+        int stage = 0, last = -1;                // UNIT == 1: the stage read last, and its phase
+        uint32_t phase = 0, last_phase = 0;
+        uint64_t limit = timeout_ns;             // UNIT == 1: a wait that gave up leaves the others no time; the lanes stay together
+        int64_t row = blockIdx.x;
+        for (; row < a.T; row += step) {
+            if (UNIT == C && !mbar_wait_warp(full0 + 8 * stage, phase, timeout_ns)) {
+                limit = 0;
+                break;
             }
             const uint8_t *st = rows_smem + stage * ring.stage_bytes, *st2 = st + ring.second_at;
             const uint32_t offx = ANY ? before_16(row_x(row)) : 0, off2 = ANY && SECOND ? before_16(row_2(row)) : 0;
             const int at = stage;
             process(
                 row, 0,
-                [&](int e, uint4 &xv, uint4 &sv) {
-                    xv = ANY ? shared_any(st + 2 * e, offx, a.H - e) : *reinterpret_cast<const uint4 *>(st + 2 * e);
-                    if (SECOND) sv = ANY ? shared_any(st2 + 2 * e, off2, a.H - e) : *reinterpret_cast<const uint4 *>(st2 + 2 * e);
+                [&](int, int e, uint4 &xv, uint4 &sv) {
+                    if constexpr (UNIT == C) {
+                        if (e >= a.H) return;
+                        xv = ANY ? shared_any(st + 2 * e, offx, a.H - e) : *reinterpret_cast<const uint4 *>(st + 2 * e);
+                        if (SECOND) sv = ANY ? shared_any(st2 + 2 * e, off2, a.H - e) : *reinterpret_cast<const uint4 *>(st2 + 2 * e);
+                    } else {
+                        if (!mbar_wait(full0 + 8 * stage, phase, limit)) limit = 0;
+                        const uint8_t *p = rows_smem + stage * ring.stage_bytes + 16 * t, *p2 = p + ring.second_at;
+                        if (e < a.H) {
+                            xv = ANY ? shared_any(p, offx, a.H - e) : *reinterpret_cast<const uint4 *>(p);
+                            if (SECOND) sv = ANY ? shared_any(p2, off2, a.H - e) : *reinterpret_cast<const uint4 *>(p2);
+                        }
+                        fence_proxy_async_smem();                  // read here, written next by the bulk copies
+                        __syncwarp();
+                        if ((t & 31) == 0) mbar_arrive(empty0 + 8 * stage);
+                        if (t == 0 && last >= 0) {                 // the stage before this one: every warp is at its end or past it
+                            if (!mbar_wait(empty0 + 8 * last, last_phase, limit)) limit = 0;
+                            else if (limit) fetch_next();
+                        }
+                        last = stage;
+                        last_phase = phase;
+                        if (++stage == ring.stages) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
+                    }
                 },
                 [&] {
-                    if (t == 0 && row + ahead < a.T) fetch(row + ahead, at);
+                    if (UNIT == C && t == 0 && row + ahead < a.T) fetch(row + ahead, 0, at);
                 });
-            if (++stage == ring.stages) {
+            if (UNIT == C && ++stage == ring.stages) {
                 stage = 0;
                 phase ^= 1;
+            }
+        }
+        if (limit == 0) {
+            if ((t & 31) == 0) atomicOr(err, ERR_PRODUCER);
+            // No copy may land after the block has left: those of the stages from here on.
+            if (t == 0) {
+                if (UNIT == C) fetched = static_cast<int>(min(int64_t(ring.stages), (a.T - row + step - 1) / step));
+                for (int k = UNIT == C ? 0 : max(0, fetched - ring.stages); k < fetched; ++k) {
+                    const int from = UNIT == C ? stage + k : k;
+                    if (!mbar_wait(full0 + 8 * (from % ring.stages), (UNIT == C ? phase : 0) ^ (from / ring.stages & 1), timeout_ns))
+                        atomicOr(err, ERR_DRAIN);
+                }
             }
         }
     }
@@ -711,29 +775,29 @@ int registers_of(K kern) {
     return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? (at.numRegs + 7) / 8 * 8 : 128;
 }
 
-inline RingPlan plan_ring(int registers, int c, int H, bool second, bool any) {
+inline RingPlan plan_ring(int registers, int c, int unit, int H, bool second, bool any) {
     constexpr int ROOM = 220 * 1024;
     RingPlan p;
     p.threads = ((H + 7) / 8 + 32 * c - 1) / (32 * c) * 32;
     p.ring.parts = 1;
-    p.ring.second_at = (2 * H + (any ? 30 : 0)) / 16 * 16;
+    p.ring.second_at = (2 * std::min(H, 8 * unit * p.threads) + (any ? 30 : 0)) / 16 * 16;
     p.ring.stage_bytes = second ? 2 * p.ring.second_at : p.ring.second_at;
     p.blocks = std::max(1, std::min({16, 1024 / p.threads, 65536 / (registers * p.threads)}));
-    while (p.blocks > 1 && 2 * p.ring.stage_bytes > unsigned(ROOM / p.blocks - 1536)) --p.blocks;
+    while (p.blocks > 1 && 2 * c / unit * p.ring.stage_bytes > unsigned(ROOM / p.blocks - 1536)) --p.blocks;
     p.ring.stages = std::min(MAX_STAGES, (ROOM / p.blocks - 1536) / static_cast<int>(p.ring.stage_bytes));
     return p;
 }
 
 template <class K>
-cudaError_t launch_ring(K kern, RingPlan p, const qgi::RowQuantArgs &a, const qgi::LaunchCtx &ctx) {
+cudaError_t launch_ring(K kern, RingPlan p, int parts, const qgi::RowQuantArgs &a, const qgi::LaunchCtx &ctx) {
     int64_t grid = int64_t(p.blocks) * ctx.num_sms;
     if (grid >= a.T) {           // one row a block
         grid = a.T;
-        p.ring.stages = 1;
+        p.ring.stages = std::min(p.ring.stages, parts);
     }
     // Inputs of more than 64 MB (half of L2) leave it first: 8192 x 8192 with residual 79.0 us against 81.3, where 4096 x 4096, whose
     // inputs may still be there for the next call, would take 21.8 us against 21.2.
-    p.ring.once = int64_t(a.T) * p.ring.stage_bytes > (int64_t(1) << 26);
+    p.ring.once = int64_t(a.T) * a.H * (a.second ? 4 : 2) > (int64_t(1) << 26);
     const int smem = p.ring.stages * static_cast<int>(p.ring.stage_bytes);
     if (smem > 40 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -765,12 +829,13 @@ cudaError_t launch_vec(const qgi::RowQuantArgs &a, const qgi::LaunchCtx &ctx) {
         auto k4 = row_quant_vec_kernel<TY, OUT, NORM, SECOND, 4, false, ANY, false>;
         auto big = row_quant_vec_kernel<TY, OUT, NORM, SECOND, 4, false, ANY, true>;
         static const int r2 = registers_of(k2), r4 = registers_of(k4), r_big = registers_of(big);
-        if (a.H > 16384) return launch_ring(big, plan_ring(r_big, 4, a.H, SECOND, ANY), a, ctx);
+        constexpr int unit = unit_of<NORM, SECOND, 4, true>;
+        if (a.H > 16384) return launch_ring(big, plan_ring(r_big, 4, unit, a.H, SECOND, ANY), 4 / unit, a, ctx);
         const bool two = a.H <= (ANY ? 8192 : 16384);              // what its blocks may hold
-        const RingPlan p2 = plan_ring(r2, 2, a.H, SECOND, ANY);
-        if (two && p2.blocks >= 2) return launch_ring(k2, p2, a, ctx);
-        const RingPlan p4 = plan_ring(r4, 4, a.H, SECOND, ANY);
-        return p4.blocks >= 2 || !two ? launch_ring(k4, p4, a, ctx) : launch_ring(k2, p2, a, ctx);
+        const RingPlan p2 = plan_ring(r2, 2, 2, a.H, SECOND, ANY);
+        if (two && p2.blocks >= 2) return launch_ring(k2, p2, 1, a, ctx);
+        const RingPlan p4 = plan_ring(r4, 4, 4, a.H, SECOND, ANY);
+        return p4.blocks >= 2 || !two ? launch_ring(k4, p4, 1, a, ctx) : launch_ring(k2, p2, 1, a, ctx);
     }
 }
 
