@@ -80,13 +80,6 @@ __device__ __forceinline__ void activate2(float &x0, float &x1, int kind) {
     mul2(x0, x1, v0 < 0.0f ? n0 : x0, v1 < 0.0f ? n1 : x1, r0, r1);
 }
 
-__device__ __forceinline__ float activate(float x, int kind) {
-    if (kind == QGEMM_ACT_NONE) return x;
-    float unused = 0.0f;
-    activate2(x, unused, kind);
-    return x;
-}
-
 __device__ __forceinline__ float to_f32(const void *p, int64_t i, int32_t dtype) {
     if (dtype == QGEMM_F32) return static_cast<const float *>(p)[i];
     if (dtype == QGEMM_F16) return __half2float(static_cast<const __half *>(p)[i]);
@@ -158,92 +151,6 @@ __device__ __forceinline__ void block_reduce(float &ss, float &amax, float2 *roo
     for (int o = 16; o > 0; o >>= 1) {
         ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
         amax = max_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-    }
-}
-
-// Rows longer than a block holds in registers: one block a row, element by element, read a second time (from the
-// caches) once the row's sum and maximum are known.  Every element is read and written by one thread, so an output may
-// be an input.
-template <class TY, int OUT>
-__global__ void __launch_bounds__(256) row_quant_any_kernel(const __grid_constant__ qgi::RowQuantArgs a) {
-    using T = typename TY::T;
-    __shared__ float2 room[8];
-    griddep_launch_dependents();
-    griddep_wait();
-    const int lane = threadIdx.x & 31;
-    for (int row = blockIdx.x; row < a.T; row += gridDim.x) {
-        const T *x = static_cast<const T *>(a.x) + row * a.ldx;
-        const T *second = static_cast<const T *>(a.second) + (a.second ? row * a.ld2 : 0);
-        auto input = [&](int c) {          // h, or the activation's product
-            float v = static_cast<float>(x[c]);
-            if (a.norm) return a.second ? v + static_cast<float>(second[c]) : v;
-            v = activate(v, a.activation);
-            return a.second ? v * static_cast<float>(second[c]) : v;
-        };
-        auto weight = [&](int c) { return a.norm && a.weight ? to_f32(a.weight, c, a.weight_dtype) : 1.0f; };
-        float f = 1.0f, r = 1.0f, ss = 0.0f, amax = 0.0f;
-        if (a.norm || OUT == OUT_INT8) {
-            for (int c = threadIdx.x; c < a.H; c += 256) {
-                const float v = input(c);
-                ss += v * v;
-                amax = max_nan(amax, fabsf(v * weight(c)));
-            }
-            block_reduce(ss, amax, room);
-            if (a.norm) {
-                const bool wide = !(ss <= FLT_MAX);
-                if (wide) {
-                    f = SHRINK;
-                    ss = 0.0f;
-                    for (int c = threadIdx.x; c < a.H; c += 256) {
-                        const float v = input(c) * f;
-                        ss += v * v;
-                    }
-                    float unused = 0.0f;
-                    block_reduce(ss, unused, room);
-                }
-                r = rsqrtf(ss / static_cast<float>(a.H) + (wide ? 0.0f : a.eps));
-                if (OUT == OUT_INT8 && (wide || !(amax <= FLT_MAX))) {
-                    amax = 0.0f;
-                    for (int c = threadIdx.x; c < a.H; c += 256)
-                        amax = max_nan(amax, fabsf(input(c) * f * r * weight(c)));
-                    float unused = 0.0f;
-                    block_reduce(unused, amax, room);
-                } else {
-                    amax *= r;
-                }
-            }
-        }
-        const float most = max_nan(amax, LEAST);
-        const Factor factor(most);
-        for (int c0 = threadIdx.x - lane; c0 < a.H; c0 += 256) {
-            const int c = c0 + lane;
-            const bool in = c < a.H;
-            const float v = in ? input(c) : 0.0f;
-            if (in && a.sum_out) {
-                T *so = static_cast<T *>(a.sum_out) + row * a.ldso;
-                const uint32_t p = TY::pack(v, 0.0f);
-                reinterpret_cast<uint16_t *>(so)[c] = static_cast<uint16_t>(p);
-            }
-            const float y = in ? (a.norm ? v * f * r * weight(c) : v) : 0.0f;
-            if constexpr (OUT == OUT_INT8) {
-                const float y4[4] = {y, 0.0f, 0.0f, 0.0f};
-                if (in) (static_cast<uint8_t *>(a.y) + row * a.ldy)[c] = static_cast<uint8_t>(codes_i8<true>(y4, factor));
-            } else if constexpr (OUT == OUT_E4M3) {
-                float m = fabsf(y);        // a block of 32 is a warp's; fmaxf passes over NaN
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-                float inv;
-                const uint32_t byte = block_scale(fmaxf(m, 0.0f), &inv);
-                if (in) (static_cast<uint8_t *>(a.y) + row * a.ldy)[c] = static_cast<uint8_t>(e4m3x2(y * inv, 0.0f));
-                if (lane == 0) (static_cast<uint8_t *>(a.scales) + row * a.lds)[c / 32] = static_cast<uint8_t>(byte);
-            } else {
-                if (in) {
-                    T *yo = static_cast<T *>(a.y) + row * a.ldy;
-                    reinterpret_cast<uint16_t *>(yo)[c] = static_cast<uint16_t>(TY::pack(y, 0.0f));
-                }
-            }
-        }
-        if (OUT == OUT_INT8 && threadIdx.x == 0) static_cast<float *>(a.scales)[row] = most / 127.0f;
     }
 }
 
@@ -324,9 +231,9 @@ __device__ __forceinline__ void load_weight8(const qgi::RowQuantArgs &a, int e, 
     if (!a.weight) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i] = 1.0f;
-    } else if (ANY && (e + 8 > a.H || before_16(a.weight) != 0)) {
+    } else if (ANY && (a.H - e < 8 || before_16(a.weight) != 0)) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = e + i < a.H ? to_f32(a.weight, e + i, a.weight_dtype) : 0.0f;
+        for (int i = 0; i < 8; ++i) w[i] = i < a.H - e ? to_f32(a.weight, int64_t(e) + i, a.weight_dtype) : 0.0f;
     } else if (a.weight_dtype == QGEMM_F32) {
         const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.weight) + e);
         const float4 u = __ldg(p), v = __ldg(p + 1);
@@ -384,6 +291,155 @@ __device__ __forceinline__ void store_warp(uint16_t *p, const uint4 &v, int n) {
         else if (n + over > 0) store_parts(p - over, w, n + over);
     }
     if (lane == 31 && n > 8 - over) store_parts(p + 8 - over, shifted(v, v, 16 - off, 8), min(n, 8) - (8 - over));
+}
+
+// Elements e .. e + 7 of a row's y, or the n of them before its end (0 and less too), as the output has them; whole warps.
+// PAIR: INT8 codes by both parts of the factor.
+template <int OUT, bool ANY, class TY, bool PAIR>
+__device__ __forceinline__ void store_row(const qgi::RowQuantArgs &a, int64_t row, uint32_t e, int n, const float (&v)[8],
+                                          const Factor &factor) {
+    if constexpr (OUT == OUT_INT8) {
+        uint8_t *y = static_cast<uint8_t *>(a.y) + row * a.ldy + e;
+        const uint2 q = make_uint2(codes_i8<PAIR>(v, factor), codes_i8<PAIR>(v + 4, factor));
+        if (n > 0) {
+            if (ANY) store_any(y, q, n);
+            else *reinterpret_cast<uint2 *>(y) = q;
+        }
+    } else if constexpr (OUT == OUT_E4M3) {
+        float m = n > 0 ? 0.0f : 1.0f;         // (lanes past the row's end share no block with others)
+        if (n > 0) {
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) m = max_num(m, v[j], v[j + 1]);
+        }
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        float inv;
+        const uint32_t byte = block_scale(m, &inv);
+        uint32_t q[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float u[4];
+            mul2(u[0], u[1], v[4 * h], v[4 * h + 1], inv, inv);
+            mul2(u[2], u[3], v[4 * h + 2], v[4 * h + 3], inv, inv);
+            q[h] = uint32_t(e4m3x2(u[0], u[1])) | uint32_t(e4m3x2(u[2], u[3])) << 16;
+        }
+        if (n > 0) {
+            uint8_t *y = static_cast<uint8_t *>(a.y) + row * a.ldy + e;
+            if (ANY) store_any(y, make_uint2(q[0], q[1]), n);
+            else *reinterpret_cast<uint2 *>(y) = make_uint2(q[0], q[1]);
+            if ((threadIdx.x & 3) == 0) (static_cast<uint8_t *>(a.scales) + row * a.lds)[e / 32] = static_cast<uint8_t>(byte);
+        }
+    } else {
+        uint16_t *y = static_cast<uint16_t *>(a.y) + row * a.ldy + e;
+        if (ANY) store_warp(y, pack8<TY>(v), n);
+        else if (n > 0) *reinterpret_cast<uint4 *>(y) = pack8<TY>(v);
+    }
+}
+
+// Rows longer than a block holds in registers: one block a row, read a second time (from L2 mostly) once the row's sum and
+// maximum are known.  Operands of any alignment.  Every element is read and written by one thread, so an output may be an
+// input.  A thread's next pieces are on their way while it works on these.  Gated SiLU to INT8 of 1024 x 65536: 136 us, 16 x 53248:
+// 15.3 us; with 512 threads, two blocks an SM, 147 and 18.4 (2048 x 53248: 228 against 212).
+template <class TY, int OUT>
+__global__ void __launch_bounds__(1024) row_quant_long_kernel(const __grid_constant__ qgi::RowQuantArgs a) {
+    __shared__ float2 room[32];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31;
+    const uint32_t H = a.H, first = 8 * threadIdx.x;               // elements of 32 bits without a sign: H ends near 2^31
+    constexpr uint32_t STEP = 8 * 1024;
+    for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
+        const uint16_t *x = static_cast<const uint16_t *>(a.x) + row * a.ldx;
+        const uint16_t *second = static_cast<const uint16_t *>(a.second) + (a.second ? row * a.ld2 : 0);
+        const uint32_t offx = before_16(x), off2 = before_16(second);
+        struct Pieces {
+            uint4 x, second;
+        };
+        auto fetch = [&](uint32_t e) {                             // elements e .. e + 7; 0 past the row's end
+            Pieces p{};
+            const int n = static_cast<int>(H - e);
+            if (n > 0) {
+                p.x = load_any(x + e, offx, n);
+                if (a.second) p.second = load_any(second + e, off2, n);
+            }
+            return p;
+        };
+        auto input = [&](const Pieces &p, float (&v)[8]) {         // h, or the activation's product
+            float s[8];
+            unpack8<TY>(p.x, v);
+            unpack8<TY>(p.second, s);
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                if (!a.norm && a.activation != QGEMM_ACT_NONE) activate2(v[j], v[j + 1], a.activation);
+                if (a.norm) add2(v[j], v[j + 1], s[j], s[j + 1]);
+                else if (a.second) mul2(v[j], v[j + 1], v[j], v[j + 1], s[j], s[j + 1]);
+            }
+        };
+        float f = 1.0f, r = 1.0f, ss = 0.0f, amax = 0.0f;
+        // Sum of (h f)^2 and maximum of |y| / r, or of |y|
+        auto measure = [&](bool scaled) {
+            ss = amax = 0.0f;
+            Pieces next = fetch(first);
+            for (uint32_t e = first; e < H; e += STEP) {
+                const Pieces here = next;
+                next = fetch(e + STEP);
+                float v[8];
+                input(here, v);
+                if (a.norm) {
+                    float w[8], s2[2] = {0.0f, 0.0f};
+                    if (OUT == OUT_INT8) load_weight8<true>(a, static_cast<int>(e), w);
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2) {
+                        mul2(v[j], v[j + 1], v[j], v[j + 1], f, f);
+                        fma2(s2[0], s2[1], v[j], v[j + 1], v[j], v[j + 1], s2[0], s2[1]);
+                        if (scaled) mul2(v[j], v[j + 1], v[j], v[j + 1], r, r);
+                        if (OUT == OUT_INT8) mul2(v[j], v[j + 1], v[j], v[j + 1], w[j], w[j + 1]);
+                    }
+                    ss += s2[0] + s2[1];
+                }
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) amax = max_nan(amax, v[j], v[j + 1]);
+            }
+            block_reduce(ss, amax, room);
+        };
+        if (a.norm || OUT == OUT_INT8) {
+            measure(false);
+            if (a.norm) {
+                const bool wide = !(ss <= FLT_MAX);
+                if (wide) {
+                    f = SHRINK;
+                    measure(false);
+                }
+                r = rsqrtf(ss / static_cast<float>(a.H) + (wide ? 0.0f : a.eps));
+                if (OUT == OUT_INT8 && (wide || !(amax <= FLT_MAX))) measure(true);
+                else amax *= r;
+            }
+        }
+        const float most = max_nan(amax, LEAST);
+        const Factor factor(most);
+        Pieces next = fetch(first);
+        for (uint32_t e0 = first - 8 * lane; e0 < H; e0 += STEP) {   // whole warps
+            const uint32_t e = e0 + 8 * lane;
+            const int n = static_cast<int>(H - e);
+            const Pieces here = next;
+            next = fetch(e + STEP);
+            float v[8];
+            input(here, v);
+            if (a.sum_out) store_warp(static_cast<uint16_t *>(a.sum_out) + row * a.ldso + e, pack8<TY>(v), n);
+            if (a.norm && n > 0) {
+                float w[8];
+                load_weight8<true>(a, static_cast<int>(e), w);
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) {
+                    mul2(v[j], v[j + 1], v[j], v[j + 1], f, f);
+                    mul2(v[j], v[j + 1], v[j], v[j + 1], r, r);
+                    mul2(v[j], v[j + 1], v[j], v[j + 1], w[j], w[j + 1]);
+                }
+            }
+            store_row<OUT, true, TY, true>(a, row, e, n, v, factor);
+        }
+        if (OUT == OUT_INT8 && threadIdx.x == 0) static_cast<float *>(a.scales)[row] = most / 127.0f;
+    }
 }
 
 __device__ __forceinline__ uint64_t l2_policy_evict_normal() {
@@ -449,10 +505,6 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
             // lane 0 has the sum of the warps' lanes, whatever the others added
             if constexpr (SUM) ss = __shfl_sync(0xFFFFFFFFu, ss, 0);
         }
-    };
-    auto put = [](auto *p, const auto &v, int n) {
-        if constexpr (ANY) store_any(p, v, n);
-        else *reinterpret_cast<std::decay_t<decltype(v)> *>(p) = v;
     };
     auto put16 = [](uint16_t *p, const uint4 &v, int n) {          // ANY: by whole warps
         if constexpr (ANY) store_warp(p, v, n);
@@ -571,8 +623,7 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
             join(ss, amax);
             read_done();
         } else {
-            if (!WARP) __syncthreads();
-            read_done();
+            static_assert(WARP);                                   // nothing of the whole row is needed
         }
         [[maybe_unused]] const float most = max_nan(amax, LEAST);
         [[maybe_unused]] const Factor factor(most);
@@ -580,44 +631,16 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
         for (int i = 0; i < C; ++i) {
             const int e = e0 + 8 * (i * nt + t);
             if (e0 + 8 * (i * nt + (t & ~31)) >= a.H) continue;         // whole warps
-            const bool in = e < a.H;
             if constexpr (NORM) {
                 float w[8];
-                weights(i, in ? e : 0, w);
+                weights(i, e < a.H ? e : 0, w);
 #pragma unroll
                 for (int j = 0; j < 8; j += 2) {
                     mul2(v[i][j], v[i][j + 1], v[i][j], v[i][j + 1], r, r);
                     mul2(v[i][j], v[i][j + 1], v[i][j], v[i][j + 1], w[j], w[j + 1]);
                 }
             }
-            if constexpr (OUT == OUT_INT8) {
-                const uint2 q = make_uint2(codes_i8<!NORM && !SECOND>(v[i], factor), codes_i8<!NORM && !SECOND>(v[i] + 4, factor));
-                if (in) put(static_cast<uint8_t *>(a.y) + row * a.ldy + e, q, a.H - e);
-            } else if constexpr (OUT == OUT_E4M3) {
-                float m = in ? 0.0f : 1.0f;                        // (lanes past the row's end share no block with others)
-                if (in) {
-#pragma unroll
-                    for (int j = 0; j < 8; j += 2) m = max_num(m, v[i][j], v[i][j + 1]);
-                }
-                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-                float inv;
-                const uint32_t byte = block_scale(m, &inv);
-                uint32_t q[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float u[4];
-                    mul2(u[0], u[1], v[i][4 * h], v[i][4 * h + 1], inv, inv);
-                    mul2(u[2], u[3], v[i][4 * h + 2], v[i][4 * h + 3], inv, inv);
-                    q[h] = uint32_t(e4m3x2(u[0], u[1])) | uint32_t(e4m3x2(u[2], u[3])) << 16;
-                }
-                if (in) {
-                    put(static_cast<uint8_t *>(a.y) + row * a.ldy + e, make_uint2(q[0], q[1]), a.H - e);
-                    if ((t & 3) == 0) (static_cast<uint8_t *>(a.scales) + row * a.lds)[e / 32] = static_cast<uint8_t>(byte);
-                }
-            } else {
-                if (ANY || in) put16(static_cast<uint16_t *>(a.y) + row * a.ldy + e, pack8<TY>(v[i]), a.H - e);
-            }
+            store_row<OUT, ANY, TY, !NORM && !SECOND>(a, row, e, a.H - e, v[i], factor);
         }
         if (OUT == OUT_INT8 && t == 0) static_cast<float *>(a.scales)[row] = most / 127.0f;
     };
@@ -775,16 +798,17 @@ int registers_of(K kern) {
     return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? (at.numRegs + 7) / 8 * 8 : 128;
 }
 
+constexpr int RING_ROOM = 220 * 1024;    // of an SM's shared memory for rings
+
 inline RingPlan plan_ring(int registers, int c, int unit, int H, bool second, bool any) {
-    constexpr int ROOM = 220 * 1024;
     RingPlan p;
     p.threads = ((H + 7) / 8 + 32 * c - 1) / (32 * c) * 32;
     p.ring.parts = 1;
     p.ring.second_at = (2 * std::min(H, 8 * unit * p.threads) + (any ? 30 : 0)) / 16 * 16;
     p.ring.stage_bytes = second ? 2 * p.ring.second_at : p.ring.second_at;
     p.blocks = std::max(1, std::min({16, 1024 / p.threads, 65536 / (registers * p.threads)}));
-    while (p.blocks > 1 && 2 * c / unit * p.ring.stage_bytes > unsigned(ROOM / p.blocks - 1536)) --p.blocks;
-    p.ring.stages = std::min(MAX_STAGES, (ROOM / p.blocks - 1536) / static_cast<int>(p.ring.stage_bytes));
+    while (p.blocks > 1 && 2 * c / unit * p.ring.stage_bytes > unsigned(RING_ROOM / p.blocks - 1536)) --p.blocks;
+    p.ring.stages = std::min(MAX_STAGES, (RING_ROOM / p.blocks - 1536) / static_cast<int>(p.ring.stage_bytes));
     return p;
 }
 
@@ -800,7 +824,7 @@ cudaError_t launch_ring(K kern, RingPlan p, int parts, const qgi::RowQuantArgs &
     p.ring.once = int64_t(a.T) * a.H * (a.second ? 4 : 2) > (int64_t(1) << 26);
     const int smem = p.ring.stages * static_cast<int>(p.ring.stage_bytes);
     if (smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_ROOM);   // the same in all threads
         if (e != cudaSuccess) return e;
     }
     return launch_dependent(kern, dim3(static_cast<unsigned>(grid)), p.threads, smem, ctx.stream, a, p.ring, ctx.err,
@@ -841,9 +865,10 @@ cudaError_t launch_vec(const qgi::RowQuantArgs &a, const qgi::LaunchCtx &ctx) {
 
 template <class TY, int OUT>
 cudaError_t launch_out(const qgi::RowQuantArgs &a, const qgi::LaunchCtx &ctx) {
-    if (a.H > 32768) {           // past what a block's registers hold
-        const dim3 grid(static_cast<unsigned>(a.T < 16 * ctx.num_sms ? a.T : 16 * ctx.num_sms));
-        return launch_dependent(row_quant_any_kernel<TY, OUT>, grid, 256, 0, ctx.stream, a);
+    // Past what a block's registers hold; and past what 32 bits with a sign count, where nothing of the whole row is needed.
+    if (a.H > (a.norm || OUT == OUT_INT8 ? 1 << 15 : 1 << 30)) {
+        const dim3 grid(static_cast<unsigned>(a.T < ctx.num_sms ? a.T : ctx.num_sms));
+        return launch_dependent(row_quant_long_kernel<TY, OUT>, grid, 1024, 0, ctx.stream, a);
     }
     const int kind = 4 * a.norm + 2 * (a.second != nullptr) + vec_eligible(a);
     switch (kind) {

@@ -583,8 +583,9 @@ qgemm_status qgemm_kv_copy_pages(const qgemm_kv_cache *kv, const int32_t *src, c
  *   scales        QGEMM_INT8: fp32 [T].  QGEMM_E4M3: UE8M0 [T, H / 32], row stride lds bytes.  Else NULL.
  * Requirements: H % 32 == 0 for QGEMM_E4M3, otherwise any H; T and H below 2^31; rows of the outputs must not overlap.
  * Sums of squares that pass fp32's range (bfloat16 inputs above about 1e18) are taken again of h * 2^-80.
- * Speed: 16-byte aligned X, residual, residual_out and weight with row strides in multiples of 8 elements, and a Y
- * aligned to 8 of its elements, with H a multiple of 8 up to 32768, take the vector kernel; any other alignment works.
+ * Speed: rows of a multiple of 8 elements, 16-byte aligned (a Y of 8 bits 8-byte) at strides of multiples of 8 elements, are
+ * read and written as they lie; others are shifted into place on the way.  Rows past 32768 elements are read twice, but
+ * for activations to QGEMM_E4M3 and dtype.
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, UNSUPPORTED_DTYPE, MISALIGNED (nothing enqueued); CUDA. */
 qgemm_status qgemm_norm_quant(const void *X, int64_t ldx, const void *residual, int64_t ldr,
                               void *residual_out, int64_t ldro, int32_t dtype, const void *weight,

@@ -45,6 +45,31 @@ def test_long_row_apart():
     ref.check_int8(y, s, x.double(), 2 * ref.U32)
 
 
+@pytest.mark.parametrize("norm", [False, True])
+def test_longest_row(norm):
+    """A row whose last elements are the last that 31 bits count."""
+    size = (1 << 31) - 1
+    x = torch.empty(1, size, dtype=F, device="cuda")
+    for i in range(0, size, 1 << 28):
+        x[:, i:i + (1 << 28)].normal_().clamp_(-5, 5)
+    x[0, -3] = -6.0
+    y, s = torch.full((1, size), 99, dtype=torch.int8, device="cuda"), torch.empty(1, device="cuda")
+    square = 1.0
+    if norm:
+        q.qgemm_norm_quant(x, None, y, s, eps=1.0)
+        square = sum(x[:, i:i + (1 << 26)].double().square().sum().item() for i in range(0, size, 1 << 26)) / size + 1.0
+    else:
+        q.qgemm_act_quant(x, y, s)
+    # the sum: 2^20 additions in a row in each of 512 threads, at most half a step each
+    scale = 6.0 / 127 / square ** 0.5
+    assert abs(s.item() - scale) <= scale * ((1 << 20) * ref.U32 if norm else 2 * ref.U32)
+    for i in (0, 1 << 30, size - 5000):
+        code = x[:, i:i + 5000].double() * (127 / 6.0)
+        assert (y[:, i:i + 5000].double() - code).abs().max() <= 0.5 + 127 * 8 * ref.U32
+        assert i or (y[:, :5000] != 99).any()
+    assert q.qgemm_poll_device_error() == 0
+
+
 def product(m, n, k, rows, columns):
     a, w = torch.empty(m, k, dtype=torch.int8, device="cuda"), torch.empty(n, k, dtype=torch.int8, device="cuda")
     for t in (a, w):
