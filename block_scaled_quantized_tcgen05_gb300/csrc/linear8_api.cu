@@ -1,6 +1,7 @@
 // linear8_api.cu -- C ABI of the 8-bit linear layers: norm and activation with 8-bit output, and the
 // product of 8-bit integers.  Argument validation only; the kernels live in row_quant.cuh and
 // w8a8_*.cu.
+#include <algorithm>
 #include <cmath>
 
 #include "linear8_internal.h"
@@ -10,6 +11,7 @@ using qgi::fail;
 namespace {
 
 constexpr int64_t MAX_COUNT = (int64_t(1) << 31) - 1;
+constexpr int64_t MOST_ROUNDED = (int64_t(1) << 31) - 4096;     // sizes that the product's kernels round up to whole tiles
 
 bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
@@ -115,6 +117,8 @@ static qgemm_status w8a8_impl(const int8_t *A, int64_t lda, const float *sa, con
         return fail(QGEMM_ERR_UNSUPPORTED_DTYPE, "C is F16 or BF16 (got %d)", c_dtype);
     QG_TRY(check_shape(M, N));
     QG_TRY(check_shape(M, K));
+    if (std::max({M, N, K}) > MOST_ROUNDED)
+        return fail(QGEMM_ERR_UNSUPPORTED_SHAPE, "dimension > %lld", (long long)MOST_ROUNDED);
     if (M == 0 || N == 0) return QGEMM_OK;
     QG_TRY(check_output(C, ldc, M, N, 2, "C"));
     if (bias) QG_TRY(check_input(bias, 0, 1, 2, "bias"));

@@ -618,11 +618,12 @@ qgemm_status qgemm_act_quant(const void *X, int64_t ldx, const void *up, int64_t
  *   bias      device [N] of c_dtype, or NULL.
  *   C         device [M, N] of c_dtype (QGEMM_F16 or QGEMM_BF16), row stride ldc elements; overlaps no input.
  * Scratch: up to 16 tokens none (32 on matrices of at most 2^25 elements): one launch, K over a cluster's CTAs where there
- * are few rows.  Otherwise the tokens' codes as halves (2 M ceil(K / 64) 64 bytes, in slices of rows that hold 512 MB at most) and, where
- * pairs of CTAs share tiles along K, fp32 partial sums (at most 40 MB on 152 SMs), from the library's pool on `stream`.
+ * are few rows.  Otherwise, from the library's pool on `stream`, the tokens' codes as halves (2 M ceil(K / 64) 64 bytes, taken in
+ * slices of as many rows as 512 MB hold, 256 at least) and, where pairs of CTAs share tiles along K, fp32 partial sums (at most 40 MB
+ * on 152 SMs).
  * Requirements: A and W 16-byte aligned with row strides in multiples of 16 (rows of any K are padded; the
- * padding is not read as data and may hold anything); scales 4-byte, bias and C 2-byte aligned; M, N, K below 2^31.  M or
- * N == 0 writes nothing; K == 0 gives the bias.
+ * padding is not read as data and may hold anything); scales 4-byte, bias and C 2-byte aligned; M, N, K at most
+ * 2^31 - 4096.  M or N == 0 writes nothing; K == 0 gives the bias.
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, UNSUPPORTED_DTYPE, MISALIGNED (nothing enqueued); CUDA (including a
  * failed scratch allocation). */
 qgemm_status qgemm_w8a8(const int8_t *A, int64_t lda, const float *a_scales, const int8_t *W, int64_t ldw,

@@ -74,6 +74,12 @@ def test_product_refusals(lib, change, status):
     refused(lib, PROD, status, **change)
 
 
+@pytest.mark.parametrize("change", [{"M": BIG - 4095}, {"N": BIG - 4095, "ldc": BIG}, {"K": BIG - 4095, "lda": BIG, "ldw": BIG}])
+def test_product_sizes_round_up_in_31_bits(lib, change):
+    """The kernels round sizes up to whole tiles in 32-bit integers."""
+    refused(lib, PROD, SHAPE, **change)
+
+
 def test_epilogue_fields(lib):
     for bad in ((2, 0), (0, -1)):
         ep = q.Epilogue(*bad)
