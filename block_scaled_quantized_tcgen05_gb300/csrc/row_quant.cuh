@@ -96,6 +96,12 @@ struct Factor {
     }
 };
 
+// Whether a norm's codes can be those of h w, whose largest magnitude is `most`: the row's factor r changes no code, and
+// takes two roundings with it.  Not where the scale has its least value, or h w may be below fp32's normal range (or NaN).
+__device__ __forceinline__ bool codes_without_r(float most, float most_y) {
+    return most <= FLT_MAX && most >= LEAST && most_y >= LEAST;
+}
+
 // Four INT8 codes of y times the factor (PAIR: both parts of it), at most 127 in magnitude: 1.5 * 2^23 added leaves the nearest integer (ties to even)
 // in the low bits.
 template <bool PAIR>
@@ -107,10 +113,10 @@ __device__ __forceinline__ uint32_t codes_i8(const float *y, const Factor &f) {
         if constexpr (PAIR) {
             mul2(c[j], c[j + 1], y[j], y[j + 1], f.lo, f.lo);
             fma2(c[j], c[j + 1], y[j], y[j + 1], f.hi, f.hi, c[j], c[j + 1]);
+            add2(c[j], c[j + 1], HALF_WAY, HALF_WAY);
         } else {
-            mul2(c[j], c[j + 1], y[j], y[j + 1], f.hi, f.hi);
+            fma2(c[j], c[j + 1], y[j], y[j + 1], f.hi, f.hi, HALF_WAY, HALF_WAY);
         }
-        add2(c[j], c[j + 1], HALF_WAY, HALF_WAY);
     }
     const uint32_t q = __byte_perm(__byte_perm(__float_as_uint(c[0]), __float_as_uint(c[1]), 0x0040),
                                    __byte_perm(__float_as_uint(c[2]), __float_as_uint(c[3]), 0x0040), 0x5410);
@@ -411,12 +417,18 @@ __global__ void __launch_bounds__(1024) row_quant_long_kernel(const __grid_const
                     measure(false);
                 }
                 r = rsqrtf(ss / static_cast<float>(a.H) + (wide ? 0.0f : a.eps));
-                if (OUT == OUT_INT8 && (wide || !(amax <= FLT_MAX))) measure(true);
-                else amax *= r;
             }
         }
-        const float most = max_nan(amax, LEAST);
-        const Factor factor(most);
+        float shown = amax * r;                                    // the largest |y|; amax that of what is turned into codes
+        if (OUT == OUT_INT8) {
+            if (a.norm && f == 1.0f && codes_without_r(amax, shown)) {
+                r = 1.0f;
+            } else {
+                if (a.norm) measure(true);
+                shown = amax = max_nan(amax, LEAST);
+            }
+        }
+        const Factor factor(amax);
         Pieces next = fetch(first);
         for (uint32_t e0 = first - 8 * lane; e0 < H; e0 += STEP) {   // whole warps
             const uint32_t e = e0 + 8 * lane;
@@ -438,7 +450,7 @@ __global__ void __launch_bounds__(1024) row_quant_long_kernel(const __grid_const
             }
             store_row<OUT, true, TY, true>(a, row, e, n, v, factor);
         }
-        if (OUT == OUT_INT8 && threadIdx.x == 0) static_cast<float *>(a.scales)[row] = most / 127.0f;
+        if (OUT == OUT_INT8 && threadIdx.x == 0) static_cast<float *>(a.scales)[row] = shown / 127.0f;
     }
 }
 
@@ -534,6 +546,7 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
     auto process = [&](int64_t row, int e0, auto &&load, auto &&read_done) {
         // h, or the activation's product; zeros past the row's end
         float v[C][8], amax = 0.0f;
+        [[maybe_unused]] float shown = 0.0f;                       // the largest |y|; amax that of what is turned into codes
         [[maybe_unused]] float r = 1.0f, ss = 0.0f;
         {
             uint4 xv[C], sv[C];
@@ -603,30 +616,34 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
                 join(ss, unused);
             }
             r = rsqrtf(fmaf(ss, per_h, wide ? 0.0f : a.eps));
-            if (OUT == OUT_INT8 && (wide || !(amax <= FLT_MAX))) {
-                amax = 0.0f;
+            if constexpr (OUT == OUT_INT8) {
+                shown = amax * r;
+                if (wide || !codes_without_r(amax, shown)) {
+                    amax = 0.0f;
 #pragma unroll
-                for (int i = 0; i < C; ++i) {
-                    const int e = e0 + 8 * (i * nt + t);
-                    if (e >= a.H) continue;
-                    float w[8];
-                    weights(i, e, w);
+                    for (int i = 0; i < C; ++i) {
+                        const int e = e0 + 8 * (i * nt + t);
+                        if (e >= a.H) continue;
+                        float w[8];
+                        weights(i, e, w);
 #pragma unroll
-                    for (int j = 0; j < 8; j += 2) amax = max_nan(amax, v[i][j] * r * w[j], v[i][j + 1] * r * w[j + 1]);
+                        for (int j = 0; j < 8; ++j) v[i][j] *= r;
+#pragma unroll
+                        for (int j = 0; j < 8; j += 2) amax = max_nan(amax, v[i][j] * w[j], v[i][j + 1] * w[j + 1]);
+                    }
+                    float unused = 0.0f;
+                    join(unused, amax);
+                    shown = amax = max_nan(amax, LEAST);
                 }
-                float unused = 0.0f;
-                join(unused, amax);
-            } else {
-                amax *= r;
             }
         } else if constexpr (OUT == OUT_INT8) {
             join(ss, amax);
             read_done();
+            shown = amax = max_nan(amax, LEAST);
         } else {
             static_assert(WARP);                                   // nothing of the whole row is needed
         }
-        [[maybe_unused]] const float most = max_nan(amax, LEAST);
-        [[maybe_unused]] const Factor factor(most);
+        [[maybe_unused]] const Factor factor(amax);
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const int e = e0 + 8 * (i * nt + t);
@@ -636,13 +653,13 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
                 weights(i, e < a.H ? e : 0, w);
 #pragma unroll
                 for (int j = 0; j < 8; j += 2) {
-                    mul2(v[i][j], v[i][j + 1], v[i][j], v[i][j + 1], r, r);
+                    if (OUT != OUT_INT8) mul2(v[i][j], v[i][j + 1], v[i][j], v[i][j + 1], r, r);
                     mul2(v[i][j], v[i][j + 1], v[i][j], v[i][j + 1], w[j], w[j + 1]);
                 }
             }
             store_row<OUT, ANY, TY, !NORM && !SECOND>(a, row, e, a.H - e, v[i], factor);
         }
-        if (OUT == OUT_INT8 && t == 0) static_cast<float *>(a.scales)[row] = most / 127.0f;
+        if (OUT == OUT_INT8 && t == 0) static_cast<float *>(a.scales)[row] = shown / 127.0f;
     };
 
     if constexpr (WARP) {
