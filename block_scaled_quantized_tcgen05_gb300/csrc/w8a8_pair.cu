@@ -20,6 +20,10 @@
 //     cut into equal ranges of K, one a pair, whatever tiles they cover: a tile that several pairs share leaves fp32 partial
 //     sums in scratch, which a reduction kernel adds in the order of K.  (The warp that finishes a piece last adding them at the
 //     kernel's end instead: 4096 x 14336 x 4096 in 310 us against 294, 256 x 4096 x 4096 29 against 21: too few loads in flight.)
+//
+// Measured: 8192^3 554 - 566 us (1.94 - 1.98 PFLOP/s, what the library's bf16 product reaches), 4096 x 14336 x 4096 246 us, 4096^3 83;
+// 64 x 28672 x 8192 46 us (5.1 TB/s of weights; a converter warp's chain of wait, read, convert, write and arrival takes
+// as long as the bytes), 333 x 5003 x 4111 19 us: the tokens' halves 4, the k-tiles 11, epilogue, partial sums and launches the rest.
 #include <algorithm>
 #include <type_traits>
 
