@@ -230,9 +230,12 @@ __device__ __forceinline__ uint4 load_any(const uint16_t *p, uint32_t off, int n
 
 // The same from a stage of the ring, `p` the element's place without the offset.
 __device__ __forceinline__ uint4 shared_any(const uint8_t *p, uint32_t off, int n) {
-    const uint4 *piece = reinterpret_cast<const uint4 *>(p);
-    if (off == 0 && n >= 8) return piece[0];
-    return shifted(piece[0], off + 2 * n > 16 ? piece[1] : make_uint4(0, 0, 0, 0), off, n);
+    if (off == 0 && n >= 8) return *reinterpret_cast<const uint4 *>(p);
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(p + (off & 12));
+    const uint32_t bits = 8 * (off & 2);
+    const uint4 all = make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                                 __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+    return n < 8 ? first_of(all, n) : all;
 }
 
 __device__ __forceinline__ uint32_t before_16(const void *p) { return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15); }
@@ -519,9 +522,8 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
             turn ^= 1;
             ss = v.x;
             amax = v.y;
-            over(warps > 16 ? 32 : warps > 8 ? 16 : warps > 4 ? 8 : 4);
-            // lane 0 has the sum of the warps' lanes, whatever the others added
-            if constexpr (SUM) ss = __shfl_sync(0xFFFFFFFFu, ss, 0);
+            over(ANY ? warps > 16 ? 32 : warps > 8 ? 16 : warps > 4 ? 8 : 4 : 32);
+            if constexpr (ANY && SUM) ss = __shfl_sync(0xFFFFFFFFu, ss, 0);
         }
     };
     auto put16 = [](uint16_t *p, const uint4 &v, int n) {          // ANY: by whole warps
@@ -548,8 +550,10 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
             load_weight8<ANY>(a, e, w);
     };
 
-    // One row: load(i, e, xv, sv) gives chunk i's operands, read_done() says that all threads have theirs.
-    auto process = [&](int64_t row, int e0, auto &&load, auto &&read_done) {
+    // One row: load(i, e, n, xv, sv) gives chunk i's operands, read_done() says that all threads have theirs.  `in`: all of the warp's
+    // elements are the row's, which saves the tests (n is the number of elements from e on that are, or at least 8).
+    auto process = [&](auto in, int64_t row, int e0, auto &&load, auto &&read_done) {
+        constexpr bool IN = decltype(in)::value;
         // h, or the activation's product; zeros past the row's end
         float v[C][8], amax = 0.0f;
         [[maybe_unused]] float shown = 0.0f;                       // the largest |y|; amax that of what is turned into codes
@@ -560,7 +564,7 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
             for (int i = 0; i < C; ++i) {
                 const int e = e0 + 8 * (i * nt + t);
                 xv[i] = sv[i] = make_uint4(0, 0, 0, 0);
-                load(i, e, xv[i], sv[i]);
+                load(i, e, IN ? 8 : a.H - e, xv[i], sv[i]);
             }
             if (!WARP && UNIT == C) fence_proxy_async_smem();      // read here, written next by the bulk copies
             float s2[2] = {0.0f, 0.0f};
@@ -574,10 +578,10 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
                     if (SECOND)
 #pragma unroll
                         for (int j = 0; j < 8; j += 2) add2(v[i][j], v[i][j + 1], s[j], s[j + 1]);
-                    if (ANY && e - 8 * (t & 31) >= a.H) continue;  // whole warps
-                    if (SECOND && a.sum_out && (ANY || e < a.H))
-                        put16(static_cast<uint16_t *>(a.sum_out) + row * a.ldso + e, pack8<TY>(v[i]), a.H - e);
-                    if (e >= a.H) continue;
+                    if (!IN && ANY && e - 8 * (t & 31) >= a.H) continue;  // whole warps
+                    if (SECOND && a.sum_out && (IN || ANY || e < a.H))
+                        put16(static_cast<uint16_t *>(a.sum_out) + row * a.ldso + e, pack8<TY>(v[i]), IN ? 8 : a.H - e);
+                    if (!IN && e >= a.H) continue;
 #pragma unroll
                     for (int j = 0; j < 8; j += 2)
                         fma2(s2[0], s2[1], v[i][j], v[i][j + 1], v[i][j], v[i][j + 1], s2[0], s2[1]);
@@ -629,7 +633,7 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
 #pragma unroll
                     for (int i = 0; i < C; ++i) {
                         const int e = e0 + 8 * (i * nt + t);
-                        if (e >= a.H) continue;
+                        if (!IN && e >= a.H) continue;
                         float w[8];
                         weights(i, e, w);
 #pragma unroll
@@ -653,17 +657,17 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const int e = e0 + 8 * (i * nt + t);
-            if (e0 + 8 * (i * nt + (t & ~31)) >= a.H) continue;         // whole warps
+            if (!IN && e0 + 8 * (i * nt + (t & ~31)) >= a.H) continue;         // whole warps
             if constexpr (NORM) {
                 float w[8];
-                weights(i, e < a.H ? e : 0, w);
+                weights(i, IN || e < a.H ? e : 0, w);
 #pragma unroll
                 for (int j = 0; j < 8; j += 2) {
                     if (OUT != OUT_INT8) mul2(v[i][j], v[i][j + 1], v[i][j], v[i][j + 1], r, r);
                     mul2(v[i][j], v[i][j + 1], v[i][j], v[i][j + 1], w[j], w[j + 1]);
                 }
             }
-            store_row<OUT, ANY, TY, !NORM && !SECOND>(a, row, e, a.H - e, v[i], factor);
+            store_row<OUT, ANY, TY, !NORM && !SECOND>(a, row, e, IN ? 8 : a.H - e, v[i], factor);
         }
         if (OUT == OUT_INT8 && t == 0) static_cast<float *>(a.scales)[row] = shown / 127.0f;
     };
@@ -677,14 +681,13 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
         keep_weights();
         const uint16_t *px = row_x(row), *p2 = SECOND ? row_2(row) : nullptr;
         const uint32_t offx = ANY ? before_16(px) : 0, off2 = ANY && SECOND ? before_16(p2) : 0;
-        process(
-            row, e0,
-            [&](int, int e, uint4 &xv, uint4 &sv) {
-                if (e >= a.H) return;
-                xv = ANY ? load_any(px + e, offx, a.H - e) : load_once(px + e);
-                if (SECOND) sv = ANY ? load_any(p2 + e, off2, a.H - e) : load_once(p2 + e);
-            },
-            [] {});
+        auto load = [&](int, int e, int n, uint4 &xv, uint4 &sv) {
+            if (n <= 0) return;
+            xv = ANY ? load_any(px + e, offx, n) : load_once(px + e);
+            if (SECOND) sv = ANY ? load_any(p2 + e, off2, n) : load_once(p2 + e);
+        };
+        if (!ANY && a.H - e0 >= 256 * C) process(std::bool_constant<!ANY>{}, row, e0, load, [] {});
+        else process(std::false_type{}, row, e0, load, [] {});
     } else {
         __shared__ uint64_t bars[UNIT == 1 ? 2 * MAX_STAGES : MAX_STAGES];
         const uint32_t sb = smem_u32(rows_smem), full0 = smem_u32(bars), empty0 = full0 + 8 * MAX_STAGES;
@@ -738,6 +741,7 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
         uint32_t phase = 0, last_phase = 0;
         uint64_t limit = timeout_ns;             // UNIT == 1: a wait that gave up leaves the others no time; the lanes stay together
         int64_t row = blockIdx.x;
+        const bool all_in = 8 * ((C - 1) * nt + (t | 31)) + 8 <= a.H;
         for (; row < a.T; row += step) {
             if (UNIT == C && !mbar_wait_warp(full0 + 8 * stage, phase, timeout_ns)) {
                 limit = 0;
@@ -746,19 +750,17 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
             const uint8_t *st = rows_smem + stage * ring.stage_bytes, *st2 = st + ring.second_at;
             const uint32_t offx = ANY ? before_16(row_x(row)) : 0, off2 = ANY && SECOND ? before_16(row_2(row)) : 0;
             const int at = stage;
-            process(
-                row, 0,
-                [&](int, int e, uint4 &xv, uint4 &sv) {
+            auto load = [&](int, int e, int n, uint4 &xv, uint4 &sv) {
                     if constexpr (UNIT == C) {
-                        if (e >= a.H) return;
-                        xv = ANY ? shared_any(st + 2 * e, offx, a.H - e) : *reinterpret_cast<const uint4 *>(st + 2 * e);
-                        if (SECOND) sv = ANY ? shared_any(st2 + 2 * e, off2, a.H - e) : *reinterpret_cast<const uint4 *>(st2 + 2 * e);
+                        if (n <= 0) return;
+                        xv = ANY ? shared_any(st + 2 * e, offx, n) : *reinterpret_cast<const uint4 *>(st + 2 * e);
+                        if (SECOND) sv = ANY ? shared_any(st2 + 2 * e, off2, n) : *reinterpret_cast<const uint4 *>(st2 + 2 * e);
                     } else {
                         if (!mbar_wait(full0 + 8 * stage, phase, limit)) limit = 0;
                         const uint8_t *p = rows_smem + stage * ring.stage_bytes + 16 * t, *p2 = p + ring.second_at;
-                        if (e < a.H) {
-                            xv = ANY ? shared_any(p, offx, a.H - e) : *reinterpret_cast<const uint4 *>(p);
-                            if (SECOND) sv = ANY ? shared_any(p2, off2, a.H - e) : *reinterpret_cast<const uint4 *>(p2);
+                        if (n > 0) {
+                            xv = ANY ? shared_any(p, offx, n) : *reinterpret_cast<const uint4 *>(p);
+                            if (SECOND) sv = ANY ? shared_any(p2, off2, n) : *reinterpret_cast<const uint4 *>(p2);
                         }
                         fence_proxy_async_smem();                  // read here, written next by the bulk copies
                         __syncwarp();
@@ -774,10 +776,13 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
                             phase ^= 1;
                         }
                     }
-                },
-                [&] {
-                    if (UNIT == C && t == 0 && row + ahead < a.T) fetch(row + ahead, 0, at);
-                });
+                };
+            auto read_done = [&] {
+                if (UNIT == C && t == 0 && row + ahead < a.T) fetch(row + ahead, 0, at);
+            };
+            // (at any alignment a second body costs more than the tests: 5003 x 5111 29.0 us against 26.8)
+            if (!ANY && all_in) process(std::bool_constant<!ANY>{}, row, 0, load, read_done);
+            else process(std::false_type{}, row, 0, load, read_done);
             if (UNIT == C && ++stage == ring.stages) {
                 stage = 0;
                 phase ^= 1;
@@ -845,7 +850,7 @@ cudaError_t launch_ring(K kern, RingPlan p, int parts, const qgi::RowQuantArgs &
     // Inputs of more than 64 MB (half of L2) leave it first: 8192 x 8192 with residual 79.0 us against 81.3, where 4096 x 4096, whose
     // inputs may still be there for the next call, would take 21.8 us against 21.2.
     p.ring.once = int64_t(a.T) * a.H * (a.second ? 4 : 2) > (int64_t(1) << 26);
-    const int smem = p.ring.stages * static_cast<int>(p.ring.stage_bytes);
+    const int smem = p.ring.stages * static_cast<int>(p.ring.stage_bytes) + 32;   // a row's last pieces at any alignment are read whole
     if (smem > 40 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_ROOM);   // the same in all threads
         if (e != cudaSuccess) return e;
@@ -878,7 +883,7 @@ cudaError_t launch_vec(const qgi::RowQuantArgs &a, const qgi::LaunchCtx &ctx) {
         static const int r2 = registers_of(k2), r4 = registers_of(k4), r_big = registers_of(big);
         constexpr int unit = unit_of<NORM, SECOND, 4, true>;
         if (a.H > 16384) return launch_ring(big, plan_ring(r_big, 4, unit, a.H, SECOND, ANY), 4 / unit, a, ctx);
-        const bool two = a.H <= (ANY ? 8192 : 16384);              // what its blocks may hold
+        const bool two = a.H <= (ANY && SECOND ? 8192 : 16384);              // what its blocks may hold
         const RingPlan p2 = plan_ring(r2, 2, 2, a.H, SECOND, ANY);
         if (two && p2.blocks >= 2) return launch_ring(k2, p2, 1, a, ctx);
         const RingPlan p4 = plan_ring(r4, 4, 4, a.H, SECOND, ANY);
