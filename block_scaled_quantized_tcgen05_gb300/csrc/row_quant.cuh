@@ -13,10 +13,10 @@
 // factor of the row, so max |h w| is taken beside the sum and both travel through one exchange, and the codes are those of
 // h w itself.
 //
-// Measured (GB300, whose copies reach 6.76 TB/s): norm with residual of 8192 x 8192 bf16 to E4M3 79.5 us, 5.93 TB/s; gated SiLU of
-// 4096 x 14336 fp16 to E4M3 50.0 us, 5.90 TB/s.  Writes beside reads and the rows' exchanges cost what is left.  Without
-// a residual the issue slots bound a norm to INT8: 5003 x 5112 22 us, 3.5 TB/s (about half of a row's instructions are its exchange's
-// and its factor's, whatever its length); rows at any alignment, 5003 x 5111: 26.9 us, their shifts.  16 x 14336: 3.1 to 3.4 us.
+// Measured (GB300, whose copies reach 6.76 TB/s): norm with residual of 8192 x 8192 bf16 to E4M3 78.3 us, 6.03 TB/s; gated SiLU of
+// 4096 x 14336 fp16 to E4M3 49.7 us, 5.95 TB/s.  Writes beside reads and the rows' exchanges cost what is left.  Without
+// a residual the issue slots bound a norm to INT8: 5003 x 5112 20.4 us, 3.8 TB/s (about half of a row's instructions are its exchange's
+// and its factor's, whatever its length); rows at any alignment, 5003 x 5111: 26.1 us, their shifts.  16 x 14336: 3.0 to 3.4 us.
 #pragma once
 
 #include <algorithm>
@@ -490,18 +490,20 @@ struct Ring {
 template <bool NORM, bool SECOND, int C, bool BIG>
 constexpr int unit_of = BIG && !NORM && SECOND ? 1 : C;
 
-// A row held by a warp (WARP, eight rows a block, loaded directly) or by a block, 8 elements a thread and chunk, chunk i of
+// A row held by L lanes of a warp (8, 16 or 32; loaded directly) or by a block (L = 0), 8 elements a thread and chunk, chunk i of
 // thread t at element 8 (i nt + t).  A block walks its rows with the next ones on their way: bulk copies fill a ring in
 // shared memory, so that loads go on through a row's sum, its exchange and its stores.  ANY: rows of any alignment and
 // length.  BIG: 1024 threads, which leaves no registers for weights.
-template <class TY, int OUT, bool NORM, bool SECOND, int C, bool WARP, bool ANY, bool BIG>
-__global__ void __launch_bounds__(WARP ? 256 : (C == 2 && !ANY) || BIG ? 1024 : 512, !WARP ? 1 : NORM ? 4 : 5)
+template <class TY, int OUT, bool NORM, bool SECOND, int C, int L, bool ANY, bool BIG>
+__global__ void __launch_bounds__(L > 0 ? 256 : (C == 2 && !ANY) || BIG ? 1024 : 512, L == 0 ? 1 : NORM ? 4 : 5)
 row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring ring, unsigned *err, uint64_t timeout_ns) {
+    constexpr bool WARP = L > 0, MANY = L == 8 || L == 16;         // MANY: rows of a warp side by side
+    static_assert(!(MANY && ANY), "stores at any alignment are a warp's");
     __shared__ float2 room[2][32];
     constexpr int UNIT = unit_of<NORM, SECOND, C, BIG>;
     extern __shared__ uint8_t rows_smem[];
     griddep_launch_dependents();
-    const int nt = WARP ? 32 : blockDim.x, t = WARP ? threadIdx.x & 31 : threadIdx.x;
+    const int nt = WARP ? L : blockDim.x, t = WARP ? threadIdx.x & (L - 1) : threadIdx.x;
     [[maybe_unused]] const float per_h = 1.0f / static_cast<float>(a.H);
     int turn = 0;
     // Sum of ss and maximum of amax (not negative: its bits' order is its own, a NaN's the largest) over the row's threads; one
@@ -511,9 +513,13 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
         auto over = [&](int width) {
             if constexpr (SUM)
                 for (int o = width / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-            if constexpr (MOST) amax = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(amax)));
+            if constexpr (MOST && MANY)
+                for (int o = width / 2; o > 0; o >>= 1)
+                    amax = __uint_as_float(max(__float_as_uint(amax), __shfl_xor_sync(0xFFFFFFFFu, __float_as_uint(amax), o)));
+            else if constexpr (MOST)
+                amax = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(amax)));
         };
-        over(32);
+        over(WARP ? L : 32);
         if constexpr (!WARP) {
             const int warps = nt >> 5;
             if ((t & 31) == 0) room[turn][t >> 5] = make_float2(ss, amax);
@@ -526,6 +532,8 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
             if constexpr (ANY && SUM) ss = __shfl_sync(0xFFFFFFFFu, ss, 0);
         }
     };
+    // Whether any row of the warp takes a path that its lanes go together (a block's rows go alone).
+    auto any_row = [](bool b) { return MANY ? __any_sync(0xFFFFFFFFu, b) != 0 : b; };
     auto put16 = [](uint16_t *p, const uint4 &v, int n) {          // ANY: by whole warps
         if constexpr (ANY) store_warp(p, v, n);
         else *reinterpret_cast<uint4 *>(p) = v;
@@ -554,6 +562,7 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
     // elements are the row's, which saves the tests (n is the number of elements from e on that are, or at least 8).
     auto process = [&](auto in, int64_t row, int e0, auto &&load, auto &&read_done) {
         constexpr bool IN = decltype(in)::value;
+        const int H = MANY && row >= a.T ? 0 : a.H;                // lanes without a row go along
         // h, or the activation's product; zeros past the row's end
         float v[C][8], amax = 0.0f;
         [[maybe_unused]] float shown = 0.0f;                       // the largest |y|; amax that of what is turned into codes
@@ -564,7 +573,7 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
             for (int i = 0; i < C; ++i) {
                 const int e = e0 + 8 * (i * nt + t);
                 xv[i] = sv[i] = make_uint4(0, 0, 0, 0);
-                load(i, e, IN ? 8 : a.H - e, xv[i], sv[i]);
+                load(i, e, IN ? 8 : H - e, xv[i], sv[i]);
             }
             if (!WARP && UNIT == C) fence_proxy_async_smem();      // read here, written next by the bulk copies
             float s2[2] = {0.0f, 0.0f};
@@ -578,10 +587,10 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
                     if (SECOND)
 #pragma unroll
                         for (int j = 0; j < 8; j += 2) add2(v[i][j], v[i][j + 1], s[j], s[j + 1]);
-                    if (!IN && ANY && e - 8 * (t & 31) >= a.H) continue;  // whole warps
-                    if (SECOND && a.sum_out && (IN || ANY || e < a.H))
-                        put16(static_cast<uint16_t *>(a.sum_out) + row * a.ldso + e, pack8<TY>(v[i]), IN ? 8 : a.H - e);
-                    if (!IN && e >= a.H) continue;
+                    if (!IN && ANY && e - 8 * (t & 31) >= H) continue;  // whole warps
+                    if (SECOND && a.sum_out && (IN || ANY || e < H))
+                        put16(static_cast<uint16_t *>(a.sum_out) + row * a.ldso + e, pack8<TY>(v[i]), IN ? 8 : H - e);
+                    if (!IN && e >= H) continue;
 #pragma unroll
                     for (int j = 0; j < 8; j += 2)
                         fma2(s2[0], s2[1], v[i][j], v[i][j + 1], v[i][j], v[i][j + 1], s2[0], s2[1]);
@@ -613,37 +622,39 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
             join(ss, amax);
             read_done();
             const bool wide = !(ss <= FLT_MAX);
-            if (wide) {                                            // rare: the sum again of h * 2^-80
-                ss = 0.0f;
+            if (any_row(wide)) {                                   // rare: the sum again of h * 2^-80
+                const float shrink = wide ? SHRINK : 1.0f;
+                float again = 0.0f, unused = 0.0f;
 #pragma unroll
                 for (int i = 0; i < C; ++i)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        v[i][j] *= SHRINK;
-                        ss = fmaf(v[i][j], v[i][j], ss);
+                        v[i][j] *= shrink;
+                        again = fmaf(v[i][j], v[i][j], again);
                     }
-                float unused = 0.0f;
-                join(ss, unused);
+                join(again, unused);
+                if (wide) ss = again;
             }
             r = rsqrtf(fmaf(ss, per_h, wide ? 0.0f : a.eps));
             if constexpr (OUT == OUT_INT8) {
                 shown = amax * r;
-                if (wide || !codes_without_r(amax, shown)) {
-                    amax = 0.0f;
+                const bool slow = wide || !codes_without_r(amax, shown);
+                if (any_row(slow)) {
+                    const float times = slow ? r : 1.0f;
+                    float most = 0.0f, unused = 0.0f;
 #pragma unroll
                     for (int i = 0; i < C; ++i) {
                         const int e = e0 + 8 * (i * nt + t);
-                        if (!IN && e >= a.H) continue;
+                        if (!IN && e >= H) continue;
                         float w[8];
                         weights(i, e, w);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) v[i][j] *= r;
+                        for (int j = 0; j < 8; ++j) v[i][j] *= times;
 #pragma unroll
-                        for (int j = 0; j < 8; j += 2) amax = max_nan(amax, v[i][j] * w[j], v[i][j + 1] * w[j + 1]);
+                        for (int j = 0; j < 8; j += 2) most = max_nan(most, v[i][j] * w[j], v[i][j + 1] * w[j + 1]);
                     }
-                    float unused = 0.0f;
-                    join(unused, amax);
-                    shown = amax = max_nan(amax, LEAST);
+                    join(unused, most);
+                    if (slow) shown = amax = max_nan(most, LEAST);
                 }
             }
         } else if constexpr (OUT == OUT_INT8) {
@@ -660,24 +671,24 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
             if (!IN && e0 + 8 * (i * nt + (t & ~31)) >= a.H) continue;         // whole warps
             if constexpr (NORM) {
                 float w[8];
-                weights(i, IN || e < a.H ? e : 0, w);
+                weights(i, IN || e < H ? e : 0, w);
 #pragma unroll
                 for (int j = 0; j < 8; j += 2) {
                     if (OUT != OUT_INT8) mul2(v[i][j], v[i][j + 1], v[i][j], v[i][j + 1], r, r);
                     mul2(v[i][j], v[i][j + 1], v[i][j], v[i][j + 1], w[j], w[j + 1]);
                 }
             }
-            store_row<OUT, ANY, TY, !NORM && !SECOND>(a, row, e, IN ? 8 : a.H - e, v[i], factor);
+            store_row<OUT, ANY, TY, !NORM && !SECOND>(a, row, e, IN ? 8 : H - e, v[i], factor);
         }
-        if (OUT == OUT_INT8 && t == 0) static_cast<float *>(a.scales)[row] = shown / 127.0f;
+        if (OUT == OUT_INT8 && t == 0 && (!MANY || H > 0)) static_cast<float *>(a.scales)[row] = shown / 127.0f;
     };
 
     if constexpr (WARP) {
         griddep_wait();
-        const int64_t at = blockIdx.x * int64_t(8) + (threadIdx.x >> 5);
-        const int64_t row = ring.parts == 1 ? at : at / ring.parts;
-        const int e0 = ring.parts == 1 ? 0 : static_cast<int>(at - row * ring.parts) * 256 * C;
-        if (row >= a.T) return;                                    // whole warps
+        const int64_t at = blockIdx.x * int64_t(256 / L) + threadIdx.x / L;
+        const int64_t row = MANY || ring.parts == 1 ? at : at / ring.parts;
+        const int e0 = MANY || ring.parts == 1 ? 0 : static_cast<int>(at - row * ring.parts) * 8 * L * C;
+        if (row - (MANY ? (threadIdx.x & 31) / L : 0) >= a.T) return;                    // whole warps
         keep_weights();
         const uint16_t *px = row_x(row), *p2 = SECOND ? row_2(row) : nullptr;
         const uint32_t offx = ANY ? before_16(px) : 0, off2 = ANY && SECOND ? before_16(p2) : 0;
@@ -686,7 +697,8 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
             xv = ANY ? load_any(px + e, offx, n) : load_once(px + e);
             if (SECOND) sv = ANY ? load_any(p2 + e, off2, n) : load_once(p2 + e);
         };
-        if (!ANY && a.H - e0 >= 256 * C) process(std::bool_constant<!ANY>{}, row, e0, load, [] {});
+        const bool all_in = !ANY && a.H - e0 >= 8 * L * C && (!MANY || row + (31 - (threadIdx.x & 31)) / L < a.T);
+        if (all_in) process(std::bool_constant<!ANY>{}, row, e0, load, [] {});
         else process(std::false_type{}, row, e0, load, [] {});
     } else {
         __shared__ uint64_t bars[UNIT == 1 ? 2 * MAX_STAGES : MAX_STAGES];
@@ -861,15 +873,21 @@ cudaError_t launch_ring(K kern, RingPlan p, int parts, const qgi::RowQuantArgs &
 
 template <class TY, int OUT, bool NORM, bool SECOND, bool ANY>
 cudaError_t launch_vec(const qgi::RowQuantArgs &a, const qgi::LaunchCtx &ctx) {
-    // Short rows a warp each; and rows in parts of 512 elements where nothing of the whole row is needed.
+    // Short rows a warp, or a part of one, each; and rows in parts of 512 elements where nothing of the whole row is needed.
     constexpr bool APART = !NORM && OUT != OUT_INT8;
     if (a.H <= 512 || APART) {
+        auto kern = row_quant_vec_kernel<TY, OUT, NORM, SECOND, 2, 32, ANY, false>;
+        int lanes = 32;
+        // 16 elements a lane: 327680 heads of 128, norm to 16 bits, 32 us against 94 with a warp each, 30000 x 256 8.0 against 10.7.
+        if constexpr (!ANY) {
+            if (a.H <= 128) kern = row_quant_vec_kernel<TY, OUT, NORM, SECOND, 2, 8, ANY, false>, lanes = 8;
+            else if (a.H <= 256) kern = row_quant_vec_kernel<TY, OUT, NORM, SECOND, 2, 16, ANY, false>, lanes = 16;
+        }
         Ring ring{};
         ring.parts = (a.H + 511) / 512;
-        const int64_t blocks = (int64_t(a.T) * ring.parts + 7) / 8;
+        const int64_t blocks = (int64_t(a.T) * ring.parts * lanes + 255) / 256;
         if (blocks < (int64_t(1) << 31))
-            return launch_dependent(row_quant_vec_kernel<TY, OUT, NORM, SECOND, 2, true, ANY, false>,
-                                    dim3(static_cast<unsigned>(blocks)), 256, 0, ctx.stream, a, ring, ctx.err, ctx.timeout_ns);
+            return launch_dependent(kern, dim3(static_cast<unsigned>(blocks)), 256, 0, ctx.stream, a, ring, ctx.err, ctx.timeout_ns);
     }
     if constexpr (APART) {
         return cudaErrorInvalidConfiguration;    // 2^43 elements
@@ -877,9 +895,9 @@ cudaError_t launch_vec(const qgi::RowQuantArgs &a, const qgi::LaunchCtx &ctx) {
         // 16 elements a thread while that leaves two blocks an SM, to alternate between loads and exchanges; else 32 (measured
         // at 4096 x 12288: norm to E4M3 56 us against 61) unless one block is all that fits either way; past 16384 elements 32 in up to
         // 1024 threads.
-        auto k2 = row_quant_vec_kernel<TY, OUT, NORM, SECOND, 2, false, ANY, false>;
-        auto k4 = row_quant_vec_kernel<TY, OUT, NORM, SECOND, 4, false, ANY, false>;
-        auto big = row_quant_vec_kernel<TY, OUT, NORM, SECOND, 4, false, ANY, true>;
+        auto k2 = row_quant_vec_kernel<TY, OUT, NORM, SECOND, 2, 0, ANY, false>;
+        auto k4 = row_quant_vec_kernel<TY, OUT, NORM, SECOND, 4, 0, ANY, false>;
+        auto big = row_quant_vec_kernel<TY, OUT, NORM, SECOND, 4, 0, ANY, true>;
         static const int r2 = registers_of(k2), r4 = registers_of(k4), r_big = registers_of(big);
         constexpr int unit = unit_of<NORM, SECOND, 4, true>;
         if (a.H > 16384) return launch_ring(big, plan_ring(r_big, 4, unit, a.H, SECOND, ANY), 4 / unit, a, ctx);
