@@ -23,9 +23,9 @@ namespace qgi {
 
 // Up to 16 tokens the weights' bytes bound the product and the weight stream is the fastest everywhere.  Up to 32 its
 // products on mma.sync begin to: it is still ahead of the pairs' three launches on small matrices (32 tokens, 4096 x 4096: 11.0 us
-// against 14.1; 8192 x 8192: 25.4 against 23.7).
+// against 13.6, 1024 x 8192: 9.5 against 10.9; 8192 x 4096: 19.5 against 16.0).
 static bool few_tokens(const W8A8Args &a) {
-    return a.M <= 16 || (a.M <= 32 && int64_t(a.N) * a.K <= int64_t(1) << 25);
+    return a.M <= 16 || (a.M <= 32 && int64_t(a.N) * a.K <= int64_t(1) << 24);
 }
 
 cudaError_t launch_w8a8(const W8A8Args &a, const LaunchCtx &ctx, bool *encode_ok) {

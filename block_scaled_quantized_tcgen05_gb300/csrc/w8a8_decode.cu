@@ -14,6 +14,7 @@
 // matrices by start and end: 8 x 4096 x 4096 7.2 us where the bytes take 2.5 (a cluster's start and its two meetings, 16 stages a
 // CTA's first copies' latency).  mma.sync is 17 % busy at 8 tokens.
 #include <algorithm>
+#include <cmath>
 
 #include "qgemm_common.cuh"
 #include "w8a8_common.cuh"
@@ -34,9 +35,13 @@ struct Cfg {
     static constexpr uint32_t W_BYTES = ROWS * KC;
     static constexpr uint32_t X_BYTES = 8 * NH * KC;
     static constexpr uint32_t STAGE = W_BYTES + X_BYTES;
-    static constexpr uint32_t OFF_RED = STAGES * STAGE;                 // sums of the warps: [warp][NF][NH][4][lane]
-    static constexpr uint32_t OFF_BAR = OFF_RED + CONSUMERS * NF * NH * 4 * 32 * 4;
-    static constexpr uint32_t SMEM = OFF_BAR + 2 * STAGES * 8 + 1024;
+    static constexpr uint32_t RED = CONSUMERS * NF * NH * 4 * 32 * 4;   // sums of the warps: [warp][NF][NH][4][lane]
+    static constexpr uint32_t OFF_BAR = STAGES * STAGE;
+    static constexpr uint32_t OFF_RED = OFF_BAR + 2 * STAGES * 8;
+    // Where K is cut a CTA has one block of rows, and its sums take the stages' place: a fourth CTA an SM at 16 tokens (8192 x
+    // 28672 45.6 -> 40.9 us).
+    static constexpr uint32_t smem(int splits) { return 1024 + (splits > 1 ? OFF_RED : OFF_RED + RED); }
+    static_assert(RED <= OFF_BAR, "sums in the stages' place");
     static_assert(STAGE % 1024 == 0, "stages stay 1 KB aligned for the 128-byte swizzle");
 };
 
@@ -92,7 +97,8 @@ w8a8_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     auto full_bar = [&](int s) { return sb + G::OFF_BAR + 8u * s; };
     auto empty_bar = [&](int s) { return sb + G::OFF_BAR + 8u * (STAGES + s); };
-    float *red = reinterpret_cast<float *>(smem + G::OFF_RED);
+    const uint32_t off_red = splits > 1 ? 0 : G::OFF_RED;
+    float *red = reinterpret_cast<float *>(smem + off_red);
 
     const int nrb = (a.N + ROWS - 1) / ROWS;     // blocks of rows
     const int nkc = (a.K + KC - 1) / KC;         // stages of all of K
@@ -195,6 +201,7 @@ w8a8_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
             stage = two ? (stage2 + 1 == STAGES ? 0 : stage2 + 1) : stage2;
             phase = two ? (stage2 + 1 == STAGES ? phase2 ^ 1 : phase2) : phase2;
         }
+        if (splits > 1) asm volatile("bar.sync 1, %0;" ::"n"(CONSUMERS * 32) : "memory");   // every warp has read its stages
 #pragma unroll
         for (int f = 0; f < NF; ++f)
 #pragma unroll
@@ -225,7 +232,7 @@ w8a8_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
             cluster_sync();
             for (int i = rank * CONSUMERS * 32 + static_cast<int>(threadIdx.x); i < ROWS * a.M; i += splits * CONSUMERS * 32) {
                 const int m = i / ROWS, r = i - m * ROWS, n = rb * ROWS + r;
-                const uint32_t addr = sb + G::OFF_RED + 4u * place(m, r);
+                const uint32_t addr = sb + off_red + 4u * place(m, r);
                 float part[8];
 #pragma unroll
                 for (int c = 0; c < 8; ++c) part[c] = c < splits ? ld_cluster(map_to_cta(addr, c)) : 0.0f;
@@ -241,6 +248,8 @@ w8a8_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     }
 }
 
+constexpr uint32_t SM_SMEM = 233472;            // shared memory of an SM, 1 KB of it each CTA's own
+
 // How the work is laid out: NF fragments of 16 rows a block, K over `splits` CTAs, and its estimated us.
 struct Layout {
     int splits;
@@ -248,24 +257,29 @@ struct Layout {
     double us;
 };
 
-// The best split for one block height.  Measured on 8192 x 8192 (1 token; 2 to 4 CTAs an SM, 80 to 160 KB of weights on
-// their way): an SM takes 13 + 0.216 KB^-1 x (its KB on their way) bytes a ns, so both an even share and many copies count;
-// all together at most 6.6 TB/s.  One block of rows a cluster, all of them at once (clusters of other than 2, 4 or 8 leave
-// room unused: 602 CTAs in clusters of 7 ran in two rounds where 608 fit), or with K whole as many as there are.
+// The best split for one block height.  Measured on 27 products (1, 8 and 16 tokens, nine matrices from 2048 x 8192 to 16384 x 19456, every
+// height and split; the rule's choice is 0.2 % behind the fastest on average, 2.2 % at most): an SM takes 5 + 0.63 KB^-1 x (its KB
+// of weights on their way) bytes a ns of its own share, tokens' rows count 1.3 times; all together at most 6.5 TB/s; both bound at once
+// cost more than either (a fourth-power mean); a cluster costs its start and meetings.  One block of rows a cluster, all of
+// them at once (clusters of other than 2, 4 or 8 leave room unused: 602 CTAs in clusters of 7 ran in two rounds where 608
+// fit), or with K whole as many as there are.  Lower blocks count 1.2 % for each fragment less: their clusters find places less evenly.
 template <class G>
 Layout layout(const qgi::W8A8Args &a, int num_sms) {
     const int64_t nrb = (int64_t(a.N) + G::ROWS - 1) / G::ROWS;
-    const int nkc = (a.K + KC - 1) / KC, per_sm = std::max(1, int(233472 / (G::SMEM + 1024)));
-    const int64_t room = int64_t(num_sms) * per_sm;
-    Layout best{1, std::min(nrb, room), 1e300};
+    const int nkc = (a.K + KC - 1) / KC;
+    Layout best{1, 1, 1e300};
     for (int s = 1; s <= 8; ++s) {
         if (nkc < 2 * s && s > 1) break;
+        const int per_sm = std::max(1, int(SM_SMEM / (G::smem(s) + 1024)));
+        const int64_t room = int64_t(num_sms) * per_sm;
         if (s > 1 && nrb * s > (s & (s - 1) ? room * 17 / 20 : room)) continue;
         const int64_t ctas = std::min(nrb * s, room), rounds = (nrb * s + ctas - 1) / ctas;
         const int64_t each = (ctas + num_sms - 1) / num_sms * rounds;                  // on the fullest SM
-        const double rate = 13.0 + 0.216 * double(std::min<int64_t>(each, per_sm) * G::STAGES * G::W_BYTES) / 1024;
-        const double own = double(each) * G::ROWS * ((nkc + s - 1) / s) * KC / 1e3 / rate;
-        const double us = std::max(own, double(a.N) * a.K / 6.6e6) + (s > 1 ? 0.8 + 0.1 * s * (1.0 + a.M / 8.0) : 0.0);
+        const double rate = 5.0 + 0.63 * double(std::min<int64_t>(each, per_sm) * G::STAGES * G::W_BYTES) / 1024;
+        const double own = double(each) * (G::W_BYTES + 1.3 * G::X_BYTES) * ((nkc + s - 1) / s) / 1e3 / rate;
+        const double all = double(a.N) * a.K / 6.5e6, own2 = own * own, all2 = all * all;
+        const double us = (std::sqrt(std::sqrt(own2 * own2 + all2 * all2)) + (s > 1 ? 0.9 + 0.15 * s * (1.0 + a.M / 8.0) : 0.0)) *
+                          (1.0 + 0.012 * (4 - G::ROWS / 16));
         if (us < best.us) best = {s, ctas, us};
     }
     return best;
@@ -280,14 +294,19 @@ cudaError_t launch_nh(const qgi::W8A8Args &a, const Layout &l, const qgi::Launch
         qgi::encode_tma_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, a.K, a.M, a.lda, KC, 8 * NH, CU_TENSOR_MAP_SWIZZLE_128B);
     if (!*encode_ok) return cudaErrorInvalidValue;
     auto kern = w8a8_decode_kernel<NH, NF, STAGES>;
-    if (G::SMEM > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
-        if (e != cudaSuccess) return e;
-    }
+    constexpr uint32_t MOST = 232448;            // of a CTA
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST);
+    if (e != cudaSuccess) return e;
+    // CTAs spread evenly: each takes the shared memory that leaves no room for more on its SM than there are on the fullest, or
+    // one more where clusters have to find their places (8 x 4096 x 4096, 512 CTAs: 7.1 us against 7.7 where five fit).
+    int64_t each = (l.grid + ctx.num_sms - 1) / ctx.num_sms;
+    if (l.splits > 1 && l.grid > each * ctx.num_sms * 17 / 20) ++each;
+    const uint32_t even = static_cast<uint32_t>(SM_SMEM / each) / 1024 * 1024 - 1024;
+    const uint32_t smem = std::max(G::smem(l.splits), std::min(MOST, even));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(l.grid));
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = G::SMEM;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = ctx.stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
