@@ -22,10 +22,10 @@ __global__ void __launch_bounds__(256) w8a8_empty_kernel(const __grid_constant__
 namespace qgi {
 
 // Up to 16 tokens the weights' bytes bound the product and the weight stream is the fastest everywhere.  Up to 32 its
-// products on mma.sync begin to: it is still ahead of the pairs' three launches on small matrices (32 tokens, 4096 x 4096: 11.0 us
-// against 13.6, 1024 x 8192: 9.5 against 10.9; 8192 x 4096: 19.5 against 16.0).
+// products on mma.sync begin to: it is still ahead of the pairs' three launches on small matrices (32 tokens, 4096 x 4096: 11.1 us
+// against 13.5, 5120 x 5120 14.2 against 15.0, 8192 x 4096 15.9 against 16.0; 8192 x 8192 24.4 against 20.9).
 static bool few_tokens(const W8A8Args &a) {
-    return a.M <= 16 || (a.M <= 32 && int64_t(a.N) * a.K <= int64_t(1) << 24);
+    return a.M <= 16 || (a.M <= 32 && int64_t(a.N) * a.K <= int64_t(1) << 25);
 }
 
 cudaError_t launch_w8a8(const W8A8Args &a, const LaunchCtx &ctx, bool *encode_ok) {

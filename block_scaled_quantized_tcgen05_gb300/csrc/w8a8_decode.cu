@@ -10,9 +10,10 @@
 // sums meet through distributed shared memory (no scratch, no second launch).  Partial sums are added in the order of
 // ranks and warps, so results repeat bit for bit.
 //
-// Bound by the weights' bytes: 1 x 28672 x 8192 36 us (6.5 TB/s), 1 x 8192 x 28672 37.7, 8 x 19456 x 16384 50.3 (6.3 TB/s); small
-// matrices by start and end: 8 x 4096 x 4096 7.2 us where the bytes take 2.5 (a cluster's start and its two meetings, 16 stages a
-// CTA's first copies' latency).  mma.sync is 17 % busy at 8 tokens.
+// Bound by the weights' bytes: 1 x 28672 x 8192 36 us (6.5 TB/s), 1 x 8192 x 28672 37.9, 8 x 16384 x 19456 50.8 (6.3 TB/s); at 16 tokens
+// the tokens' rows, read again for every block of rows, add 5 to 12 % (39 and 42.6 us); small matrices by start and end: 4096 x
+// 4096 6.6 us for 1 token, 7.1 for 8, where the bytes take 2.5 (a cluster's start and its two meetings, the first copies' latency).
+// mma.sync is 17 % busy at 8 tokens.
 #include <algorithm>
 #include <cmath>
 

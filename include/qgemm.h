@@ -617,7 +617,7 @@ qgemm_status qgemm_act_quant(const void *X, int64_t ldx, const void *up, int64_t
  *   W         device int8 [N, K], row stride ldw bytes;  w_scales fp32 [N].
  *   bias      device [N] of c_dtype, or NULL.
  *   C         device [M, N] of c_dtype (QGEMM_F16 or QGEMM_BF16), row stride ldc elements; overlaps no input.
- * Scratch: up to 16 tokens none (32 on matrices of at most 2^24 elements): one launch, K over a cluster's CTAs where there
+ * Scratch: up to 16 tokens none (32 on matrices of at most 2^25 elements): one launch, K over a cluster's CTAs where there
  * are few rows.  Otherwise, from the library's pool on `stream`, the tokens' codes as halves (2 M ceil(K / 64) 64 bytes, taken in
  * slices of as many rows as 512 MB hold, 256 at least) and, where pairs of CTAs share tiles along K, fp32 partial sums (at most 40 MB
  * on 152 SMs).
