@@ -44,7 +44,7 @@ struct W8A8Args {
     int M, N, K;
 };
 cudaError_t launch_w8a8(const W8A8Args &a, const LaunchCtx &ctx, bool *encode_ok);
-// At most 32 tokens: a weight stream (w8a8_decode.cu).
+// At most 64 tokens: a weight stream (w8a8_decode.cu).
 cudaError_t launch_w8a8_decode(const W8A8Args &a, const LaunchCtx &ctx, bool *encode_ok);
 // On CTA pairs: any shape (w8a8_pair.cu).
 cudaError_t launch_w8a8_pair(const W8A8Args &a, const LaunchCtx &ctx, bool *encode_ok);

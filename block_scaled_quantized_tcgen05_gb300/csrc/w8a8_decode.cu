@@ -15,6 +15,7 @@
 // 4096 6.6 us for 1 token, 7.1 for 8, where the bytes take 2.5 (a cluster's start and its two meetings, the first copies' latency).
 // mma.sync is 17 % busy at 8 tokens.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "qgemm_common.cuh"
@@ -298,16 +299,9 @@ cudaError_t launch_nh(const qgi::W8A8Args &a, const Layout &l, const qgi::Launch
     constexpr uint32_t MOST = 232448;            // of a CTA
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST);
     if (e != cudaSuccess) return e;
-    // CTAs spread evenly: each takes the shared memory that leaves no room for more on its SM than there are on the fullest, or
-    // one more where clusters have to find their places (8 x 4096 x 4096, 512 CTAs: 7.1 us against 7.7 where five fit).
-    int64_t each = (l.grid + ctx.num_sms - 1) / ctx.num_sms;
-    if (l.splits > 1 && l.grid > each * ctx.num_sms * 17 / 20) ++each;
-    const uint32_t even = static_cast<uint32_t>(SM_SMEM / each) / 1024 * 1024 - 1024;
-    const uint32_t smem = std::max(G::smem(l.splits), std::min(MOST, even));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(l.grid));
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = smem;
     cfg.stream = ctx.stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -317,6 +311,21 @@ cudaError_t launch_nh(const qgi::W8A8Args &a, const Layout &l, const qgi::Launch
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
+    // CTAs spread evenly: each takes the shared memory that leaves no room for more on its SM than there are on the fullest (8 x
+    // 4096 x 4096, 512 CTAs: 7.1 us against 7.7 where five fit), or than the clusters need to be there all at once (16 of 8 are not
+    // at one CTA an SM: 40 x 512 x 8192 ran in two rounds), which is asked once.
+    static std::atomic<int> at_once[9][17];
+    int64_t each = (l.grid + ctx.num_sms - 1) / ctx.num_sms;
+    for (;; ++each) {
+        cfg.dynamicSmemBytes = std::max(G::smem(l.splits), std::min(MOST, uint32_t(SM_SMEM / each) / 1024 * 1024 - 1024));
+        if (l.splits == 1 || each > 16 || cfg.dynamicSmemBytes == G::smem(l.splits)) break;
+        int clusters = at_once[l.splits][each].load(std::memory_order_relaxed);
+        if (clusters == 0) {
+            if (cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) != cudaSuccess) clusters = 0;
+            at_once[l.splits][each].store(std::max(clusters, 1), std::memory_order_relaxed);
+        }
+        if (int64_t(clusters) * l.splits >= l.grid) break;
+    }
     return cudaLaunchKernelEx(&cfg, kern, tmW, tmX, a, l.splits, ctx.epi, ctx.err, ctx.timeout_ns);
 }
 
@@ -336,7 +345,9 @@ namespace qgi {
 cudaError_t launch_w8a8_decode(const W8A8Args &a, const LaunchCtx &ctx, bool *encode_ok) {
     if (a.M <= 8) return launch_tokens<1>(a, ctx, encode_ok);
     if (a.M <= 16) return launch_tokens<2>(a, ctx, encode_ok);
-    return launch_nh<4, 2, 6>(a, layout<Cfg<4, 2, 6>>(a, ctx.num_sms), ctx, encode_ok);
+    if (a.M <= 32) return launch_nh<4, 2, 6>(a, layout<Cfg<4, 2, 6>>(a, ctx.num_sms), ctx, encode_ok);
+    // past 32 tokens two fragments a block and four stages: sums take as many registers as 64 tokens need
+    return launch_nh<8, 2, 4>(a, layout<Cfg<8, 2, 4>>(a, ctx.num_sms), ctx, encode_ok);
 }
 
 }  // namespace qgi

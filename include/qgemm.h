@@ -617,10 +617,10 @@ qgemm_status qgemm_act_quant(const void *X, int64_t ldx, const void *up, int64_t
  *   W         device int8 [N, K], row stride ldw bytes;  w_scales fp32 [N].
  *   bias      device [N] of c_dtype, or NULL.
  *   C         device [M, N] of c_dtype (QGEMM_F16 or QGEMM_BF16), row stride ldc elements; overlaps no input.
- * Scratch: up to 16 tokens none (32 on matrices of at most 2^25 elements): one launch, K over a cluster's CTAs where there
- * are few rows.  Otherwise, from the library's pool on `stream`, the tokens' codes as halves (2 M ceil(K / 64) 64 bytes, taken in
- * slices of as many rows as 512 MB hold, 256 at least) and, where pairs of CTAs share tiles along K, fp32 partial sums (at most 40 MB
- * on 152 SMs).
+ * Scratch: none up to 16 tokens, up to 32 on matrices of at most 2^25 elements and up to 64 on such of at most 2^22 with at most 2048
+ * channels: one launch, K over a cluster's CTAs where there are few rows.  Otherwise, from the library's pool on `stream`, the
+ * tokens' codes as halves (2 M ceil(K / 64) 64 bytes, taken in slices of as many rows as 512 MB hold, 256 at least) and, where
+ * pairs of CTAs share tiles along K, fp32 partial sums (at most 40 MB on 152 SMs).
  * Requirements: A and W 16-byte aligned with row strides in multiples of 16 (rows of any K are padded; the
  * padding is not read as data and may hold anything); scales 4-byte, bias and C 2-byte aligned; M, N, K at most
  * 2^31 - 4096.  M or N == 0 writes nothing; K == 0 gives the bias.
