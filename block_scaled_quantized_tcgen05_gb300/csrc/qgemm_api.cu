@@ -86,14 +86,16 @@ cudaError_t scratch_alloc(size_t bytes, const LaunchCtx &ctx, void **p) {
             props.allocType = cudaMemAllocationTypePinned;
             props.location.type = cudaMemLocationTypeDevice;
             props.location.id = ctx.device;
-            cudaError_t e = cudaMemPoolCreate(&d.pool, &props);
-            if (e != cudaSuccess) {
-                d.pool = nullptr;
-                return e;
-            }
-            uint64_t keep = UINT64_MAX;   // never hand memory back at synchronisation points
-            e = cudaMemPoolSetAttribute(d.pool, cudaMemPoolAttrReleaseThreshold, &keep);
+            // The pool is made outside whatever this thread's stream captures: nothing of it is the graph's.
+            cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+            cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
             if (e != cudaSuccess) return e;
+            e = cudaMemPoolCreate(&d.pool, &props);
+            if (e != cudaSuccess) d.pool = nullptr;
+            uint64_t keep = UINT64_MAX;   // never hand memory back at synchronisation points
+            if (e == cudaSuccess) e = cudaMemPoolSetAttribute(d.pool, cudaMemPoolAttrReleaseThreshold, &keep);
+            const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
+            if (e != cudaSuccess || back != cudaSuccess) return e != cudaSuccess ? e : back;
         }
         pool = d.pool;
     }
