@@ -108,8 +108,8 @@ __device__ __forceinline__ bool codes_without_r(float most, float most_y) {
     return most <= FLT_MAX && most >= LEAST && most_y >= LEAST;
 }
 
-// Four INT8 codes of y times the factor (PAIR: both parts of it), at most 127 in magnitude: 1.5 * 2^23 added leaves the nearest integer (ties to even)
-// in the low bits.
+// Four INT8 codes of y times the factor (PAIR: both parts of it), at most 127 in magnitude: 1.5 * 2^23 added leaves the
+// nearest integer (ties to even) in the low bits.
 template <bool PAIR>
 __device__ __forceinline__ uint32_t codes_i8(const float *y, const Factor &f) {
     constexpr float HALF_WAY = 12582912.0f;
@@ -864,7 +864,8 @@ cudaError_t launch_ring(K kern, RingPlan p, int parts, const qgi::RowQuantArgs &
     p.ring.once = int64_t(a.T) * a.H * (a.second ? 4 : 2) > (int64_t(1) << 26);
     const int smem = p.ring.stages * static_cast<int>(p.ring.stage_bytes) + 32;   // a row's last pieces at any alignment are read whole
     if (smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_ROOM);   // the same in all threads
+        // (one size, so that calls of two threads do not lower each other's)
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_ROOM);
         if (e != cudaSuccess) return e;
     }
     return launch_dependent(kern, dim3(static_cast<unsigned>(grid)), p.threads, smem, ctx.stream, a, p.ring, ctx.err,

@@ -706,7 +706,8 @@ cudaError_t launch_w8a8_pair(const W8A8Args &a, const LaunchCtx &ctx, bool *enco
         part.sa += m0;
         part.C = static_cast<uint16_t *>(a.C) + m0 * a.ldc;
         part.M = static_cast<int>(std::min<int64_t>(slice, a.M - m0));
-        e = launch_slice(part, reinterpret_cast<uint16_t *>(base), ldh, reinterpret_cast<float *>(base + x_bytes), bt, part.M == slice ? shares : last, tmW, ctx, encode_ok);
+        e = launch_slice(part, reinterpret_cast<uint16_t *>(base), ldh, reinterpret_cast<float *>(base + x_bytes), bt,
+                         part.M == slice ? shares : last, tmW, ctx, encode_ok);
     }
     const cudaError_t f = scratch_free(ws, ctx);
     return e != cudaSuccess ? e : f;
