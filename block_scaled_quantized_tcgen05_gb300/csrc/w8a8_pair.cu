@@ -22,8 +22,7 @@
 //     kernel's end instead: 4096 x 14336 x 4096 in 310 us against 294, 256 x 4096 x 4096 29 against 21: too few loads in flight.)
 //
 // Measured: 8192^3 554 - 566 us (1.94 - 1.98 PFLOP/s, what the library's bf16 product reaches), 4096 x 14336 x 4096 246 us, 4096^3 83;
-// 64 x 28672 x 8192 46 us (5.1 TB/s of weights; a converter warp's chain of wait, read, convert, write and arrival takes
-// as long as the bytes), 333 x 5003 x 4111 19 us: the tokens' halves 4, the k-tiles 11, epilogue, partial sums and launches the rest.
+// 64 x 28672 x 8192 44 us (5.4 TB/s of weights; 6.3 in the middle, the rest start and end), 333 x 5003 x 4111 19 us: the tokens' halves 4, the k-tiles 11, epilogue, partial sums and launches the rest.
 #include <algorithm>
 #include <type_traits>
 
@@ -244,6 +243,9 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
         // ---------------------------------------------------------------- weights' producer
         // It need not wait for the kernel ahead, which makes the tokens' halves, touches no weights and has let this one start
         // only after all work ahead of it was done: the first weights are on their way meanwhile.
+        // Weights that at most four tiles read, at nearly the same time, leave L2 first (64 x 28672 x 8192 46.9 -> 44.0 us, 64 x 16384
+        // x 19456 65.9 -> 55.8, 1024 x 8192 x 28672 263 -> 252); of more, some come later (4096 x 28672 x 8192 962 -> 990).
+        const uint64_t policy = tiles_t <= 4 ? l2_policy_evict_first() : l2_policy_evict_normal();
         uint32_t slot_raw = 0, phase = 0;
         int issued = 0;
         bool ok = true;
@@ -259,7 +261,7 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                 }
                 if (elect_one()) {
                     mbar_arrive_expect_tx(raw_full(slot_raw), G::RAW_BYTES);
-                    tma_load_2d(sb + G::OFF_RAW + slot_raw * G::RAW_BYTES, &tmW, raw_full(slot_raw), kt * BK, w0);
+                    tma_load_2d_hint(sb + G::OFF_RAW + slot_raw * G::RAW_BYTES, &tmW, raw_full(slot_raw), kt * BK, w0, policy);
                 }
                 __syncwarp();
                 ++issued;
@@ -603,11 +605,11 @@ Shares share(int bt, Cut cut, int M, int N, int K, int num_sms) {
 // Estimated us of a plan: the waves' walks over K, what stays open at a tile's end, the reduction's launch and traffic.
 // Measured: a k-tile takes a pair 0.29, 0.34 and 0.30 us (64, 128 and 128 k for 256, 128 and 64 tokens; matrices that stay in L2);
 // a wave of 256-token tiles, with one accumulator, ends 2.8 us after its walk, of smaller ones 0.2 (1.5 the last); all pairs together
-// get 5.8 TB/s of weights from memory, which each weight leaves once however many token tiles meet it; partial sums are written and
+// get 6.3 TB/s of weights from memory, which each weight leaves once however many token tiles meet it; partial sums are written and
 // read at 5 TB/s.
 double cost(int bt, const Shares &s, int M, int K) {
     const double per_kt = bt == 256 ? 0.29 : bt == 128 ? 0.34 : 0.30, ends = bt == 256 ? 2.8 : 0.2;
-    const double tile_us = double(2 * BW) * K / ((M + bt - 1) / bt) / 5.8e6;           // a tile's weights from memory
+    const double tile_us = double(2 * BW) * K / ((M + bt - 1) / bt) / 6.3e6;           // a tile's weights from memory
     const int waves = s.pairs ? s.full / s.pairs : 0;
     double us = waves * (std::max(s.KT * per_kt, s.pairs * tile_us) + ends);
     if (s.rest) us += std::max(double(s.rest) * s.KT / s.sharers * per_kt, s.rest * tile_us) + ends;
