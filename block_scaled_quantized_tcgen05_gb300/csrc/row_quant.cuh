@@ -34,6 +34,7 @@ constexpr float LEAST = 0x1p-100f;      // the least magnitude an INT8 row's sca
 constexpr float SHRINK = 0x1p-80f;      // factor on h where the sum of squares passed fp32's range
 
 constexpr int MAX_STAGES = 8;           // of a block's ring
+constexpr int LONGEST = 1 << 15;        // elements of a row that a block's registers hold
 
 enum Out { OUT_INT8, OUT_E4M3, OUT_16 };
 
@@ -486,12 +487,15 @@ struct Ring {
 template <bool NORM, bool SECOND, int C, bool BIG>
 constexpr int unit_of = BIG && !NORM && SECOND ? 1 : C;
 
+// Threads that a block of the ring kernel may have: its launch bound, and what the host chooses by.
+constexpr int most_threads(int c, bool any, bool big) { return (c == 2 && !any) || big ? 1024 : 512; }
+
 // A row held by L lanes of a warp (8, 16 or 32; loaded directly) or by a block (L = 0), 8 elements a thread and chunk, chunk i of
 // thread t at element 8 (i nt + t).  A block walks its rows with the next ones on their way: bulk copies fill a ring in
 // shared memory, so that loads go on through a row's sum, its exchange and its stores.  ANY: rows of any alignment and
 // length.  BIG: 1024 threads, which leaves no registers for weights.
 template <class TY, int OUT, bool NORM, bool SECOND, int C, int L, bool ANY, bool BIG>
-__global__ void __launch_bounds__(L > 0 ? 256 : (C == 2 && !ANY) || BIG ? 1024 : 512, L == 0 ? 1 : NORM ? 4 : 5)
+__global__ void __launch_bounds__(L > 0 ? 256 : most_threads(C, ANY, BIG), L == 0 ? 1 : NORM ? 4 : 5)
 row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring ring, unsigned *err, uint64_t timeout_ns) {
     constexpr bool WARP = L > 0, MANY = L == 8 || L == 16;         // MANY: rows of a warp side by side
     static_assert(!(MANY && ANY), "stores at any alignment are a warp's");
@@ -894,16 +898,17 @@ cudaError_t launch_vec(const qgi::RowQuantArgs &a, const qgi::LaunchCtx &ctx) {
         return cudaErrorInvalidConfiguration;    // 2^43 elements
     } else {
         // 16 elements a thread while that leaves two blocks an SM, to alternate between loads and exchanges; else 32 (measured
-        // at 4096 x 12288: norm to E4M3 56 us against 61) unless one block is all that fits either way; past 16384 elements 32 in up to
-        // 1024 threads.
+        // at 4096 x 12288: norm to E4M3 56 us against 61) unless one block is all that fits either way and the first may have the threads;
+        // past 16384 elements 32 in up to 1024 threads.
         auto k2 = row_quant_vec_kernel<TY, OUT, NORM, SECOND, 2, 0, ANY, false>;
         auto k4 = row_quant_vec_kernel<TY, OUT, NORM, SECOND, 4, 0, ANY, false>;
         auto big = row_quant_vec_kernel<TY, OUT, NORM, SECOND, 4, 0, ANY, true>;
+        static_assert(32 * most_threads(4, ANY, false) >= 16384 && 32 * most_threads(4, ANY, true) >= LONGEST, "every row has a kernel");
         static const int r2 = registers_of(k2), r4 = registers_of(k4), r_big = registers_of(big);
         constexpr int unit = unit_of<NORM, SECOND, 4, true>;
         if (a.H > 16384) return launch_ring(big, plan_ring(r_big, 4, unit, a.H, SECOND, ANY), 4 / unit, a, ctx);
-        const bool two = a.H <= (ANY && SECOND ? 8192 : 16384);              // what its blocks may hold
         const RingPlan p2 = plan_ring(r2, 2, 2, a.H, SECOND, ANY);
+        const bool two = p2.threads <= most_threads(2, ANY, false);
         if (two && p2.blocks >= 2) return launch_ring(k2, p2, 1, a, ctx);
         const RingPlan p4 = plan_ring(r4, 4, 4, a.H, SECOND, ANY);
         return p4.blocks >= 2 || !two ? launch_ring(k4, p4, 1, a, ctx) : launch_ring(k2, p2, 1, a, ctx);
@@ -913,7 +918,7 @@ cudaError_t launch_vec(const qgi::RowQuantArgs &a, const qgi::LaunchCtx &ctx) {
 template <class TY, int OUT>
 cudaError_t launch_out(const qgi::RowQuantArgs &a, const qgi::LaunchCtx &ctx) {
     // Past what a block's registers hold; and past what 32 bits with a sign count, where nothing of the whole row is needed.
-    if (a.H > (a.norm || OUT == OUT_INT8 ? 1 << 15 : 1 << 30)) {
+    if (a.H > (a.norm || OUT == OUT_INT8 ? LONGEST : 1 << 30)) {
         const dim3 grid(static_cast<unsigned>(a.T < ctx.num_sms ? a.T : ctx.num_sms));
         return launch_dependent(row_quant_long_kernel<TY, OUT>, grid, 1024, 0, ctx.stream, a);
     }
