@@ -227,7 +227,7 @@ __device__ __forceinline__ uint4 load_any(const uint16_t *p, uint32_t off, int n
     if (off == 0 && n >= 8) return load_once(piece);
     const uint4 lo = load_once(piece);
     uint4 hi = make_uint4(0, 0, 0, 0);
-    if (off + 2 * n > 16) hi = load_once(piece + 1);
+    if (n > 8 - static_cast<int>(off) / 2) hi = load_once(piece + 1);        // (a row's bytes may pass 32 bits)
     return shifted(lo, hi, off, n);
 }
 
