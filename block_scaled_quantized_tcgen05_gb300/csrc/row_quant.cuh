@@ -31,7 +31,7 @@ namespace {
 using namespace qg;
 
 constexpr float LEAST = 0x1p-100f;      // the least magnitude an INT8 row's scale is taken from
-constexpr float SHRINK = 0x1p-80f;      // factor on h where the sum of squares passed fp32's range
+constexpr float SHRINK = 0x1p-80f;      // factor on h where the sum of squares, or its mean and eps, passed fp32's range
 
 constexpr int MAX_STAGES = 8;           // of a block's ring
 constexpr int LONGEST = 1 << 15;        // elements of a row that a block's registers hold
@@ -423,12 +423,13 @@ __global__ void __launch_bounds__(1024) row_quant_long_kernel(const __grid_const
         if (a.norm || OUT == OUT_INT8) {
             measure(false);
             if (a.norm) {
-                const bool wide = !(ss <= FLT_MAX);
+                const float count = static_cast<float>(a.H);
+                const bool wide = !(ss / count + a.eps <= FLT_MAX);
                 if (wide) {
                     f = SHRINK;
                     measure(false);
                 }
-                r = rsqrtf(ss / static_cast<float>(a.H) + (wide ? 0.0f : a.eps));
+                r = rsqrtf(ss / count + (wide ? a.eps * SHRINK * SHRINK : a.eps));
             }
         }
         float shown = amax * r;                                    // the largest |y|; amax that of what is turned into codes
@@ -621,7 +622,7 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
         if constexpr (NORM) {
             join(ss, amax);
             read_done();
-            const bool wide = !(ss <= FLT_MAX);
+            const bool wide = !(fmaf(ss, per_h, a.eps) <= FLT_MAX);
             if (any_row(wide)) {                                   // rare: the sum again of h * 2^-80
                 const float shrink = wide ? SHRINK : 1.0f;
                 float again = 0.0f, unused = 0.0f;
@@ -635,7 +636,7 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
                 join(again, unused);
                 if (wide) ss = again;
             }
-            r = rsqrtf(fmaf(ss, per_h, wide ? 0.0f : a.eps));
+            r = rsqrtf(fmaf(ss, per_h, wide ? a.eps * SHRINK * SHRINK : a.eps));
             if constexpr (OUT == OUT_INT8) {
                 shown = amax * r;
                 const bool slow = wide || !codes_without_r(amax, shown);
