@@ -106,9 +106,10 @@ struct Factor {
 };
 
 // Whether a norm's codes can be those of h w, whose largest magnitude is `most`: the row's factor r changes no code, and
-// takes two roundings with it.  Not where the scale has its least value, or h w may be below fp32's normal range (or NaN).
+// takes two roundings with it.  Not where the scale has its least value or none (y passes fp32's range), or h w may be below
+// fp32's normal range (or NaN).
 __device__ __forceinline__ bool codes_without_r(float most, float most_y) {
-    return most <= FLT_MAX && most >= LEAST && most_y >= LEAST;
+    return most <= FLT_MAX && most >= LEAST && most_y <= FLT_MAX && most_y >= LEAST;
 }
 
 // Four INT8 codes of y times the factor (PAIR: both parts of it), at most 127 in magnitude: 1.5 * 2^23 added leaves the
