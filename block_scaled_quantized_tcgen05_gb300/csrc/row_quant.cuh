@@ -525,7 +525,8 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
         if constexpr (!WARP) {
             const int warps = nt >> 5;
             if ((t & 31) == 0) room[turn][t >> 5] = make_float2(ss, amax);
-            __syncthreads();
+            // Warps come here from two bodies of `process` at once where a row does not fill its block: the barrier by its number.
+            asm volatile("barrier.sync 0;" ::: "memory");
             const float2 v = (t & 31) < warps ? room[turn][t & 31] : make_float2(0.0f, 0.0f);
             turn ^= 1;
             ss = v.x;
