@@ -25,7 +25,7 @@ thread_local char g_last_msg[512] = "";
 // bound on every device-side wait; set from any host thread, read at each launch
 std::atomic<uint64_t> g_timeout_ns{4000000000ull};
 
-constexpr int MAX_DEVICES = 64;
+using qgi::MAX_DEVICES;
 struct DeviceInfo {
     bool ready = false;
     int num_sms = 0;

@@ -26,12 +26,14 @@ namespace qgi {
 constexpr int EPI_ACCUMULATE = 1;   // add the existing C (fp16) to the fp32 accumulator
 constexpr int EPI_RELU = 2;         // max(x, +0) before rounding
 
+constexpr int MAX_DEVICES = 64;     // launch_ctx refuses an index past them
+
 struct LaunchCtx {
     cudaStream_t stream;
     unsigned *err;        // device error word
     uint64_t timeout_ns;  // bound on every device-side wait
     int num_sms;
-    int device;
+    int device;           // below MAX_DEVICES
     int epi = 0;          // EPI_* flags of the output epilogue
 };
 

@@ -20,6 +20,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 #include <cfloat>
 #include <type_traits>
 
@@ -839,10 +840,20 @@ struct RingPlan {
     int threads, blocks;
 };
 
+// A kernel's registers a thread, asked once a device (`known`: 0 until then; a query that failed is not kept).
 template <class K>
-int registers_of(K kern) {
-    cudaFuncAttributes at;
-    return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? (at.numRegs + 7) / 8 * 8 : 128;
+int registers_of(K kern, std::atomic<int> &known) {
+    int registers = known.load(std::memory_order_relaxed);
+    if (registers == 0) {
+        cudaFuncAttributes at;
+        if (cudaFuncGetAttributes(&at, kern) != cudaSuccess) {
+            cudaGetLastError();              // the launch will say what is wrong
+            return 128;
+        }
+        registers = (at.numRegs + 7) / 8 * 8;
+        known.store(registers, std::memory_order_relaxed);
+    }
+    return registers;
 }
 
 constexpr int RING_ROOM = 220 * 1024;    // of an SM's shared memory for rings
@@ -907,13 +918,14 @@ cudaError_t launch_vec(const qgi::RowQuantArgs &a, const qgi::LaunchCtx &ctx) {
         auto k4 = row_quant_vec_kernel<TY, OUT, NORM, SECOND, 4, 0, ANY, false>;
         auto big = row_quant_vec_kernel<TY, OUT, NORM, SECOND, 4, 0, ANY, true>;
         static_assert(32 * most_threads(4, ANY, false) >= 16384 && 32 * most_threads(4, ANY, true) >= LONGEST, "every row has a kernel");
-        static const int r2 = registers_of(k2), r4 = registers_of(k4), r_big = registers_of(big);
+        static std::atomic<int> known[qgi::MAX_DEVICES][3];
+        std::atomic<int>(&r)[3] = known[ctx.device];
         constexpr int unit = unit_of<NORM, SECOND, 4, true>;
-        if (a.H > 16384) return launch_ring(big, plan_ring(r_big, 4, unit, a.H, SECOND, ANY), 4 / unit, a, ctx);
-        const RingPlan p2 = plan_ring(r2, 2, 2, a.H, SECOND, ANY);
+        if (a.H > 16384) return launch_ring(big, plan_ring(registers_of(big, r[2]), 4, unit, a.H, SECOND, ANY), 4 / unit, a, ctx);
+        const RingPlan p2 = plan_ring(registers_of(k2, r[0]), 2, 2, a.H, SECOND, ANY);
         const bool two = p2.threads <= most_threads(2, ANY, false);
         if (two && p2.blocks >= 2) return launch_ring(k2, p2, 1, a, ctx);
-        const RingPlan p4 = plan_ring(r4, 4, 4, a.H, SECOND, ANY);
+        const RingPlan p4 = plan_ring(registers_of(k4, r[1]), 4, 4, a.H, SECOND, ANY);
         return p4.blocks >= 2 || !two ? launch_ring(k4, p4, 1, a, ctx) : launch_ring(k2, p2, 1, a, ctx);
     }
 }

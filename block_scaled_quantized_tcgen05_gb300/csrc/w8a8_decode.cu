@@ -313,16 +313,21 @@ cudaError_t launch_nh(const qgi::W8A8Args &a, const Layout &l, const qgi::Launch
     cfg.numAttrs = 2;
     // CTAs spread evenly: each takes the shared memory that leaves no room for more on its SM than there are on the fullest (8 x
     // 4096 x 4096, 512 CTAs: 7.1 us against 7.7 where five fit), or than the clusters need to be there all at once (16 of 8 are not
-    // at one CTA an SM: 40 x 512 x 8192 ran in two rounds), which is asked once.
-    static std::atomic<int> at_once[9][17];
+    // at one CTA an SM: 40 x 512 x 8192 ran in two rounds), which is asked once a device.
+    static std::atomic<int> at_once[qgi::MAX_DEVICES][9][17];
     int64_t each = (l.grid + ctx.num_sms - 1) / ctx.num_sms;
     for (;; ++each) {
         cfg.dynamicSmemBytes = std::max(G::smem(l.splits), std::min(MOST, uint32_t(SM_SMEM / each) / 1024 * 1024 - 1024));
         if (l.splits == 1 || each > 16 || cfg.dynamicSmemBytes == G::smem(l.splits)) break;
-        int clusters = at_once[l.splits][each].load(std::memory_order_relaxed);
+        std::atomic<int> &known = at_once[ctx.device][l.splits][each];
+        int clusters = known.load(std::memory_order_relaxed);
         if (clusters == 0) {
-            if (cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) != cudaSuccess) clusters = 0;
-            at_once[l.splits][each].store(std::max(clusters, 1), std::memory_order_relaxed);
+            if (cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) != cudaSuccess) {
+                cudaGetLastError();              // not kept: the even share will do, and the launch says what is wrong
+                break;
+            }
+            clusters = std::max(clusters, 1);
+            known.store(clusters, std::memory_order_relaxed);
         }
         if (int64_t(clusters) * l.splits >= l.grid) break;
     }
