@@ -245,10 +245,17 @@ __device__ __forceinline__ uint4 shared_any(const uint8_t *p, uint32_t off, int 
 
 __device__ __forceinline__ uint32_t before_16(const void *p) { return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15); }
 
+// Debug build: n elements of `item` bytes at p, or fewer where n is more than the 8 of a thread, lie in the T rows of H elements at
+// `base`.
+__device__ __forceinline__ bool in_rows([[maybe_unused]] unsigned *err, const qgi::RowQuantArgs &a, const void *p, int n, int item,
+                                        const void *base, int64_t ld) {
+    return QG_IN_RANGE(err, p, min(n, 8) * item, base, ((a.T - 1) * ld + a.H) * item);
+}
+
 // Weights of elements e .. e + 7 (0 past the row's end).
 template <bool ANY>
-__device__ __forceinline__ void load_weight8(const qgi::RowQuantArgs &a, int e, float (&w)[8]) {
-    if (!a.weight) {
+__device__ __forceinline__ void load_weight8(const qgi::RowQuantArgs &a, int e, float (&w)[8], unsigned *err) {
+    if (!a.weight || !QG_IN_BOUNDS(err, e >= 0 && e < a.H && (ANY || a.H - e >= 8))) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i] = 1.0f;
     } else if (ANY && (a.H - e < 8 || before_16(a.weight) != 0)) {
@@ -317,7 +324,9 @@ __device__ __forceinline__ void store_warp(uint16_t *p, const uint4 &v, int n) {
 // PAIR: INT8 codes by both parts of the factor.
 template <int OUT, bool ANY, class TY, bool PAIR>
 __device__ __forceinline__ void store_row(const qgi::RowQuantArgs &a, int64_t row, uint32_t e, int n, const float (&v)[8],
-                                          const Factor &factor) {
+                                          const Factor &factor, unsigned *err) {
+    if (n > 0 && !in_rows(err, a, static_cast<uint8_t *>(a.y) + (row * a.ldy + e) * (OUT == OUT_16 ? 2 : 1), n, OUT == OUT_16 ? 2 : 1, a.y, a.ldy))
+        n = 0;
     if constexpr (OUT == OUT_INT8) {
         uint8_t *y = static_cast<uint8_t *>(a.y) + row * a.ldy + e;
         const uint2 q = make_uint2(codes_i8<PAIR>(v, factor), codes_i8<PAIR>(v + 4, factor));
@@ -347,7 +356,9 @@ __device__ __forceinline__ void store_row(const qgi::RowQuantArgs &a, int64_t ro
             uint8_t *y = static_cast<uint8_t *>(a.y) + row * a.ldy + e;
             if (ANY) store_any(y, make_uint2(q[0], q[1]), n);
             else *reinterpret_cast<uint2 *>(y) = make_uint2(q[0], q[1]);
-            if ((threadIdx.x & 3) == 0) (static_cast<uint8_t *>(a.scales) + row * a.lds)[e / 32] = static_cast<uint8_t>(byte);
+            if ((threadIdx.x & 3) == 0 && QG_IN_RANGE(err, static_cast<uint8_t *>(a.scales) + row * a.lds + e / 32, 1, a.scales,
+                                                      (a.T - 1) * a.lds + a.H / 32))
+                (static_cast<uint8_t *>(a.scales) + row * a.lds)[e / 32] = static_cast<uint8_t>(byte);
         }
     } else {
         uint16_t *y = static_cast<uint16_t *>(a.y) + row * a.ldy + e;
@@ -361,7 +372,7 @@ __device__ __forceinline__ void store_row(const qgi::RowQuantArgs &a, int64_t ro
 // input.  A thread's next pieces are on their way while it works on these.  Gated SiLU to INT8 of 1024 x 65536: 136 us, 16 x 53248:
 // 15.3 us; with 512 threads, two blocks an SM, 147 and 18.4 (2048 x 53248: 228 against 212).
 template <class TY, int OUT>
-__global__ void __launch_bounds__(1024) row_quant_long_kernel(const __grid_constant__ qgi::RowQuantArgs a) {
+__global__ void __launch_bounds__(1024) row_quant_long_kernel(const __grid_constant__ qgi::RowQuantArgs a, unsigned *err) {
     __shared__ float2 room[32];
     griddep_launch_dependents();
     griddep_wait();
@@ -379,8 +390,8 @@ __global__ void __launch_bounds__(1024) row_quant_long_kernel(const __grid_const
             Pieces p{};
             const int n = static_cast<int>(H - e);
             if (n > 0) {
-                p.x = load_any(x + e, offx, n);
-                if (a.second) p.second = load_any(second + e, off2, n);
+                if (in_rows(err, a, x + e, n, 2, a.x, a.ldx)) p.x = load_any(x + e, offx, n);
+                if (a.second && in_rows(err, a, second + e, n, 2, a.second, a.ld2)) p.second = load_any(second + e, off2, n);
             }
             return p;
         };
@@ -407,7 +418,7 @@ __global__ void __launch_bounds__(1024) row_quant_long_kernel(const __grid_const
                 input(here, v);
                 if (a.norm) {
                     float w[8], s2[2] = {0.0f, 0.0f};
-                    if (OUT == OUT_INT8) load_weight8<true>(a, static_cast<int>(e), w);
+                    if (OUT == OUT_INT8) load_weight8<true>(a, static_cast<int>(e), w, err);
 #pragma unroll
                     for (int j = 0; j < 8; j += 2) {
                         mul2(v[j], v[j + 1], v[j], v[j + 1], f, f);
@@ -452,10 +463,13 @@ __global__ void __launch_bounds__(1024) row_quant_long_kernel(const __grid_const
             next = fetch(e + STEP);
             float v[8];
             input(here, v);
-            if (a.sum_out) store_warp(static_cast<uint16_t *>(a.sum_out) + row * a.ldso + e, pack8<TY>(v), n);
+            if (a.sum_out) {
+                uint16_t *sum = static_cast<uint16_t *>(a.sum_out) + row * a.ldso + e;
+                store_warp(sum, pack8<TY>(v), n > 0 && !in_rows(err, a, sum, n, 2, a.sum_out, a.ldso) ? 0 : n);
+            }
             if (a.norm && n > 0) {
                 float w[8];
-                load_weight8<true>(a, static_cast<int>(e), w);
+                load_weight8<true>(a, static_cast<int>(e), w, err);
 #pragma unroll
                 for (int j = 0; j < 8; j += 2) {
                     mul2(v[j], v[j + 1], v[j], v[j + 1], f, f);
@@ -463,9 +477,9 @@ __global__ void __launch_bounds__(1024) row_quant_long_kernel(const __grid_const
                     mul2(v[j], v[j + 1], v[j], v[j + 1], w[j], w[j + 1]);
                 }
             }
-            store_row<OUT, true, TY, true>(a, row, e, n, v, factor);
+            store_row<OUT, true, TY, true>(a, row, e, n, v, factor, err);
         }
-        if (OUT == OUT_INT8 && threadIdx.x == 0) static_cast<float *>(a.scales)[row] = shown / 127.0f;
+        if (OUT == OUT_INT8 && threadIdx.x == 0 && QG_IN_BOUNDS(err, row < a.T)) static_cast<float *>(a.scales)[row] = shown / 127.0f;
     }
 }
 
@@ -538,9 +552,11 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
     };
     // Whether any row of the warp takes a path that its lanes go together (a block's rows go alone).
     auto any_row = [](bool b) { return MANY ? __any_sync(0xFFFFFFFFu, b) != 0 : b; };
-    auto put16 = [](uint16_t *p, const uint4 &v, int n) {          // ANY: by whole warps
+    auto put_sum = [&](int64_t row, int e, const uint4 &v, int n) {            // ANY: by whole warps
+        uint16_t *p = static_cast<uint16_t *>(a.sum_out) + row * a.ldso + e;
+        if (n > 0 && !in_rows(err, a, p, n, 2, a.sum_out, a.ldso)) n = 0;
         if constexpr (ANY) store_warp(p, v, n);
-        else *reinterpret_cast<uint4 *>(p) = v;
+        else if (n > 0) *reinterpret_cast<uint4 *>(p) = v;
     };
     auto row_x = [&](int64_t row) { return static_cast<const uint16_t *>(a.x) + row * a.ldx; };
     auto row_2 = [&](int64_t row) { return static_cast<const uint16_t *>(a.second) + row * a.ld2; };
@@ -552,14 +568,14 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
         if constexpr (KEEP)
 #pragma unroll
             for (int i = 0; i < C; ++i)
-                if (8 * (i * nt + t) < a.H) load_weight8<ANY>(a, 8 * (i * nt + t), wkept[i]);
+                if (8 * (i * nt + t) < a.H) load_weight8<ANY>(a, 8 * (i * nt + t), wkept[i], err);
     };
     auto weights = [&](int i, int e, float (&w)[8]) {
         if constexpr (KEEP)
 #pragma unroll
             for (int j = 0; j < 8; ++j) w[j] = wkept[i][j];
         else
-            load_weight8<ANY>(a, e, w);
+            load_weight8<ANY>(a, e, w, err);
     };
 
     // One row: load(i, e, n, xv, sv) gives chunk i's operands, read_done() says that all threads have theirs.  `in`: all of the warp's
@@ -593,7 +609,7 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
                         for (int j = 0; j < 8; j += 2) add2(v[i][j], v[i][j + 1], s[j], s[j + 1]);
                     if (!IN && ANY && e - 8 * (t & 31) >= H) continue;  // whole warps
                     if (SECOND && a.sum_out && (IN || ANY || e < H))
-                        put16(static_cast<uint16_t *>(a.sum_out) + row * a.ldso + e, pack8<TY>(v[i]), IN ? 8 : H - e);
+                        put_sum(row, e, pack8<TY>(v[i]), IN ? 8 : H - e);
                     if (!IN && e >= H) continue;
 #pragma unroll
                     for (int j = 0; j < 8; j += 2)
@@ -683,12 +699,12 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
                         mul2(v[i][j], v[i][j + 1], v[i][j], v[i][j + 1], w[j], w[j + 1]);
                     }
                 }
-                store_row<OUT, ANY, TY, decltype(pair)::value>(a, row, e, IN ? 8 : H - e, v[i], factor);
+                store_row<OUT, ANY, TY, decltype(pair)::value>(a, row, e, IN ? 8 : H - e, v[i], factor, err);
             }
         };
         if (NORM || !SECOND || OUT != OUT_INT8 || a.activation == QGEMM_ACT_NONE) store(std::true_type{});
         else store(std::false_type{});
-        if (OUT == OUT_INT8 && t == 0 && (!MANY || H > 0)) static_cast<float *>(a.scales)[row] = shown / 127.0f;
+        if (OUT == OUT_INT8 && t == 0 && (!MANY || H > 0) && QG_IN_BOUNDS(err, row >= 0 && row < a.T)) static_cast<float *>(a.scales)[row] = shown / 127.0f;
     };
 
     if constexpr (WARP) {
@@ -701,9 +717,9 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
         const uint16_t *px = row_x(row), *p2 = SECOND ? row_2(row) : nullptr;
         const uint32_t offx = ANY ? before_16(px) : 0, off2 = ANY && SECOND ? before_16(p2) : 0;
         auto load = [&](int, int e, int n, uint4 &xv, uint4 &sv) {
-            if (n <= 0) return;
+            if (n <= 0 || !in_rows(err, a, px + e, n, 2, a.x, a.ldx)) return;
             xv = ANY ? load_any(px + e, offx, n) : load_once(px + e);
-            if (SECOND) sv = ANY ? load_any(p2 + e, off2, n) : load_once(p2 + e);
+            if (SECOND && in_rows(err, a, p2 + e, n, 2, a.second, a.ld2)) sv = ANY ? load_any(p2 + e, off2, n) : load_once(p2 + e);
         };
         const bool all_in = !ANY && a.H - e0 >= 8 * L * C && (!MANY || row + (31 - (threadIdx.x & 31)) / L < a.T);
         if (all_in) process(std::bool_constant<!ANY>{}, row, e0, load, [] {});
@@ -733,6 +749,13 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
                 bytes2 = (2 * n + off2 + 15) & ~15u;
             }
             const uint32_t bar = full0 + 8 * stage, dst = sb + stage * ring.stage_bytes;
+            // debug build: the part lies in its row, its pieces begin at 16 bytes and fit the stage
+            if (!QG_IN_BOUNDS(err, row >= 0 && row < a.T && n > 0 && first + n <= a.H && stage < ring.stages &&
+                                       (reinterpret_cast<uintptr_t>(px) - offx) % 16 == 0 && (!SECOND || (reinterpret_cast<uintptr_t>(p2) - off2) % 16 == 0) &&
+                                       bytes <= (SECOND ? ring.second_at : ring.stage_bytes) && (!SECOND || ring.second_at + bytes2 <= ring.stage_bytes))) {
+                mbar_arrive(bar);
+                return;
+            }
             mbar_arrive_expect_tx(bar, bytes + bytes2);
             const uint64_t policy = ring.once ? l2_policy_evict_first() : l2_policy_evict_normal();
             bulk_load_hint(dst, reinterpret_cast<const uint8_t *>(px) - offx, bytes, bar, policy);
@@ -935,7 +958,7 @@ cudaError_t launch_out(const qgi::RowQuantArgs &a, const qgi::LaunchCtx &ctx) {
     // Past what a block's registers hold; and past what 32 bits with a sign count, where nothing of the whole row is needed.
     if (a.H > (a.norm || OUT == OUT_INT8 ? LONGEST : 1 << 30)) {
         const dim3 grid(static_cast<unsigned>(a.T < ctx.num_sms ? a.T : ctx.num_sms));
-        return launch_dependent(row_quant_long_kernel<TY, OUT>, grid, 1024, 0, ctx.stream, a);
+        return launch_dependent(row_quant_long_kernel<TY, OUT>, grid, 1024, 0, ctx.stream, a, ctx.err);
     }
     const int kind = 4 * a.norm + 2 * (a.second != nullptr) + vec_eligible(a);
     switch (kind) {

@@ -216,6 +216,7 @@ w8a8_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
             return (((r >> 4) * NH + (m >> 3)) * 4 + ((r >> 3) & 1) * 2 + (m & 1)) * 32 + (r & 7) * 4 + ((m & 7) >> 1);
         };
         auto store = [&](int m, int n, float sum) {
+            if (!QG_IN_BOUNDS(err, m >= 0 && m < a.M && n >= 0 && n < a.N)) return;
             uint16_t *dst = static_cast<uint16_t *>(a.C) + m * a.ldc + n;
             const float bias = a.bias ? load_16(a.bias, n, a.bf16) : 0.0f;
             const float old = epi & qgi::EPI_ACCUMULATE ? load_16(dst, 0, a.bf16) : 0.0f;

@@ -431,6 +431,7 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                 }
                 const int mc = m0 + ch * 32;
                 if (where >= 0) {
+                    if (!QG_IN_BOUNDS(err, where < 2 * shares.sharers && shares.shared() && half * (BT / 2) + ch * 32 + 32 <= BT)) continue;
                     // this range's sums, [token of the tile][weight row of the tile]: a store writes 32 consecutive floats
                     float *pl = P + (int64_t(where) * BT + half * (BT / 2) + ch * 32) * (2 * BW) + rank * BW + q * 32 + lane;
 #pragma unroll
@@ -458,7 +459,7 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                 } else if (n < N) {
 #pragma unroll
                     for (int c = 0; c < 32; ++c) {
-                        if (mc + c >= M) continue;
+                        if (mc + c >= M || !QG_IN_BOUNDS(err, mc + c >= 0 && n >= 0)) continue;
                         uint16_t *dst = static_cast<uint16_t *>(a.C) + (mc + c) * a.ldc + n;
                         const float old = epi & qgi::EPI_ACCUMULATE ? load_16(dst, 0, BF16) : 0.0f;
                         *dst = round_16(finish(__uint_as_float(v[c]), sa_room[ch * 32 + c], sw, bias, old, epi), BF16);
@@ -471,7 +472,7 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                 if (lane == 0) {
 #pragma unroll
                     for (int ch = 0; ch < G::CHUNKS; ++ch)   // blocks wholly past M or N are not stored
-                        if (n0 < N && m0 + ch * 32 < M) tma_store_2d(&tmC, stg + ch * 2048, n0, m0 + ch * 32);
+                        if (n0 < N && m0 + ch * 32 < M && QG_IN_BOUNDS(err, n0 >= 0 && n0 % 8 == 0 && m0 >= 0)) tma_store_2d(&tmC, stg + ch * 2048, n0, m0 + ch * 32);
                     bulk_commit();
                 }
             }
@@ -488,7 +489,7 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
 
 // The tokens' codes as halves, rows of `ldh` (K rounded up to 16, at least): 16 codes a thread.
 __global__ void __launch_bounds__(256) codes_to_f16_kernel(const int8_t *__restrict__ A, int64_t lda, int M, int K,
-                                                           uint16_t *__restrict__ H, int64_t ldh) {
+                                                           uint16_t *__restrict__ H, int64_t ldh, unsigned *err) {
     griddep_wait();
     griddep_launch_dependents();                                   // after the wait: see the pair kernel's early copies
     const int per_row = (K + 15) / 16;
@@ -513,6 +514,7 @@ __global__ void __launch_bounds__(256) codes_to_f16_kernel(const int8_t *__restr
         i8x4_to_f16(d.z, o[4], o[5]);
         i8x4_to_f16(d.w, o[6], o[7]);
         uint4 *dst = reinterpret_cast<uint4 *>(H + m * ldh + k);
+        if (!QG_IN_BOUNDS(err, m < M && k < K && k + 16 <= ldh)) continue;
         dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
         dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
@@ -522,7 +524,7 @@ __global__ void __launch_bounds__(256) codes_to_f16_kernel(const int8_t *__restr
 // thread, four tokens' rows of 256 columns at a time.  What goes by tile or column is found once a block.
 template <int BT>
 __global__ void __launch_bounds__(256) w8a8_reduce_kernel(const float *__restrict__ P, const __grid_constant__ Shares shares,
-                                                          const __grid_constant__ qgi::W8A8Args a, int parts, int vec, int epi) {
+                                                          const __grid_constant__ qgi::W8A8Args a, int parts, int vec, int epi, unsigned *err) {
     griddep_launch_dependents();
     constexpr int64_t SLOT = int64_t(BT) * (2 * BW);
     const int t = blockIdx.x / parts, part = blockIdx.x - t * parts;
@@ -533,6 +535,7 @@ __global__ void __launch_bounds__(256) w8a8_reduce_kernel(const float *__restric
     // piece p of the tile is the first of its pair's range where that begins inside the tile or at its start: all but p0's may
     const float *first = P + (2 * p0 + (shares.begin(p0) >= uint32_t(t) * shares.KT ? 0 : 1)) * SLOT + col, *others = P + col;
     if (p0 == p1 || n >= a.N) return;            // a whole tile, written by its pair
+    if (!QG_IN_BOUNDS(err, t < shares.rest && p0 >= 0 && p0 < p1 && p1 < shares.sharers)) return;
     griddep_wait();
     float sw[4], bias[4];
 #pragma unroll
@@ -543,7 +546,7 @@ __global__ void __launch_bounds__(256) w8a8_reduce_kernel(const float *__restric
     const bool whole = vec && n + 4 <= a.N;
     for (int token = 4 * part + static_cast<int>(threadIdx.x >> 6); token < BT; token += 4 * parts) {
         const int64_t m = int64_t(tb) * BT + token;
-        if (m >= a.M) break;
+        if (m >= a.M || !QG_IN_BOUNDS(err, m >= 0 && token < BT && n >= 0)) break;
         const int row = token * (2 * BW);
         float4 sum = __ldcg(reinterpret_cast<const float4 *>(first + row));
         for (int p = p0 + 1; p <= p1; p += 8) {  // eight pieces' loads at once, whatever is left of them
@@ -644,7 +647,7 @@ cudaError_t launch_bt(const qgi::W8A8Args &a, const CUtensorMap &tmX, const CUte
     if (e == cudaSuccess && shares.shared()) {
         const int vec = reinterpret_cast<uintptr_t>(a.C) % 8 == 0 && a.ldc % 4 == 0;
         const int parts = std::max(1, std::min(BT / 4, (4 * ctx.num_sms + shares.rest - 1) / shares.rest));
-        e = launch_dependent(w8a8_reduce_kernel<BT>, dim3(shares.rest * parts), 256, 0, ctx.stream, P, shares, a, parts, vec, ctx.epi);
+        e = launch_dependent(w8a8_reduce_kernel<BT>, dim3(shares.rest * parts), 256, 0, ctx.stream, P, shares, a, parts, vec, ctx.epi, ctx.err);
     }
     return e;
 }
@@ -676,7 +679,7 @@ static cudaError_t launch_slice(const W8A8Args &a, uint16_t *H, int64_t ldh, flo
         tmC = tmX;   // unused
     if (!*encode_ok) return cudaErrorInvalidValue;
     cudaError_t e = launch_dependent(codes_to_f16_kernel, dim3(grid_for(a.M * int64_t((a.K + 15) / 16), ctx)), 256, 0,
-                                     ctx.stream, a.A, a.lda, a.M, a.K, H, ldh);
+                                     ctx.stream, a.A, a.lda, a.M, a.K, H, ldh, ctx.err);
     if (e == cudaSuccess)
         e = bt == 64    ? launch_bt<64>(a, tmX, tmW, tmC, c_tma, shares, P, ctx)
             : bt == 128 ? launch_bt<128>(a, tmX, tmW, tmC, c_tma, shares, P, ctx)
