@@ -558,7 +558,7 @@ qgemm_status qgemm_kv_copy_pages(const qgemm_kv_cache *kv, const int32_t *src, c
  *   QGEMM_INT8  q[t, c] = rne(y[t, c] * 127 / a), s[t] = a / 127 (fp32), a = max(max_c |y[t, c]|, 2^-100):
  *               the operands of qgemm_w8a8.  Codes lie in -127 .. 127.  A row that holds a NaN gets the
  *               scale NaN, one that holds an infinity and no NaN the scale infinity with codes 0: the product's
- *               row is NaN in both cases.
+ *               row is NaN in both cases (under `relu` 0, as max(x, +0) of a NaN is +0 in all of this library).
  *   QGEMM_E4M3  per 32 elements X = floor(log2(amax)) - 8 (at least -127) as byte X + 127 and e4m3_rn(y * 2^-X)
  *               saturated to +-448, as qgemm_kv_append stores a bfloat16 cache: the operands of
  *               qgemm_mxfp8.  An all-zero block gets byte 127; NaN elements become E4M3's NaN, infinite
@@ -581,7 +581,8 @@ qgemm_status qgemm_kv_copy_pages(const qgemm_kv_cache *kv, const int32_t *src, c
  *   Y             device [T, H] of y_dtype: QGEMM_INT8, QGEMM_E4M3 or dtype; row stride ldy elements.  A Y of dtype
  *                 may be X (with its row stride), where residual_out is not; otherwise Y overlaps no input.
  *   scales        QGEMM_INT8: fp32 [T].  QGEMM_E4M3: UE8M0 [T, H / 32], row stride lds bytes.  Else NULL.
- * Requirements: H % 32 == 0 for QGEMM_E4M3, otherwise any H; T and H below 2^31; rows of the outputs must not overlap.
+ * Requirements: H % 32 == 0 for QGEMM_E4M3, otherwise any H; T and H below 2^31; rows of the outputs must not overlap.  T == 0 or
+ * H == 0 writes nothing, scales included.
  * Sums of squares that pass fp32's range (bfloat16 inputs above about 1e18) are taken again of h * 2^-80.
  * Speed: rows of a multiple of 8 elements, 16-byte aligned (a Y of 8 bits 8-byte) at strides of multiples of 8 elements, are
  * read and written as they lie; others are shifted into place on the way.  Rows past 32768 elements are read twice, but
@@ -612,7 +613,8 @@ qgemm_status qgemm_act_quant(const void *X, int64_t ldx, const void *up, int64_t
 /* Product of 8-bit integers with a scale for each token and each channel:
  *   C[m, n] = round( (sum_k A[m, k] W[n, k]) * a_scales[m] * w_scales[n] [+ bias[n]] ).
  * Codes are two's complement int8, -128 included, multiplied as halves on the tensor cores (exact products, fp32 sums):
- * integer sums below 2^24 are exact, larger ones carry fp32's rounding.  Scales are applied to the sum in fp32; one rounding at the end.
+ * integer sums that stay below 2^24 on their way are exact; past it each of the K / 16 accumulations may lose up to 2^-23 of the sum so
+ * far, as the tensor cores cut it.  Scales are applied to the sum in fp32; one rounding at the end.
  *   A         device int8 [M, K], row stride lda bytes;  a_scales fp32 [M].
  *   W         device int8 [N, K], row stride ldw bytes;  w_scales fp32 [N].
  *   bias      device [N] of c_dtype, or NULL.
