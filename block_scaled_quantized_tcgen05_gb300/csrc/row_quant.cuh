@@ -15,8 +15,9 @@
 //
 // Measured (GB300, whose copies reach 6.76 TB/s): norm with residual of 8192 x 8192 bf16 to E4M3 78.3 us, 6.03 TB/s; gated SiLU of
 // 4096 x 14336 fp16 to E4M3 49.7 us, 5.95 TB/s.  Writes beside reads and the rows' exchanges cost what is left.  Without
-// a residual the issue slots bound a norm to INT8: 5003 x 5112 20.4 us, 3.8 TB/s (about half of a row's instructions are its exchange's
-// and its factor's, whatever its length); rows at any alignment, 5003 x 5111: 26.1 us, their shifts.  16 x 14336: 3.0 to 3.4 us.
+// a residual the issue slots bound a norm to INT8: 5003 x 5112 22.7 us, 3.4 TB/s (about half of a row's instructions are its exchange's
+// and its factor's, whatever its length); rows at any alignment, 5003 x 5111: 27.6 us, their shifts, and past 8192 elements, one
+// block of 512 threads an SM, 5003 x 12289: 65 us, 2.8 TB/s.  16 x 14336: 3.0 to 3.4 us.
 #pragma once
 
 #include <algorithm>
@@ -95,7 +96,7 @@ __device__ __forceinline__ float to_f32(const void *p, int64_t i, int32_t dtype)
 }
 
 // 127 / a as a pair: values half-way between codes are common (half of the row's largest is one, in a row as it is, in a norm's
-// h w, in a product of two operands), and a factor rounded to 32 bits moves them to either side.  One part alone saves 4 to 7 %
+// h w, in a product of two operands), and a factor rounded to 32 bits moves them to either side.  One part alone saves 4 to 8 %
 // where issue slots are the bound (norm without residual, 5003 x 5112: 20.6 us against 22.1; gated SiLU, 4096 x 12288: 41.4 against
 // 45.0) and 0 to 2 % elsewhere; it is taken for a gated SiLU or GELU only, whose values carry errors of their own.
 struct Factor {
@@ -325,8 +326,8 @@ __device__ __forceinline__ void store_warp(uint16_t *p, const uint4 &v, int n) {
 template <int OUT, bool ANY, class TY, bool PAIR>
 __device__ __forceinline__ void store_row(const qgi::RowQuantArgs &a, int64_t row, uint32_t e, int n, const float (&v)[8],
                                           const Factor &factor, unsigned *err) {
-    if (n > 0 && !in_rows(err, a, static_cast<uint8_t *>(a.y) + (row * a.ldy + e) * (OUT == OUT_16 ? 2 : 1), n, OUT == OUT_16 ? 2 : 1, a.y, a.ldy))
-        n = 0;
+    constexpr int ITEM = OUT == OUT_16 ? 2 : 1;
+    if (n > 0 && !in_rows(err, a, static_cast<uint8_t *>(a.y) + (row * a.ldy + e) * ITEM, n, ITEM, a.y, a.ldy)) n = 0;
     if constexpr (OUT == OUT_INT8) {
         uint8_t *y = static_cast<uint8_t *>(a.y) + row * a.ldy + e;
         const uint2 q = make_uint2(codes_i8<PAIR>(v, factor), codes_i8<PAIR>(v + 4, factor));
@@ -370,7 +371,8 @@ __device__ __forceinline__ void store_row(const qgi::RowQuantArgs &a, int64_t ro
 // Rows longer than a block holds in registers: one block a row, read a second time (from L2 mostly) once the row's sum and
 // maximum are known.  Operands of any alignment.  Every element is read and written by one thread, so an output may be an
 // input.  A thread's next pieces are on their way while it works on these.  Gated SiLU to INT8 of 1024 x 65536: 136 us, 16 x 53248:
-// 15.3 us; with 512 threads, two blocks an SM, 147 and 18.4 (2048 x 53248: 228 against 212).
+// 15.3 - 16.8 us; with 512 threads, two blocks an SM, 147 and 18.4 (2048 x 53248: 228 against 212).  Norm with residual to INT8 of 1024 x
+// 65536: 145 us.
 template <class TY, int OUT>
 __global__ void __launch_bounds__(1024) row_quant_long_kernel(const __grid_constant__ qgi::RowQuantArgs a, unsigned *err) {
     __shared__ float2 room[32];
@@ -704,7 +706,8 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
         };
         if (NORM || !SECOND || OUT != OUT_INT8 || a.activation == QGEMM_ACT_NONE) store(std::true_type{});
         else store(std::false_type{});
-        if (OUT == OUT_INT8 && t == 0 && (!MANY || H > 0) && QG_IN_BOUNDS(err, row >= 0 && row < a.T)) static_cast<float *>(a.scales)[row] = shown / 127.0f;
+        if (OUT == OUT_INT8 && t == 0 && (!MANY || H > 0) && QG_IN_BOUNDS(err, row >= 0 && row < a.T))
+            static_cast<float *>(a.scales)[row] = shown / 127.0f;
     };
 
     if constexpr (WARP) {
@@ -751,8 +754,10 @@ row_quant_vec_kernel(const __grid_constant__ qgi::RowQuantArgs a, const Ring rin
             const uint32_t bar = full0 + 8 * stage, dst = sb + stage * ring.stage_bytes;
             // debug build: the part lies in its row, its pieces begin at 16 bytes and fit the stage
             if (!QG_IN_BOUNDS(err, row >= 0 && row < a.T && n > 0 && first + n <= a.H && stage < ring.stages &&
-                                       (reinterpret_cast<uintptr_t>(px) - offx) % 16 == 0 && (!SECOND || (reinterpret_cast<uintptr_t>(p2) - off2) % 16 == 0) &&
-                                       bytes <= (SECOND ? ring.second_at : ring.stage_bytes) && (!SECOND || ring.second_at + bytes2 <= ring.stage_bytes))) {
+                                       (reinterpret_cast<uintptr_t>(px) - offx) % 16 == 0 &&
+                                       bytes <= (SECOND ? ring.second_at : ring.stage_bytes)) ||
+                (SECOND && !QG_IN_BOUNDS(err, (reinterpret_cast<uintptr_t>(p2) - off2) % 16 == 0 &&
+                                                  ring.second_at + bytes2 <= ring.stage_bytes))) {
                 mbar_arrive(bar);
                 return;
             }

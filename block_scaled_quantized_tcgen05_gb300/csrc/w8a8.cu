@@ -27,7 +27,7 @@ namespace qgi {
 // Up to 64 where the launches are most of the time and few blocks of rows keep the tokens' rows from being read often (40
 // tokens, 2048 x 2048: 7.7 us against 9.9, 1024 x 1024 5.2 against 7.6; 64 tokens 8.7 against 10.4, 7.2 against 7.7; 4096 x 1024 9.2
 // against 8.2).  Of 13 matrices that the rule takes, at 33 to 64 tokens, the stream is ahead by 1 to 33 %, but for 1536 x 2560 at 56
-// and 64 tokens (9.9 us against 9.7, 10.3 against 9.8), whose blocks of rows leave the last round short; 512 x 8192 at 64 is even.
+// and 64 tokens (9.9 us against 9.7, 10.3 against 9.8) and 512 x 8192 at 64 (even); no bound on sizes tells them from their neighbours.
 static bool few_tokens(const W8A8Args &a) {
     const int64_t weights = int64_t(a.N) * a.K;
     return a.M <= 16 || (a.M <= 32 && weights <= int64_t(1) << 25) ||

@@ -8,7 +8,7 @@
 namespace qg {
 
 // 4 int8 (one word) -> two fp16x2 of the same integers in order: q + 128 placed as a byte into the mantissa
-// of 1024, less 1152 (both exact).
+// of 1024, less 1152 (both exact; a published integer-to-half technique, as in the int8 GEMV).
 __device__ __forceinline__ void i8x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
     const uint32_t u = w ^ 0x80808080u;
     const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140u);       // halves 0x64|b0, 0x64|b1

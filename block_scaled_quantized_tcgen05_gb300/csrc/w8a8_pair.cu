@@ -21,7 +21,8 @@
 //     sums in scratch, which a reduction kernel adds in the order of K.  (The warp that finishes a piece last adding them at the
 //     kernel's end instead: 4096 x 14336 x 4096 in 310 us against 294, 256 x 4096 x 4096 29 against 21: too few loads in flight.)
 //
-// Measured: 8192^3 554 - 566 us (1.94 - 1.98 PFLOP/s, what the library's bf16 product reaches), 4096 x 14336 x 4096 246 us, 4096^3 83;
+// Measured: 8192^3 543 - 566 us (1.94 - 2.02 PFLOP/s, what the library's bf16 product reaches), 4096 x 14336 x 4096 246 us, 4096^3 83 (issued
+// one after another for long, under the power cap, 580 - 590 and 261 - 264);
 // 64 x 28672 x 8192 44 us (5.4 TB/s of weights; 6.3 in the middle, the rest start and end), 333 x 5003 x 4111 19 us: the tokens' halves 4, the k-tiles 11, epilogue, partial sums and launches the rest.
 #include <algorithm>
 #include <type_traits>
@@ -244,7 +245,7 @@ w8a8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
         // It need not wait for the kernel ahead, which makes the tokens' halves, touches no weights and has let this one start
         // only after all work ahead of it was done: the first weights are on their way meanwhile.
         // Weights that at most four tiles read, at nearly the same time, leave L2 first (64 x 28672 x 8192 46.9 -> 44.0 us, 64 x 16384
-        // x 19456 65.9 -> 55.8, 1024 x 8192 x 28672 263 -> 252); of more, some come later (4096 x 28672 x 8192 962 -> 990).
+        // x 19456 65.9 -> 54.5, 1024 x 8192 x 28672 263 -> 252); of more, some come later (4096 x 28672 x 8192 962 -> 990).
         const uint64_t policy = tiles_t <= 4 ? l2_policy_evict_first() : l2_policy_evict_normal();
         uint32_t slot_raw = 0, phase = 0;
         int issued = 0;
