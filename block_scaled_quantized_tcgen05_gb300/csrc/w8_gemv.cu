@@ -24,6 +24,7 @@
 // not depend on timing.  CTAs are persistent over 64-row blocks.
 #include <cuda_fp16.h>
 
+#include "int8_f16.cuh"
 #include "qgemm_common.cuh"
 #include "qgemm_debug.cuh"
 #include "qgemm_internal.h"
@@ -57,28 +58,6 @@ struct GCfg {
     static constexpr uint32_t SMEM = OFF_RED + RED_BYTES + 1024;
     static_assert(STAGE % 1024 == 0, "stages stay 1 KB aligned for the 128-byte swizzle");
 };
-
-// 4 int8 (one 32-bit word) -> two fp16x2 holding the exact integers (q0,q1), (q2,q3).
-__device__ __forceinline__ void i8x4_to_f16x2(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    const uint32_t u = w ^ 0x80808080u;                       // q + 128, as unsigned bytes
-    const uint32_t a = __byte_perm(u, 0x64646464u, 0x5140u);  // halves 0x64|b0, 0x64|b1
-    const uint32_t b = __byte_perm(u, 0x64646464u, 0x5342u);  // halves 0x64|b2, 0x64|b3
-    const uint32_t bias = 0x64806480u;                        // 1152.0 = 1024 + 128
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(bias));
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(bias));
-}
-
-// Not volatile: a pure function of its registers, so the compiler may interleave the MMAs of
-// independent fragments.
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                          uint32_t b1, const float (&c)[4]) {
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%10,%11,%12,%13};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
-          "f"(c[2]), "f"(c[3]));
-}
 
 // Scale bytes of blocks 16 G .. 16 G + 15 of one row (the four 32-blocks of four consecutive
 // stages) as four little-endian words; bytes past the row's last block read as 127 (2^0; their
@@ -127,10 +106,10 @@ __device__ __forceinline__ void stage_math(float (&acc)[NF][NH][4], const uint8_
         const uint2 wa = *reinterpret_cast<const uint2 *>(st + wrow + f * 16 * 128);
         const uint2 wb = *reinterpret_cast<const uint2 *>(st + wrow + (f * 16 + 8) * 128);
         uint32_t a0[4], a1[4];
-        i8x4_to_f16x2(wa.x, a0[0], a0[2]);
-        i8x4_to_f16x2(wb.x, a0[1], a0[3]);
-        i8x4_to_f16x2(wa.y, a1[0], a1[2]);
-        i8x4_to_f16x2(wb.y, a1[1], a1[3]);
+        i8x4_to_f16(wa.x, a0[0], a0[2]);
+        i8x4_to_f16(wb.x, a0[1], a0[3]);
+        i8x4_to_f16(wa.y, a1[0], a1[2]);
+        i8x4_to_f16(wb.y, a1[1], a1[3]);
         const uint32_t b0 = (e0[f] >> sh) & 0xFFu, b1 = (e1[f] >> sh) & 0xFFu;
         const float sa = EXACT ? ue8m0_to_f32(b0) : __uint_as_float(b0 << 23);
         const float sbv = EXACT ? ue8m0_to_f32(b1) : __uint_as_float(b1 << 23);

@@ -47,12 +47,6 @@ struct Cfg {
     static_assert(STAGE % 1024 == 0, "stages stay 1 KB aligned for the 128-byte swizzle");
 };
 
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 __device__ __forceinline__ float ld_cluster(uint32_t addr) {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
@@ -80,8 +74,8 @@ __device__ __forceinline__ void stage_math(float (&acc)[NF][NH][4], const uint8_
         i8x4_to_f16(wb.y, a1[1], a1[3]);
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-            mma_16816(acc[f][h], a0, x[h][0], x[h][1]);
-            mma_16816(acc[f][h], a1, x[h][2], x[h][3]);
+            mma_16816(acc[f][h], a0, x[h][0], x[h][1], acc[f][h]);
+            mma_16816(acc[f][h], a1, x[h][2], x[h][3], acc[f][h]);
         }
     }
 }
